@@ -15,6 +15,7 @@
 #include "gdr_internal.h"
 #include "gdr_backward.h"
 #include "gdr_epilogue.h"
+#include "gdr_serve.h"
 
 namespace gdr {
 
@@ -601,7 +602,10 @@ gdr_status gdr_sync_status(gdr_stream_t stream) {
   if (word != 0) {
     const int zero = 0;
     cudaMemcpyToSymbol(g_error_word, &zero, sizeof(int));
-    if (word == kErrDeviceIndex) return fail(GDR_ERR_DEVICE_INDEX, "a fork's trunk index was out of range");
+    if (word == kErrDeviceIndex)
+      return fail(GDR_ERR_DEVICE_INDEX, "an index, length or page read on the device was out of range (a fork's trunk "
+                                        "index, a row's length, a page of a table, a row listed twice)");
+    if (word == kErrNoPages) return fail(GDR_ERR_NO_PAGES, "the cache had too few free pages");
     if (word == kErrTimeout) return fail(GDR_ERR_TIMEOUT, "a kernel wait ran past its limit");
     return fail(GDR_ERR_CUDA, "device error word %d", word);
   }
@@ -616,6 +620,7 @@ const char* gdr_status_string(gdr_status s) {
     case GDR_ERR_CUDA: return "GDR_ERR_CUDA";
     case GDR_ERR_DEVICE_INDEX: return "GDR_ERR_DEVICE_INDEX";
     case GDR_ERR_TIMEOUT: return "GDR_ERR_TIMEOUT";
+    case GDR_ERR_NO_PAGES: return "GDR_ERR_NO_PAGES";
   }
   return "GDR_ERR_UNKNOWN";
 }
@@ -680,6 +685,13 @@ const char* gdr_kernel_name(int id) {
     case kKernBackwardReduce: return "gdr_backward_reduce";
     case kKernChunkAdjoint: return "gdr_chunk_adjoint";
     case kKernChunkBwdLocal: return "gdr_chunk_bwd_local";
+    case kKernQkNormRope: return "gdr_qk_norm_rope";
+    case kKernQkNormRopeBwd: return "gdr_qk_norm_rope_backward";
+    case kKernTreeAttn: return "gdr_tree_attn";
+    case kKernTreeAttnJoin: return "gdr_tree_attn_join";
+    case kKernVerifyDraft: return "gdr_verify_draft";
+    case kKernCacheAlloc: return "gdr_cache_alloc";
+    case kKernCacheCopy: return "gdr_cache_copy";
   }
   return nullptr;
 }

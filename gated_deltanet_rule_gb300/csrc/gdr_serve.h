@@ -1,0 +1,120 @@
+// Internal declarations of the attention-layer operators of a speculative step (not part of the
+// ABI): q/k norm + rotation, tree attention over pages, draft verification, cache pages.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "gdr_backward.h"
+#include "gdr_epilogue.h"
+#include "gdr_internal.h"
+
+namespace gdr {
+
+// Stage-timer ids, after the existing kernels'.
+constexpr int kKernQkNormRope = 9;
+constexpr int kKernQkNormRopeBwd = 10;
+constexpr int kKernTreeAttn = 11;
+constexpr int kKernTreeAttnJoin = 12;
+constexpr int kKernVerifyDraft = 13;
+constexpr int kKernCacheAlloc = 14;
+constexpr int kKernCacheCopy = 15;
+
+constexpr int kNumSMs = 152;   // GB300
+
+// RMS norm of every query and key head and the rotation by position. The three entry points share
+// these arguments: dense outputs (k_out set), keys and values into pages (k_pages set), gradient
+// (dq set; q_out, k_out unused).
+struct RopeArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* q_w;
+  const float* k_w;
+  const double* inv_freq;
+  const int32_t* pos;
+  float eps;
+  int interleaved;
+  void* q_out;
+  void* k_out;
+  long long q_tok, q_head, k_tok, k_head, v_tok, v_head;   // strides in elements
+  int B, N, Hq, Hk, D, R;
+  bool bf16;
+  // pages
+  void* k_pages;
+  void* v_pages;
+  const int32_t* table;
+  const int32_t* ctx;
+  const int32_t* lengths;
+  int P, page, M;
+  // gradient
+  const void* dq_out;
+  const void* dk_out;
+  float* dq;
+  float* dk;
+  float* dq_w;
+  float* dk_w;
+  float* partial;
+  int* err;
+  int split;   // warps that share a token's heads (set by the launch)
+};
+cudaError_t launch_qk_norm_rope(RopeArgs a, cudaStream_t s);
+cudaError_t launch_qk_norm_rope_backward(RopeArgs a, cudaStream_t s);
+size_t qk_norm_rope_backward_workspace_bytes(int D);
+
+// Verification of drafted tokens: one cluster of blocks per row walks the row's tree.
+struct VerifyArgs {
+  const int32_t* tokens;
+  const int32_t* parents;
+  const int32_t* lengths;
+  const void* p;
+  const void* q;        // NULL: given drafts
+  const float* u;
+  const float* u_next;
+  int32_t* path;
+  int32_t* n_path;
+  int32_t* next_token;
+  int B, N, V;
+  bool bf16;
+  int* err;
+};
+constexpr int kVerifyMaxNodes = 1024;   // nodes of a row whose scalars fit the kernel's shared memory
+cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t s);
+
+// Cache pages with reference counts (a page is free when its count is 0).
+struct CacheArgs {
+  uint8_t* k_cache;          // [layers, P, page, row_bytes]
+  uint8_t* v_cache;
+  int32_t* table;            // [rows, M]
+  int32_t* ctx;              // [rows]
+  int32_t* refs;             // [P]
+  const int32_t* src;        // [F] (fork only)
+  const int32_t* dst;        // [F]
+  int layers, P, page, rows, M, F;
+  long long row_bytes;
+  int extra;                 // reserve: positions past ctx that must have pages
+  int32_t* ws;               // need [F], first [F], count; free list
+  int* err;
+};
+size_t cache_workspace_bytes(int F, int M);
+cudaError_t launch_cache_fork(const CacheArgs& a, cudaStream_t s);
+cudaError_t launch_cache_reserve(const CacheArgs& a, cudaStream_t s);
+cudaError_t launch_cache_free(const CacheArgs& a, cudaStream_t s);
+
+struct CompactArgs {
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  const int32_t* table;
+  const int32_t* ctx;
+  const int32_t* path;       // [B, W]
+  const int32_t* n_path;     // [B]
+  int32_t* new_ctx;          // [B]
+  int layers, P, page, B, M, W;
+  long long row_bytes;
+  int* err;
+};
+constexpr int kCompactMaxPath = 2048;   // path entries whose slots fit the kernel's shared memory
+cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t s);
+
+}  // namespace gdr

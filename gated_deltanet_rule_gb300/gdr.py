@@ -16,7 +16,8 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libgdr.so")
 
-GDR_OK, GDR_ERR_INVALID_ARG, GDR_ERR_UNSUPPORTED, GDR_ERR_CUDA, GDR_ERR_DEVICE_INDEX, GDR_ERR_TIMEOUT = range(6)
+GDR_OK, GDR_ERR_INVALID_ARG, GDR_ERR_UNSUPPORTED, GDR_ERR_CUDA, GDR_ERR_DEVICE_INDEX, GDR_ERR_TIMEOUT, \
+    GDR_ERR_NO_PAGES = range(7)
 GDR_F32, GDR_BF16 = 0, 1
 D = 128
 
@@ -27,6 +28,9 @@ EXPORTS = ["gdr_chunk_workspace_bytes", "gdr_chunk_fwd", "gdr_chunk_fwd_varlen",
            "gdr_backward_workspace_bytes", "gdr_backward",
            "gdr_backward_chunked_workspace_bytes", "gdr_backward_chunked",
            "gdr_chunk_fwd_save", "gdr_backward_chunked_saved",
+           "gdr_qk_norm_rope", "gdr_qk_norm_rope_append", "gdr_qk_norm_rope_backward_workspace_bytes",
+           "gdr_qk_norm_rope_backward", "gdr_verify_draft",
+           "gdr_cache_workspace_bytes", "gdr_cache_reserve", "gdr_cache_fork", "gdr_cache_free", "gdr_cache_compact",
            "gdr_sync_status", "gdr_status_string", "gdr_last_error_message",
            "gdr_stage_timer_enable", "gdr_stage_timer_collect", "gdr_kernel_name", "gdr_debug_set_wait_budget"]
 
@@ -87,6 +91,29 @@ def lib() -> ctypes.CDLL:
     L.gdr_backward_chunked_saved.restype = i
     L.gdr_chunk_fwd_save.argtypes = [vp, vp, vp, fp, fp, fp, vp, fp, i, i, i, i, i, i, vp, sz, vp]
     L.gdr_chunk_fwd_save.restype = i
+    ll, f32 = ctypes.c_longlong, ctypes.c_float
+    L.gdr_qk_norm_rope.argtypes = [vp, vp, fp, fp, vp, vp, f32, i, vp, vp, i, i, i, i, i, i, ll, ll, ll, ll, i, vp]
+    L.gdr_qk_norm_rope.restype = i
+    L.gdr_qk_norm_rope_append.argtypes = [vp, vp, vp, fp, fp, vp, vp, f32, i, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i,
+                                          i, i, i, ll, ll, ll, ll, ll, ll, i, vp]
+    L.gdr_qk_norm_rope_append.restype = i
+    L.gdr_qk_norm_rope_backward_workspace_bytes.argtypes = [i]
+    L.gdr_qk_norm_rope_backward_workspace_bytes.restype = sz
+    L.gdr_qk_norm_rope_backward.argtypes = [vp, vp, fp, fp, vp, vp, vp, vp, f32, i, fp, fp, fp, fp, i, i, i, i, i, i, ll,
+                                            ll, ll, ll, i, vp, sz, vp]
+    L.gdr_qk_norm_rope_backward.restype = i
+    L.gdr_verify_draft.argtypes = [vp, vp, vp, vp, vp, fp, fp, vp, vp, vp, i, i, i, i, vp]
+    L.gdr_verify_draft.restype = i
+    L.gdr_cache_workspace_bytes.argtypes = [i, i]
+    L.gdr_cache_workspace_bytes.restype = sz
+    L.gdr_cache_reserve.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, vp, sz, vp]
+    L.gdr_cache_reserve.restype = i
+    L.gdr_cache_fork.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, ll, vp, sz, vp]
+    L.gdr_cache_fork.restype = i
+    L.gdr_cache_free.argtypes = [vp, vp, vp, vp, i, i, i, i, vp]
+    L.gdr_cache_free.restype = i
+    L.gdr_cache_compact.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, ll, vp]
+    L.gdr_cache_compact.restype = i
     L.gdr_sync_status.argtypes = [vp]
     L.gdr_sync_status.restype = i
     L.gdr_status_string.argtypes = [i]
@@ -435,6 +462,209 @@ def gdr_backward_chunked(q, k, v, g, beta, S0, dO, dS_T=None, ws=None, stream=No
     _check(fn(_p(q), _p(k), _p(v), _p(g), _p(beta), _p(S0), _p(dO), _p(dS_T), _p(dq), _p(dk), _p(dv), _p(dg),
               _p(dbeta), _p(dS0), B, L, Hk, Hv, Dk, _dtype_code(q), _p(ws), ws_bytes, _stream(stream)))
     return dq, dk, dv, dg, dbeta, dS0
+
+
+# --------------------------------------------------------------------------------------------------
+# softmax-attention layers: drafted tokens over a cache of pages
+# --------------------------------------------------------------------------------------------------
+def _need_ints(**tensors):
+    for name, t in tensors.items():
+        if t is not None:
+            _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.int32 and t.is_contiguous(),
+                  f"{name} must be a contiguous CUDA int32 tensor")
+
+
+def _heads(name, t, like=None):
+    """Strides (token, head) of [B, N, H, D], which may be a slice of a wider projection."""
+    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 4, f"{name} must be a CUDA tensor [B, N, H, D]")
+    _need(t.shape[3] == 1 or t.stride(3) == 1, f"{name}: the last dimension must be contiguous")
+    if like is not None:
+        _need(t.dtype == like.dtype and t.shape[:2] == like.shape[:2] and t.shape[3] == like.shape[3],
+              f"{name} must share q's dtype, rows, tokens and head dimension")
+    B, N, H, Dk = t.shape
+    tok = t.stride(1) if N > 1 else (t.stride(0) if B > 1 else H * Dk)
+    _need(B == 1 or N == 1 or t.stride(0) == N * tok, f"{name}: tokens of all rows must lie at one stride")
+    return tok, (t.stride(2) if H > 1 else Dk)
+
+
+def _rope_common(q, k, q_w, k_w, inv_freq, pos):
+    q_tok, q_head = _heads("q", q)
+    k_tok, k_head = _heads("k", k, q)
+    B, N, Hq, Dk = q.shape
+    for name, w in (("q_w", q_w), ("k_w", k_w)):
+        _need(isinstance(w, torch.Tensor) and w.is_cuda and w.dtype == torch.float32 and w.shape == (Dk,)
+              and w.is_contiguous(), f"{name} must be contiguous CUDA float32 [D]")
+    _need(isinstance(inv_freq, torch.Tensor) and inv_freq.is_cuda and inv_freq.dtype == torch.float64
+          and inv_freq.dim() == 1 and inv_freq.is_contiguous(), "inv_freq must be contiguous CUDA float64 [R / 2]")
+    _need_ints(pos=pos)
+    _need(pos.shape == (B, N), "pos must be [B, N]")
+    return B, N, Hq, k.shape[2], Dk, 2 * inv_freq.shape[0], q_tok, q_head, k_tok, k_head, _dtype_code(q)
+
+
+def _check_out(name, t, shape, dtype):
+    _need(t.is_cuda and t.is_contiguous() and tuple(t.shape) == tuple(shape) and t.dtype == dtype,
+          f"{name} must be a contiguous CUDA tensor of shape {tuple(shape)} and dtype {dtype}")
+
+
+def _pages(k_pages, v_pages, table, ctx, B, Hk, Dk, dtype):
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        _need(isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and t.dim() == 4 and t.dtype == dtype
+              and t.shape == k_pages.shape, f"{name} must be a contiguous CUDA tensor [P, page, Hk, D] of q's dtype")
+    P, page, H, Dp = k_pages.shape
+    _need((H, Dp) == (Hk, Dk), "pages must hold k's heads and head dimension")
+    _need_ints(table=table, ctx=ctx)
+    _need(table.dim() == 2 and table.shape[0] == B and ctx.shape == (B,), "table must be [B, M] and ctx [B]")
+    return P, page, table.shape[1]
+
+
+def gdr_qk_norm_rope(q, k, q_w, k_w, inv_freq, pos, eps: float = 1e-6, interleaved: bool = False, q_out=None,
+                     k_out=None, stream=None):
+    """RMS norm of every head of q [B,N,Hq,D] and k [B,N,Hk,D] (views of one projection are read in
+    place) and the rotation of its first R = 2 len(inv_freq) elements by pos [B,N] int32 times inv_freq
+    (float64). Returns (q_out, k_out), contiguous, in q's dtype."""
+    B, N, Hq, Hk, Dk, R, q_tok, q_head, k_tok, k_head, dt = _rope_common(q, k, q_w, k_w, inv_freq, pos)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device) if k_out is None else k_out
+    _check_out("q_out", q_out, q.shape, q.dtype)
+    _check_out("k_out", k_out, k.shape, q.dtype)
+    _check(lib().gdr_qk_norm_rope(_p(q), _p(k), _p(q_w), _p(k_w), _p(inv_freq), _p(pos), float(eps), int(interleaved),
+                                  _p(q_out), _p(k_out), B, N, Hq, Hk, Dk, R, q_tok, q_head, k_tok, k_head, dt,
+                                  _stream(stream)))
+    return q_out, k_out
+
+
+def gdr_qk_norm_rope_append(q, k, v, q_w, k_w, inv_freq, pos, k_pages, v_pages, table, ctx, lengths=None,
+                            eps: float = 1e-6, interleaved: bool = False, q_out=None, stream=None):
+    """gdr_qk_norm_rope that leaves the keys, and v as it is, in the pages of table [B,M] at positions
+    ctx[b] + i (i < lengths[b] where given). Returns q_out."""
+    B, N, Hq, Hk, Dk, R, q_tok, q_head, k_tok, k_head, dt = _rope_common(q, k, q_w, k_w, inv_freq, pos)
+    v_tok, v_head = _heads("v", v, q)
+    _need(v.shape == k.shape, "v must have k's shape")
+    P, page, M = _pages(k_pages, v_pages, table, ctx, B, Hk, Dk, q.dtype)
+    _need_ints(lengths=lengths)
+    _need(lengths is None or lengths.shape == (B,), "lengths must be [B]")
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    _check_out("q_out", q_out, q.shape, q.dtype)
+    _check(lib().gdr_qk_norm_rope_append(_p(q), _p(k), _p(v), _p(q_w), _p(k_w), _p(inv_freq), _p(pos), float(eps),
+                                         int(interleaved), _p(q_out), _p(k_pages), _p(v_pages), _p(table), _p(ctx),
+                                         _p(lengths), P, page, M, B, N, Hq, Hk, Dk, R, q_tok, q_head, k_tok, k_head,
+                                         v_tok, v_head, dt, _stream(stream)))
+    return q_out
+
+
+def gdr_qk_norm_rope_backward(q, k, q_w, k_w, inv_freq, pos, dq_out, dk_out, eps: float = 1e-6,
+                              interleaved: bool = False, ws=None, stream=None):
+    """Gradients of gdr_qk_norm_rope from dq_out, dk_out (contiguous, q's dtype): (dq, dk, dq_w, dk_w),
+    all float32."""
+    B, N, Hq, Hk, Dk, R, q_tok, q_head, k_tok, k_head, dt = _rope_common(q, k, q_w, k_w, inv_freq, pos)
+    _check_out("dq_out", dq_out, q.shape, q.dtype)
+    _check_out("dk_out", dk_out, k.shape, q.dtype)
+    f32 = dict(dtype=torch.float32, device=q.device)
+    dq, dk = torch.empty(q.shape, **f32), torch.empty(k.shape, **f32)
+    dq_w, dk_w = torch.empty(Dk, **f32), torch.empty(Dk, **f32)
+    if ws is None:
+        ws = torch.empty(max(int(lib().gdr_qk_norm_rope_backward_workspace_bytes(Dk)), 1), dtype=torch.uint8,
+                         device=q.device)
+    _check(lib().gdr_qk_norm_rope_backward(_p(q), _p(k), _p(q_w), _p(k_w), _p(inv_freq), _p(pos), _p(dq_out),
+                                           _p(dk_out), float(eps), int(interleaved), _p(dq), _p(dk), _p(dq_w),
+                                           _p(dk_w), B, N, Hq, Hk, Dk, R, q_tok, q_head, k_tok, k_head, dt, _p(ws),
+                                           ws.numel() * ws.element_size(), _stream(stream)))
+    return dq, dk, dq_w, dk_w
+
+
+def gdr_verify_draft(tokens, parents, lengths, p, q, u, u_next, path=None, n_path=None, next_token=None, stream=None):
+    """Walks each row's tree of drafted tokens (tokens, parents [B,N] int32, lengths [B]) against the
+    target's probabilities p [B,N,V] and the drafts' q [B,N,V] (None: given drafts) with the uniform
+    numbers u [B,N], u_next [B]. Returns (path [B,N] of accepted nodes, root first, -1 after them;
+    n_path [B]; next_token [B])."""
+    _need_ints(tokens=tokens, parents=parents, lengths=lengths, path=path, n_path=n_path, next_token=next_token)
+    _need(isinstance(p, torch.Tensor) and p.is_cuda and p.is_contiguous() and p.dim() == 3,
+          "p must be a contiguous CUDA tensor [B, N, V]")
+    B, N, V = p.shape
+    _need(q is None or (q.is_cuda and q.is_contiguous() and q.shape == p.shape and q.dtype == p.dtype),
+          "q must be None or like p")
+    _need(tokens.shape == (B, N) and parents.shape == (B, N) and lengths.shape == (B,),
+          "tokens and parents must be [B, N] and lengths [B]")
+    for name, t, shape in (("u", u, (B, N)), ("u_next", u_next, (B,))):
+        _need(t.is_cuda and t.is_contiguous() and t.dtype == torch.float32 and tuple(t.shape) == shape,
+              f"{name} must be contiguous CUDA float32 {shape}")
+    i32 = dict(dtype=torch.int32, device=p.device)
+    path = torch.empty(B, N, **i32) if path is None else path
+    n_path = torch.empty(B, **i32) if n_path is None else n_path
+    next_token = torch.empty(B, **i32) if next_token is None else next_token
+    _need(path.shape == (B, N) and n_path.shape == (B,) and next_token.shape == (B,),
+          "path must be [B, N], n_path and next_token [B]")
+    _check(lib().gdr_verify_draft(_p(tokens), _p(parents), _p(lengths), _p(p), _p(q), _p(u), _p(u_next), _p(path),
+                                  _p(n_path), _p(next_token), B, N, V, _dtype_code(p), _stream(stream)))
+    return path, n_path, next_token
+
+
+def _cache(k_cache, v_cache):
+    """(layers, P, page, row bytes) of caches [layers, P, page, Hk, D]."""
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _need(isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and t.dim() == 5
+              and t.shape == k_cache.shape and t.dtype == k_cache.dtype,
+              f"{name} must be a contiguous CUDA tensor [layers, P, page, Hk, D]")
+    layers, P, page, Hk, Dk = k_cache.shape
+    return layers, P, page, Hk * Dk * k_cache.element_size()
+
+
+def _row_list(table, ctx, refs, **lists):
+    _need_ints(table=table, ctx=ctx, refs=refs, **lists)
+    _need(table.dim() == 2 and ctx.shape == (table.shape[0],) and refs.dim() == 1,
+          "table must be [rows, M], ctx [rows] and refs [P]")
+    n = [t.shape for t in lists.values()]
+    _need(all(len(x) == 1 and x == n[0] for x in n), "row lists must be [F]")
+    return n[0][0], table.shape[0], table.shape[1]
+
+
+def cache_workspace_bytes(F: int, M: int) -> int:
+    return int(lib().gdr_cache_workspace_bytes(F, M))
+
+
+def _cache_ws(ws, F, M, device):
+    if ws is None:
+        ws = torch.empty(max(cache_workspace_bytes(F, M), 16), dtype=torch.uint8, device=device)
+    return ws, ws.numel() * ws.element_size()
+
+
+def gdr_cache_reserve(table, ctx, refs, rows, extra: int, page: int, ws=None, stream=None) -> None:
+    """Gives rows (int32 [F]) pages so that ctx + extra positions of each fit; table, refs in place."""
+    F, R, M = _row_list(table, ctx, refs, rows=rows)
+    ws, ws_bytes = _cache_ws(ws, F, M, table.device)
+    _check(lib().gdr_cache_reserve(_p(table), _p(ctx), _p(refs), _p(rows), int(extra), F, R, M, refs.shape[0], int(page),
+                                   _p(ws), ws_bytes, _stream(stream)))
+
+
+def gdr_cache_fork(k_cache, v_cache, table, ctx, refs, src, dst, ws=None, stream=None) -> None:
+    """Row dst[f] becomes a copy of row src[f]: full pages shared, the last one copied. In place."""
+    layers, P, page, row_bytes = _cache(k_cache, v_cache)
+    F, R, M = _row_list(table, ctx, refs, dst=dst, src=src)
+    _need(refs.shape == (P,), "refs must be [P]")
+    ws, ws_bytes = _cache_ws(ws, F, M, table.device)
+    _check(lib().gdr_cache_fork(_p(k_cache), _p(v_cache), _p(table), _p(ctx), _p(refs), _p(src), _p(dst), F, R, M, layers,
+                                P, page, row_bytes, _p(ws), ws_bytes, _stream(stream)))
+
+
+def gdr_cache_free(table, ctx, refs, rows, stream=None) -> None:
+    """Gives the pages of rows (int32 [F]) back; table, ctx, refs in place."""
+    F, R, M = _row_list(table, ctx, refs, rows=rows)
+    _check(lib().gdr_cache_free(_p(table), _p(ctx), _p(refs), _p(rows), F, R, M, refs.shape[0], _stream(stream)))
+
+
+def gdr_cache_compact(k_cache, v_cache, table, ctx, path, n_path, new_ctx=None, stream=None):
+    """Moves the entries of the accepted paths (gdr_verify_draft's path, n_path) to the front of their
+    rows in every layer; returns new_ctx = ctx + n_path (which may not be ctx itself)."""
+    layers, P, page, row_bytes = _cache(k_cache, v_cache)
+    _need_ints(table=table, ctx=ctx, path=path, n_path=n_path, new_ctx=new_ctx)
+    _need(path.dim() == 2 and table.dim() == 2, "path must be [B, W] and table [B, M]")
+    B, W = path.shape
+    new_ctx = torch.empty_like(ctx) if new_ctx is None else new_ctx
+    _need(table.shape[0] == B and ctx.shape == (B,) and n_path.shape == (B,) and new_ctx.shape == (B,),
+          "table, ctx, n_path and new_ctx must have path's rows")
+    _check(lib().gdr_cache_compact(_p(k_cache), _p(v_cache), _p(table), _p(ctx), _p(path), _p(n_path), _p(new_ctx), B, W,
+                                   table.shape[1], layers, P, page, row_bytes, _stream(stream)))
+    return new_ctx
 
 
 def gdr_sync_status(stream=None) -> None:

@@ -39,8 +39,9 @@ typedef enum {
   GDR_ERR_INVALID_ARG = 1,   /* null pointer, bad size, misalignment, workspace too small  */
   GDR_ERR_UNSUPPORTED = 2,   /* a size the kernels do not implement (D != 128)            */
   GDR_ERR_CUDA = 3,          /* a CUDA runtime call failed (launch, sync, encode)          */
-  GDR_ERR_DEVICE_INDEX = 4,  /* a fork's trunk index was outside [0, N)                    */
-  GDR_ERR_TIMEOUT = 5        /* a kernel wait ran past its limit; the kernel stopped early */
+  GDR_ERR_DEVICE_INDEX = 4,  /* an index, length or page read on the device was out of range */
+  GDR_ERR_TIMEOUT = 5,       /* a kernel wait ran past its limit; the kernel stopped early */
+  GDR_ERR_NO_PAGES = 6       /* a cache had fewer free pages than its rows needed          */
 } gdr_status;
 
 typedef enum { GDR_F32 = 0, GDR_BF16 = 1 } gdr_dtype;
@@ -320,6 +321,133 @@ gdr_status gdr_backward_chunked_saved(const void* q, const void* k, const void* 
                                       float* dq, float* dk, float* dv, float* dg, float* dbeta, float* dS0, int B,
                                       int L, int Hk, int Hv, int D, gdr_dtype dt, void* saved, size_t saved_bytes,
                                       gdr_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------------------------
+ * Softmax-attention layers beside the gated delta rule layers: the operators of a decoding step
+ * that drafts tokens, checks them and keeps what was accepted. Keys and values live in pages that
+ * rows (sequences, forks) share:
+ *   k_pages, v_pages [P, page, Hk, D] dt   one layer's pages (one layer of [layers, P, page, Hk, D])
+ *   table [rows, M] int32                  row b's positions [m page, (m+1) page) live in page
+ *                                          table[b][m]; -1 where the row holds none
+ *   ctx   [rows] int32                     committed positions of each row
+ * page is 16, 32, 64 or 128; D is 64, 128 or 256; Hq is a multiple of Hk (query head h reads key
+ * head h / (Hq / Hk)). Drafted nodes 0 .. N-1 of row b (node 0 the last committed token, whose
+ * keys are not in the cache yet; every node after its parent) take positions ctx[b] .. ctx[b]+N-1
+ * until the accepted ones are moved to the front; lengths [B] int32 (NULL = N) gives each row's
+ * nodes. A length outside [0, N], a context that leaves the table, or a page outside [0, P) is
+ * recorded as GDR_ERR_DEVICE_INDEX.
+ * ---------------------------------------------------------------------------------------------
+ */
+
+/*
+ * RMS norm of every query and key head and the rotation by position, in one pass:
+ *   y = w x / sqrt(mean(x^2) + eps);  pair j < R/2 of y turned by the angle pos * inv_freq[j];
+ *   elements R .. D-1 pass through.
+ * Pairs are (j, j + R/2), or (2j, 2j + 1) with interleaved != 0.
+ *   q [B, N, Hq, D], k [B, N, Hk, D] dt   token i of row b starts at (b N + i) *_tok elements, head h
+ *                          *_head further (slices of one projection are read in place); strides
+ *                          multiples of 16 bytes
+ *   q_w, k_w [D] float32   norm weights;  eps >= 0
+ *   inv_freq [R/2] float64 radians per position;  pos [B, N] int32
+ *   q_out [B, N, Hq, D], k_out [B, N, Hk, D] dt   contiguous; may not overlap q or k
+ * R is a multiple of 8 in [0, D]. Arithmetic is float32 with one rounding of the outputs; angles are
+ * formed modulo a turn in 64-bit integers (exact to 2^-32 turn at any position).
+ */
+gdr_status gdr_qk_norm_rope(const void* q, const void* k, const float* q_w, const float* k_w,
+                            const double* inv_freq, const int32_t* pos, float eps, int interleaved, void* q_out,
+                            void* k_out, int B, int N, int Hq, int Hk, int D, int R, long long q_tok,
+                            long long q_head, long long k_tok, long long k_head, gdr_dtype dt,
+                            gdr_stream_t stream);
+
+/*
+ * The same, leaving keys and values in the cache: k normed and rotated, v [B, N, Hk, D] (strided like
+ * k) as it is, at positions ctx[b] + i of row b for i < lengths[b] (all N if NULL). q_out is computed
+ * for every i. A row whose length or context is out of range, or a position whose page is, writes
+ * nothing to the pages.
+ */
+gdr_status gdr_qk_norm_rope_append(const void* q, const void* k, const void* v, const float* q_w,
+                                   const float* k_w, const double* inv_freq, const int32_t* pos, float eps,
+                                   int interleaved, void* q_out, void* k_pages, void* v_pages,
+                                   const int32_t* table, const int32_t* ctx, const int32_t* lengths, int P,
+                                   int page, int M, int B, int N, int Hq, int Hk, int D, int R, long long q_tok,
+                                   long long q_head, long long k_tok, long long k_head, long long v_tok,
+                                   long long v_head, gdr_dtype dt, gdr_stream_t stream);
+
+/*
+ * Gradient of gdr_qk_norm_rope: from dq_out, dk_out (contiguous, dt) the gradients dq, dk (contiguous,
+ * float32) and dq_w, dk_w [D] float32, with dy = R^T dout and r = 1 / sqrt(mean(x^2) + eps):
+ *   dx = r (w dy - x r^2 mean(w dy x)),  dw = sum over tokens and heads of dy x r.
+ * ws holds at least gdr_qk_norm_rope_backward_workspace_bytes(D) bytes. The sums run in a fixed order.
+ * Outputs and ws overlap nothing.
+ */
+size_t gdr_qk_norm_rope_backward_workspace_bytes(int D);
+gdr_status gdr_qk_norm_rope_backward(const void* q, const void* k, const float* q_w, const float* k_w,
+                                     const double* inv_freq, const int32_t* pos, const void* dq_out,
+                                     const void* dk_out, float eps, int interleaved, float* dq, float* dk,
+                                     float* dq_w, float* dk_w, int B, int N, int Hq, int Hk, int D, int R,
+                                     long long q_tok, long long q_head, long long k_tok, long long k_head,
+                                     gdr_dtype dt, void* ws, size_t ws_bytes, gdr_stream_t stream);
+
+/*
+ * Verification of drafted tokens against the target's probabilities (speculative sampling over a
+ * tree; a chain is the tree of one child each). Per row, from the root on: at node `cur` the
+ * candidates are its children in index order. With (c, Z) = (0, 1) and rho = max(p[cur] - c q[cur], 0),
+ * candidate i of token t is accepted (and becomes cur) if u[i] q[cur][t] Z < rho[t]; a refusal sets
+ * c' = c + Z and Z' = sum max(p - c' q, 0), the normalised residual of the refused draft, unless that
+ * sum is 0 (then the state stays). With q NULL the drafts are given rather than drawn: a candidate is
+ * accepted if u[i] Z < rho[t], and a refusal takes p[t] out (rho[t] = 0, Z loses it). Where no
+ * candidate is left, next_token is the smallest t whose running sum of rho passes u_next times the
+ * total (the last t with rho > 0 if none does; p itself stands in for an empty rho; -1 for an empty p).
+ *   tokens, parents [B, N] int32   node i > 0 has parent parents[i] in [0, i); node 0 is the root.
+ *                                  A node with a parent or token out of range is no candidate
+ *                                  (GDR_ERR_DEVICE_INDEX)
+ *   lengths [B] int32              nodes of each row, in [0, N]; 0: path -1, n_path 0, next_token -1;
+ *                                  outside: the row's outputs untouched, GDR_ERR_DEVICE_INDEX
+ *   p [B, N, V], q [B, N, V] or NULL, dt   target and draft probabilities at each node (entries that
+ *                                  are not > 0 count as 0); q's row of a node is what its children
+ *                                  were drawn from
+ *   u [B, N], u_next [B] float32   uniform numbers in [0, 1)
+ *   path [B, N] int32              accepted nodes, the root first, then -1
+ *   n_path, next_token [B] int32
+ * Sums are carried to about 2^-46. N <= 1024, V < 2^30.
+ */
+gdr_status gdr_verify_draft(const int32_t* tokens, const int32_t* parents, const int32_t* lengths, const void* p,
+                            const void* q, const float* u, const float* u_next, int32_t* path, int32_t* n_path,
+                            int32_t* next_token, int B, int N, int V, gdr_dtype dt, gdr_stream_t stream);
+
+/*
+ * Pages. refs [P] int32 counts the rows that hold each page; a page is free when its count is 0, and
+ * pages are handed out lowest first to the listed rows in order, so results do not depend on timing.
+ * k_cache, v_cache [layers, P, page, row_bytes] hold every layer's entries, row_bytes the bytes of one
+ * position (Hk D times the element size; a multiple of 16). ws holds at least
+ * gdr_cache_workspace_bytes(F, M) bytes (F listed rows). Row lists are int32 [F].
+ *
+ * gdr_cache_reserve: rows[f] gets pages so that its ctx + extra positions fit.
+ * gdr_cache_fork: row dst[f] gives back what it holds and becomes a copy of row src[f]: the full pages
+ *   of src's ctx positions are shared, the partly filled last one is copied (its valid positions) to a
+ *   new page.
+ * gdr_cache_free: rows[f] gives back its pages (table -1, ctx 0).
+ * gdr_cache_compact: the entries at ctx + path[b][i] move to ctx + i for i < n_path[b] in every layer
+ *   (path rising, as gdr_verify_draft leaves it), and new_ctx[b] = ctx[b] + n_path[b]. new_ctx may
+ *   not overlap ctx.
+ * A row is refused, untouched, with GDR_ERR_DEVICE_INDEX, if its index is out of range, an earlier
+ * entry lists it too, a fork's source is itself listed as dst, its context or pages are out of range
+ * (reserve: or fewer than its context needs), or its path does not rise inside the table. Where pages
+ * run out (GDR_ERR_NO_PAGES) a row to be reserved stays as it was and a row to be forked is left empty.
+ */
+size_t gdr_cache_workspace_bytes(int F, int M);
+gdr_status gdr_cache_reserve(int32_t* table, const int32_t* ctx, int32_t* refs, const int32_t* rows, int extra,
+                             int F, int R, int M, int P, int page, void* ws, size_t ws_bytes,
+                             gdr_stream_t stream);
+gdr_status gdr_cache_fork(void* k_cache, void* v_cache, int32_t* table, int32_t* ctx, int32_t* refs,
+                          const int32_t* src, const int32_t* dst, int F, int R, int M, int layers, int P, int page,
+                          long long row_bytes, void* ws, size_t ws_bytes, gdr_stream_t stream);
+gdr_status gdr_cache_free(int32_t* table, int32_t* ctx, int32_t* refs, const int32_t* rows, int F, int R, int M,
+                          int P, gdr_stream_t stream);
+gdr_status gdr_cache_compact(void* k_cache, void* v_cache, const int32_t* table, const int32_t* ctx,
+                             const int32_t* path, const int32_t* n_path, int32_t* new_ctx, int B, int W, int M,
+                             int layers, int P, int page, long long row_bytes, gdr_stream_t stream);
 
 /* Synchronise `stream`, then read and clear the sticky device error word of the current device. */
 gdr_status gdr_sync_status(gdr_stream_t stream);
