@@ -63,6 +63,25 @@ cudaError_t launch_qk_norm_rope(RopeArgs a, cudaStream_t s);
 cudaError_t launch_qk_norm_rope_backward(RopeArgs a, cudaStream_t s);
 size_t qk_norm_rope_backward_workspace_bytes(int D);
 
+// Attention of a tree or chain of drafted nodes over the cache's pages (bf16).
+struct TreeAttnArgs {
+  const void* q;             // [B, N, Hq, D]
+  const void* k_pages;       // [P, page, Hk, D]
+  const void* v_pages;
+  const int32_t* table;      // [B, M]
+  const int32_t* ctx;        // [B]
+  const int32_t* lengths;    // [B] or NULL
+  const uint64_t* mask;      // [B, N, W] or NULL (node i sees nodes <= i)
+  float scale;
+  void* o;                   // [B, N, Hq, D]
+  float* lse;                // [B, N, Hq] or NULL
+  int B, N, Hq, Hk, D, P, page, M;
+  uint8_t* ws;
+  int* err;
+};
+size_t tree_attn_workspace_bytes(int D);
+cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t s);
+
 // Verification of drafted tokens: one cluster of blocks per row walks the row's tree.
 struct VerifyArgs {
   const int32_t* tokens;

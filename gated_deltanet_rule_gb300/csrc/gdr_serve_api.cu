@@ -229,6 +229,45 @@ gdr_status gdr_qk_norm_rope_backward(const void* q, const void* k, const float* 
   return launched(launch_qk_norm_rope_backward(a, reinterpret_cast<cudaStream_t>(stream)), who);
 }
 
+size_t gdr_tree_attn_workspace_bytes(int D) {
+  return D == 64 || D == 128 || D == 256 ? tree_attn_workspace_bytes(D) : 0;
+}
+
+gdr_status gdr_tree_attn(const void* q, const void* k_pages, const void* v_pages, const int32_t* table,
+                         const int32_t* ctx, const int32_t* lengths, const uint64_t* mask, float scale, void* o,
+                         float* lse, int B, int N, int Hq, int Hk, int D, int P, int page, int M, gdr_dtype dt,
+                         void* ws, size_t ws_bytes, gdr_stream_t stream) {
+  const char* who = "gdr_tree_attn";
+  if (!q || !k_pages || !v_pages || !table || !ctx || !o)
+    return fail(GDR_ERR_INVALID_ARG, "%s: q, k_pages, v_pages, table, ctx and o must be non-NULL", who);
+  gdr_status st = check_heads(B, N, Hq, Hk, D, dt, who);
+  if (st == GDR_OK && dt != GDR_BF16) st = fail(GDR_ERR_UNSUPPORTED, "%s: bfloat16 only (dt=%d)", who, (int)dt);
+  if (st == GDR_OK) st = check_pages(P, page, M, who);
+  if (st != GDR_OK) return st;
+  if (Hq / Hk > 128) return fail(GDR_ERR_UNSUPPORTED, "%s: Hq/Hk=%d exceeds 128 heads a group", who, Hq / Hk);
+  if (B > 65535 || (long long)N * Hq > 1 << 28) return fail(GDR_ERR_UNSUPPORTED, "%s: B=%d or N*Hq too large", who, B);
+  if (!(scale > 0.f) || scale > 1e30f) return fail(GDR_ERR_INVALID_ARG, "%s: scale must be positive and finite", who);
+  for (const void* p : {q, k_pages, v_pages, (const void*)o})
+    if (!aligned(p, 16)) return fail(GDR_ERR_INVALID_ARG, "%s: q, k_pages, v_pages and o must be 16-byte aligned", who);
+  for (const void* p : {(const void*)table, (const void*)ctx, (const void*)lengths, (const void*)lse})
+    if (!aligned(p, 4)) return fail(GDR_ERR_INVALID_ARG, "%s: table, ctx, lengths and lse must be 4-byte aligned", who);
+  if (!aligned(mask, 8)) return fail(GDR_ERR_INVALID_ARG, "%s: mask must be 8-byte aligned", who);
+  const size_t need = tree_attn_workspace_bytes(D);
+  st = check_ws(ws, ws_bytes, need, who);
+  if (st != GDR_OK) return st;
+  const unsigned long long rows = (unsigned long long)B * N * Hq, pages = (unsigned long long)P * page * Hk * D * 2;
+  st = apart({{o, rows * D * 2, "o"}, {lse, rows * 4, "lse"}, {ws, need, "ws"}},
+             {{q, rows * D * 2, "q"}, {k_pages, pages, "k_pages"}, {v_pages, pages, "v_pages"},
+              {table, (unsigned long long)B * M * 4, "table"}, {ctx, B * 4ull, "ctx"}, {lengths, B * 4ull, "lengths"},
+              {mask, (unsigned long long)B * N * ((N + 63) / 64) * 8, "mask"}}, who);
+  if (st != GDR_OK) return st;
+  int* err = device_error_word();
+  if (!err) return no_device(who);
+  const TreeAttnArgs a{q, k_pages, v_pages, table, ctx, lengths, mask, scale, o, lse, B, N, Hq, Hk, D, P, page, M,
+                       static_cast<uint8_t*>(ws), err};
+  return launched(launch_tree_attn(a, reinterpret_cast<cudaStream_t>(stream)), who);
+}
+
 gdr_status gdr_verify_draft(const int32_t* tokens, const int32_t* parents, const int32_t* lengths, const void* p,
                             const void* q, const float* u, const float* u_next, int32_t* path, int32_t* n_path,
                             int32_t* next_token, int B, int N, int V, gdr_dtype dt, gdr_stream_t stream) {

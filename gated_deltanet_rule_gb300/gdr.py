@@ -29,7 +29,7 @@ EXPORTS = ["gdr_chunk_workspace_bytes", "gdr_chunk_fwd", "gdr_chunk_fwd_varlen",
            "gdr_backward_chunked_workspace_bytes", "gdr_backward_chunked",
            "gdr_chunk_fwd_save", "gdr_backward_chunked_saved",
            "gdr_qk_norm_rope", "gdr_qk_norm_rope_append", "gdr_qk_norm_rope_backward_workspace_bytes",
-           "gdr_qk_norm_rope_backward", "gdr_verify_draft",
+           "gdr_qk_norm_rope_backward", "gdr_tree_attn_workspace_bytes", "gdr_tree_attn", "gdr_verify_draft",
            "gdr_cache_workspace_bytes", "gdr_cache_reserve", "gdr_cache_fork", "gdr_cache_free", "gdr_cache_compact",
            "gdr_sync_status", "gdr_status_string", "gdr_last_error_message",
            "gdr_stage_timer_enable", "gdr_stage_timer_collect", "gdr_kernel_name", "gdr_debug_set_wait_budget"]
@@ -102,6 +102,10 @@ def lib() -> ctypes.CDLL:
     L.gdr_qk_norm_rope_backward.argtypes = [vp, vp, fp, fp, vp, vp, vp, vp, f32, i, fp, fp, fp, fp, i, i, i, i, i, i, ll,
                                             ll, ll, ll, i, vp, sz, vp]
     L.gdr_qk_norm_rope_backward.restype = i
+    L.gdr_tree_attn_workspace_bytes.argtypes = [i]
+    L.gdr_tree_attn_workspace_bytes.restype = sz
+    L.gdr_tree_attn.argtypes = [vp, vp, vp, vp, vp, vp, vp, f32, vp, fp, i, i, i, i, i, i, i, i, i, vp, sz, vp]
+    L.gdr_tree_attn.restype = i
     L.gdr_verify_draft.argtypes = [vp, vp, vp, vp, vp, fp, fp, vp, vp, vp, i, i, i, i, vp]
     L.gdr_verify_draft.restype = i
     L.gdr_cache_workspace_bytes.argtypes = [i, i]
@@ -570,6 +574,42 @@ def gdr_qk_norm_rope_backward(q, k, q_w, k_w, inv_freq, pos, dq_out, dk_out, eps
                                            _p(dk_w), B, N, Hq, Hk, Dk, R, q_tok, q_head, k_tok, k_head, dt, _p(ws),
                                            ws.numel() * ws.element_size(), _stream(stream)))
     return dq, dk, dq_w, dk_w
+
+
+def tree_attn_workspace_bytes(D: int = D) -> int:
+    return int(lib().gdr_tree_attn_workspace_bytes(D))
+
+
+def gdr_tree_attn(q, k_pages, v_pages, table, ctx, lengths=None, mask=None, scale: float | None = None, o=None,
+                  lse=None, want_lse: bool = False, ws=None, stream=None):
+    """Attention of the nodes q [B,N,Hq,D] bf16 over each row's ctx[b] positions and the nodes that
+    mask [B,N,ceil(N/64)] int64 (bit j: node i sees node j; None: nodes 0 .. i) lets them see, the pages
+    already holding the nodes' keys and values. scale defaults to D^-1/2. Returns o, or (o, lse [B,N,Hq]
+    float32) with want_lse or lse given."""
+    _need(isinstance(q, torch.Tensor) and q.is_cuda and q.is_contiguous() and q.dim() == 4 and q.dtype == torch.bfloat16,
+          "q must be a contiguous CUDA bfloat16 tensor [B, N, Hq, D]")
+    B, N, Hq, Dk = q.shape
+    _need(isinstance(k_pages, torch.Tensor) and k_pages.dim() == 4, "k_pages must be [P, page, Hk, D]")
+    Hk = k_pages.shape[2]
+    P, page, M = _pages(k_pages, v_pages, table, ctx, B, Hk, Dk, q.dtype)
+    _need_ints(lengths=lengths)
+    _need(lengths is None or lengths.shape == (B,), "lengths must be [B]")
+    if mask is not None:
+        _need(mask.is_cuda and mask.is_contiguous() and mask.dtype == torch.int64 and mask.shape == (B, N, (N + 63) // 64),
+              "mask must be contiguous CUDA int64 [B, N, ceil(N / 64)]")
+    if o is None:
+        o = torch.empty_like(q)
+    _check_out("o", o, q.shape, q.dtype)
+    if lse is None and want_lse:
+        lse = torch.empty(B, N, Hq, dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _check_out("lse", lse, (B, N, Hq), torch.float32)
+    if ws is None:
+        ws = torch.empty(max(tree_attn_workspace_bytes(Dk), 16), dtype=torch.uint8, device=q.device)
+    _check(lib().gdr_tree_attn(_p(q), _p(k_pages), _p(v_pages), _p(table), _p(ctx), _p(lengths), _p(mask),
+                               float(Dk ** -0.5 if scale is None else scale), _p(o), _p(lse), B, N, Hq, Hk, Dk, P, page, M,
+                               GDR_BF16, _p(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    return o if lse is None else (o, lse)
 
 
 def gdr_verify_draft(tokens, parents, lengths, p, q, u, u_next, path=None, n_path=None, next_token=None, stream=None):

@@ -390,6 +390,29 @@ gdr_status gdr_qk_norm_rope_backward(const void* q, const void* k, const float* 
                                      gdr_dtype dt, void* ws, size_t ws_bytes, gdr_stream_t stream);
 
 /*
+ * Attention of each row's drafted nodes over its committed positions and the nodes they see:
+ *   o[b][i][h] = sum_j p_j v_j,  p = softmax_j(scale q[b][i][h] . k_j),  lse[b][i][h] = log sum_j e^(scale q . k_j)
+ *   q, o [B, N, Hq, D] bfloat16;  k_pages, v_pages, table, ctx, lengths as above (the nodes' own keys
+ *   and values already in the pages, at ctx[b] + node)
+ *   mask [B, N, W] uint64, W = ceil(N / 64): bit j % 64 of word j / 64 says that node i sees node j
+ *        (nodes at or past the row's length are never seen); NULL: node i sees nodes 0 .. i (a chain;
+ *        N = 1 is the plain decode step, ctx = 0 a prefill)
+ *   lse [B, N, Hq] float32, or NULL;  scale > 0
+ *   ws at least gdr_tree_attn_workspace_bytes(D) bytes (0 for a D that is not implemented)
+ * A node that sees nothing, and every node at or past its row's length, gets o = 0 and lse = -inf.
+ * Values of unseen positions do not matter, infinities and NaN included. A row whose length or context
+ * is out of range counts as having no nodes; a page out of range is read as zeros; both record
+ * GDR_ERR_DEVICE_INDEX. bfloat16 only (dt other than GDR_BF16: GDR_ERR_UNSUPPORTED), Hq / Hk <= 128.
+ * Scores, sums and accumulators are float32; the softmax weights are rounded to bfloat16 for their
+ * product with v, o once at the end.
+ */
+size_t gdr_tree_attn_workspace_bytes(int D);
+gdr_status gdr_tree_attn(const void* q, const void* k_pages, const void* v_pages, const int32_t* table,
+                         const int32_t* ctx, const int32_t* lengths, const uint64_t* mask, float scale, void* o,
+                         float* lse, int B, int N, int Hq, int Hk, int D, int P, int page, int M, gdr_dtype dt,
+                         void* ws, size_t ws_bytes, gdr_stream_t stream);
+
+/*
  * Verification of drafted tokens against the target's probabilities (speculative sampling over a
  * tree; a chain is the tree of one child each). Per row, from the root on: at node `cur` the
  * candidates are its children in index order. With (c, Z) = (0, 1) and rho = max(p[cur] - c q[cur], 0),

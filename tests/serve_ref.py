@@ -141,3 +141,34 @@ class Pool:
                 self.k[:, e, o], self.v[:, e, o] = old[i]
             out.append(self.ctx[b] + n)
         return out
+
+
+# ---- attention -----------------------------------------------------------------------------------
+def tree_attn(q, k_pages, v_pages, table, ctx, lengths, see, scale):
+    """(o, lse, A, E): A = sum_j p_j |v_j| and E = max_j scale sum_d |q_d k_jd| set the errors' size.
+    see [B, N, N] truth values among nodes; unseen positions are left out of every sum."""
+    B, N, Hq, D = q.shape
+    page, Hk = k_pages.shape[1:3]
+    o = torch.zeros(B, N, Hq, D, dtype=torch.float64)
+    lse = torch.full((B, N, Hq), -math.inf, dtype=torch.float64)
+    A, E = torch.zeros_like(o), torch.zeros_like(lse)
+    for b in range(B):
+        n, c = int(lengths[b]), int(ctx[b])
+        at = torch.arange(c + n)
+        if c + n == 0:
+            continue
+        pages = table[b].long()[at // page]
+        k, v = k_pages[pages, at % page].double(), v_pages[pages, at % page].double()   # [c + n, Hk, D]
+        for i in range(n):
+            vis = torch.cat([torch.ones(c, dtype=torch.bool), see[b, i, :n]])
+            if not vis.any():
+                continue
+            ki, vi = k[vis], v[vis]
+            for h in range(Hq):
+                kh, vh = ki[:, h // (Hq // Hk)], vi[:, h // (Hq // Hk)]
+                s = kh @ q[b, i, h].double() * scale
+                lse[b, i, h] = torch.logsumexp(s, 0)
+                p = torch.softmax(s, 0)
+                o[b, i, h], A[b, i, h] = p @ vh, p @ vh.abs()
+                E[b, i, h] = (kh.abs() @ q[b, i, h].double().abs()).max() * scale
+    return o, lse, A, E

@@ -72,6 +72,22 @@ def test_norm_rope_backward(L):
     assert _back(L, D=32) == UNS
 
 
+def _attn(L, q=A(1), k=A(2), v=A(3), table=A(4), ctx=A(5), mask=A(6), scale=0.1, o=A(7), lse=A(8), B=2, N=4, Hq=4, Hk=2, D=128,
+          P=9, page=16, M=4, dt=1, ws=A(9), n=1 << 34):
+    return L.gdr_tree_attn(q, k, v, table, ctx, None, mask, scale, o, lse, B, N, Hq, Hk, D, P, page, M, dt, ws, n, None)
+
+
+def test_tree_attn(L):
+    need = L.gdr_tree_attn_workspace_bytes(128)
+    assert need > 0 and L.gdr_tree_attn_workspace_bytes(80) == 0
+    for kw in (dict(q=None), dict(v=None), dict(table=None), dict(o=None), dict(N=0), dict(Hq=5), dict(scale=0.0), dict(scale=-1.0),
+               dict(scale=float("nan")), dict(scale=float("inf")), dict(k=off(2)), dict(mask=off(6)), dict(lse=off(8, 2)),
+               dict(ws=None), dict(n=need - 1), dict(o=A(1)), dict(lse=A(7)), dict(o=A(3)), dict(ws=off(2, 64)), dict(P=0)):
+        assert _attn(L, **kw) == INV, kw
+    for kw in (dict(D=32), dict(dt=0), dict(page=48), dict(Hq=258, Hk=2), dict(B=70000)):
+        assert _attn(L, **kw) == UNS, kw
+
+
 def _verify(L, tokens=A(1), p=A(2), q=A(3), path=A(4), nxt=A(5), B=2, N=4, V=100, dt=0, u=A(7)):
     return L.gdr_verify_draft(tokens, A(8), A(9), p, q, u, A(10), path, A(11), nxt, B, N, V, dt, None)
 
