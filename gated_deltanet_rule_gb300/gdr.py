@@ -145,12 +145,13 @@ def _check(status: int) -> None:
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream(stream) -> int:
+    if stream is None:   # the raw handle: building a Stream object costs more than a small kernel
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -470,55 +471,65 @@ def gdr_backward_chunked(q, k, v, g, beta, S0, dO, dS_T=None, ws=None, stream=No
 
 # --------------------------------------------------------------------------------------------------
 # softmax-attention layers: drafted tokens over a cache of pages
+#
+# Single-token calls take a few microseconds of GPU time, so these bindings check with one plain
+# condition each and build a message only to raise it.
 # --------------------------------------------------------------------------------------------------
-def _need_ints(**tensors):
-    for name, t in tensors.items():
-        if t is not None:
-            _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == torch.int32 and t.is_contiguous(),
-                  f"{name} must be a contiguous CUDA int32 tensor")
+def _is(t, dtype, shape=None) -> bool:
+    """A contiguous CUDA tensor of this dtype (and shape)."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous()
+            and (shape is None or t.shape == shape))
 
 
-def _heads(name, t, like=None):
+def _heads(name, t, like):
     """Strides (token, head) of [B, N, H, D], which may be a slice of a wider projection."""
-    _need(isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 4, f"{name} must be a CUDA tensor [B, N, H, D]")
-    _need(t.shape[3] == 1 or t.stride(3) == 1, f"{name}: the last dimension must be contiguous")
-    if like is not None:
-        _need(t.dtype == like.dtype and t.shape[:2] == like.shape[:2] and t.shape[3] == like.shape[3],
-              f"{name} must share q's dtype, rows, tokens and head dimension")
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 4):
+        raise ValueError(f"{name} must be a CUDA tensor [B, N, H, D]")
     B, N, H, Dk = t.shape
-    tok = t.stride(1) if N > 1 else (t.stride(0) if B > 1 else H * Dk)
-    _need(B == 1 or N == 1 or t.stride(0) == N * tok, f"{name}: tokens of all rows must lie at one stride")
-    return tok, (t.stride(2) if H > 1 else Dk)
+    sb, sn, sh, sd = t.stride()
+    if t is not like and not (t.dtype is like.dtype and (B, N) == like.shape[:2] and Dk == like.shape[3]):
+        raise ValueError(f"{name} must share q's dtype, rows, tokens and head dimension")
+    if sd != 1 and Dk > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    tok = sn if N > 1 else (sb if B > 1 else H * Dk)
+    if B > 1 and N > 1 and sb != N * tok:
+        raise ValueError(f"{name}: tokens of all rows must lie at one stride")
+    return tok, (sh if H > 1 else Dk)
 
 
 def _rope_common(q, k, q_w, k_w, inv_freq, pos):
-    q_tok, q_head = _heads("q", q)
+    q_tok, q_head = _heads("q", q, q)
     k_tok, k_head = _heads("k", k, q)
     B, N, Hq, Dk = q.shape
-    for name, w in (("q_w", q_w), ("k_w", k_w)):
-        _need(isinstance(w, torch.Tensor) and w.is_cuda and w.dtype == torch.float32 and w.shape == (Dk,)
-              and w.is_contiguous(), f"{name} must be contiguous CUDA float32 [D]")
-    _need(isinstance(inv_freq, torch.Tensor) and inv_freq.is_cuda and inv_freq.dtype == torch.float64
-          and inv_freq.dim() == 1 and inv_freq.is_contiguous(), "inv_freq must be contiguous CUDA float64 [R / 2]")
-    _need_ints(pos=pos)
-    _need(pos.shape == (B, N), "pos must be [B, N]")
+    if not (_is(q_w, torch.float32, (Dk,)) and _is(k_w, torch.float32, (Dk,))):
+        raise ValueError("q_w and k_w must be contiguous CUDA float32 [D]")
+    if not (_is(inv_freq, torch.float64) and inv_freq.dim() == 1):
+        raise ValueError("inv_freq must be contiguous CUDA float64 [R / 2]")
+    if not _is(pos, torch.int32, (B, N)):
+        raise ValueError("pos must be contiguous CUDA int32 [B, N]")
     return B, N, Hq, k.shape[2], Dk, 2 * inv_freq.shape[0], q_tok, q_head, k_tok, k_head, _dtype_code(q)
 
 
-def _check_out(name, t, shape, dtype):
-    _need(t.is_cuda and t.is_contiguous() and tuple(t.shape) == tuple(shape) and t.dtype == dtype,
-          f"{name} must be a contiguous CUDA tensor of shape {tuple(shape)} and dtype {dtype}")
+def _pages(k_pages, v_pages, table, ctx, B, Dk, dtype):
+    """(P, page, Hk, M)"""
+    if not (_is(k_pages, dtype) and k_pages.dim() == 4 and _is(v_pages, dtype, k_pages.shape) and k_pages.shape[3] == Dk):
+        raise ValueError("k_pages and v_pages must be contiguous CUDA tensors [P, page, Hk, D] of q's dtype and head dimension")
+    if not (_is(table, torch.int32) and table.dim() == 2 and table.shape[0] == B and _is(ctx, torch.int32, (B,))):
+        raise ValueError("table must be contiguous CUDA int32 [B, M] and ctx [B]")
+    return *k_pages.shape[:3], table.shape[1]
 
 
-def _pages(k_pages, v_pages, table, ctx, B, Hk, Dk, dtype):
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        _need(isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and t.dim() == 4 and t.dtype == dtype
-              and t.shape == k_pages.shape, f"{name} must be a contiguous CUDA tensor [P, page, Hk, D] of q's dtype")
-    P, page, H, Dp = k_pages.shape
-    _need((H, Dp) == (Hk, Dk), "pages must hold k's heads and head dimension")
-    _need_ints(table=table, ctx=ctx)
-    _need(table.dim() == 2 and table.shape[0] == B and ctx.shape == (B,), "table must be [B, M] and ctx [B]")
-    return P, page, table.shape[1]
+def _out(name, t, shape, dtype, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not _is(t, dtype, shape):
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of shape {tuple(shape)} and dtype {dtype}")
+    return t
+
+
+def _lengths(lengths, B):
+    if lengths is not None and not _is(lengths, torch.int32, (B,)):
+        raise ValueError("lengths must be contiguous CUDA int32 [B]")
 
 
 def gdr_qk_norm_rope(q, k, q_w, k_w, inv_freq, pos, eps: float = 1e-6, interleaved: bool = False, q_out=None,
@@ -527,13 +538,11 @@ def gdr_qk_norm_rope(q, k, q_w, k_w, inv_freq, pos, eps: float = 1e-6, interleav
     place) and the rotation of its first R = 2 len(inv_freq) elements by pos [B,N] int32 times inv_freq
     (float64). Returns (q_out, k_out), contiguous, in q's dtype."""
     B, N, Hq, Hk, Dk, R, q_tok, q_head, k_tok, k_head, dt = _rope_common(q, k, q_w, k_w, inv_freq, pos)
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-    k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device) if k_out is None else k_out
-    _check_out("q_out", q_out, q.shape, q.dtype)
-    _check_out("k_out", k_out, k.shape, q.dtype)
-    _check(lib().gdr_qk_norm_rope(_p(q), _p(k), _p(q_w), _p(k_w), _p(inv_freq), _p(pos), float(eps), int(interleaved),
-                                  _p(q_out), _p(k_out), B, N, Hq, Hk, Dk, R, q_tok, q_head, k_tok, k_head, dt,
-                                  _stream(stream)))
+    q_out = _out("q_out", q_out, q.shape, q.dtype, q.device)
+    k_out = _out("k_out", k_out, k.shape, q.dtype, q.device)
+    _check(lib().gdr_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_w.data_ptr(), k_w.data_ptr(), inv_freq.data_ptr(),
+                                  pos.data_ptr(), eps, interleaved, q_out.data_ptr(), k_out.data_ptr(), B, N, Hq, Hk, Dk,
+                                  R, q_tok, q_head, k_tok, k_head, dt, _stream(stream)))
     return q_out, k_out
 
 
@@ -543,14 +552,14 @@ def gdr_qk_norm_rope_append(q, k, v, q_w, k_w, inv_freq, pos, k_pages, v_pages, 
     ctx[b] + i (i < lengths[b] where given). Returns q_out."""
     B, N, Hq, Hk, Dk, R, q_tok, q_head, k_tok, k_head, dt = _rope_common(q, k, q_w, k_w, inv_freq, pos)
     v_tok, v_head = _heads("v", v, q)
-    _need(v.shape == k.shape, "v must have k's shape")
-    P, page, M = _pages(k_pages, v_pages, table, ctx, B, Hk, Dk, q.dtype)
-    _need_ints(lengths=lengths)
-    _need(lengths is None or lengths.shape == (B,), "lengths must be [B]")
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-    _check_out("q_out", q_out, q.shape, q.dtype)
-    _check(lib().gdr_qk_norm_rope_append(_p(q), _p(k), _p(v), _p(q_w), _p(k_w), _p(inv_freq), _p(pos), float(eps),
-                                         int(interleaved), _p(q_out), _p(k_pages), _p(v_pages), _p(table), _p(ctx),
+    P, page, H, M = _pages(k_pages, v_pages, table, ctx, B, Dk, q.dtype)
+    if v.shape[2] != Hk or H != Hk:
+        raise ValueError("v and the pages must have k's heads")
+    _lengths(lengths, B)
+    q_out = _out("q_out", q_out, q.shape, q.dtype, q.device)
+    _check(lib().gdr_qk_norm_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_w.data_ptr(), k_w.data_ptr(),
+                                         inv_freq.data_ptr(), pos.data_ptr(), eps, interleaved, q_out.data_ptr(),
+                                         k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), ctx.data_ptr(),
                                          _p(lengths), P, page, M, B, N, Hq, Hk, Dk, R, q_tok, q_head, k_tok, k_head,
                                          v_tok, v_head, dt, _stream(stream)))
     return q_out
@@ -561,17 +570,17 @@ def gdr_qk_norm_rope_backward(q, k, q_w, k_w, inv_freq, pos, dq_out, dk_out, eps
     """Gradients of gdr_qk_norm_rope from dq_out, dk_out (contiguous, q's dtype): (dq, dk, dq_w, dk_w),
     all float32."""
     B, N, Hq, Hk, Dk, R, q_tok, q_head, k_tok, k_head, dt = _rope_common(q, k, q_w, k_w, inv_freq, pos)
-    _check_out("dq_out", dq_out, q.shape, q.dtype)
-    _check_out("dk_out", dk_out, k.shape, q.dtype)
-    f32 = dict(dtype=torch.float32, device=q.device)
-    dq, dk = torch.empty(q.shape, **f32), torch.empty(k.shape, **f32)
-    dq_w, dk_w = torch.empty(Dk, **f32), torch.empty(Dk, **f32)
+    if not (_is(dq_out, q.dtype, q.shape) and _is(dk_out, q.dtype, k.shape)):
+        raise ValueError("dq_out and dk_out must be contiguous CUDA tensors like q and k")
+    dev = q.device
+    dq, dk = (torch.empty(t.shape, dtype=torch.float32, device=dev) for t in (q, k))
+    dq_w, dk_w = (torch.empty(Dk, dtype=torch.float32, device=dev) for _ in "qk")
     if ws is None:
-        ws = torch.empty(max(int(lib().gdr_qk_norm_rope_backward_workspace_bytes(Dk)), 1), dtype=torch.uint8,
-                         device=q.device)
-    _check(lib().gdr_qk_norm_rope_backward(_p(q), _p(k), _p(q_w), _p(k_w), _p(inv_freq), _p(pos), _p(dq_out),
-                                           _p(dk_out), float(eps), int(interleaved), _p(dq), _p(dk), _p(dq_w),
-                                           _p(dk_w), B, N, Hq, Hk, Dk, R, q_tok, q_head, k_tok, k_head, dt, _p(ws),
+        ws = torch.empty(max(int(lib().gdr_qk_norm_rope_backward_workspace_bytes(Dk)), 16), dtype=torch.uint8, device=dev)
+    _check(lib().gdr_qk_norm_rope_backward(q.data_ptr(), k.data_ptr(), q_w.data_ptr(), k_w.data_ptr(),
+                                           inv_freq.data_ptr(), pos.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), eps,
+                                           interleaved, dq.data_ptr(), dk.data_ptr(), dq_w.data_ptr(), dk_w.data_ptr(),
+                                           B, N, Hq, Hk, Dk, R, q_tok, q_head, k_tok, k_head, dt, ws.data_ptr(),
                                            ws.numel() * ws.element_size(), _stream(stream)))
     return dq, dk, dq_w, dk_w
 
@@ -586,29 +595,23 @@ def gdr_tree_attn(q, k_pages, v_pages, table, ctx, lengths=None, mask=None, scal
     mask [B,N,ceil(N/64)] int64 (bit j: node i sees node j; None: nodes 0 .. i) lets them see, the pages
     already holding the nodes' keys and values. scale defaults to D^-1/2. Returns o, or (o, lse [B,N,Hq]
     float32) with want_lse or lse given."""
-    _need(isinstance(q, torch.Tensor) and q.is_cuda and q.is_contiguous() and q.dim() == 4 and q.dtype == torch.bfloat16,
-          "q must be a contiguous CUDA bfloat16 tensor [B, N, Hq, D]")
+    if not (_is(q, torch.bfloat16) and q.dim() == 4):
+        raise ValueError("q must be a contiguous CUDA bfloat16 tensor [B, N, Hq, D]")
     B, N, Hq, Dk = q.shape
-    _need(isinstance(k_pages, torch.Tensor) and k_pages.dim() == 4, "k_pages must be [P, page, Hk, D]")
-    Hk = k_pages.shape[2]
-    P, page, M = _pages(k_pages, v_pages, table, ctx, B, Hk, Dk, q.dtype)
-    _need_ints(lengths=lengths)
-    _need(lengths is None or lengths.shape == (B,), "lengths must be [B]")
-    if mask is not None:
-        _need(mask.is_cuda and mask.is_contiguous() and mask.dtype == torch.int64 and mask.shape == (B, N, (N + 63) // 64),
-              "mask must be contiguous CUDA int64 [B, N, ceil(N / 64)]")
-    if o is None:
-        o = torch.empty_like(q)
-    _check_out("o", o, q.shape, q.dtype)
-    if lse is None and want_lse:
-        lse = torch.empty(B, N, Hq, dtype=torch.float32, device=q.device)
-    if lse is not None:
-        _check_out("lse", lse, (B, N, Hq), torch.float32)
+    P, page, Hk, M = _pages(k_pages, v_pages, table, ctx, B, Dk, torch.bfloat16)
+    _lengths(lengths, B)
+    if mask is not None and not _is(mask, torch.int64, (B, N, (N + 63) // 64)):
+        raise ValueError("mask must be contiguous CUDA int64 [B, N, ceil(N / 64)]")
+    dev = q.device
+    o = _out("o", o, q.shape, torch.bfloat16, dev)
+    if lse is not None or want_lse:
+        lse = _out("lse", lse, (B, N, Hq), torch.float32, dev)
     if ws is None:
-        ws = torch.empty(max(tree_attn_workspace_bytes(Dk), 16), dtype=torch.uint8, device=q.device)
-    _check(lib().gdr_tree_attn(_p(q), _p(k_pages), _p(v_pages), _p(table), _p(ctx), _p(lengths), _p(mask),
-                               float(Dk ** -0.5 if scale is None else scale), _p(o), _p(lse), B, N, Hq, Hk, Dk, P, page, M,
-                               GDR_BF16, _p(ws), ws.numel() * ws.element_size(), _stream(stream)))
+        ws = torch.empty(max(tree_attn_workspace_bytes(Dk), 16), dtype=torch.uint8, device=dev)
+    _check(lib().gdr_tree_attn(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), ctx.data_ptr(),
+                               _p(lengths), _p(mask), Dk ** -0.5 if scale is None else scale, o.data_ptr(), _p(lse), B, N,
+                               Hq, Hk, Dk, P, page, M, GDR_BF16, ws.data_ptr(), ws.numel() * ws.element_size(),
+                               _stream(stream)))
     return o if lse is None else (o, lse)
 
 
@@ -617,45 +620,43 @@ def gdr_verify_draft(tokens, parents, lengths, p, q, u, u_next, path=None, n_pat
     target's probabilities p [B,N,V] and the drafts' q [B,N,V] (None: given drafts) with the uniform
     numbers u [B,N], u_next [B]. Returns (path [B,N] of accepted nodes, root first, -1 after them;
     n_path [B]; next_token [B])."""
-    _need_ints(tokens=tokens, parents=parents, lengths=lengths, path=path, n_path=n_path, next_token=next_token)
-    _need(isinstance(p, torch.Tensor) and p.is_cuda and p.is_contiguous() and p.dim() == 3,
-          "p must be a contiguous CUDA tensor [B, N, V]")
+    if not (isinstance(p, torch.Tensor) and p.dim() == 3 and _is(p, p.dtype)):
+        raise ValueError("p must be a contiguous CUDA tensor [B, N, V]")
+    dt = _dtype_code(p)
     B, N, V = p.shape
-    _need(q is None or (q.is_cuda and q.is_contiguous() and q.shape == p.shape and q.dtype == p.dtype),
-          "q must be None or like p")
-    _need(tokens.shape == (B, N) and parents.shape == (B, N) and lengths.shape == (B,),
-          "tokens and parents must be [B, N] and lengths [B]")
-    for name, t, shape in (("u", u, (B, N)), ("u_next", u_next, (B,))):
-        _need(t.is_cuda and t.is_contiguous() and t.dtype == torch.float32 and tuple(t.shape) == shape,
-              f"{name} must be contiguous CUDA float32 {shape}")
-    i32 = dict(dtype=torch.int32, device=p.device)
-    path = torch.empty(B, N, **i32) if path is None else path
-    n_path = torch.empty(B, **i32) if n_path is None else n_path
-    next_token = torch.empty(B, **i32) if next_token is None else next_token
-    _need(path.shape == (B, N) and n_path.shape == (B,) and next_token.shape == (B,),
-          "path must be [B, N], n_path and next_token [B]")
-    _check(lib().gdr_verify_draft(_p(tokens), _p(parents), _p(lengths), _p(p), _p(q), _p(u), _p(u_next), _p(path),
-                                  _p(n_path), _p(next_token), B, N, V, _dtype_code(p), _stream(stream)))
+    if q is not None and not _is(q, p.dtype, p.shape):
+        raise ValueError("q must be None or like p")
+    if not (_is(tokens, torch.int32, (B, N)) and _is(parents, torch.int32, (B, N)) and _is(lengths, torch.int32, (B,))):
+        raise ValueError("tokens and parents must be contiguous CUDA int32 [B, N] and lengths [B]")
+    if not (_is(u, torch.float32, (B, N)) and _is(u_next, torch.float32, (B,))):
+        raise ValueError("u must be contiguous CUDA float32 [B, N] and u_next [B]")
+    dev = p.device
+    path = _out("path", path, (B, N), torch.int32, dev)
+    n_path = _out("n_path", n_path, (B,), torch.int32, dev)
+    next_token = _out("next_token", next_token, (B,), torch.int32, dev)
+    _check(lib().gdr_verify_draft(tokens.data_ptr(), parents.data_ptr(), lengths.data_ptr(), p.data_ptr(), _p(q),
+                                  u.data_ptr(), u_next.data_ptr(), path.data_ptr(), n_path.data_ptr(),
+                                  next_token.data_ptr(), B, N, V, dt, _stream(stream)))
     return path, n_path, next_token
 
 
 def _cache(k_cache, v_cache):
     """(layers, P, page, row bytes) of caches [layers, P, page, Hk, D]."""
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _need(isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous() and t.dim() == 5
-              and t.shape == k_cache.shape and t.dtype == k_cache.dtype,
-              f"{name} must be a contiguous CUDA tensor [layers, P, page, Hk, D]")
+    if not (isinstance(k_cache, torch.Tensor) and k_cache.dim() == 5 and _is(k_cache, k_cache.dtype)
+            and _is(v_cache, k_cache.dtype, k_cache.shape)):
+        raise ValueError("k_cache and v_cache must be contiguous CUDA tensors [layers, P, page, Hk, D] of one dtype")
     layers, P, page, Hk, Dk = k_cache.shape
     return layers, P, page, Hk * Dk * k_cache.element_size()
 
 
-def _row_list(table, ctx, refs, **lists):
-    _need_ints(table=table, ctx=ctx, refs=refs, **lists)
-    _need(table.dim() == 2 and ctx.shape == (table.shape[0],) and refs.dim() == 1,
-          "table must be [rows, M], ctx [rows] and refs [P]")
-    n = [t.shape for t in lists.values()]
-    _need(all(len(x) == 1 and x == n[0] for x in n), "row lists must be [F]")
-    return n[0][0], table.shape[0], table.shape[1]
+def _row_list(table, ctx, refs, rows, more=None):
+    """(F, rows, M)"""
+    if not (_is(table, torch.int32) and table.dim() == 2 and _is(ctx, torch.int32, table.shape[:1])
+            and _is(refs, torch.int32) and refs.dim() == 1):
+        raise ValueError("table must be contiguous CUDA int32 [rows, M], ctx [rows] and refs [P]")
+    if not (_is(rows, torch.int32) and rows.dim() == 1 and (more is None or _is(more, torch.int32, rows.shape))):
+        raise ValueError("row lists must be contiguous CUDA int32 [F]")
+    return rows.shape[0], *table.shape
 
 
 def cache_workspace_bytes(F: int, M: int) -> int:
@@ -670,40 +671,45 @@ def _cache_ws(ws, F, M, device):
 
 def gdr_cache_reserve(table, ctx, refs, rows, extra: int, page: int, ws=None, stream=None) -> None:
     """Gives rows (int32 [F]) pages so that ctx + extra positions of each fit; table, refs in place."""
-    F, R, M = _row_list(table, ctx, refs, rows=rows)
+    F, R, M = _row_list(table, ctx, refs, rows)
     ws, ws_bytes = _cache_ws(ws, F, M, table.device)
-    _check(lib().gdr_cache_reserve(_p(table), _p(ctx), _p(refs), _p(rows), int(extra), F, R, M, refs.shape[0], int(page),
-                                   _p(ws), ws_bytes, _stream(stream)))
+    _check(lib().gdr_cache_reserve(table.data_ptr(), ctx.data_ptr(), refs.data_ptr(), rows.data_ptr(), extra, F, R, M,
+                                   refs.shape[0], page, ws.data_ptr(), ws_bytes, _stream(stream)))
 
 
 def gdr_cache_fork(k_cache, v_cache, table, ctx, refs, src, dst, ws=None, stream=None) -> None:
     """Row dst[f] becomes a copy of row src[f]: full pages shared, the last one copied. In place."""
     layers, P, page, row_bytes = _cache(k_cache, v_cache)
-    F, R, M = _row_list(table, ctx, refs, dst=dst, src=src)
-    _need(refs.shape == (P,), "refs must be [P]")
+    F, R, M = _row_list(table, ctx, refs, dst, src)
+    if refs.shape[0] != P:
+        raise ValueError("refs must be [P]")
     ws, ws_bytes = _cache_ws(ws, F, M, table.device)
-    _check(lib().gdr_cache_fork(_p(k_cache), _p(v_cache), _p(table), _p(ctx), _p(refs), _p(src), _p(dst), F, R, M, layers,
-                                P, page, row_bytes, _p(ws), ws_bytes, _stream(stream)))
+    _check(lib().gdr_cache_fork(k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), ctx.data_ptr(), refs.data_ptr(),
+                                src.data_ptr(), dst.data_ptr(), F, R, M, layers, P, page, row_bytes, ws.data_ptr(),
+                                ws_bytes, _stream(stream)))
 
 
 def gdr_cache_free(table, ctx, refs, rows, stream=None) -> None:
     """Gives the pages of rows (int32 [F]) back; table, ctx, refs in place."""
-    F, R, M = _row_list(table, ctx, refs, rows=rows)
-    _check(lib().gdr_cache_free(_p(table), _p(ctx), _p(refs), _p(rows), F, R, M, refs.shape[0], _stream(stream)))
+    F, R, M = _row_list(table, ctx, refs, rows)
+    _check(lib().gdr_cache_free(table.data_ptr(), ctx.data_ptr(), refs.data_ptr(), rows.data_ptr(), F, R, M,
+                                refs.shape[0], _stream(stream)))
 
 
 def gdr_cache_compact(k_cache, v_cache, table, ctx, path, n_path, new_ctx=None, stream=None):
     """Moves the entries of the accepted paths (gdr_verify_draft's path, n_path) to the front of their
     rows in every layer; returns new_ctx = ctx + n_path (which may not be ctx itself)."""
     layers, P, page, row_bytes = _cache(k_cache, v_cache)
-    _need_ints(table=table, ctx=ctx, path=path, n_path=n_path, new_ctx=new_ctx)
-    _need(path.dim() == 2 and table.dim() == 2, "path must be [B, W] and table [B, M]")
+    if not (_is(path, torch.int32) and path.dim() == 2):
+        raise ValueError("path must be contiguous CUDA int32 [B, W]")
     B, W = path.shape
-    new_ctx = torch.empty_like(ctx) if new_ctx is None else new_ctx
-    _need(table.shape[0] == B and ctx.shape == (B,) and n_path.shape == (B,) and new_ctx.shape == (B,),
-          "table, ctx, n_path and new_ctx must have path's rows")
-    _check(lib().gdr_cache_compact(_p(k_cache), _p(v_cache), _p(table), _p(ctx), _p(path), _p(n_path), _p(new_ctx), B, W,
-                                   table.shape[1], layers, P, page, row_bytes, _stream(stream)))
+    if not (_is(table, torch.int32) and table.dim() == 2 and table.shape[0] == B and _is(ctx, torch.int32, (B,))
+            and _is(n_path, torch.int32, (B,))):
+        raise ValueError("table must be contiguous CUDA int32 [B, M], ctx and n_path [B]")
+    new_ctx = _out("new_ctx", new_ctx, (B,), torch.int32, ctx.device)
+    _check(lib().gdr_cache_compact(k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), ctx.data_ptr(),
+                                   path.data_ptr(), n_path.data_ptr(), new_ctx.data_ptr(), B, W, table.shape[1], layers, P,
+                                   page, row_bytes, _stream(stream)))
     return new_ctx
 
 
