@@ -4,11 +4,14 @@
 // Pairs are (j, j + R/2), or (2j, 2j + 1) when interleaved. Forward (dense outputs, or k and v left
 // in a cache's pages) and gradient.
 //
-// Layout: D/8 lanes hold one head, eight elements each, chosen so that both members of a pair lie in
-// one lane: in the half-split form a lane of the rotated part holds four elements at 4 l and their
-// partners at R/2 + 4 l, every other lane eight neighbours. Pair j of lane l is 4 l + (0..3) in both
-// forms, so a lane's four angles serve every head of its token and the loop over heads needs no
-// exchange but the sum of squares (shuffles over the head's lanes).
+// Layout: D/16 lanes hold one head, two runs of eight elements each (16-byte loads of bf16), chosen so
+// that both members of a pair lie in one lane: in the half-split form a lane of the rotated part holds
+// eight elements at 8 l and their partners at R/2 + 8 l, every other lane sixteen neighbours. Pair j of
+// lane l is 8 l + (0..7) in both forms. The head's sum of squares is the only exchange (shuffles).
+//
+// A block takes the heads of one kind (queries, keys, or values to be copied) of a few tokens: it forms
+// the tokens' cosines and sines once in shared memory, one entry a thread, and its warps then walk the
+// (token, head) rows. Forming them in every warp instead cost a third of the instructions.
 //
 // Angles: pos inv_freq is formed in turns modulo one by 64-bit integer arithmetic (inv_freq / 2 pi as
 // a 64-bit binary fraction, times the position, dropping whole turns), exact to 2^-32 turn at any
@@ -25,34 +28,48 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;   // heads per lane in flight: 4 x 2 loads of 8 or 16 bytes
+constexpr int kPairs = 2048;   // (token, pair) angles of a block
 
+// Eight consecutive elements as loaded.
 template <typename T>
-struct Raw;   // four consecutive elements as loaded
+struct Raw;
 template <>
 struct Raw<__nv_bfloat16> {
-  uint2 u;
-  __device__ void load(const __nv_bfloat16* p) { u = __ldg(reinterpret_cast<const uint2*>(p)); }
-  __device__ void get(float* x) const {
-    x[0] = __uint_as_float(u.x << 16);
-    x[1] = __uint_as_float(u.x & 0xFFFF0000u);
-    x[2] = __uint_as_float(u.y << 16);
-    x[3] = __uint_as_float(u.y & 0xFFFF0000u);
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void get(float* x) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[2 * e] = __uint_as_float(w[e] << 16);
+      x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+    }
   }
-  __device__ static void put(__nv_bfloat16* p, const float* x) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(ptx::pack_bf16x2(x[0], x[1]), ptx::pack_bf16x2(x[2], x[3]));
+  __device__ __forceinline__ static void put(__nv_bfloat16* p, const float* x) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(ptx::pack_bf16x2(x[0], x[1]), ptx::pack_bf16x2(x[2], x[3]),
+                                              ptx::pack_bf16x2(x[4], x[5]), ptx::pack_bf16x2(x[6], x[7]));
   }
-  __device__ void copy(__nv_bfloat16* p) const { *reinterpret_cast<uint2*>(p) = u; }
+  __device__ __forceinline__ void copy(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
 };
 template <>
 struct Raw<float> {
-  float4 u;
-  __device__ void load(const float* p) { u = __ldg(reinterpret_cast<const float4*>(p)); }
-  __device__ void get(float* x) const { x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w; }
-  __device__ static void put(float* p, const float* x) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  float4 u, v;
+  __device__ __forceinline__ void load(const float* p) {
+    u = __ldg(reinterpret_cast<const float4*>(p));
+    v = __ldg(reinterpret_cast<const float4*>(p) + 1);
   }
-  __device__ void copy(float* p) const { *reinterpret_cast<float4*>(p) = u; }
+  __device__ __forceinline__ void get(float* x) const {
+    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+    x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+  }
+  __device__ __forceinline__ static void put(float* p, const float* x) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
+  __device__ __forceinline__ void copy(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = u;
+    reinterpret_cast<float4*>(p)[1] = v;
+  }
 };
 
 // inv_freq / (2 pi) modulo one as a 64-bit binary fraction, from the bits of the double.
@@ -84,37 +101,51 @@ __device__ __forceinline__ void turn_sincos(uint64_t frac, int pos, float& c, fl
   if (quad & 2) s = -s;
 }
 
-// What a lane holds: its two runs of four elements of a head, and its pairs' turn fractions.
+// What a lane holds of a head: two runs of eight elements.
 template <int D>
 struct Lane {
-  static constexpr int kLanes = D / 8;         // lanes of one head
-  static constexpr int kHeads = 32 / kLanes;   // heads of one warp
+  static constexpr int kLanes = D / 16;        // lanes of one head
+  static constexpr int kHeads = 32 / kLanes;   // rows of one warp
   int sub, l, off0, off1;
   bool turns;
-  uint64_t frac[4];
-  __device__ void init(const RopeArgs& a) {
+  __device__ __forceinline__ explicit Lane(const RopeArgs& a) {
     const int lane = threadIdx.x & 31;
     sub = lane / kLanes;
     l = lane % kLanes;
-    turns = 8 * l < a.R;
+    turns = 16 * l < a.R;
     const bool split = turns && !a.interleaved;
-    off0 = split ? 4 * l : 8 * l;
-    off1 = split ? a.R / 2 + 4 * l : 8 * l + 4;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) frac[j] = turns ? turn_fraction(a.inv_freq[4 * l + j]) : 0;
-  }
-  __device__ void angles(int pos, float* c, float* s) const {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) turn_sincos(frac[j], pos, c[j], s[j]);
+    off0 = split ? 8 * l : 16 * l;
+    off1 = split ? a.R / 2 + 8 * l : 16 * l + 8;
   }
 };
 
-// Turn a lane's eight values; sgn = -1 turns back. A lane outside the rotated part has angle zero.
-__device__ __forceinline__ void turn(float* y, const float* c, const float* s, bool interleaved, float sgn) {
+// cos and sin of a block's tokens [t0, t0 + n) into cs[token][pair][cos | sin runs of eight].
+__device__ __forceinline__ void form_angles(const RopeArgs& a, long long t0, int n, float* cs) {
+  const int half = a.R / 2;
+  for (int x = threadIdx.x; x < n * half; x += kThreads) {
+    const int t = x / half, j = x - t * half;
+    float c, s;
+    turn_sincos(turn_fraction(__ldg(a.inv_freq + j)), __ldg(a.pos + t0 + t), c, s);
+    float* at = cs + t * a.R + (j >> 3) * 16 + (j & 7);   // lane l's eight cosines, then its eight sines
+    at[0] = c;
+    at[8] = s;
+  }
+}
+
+// Turn a lane's sixteen values by its pairs' angles; kBack turns back.
+template <bool kInter, bool kBack>
+__device__ __forceinline__ void turn(float* y, const float* cs) {
+  float c[8], s[8];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int ia = interleaved ? 2 * j : j, ib = interleaved ? 2 * j + 1 : j + 4;
-    const float ya = y[ia], yb = y[ib], sj = sgn * s[j];
+  for (int q = 0; q < 2; ++q) {
+    const float4 cv = reinterpret_cast<const float4*>(cs)[q], sv = reinterpret_cast<const float4*>(cs)[q + 2];
+    c[4 * q] = cv.x; c[4 * q + 1] = cv.y; c[4 * q + 2] = cv.z; c[4 * q + 3] = cv.w;
+    s[4 * q] = sv.x; s[4 * q + 1] = sv.y; s[4 * q + 2] = sv.z; s[4 * q + 3] = sv.w;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int ia = kInter ? 2 * j : j, ib = kInter ? 2 * j + 1 : j + 8;
+    const float ya = y[ia], yb = y[ib], sj = kBack ? -s[j] : s[j];
     y[ia] = ya * c[j] - yb * sj;
     y[ib] = yb * c[j] + ya * sj;
   }
@@ -123,250 +154,284 @@ __device__ __forceinline__ void turn(float* y, const float* c, const float* s, b
 template <int D>
 __device__ __forceinline__ float head_sum(float v) {
 #pragma unroll
-  for (int m = D / 16; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  for (int m = D / 32; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
   return v;
 }
 
-__device__ __forceinline__ void load8(const float* w, int off0, int off1, float* x) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(w + off0)), b = __ldg(reinterpret_cast<const float4*>(w + off1));
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+__device__ __forceinline__ void load16(const float* w, int off0, int off1, float* x) {
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(w + off0) + q), b = __ldg(reinterpret_cast<const float4*>(w + off1) + q);
+    x[4 * q] = a.x; x[4 * q + 1] = a.y; x[4 * q + 2] = a.z; x[4 * q + 3] = a.w;
+    x[8 + 4 * q] = b.x; x[8 + 4 * q + 1] = b.y; x[8 + 4 * q + 2] = b.z; x[8 + 4 * q + 3] = b.w;
+  }
 }
 
-// One warp takes a share of one token's heads (shares interleave: share p takes the head groups p,
-// p + split, ...). HBM-bound: each element is read and written once.
+// The (token, head) row `x` of a block's tokens: token and head by one multiplication (x < 2^16).
+__device__ __forceinline__ void row_at(int x, int H, uint32_t magic, int& t, int& h) {
+  t = (int)__umulhi((uint32_t)x, magic);
+  h = x - t * H;
+  if (h >= H) {   // (magic = floor(2^32 / H): the quotient may be one short)
+    h -= H;
+    ++t;
+  }
+}
+
+// One kind of heads of a block's tokens: their strides, weights and destination.
+template <typename T>
+struct Kind {
+  const T* src;
+  long long tok, head;
+  const float* w;
+  T* out;          // dense rows, or the pages
+  int H, tokens;   // heads; tokens of a block
+};
+
+// Normed, turned and written (kPages: keys into the pages, values copied there). HBM-bound: each element
+// is read and written once, 16 bytes a load, two rows of every lane in flight.
 template <typename T, int D, bool kPages, bool kInter>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a) {
-  const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  __shared__ __align__(16) float cs[2 * kPairs];
+  __shared__ long long slot[kPairs];
+  const Lane<D> ln(a);
   const long long tokens = (long long)a.B * a.N;
-  if (unit >= tokens * a.split) return;
-  const long long token = unit / a.split;
-  const int share = (int)(unit - token * a.split);
-  Lane<D> ln;
-  ln.init(a);
-  const int pos = __ldg(a.pos + token);
-  float c[4], s[4], qw[8], kw[8];
-  ln.angles(pos, c, s);
-  load8(a.q_w, ln.off0, ln.off1, qw);
-  load8(a.k_w, ln.off0, ln.off1, kw);
-  const int heads = a.Hq + (kPages ? 2 : 1) * a.Hk;
-  const int groups = (heads + Lane<D>::kHeads - 1) / Lane<D>::kHeads;
-  long long slot = -1;   // the position's slot in the pages laid end to end
-  if (kPages) {
-    const int b = (int)(token / a.N), i = (int)(token - (long long)b * a.N);
-    const int n = a.lengths ? __ldg(a.lengths + b) : a.N;
-    const int ctx = __ldg(a.ctx + b);
-    if (n < 0 || n > a.N || ctx < 0 || (long long)ctx + n > (long long)a.M * a.page) {
-      if ((threadIdx.x & 31) == 0) atomicCAS(a.err, 0, kErrDeviceIndex);
-    } else if (i < n) {
-      const int at = ctx + i;
-      const int pg = __ldg(a.table + (long long)b * a.M + at / a.page);
-      if (pg < 0 || pg >= a.P) {
-        if ((threadIdx.x & 31) == 0) atomicCAS(a.err, 0, kErrDeviceIndex);
-      } else {
-        slot = (long long)pg * a.page + at % a.page;
+  const int kind = blockIdx.x < a.blocks[0] ? 0 : blockIdx.x < a.blocks[0] + a.blocks[1] ? 1 : 2;
+  const long long block = blockIdx.x - (kind == 0 ? 0 : kind == 1 ? a.blocks[0] : a.blocks[0] + a.blocks[1]);
+  Kind<T> k;
+  if (kind == 0) k = {static_cast<const T*>(a.q), a.q_tok, a.q_head, a.q_w, static_cast<T*>(a.q_out), a.Hq, a.tokens[0]};
+  else if (kind == 1)
+    k = {static_cast<const T*>(a.k), a.k_tok, a.k_head, a.k_w, static_cast<T*>(kPages ? a.k_pages : a.k_out), a.Hk, a.tokens[1]};
+  else k = {static_cast<const T*>(a.v), a.v_tok, a.v_head, nullptr, static_cast<T*>(a.v_pages), a.Hk, a.tokens[1]};
+  const long long t0 = block * k.tokens;
+  const int n = (int)min((long long)k.tokens, tokens - t0), rows = n * k.H;
+  const uint32_t magic = k.H == 1 ? 0xFFFFFFFFu : (uint32_t)((1ull << 32) / k.H);
+  const int warp = threadIdx.x >> 5, step = kWarps * Lane<D>::kHeads;
+  const bool to_pages = kPages && kind > 0;
+
+  // the first rows are on their way while the angles are formed
+  constexpr int kAhead = 2;
+  Raw<T> raw[kAhead][2];
+  auto load = [&](int u, int x) {
+    if (x >= rows) return;
+    int t, h;
+    row_at(x, k.H, magic, t, h);
+    const T* src = k.src + (t0 + t) * k.tok + h * k.head;
+    raw[u][0].load(src + ln.off0);
+    raw[u][1].load(src + ln.off1);
+  };
+  const int x0 = warp * Lane<D>::kHeads + ln.sub;
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) load(u, x0 + u * step);
+  float w[16];
+  if (kind < 2) {
+    load16(k.w, ln.off0, ln.off1, w);
+    form_angles(a, t0, n, cs);
+  }
+  if (to_pages) {
+    for (int t = threadIdx.x; t < n; t += kThreads) {
+      const int b = (int)((t0 + t) / a.N), i = (int)(t0 + t - (long long)b * a.N);
+      const int len = a.lengths ? __ldg(a.lengths + b) : a.N, ctx = __ldg(a.ctx + b);
+      long long at = -1;   // the position's slot in the pages laid end to end
+      if (len < 0 || len > a.N || ctx < 0 || (long long)ctx + len > (long long)a.M * a.page) {
+        atomicCAS(a.err, 0, kErrDeviceIndex);
+      } else if (i < len) {
+        const int pos = ctx + i, pg = __ldg(a.table + (long long)b * a.M + pos / a.page);
+        if (pg < 0 || pg >= a.P) atomicCAS(a.err, 0, kErrDeviceIndex);
+        else at = (long long)pg * a.page + pos % a.page;
       }
+      slot[t] = at;
     }
   }
-  for (int g0 = share; g0 < groups; g0 += a.split * kUnroll) {
-    Raw<T> raw[kUnroll][2];
+  __syncthreads();
+  for (int xw = warp * Lane<D>::kHeads; xw < rows; xw += kAhead * step) {   // the same in every lane
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int head = (g0 + u * a.split) * Lane<D>::kHeads + ln.sub;
-      if (head >= heads) continue;
-      const T* src = head < a.Hq ? static_cast<const T*>(a.q) + token * a.q_tok + head * a.q_head
-                     : (!kPages || head < a.Hq + a.Hk)
-                         ? static_cast<const T*>(a.k) + token * a.k_tok + (head - a.Hq) * a.k_head
-                         : static_cast<const T*>(a.v) + token * a.v_tok + (head - a.Hq - a.Hk) * a.v_head;
-      raw[u][0].load(src + ln.off0);
-      raw[u][1].load(src + ln.off1);
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int head = (g0 + u * a.split) * Lane<D>::kHeads + ln.sub;
-      if ((g0 + u * a.split) * Lane<D>::kHeads >= heads) break;   // the same in every lane
-      const bool live = head < heads;
-      float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (live) {
-        raw[u][0].get(y);
-        raw[u][1].get(y + 4);
-      }
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-      ss = head_sum<D>(ss);
-      const float r = rsqrtf(ss * (1.f / D) + a.eps);
-      const bool is_q = head < a.Hq;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = (is_q ? qw[e] : kw[e]) * y[e] * r;
-      if (ln.turns) turn(y, c, s, kInter, 1.f);
-      if (!live) continue;
-      if (is_q) {
-        T* out = static_cast<T*>(a.q_out) + (token * a.Hq + head) * D;
-        Raw<T>::put(out + ln.off0, y);
-        Raw<T>::put(out + ln.off1, y + 4);
-      } else if (!kPages) {
-        T* out = static_cast<T*>(a.k_out) + (token * a.Hk + head - a.Hq) * D;
-        Raw<T>::put(out + ln.off0, y);
-        Raw<T>::put(out + ln.off1, y + 4);
-      } else if (slot >= 0) {
-        if (head < a.Hq + a.Hk) {
-          T* out = static_cast<T*>(a.k_pages) + (slot * a.Hk + head - a.Hq) * D;
-          Raw<T>::put(out + ln.off0, y);
-          Raw<T>::put(out + ln.off1, y + 4);
-        } else {
-          T* out = static_cast<T*>(a.v_pages) + (slot * a.Hk + head - a.Hq - a.Hk) * D;
+    for (int u = 0; u < kAhead; ++u) {
+      const int x = xw + u * step + ln.sub;
+      if (xw + u * step >= rows) break;   // the same in every lane
+      const bool live = x < rows;
+      int t, h;
+      row_at(live ? x : rows - 1, k.H, magic, t, h);
+      const long long row = to_pages ? slot[t] : t0 + t;
+      T* out = k.out + (row * k.H + h) * D;
+      const bool write = live && row >= 0;
+      if (kPages && kind == 2) {
+        if (write) {
           raw[u][0].copy(out + ln.off0);
           raw[u][1].copy(out + ln.off1);
         }
+      } else {
+        float y[16];
+        raw[u][0].get(y);
+        raw[u][1].get(y + 8);
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          s0 = fmaf(y[e], y[e], s0);
+          s1 = fmaf(y[e + 1], y[e + 1], s1);
+        }
+        const float ss = head_sum<D>(live ? s0 + s1 : 0.f);
+        const float r = rsqrtf(ss * (1.f / D) + a.eps);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] = w[e] * y[e] * r;
+        if (ln.turns) turn<kInter, false>(y, cs + t * a.R + ln.l * 16);
+        if (write) {
+          Raw<T>::put(out + ln.off0, y);
+          Raw<T>::put(out + ln.off1, y + 8);
+        }
       }
+      load(u, x + kAhead * step);
     }
   }
 }
 
-constexpr int kBwdBlocks = kNumSMs * 4;   // blocks of the gradient, and rows of its partial sums
+constexpr int kBwdBlocks = kNumSMs * 6;   // blocks of the gradient, and rows of its partial sums, at most
 
 // Gradient, with dy = R^T dout and r = 1 / sqrt(mean(x^2) + eps):
 //   dx = r (w dy - x r^2 mean(w dy x)),  dw = sum over tokens and heads of dy x r.
-// Blocks walk the (token, share) units; a lane keeps the weight gradients of its eight elements in
-// registers over all its units, the block adds its lanes in a fixed order and writes one row of
-// partial sums [block][q | k][D], which the second kernel adds in order: no atomics, the same bits
-// every time.
+// As the forward, but a block walks several groups of tokens of one kind and keeps the weight gradients
+// of a lane's sixteen elements in registers over all of them; it adds its lanes in a fixed order and
+// writes one row of partial sums, which the second kernel adds in order: no atomics, the same bits every
+// time.
 template <typename T, int D, bool kInter>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeArgs a) {
-  Lane<D> ln;
-  ln.init(a);
-  float qw[8], kw[8], gq[8], gk[8];
-  load8(a.q_w, ln.off0, ln.off1, qw);
-  load8(a.k_w, ln.off0, ln.off1, kw);
+  __shared__ __align__(16) float cs[2 * kPairs];
+  __shared__ float acc[kWarps][D];
+  const Lane<D> ln(a);
+  const long long tokens = (long long)a.B * a.N;
+  const bool is_q = blockIdx.x < a.blocks[0];
+  const T* src = static_cast<const T*>(is_q ? a.q : a.k);
+  const T* dsrc = static_cast<const T*>(is_q ? a.dq_out : a.dk_out);
+  float* dst = is_q ? a.dq : a.dk;
+  const long long tok = is_q ? a.q_tok : a.k_tok, head = is_q ? a.q_head : a.k_head;
+  const int H = is_q ? a.Hq : a.Hk, per = a.tokens[is_q ? 0 : 1];
+  const uint32_t magic = H == 1 ? 0xFFFFFFFFu : (uint32_t)((1ull << 32) / H);
+  const int warp = threadIdx.x >> 5, step = kWarps * Lane<D>::kHeads;
+  const int stride = a.blocks[is_q ? 0 : 1];
+  float w[16], g[16];
+  load16(is_q ? a.q_w : a.k_w, ln.off0, ln.off1, w);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) gq[e] = gk[e] = 0.f;
-  const int warp = threadIdx.x >> 5;
-  const long long units = (long long)a.B * a.N * a.split;
-  const int heads = a.Hq + a.Hk;
-  const int groups = (heads + Lane<D>::kHeads - 1) / Lane<D>::kHeads;
-  for (long long unit = (long long)blockIdx.x * kWarps + warp; unit < units; unit += (long long)gridDim.x * kWarps) {
-    const long long token = unit / a.split;
-    const int share = (int)(unit - token * a.split);
-    float c[4], s[4];
-    ln.angles(__ldg(a.pos + token), c, s);
-    for (int g0 = share; g0 < groups; g0 += a.split * 2) {
-      Raw<T> rx[2][2], rd[2][2];
+  for (int e = 0; e < 16; ++e) g[e] = 0.f;
+  for (long long group = is_q ? blockIdx.x : blockIdx.x - a.blocks[0]; group * per < tokens; group += stride) {
+    const long long t0 = group * per;
+    const int n = (int)min((long long)per, tokens - t0), rows = n * H;
+    Raw<T> rx[2], rd[2];
+    auto load = [&](int x) {
+      if (x >= rows) return;
+      int t, h;
+      row_at(x, H, magic, t, h);
+      const T* s = src + (t0 + t) * tok + h * head;
+      const T* d = dsrc + ((t0 + t) * H + h) * D;
+      rx[0].load(s + ln.off0);
+      rx[1].load(s + ln.off1);
+      rd[0].load(d + ln.off0);
+      rd[1].load(d + ln.off1);
+    };
+    load(warp * Lane<D>::kHeads + ln.sub);
+    __syncthreads();   // the group before has been walked
+    form_angles(a, t0, n, cs);
+    __syncthreads();
+    for (int xw = warp * Lane<D>::kHeads; xw < rows; xw += step) {   // the same in every lane
+      const int x = xw + ln.sub;
+      const bool live = x < rows;
+      int t, h;
+      row_at(live ? x : rows - 1, H, magic, t, h);
+      float y[16], dy[16];
+      rx[0].get(y);
+      rx[1].get(y + 8);
+      rd[0].get(dy);
+      rd[1].get(dy + 8);
+      load(x + step);
+      if (ln.turns) turn<kInter, true>(dy, cs + t * a.R + ln.l * 16);
+      float s0 = 0.f, s1 = 0.f, d0 = 0.f, d1 = 0.f;
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int head = (g0 + u * a.split) * Lane<D>::kHeads + ln.sub;
-        if (head >= heads) continue;
-        const bool is_q = head < a.Hq;
-        const T* src = is_q ? static_cast<const T*>(a.q) + token * a.q_tok + head * a.q_head
-                            : static_cast<const T*>(a.k) + token * a.k_tok + (head - a.Hq) * a.k_head;
-        const T* dsrc = is_q ? static_cast<const T*>(a.dq_out) + (token * a.Hq + head) * D
-                             : static_cast<const T*>(a.dk_out) + (token * a.Hk + head - a.Hq) * D;
-        rx[u][0].load(src + ln.off0);
-        rx[u][1].load(src + ln.off1);
-        rd[u][0].load(dsrc + ln.off0);
-        rd[u][1].load(dsrc + ln.off1);
+      for (int e = 0; e < 16; e += 2) {
+        s0 = fmaf(y[e], y[e], s0);
+        s1 = fmaf(y[e + 1], y[e + 1], s1);
+        d0 = fmaf(w[e] * dy[e], y[e], d0);
+        d1 = fmaf(w[e + 1] * dy[e + 1], y[e + 1], d1);
       }
+      const float ss = head_sum<D>(live ? s0 + s1 : 0.f), dot = head_sum<D>(live ? d0 + d1 : 0.f);
+      if (!live) continue;
+      const float r = rsqrtf(ss * (1.f / D) + a.eps);
+      const float m = dot * (1.f / D) * r * r;
+      float dx[16];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int head = (g0 + u * a.split) * Lane<D>::kHeads + ln.sub;
-        if ((g0 + u * a.split) * Lane<D>::kHeads >= heads) break;   // the same in every lane
-        const bool live = head < heads, is_q = head < a.Hq;
-        float x[8], dy[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = dy[e] = 0.f;
-        if (live) {
-          rx[u][0].get(x);
-          rx[u][1].get(x + 4);
-          rd[u][0].get(dy);
-          rd[u][1].get(dy + 4);
-        }
-        if (ln.turns) turn(dy, c, s, kInter, -1.f);
-        float ss = 0.f, dot = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          ss = fmaf(x[e], x[e], ss);
-          dot = fmaf((is_q ? qw[e] : kw[e]) * dy[e], x[e], dot);
-        }
-        ss = head_sum<D>(ss);
-        dot = head_sum<D>(dot);
-        if (!live) continue;
-        const float r = rsqrtf(ss * (1.f / D) + a.eps);
-        const float m = dot * (1.f / D) * r * r;
-        float dx[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          dx[e] = r * ((is_q ? qw[e] : kw[e]) * dy[e] - x[e] * m);
-          const float g = dy[e] * x[e] * r;
-          if (is_q) gq[e] += g;
-          else gk[e] += g;
-        }
-        float* out = is_q ? a.dq + (token * a.Hq + head) * D : a.dk + (token * a.Hk + head - a.Hq) * D;
-        Raw<float>::put(out + ln.off0, dx);
-        Raw<float>::put(out + ln.off1, dx + 4);
+      for (int e = 0; e < 16; ++e) {
+        dx[e] = r * (w[e] * dy[e] - y[e] * m);
+        g[e] = fmaf(dy[e], y[e] * r, g[e]);
       }
+      float* out = dst + ((t0 + t) * H + h) * D;
+      Raw<float>::put(out + ln.off0, dx);
+      Raw<float>::put(out + ln.off1, dx + 8);
     }
   }
   // the block's sum: lanes of equal elements within a warp, then the warps in order
-  __shared__ float acc[kWarps][2 * D];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < 16; ++e) {
 #pragma unroll
-    for (int m = 16; m >= Lane<D>::kLanes; m >>= 1) {
-      gq[e] += __shfl_xor_sync(0xffffffffu, gq[e], m);
-      gk[e] += __shfl_xor_sync(0xffffffffu, gk[e], m);
-    }
-    if (ln.sub == 0) {
-      const int off = (e < 4 ? ln.off0 : ln.off1) + (e & 3);
-      acc[warp][off] = gq[e];
-      acc[warp][D + off] = gk[e];
-    }
+    for (int m = 16; m >= Lane<D>::kLanes; m >>= 1) g[e] += __shfl_xor_sync(0xffffffffu, g[e], m);
+    if (ln.sub == 0) acc[warp][(e < 8 ? ln.off0 : ln.off1) + (e & 7)] = g[e];
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+  for (int i = threadIdx.x; i < D; i += kThreads) {
     float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) sum += acc[w][i];
-    a.partial[(long long)blockIdx.x * 2 * D + i] = sum;
+    for (int v = 0; v < kWarps; ++v) sum += acc[v][i];
+    a.partial[(long long)blockIdx.x * D + i] = sum;
   }
 }
 
-// dw: 32 lanes add a column's partial rows (lane l rows l, l + 32, ...), then the lanes by a fixed tree.
-__global__ void __launch_bounds__(1024) qk_norm_rope_bwd_join_kernel(const float* partial, int rows, int D, float* dq_w,
-                                                                     float* dk_w) {
+// dw: a block adds 32 columns of one kind's partial rows, 32 rows of threads taking every 32nd row, then
+// those by a fixed tree.
+__global__ void __launch_bounds__(1024) qk_norm_rope_bwd_join_kernel(const RopeArgs a) {
   __shared__ float tile[32][33];
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), part = threadIdx.x >> 5;
+  ptx::wait_prerequisite();
+  const int kind = blockIdx.y, first = kind ? a.blocks[0] : 0, rows = a.blocks[kind];
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const float* p = a.partial + (long long)first * a.D + blockIdx.x * 32 + lane;
   float sum = 0.f;
-  for (int r = part; r < rows; r += 32) sum += partial[(long long)r * 2 * D + col];
-  tile[part][threadIdx.x & 31] = sum;
+#pragma unroll 8
+  for (int r = part; r < rows; r += 32) sum += p[(long long)r * a.D];
+  tile[part][lane] = sum;
   __syncthreads();
-  sum = tile[threadIdx.x & 31][part];   // warp `part` adds column blockIdx.x * 32 + part
+  sum = tile[lane][part];   // warp `part` adds column 32 blockIdx.x + part
 #pragma unroll
   for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-  if ((threadIdx.x & 31) == 0) {
-    const int c = blockIdx.x * 32 + part;
-    if (c < D) dq_w[c] = sum;
-    else dk_w[c - D] = sum;
-  }
+  if (lane == 0) (kind ? a.dk_w : a.dq_w)[blockIdx.x * 32 + part] = sum;
+}
+
+// Tokens of a block so that its rows come to about `rows`, within the shared memory for angles.
+int tokens_of(const RopeArgs& a, int H, int rows, long long tokens) {
+  const int most = a.R > 0 ? 2 * kPairs / a.R : kPairs;
+  long long t = (rows + H - 1) / H;
+  if (t > most) t = most;
+  if (t > tokens) t = tokens;
+  return (int)(t < 1 ? 1 : t);
+}
+// Rows of a block: a few for each of its warps' lane groups when there are many, so that the angles'
+// forming and the block's start are spread over them; one round when that is needed to fill the SMs.
+int rows_of(int D, long long rows, int rounds) {
+  const int round = kWarps * (32 / (D / 16));
+  const long long full = rows / ((long long)kNumSMs * 6 * round);
+  return (int)(full < 1 ? 1 : full > rounds ? rounds : full) * round;
 }
 
 template <typename T, int D>
 cudaError_t forward(RopeArgs& a, cudaStream_t s) {
-  const int heads = a.Hq + (a.k_pages ? 2 : 1) * a.Hk;
-  const int groups = (heads + Lane<D>::kHeads - 1) / Lane<D>::kHeads;
   const long long tokens = (long long)a.B * a.N;
-  // shares of a token: enough warps to fill the GPU (48 a SM) when tokens are few, and about eight
-  // head groups a warp when they are many (the angles are formed once per share)
-  const long long fill = (kNumSMs * 48 + tokens - 1) / tokens;
-  const int want = (int)(fill > (groups + 7) / 8 ? fill : (groups + 7) / 8);
-  a.split = want < groups ? want : groups;
-  const long long blocks = (tokens * a.split + kWarps - 1) / kWarps;
+  const int rows = rows_of(D, tokens * (a.Hq + a.Hk), 6);
+  a.tokens[0] = tokens_of(a, a.Hq, rows, tokens);
+  a.tokens[1] = tokens_of(a, a.Hk, rows, tokens);
+  a.blocks[0] = (int)((tokens + a.tokens[0] - 1) / a.tokens[0]);
+  a.blocks[1] = (int)((tokens + a.tokens[1] - 1) / a.tokens[1]);
+  const unsigned blocks = a.blocks[0] + (a.k_pages ? 2 : 1) * a.blocks[1];
   const int slot = stage_timer_begin(s, kKernQkNormRope);
   if (a.k_pages) {
-    if (a.interleaved) qk_norm_rope_kernel<T, D, true, true><<<(unsigned)blocks, kThreads, 0, s>>>(a);
-    else qk_norm_rope_kernel<T, D, true, false><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    if (a.interleaved) qk_norm_rope_kernel<T, D, true, true><<<blocks, kThreads, 0, s>>>(a);
+    else qk_norm_rope_kernel<T, D, true, false><<<blocks, kThreads, 0, s>>>(a);
   } else {
-    if (a.interleaved) qk_norm_rope_kernel<T, D, false, true><<<(unsigned)blocks, kThreads, 0, s>>>(a);
-    else qk_norm_rope_kernel<T, D, false, false><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+    if (a.interleaved) qk_norm_rope_kernel<T, D, false, true><<<blocks, kThreads, 0, s>>>(a);
+    else qk_norm_rope_kernel<T, D, false, false><<<blocks, kThreads, 0, s>>>(a);
   }
   const cudaError_t e = cudaGetLastError();
   stage_timer_end(slot, s);
@@ -375,19 +440,32 @@ cudaError_t forward(RopeArgs& a, cudaStream_t s) {
 
 template <typename T, int D>
 cudaError_t backward(RopeArgs& a, cudaStream_t s) {
-  const int groups = (a.Hq + a.Hk + Lane<D>::kHeads - 1) / Lane<D>::kHeads;
   const long long tokens = (long long)a.B * a.N;
-  const long long fill = (kBwdBlocks * kWarps + tokens - 1) / tokens;
-  a.split = (int)(fill < groups ? fill : groups);
-  long long blocks = (tokens * a.split + kWarps - 1) / kWarps;
-  if (blocks > kBwdBlocks) blocks = kBwdBlocks;
+  const int rows = rows_of(D, tokens * (a.Hq + a.Hk), 4);
+  a.tokens[0] = tokens_of(a, a.Hq, rows, tokens);
+  a.tokens[1] = tokens_of(a, a.Hk, rows, tokens);
+  const long long gq = (tokens + a.tokens[0] - 1) / a.tokens[0], gk = (tokens + a.tokens[1] - 1) / a.tokens[1];
+  // blocks in proportion to the kinds' rows, at most kBwdBlocks in all
+  long long bq = (long long)(kBwdBlocks - 1) * a.Hq / (a.Hq + a.Hk);
+  if (bq < 1) bq = 1;
+  a.blocks[0] = (int)(gq < bq ? gq : bq);
+  a.blocks[1] = (int)(gk < kBwdBlocks - bq ? gk : kBwdBlocks - bq);
+  const unsigned blocks = a.blocks[0] + a.blocks[1];
   const int slot = stage_timer_begin(s, kKernQkNormRopeBwd);
-  if (a.interleaved) qk_norm_rope_bwd_kernel<T, D, true><<<(unsigned)blocks, kThreads, 0, s>>>(a);
-  else qk_norm_rope_bwd_kernel<T, D, false><<<(unsigned)blocks, kThreads, 0, s>>>(a);
+  if (a.interleaved) qk_norm_rope_bwd_kernel<T, D, true><<<blocks, kThreads, 0, s>>>(a);
+  else qk_norm_rope_bwd_kernel<T, D, false><<<blocks, kThreads, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) {
-    qk_norm_rope_bwd_join_kernel<<<2 * D / 32, 1024, 0, s>>>(a.partial, (int)blocks, D, a.dq_w, a.dk_w);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(D / 32, 2);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, qk_norm_rope_bwd_join_kernel, a);
   }
   stage_timer_end(slot, s);
   return e;
@@ -395,7 +473,7 @@ cudaError_t backward(RopeArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t qk_norm_rope_backward_workspace_bytes(int D) { return (size_t)kBwdBlocks * 2 * D * sizeof(float); }
+size_t qk_norm_rope_backward_workspace_bytes(int D) { return (size_t)kBwdBlocks * D * sizeof(float); }
 
 cudaError_t launch_qk_norm_rope(RopeArgs a, cudaStream_t s) {
   switch (a.D) {

@@ -57,7 +57,8 @@ struct RopeArgs {
   float* dk_w;
   float* partial;
   int* err;
-  int split;   // warps that share a token's heads (set by the launch)
+  // set by the launch: blocks of queries and of keys (values as keys), and tokens of each one's block
+  int blocks[2], tokens[2];
 };
 cudaError_t launch_qk_norm_rope(RopeArgs a, cudaStream_t s);
 cudaError_t launch_qk_norm_rope_backward(RopeArgs a, cudaStream_t s);

@@ -76,8 +76,8 @@ gdr_status check_rope(const RopeArgs& a, gdr_dtype dt, const char* who) {
     return fail(GDR_ERR_INVALID_ARG, "%s: q, k, q_w, k_w, inv_freq and pos must be non-NULL", who);
   gdr_status st = check_heads(a.B, a.N, a.Hq, a.Hk, a.D, dt, who);
   if (st != GDR_OK) return st;
-  if (a.R < 0 || a.R > a.D || a.R % 8 != 0)
-    return fail(GDR_ERR_INVALID_ARG, "%s: R=%d is not a multiple of 8 in [0, D]", who, a.R);
+  if (a.R < 0 || a.R > a.D || a.R % 16 != 0)
+    return fail(GDR_ERR_INVALID_ARG, "%s: R=%d is not a multiple of 16 in [0, D]", who, a.R);
   if (!(a.eps >= 0.f)) return fail(GDR_ERR_INVALID_ARG, "%s: eps must be >= 0", who);
   const int es = dt == GDR_BF16 ? 2 : 4;
   const long long strides[] = {a.q_tok, a.q_head, a.k_tok, a.k_head, a.v_tok, a.v_head};

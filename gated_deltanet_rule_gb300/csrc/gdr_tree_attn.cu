@@ -608,16 +608,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of items that several blocks shared, and fills the rows of absent nodes (0, -inf).
-// A warp takes one (node, query head) row: o = sum_s e^(lse_s - lse) o_s over its parts in order.
-constexpr int kJoinThreads = 256;
-template <int D>
+// Joins the parts of items that several blocks shared, and fills the rows of absent nodes (0, -inf):
+// o = sum_s e^(lse_s - lse) o_s over a row's parts. Few items have many parts each (one item is cut over
+// up to every block) and few rows: kRowWarps = 8 warps then share a (node, query head) row, warp w
+// taking parts w, w + 8, ... and the block adding the warps' sums in order; with many items a row has
+// one to three parts and one warp takes it. Parts are read four at a time: the loop is bound by their
+// latency, 33 -> 8 us for 38 parts of 224 rows of 256.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+template <int D, int kRowWarps>
 __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const Args a) {
   constexpr int KT = Cfg<D>::KT, kVec = D / 32;
-  __shared__ long long warps[kJoinThreads / 32];
-  const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
-  long long mine = 0;   // units of rows before b, and in all
-  long long before_b = 0;
+  __shared__ long long sums[2][kJoinWarps];
+  __shared__ float s_acc[kRowWarps > 1 ? kRowWarps : 1][D];
+  __shared__ float s_sum[kJoinWarps];
+  const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long long mine = 0, before_b = 0;   // units of all rows, and of rows before b
   for (int r = tid; r < a.B; r += kJoinThreads) {
     int n, ctx;
     row_of(a, r, n, ctx);
@@ -626,12 +631,12 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const Args
     if (r < b) before_b += u;
   }
   long long dummy;
-  const long long total = block_sum(mine, warps, dummy);
-  __syncthreads();
-  before_b = block_sum(before_b, warps, dummy);
+  const long long total = block_sum(mine, sums[0], dummy);
+  before_b = block_sum(before_b, sums[1], dummy);
   wait_prerequisite();
-  const int r = blockIdx.x * (kJoinThreads / 32) + (tid >> 5);   // node Hq + head
+  const int r = kRowWarps > 1 ? blockIdx.x : blockIdx.x * kJoinWarps + warp;   // node Hq + head
   if (r >= a.N * a.Hq) return;
+  const int part0 = kRowWarps > 1 ? warp : 0;
   const int i = r / a.Hq, h = r % a.Hq;
   int n, ctx;
   row_of(a, b, n, ctx);
@@ -646,14 +651,16 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const Args
     for (int t = 0; t < mt; ++t) x0 += tiles_of<KT>(a, n, ctx, t);
     const long long x1 = x0 + tiles_of<KT>(a, n, ctx, mt);
     const int c0 = block_of(total, x0), c1 = block_of(total, x1 - 1);
-    if (c0 == c1) return;   // written whole
+    if (c0 == c1) return;   // written whole (the same in every warp of the row)
+    // (blocks between c0 and c1 all hold a unit: the item's units are consecutive, and a block without
+    // units holds none of them, which first_unit(c) == first_unit(c + 1) says)
+    auto share = [&](int c) { return first_unit(total, c) < first_unit(total, c + 1); };
     // a block's first segment is its part 0: block c0's only where the item starts its share
     auto part = [&](int c) { return (size_t)(2 * c + (first_unit(total, c) < x0)) * kM + row; };
     float top = -INFINITY;
     bool nan = false;
     for (int c = c0 + lane; c <= c1; c += 32) {
-      if (first_unit(total, c) == first_unit(total, c + 1)) continue;   // a block without units
-      const float x = a.part_lse[part(c)];
+      const float x = share(c) ? a.part_lse[part(c)] : -INFINITY;
       nan |= x != x;
       top = fmaxf(top, x);
     }
@@ -662,21 +669,54 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const Args
     nan = __any_sync(0xffffffffu, nan);
     const float ref = top == -INFINITY ? 0.f : top;
     float sum = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-      if (first_unit(total, c) == first_unit(total, c + 1)) continue;
-      const size_t p = part(c);
-      const float w = ex2_approx((a.part_lse[p] - ref) * kLog2e);
-      sum += w;
-      const float* po = a.part_o + p * D + lane * kVec;
-      if (w != 0.f) {
+    for (int cc = c0 + part0; cc <= c1; cc += 4 * kRowWarps) {
+      float w[4], x[4][kVec];
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) acc[e] = fmaf(w, po[e], acc[e]);
+      for (int u = 0; u < 4; ++u) {
+        const int c = cc + u * kRowWarps;
+        const bool there = c <= c1 && share(c);
+        const size_t p = there ? part(c) : part(c0);
+        w[u] = there ? a.part_lse[p] : -INFINITY;
+        const float* po = a.part_o + p * D + lane * kVec;
+#pragma unroll
+        for (int e = 0; e < kVec; e += 2) {
+          const float2 y = *reinterpret_cast<const float2*>(po + e);
+          x[u][e] = y.x;
+          x[u][e + 1] = y.y;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float f = ex2_approx((w[u] - ref) * kLog2e);
+        sum += f;
+        if (f != 0.f) {   // a part that saw nothing may hold anything
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) acc[e] = fmaf(f, x[u][e], acc[e]);
+        }
+      }
+    }
+    if constexpr (kRowWarps > 1) {
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) s_acc[warp][lane * kVec + e] = acc[e];
+      if (lane == 0) s_sum[warp] = sum;
+      __syncthreads();   // (every warp of the block is here: they share the row)
+      if (warp > 0) return;
+      sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kRowWarps; ++w) {
+        sum += s_sum[w];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) acc[e] += s_acc[w][lane * kVec + e];
       }
     }
     const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
 #pragma unroll
     for (int e = 0; e < kVec; ++e) acc[e] *= inv;
     lse = nan ? NAN : sum > 0.f ? ref + logf(sum) : -INFINITY;
+  } else if (kRowWarps > 1 && warp > 0) {
+    return;
   }
   __nv_bfloat16* out = a.o + orow * D + lane * kVec;
 #pragma unroll
@@ -739,7 +779,9 @@ cudaError_t launch(const TreeAttnArgs& p, cudaStream_t st) {
   stage_timer_end(slot, st);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.N * p.Hq + kJoinThreads / 32 - 1) / (kJoinThreads / 32), p.B);
+  // (64 items: three parts or fewer each)
+  const bool few = (long long)p.B * p.Hk * ((p.N + a.npt - 1) / a.npt) <= 64;
+  cfg.gridDim = dim3(few ? p.N * p.Hq : (p.N * p.Hq + kJoinWarps - 1) / kJoinWarps, p.B);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -748,7 +790,7 @@ cudaError_t launch(const TreeAttnArgs& p, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   slot = stage_timer_begin(st, kKernTreeAttnJoin);
-  e = cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D>, a);
+  e = few ? cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D, 8>, a) : cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D, 1>, a);
   stage_timer_end(slot, st);
   return e;
 }

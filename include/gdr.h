@@ -351,7 +351,7 @@ gdr_status gdr_backward_chunked_saved(const void* q, const void* k, const void* 
  *   q_w, k_w [D] float32   norm weights;  eps >= 0
  *   inv_freq [R/2] float64 radians per position;  pos [B, N] int32
  *   q_out [B, N, Hq, D], k_out [B, N, Hk, D] dt   contiguous; may not overlap q or k
- * R is a multiple of 8 in [0, D]. Arithmetic is float32 with one rounding of the outputs; angles are
+ * R is a multiple of 16 in [0, D]. Arithmetic is float32 with one rounding of the outputs; angles are
  * formed modulo a turn in 64-bit integers (exact to 2^-32 turn at any position).
  */
 gdr_status gdr_qk_norm_rope(const void* q, const void* k, const float* q_w, const float* k_w,

@@ -35,8 +35,8 @@ def _rope(L, q=A(1), k=A(2), qw=A(3), kw=A(4), inv=A(5), pos=A(6), eps=1e-6, qo=
 
 
 def test_norm_rope(L):
-    for kw in (dict(q=None), dict(inv=None), dict(ko=None), dict(B=0), dict(N=0), dict(Hq=3), dict(dt=9), dict(R=4), dict(R=136),
-               dict(R=-8), dict(eps=-1.0), dict(eps=float("nan")), dict(qt=4), dict(kh=-128), dict(q=off(1)), dict(qo=off(7)),
+    for kw in (dict(q=None), dict(inv=None), dict(ko=None), dict(B=0), dict(N=0), dict(Hq=3), dict(dt=9), dict(R=8), dict(R=144),
+               dict(R=-16), dict(eps=-1.0), dict(eps=float("nan")), dict(qt=4), dict(kh=-128), dict(q=off(1)), dict(qo=off(7)),
                dict(inv=off(5)), dict(pos=off(6, 2)), dict(qo=A(1)), dict(ko=off(2, 16)), dict(ko=A(7))):
         assert _rope(L, **kw) == INV, kw
     assert _rope(L, D=96) == UNS and "D=96" in msg(L)
