@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) fork_take_kernel(const CacheArgs a, 
     return;
   }
   const int src = a.src[f], dst = a.dst[f], n = a.ctx[src];
-  const int full = n / a.page, part = n % a.page;
+  const int full = n >> a.page_shift, part = n & (a.page - 1);
   const int32_t* from = a.table + (size_t)src * a.M;
   const int fresh = need ? ws_list(a)[first] : -1;
   if (blockIdx.y == 0 && blockIdx.z == 0) {
@@ -193,15 +193,16 @@ __global__ void __launch_bounds__(kThreads) fork_take_kernel(const CacheArgs a, 
   const uint4* s = reinterpret_cast<const uint4*>(base + (size_t)from[full] * page_bytes);
   uint4* d = reinterpret_cast<uint4*>(base + (size_t)fresh * page_bytes);
   const long long vecs = (long long)part * a.row_bytes / 16, step = (long long)shares * kThreads;
-  long long i = (long long)blockIdx.z * kThreads + tid;
-  for (; i + 3 * step < vecs; i += 4 * step) {
-    const uint4 x0 = s[i], x1 = s[i + step], x2 = s[i + 2 * step], x3 = s[i + 3 * step];
-    d[i] = x0;
-    d[i + step] = x1;
-    d[i + 2 * step] = x2;
-    d[i + 3 * step] = x3;
+  constexpr int kFlight = 8;
+  for (long long i = (long long)blockIdx.z * kThreads + tid; i < vecs; i += kFlight * step) {
+    uint4 x[kFlight];
+#pragma unroll
+    for (int e = 0; e < kFlight; ++e)
+      if (i + e * step < vecs) x[e] = s[i + e * step];
+#pragma unroll
+    for (int e = 0; e < kFlight; ++e)
+      if (i + e * step < vecs) d[i + e * step] = x[e];
   }
-  for (; i < vecs; i += step) d[i] = s[i];
 }
 
 __global__ void __launch_bounds__(kThreads) reserve_take_kernel(const CacheArgs a) {
@@ -307,9 +308,12 @@ cudaError_t launch_cache_fork(const CacheArgs& a, cudaStream_t s) {
   if (e == cudaSuccess) e = launch_after(alloc_kernel, dim3(1), kAllocThreads, s, a);
   stage_timer_end(slot, s);
   if (e != cudaSuccess) return e;
-  // about 16 KiB a block of the largest copy
-  const long long vecs = (long long)a.page * a.row_bytes / 16;
-  long long shares = (vecs + 4 * kThreads - 1) / (4 * kThreads);
+  // blocks of a copy: one, or as many as bring the launch to eight blocks a SM (32 KiB a pass and block:
+  // a block's start costs as much as copying a few KiB)
+  const long long vecs = (long long)a.page * a.row_bytes / 16, copies = 2ll * a.layers * a.F;
+  long long shares = (kNumSMs * 8 + copies - 1) / copies;
+  const long long most = (vecs + kThreads - 1) / kThreads;
+  if (shares > most) shares = most;
   if (shares > 64) shares = 64;
   slot = stage_timer_begin(s, kKernCacheCopy);
   e = launch_after(fork_take_kernel, dim3(a.F, 2 * a.layers, (unsigned)shares), kThreads, s, a, (int)shares);

@@ -28,7 +28,31 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kPairs = 2048;   // (token, pair) angles of a block
+constexpr int kPairs = 2048;       // (token, pair) angles of a block
+constexpr int kMostTokens = 256;   // tokens of a block
+
+// Two floats in one register pair: the packed operations halve the instructions of this kernel, whose
+// issue rate is what bounds it beside HBM.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 pack(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack(F2 x, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x.v)); }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 neg2(F2 a) { return {a.v ^ 0x8000000080000000ull}; }
 
 // Eight consecutive elements as loaded.
 template <typename T>
@@ -37,17 +61,20 @@ template <>
 struct Raw<__nv_bfloat16> {
   uint4 u;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void get(float* x) const {
+  __device__ __forceinline__ void get(F2* x) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[2 * e] = __uint_as_float(w[e] << 16);
-      x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-    }
+    for (int e = 0; e < 4; ++e) x[e] = pack(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
   }
-  __device__ __forceinline__ static void put(__nv_bfloat16* p, const float* x) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(ptx::pack_bf16x2(x[0], x[1]), ptx::pack_bf16x2(x[2], x[3]),
-                                              ptx::pack_bf16x2(x[4], x[5]), ptx::pack_bf16x2(x[6], x[7]));
+  __device__ __forceinline__ static void put(__nv_bfloat16* p, const F2* x) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float lo, hi;
+      unpack(x[e], lo, hi);
+      w[e] = ptx::pack_bf16x2(lo, hi);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   __device__ __forceinline__ void copy(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
 };
@@ -58,13 +85,15 @@ struct Raw<float> {
     u = __ldg(reinterpret_cast<const float4*>(p));
     v = __ldg(reinterpret_cast<const float4*>(p) + 1);
   }
-  __device__ __forceinline__ void get(float* x) const {
-    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-    x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+  __device__ __forceinline__ void get(F2* x) const {
+    x[0] = pack(u.x, u.y);
+    x[1] = pack(u.z, u.w);
+    x[2] = pack(v.x, v.y);
+    x[3] = pack(v.z, v.w);
   }
-  __device__ __forceinline__ static void put(float* p, const float* x) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  __device__ __forceinline__ static void put(float* p, const F2* x) {
+    reinterpret_cast<ulonglong2*>(p)[0] = make_ulonglong2(x[0].v, x[1].v);
+    reinterpret_cast<ulonglong2*>(p)[1] = make_ulonglong2(x[2].v, x[3].v);
   }
   __device__ __forceinline__ void copy(float* p) const {
     reinterpret_cast<float4*>(p)[0] = u;
@@ -119,35 +148,64 @@ struct Lane {
   }
 };
 
-// cos and sin of a block's tokens [t0, t0 + n) into cs[token][pair][cos | sin runs of eight].
+// cos and sin of a block's tokens [t0, t0 + n) into cs, R floats a token.
 __device__ __forceinline__ void form_angles(const RopeArgs& a, long long t0, int n, float* cs) {
   const int half = a.R / 2;
   for (int x = threadIdx.x; x < n * half; x += kThreads) {
     const int t = x / half, j = x - t * half;
     float c, s;
     turn_sincos(turn_fraction(__ldg(a.inv_freq + j)), __ldg(a.pos + t0 + t), c, s);
-    float* at = cs + t * a.R + (j >> 3) * 16 + (j & 7);   // lane l's eight cosines, then its eight sines
+    // four runs of [lane][4]: the lanes' first and last four cosines, then sines, so that the lanes of a
+    // head read neighbouring 16 bytes
+    float* at = cs + t * a.R + ((j >> 2) & 1) * (a.R / 4) + (j >> 3) * 4 + (j & 3);
     at[0] = c;
-    at[8] = s;
+    at[a.R / 2] = s;
   }
 }
 
-// Turn a lane's sixteen values by its pairs' angles; kBack turns back.
-template <bool kInter, bool kBack>
-__device__ __forceinline__ void turn(float* y, const float* cs) {
-  float c[8], s[8];
+// A lane's pairs' cosines and sines, as four packed pairs each.
+__device__ __forceinline__ void read_angles(const float* cs, int R, int l, F2* c, F2* s) {
+  const ulonglong2* at = reinterpret_cast<const ulonglong2*>(cs) + l;
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const float4 cv = reinterpret_cast<const float4*>(cs)[q], sv = reinterpret_cast<const float4*>(cs)[q + 2];
-    c[4 * q] = cv.x; c[4 * q + 1] = cv.y; c[4 * q + 2] = cv.z; c[4 * q + 3] = cv.w;
-    s[4 * q] = sv.x; s[4 * q + 1] = sv.y; s[4 * q + 2] = sv.z; s[4 * q + 3] = sv.w;
+    const ulonglong2 cv = at[q * (R / 16)], sv = at[(q + 2) * (R / 16)];
+    c[2 * q] = {cv.x};
+    c[2 * q + 1] = {cv.y};
+    s[2 * q] = {sv.x};
+    s[2 * q + 1] = {sv.y};
   }
+}
+
+// Turn a lane's sixteen values (eight packed pairs) by its angles; kBack turns back.
+template <bool kInter, bool kBack>
+__device__ __forceinline__ void turn(F2* y, const float* cs, int R, int l) {
+  F2 c[4], s[4];
+  read_angles(cs, R, l, c, s);
+  if (kInter) {   // (y_2j, y_2j+1) are the members of pair j
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int ia = kInter ? 2 * j : j, ib = kInter ? 2 * j + 1 : j + 8;
-    const float ya = y[ia], yb = y[ib], sj = kBack ? -s[j] : s[j];
-    y[ia] = ya * c[j] - yb * sj;
-    y[ib] = yb * c[j] + ya * sj;
+    for (int q = 0; q < 4; ++q) {
+      float c0, c1, s0, s1;
+      unpack(c[q], c0, c1);
+      unpack(s[q], s0, s1);
+      if (kBack) {
+        s0 = -s0;
+        s1 = -s1;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float ya, yb;
+        unpack(y[2 * q + u], ya, yb);
+        const float cj = u ? c1 : c0, sj = u ? s1 : s0;
+        y[2 * q + u] = pack(ya * cj - yb * sj, yb * cj + ya * sj);
+      }
+    }
+  } else {        // y[q] holds the first members of pairs 2q and 2q + 1, y[4 + q] the second ones
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const F2 ya = y[q], yb = y[4 + q], sq = kBack ? neg2(s[q]) : s[q];
+      y[q] = fma2(ya, c[q], neg2(mul2(yb, sq)));
+      y[4 + q] = fma2(yb, c[q], mul2(ya, sq));
+    }
   }
 }
 
@@ -158,12 +216,14 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ void load16(const float* w, int off0, int off1, float* x) {
+__device__ __forceinline__ void load16(const float* w, int off0, int off1, F2* x) {
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(w + off0) + q), b = __ldg(reinterpret_cast<const float4*>(w + off1) + q);
-    x[4 * q] = a.x; x[4 * q + 1] = a.y; x[4 * q + 2] = a.z; x[4 * q + 3] = a.w;
-    x[8 + 4 * q] = b.x; x[8 + 4 * q + 1] = b.y; x[8 + 4 * q + 2] = b.z; x[8 + 4 * q + 3] = b.w;
+    x[2 * q] = pack(a.x, a.y);
+    x[2 * q + 1] = pack(a.z, a.w);
+    x[4 + 2 * q] = pack(b.x, b.y);
+    x[4 + 2 * q + 1] = pack(b.z, b.w);
   }
 }
 
@@ -192,7 +252,7 @@ struct Kind {
 template <typename T, int D, bool kPages, bool kInter>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a) {
   __shared__ __align__(16) float cs[2 * kPairs];
-  __shared__ long long slot[kPairs];
+  __shared__ long long slot[kMostTokens];
   const Lane<D> ln(a);
   const long long tokens = (long long)a.B * a.N;
   const int kind = blockIdx.x < a.blocks[0] ? 0 : blockIdx.x < a.blocks[0] + a.blocks[1] ? 1 : 2;
@@ -208,6 +268,8 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
   const int warp = threadIdx.x >> 5, step = kWarps * Lane<D>::kHeads;
   const bool to_pages = kPages && kind > 0;
 
+  const T* base = k.src + t0 * k.tok;
+  const int tok = (int)k.tok, head = (int)k.head;
   // the first rows are on their way while the angles are formed
   constexpr int kAhead = 2;
   Raw<T> raw[kAhead][2];
@@ -215,14 +277,14 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
     if (x >= rows) return;
     int t, h;
     row_at(x, k.H, magic, t, h);
-    const T* src = k.src + (t0 + t) * k.tok + h * k.head;
+    const T* src = base + (t * tok + h * head);   // (below 2^31: tokens of a block <= 256)
     raw[u][0].load(src + ln.off0);
     raw[u][1].load(src + ln.off1);
   };
   const int x0 = warp * Lane<D>::kHeads + ln.sub;
 #pragma unroll
   for (int u = 0; u < kAhead; ++u) load(u, x0 + u * step);
-  float w[16];
+  F2 w[8];
   if (kind < 2) {
     load16(k.w, ln.off0, ln.off1, w);
     form_angles(a, t0, n, cs);
@@ -239,7 +301,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
         if (pg < 0 || pg >= a.P) atomicCAS(a.err, 0, kErrDeviceIndex);
         else at = (long long)pg * a.page + pos % a.page;
       }
-      slot[t] = at;
+      slot[t] = at;   // (-1: h is below H, so -H + h stays negative)
     }
   }
   __syncthreads();
@@ -251,32 +313,32 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
       const bool live = x < rows;
       int t, h;
       row_at(live ? x : rows - 1, k.H, magic, t, h);
-      const long long row = to_pages ? slot[t] : t0 + t;
-      T* out = k.out + (row * k.H + h) * D;
-      const bool write = live && row >= 0;
+      const long long first = to_pages ? slot[t] * k.H + h : t0 * k.H + x;
+      T* out = k.out + first * D;
+      const bool write = live && first >= 0;
       if (kPages && kind == 2) {
         if (write) {
           raw[u][0].copy(out + ln.off0);
           raw[u][1].copy(out + ln.off1);
         }
       } else {
-        float y[16];
+        F2 y[8];
         raw[u][0].get(y);
-        raw[u][1].get(y + 8);
-        float s0 = 0.f, s1 = 0.f;
+        raw[u][1].get(y + 4);
+        F2 sq = mul2(y[0], y[0]);
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          s0 = fmaf(y[e], y[e], s0);
-          s1 = fmaf(y[e + 1], y[e + 1], s1);
-        }
+        for (int e = 1; e < 8; ++e) sq = fma2(y[e], y[e], sq);
+        float s0, s1;
+        unpack(sq, s0, s1);
         const float ss = head_sum<D>(live ? s0 + s1 : 0.f);
         const float r = rsqrtf(ss * (1.f / D) + a.eps);
+        const F2 rr = pack(r, r);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) y[e] = w[e] * y[e] * r;
-        if (ln.turns) turn<kInter, false>(y, cs + t * a.R + ln.l * 16);
+        for (int e = 0; e < 8; ++e) y[e] = mul2(mul2(w[e], y[e]), rr);
+        if (ln.turns) turn<kInter, false>(y, cs + t * a.R, a.R, ln.l);
         if (write) {
           Raw<T>::put(out + ln.off0, y);
-          Raw<T>::put(out + ln.off1, y + 8);
+          Raw<T>::put(out + ln.off1, y + 4);
         }
       }
       load(u, x + kAhead * step);
@@ -307,10 +369,10 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeAr
   const uint32_t magic = H == 1 ? 0xFFFFFFFFu : (uint32_t)((1ull << 32) / H);
   const int warp = threadIdx.x >> 5, step = kWarps * Lane<D>::kHeads;
   const int stride = a.blocks[is_q ? 0 : 1];
-  float w[16], g[16];
+  F2 w[8], g[8];
   load16(is_q ? a.q_w : a.k_w, ln.off0, ln.off1, w);
 #pragma unroll
-  for (int e = 0; e < 16; ++e) g[e] = 0.f;
+  for (int e = 0; e < 8; ++e) g[e] = {0};
   for (long long group = is_q ? blockIdx.x : blockIdx.x - a.blocks[0]; group * per < tokens; group += stride) {
     const long long t0 = group * per;
     const int n = (int)min((long long)per, tokens - t0), rows = n * H;
@@ -319,8 +381,8 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeAr
       if (x >= rows) return;
       int t, h;
       row_at(x, H, magic, t, h);
-      const T* s = src + (t0 + t) * tok + h * head;
-      const T* d = dsrc + ((t0 + t) * H + h) * D;
+      const T* s = src + t0 * tok + (t * (int)tok + h * (int)head);
+      const T* d = dsrc + (t0 * H + x) * D;
       rx[0].load(s + ln.off0);
       rx[1].load(s + ln.off1);
       rd[0].load(d + ln.off0);
@@ -335,42 +397,53 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeAr
       const bool live = x < rows;
       int t, h;
       row_at(live ? x : rows - 1, H, magic, t, h);
-      float y[16], dy[16];
+      F2 y[8], dy[8];
       rx[0].get(y);
-      rx[1].get(y + 8);
+      rx[1].get(y + 4);
       rd[0].get(dy);
-      rd[1].get(dy + 8);
+      rd[1].get(dy + 4);
       load(x + step);
-      if (ln.turns) turn<kInter, true>(dy, cs + t * a.R + ln.l * 16);
-      float s0 = 0.f, s1 = 0.f, d0 = 0.f, d1 = 0.f;
+      if (ln.turns) turn<kInter, true>(dy, cs + t * a.R, a.R, ln.l);
+      F2 sq = mul2(y[0], y[0]), dt = mul2(mul2(w[0], dy[0]), y[0]);
 #pragma unroll
-      for (int e = 0; e < 16; e += 2) {
-        s0 = fmaf(y[e], y[e], s0);
-        s1 = fmaf(y[e + 1], y[e + 1], s1);
-        d0 = fmaf(w[e] * dy[e], y[e], d0);
-        d1 = fmaf(w[e + 1] * dy[e + 1], y[e + 1], d1);
+      for (int e = 1; e < 8; ++e) {
+        sq = fma2(y[e], y[e], sq);
+        dt = fma2(mul2(w[e], dy[e]), y[e], dt);
       }
+      float s0, s1, d0, d1;
+      unpack(sq, s0, s1);
+      unpack(dt, d0, d1);
       const float ss = head_sum<D>(live ? s0 + s1 : 0.f), dot = head_sum<D>(live ? d0 + d1 : 0.f);
       if (!live) continue;
       const float r = rsqrtf(ss * (1.f / D) + a.eps);
-      const float m = dot * (1.f / D) * r * r;
-      float dx[16];
+      const float m = -dot * (1.f / D) * r * r;
+      const F2 rr = pack(r, r), mm = pack(m, m);
+      F2 dx[8];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        dx[e] = r * (w[e] * dy[e] - y[e] * m);
-        g[e] = fmaf(dy[e], y[e] * r, g[e]);
+      for (int e = 0; e < 8; ++e) {
+        dx[e] = mul2(rr, fma2(y[e], mm, mul2(w[e], dy[e])));
+        g[e] = fma2(dy[e], mul2(y[e], rr), g[e]);
       }
-      float* out = dst + ((t0 + t) * H + h) * D;
+      float* out = dst + (t0 * H + x) * D;
       Raw<float>::put(out + ln.off0, dx);
-      Raw<float>::put(out + ln.off1, dx + 8);
+      Raw<float>::put(out + ln.off1, dx + 4);
     }
   }
   // the block's sum: lanes of equal elements within a warp, then the warps in order
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
+  for (int e = 0; e < 8; ++e) {
+    float g0, g1;
+    unpack(g[e], g0, g1);
 #pragma unroll
-    for (int m = 16; m >= Lane<D>::kLanes; m >>= 1) g[e] += __shfl_xor_sync(0xffffffffu, g[e], m);
-    if (ln.sub == 0) acc[warp][(e < 8 ? ln.off0 : ln.off1) + (e & 7)] = g[e];
+    for (int m = 16; m >= Lane<D>::kLanes; m >>= 1) {
+      g0 += __shfl_xor_sync(0xffffffffu, g0, m);
+      g1 += __shfl_xor_sync(0xffffffffu, g1, m);
+    }
+    if (ln.sub == 0) {
+      float* at = acc[warp] + (e < 4 ? ln.off0 : ln.off1) + 2 * (e & 3);
+      at[0] = g0;
+      at[1] = g1;
+    }
   }
   __syncthreads();
   for (int i = threadIdx.x; i < D; i += kThreads) {
@@ -402,7 +475,7 @@ __global__ void __launch_bounds__(1024) qk_norm_rope_bwd_join_kernel(const RopeA
 
 // Tokens of a block so that its rows come to about `rows`, within the shared memory for angles.
 int tokens_of(const RopeArgs& a, int H, int rows, long long tokens) {
-  const int most = a.R > 0 ? 2 * kPairs / a.R : kPairs;
+  const int most = a.R > 0 && 2 * kPairs / a.R < kMostTokens ? 2 * kPairs / a.R : kMostTokens;
   long long t = (rows + H - 1) / H;
   if (t > most) t = most;
   if (t > tokens) t = tokens;

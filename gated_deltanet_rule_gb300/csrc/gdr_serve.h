@@ -112,6 +112,7 @@ struct CacheArgs {
   const int32_t* src;        // [F] (fork only)
   const int32_t* dst;        // [F]
   int layers, P, page, rows, M, F;
+  int page_shift;            // log2(page)
   long long row_bytes;
   int extra;                 // reserve: positions past ctx that must have pages
   int32_t* ws;               // need [F], first [F], count; free list

@@ -82,8 +82,10 @@ gdr_status check_rope(const RopeArgs& a, gdr_dtype dt, const char* who) {
   const int es = dt == GDR_BF16 ? 2 : 4;
   const long long strides[] = {a.q_tok, a.q_head, a.k_tok, a.k_head, a.v_tok, a.v_head};
   for (long long s : strides)
-    if (s < 0 || s * es % 16 != 0 || s > (1ll << 32))
-      return fail(GDR_ERR_INVALID_ARG, "%s: strides must be multiples of 16 bytes in [0, 2^32]", who);
+    if (s < 0 || s * es % 16 != 0 || s > (1ll << 22))
+      return fail(GDR_ERR_INVALID_ARG, "%s: strides must be multiples of 16 bytes, of at most 2^22 elements", who);
+  if (a.Hq * a.q_head > (1ll << 30) || a.Hk * a.k_head > (1ll << 30) || a.Hk * a.v_head > (1ll << 30))
+    return fail(GDR_ERR_UNSUPPORTED, "%s: a token's heads span more than 2^30 elements", who);
   for (const void* p : {a.q, a.k, a.v, (const void*)a.q_w, (const void*)a.k_w})
     if (p && !aligned(p, 16)) return fail(GDR_ERR_INVALID_ARG, "%s: q, k, v, q_w and k_w must be 16-byte aligned", who);
   if (!aligned(a.inv_freq, 8) || !aligned(a.pos, 4))
@@ -331,7 +333,7 @@ gdr_status gdr_cache_fork(void* k_cache, void* v_cache, int32_t* table, int32_t*
   CacheArgs a{};
   a.k_cache = static_cast<uint8_t*>(k_cache); a.v_cache = static_cast<uint8_t*>(v_cache);
   a.table = table; a.ctx = ctx; a.refs = refs; a.src = src; a.dst = dst;
-  a.layers = layers; a.P = P; a.page = page; a.rows = R; a.M = M; a.F = F; a.row_bytes = row_bytes;
+  a.layers = layers; a.P = P; a.page = page; a.page_shift = __builtin_ctz((unsigned)page); a.rows = R; a.M = M; a.F = F; a.row_bytes = row_bytes;
   a.ws = static_cast<int32_t*>(ws);
   a.err = device_error_word();
   if (!a.err) return no_device(who);

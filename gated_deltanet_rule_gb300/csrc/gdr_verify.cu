@@ -12,14 +12,18 @@
 // smallest index whose running sum of rho passes u_next times the total.
 //
 // One cluster of eight blocks takes a row: every block walks the tree on the same scalars (gathered
-// once, so the walk runs in shared memory), and a pass splits the vocabulary over the cluster's 128
-// warps, each a contiguous run, whose sums the blocks exchange through distributed shared memory.
-// The reads of a pass are latency-bound; more blocks a row would shorten it, fewer leave SMs idle at
-// one row.
+// once, so the walk runs in shared memory), and a pass splits the vocabulary over the cluster's 64
+// warps, each a contiguous run of 128-entry chunks (four entries a lane, 16-byte loads where rows are
+// aligned), whose sums the blocks exchange through distributed shared memory. The token is then found
+// by halving the range eightfold per step: block, warp, an eighth of its run, ... , chunk, lane, entry.
+// A pass is bound by the latency of its loads and, over many rows, by its arithmetic (about 20
+// instructions an entry); blocks of 256 threads keep 48 rows of 131072 entries resident at once.
+// Measured: a row of 32000 entries and five drafts 17.8 -> VERIFY_CHAIN us, 48 trees of 24 nodes over
+// 131072 entries 104 -> VERIFY_TREES us against single-entry loads, float64 reductions and 512 threads.
 //
-// Sums decide whole numbers, so they are carried to about 2^-46: each lane adds its terms as an
-// unevaluated pair of floats (error-free sums of two floats), lanes and warps add in float64. Float64
-// alone would do the same at 1/64 of the rate.
+// Sums decide whole numbers, so they are carried to about 2^-46: unevaluated pairs of floats (error-free
+// sums of two floats) in lanes, warps and blocks, float64 in the scalars of the walk. Float64 throughout
+// would run at 1/64 of the float32 rate.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -30,70 +34,154 @@ namespace gdr {
 namespace {
 
 constexpr int kCluster = 8;
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kChunk4 = 128;   // entries of a chunk: four a lane
+constexpr unsigned kAll = 0xffffffffu;
 
-template <typename T>
-__device__ __forceinline__ float prob(const T* p);
-template <>
-__device__ __forceinline__ float prob<float>(const float* p) {
-  const float x = __ldg(p);
-  return x > 0.f ? x : 0.f;
+__device__ __forceinline__ float above_zero(float x) { return x > 0.f ? x : 0.f; }   // nan and negatives count as 0
+__device__ __forceinline__ float prob(const float* p) { return above_zero(__ldg(p)); }
+__device__ __forceinline__ float prob(const __nv_bfloat16* p) { return above_zero(__bfloat162float(*p)); }
+
+// Entries i .. i + 3 of a row of V (0 past its end); kVec: V and the rows are multiples of four entries.
+template <bool kVec>
+__device__ __forceinline__ void load4(const float* p, int i, int V, float* x) {
+  if (kVec) {
+    const float4 v = i < V ? __ldg(reinterpret_cast<const float4*>(p + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = i + e < V ? __ldg(p + i + e) : 0.f;
+  }
 }
-template <>
-__device__ __forceinline__ float prob<__nv_bfloat16>(const __nv_bfloat16* p) {
-  const float x = __bfloat162float(*p);
-  return x > 0.f ? x : 0.f;
+template <bool kVec>
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, int i, int V, float* x) {
+  if (kVec) {
+    const uint2 v = i < V ? __ldg(reinterpret_cast<const uint2*>(p + i)) : make_uint2(0u, 0u);
+    x[0] = __uint_as_float(v.x << 16);
+    x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(v.y << 16);
+    x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = i + e < V ? __bfloat162float(p[i + e]) : 0.f;
+  }
 }
 
+// A sum as an unevaluated pair hi + lo.
+struct Pair {
+  float hi, lo;
+};
 // a + b as s + e exactly
 __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
   s = __fadd_rn(a, b);
   const float bb = __fadd_rn(s, -a);
   e = __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -bb)), __fadd_rn(b, -bb));
 }
-
-// rho = max(p - c q, 0) as a pair of floats
-__device__ __forceinline__ void residual(float p, float q, float ch, float cl, float& hi, float& lo) {
-  const float t = __fmul_rn(ch, q);
-  const float te = __fmaf_rn(cl, q, __fmaf_rn(ch, q, -t));
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
   float s, e;
-  two_sum(p, -t, s, e);
-  e = __fadd_rn(e, -te);
-  const bool pos = __fadd_rn(s, e) > 0.f;
-  hi = pos ? s : 0.f;
-  lo = pos ? e : 0.f;
+  two_sum(a.hi, b.hi, s, e);
+  return {s, __fadd_rn(__fadd_rn(a.lo, b.lo), e)};
+}
+__device__ __forceinline__ double wide(Pair a) { return (double)a.hi + (double)a.lo; }
+template <int kLanes>
+__device__ __forceinline__ Pair lanes_sum(Pair v) {   // the same in every lane of the group
+#pragma unroll
+  for (int m = kLanes / 2; m >= 1; m >>= 1) v = add(v, {__shfl_xor_sync(kAll, v.hi, m), __shfl_xor_sync(kAll, v.lo, m)});
+  return v;
 }
 
-struct Shared {
-  double ctas[2][kCluster];     // totals of the cluster's blocks, by pass parity
-  int ctas_last[2][kCluster];   // their last index with rho > 0
-  double warps[kWarps];
-  int warps_last[kWarps];
-  float ch, cl;
-  int cur, n_gone, act, look, token;
-  double target;
-};
-
-// rho of one vocabulary entry under the present state (c = 0: p without the tokens taken out)
-template <typename T>
+// rho of four entries: max(p - c q, 0) with c = ch + cl (q NULL or c = 0: p), or 0 for a token taken out.
+template <typename T, bool kVec>
 struct Dist {
   const T* p;
   const T* q;
   float ch, cl;
   const int* gone;
-  int n_gone;
-  __device__ __forceinline__ void at(int i, float& hi, float& lo) const {
-    hi = prob(p + i);
-    lo = 0.f;
-    if (q) residual(hi, prob(q + i), ch, cl, hi, lo);
-    for (int g = 0; g < n_gone; ++g)
-      if (gone[g] == i) hi = 0.f;
+  int n_gone, V;
+  __device__ __forceinline__ void of(const float* pv, const float* qv, int i, Pair* rho) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = above_zero(pv[e]);
+      rho[e] = {x, 0.f};
+      if (q) {
+        const float y = above_zero(qv[e]);
+        const float t = __fmul_rn(ch, y), te = __fmaf_rn(cl, y, __fmaf_rn(ch, y, -t));
+        float s, r;
+        two_sum(x, -t, s, r);
+        r = __fadd_rn(r, -te);
+        const bool pos = __fadd_rn(s, r) > 0.f;
+        rho[e] = {pos ? s : 0.f, pos ? r : 0.f};
+      }
+    }
+    for (int g = 0; g < n_gone; ++g) {
+      const int at = gone[g] - i;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (at == e) rho[e] = {0.f, 0.f};
+    }
+  }
+  // Sum of chunks [c0, c1), the same in every lane.
+  __device__ __forceinline__ Pair sum(int c0, int c1) const {
+    constexpr int kBatch = 4;   // chunks in flight
+    const int lane = threadIdx.x & 31;
+    Pair acc[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = {0.f, 0.f};
+    for (int c = c0; c < c1; c += kBatch) {
+      float pv[kBatch][4], qv[kBatch][4];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = c + k < c1 ? (c + k) * kChunk4 + 4 * lane : V;
+        load4<kVec>(p, i, V, pv[k]);
+        if (q) load4<kVec>(q, i, V, qv[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        Pair rho[4];
+        of(pv[k], qv[k], c + k < c1 ? (c + k) * kChunk4 + 4 * lane : V, rho);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = add(acc[e], rho[e]);
+      }
+    }
+    return lanes_sum<32>(add(add(acc[0], acc[1]), add(acc[2], acc[3])));
   }
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) verify_kernel(const VerifyArgs a) {
+// Of n <= 32 parts (lane r < n holds part r's sum), the first whose running sum passes the target; the
+// target then counts from that part's start. Where none passes (the sums agree with the whole only to
+// rounding, or u_next is not below 1) the last part that holds anything, and the target becomes
+// infinite, so that later steps do the same. -1 if every part is empty.
+__device__ __forceinline__ int pick(double v, int n, double& target) {
+  const int lane = threadIdx.x & 31;
+  double incl = lane < n ? v : 0.0;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    if (m >= n) break;
+    const double up = __shfl_up_sync(kAll, incl, m);
+    if (lane >= m) incl += up;
+  }
+  const unsigned over = __ballot_sync(kAll, lane < n && v > 0.0 && incl > target);
+  const unsigned any = __ballot_sync(kAll, lane < n && v > 0.0);
+  if (over) {
+    const int who = __ffs(over) - 1;
+    target -= __shfl_sync(kAll, incl - v, who);
+    return who;
+  }
+  target = INFINITY;
+  return any ? 31 - __clz(any) : -1;
+}
+
+struct Shared {
+  Pair ctas[2][kCluster];   // totals of the cluster's blocks, by pass parity
+  Pair warps[kWarps];
+  float ch, cl;
+  int cur, n_gone, act, found, c0, c1;
+  double target;
+};
+
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCluster, 1, 1) verify_kernel(const VerifyArgs a) {
   extern __shared__ __align__(16) uint8_t dyn[];
   __shared__ Shared sh;
   float* s_p = reinterpret_cast<float*>(dyn);          // p and q of node i's token at its parent
@@ -113,9 +201,11 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) ver
   const size_t row = (size_t)b * a.N;
   const T* P = static_cast<const T*>(a.p) + row * a.V;
   const T* Q = a.q ? static_cast<const T*>(a.q) + row * a.V : nullptr;
+  const double u_next = (double)__ldg(a.u_next + b);
   for (int i = tid + 1; i < n; i += kThreads) {
     int parent = __ldg(a.parents + row + i);
     const int t = __ldg(a.tokens + row + i);
+    s_u[i] = __ldg(a.u + row + i);
     if (parent < 0 || parent >= i || t < 0 || t >= a.V) {
       atomicCAS(a.err, 0, kErrDeviceIndex);
       parent = -1;
@@ -125,23 +215,19 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) ver
     }
     s_parent[i] = parent;
     s_token[i] = t;
-    s_u[i] = __ldg(a.u + row + i);
   }
   __syncthreads();
 
-  // the vocabulary's runs: warp w of block r takes run r kWarps + w
-  const int run = (((a.V + kCluster * kWarps - 1) / (kCluster * kWarps)) + 31) & ~31;
-  const long long lo_ll = (long long)(rank * kWarps + warp) * run;
-  const int lo = (int)(lo_ll < a.V ? lo_ll : a.V), hi = lo + run < a.V ? lo + run : a.V;
+  // the vocabulary's chunks, in contiguous runs: block r's, and of those warp w's
+  const int chunks = (a.V + kChunk4 - 1) / kChunk4;
+  auto first = [&](int w) { return (int)((long long)chunks * w / (kCluster * kWarps)); };
+  const int run0 = first(rank * kWarps + warp), run1 = first(rank * kWarps + warp + 1);
 
   // thread 0's walk
   int cur = 0, i = 1, count = 0, n_gone = 0, pass = 0;
-  double c = 0.0, Z = 1.0, c_new = 0.0, u_next = 0.0;
+  double c = 0.0, Z = 1.0, c_new = 0.0;
   bool summed = false, bare = false;   // the totals at hand are the present state's; rho given up for p
-  if (tid == 0 && n > 0) {
-    s_path[count++] = 0;
-    u_next = (double)__ldg(a.u_next + b);
-  }
+  if (tid == 0 && n > 0) s_path[count++] = 0;
   enum { kRefused = 0, kSum = 1, kDone = 2 };
   if (n > 0) {
     while (true) {
@@ -182,48 +268,23 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) ver
       __syncthreads();
       const int act = sh.act;
       if (act == kDone) break;
-      const Dist<T> dist{P + (size_t)sh.cur * a.V, (Q && sh.ch != 0.f) ? Q + (size_t)sh.cur * a.V : nullptr,
-                         sh.ch, sh.cl, s_gone, sh.n_gone};
-      float hs = 0.f, ls = 0.f;
-      int last = -1;
-#pragma unroll 8
-      for (int j = lo + lane; j < hi; j += 32) {
-        float h, l, e;
-        dist.at(j, h, l);
-        if (h > 0.f) last = j;
-        two_sum(hs, h, hs, e);
-        ls += l + e;
-      }
-      double sum = (double)hs + (double)ls;
-#pragma unroll
-      for (int m = 16; m >= 1; m >>= 1) {
-        sum += __shfl_xor_sync(0xffffffffu, sum, m);
-        last = max(last, __shfl_xor_sync(0xffffffffu, last, m));
-      }
-      if (lane == 0) {
-        sh.warps[warp] = sum;
-        sh.warps_last[warp] = last;
-      }
+      const Dist<T, kVec> dist{P + (size_t)sh.cur * a.V, (Q && sh.ch != 0.f) ? Q + (size_t)sh.cur * a.V : nullptr,
+                               sh.ch, sh.cl, s_gone, sh.n_gone, a.V};
+      const Pair mine = dist.sum(run0, run1);
+      if (lane == 0) sh.warps[warp] = mine;
       __syncthreads();
       const int par = pass & 1;
-      if (tid < kCluster) {   // thread r tells block r
-        double total = 0.0;
-        int block_last = -1;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          total += sh.warps[w];
-          block_last = max(block_last, sh.warps_last[w]);
-        }
-        const uint32_t da = ptx::dsmem_addr(&sh.ctas[par][rank], tid), la = ptx::dsmem_addr(&sh.ctas_last[par][rank], tid);
-        asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(da), "d"(total) : "memory");
-        asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(la), "r"(block_last) : "memory");
+      if (warp == 0) {   // the block's total, told to every block by a lane each
+        const Pair total = lanes_sum<kWarps>(sh.warps[lane & (kWarps - 1)]);
+        if (lane < kCluster)
+          asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(ptx::dsmem_addr(&sh.ctas[par][rank], lane)),
+                       "f"(total.hi), "f"(total.lo)
+                       : "memory");
       }
       ptx::cluster_sync_all();
       ++pass;
-      if (tid == 0) {
-        double total = 0.0;
-#pragma unroll
-        for (int r = 0; r < kCluster; ++r) total += sh.ctas[par][r];
+      if (warp == 0) {
+        const double total = wide(lanes_sum<kCluster>(sh.ctas[par][lane & (kCluster - 1)]));
         if (act == kRefused) {
           summed = total > 0.0;
           if (summed) {
@@ -239,100 +300,70 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) ver
         }
       }
     }
-    // the next token: the block, then the warp, then the entry where the running sum passes the target
-    const int par = (pass - 1) & 1;
-    if (tid == 0) {
-      double total = 0.0, before = 0.0;
-      int block = -1, all_last = -1;
-#pragma unroll
-      for (int r = 0; r < kCluster; ++r) {
-        total += sh.ctas[par][r];
-        all_last = max(all_last, sh.ctas_last[par][r]);
+    // the next token: the block, the warp, then eighths of the range down to a chunk
+    if (warp == 0) {
+      const int par = (pass - 1) & 1;
+      const Pair mine = sh.ctas[par][lane & (kCluster - 1)];
+      double target = u_next * wide(lanes_sum<kCluster>(mine));
+      const int block = pick(wide(mine), kCluster, target);
+      int w = -1;
+      if (block == rank) w = pick(wide(sh.warps[lane & (kWarps - 1)]), kWarps, target);
+      if (lane == 0) {
+        sh.found = block == rank;
+        sh.c0 = first(rank * kWarps + w);
+        sh.c1 = first(rank * kWarps + w + 1);
+        sh.target = target;
+        if (block < 0 && rank == 0) a.next_token[b] = -1;   // an empty distribution
       }
-      double target = u_next * total;
-#pragma unroll
-      for (int r = 0; r < kCluster; ++r) {
-        if (block < 0 && before + sh.ctas[par][r] > target) {
-          block = r;
-          target -= before;
-        }
-        if (block < 0) before += sh.ctas[par][r];
-      }
-      int w_found = -1;
-      if (block == rank) {
-        before = 0.0;
-        int w_last = -1;
-        for (int w = 0; w < kWarps; ++w) {
-          if (sh.warps[w] > 0.0) w_last = w;
-          if (w_found < 0 && before + sh.warps[w] > target) {
-            w_found = w;
-            target -= before;
-          }
-          if (w_found < 0) before += sh.warps[w];
-        }
-        if (w_found < 0) {   // by rounding alone: the block's last run with anything in it
-          w_found = w_last;
-          target -= before;
-        }
-      }
-      sh.target = target;
-      sh.look = w_found;   // the warp of this block that looks, if any
-      sh.token = (block < 0 && rank == 0) ? all_last : -2;   // nothing passes the target (u_next of 1, an empty row)
     }
     __syncthreads();
-    const Dist<T> dist{P + (size_t)sh.cur * a.V, (Q && sh.ch != 0.f) ? Q + (size_t)sh.cur * a.V : nullptr,
-                       sh.ch, sh.cl, s_gone, sh.n_gone};
-    if (warp == sh.look) {
-      // each lane adds a 32nd of the run, a scan over lanes finds the lane, a second one the entry
-      double target = sh.target;
-      const int piece = run / 32;
-      const int p0 = min(lo + lane * piece, hi), p1 = min(p0 + piece, hi);
-      float hs = 0.f, ls = 0.f;
-#pragma unroll 8
-      for (int j = p0; j < p1; ++j) {
-        float h, l, e;
-        dist.at(j, h, l);
-        two_sum(hs, h, hs, e);
-        ls += l + e;
-      }
-      const double mine = (double)hs + (double)ls;
-      double incl = mine;
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const double up = __shfl_up_sync(0xffffffffu, incl, m);
-        if (lane >= m) incl += up;
-      }
-      const unsigned over = __ballot_sync(0xffffffffu, incl > target);
-      int token = sh.warps_last[warp];   // where rounding leaves nothing above the target
-      if (over) {
-        const int who = __ffs(over) - 1;
-        target -= __shfl_sync(0xffffffffu, incl - mine, who);
-        const int q0 = __shfl_sync(0xffffffffu, p0, who), q1 = __shfl_sync(0xffffffffu, p1, who);
-        bool found = false;
-        for (int j0 = q0; j0 < q1 && !found; j0 += 32) {
-          float h = 0.f, l = 0.f;
-          if (j0 + lane < q1) dist.at(j0 + lane, h, l);
-          const double x = (double)h + (double)l;
-          double in2 = x;
-#pragma unroll
-          for (int m = 1; m < 32; m <<= 1) {
-            const double up = __shfl_up_sync(0xffffffffu, in2, m);
-            if (lane >= m) in2 += up;
+    if (sh.found) {
+      const Dist<T, kVec> dist{P + (size_t)sh.cur * a.V, (Q && sh.ch != 0.f) ? Q + (size_t)sh.cur * a.V : nullptr,
+                               sh.ch, sh.cl, s_gone, sh.n_gone, a.V};
+      int c0 = sh.c0, c1 = sh.c1;
+      while (c1 - c0 > 1) {
+        const int per = (c1 - c0 + kWarps - 1) / kWarps;
+        const Pair mine = dist.sum(min(c1, c0 + warp * per), min(c1, c0 + (warp + 1) * per));
+        if (lane == 0) sh.warps[warp] = mine;
+        __syncthreads();
+        if (warp == 0) {
+          double target = sh.target;
+          const int w = max(0, pick(wide(sh.warps[lane & (kWarps - 1)]), kWarps, target));
+          if (lane == 0) {
+            sh.c0 = c0 + w * per;
+            sh.c1 = min(c1, c0 + (w + 1) * per);
+            sh.target = target;
           }
-          const unsigned hit = __ballot_sync(0xffffffffu, in2 > target && x > 0.0);
-          const unsigned any = __ballot_sync(0xffffffffu, x > 0.0);
-          if (hit) {
-            token = j0 + __ffs(hit) - 1;
-            found = true;
-          } else if (any) {
-            token = j0 + 31 - __clz(any);
+        }
+        __syncthreads();
+        c0 = sh.c0;
+        c1 = sh.c1;
+      }
+      if (warp == 0) {
+        const int at = c0 * kChunk4 + 4 * lane;
+        float pv[4], qv[4];
+        load4<kVec>(dist.p, at, a.V, pv);
+        if (dist.q) load4<kVec>(dist.q, at, a.V, qv);
+        Pair rho[4];
+        dist.of(pv, qv, at, rho);
+        double target = sh.target;
+        const int who = max(0, pick(wide(add(add(rho[0], rho[1]), add(rho[2], rho[3]))), 32, target));
+        if (lane == who) {
+          int token = at;
+          bool found = false;
+          double run = 0.0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const double x = wide(rho[e]);
+            run += x;
+            if (!found && x > 0.0) {
+              token = at + e;           // the last that holds anything, unless one passes the target
+              found = run > target;
+            }
           }
-          target -= __shfl_sync(0xffffffffu, in2, 31);
+          a.next_token[b] = token;
         }
       }
-      if (lane == 0) a.next_token[b] = token;
-    } else if (tid == 0 && sh.token != -2) {
-      a.next_token[b] = sh.token;
     }
   } else if (rank == 0 && tid == 0) {
     a.next_token[b] = -1;
@@ -349,13 +380,21 @@ __global__ void __launch_bounds__(kThreads) __cluster_dims__(kCluster, 1, 1) ver
   ptx::cluster_sync_all();   // no block leaves while another may still write to its shared memory
 }
 
+template <typename T>
+void launch(const VerifyArgs& a, bool vec, cudaStream_t s) {
+  const size_t smem = (size_t)a.N * 7 * 4;
+  if (vec) verify_kernel<T, true><<<a.B * kCluster, kThreads, smem, s>>>(a);
+  else verify_kernel<T, false><<<a.B * kCluster, kThreads, smem, s>>>(a);
+}
+
 }  // namespace
 
 cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t s) {
-  const size_t smem = (size_t)a.N * 7 * 4;
+  const uintptr_t quad = a.bf16 ? 8 : 16;   // bytes of four entries
+  const bool vec = a.V % 4 == 0 && reinterpret_cast<uintptr_t>(a.p) % quad == 0 && reinterpret_cast<uintptr_t>(a.q) % quad == 0;
   const int slot = stage_timer_begin(s, kKernVerifyDraft);
-  if (a.bf16) verify_kernel<__nv_bfloat16><<<a.B * kCluster, kThreads, smem, s>>>(a);
-  else verify_kernel<float><<<a.B * kCluster, kThreads, smem, s>>>(a);
+  if (a.bf16) launch<__nv_bfloat16>(a, vec, s);
+  else launch<float>(a, vec, s);
   const cudaError_t e = cudaGetLastError();
   stage_timer_end(slot, s);
   return e;

@@ -347,7 +347,7 @@ gdr_status gdr_backward_chunked_saved(const void* q, const void* k, const void* 
  * Pairs are (j, j + R/2), or (2j, 2j + 1) with interleaved != 0.
  *   q [B, N, Hq, D], k [B, N, Hk, D] dt   token i of row b starts at (b N + i) *_tok elements, head h
  *                          *_head further (slices of one projection are read in place); strides
- *                          multiples of 16 bytes
+ *                          multiples of 16 bytes, of at most 2^22 elements
  *   q_w, k_w [D] float32   norm weights;  eps >= 0
  *   inv_freq [R/2] float64 radians per position;  pos [B, N] int32
  *   q_out [B, N, Hq, D], k_out [B, N, Hk, D] dt   contiguous; may not overlap q or k
