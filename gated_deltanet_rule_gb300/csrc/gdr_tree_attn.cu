@@ -9,12 +9,20 @@
 // and the padding of few rows to 128 is free; above that the tensor cores and the exponentials bound it.
 //
 // One persistent block per SM: one warp loads (TMA boxes of a page's positions into a ring of tile
-// buffers), one thread issues the products (tcgen05: S = Q K^T into one of two TMEM buffers, O += P V
-// with P read from TMEM), eight warps do the softmax: warps w and w + 4 share 32 rows, each half of
-// the tile's columns. S of tile t + 1 is formed while the softmax works on tile t, and P V of tile t
-// while it works on tile t + 1.
+// buffers), one issues the products (tcgen05: S = Q K^T into TMEM, O += P V with P read from TMEM), two
+// warpgroups do the softmax. Three forms share this frame:
+//   kWide   D <= 128 and more than 128 rows a key head: two M tiles an item, one a warpgroup; both read the
+//           same key/value tiles, the products of one run under the softmax of the other.
+//   kNarrow D <= 128, up to 128 rows: one M tile, the warpgroups take every other key tile, each with
+//           its own accumulator, maximum and sum, joined at the end of the segment.
+//   kSplit  D = 256: an accumulator takes half of TMEM, so there is one: the warpgroups take half of each
+//           tile's columns, S alternates between two buffers.
+// A warp of kWide and kNarrow holds whole rows of S (a row a thread): no exchange inside a tile.
+// The products are issued by an elected lane of a converged warp, straight-line, from descriptors that
+// are one word plus a constant: 64 cycles a 128 x 128 x 16 product, against about 100 from a branch on
+// the lane index.
 //
-// Work split: all (row, key head, M tile) items laid end to end are (sum of their key tiles) units; block
+// Work split: all (row, key head, M tile or pair of them) items laid end to end are (sum of their key tiles) units; block
 // c of C takes units [c U / C, (c + 1) U / C), so every SM reads the same number of tiles whatever the
 // rows' lengths. An item cut across blocks leaves its parts (O / l and lse in float32) in the workspace
 // and a second kernel joins them in order.
@@ -48,6 +56,8 @@ constexpr int kM = 128;         // rows of an M tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr long long kDrainBudget = 2000000000ll;   // cycles an aborting block waits for its own work
 
+enum Form { kSplit = 0, kNarrow = 1, kWide = 2 };
+
 struct Args {
   const int32_t* table;
   const int32_t* ctx;
@@ -57,20 +67,23 @@ struct Args {
   float sl2;                 // scale log2(e)
   __nv_bfloat16* o;
   float* lse;
-  float* part_o;             // [2 C][128][D]
-  float* part_lse;           // [2 C][128]
-  int B, N, Hq, Hk, G, npt, W, P, page, M;
+  float* part_o;             // [2 C][rows of an item][D]
+  float* part_lse;           // [2 C][rows of an item]
+  int B, N, Hq, Hk, G, W, P, page, page_shift, M;
+  int npt, npi;              // nodes of an M tile, of an item
   long long budget;
   int* err;
 };
 
-template <int D>
+template <int D, int kForm>
 struct Cfg {
-  static constexpr int KT = D == 256 ? 64 : 128;             // positions of a tile
+  static constexpr int KT = kForm == kSplit ? 64 : 128;      // positions of a tile
+  static constexpr int kTiles = kForm == kWide ? 2 : 1;      // M tiles of an item
+  static constexpr int kRows = kTiles * kM;
   static constexpr uint32_t kTile = KT * D * 2;              // bytes of a K or V tile
-  static constexpr int NS = D == 64 ? 8 : D == 128 ? 6 : 5;  // tile buffers
-  static constexpr uint32_t kQ = kM * D * 2;
-  static constexpr uint32_t kRing = kQ;
+  static constexpr int NS = D == 64 ? 8 : D == 128 && kForm == kNarrow ? 6 : 5;   // tile buffers
+  static constexpr uint32_t kQTile = kM * D * 2;
+  static constexpr uint32_t kRing = kTiles * kQTile;
   static constexpr uint32_t kRed = kRing + NS * kTile;       // float [2][2][128]
   static constexpr uint32_t kBars = kRed + 2048;
   static constexpr uint32_t kSmem = kBars + 512;
@@ -80,8 +93,8 @@ struct Cfg {
 struct Bars {
   uint64_t full[8], empty[8];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], pv[2];
-  uint64_t clean;      // V of a masked tile has been cleaned (eight warps)
+  uint64_t s_full[2], p_full[2], pv[2];   // by stream (kSplit: by buffer)
+  uint64_t o_free;     // the segment's accumulators have been read
   uint64_t drain;
   uint32_t tmem;
   int bad[3];          // a cleaned node element was not finite, by segment modulo three
@@ -101,18 +114,18 @@ __device__ __forceinline__ bool row_of(const Args& a, int b, int& n, int& ctx) {
   }
   return true;
 }
-// Key tiles of M tile mt: a chain's M tile needs no position past its last node.
+// Key tiles of item mt of a row: a chain's item needs no position past its last node.
 template <int KT>
 __device__ __forceinline__ int tiles_of(const Args& a, int n, int ctx, int mt) {
-  const int nodes = a.mask ? n : min(n, (mt + 1) * a.npt);
+  const int nodes = a.mask ? n : min(n, (mt + 1) * a.npi);
   return (ctx + nodes + KT - 1) / KT;
 }
 // Units of one key head of a row.
 template <int KT>
 __device__ __forceinline__ long long units_of(const Args& a, int n, int ctx) {
   if (n == 0) return 0;
-  const int mts = (n + a.npt - 1) / a.npt;
-  if (a.mask) return (long long)mts * tiles_of<KT>(a, n, ctx, 0);
+  const int mts = (n + a.npi - 1) / a.npi;
+  if (a.mask || mts == 1) return (long long)mts * tiles_of<KT>(a, n, ctx, mts - 1);
   long long u = 0;
   for (int mt = 0; mt < mts; ++mt) u += tiles_of<KT>(a, n, ctx, mt);
   return u;
@@ -144,7 +157,7 @@ struct Walk {
     if (todo <= 0) return false;
     if (index >= 0) {   // the last segment ended its item
       t1 = 0;
-      if (++mt * a.npt >= n) {
+      if (++mt * a.npi >= n) {
         mt = 0;
         if (++hk == a.Hk) {
           hk = 0;
@@ -162,11 +175,56 @@ struct Walk {
     ++index;
     return true;
   }
+  // M tiles of the item that have nodes
+  __device__ __forceinline__ int m_tiles(const Args& a) const { return mt * a.npi + a.npt < n ? a.npi / a.npt : 1; }
 };
 
-// mbar_wait by a whole warp, with one answer for all its lanes.
+// mbar_wait by a whole warp, with one answer for all its lanes. A budget of 0 does not wait at all
+// (try_wait may suspend the thread for a while before it answers).
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, long long budget) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, budget));
+  bool ok;
+  if (budget == 0) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    ok = done != 0;
+  } else {
+    ok = mbar_wait(bar, parity, budget);
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ uint64_t desc64(uint32_t lo, uint32_t hi) { return (uint64_t)lo | ((uint64_t)hi << 32); }
+
+// Two floats in one register pair.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 pack2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(F2 x, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x.v)); }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
 }
 
 // Sum over the block's threads (all of them call), and this thread's sum of those before it.
@@ -237,21 +295,142 @@ __device__ __noinline__ void add_back(const Args& a, int b, int hk, int i, int n
   }
 }
 
-template <int D>
+// Cleans positions from ctx on of a V tile in shared memory: past the row's nodes to 0, elements that are
+// not finite to 0 as well (true if there are any). Threads [0, count) share it.
+template <int D, int KT>
+__device__ __forceinline__ bool clean_tile(uint8_t* vt, int t, int ctx, int end, int thread, int count) {
+  const int r0 = max(0, ctx - t * KT);
+  bool bad = false;
+  for (int x = thread; x < (KT - r0) * (D / 8); x += count) {
+    const int r = r0 + x / (D / 8), ch = x % (D / 8);
+    uint4* p = reinterpret_cast<uint4*>(vt + (ch >> 3) * KT * 128 + r * 128 + (ch & 7) * 16);
+    if (t * KT + r >= end) {
+      *p = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    uint4 v = *p;
+    uint32_t* u = reinterpret_cast<uint32_t*>(&v);
+    bool hit = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if ((u[e] & 0x7F80u) == 0x7F80u) {
+        u[e] &= 0xFFFF0000u;
+        hit = true;
+      }
+      if ((u[e] & 0x7F800000u) == 0x7F800000u) {
+        u[e] &= 0xFFFFu;
+        hit = true;
+      }
+    }
+    if (hit) {
+      *p = v;
+      bad = true;
+    }
+  }
+  return bad;
+}
+
+// Largest of n scores, with four chains.
+template <int n>
+__device__ __forceinline__ float largest(const float* x) {
+  float m[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+  for (int c = 4; c < n; c += 4) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m[e] = fmaxf(m[e], x[c + e]);
+  }
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+// p = 2^(x sl2 + off) of n scores as bf16 pairs; returns their float32 sum.
+template <int n>
+__device__ __forceinline__ float weights(const float* x, float sl2, float off, uint32_t* p) {
+  const F2 k = pack2(sl2, sl2), o = pack2(off, off);
+  F2 sum[2] = {{0}, {0}};
+#pragma unroll
+  for (int c = 0; c < n; c += 2) {
+    float a, b;
+    unpack2(fma2(pack2(x[c], x[c + 1]), k, o), a, b);
+    a = ex2_approx(a);
+    b = ex2_approx(b);
+    sum[(c >> 1) & 1] = add2(sum[(c >> 1) & 1], pack2(a, b));
+    p[c >> 1] = pack_bf16x2(a, b);
+  }
+  float a, b;
+  unpack2(add2(sum[0], sum[1]), a, b);
+  return a + b;
+}
+template <int n>
+__device__ __forceinline__ void hide(float* x, uint64_t seen) {
+#pragma unroll
+  for (int c = 0; c < n; ++c)
+    if (!(seen >> c & 1)) x[c] = -INFINITY;
+}
+// Multiplies kCols accumulator columns of the warp's rows.
+template <int kCols>
+__device__ __forceinline__ void rescale(uint32_t at, float f) {
+#pragma unroll 2
+  for (int c = 0; c < kCols; c += 32) {
+    float o[32];
+    uint32_t u[32];
+    tmem_ld32(at + c, o);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * f);
+    tmem_st32(at + c, u);
+  }
+}
+// Scaled accumulator columns to o (bf16) or to the part (float32).
+__device__ __forceinline__ void put32(const float* o, bool whole, __nv_bfloat16* out, float* part) {
+  if (whole) {
+    uint4* to = reinterpret_cast<uint4*>(out);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      to[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
+                         pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+  } else {
+    float4* to = reinterpret_cast<float4*>(part);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) to[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+  }
+}
+
+constexpr uint32_t kSoftmaxBar = 1;   // named barrier of the eight softmax warps; 2 .. 5: pairs of kSplit
+
+template <int D, int kForm>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_attn_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                     const __grid_constant__ CUtensorMap mv, const Args a) {
-  using C = Cfg<D>;
-  constexpr int KT = C::KT, NS = C::NS, kCols = KT / 2;
+                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ Args a) {
+  using C = Cfg<D, kForm>;
+  constexpr int KT = C::KT, NS = C::NS;
   extern __shared__ __align__(1024) uint8_t sm[];
   Bars& s = *reinterpret_cast<Bars*>(sm + C::kBars);
   float* red = reinterpret_cast<float*>(sm + C::kRed);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   if (smem_u32(sm) & 1023u) {   // the swizzled tiles rely on it
     if (tid == 0) atomicCAS(a.err, 0, kErrTimeout);
     return;
   }
 
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], 1);
+    }
+    mbar_init(&s.q_full, 1);
+    mbar_init(&s.q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.s_full[i], 1);
+      mbar_init(&s.p_full[i], kForm == kSplit ? 8 : 4);
+      mbar_init(&s.pv[i], 1);
+    }
+    mbar_init(&s.o_free, 8);
+    mbar_init(&s.drain, 1);
+    for (int i = 0; i < 3; ++i) s.bad[i] = 0;
+    fence_mbar_init();
+    prefetch_tmap(&mq);
+    prefetch_tmap(&mk);
+    prefetch_tmap(&mv);
+  }
+  if (warp == 1) tmem_alloc(&s.tmem, 512);
   // the block's share of the units
   {
     const int per = (a.B + kThreads - 1) / kThreads, r0 = min(a.B, tid * per), r1 = min(a.B, r0 + per);
@@ -286,65 +465,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
-  if (tid == 0) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&s.full[i], 1);
-      mbar_init(&s.empty[i], 1);
-    }
-    mbar_init(&s.q_full, 1);
-    mbar_init(&s.q_empty, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.s_full[i], 1);
-      mbar_init(&s.p_full[i], 8);
-      mbar_init(&s.pv[i], 1);
-    }
-    mbar_init(&s.clean, 8);
-    mbar_init(&s.drain, 1);
-    for (int i = 0; i < 3; ++i) s.bad[i] = 0;
-    fence_mbar_init();
-    prefetch_tmap(&mq);
-    prefetch_tmap(&mk);
-    prefetch_tmap(&mv);
-  }
-  if (warp == 1) tmem_alloc(&s.tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tb = s.tmem;
   launch_dependents();
-
+  // A softmax thread holds a row of S in registers. The block was launched with 384 x 168 registers; the
+  // first warpgroup gives back 128 x 88 of them, the other two take 256 x 40.
   bool ok = true;
-  if (warp == 0) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 0) {
     // ------------------------------------------------------------------------------ loads
     Walk<KT> w;
     w.start(a, s);
     const int rows = min(a.page, KT);                       // positions of one box
     const uint32_t box = rows * 128u;                       // its bytes in one 64-column slab
+    const int most = KT / rows;                             // boxes of a tile
     long long it = 0;                                       // tiles loaded
     int q_loads = 0;
     while (ok && w.next(a)) {
+      const int end = w.ctx + w.n;
+      const int32_t* table = a.table + (size_t)w.b * a.M;
+      // this lane's box of tile t: its page, or -1 where the tile has no such box
+      auto page_at = [&](int t) {
+        const int pos = t * KT + lane * rows;
+        return lane < most && pos < end ? __ldg(table + (pos >> a.page_shift)) : -1;
+      };
+      int pg = page_at(w.t0);
       if (w.index > 0) ok = warp_wait(&s.q_empty, (w.index - 1) & 1, a.budget);
       if (!ok) break;
       if (lane == 0) {
-        mbar_arrive_expect_tx(&s.q_full, (uint32_t)(D / 64) * a.G * a.npt * 128u);
-        for (int h = 0; h < D / 64; ++h)
-          tma_load_4d(sm + h * kM * 128, &mq, &s.q_full, h * 64, w.hk * a.G, w.mt * a.npt, w.b);
+        const int m_tiles = w.m_tiles(a);
+        mbar_arrive_expect_tx(&s.q_full, (uint32_t)(D / 64) * m_tiles * a.G * a.npt * 128u);
+        for (int m = 0; m < m_tiles; ++m)
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_4d(sm + m * C::kQTile + h * kM * 128, &mq, &s.q_full, h * 64, w.hk * a.G, w.mt * a.npi + m * a.npt, w.b);
       }
+      __syncwarp();
       ++q_loads;
-      const int end = w.ctx + w.n;
-      const int32_t* table = a.table + (size_t)w.b * a.M;
       for (int t = w.t0; ok && t < w.t1; ++t) {
-        const int base = t * KT;
-        const int pieces = min(KT / rows, (end - base + rows - 1) / rows);
-        int pg = -1, at = 0;
-        if (lane < pieces) {
-          const int pos = base + lane * rows;
-          pg = __ldg(table + pos / a.page);
-          at = pos % a.page;
-          if (pg < 0 || pg >= a.P) {   // read as zeros (a coordinate outside the tensor) and reported
-            atomicCAS(a.err, 0, kErrDeviceIndex);
-            pg = -1;
-          }
+        const int pieces = min(most, (end - t * KT + rows - 1) / rows);
+        const int at = (t * KT + lane * rows) & (a.page - 1);
+        int src = pg;
+        if (t + 1 < w.t1) pg = page_at(t + 1);   // (in flight while this tile waits for its buffers)
+        if (lane < pieces && (src < 0 || src >= a.P)) {   // read as zeros (outside the tensor) and reported
+          atomicCAS(a.err, 0, kErrDeviceIndex);
+          src = -1;
         }
         for (int kv = 0; kv < 2; ++kv, ++it) {
           const int slot = (int)(it % NS);
@@ -354,9 +521,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane < pieces) {
             uint8_t* dst = sm + C::kRing + slot * C::kTile + lane * box;
+#pragma unroll
             for (int h = 0; h < D / 64; ++h)
-              tma_load_4d(dst + h * KT * 128, kv ? &mv : &mk, &s.full[slot], h * 64, w.hk, at, pg);
+              tma_load_4d(dst + h * KT * 128, kv ? &mv : &mk, &s.full[slot], h * 64, w.hk, at, src);
           }
+          __syncwarp();
         }
       }
     }
@@ -364,238 +533,284 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (long long i = it > NS ? it - NS : 0; i < it; ++i)
       warp_wait(&s.full[i % NS], (uint32_t)(i / NS) & 1, kDrainBudget);
     if (q_loads > 0) warp_wait(&s.q_full, (q_loads - 1) & 1, kDrainBudget);
-  } else if (warp == 1) {
+    } else if (warp == 1) {
     // ------------------------------------------------------------------------------ products
-    if (lane == 0) {
-      Walk<KT> w;
-      w.start(a, s);
-      constexpr uint32_t kIdS = idesc_bf16(kM, KT, false, false), kIdO = idesc_bf16(kM, D, false, true);
-      const uint32_t qb = smem_u32(sm), ring = smem_u32(sm + C::kRing);
-      long long g = 0;   // tiles begun, over all segments
-      while (ok && w.next(a)) {
-        ok = mbar_wait(&s.q_full, w.index & 1, a.budget);
-        const int T = w.t1 - w.t0;
-        // S of tile x: its buffer is free once P V of tile x - 2 is done
-        auto scores = [&](long long x, bool last) {
-          if (x >= 2) ok = ok && mbar_wait(&s.pv[x & 1], (uint32_t)((x - 2) >> 1) & 1, a.budget);
-          const int slot = (int)((2 * x) % NS);
-          ok = ok && mbar_wait(&s.full[slot], (uint32_t)((2 * x) / NS) & 1, a.budget);
-          if (!ok) return;
-          tc_fence_after();
-          const uint32_t kb = ring + slot * C::kTile;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_bf16(tb + (uint32_t)(x & 1) * KT, smem_desc(qb + (kk >> 2) * kM * 128 + (kk & 3) * 32, 16, 1024),
-                     smem_desc(kb + (kk >> 2) * KT * 128 + (kk & 3) * 32, 16, 1024), kIdS, kk > 0);
-          mma_commit(&s.s_full[x & 1]);
-          mma_commit(&s.empty[slot]);
-          if (last) mma_commit(&s.q_empty);
-        };
-        if (ok) scores(g, T == 1);
-        for (int j = 0; ok && j < T; ++j, ++g) {
-          if (j + 1 < T) scores(g + 1, j + 2 == T);
-          ok = ok && mbar_wait(&s.p_full[g & 1], (uint32_t)(g >> 1) & 1, a.budget);
-          const int slot = (int)((2 * g + 1) % NS);
-          ok = ok && mbar_wait(&s.full[slot], (uint32_t)((2 * g + 1) / NS) & 1, a.budget);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t vb = ring + slot * C::kTile, pb = tb + (uint32_t)(g & 1) * KT;
-#pragma unroll
-          for (int kk = 0; kk < KT / 16; ++kk)
-            mma_f16_tmem_a(tb + C::kTmemO, pb + kk * 8, smem_desc(vb + kk * 2048, KT * 128, 1024), kIdO, j > 0 || kk > 0);
-          mma_commit(&s.pv[g & 1]);
-          mma_commit(&s.empty[slot]);
-        }
-      }
-      // no product of this block is left in flight
-      mma_commit(&s.drain);
-      mbar_wait(&s.drain, 0, kDrainBudget);
-    }
-  } else if (warp >= 4) {
-    // ------------------------------------------------------------------------------ softmax
     Walk<KT> w;
     w.start(a, s);
-    const int half = (warp - 4) >> 2, quarter = warp & 3, row = 32 * quarter + lane;
-    const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
-    const uint32_t pair_bar = 1 + quarter;
-    const int wtid = tid - 128;
-    long long g = 0;
-    uint32_t cleaned = 0;   // masked tiles so far
-    while (ok && w.next(a)) {
-      if (wtid == 0) s.bad[(w.index + 1) % 3] = 0;   // read two segments ago, set in the next
-      const int used = min(a.npt, w.n - w.mt * a.npt) * a.G;
-      const bool active = 32 * quarter < used, live = row < used;
-      const int i = w.mt * a.npt + (live ? row / a.G : 0), hg = live ? row % a.G : 0;
-      const uint64_t* words = a.mask ? a.mask + ((size_t)w.b * a.N + i) * a.W : nullptr;
-      const int end = w.ctx + w.n;
-      float m_ref = -INFINITY, l = 0.f;
-      bool masked_any = false;
-      for (int t = w.t0; t < w.t1; ++t, ++g) {
-        const bool masked = (t + 1) * KT > w.ctx;
-        if (masked) {
-          // clean V of positions past ctx
-          masked_any = true;
-          const long long vi = 2 * g + 1;
-          const int slot = (int)(vi % NS);
-          ok = ok && warp_wait(&s.full[slot], (uint32_t)(vi / NS) & 1, a.budget);
-          if (ok) {
-            uint8_t* vt = sm + C::kRing + slot * C::kTile;
-            const int r0 = max(0, w.ctx - t * KT);
-            bool bad = false;
-            for (int x = wtid; x < (KT - r0) * (D / 8); x += 256) {
-              const int r = r0 + x / (D / 8), ch = x % (D / 8);
-              uint4* p = reinterpret_cast<uint4*>(vt + (ch >> 3) * KT * 128 + r * 128 + (ch & 7) * 16);
-              if (t * KT + r >= end) {
-                *p = make_uint4(0, 0, 0, 0);
-              } else {
-                uint4 v = *p;
-                uint32_t* u = reinterpret_cast<uint32_t*>(&v);
-                bool hit = false;
+    const bool lead = elected();
+    constexpr uint32_t kIdS = idesc_bf16(kM, KT, false, false), kIdO = idesc_bf16(kM, D, false, true);
+    const uint32_t q_lo = (uint32_t)smem_desc(smem_u32(sm), 16, 1024), k_lo = (uint32_t)smem_desc(smem_u32(sm + C::kRing), 16, 1024);
+    const uint32_t v_lo = (uint32_t)smem_desc(smem_u32(sm + C::kRing), KT * 128, 1024);
+    const uint32_t hi = (uint32_t)(smem_desc(0, 16, 1024) >> 32);   // (the strides' high word is the same for all three)
+    // S[buffer] = Q[M tile] K[slot]^T; the K buffer and Q are given back by the last products that read them
+    auto scores = [&](int buf, int m, int slot, bool free_k, bool free_q) {
+      const uint32_t q0 = __shfl_sync(0xffffffffu, q_lo + m * (C::kQTile >> 4), 0);
+      const uint32_t k0 = __shfl_sync(0xffffffffu, k_lo + slot * (C::kTile >> 4), 0);
+      const uint32_t d = __shfl_sync(0xffffffffu, tb + buf * KT, 0);
+      tc_fence_after();
+      if (lead) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  if ((u[e] & 0x7F80u) == 0x7F80u) {
-                    u[e] &= 0xFFFF0000u;
-                    hit = true;
-                  }
-                  if ((u[e] & 0x7F800000u) == 0x7F800000u) {
-                    u[e] &= 0xFFFFu;
-                    hit = true;
-                  }
-                }
-                if (hit) {
-                  *p = v;
-                  bad = true;
-                }
-              }
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_bf16(d, desc64(q0 + (((kk >> 2) * kM * 128 + (kk & 3) * 32) >> 4), hi),
+                   desc64(k0 + (((kk >> 2) * KT * 128 + (kk & 3) * 32) >> 4), hi), kIdS, kk > 0);
+        mma_commit(&s.s_full[buf]);
+        if (free_k) mma_commit(&s.empty[slot]);
+        if (free_q) mma_commit(&s.q_empty);
+      }
+      __syncwarp();
+    };
+    // O[stream] (+)= P[buffer] V[slot]
+    auto outputs = [&](int buf, uint32_t o_col, int slot, bool more, bool free_v) {
+      const uint32_t v0 = __shfl_sync(0xffffffffu, v_lo + slot * (C::kTile >> 4), 0);
+      const uint32_t p = __shfl_sync(0xffffffffu, tb + buf * KT, 0), d = __shfl_sync(0xffffffffu, tb + o_col, 0);
+      const uint32_t acc = __shfl_sync(0xffffffffu, (uint32_t)more, 0);
+      tc_fence_after();
+      if (lead) {
+#pragma unroll
+        for (int kk = 0; kk < KT / 16; ++kk)
+          mma_f16_tmem_a(d, p + kk * 8, desc64(v0 + ((kk * 2048) >> 4), hi), kIdO, kk > 0 ? 1u : acc);
+        mma_commit(&s.pv[buf]);
+        if (free_v) mma_commit(&s.empty[slot]);
+      }
+      __syncwarp();
+    };
+    auto filled = [&](long long fill) { return warp_wait(&s.full[fill % NS], (uint32_t)(fill / NS) & 1, a.budget); };
+    long long g = 0;                // tiles of the segments before
+    long long steps[2] = {0, 0};    // products of each stream (kSplit: buffer) so far
+    while (ok && w.next(a)) {
+      ok = warp_wait(&s.q_full, w.index & 1, a.budget);
+      const int T = w.t1 - w.t0;
+      if constexpr (kForm == kSplit) {
+        for (int j = -1; ok && j < T; ++j) {
+          if (j + 1 < T) {          // S of tile j + 1: its buffer is free once P V of tile j - 1 is done
+            const long long x = g + j + 1;
+            if (x >= 2) ok = warp_wait(&s.pv[x & 1], (uint32_t)((x - 2) >> 1) & 1, a.budget);
+            ok = ok && filled(2 * x);
+            if (!ok) break;
+            scores((int)(x & 1), 0, (int)((2 * x) % NS), true, j + 2 == T);
+          }
+          if (j >= 0) {
+            const long long x = g + j;
+            if (j == 0 && w.index > 0) ok = warp_wait(&s.o_free, (w.index - 1) & 1, a.budget);
+            ok = ok && warp_wait(&s.p_full[x & 1], (uint32_t)(x >> 1) & 1, a.budget);
+            ok = ok && filled(2 * x + 1);
+            if (!ok) break;
+            outputs((int)(x & 1), C::kTmemO, (int)((2 * x + 1) % NS), j > 0, true);
+          }
+        }
+      } else {
+        const int streams = kForm == kWide ? w.m_tiles(a) : 2;
+        // stream st takes tile j = k (kWide) or 2 k + st (kNarrow) at its step k
+        auto tile = [&](int st, int k) { return kForm == kWide ? k : 2 * k + st; };
+        const int last = kForm == kWide ? T : (T + 1) / 2;
+        for (int k = 0; ok && k <= last; ++k) {
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            if (!ok || st >= streams) break;
+            if (k > 0 && tile(st, k - 1) < T) {
+              const int j = tile(st, k - 1);
+              const long long fill = 2 * (g + j) + 1;
+              if (k == 1 && w.index > 0 && st == 0) ok = warp_wait(&s.o_free, (w.index - 1) & 1, a.budget);
+              ok = ok && warp_wait(&s.p_full[st], (uint32_t)(steps[st] - 1) & 1, a.budget);
+              ok = ok && filled(fill);
+              if (!ok) break;
+              outputs(st, C::kTmemO + st * D, (int)(fill % NS), k > 1, kForm == kNarrow || st == streams - 1);
             }
-            if (bad) s.bad[w.index % 3] = 1;
+            if (tile(st, k) < T) {   // S of the next tile, over P of the last one
+              const int j = tile(st, k);
+              const long long fill = 2 * (g + j);
+              if (steps[st] > 0) ok = warp_wait(&s.pv[st], (uint32_t)(steps[st] - 1) & 1, a.budget);
+              ok = ok && filled(fill);
+              if (!ok) break;
+              const bool end_k = kForm == kNarrow || st == streams - 1;
+              scores(st, kForm == kWide ? st : 0, (int)(fill % NS), end_k, j == T - 1 && end_k);
+              ++steps[st];
+            }
+          }
+        }
+      }
+      g += T;
+    }
+    // no product of this block is left in flight
+    if (lead) mma_commit(&s.drain);
+    warp_wait(&s.drain, 0, kDrainBudget);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ------------------------------------------------------------------------------ softmax
+    // A warp whose wait ran out (ok) goes on through the loops without touching TMEM, so that the named
+    // barriers stay matched; every other wait of the block then runs out as well.
+    Walk<KT> w;
+    w.start(a, s);
+    const int st = (warp - 4) >> 2, quarter = warp & 3, row = 32 * quarter + lane;   // st: stream, or half of the columns
+    const uint32_t rows_at = tb + ((uint32_t)(32 * quarter) << 16);
+    const int wtid = tid - 128;
+    long long g = 0, step = 0;
+    while (w.next(a)) {
+      const int m = kForm == kWide ? st : 0;                     // M tile of the item
+      const int node0 = w.mt * a.npi + m * a.npt;
+      const int used = max(0, min(a.npt, w.n - node0)) * a.G;
+      const bool active = 32 * quarter < used, live = row < used;
+      const int i = node0 + (live ? row / a.G : 0), hg = live ? row % a.G : 0;
+      const uint64_t* words = a.mask && live ? a.mask + ((size_t)w.b * a.N + i) * a.W : nullptr;
+      const int end = w.ctx + w.n;
+      const int T = w.t1 - w.t0;
+      const bool masked_any = w.t1 * KT > w.ctx;
+      float m_ref = -INFINITY, l = 0.f;
+      const bool works = kForm != kWide || st == 0 || used > 0;   // (an item's second M tile may be empty)
+      constexpr int kStep = kForm == kNarrow ? 2 : 1;
+      for (int j = kForm == kNarrow ? st : 0; works && j < T; j += kStep, ++step) {
+        const int t = w.t0 + j;
+        const bool masked = (t + 1) * KT > w.ctx;
+        const int buf = kForm == kSplit ? (int)((g + j) & 1) : st;
+        const uint32_t phase = kForm == kSplit ? (uint32_t)((g + j) >> 1) & 1 : (uint32_t)step & 1;
+        // (kWide: the first M tile's product with V is issued first, so its warps clean for both)
+        if (masked && (kForm != kWide || st == 0)) {
+          const long long fill = 2 * (g + j) + 1;
+          ok = ok && warp_wait(&s.full[fill % NS], (uint32_t)(fill / NS) & 1, a.budget);
+          if (ok) {
+            uint8_t* vt = sm + C::kRing + (fill % NS) * C::kTile;
+            if (clean_tile<D, KT>(vt, t, w.ctx, end, kForm == kSplit ? wtid : wtid & 127, kForm == kSplit ? 256 : 128))
+              s.bad[w.index % 3] = 1;
             fence_async_smem();
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s.clean);
-          ++cleaned;
         }
-        ok = ok && warp_wait(&s.s_full[g & 1], (uint32_t)(g >> 1) & 1, a.budget);
-        const uint32_t sb = tb + lane_base + (uint32_t)(g & 1) * KT;
+        ok = ok && warp_wait(&s.s_full[buf], phase, a.budget);
+        const uint32_t sb = rows_at + buf * KT;
         if (active) {
+          // this thread's columns of its row: all, or a half
+          constexpr int kCols = kForm == kSplit ? KT / 2 : KT;
+          const int col0 = kForm == kSplit ? st * kCols : 0;
           float x[kCols];
           if (ok) {
             tc_fence_after();
-            if constexpr (kCols == 64) tmem_ld64(sb + half * kCols, x);
-            else tmem_ld32(sb + half * kCols, x);
+            if constexpr (kCols == 32) {
+              tmem_ld32(sb + col0, x);
+            } else {
+              tmem_ld64(sb, x);
+              tmem_ld64(sb + 64, x + 64);
+            }
           }
           if (masked && live) {
-            const uint64_t vis = seen(a, words, i, w.n, (long long)t * KT + half * kCols - w.ctx);
-#pragma unroll
-            for (int c = 0; c < kCols; ++c)
-              if (!(vis >> c & 1)) x[c] = -INFINITY;
+            const long long rel = (long long)t * KT + col0 - w.ctx;
+            if constexpr (kCols == 32) {
+              hide<32>(x, seen(a, words, i, w.n, rel));
+            } else {
+              hide<64>(x, seen(a, words, i, w.n, rel));
+              hide<64>(x + 64, seen(a, words, i, w.n, rel + 64));
+            }
           }
-          float mx = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < kCols; ++c) mx = fmaxf(mx, x[c]);
-          float* mine = red + (g & 1) * 256;
-          mine[half * 128 + row] = mx;
-          tc_fence_before();   // (P goes over scores that the other half has read)
-          ok = named_bar_and(pair_bar, 64, ok);   // both halves leave together
-          if (!ok) break;
-          tc_fence_after();
-          mx = fmaxf(mx, mine[(half ^ 1) * 128 + row]);
+          float mx = largest<kCols>(x);
+          if constexpr (kForm == kSplit) {
+            float* mine = red + ((g + j) & 1) * 256;
+            mine[st * 128 + row] = mx;
+            tc_fence_before();   // (P goes over scores that the other half has read)
+            ok = named_bar_and(2 + quarter, 64, ok);
+            tc_fence_after();
+            mx = fmaxf(mx, mine[(st ^ 1) * 128 + row]);
+          }
           // (rows past the tile's nodes hold arbitrary scores and never ask for a new reference)
           const bool need = live && mx > m_ref && (m_ref == -INFINITY || (mx - m_ref) * a.sl2 > 8.f);
           if (__any_sync(0xffffffffu, need)) {
             const float m_new = live ? fmaxf(m_ref, mx) : m_ref;
-            if (t > w.t0) {
+            if (j >= kStep) {
               const float f = m_ref == m_new ? 1.f : ex2_approx((m_ref - m_new) * a.sl2);
               l *= f;
-              ok = warp_wait(&s.pv[(g - 1) & 1], (uint32_t)((g - 1) >> 1) & 1, a.budget);
+              if (kForm == kSplit) ok = ok && warp_wait(&s.pv[buf ^ 1], (uint32_t)((g + j - 1) >> 1) & 1, a.budget);
+              else ok = ok && warp_wait(&s.pv[st], (uint32_t)(step - 1) & 1, a.budget);
               if (ok) {
                 tc_fence_after();
-#pragma unroll
-                for (int c = 0; c < D / 2; c += 32) {
-                  float o[32];
-                  uint32_t u[32];
-                  const uint32_t at = tb + lane_base + C::kTmemO + half * (D / 2) + c;
-                  tmem_ld32(at, o);
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * f);
-                  tmem_st32(at, u);
-                }
+                if (kForm == kSplit) rescale<D / 2>(rows_at + C::kTmemO + st * (D / 2), f);
+                else rescale<D>(rows_at + C::kTmemO + st * D, f);
               }
             }
             m_ref = m_new;
           }
           const float off = m_ref == -INFINITY ? 0.f : -m_ref * a.sl2;
-          uint32_t p[kCols / 2];
-          float sum = 0.f;
+          if constexpr (kCols == 32) {
+            uint32_t p[16];
+            l += weights<32>(x, a.sl2, off, p);
+            if (ok) tmem_st16_nowait(sb + st * 16, p);
+          } else {
 #pragma unroll
-          for (int c = 0; c < kCols; c += 2) {
-            const float e0 = ex2_approx(fmaf(x[c], a.sl2, off)), e1 = ex2_approx(fmaf(x[c + 1], a.sl2, off));
-            sum += e0 + e1;
-            p[c / 2] = pack_bf16x2(e0, e1);
-          }
-          l += sum;
-          if (ok) {
-            if constexpr (kCols == 64) {
-              tmem_st32(sb + half * 32, p);
-            } else {
-              tmem_st16_nowait(sb + half * 16, p);
-              tmem_wait_st();
+            for (int c = 0; c < 128; c += 32) {
+              uint32_t p[16];
+              l += weights<32>(x + c, a.sl2, off, p);
+              if (ok) tmem_st16_nowait(sb + c / 2, p);
             }
           }
+          if (ok) tmem_wait_st();
         }
-        if (!active && !ok) break;
         tc_fence_before();
         __syncwarp();
-        if (lane == 0 && ok) mbar_arrive(&s.p_full[g & 1]);
+        if (lane == 0 && ok) mbar_arrive(&s.p_full[buf]);
       }
-      if (!ok && !active) break;
-      // the segment's result
-      const long long last = g - 1;
-      ok = ok && warp_wait(&s.pv[last & 1], (uint32_t)(last >> 1) & 1, a.budget);
-      if (masked_any) ok = ok && warp_wait(&s.clean, (cleaned - 1) & 1, a.budget);
-      if (!active) continue;
-      float* mine = red + (g & 1) * 256;
-      mine[half * 128 + row] = l;
-      ok = named_bar_and(pair_bar, 64, ok);
-      if (!ok) break;
-      l += mine[(half ^ 1) * 128 + row];
-      tc_fence_after();
-      const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-      const float lse = l > 0.f || l != l ? m_ref * a.sl2 * (1.f / kLog2e) + logf(l) : -INFINITY;
-      const bool whole = w.t0 == 0 && w.t1 == w.tiles;
+      // the segment's result: the last product of this stream, then what the warpgroups tell each other
+      if (works && T > (kForm == kNarrow ? st : 0)) {
+        if (kForm == kSplit) ok = ok && warp_wait(&s.pv[(g + T - 1) & 1], (uint32_t)((g + T - 1) >> 1) & 1, a.budget);
+        else ok = ok && warp_wait(&s.pv[st], (uint32_t)(step - 1) & 1, a.budget);
+      }
+      float* ml = red + ((g + T) & 1) * 256;   // (kSplit: not where the last tile's maxima are)
+      float2* both_ml = reinterpret_cast<float2*>(red);
+      if constexpr (kForm == kSplit) ml[st * 128 + row] = l;
+      if constexpr (kForm == kNarrow) both_ml[st * 128 + row] = make_float2(m_ref, l);
+      ok = named_bar_and(kSoftmaxBar, 256, ok);
       const bool bad = masked_any && s.bad[w.index % 3];
+      if (wtid == 0) s.bad[(w.index + 2) % 3] = 0;   // read before this barrier, set after the next
+      float self = 1.f, other = 0.f;                  // kNarrow: factors of the two streams' accumulators
+      if constexpr (kForm == kSplit) l += ml[(st ^ 1) * 128 + row];
+      if constexpr (kForm == kNarrow) {
+        const float2 two = both_ml[(st ^ 1) * 128 + row];
+        const float top = fmaxf(m_ref, two.x);
+        self = m_ref == top ? 1.f : ex2_approx((m_ref - top) * a.sl2);
+        other = two.x == top ? 1.f : ex2_approx((two.x - top) * a.sl2);
+        l = l * self + two.y * other;
+        m_ref = top;
+      }
+      if constexpr (kForm != kWide) ok = named_bar_and(kSoftmaxBar, 256, ok);   // `red` may be written again
+      const bool sees = l > 0.f || l != l;
+      const float inv = sees ? 1.f / l : 0.f;
+      const float lse = sees ? m_ref * a.sl2 * (1.f / kLog2e) + logf(l) : -INFINITY;
+      const bool whole = w.t0 == 0 && w.t1 == w.tiles;
       const size_t orow = ((size_t)w.b * a.N + i) * a.Hq + w.hk * a.G + hg;
-      const size_t prow = (size_t)(2 * blockIdx.x + (w.index > 0)) * kM + row;
+      const size_t prow = (size_t)(2 * blockIdx.x + (w.index > 0)) * C::kRows + m * kM + row;
+      constexpr int kOut = kForm == kWide ? D : D / 2;           // this thread's output columns
+      const int d0 = kForm == kWide ? 0 : st * (D / 2);
+      if (active && ok) {
+        tc_fence_after();
+        const bool both = kForm == kNarrow && T > 1;             // (one tile: the second accumulator was not written)
+        const float f0 = (st == 0 || kForm != kNarrow ? self : other) * inv, f1 = (st == 0 ? other : self) * inv;
 #pragma unroll
-      for (int c = 0; c < D / 2; c += 32) {
-        float o[32];
-        const int d0 = half * (D / 2) + c;
-        tmem_ld32(tb + lane_base + C::kTmemO + d0, o);
-        if (!live) continue;
+        for (int c = 0; c < kOut; c += 32) {
+          float o[32];
+          tmem_ld32(rows_at + C::kTmemO + (kForm == kWide ? st * D : 0) + d0 + c, o);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] *= inv;
-        if (whole) {
-          uint4* out = reinterpret_cast<uint4*>(a.o + orow * D + d0);
+          for (int e = 0; e < 32; ++e) o[e] *= f0;
+          if constexpr (kForm == kNarrow) {
+            if (both) {
+              float o1[32];
+              tmem_ld32(rows_at + C::kTmemO + D + d0 + c, o1);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            out[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
-                                pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
-        } else {
-          float4* out = reinterpret_cast<float4*>(a.part_o + prow * D + d0);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) out[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], f1, o[e]);
+            }
+          }
+          if (live) put32(o, whole, a.o + orow * D + d0 + c, a.part_o + prow * D + d0 + c);
+        }
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0 && ok) mbar_arrive(&s.o_free);
+      if (active && live && ok) {
+        if (bad) {
+          if (whole) add_back(a, w.b, w.hk, i, w.n, w.ctx, w.t0 * KT, w.t1 * KT, D, d0, kOut, a.o + orow * D + d0);
+          else add_back(a, w.b, w.hk, i, w.n, w.ctx, w.t0 * KT, w.t1 * KT, D, d0, kOut, a.part_o + prow * D + d0);
+        }
+        if (kForm == kWide || st == 0) {
+          if (!whole) a.part_lse[prow] = lse;
+          else if (a.lse) a.lse[orow] = lse;
         }
       }
-      if (bad && live) {
-        const int d0 = half * (D / 2);
-        if (whole) add_back(a, w.b, w.hk, i, w.n, w.ctx, w.t0 * KT, w.t1 * KT, D, d0, D / 2, a.o + orow * D + d0);
-        else add_back(a, w.b, w.hk, i, w.n, w.ctx, w.t0 * KT, w.t1 * KT, D, d0, D / 2, a.part_o + prow * D + d0);
-      }
-      if (half == 0 && live) {
-        if (!whole) a.part_lse[prow] = lse;
-        else if (a.lse) a.lse[orow] = lse;
-      }
-      tc_fence_before();
+      g += T;
     }
   }
   if (!ok && lane == 0) atomicCAS(a.err, 0, kErrTimeout);
@@ -609,19 +824,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of items that several blocks shared, and fills the rows of absent nodes (0, -inf):
-// o = sum_s e^(lse_s - lse) o_s over a row's parts. Few items have many parts each (one item is cut over
-// up to every block) and few rows: kRowWarps = 8 warps then share a (node, query head) row, warp w
-// taking parts w, w + 8, ... and the block adding the warps' sums in order; with many items a row has
-// one to three parts and one warp takes it. Parts are read four at a time: the loop is bound by their
-// latency, 33 -> 8 us for 38 parts of 224 rows of 256.
+// o = sum_s e^(lse_s - lse) o_s over a row's parts. A block takes rows of one item, so an item that one
+// block wrote whole costs a block's start and no more. Few items have many parts each (one item is cut
+// over up to every block): with kShare the block's eight warps share a row, warp w taking parts w, w + 8,
+// ... and the block adding the warps' sums in order; otherwise a warp takes a row. Parts are read four at
+// a time: the loop is bound by their latency (38 parts of 224 rows of 256: 33 us one after the other by
+// one warp a row, 8 us so).
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
-template <int D, int kRowWarps>
-__global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const Args a) {
-  constexpr int KT = Cfg<D>::KT, kVec = D / 32;
+template <int D, int KT, int kRows, bool kShare>
+__global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const __grid_constant__ Args a, int mts, int splits) {
+  constexpr int kVec = D / 32;
   __shared__ long long sums[2][kJoinWarps];
-  __shared__ float s_acc[kRowWarps > 1 ? kRowWarps : 1][D];
+  __shared__ float s_acc[kShare ? kJoinWarps : 1][D];
   __shared__ float s_sum[kJoinWarps];
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int item = blockIdx.x / splits, split = blockIdx.x - item * splits;
+  const int hk = item / mts, mt = item - hk * mts;
   long long mine = 0, before_b = 0;   // units of all rows, and of rows before b
   for (int r = tid; r < a.B; r += kJoinThreads) {
     int n, ctx;
@@ -633,95 +851,103 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const Args
   long long dummy;
   const long long total = block_sum(mine, sums[0], dummy);
   before_b = block_sum(before_b, sums[1], dummy);
-  wait_prerequisite();
-  const int r = kRowWarps > 1 ? blockIdx.x : blockIdx.x * kJoinWarps + warp;   // node Hq + head
-  if (r >= a.N * a.Hq) return;
-  const int part0 = kRowWarps > 1 ? warp : 0;
-  const int i = r / a.Hq, h = r % a.Hq;
   int n, ctx;
   row_of(a, b, n, ctx);
-  const size_t orow = (size_t)b * a.N * a.Hq + r;
-  float acc[kVec];
-#pragma unroll
-  for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
-  float lse = -INFINITY;
-  if (i < n) {
-    const int hk = h / a.G, mt = i / a.npt, row = (i - mt * a.npt) * a.G + h % a.G;
-    long long x0 = before_b + hk * units_of<KT>(a, n, ctx);
-    for (int t = 0; t < mt; ++t) x0 += tiles_of<KT>(a, n, ctx, t);
-    const long long x1 = x0 + tiles_of<KT>(a, n, ctx, mt);
-    const int c0 = block_of(total, x0), c1 = block_of(total, x1 - 1);
-    if (c0 == c1) return;   // written whole (the same in every warp of the row)
-    // (blocks between c0 and c1 all hold a unit: the item's units are consecutive, and a block without
-    // units holds none of them, which first_unit(c) == first_unit(c + 1) says)
-    auto share = [&](int c) { return first_unit(total, c) < first_unit(total, c + 1); };
-    // a block's first segment is its part 0: block c0's only where the item starts its share
-    auto part = [&](int c) { return (size_t)(2 * c + (first_unit(total, c) < x0)) * kM + row; };
-    float top = -INFINITY;
-    bool nan = false;
-    for (int c = c0 + lane; c <= c1; c += 32) {
-      const float x = share(c) ? a.part_lse[part(c)] : -INFINITY;
-      nan |= x != x;
-      top = fmaxf(top, x);
-    }
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-    nan = __any_sync(0xffffffffu, nan);
-    const float ref = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-    for (int cc = c0 + part0; cc <= c1; cc += 4 * kRowWarps) {
-      float w[4], x[4][kVec];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int c = cc + u * kRowWarps;
-        const bool there = c <= c1 && share(c);
-        const size_t p = there ? part(c) : part(c0);
-        w[u] = there ? a.part_lse[p] : -INFINITY;
-        const float* po = a.part_o + p * D + lane * kVec;
-#pragma unroll
-        for (int e = 0; e < kVec; e += 2) {
-          const float2 y = *reinterpret_cast<const float2*>(po + e);
-          x[u][e] = y.x;
-          x[u][e + 1] = y.y;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float f = ex2_approx((w[u] - ref) * kLog2e);
-        sum += f;
-        if (f != 0.f) {   // a part that saw nothing may hold anything
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) acc[e] = fmaf(f, x[u][e], acc[e]);
-        }
-      }
-    }
-    if constexpr (kRowWarps > 1) {
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) s_acc[warp][lane * kVec + e] = acc[e];
-      if (lane == 0) s_sum[warp] = sum;
-      __syncthreads();   // (every warp of the block is here: they share the row)
-      if (warp > 0) return;
-      sum = 0.f;
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
-#pragma unroll
-      for (int w = 0; w < kRowWarps; ++w) {
-        sum += s_sum[w];
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) acc[e] += s_acc[w][lane * kVec + e];
-      }
-    }
-    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) acc[e] *= inv;
-    lse = nan ? NAN : sum > 0.f ? ref + logf(sum) : -INFINITY;
-  } else if (kRowWarps > 1 && warp > 0) {
-    return;
+  const int node0 = mt * a.npi, nodes = min(a.npi, a.N - node0);
+  int c0 = 0, c1 = 0;
+  long long x0 = 0;
+  if (node0 < n) {
+    x0 = before_b + hk * units_of<KT>(a, n, ctx);
+    if (a.mask) x0 += (long long)mt * tiles_of<KT>(a, n, ctx, 0);
+    else
+      for (int t = 0; t < mt; ++t) x0 += tiles_of<KT>(a, n, ctx, t);
+    c0 = block_of(total, x0);
+    c1 = block_of(total, x0 + tiles_of<KT>(a, n, ctx, mt) - 1);
   }
-  __nv_bfloat16* out = a.o + orow * D + lane * kVec;
+  wait_prerequisite();
+  const bool cut = c0 != c1;
+  if (!cut && node0 + nodes <= n) return;   // written whole, no absent nodes
+  auto share = [&](int c) { return first_unit(total, c) < first_unit(total, c + 1); };   // the block has units
+  // a block's first segment is its part 0: block c0's only where the item starts its share
+  auto part0 = [&](int c) { return (size_t)(2 * c + (first_unit(total, c) < x0)) * kRows; };
+  for (int rr = kShare ? split : split * kJoinWarps + warp; rr < nodes * a.G; rr += splits * (kShare ? 1 : kJoinWarps)) {
+    const int nl = rr / a.G, hg = rr - nl * a.G, m = nl / a.npt;
+    const int i = node0 + nl, row = m * kM + (nl - m * a.npt) * a.G + hg;
+    const size_t orow = ((size_t)b * a.N + i) * a.Hq + hk * a.G + hg;
+    float acc[kVec];
 #pragma unroll
-  for (int e = 0; e < kVec; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(acc[e], acc[e + 1]);
-  if (lane == 0 && a.lse) a.lse[orow] = lse;
+    for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
+    float lse = -INFINITY;
+    if (i < n) {
+      if (!cut) continue;   // (the same in every warp of the row)
+      float top = -INFINITY;
+      bool nan = false;
+      for (int c = c0 + lane; c <= c1; c += 32) {
+        const float x = share(c) ? a.part_lse[part0(c) + row] : -INFINITY;
+        nan |= x != x;
+        top = fmaxf(top, x);
+      }
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      nan = __any_sync(0xffffffffu, nan);
+      const float ref = top == -INFINITY ? 0.f : top;
+      float sum = 0.f;
+      constexpr int kStep = kShare ? kJoinWarps : 1;
+      for (int cc = c0 + (kShare ? warp : 0); cc <= c1; cc += 4 * kStep) {
+        float w[4], x[4][kVec];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int c = cc + u * kStep;
+          const bool there = c <= c1 && share(c);
+          const size_t p = part0(there ? c : c0) + row;
+          w[u] = there ? a.part_lse[p] : -INFINITY;
+          const float* po = a.part_o + p * D + lane * kVec;
+#pragma unroll
+          for (int e = 0; e < kVec; e += 2) {
+            const float2 y = *reinterpret_cast<const float2*>(po + e);
+            x[u][e] = y.x;
+            x[u][e + 1] = y.y;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float f = ex2_approx((w[u] - ref) * kLog2e);
+          sum += f;
+          if (f != 0.f) {   // a part that saw nothing may hold anything
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) acc[e] = fmaf(f, x[u][e], acc[e]);
+          }
+        }
+      }
+      if constexpr (kShare) {
+        __syncthreads();   // (the row before has been read)
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) s_acc[warp][lane * kVec + e] = acc[e];
+        if (lane == 0) s_sum[warp] = sum;
+        __syncthreads();
+        if (warp > 0) continue;
+        sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
+#pragma unroll
+        for (int v = 0; v < kJoinWarps; ++v) {
+          sum += s_sum[v];
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) acc[e] += s_acc[v][lane * kVec + e];
+        }
+      }
+      const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) acc[e] *= inv;
+      lse = nan ? NAN : sum > 0.f ? ref + logf(sum) : -INFINITY;
+    } else if (kShare && warp > 0) {
+      continue;
+    }
+    __nv_bfloat16* out = a.o + orow * D + lane * kVec;
+#pragma unroll
+    for (int e = 0; e < kVec; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(acc[e], acc[e + 1]);
+    if (lane == 0 && a.lse) a.lse[orow] = lse;
+  }
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -750,13 +976,13 @@ bool make_map(CUtensorMap* m, const void* base, int D, int d1, int d2, int d3, i
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, int kForm>
 cudaError_t launch(const TreeAttnArgs& p, cudaStream_t st) {
-  using C = Cfg<D>;
+  using C = Cfg<D, kForm>;
   Args a{};
   a.G = p.Hq / p.Hk;
-  a.npt = kM / a.G;
-  if (a.npt > p.N) a.npt = p.N;
+  a.npt = std::min(kM / a.G, p.N);
+  a.npi = C::kTiles * a.npt;
   CUtensorMap mq, mk, mv;
   if (!make_map(&mq, p.q, D, p.Hq, p.N, p.B, a.G, a.npt) ||
       !make_map(&mk, p.k_pages, D, p.Hk, p.page, p.P, 1, std::min(p.page, C::KT)) ||
@@ -768,20 +994,23 @@ cudaError_t launch(const TreeAttnArgs& p, cudaStream_t st) {
   a.o = static_cast<__nv_bfloat16*>(p.o);
   a.lse = p.lse;
   a.part_o = reinterpret_cast<float*>(p.ws);
-  a.part_lse = a.part_o + (size_t)2 * kBlocks * kM * D;
+  a.part_lse = a.part_o + (size_t)2 * kBlocks * C::kRows * D;
   a.B = p.B; a.N = p.N; a.Hq = p.Hq; a.Hk = p.Hk; a.W = (p.N + 63) / 64; a.P = p.P; a.page = p.page; a.M = p.M;
+  a.page_shift = __builtin_ctz((unsigned)p.page);
   a.budget = wait_budget_cycles();
   a.err = p.err;
-  cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D, kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   int slot = stage_timer_begin(st, kKernTreeAttn);
-  tree_attn_kernel<D><<<kBlocks, kThreads, C::kSmem, st>>>(mq, mk, mv, a);
+  tree_attn_kernel<D, kForm><<<kBlocks, kThreads, C::kSmem, st>>>(mq, mk, mv, a);
   stage_timer_end(slot, st);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int mts = (p.N + a.npi - 1) / a.npi;
+  const long long items = (long long)p.B * p.Hk * mts;
+  const bool share = items <= 16;   // ten parts a row and more; below, eight warps would find one or two each
+  const int splits = share ? a.npi * a.G : (int)std::max(1ll, std::min(8ll, 1024 / items));
   cudaLaunchConfig_t cfg = {};
-  // (64 items: three parts or fewer each)
-  const bool few = (long long)p.B * p.Hk * ((p.N + a.npt - 1) / a.npt) <= 64;
-  cfg.gridDim = dim3(few ? p.N * p.Hq : (p.N * p.Hq + kJoinWarps - 1) / kJoinWarps, p.B);
+  cfg.gridDim = dim3((unsigned)(p.Hk * mts * splits), p.B);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -790,17 +1019,25 @@ cudaError_t launch(const TreeAttnArgs& p, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   slot = stage_timer_begin(st, kKernTreeAttnJoin);
-  e = few ? cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D, 8>, a) : cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D, 1>, a);
+  e = share ? cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D, C::KT, C::kRows, true>, a, mts, splits)
+            : cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D, C::KT, C::kRows, false>, a, mts, splits);
   stage_timer_end(slot, st);
   return e;
 }
 
+template <int D>
+cudaError_t launch_two(const TreeAttnArgs& a, cudaStream_t s) {
+  // more nodes than one M tile holds: two M tiles share the key/value tiles' way through shared memory
+  return a.N > kM / (a.Hq / a.Hk) ? launch<D, kWide>(a, s) : launch<D, kNarrow>(a, s);
+}
+
 }  // namespace
 
-size_t tree_attn_workspace_bytes(int D) { return (size_t)2 * kBlocks * kM * (D + 1) * sizeof(float); }
+// Two parts a block, each of the largest item's rows: 256, or 128 for D = 256.
+size_t tree_attn_workspace_bytes(int D) { return (size_t)2 * kBlocks * (D == 256 ? kM : 2 * kM) * (D + 1) * sizeof(float); }
 
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t s) {
-  return a.D == 64 ? launch<64>(a, s) : a.D == 128 ? launch<128>(a, s) : launch<256>(a, s);
+  return a.D == 64 ? launch_two<64>(a, s) : a.D == 128 ? launch_two<128>(a, s) : launch<256, kSplit>(a, s);
 }
 
 }  // namespace gdr
