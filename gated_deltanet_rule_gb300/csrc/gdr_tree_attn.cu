@@ -12,7 +12,10 @@
 // buffers), one issues the products (tcgen05: S = Q K^T into TMEM, O += P V with P read from TMEM), two
 // warpgroups do the softmax. Three forms share this frame:
 //   kWide   D <= 128 and more than 128 rows a key head: two M tiles an item, one a warpgroup; both read the
-//           same key/value tiles, the products of one run under the softmax of the other.
+//           same key/value tiles, the products of one run under the softmax of the other. (Tiles of 64
+//           positions with two S buffers a stream, so that S is always there in time, were slower, 119
+//           against 98 us for 8 trees of 64 nodes over 16384 positions: products of N = 64 are bound by
+//           reading Q from shared memory, and every product costs two waits.)
 //   kNarrow D <= 128, up to 128 rows: one M tile, the warpgroups take every other key tile, each with
 //           its own accumulator, maximum and sum, joined at the end of the segment.
 //   kSplit  D = 256: an accumulator takes half of TMEM, so there is one: the warpgroups take half of each
@@ -81,19 +84,19 @@ struct Cfg {
   static constexpr int kTiles = kForm == kWide ? 2 : 1;      // M tiles of an item
   static constexpr int kRows = kTiles * kM;
   static constexpr uint32_t kTile = KT * D * 2;              // bytes of a K or V tile
-  static constexpr int NS = D == 64 ? 8 : D == 128 && kForm == kNarrow ? 6 : 5;   // tile buffers
+  static constexpr int NS = D == 64 ? 8 : kForm == kNarrow ? 6 : 5;   // tile buffers
   static constexpr uint32_t kQTile = kM * D * 2;
   static constexpr uint32_t kRing = kTiles * kQTile;
   static constexpr uint32_t kRed = kRing + NS * kTile;       // float [2][2][128]
   static constexpr uint32_t kBars = kRed + 2048;
   static constexpr uint32_t kSmem = kBars + 512;
-  static constexpr uint32_t kTmemO = 2 * KT;                 // S buffers at columns 0 and KT
+  static constexpr uint32_t kTmemO = 2 * KT;                 // two S buffers at columns 0 and KT: kSplit's tiles alternate, else one a stream
 };
 
 struct Bars {
   uint64_t full[8], empty[8];
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], pv[2];   // by stream (kSplit: by buffer)
+  uint64_t s_full[2], p_full[2], pv[2];   // by S buffer: S formed, P written, P V done
   uint64_t o_free;     // the segment's accumulators have been read
   uint64_t drain;
   uint32_t tmem;
@@ -179,24 +182,21 @@ struct Walk {
   __device__ __forceinline__ int m_tiles(const Args& a) const { return mt * a.npi + a.npt < n ? a.npi / a.npt : 1; }
 };
 
-// mbar_wait by a whole warp, with one answer for all its lanes. A budget of 0 does not wait at all
-// (try_wait may suspend the thread for a while before it answers).
+// Whether the phase with this parity is complete, at once (try_wait may suspend the thread for a while).
+__device__ __forceinline__ bool test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// mbar_wait by a whole warp, with one answer for all its lanes. A budget of 0 does not wait at all.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, long long budget) {
-  bool ok;
-  if (budget == 0) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    ok = done != 0;
-  } else {
-    ok = mbar_wait(bar, parity, budget);
-  }
-  return __all_sync(0xffffffffu, ok);
+  return __all_sync(0xffffffffu, budget == 0 ? test_wait(bar, parity) : mbar_wait(bar, parity, budget));
 }
 // One lane of a converged warp.
 __device__ __forceinline__ bool elected() {
@@ -226,6 +226,20 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
   return r;
 }
+
+// A place in the ring of tile buffers: the buffer, and the parity of its present use.
+template <int NS>
+struct Ring {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void step(int n) {
+    slot += n;
+    if (slot >= NS) {
+      slot -= NS;
+      parity ^= 1;
+    }
+  }
+};
 
 // Sum over the block's threads (all of them call), and this thread's sum of those before it.
 __device__ __forceinline__ long long block_sum(long long v, long long* warps, long long& before) {
@@ -470,6 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tb = s.tmem;
   launch_dependents();
+  __syncwarp();
   // A softmax thread holds a row of S in registers. The block was launched with 384 x 168 registers; the
   // first warpgroup gives back 128 x 88 of them, the other two take 256 x 40.
   bool ok = true;
@@ -482,7 +497,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rows = min(a.page, KT);                       // positions of one box
     const uint32_t box = rows * 128u;                       // its bytes in one 64-column slab
     const int most = KT / rows;                             // boxes of a tile
-    long long it = 0;                                       // tiles loaded
+    Ring<NS> ring;
+    int loads = 0;                                          // tiles loaded, at most NS counted
     int q_loads = 0;
     while (ok && w.next(a)) {
       const int end = w.ctx + w.n;
@@ -493,17 +509,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         return lane < most && pos < end ? __ldg(table + (pos >> a.page_shift)) : -1;
       };
       int pg = page_at(w.t0);
-      if (w.index > 0) ok = warp_wait(&s.q_empty, (w.index - 1) & 1, a.budget);
-      if (!ok) break;
-      if (lane == 0) {
-        const int m_tiles = w.m_tiles(a);
-        mbar_arrive_expect_tx(&s.q_full, (uint32_t)(D / 64) * m_tiles * a.G * a.npt * 128u);
-        for (int m = 0; m < m_tiles; ++m)
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_4d(sm + m * C::kQTile + h * kM * 128, &mq, &s.q_full, h * 64, w.hk * a.G, w.mt * a.npi + m * a.npt, w.b);
-      }
-      __syncwarp();
-      ++q_loads;
       for (int t = w.t0; ok && t < w.t1; ++t) {
         const int pieces = min(most, (end - t * KT + rows - 1) / rows);
         const int at = (t * KT + lane * rows) & (a.page - 1);
@@ -513,9 +518,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           atomicCAS(a.err, 0, kErrDeviceIndex);
           src = -1;
         }
-        for (int kv = 0; kv < 2; ++kv, ++it) {
-          const int slot = (int)(it % NS);
-          if (it >= NS) ok = warp_wait(&s.empty[slot], (uint32_t)(it / NS - 1) & 1, a.budget);
+        for (int kv = 0; kv < 2; ++kv) {
+          const int slot = ring.slot;
+          if (loads == NS) ok = warp_wait(&s.empty[slot], ring.parity ^ 1, a.budget);
+          else ++loads;
           if (!ok) break;
           if (lane == 0) mbar_arrive_expect_tx(&s.full[slot], pieces * box * (D / 64));
           __syncwarp();
@@ -526,12 +532,29 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_4d(dst + h * KT * 128, kv ? &mv : &mk, &s.full[slot], h * 64, w.hk, at, src);
           }
           __syncwarp();
+          ring.step(1);
+        }
+        if (!ok) break;
+        if (t == w.t0) {
+          // the segment's queries, once the last segment's are done with: after the first tile, which
+          // needs only free buffers, is on its way
+          if (w.index > 0) ok = warp_wait(&s.q_empty, (w.index - 1) & 1, a.budget);
+          if (!ok) break;
+          if (lane == 0) {
+            const int m_tiles = w.m_tiles(a);
+            mbar_arrive_expect_tx(&s.q_full, (uint32_t)(D / 64) * m_tiles * a.G * a.npt * 128u);
+            for (int m = 0; m < m_tiles; ++m)
+              for (int h = 0; h < D / 64; ++h)
+                tma_load_4d(sm + m * C::kQTile + h * kM * 128, &mq, &s.q_full, h * 64, w.hk * a.G, w.mt * a.npi + m * a.npt, w.b);
+          }
+          __syncwarp();
+          ++q_loads;
         }
       }
     }
     // no copy of this block is left in flight
-    for (long long i = it > NS ? it - NS : 0; i < it; ++i)
-      warp_wait(&s.full[i % NS], (uint32_t)(i / NS) & 1, kDrainBudget);
+    // (a buffer before the ring's place is in its present round, the others are in the one before)
+    for (int i = 0; i < loads; ++i) warp_wait(&s.full[i], i < ring.slot ? ring.parity : ring.parity ^ 1, kDrainBudget);
     if (q_loads > 0) warp_wait(&s.q_full, (q_loads - 1) & 1, kDrainBudget);
     } else if (warp == 1) {
     // ------------------------------------------------------------------------------ products
@@ -544,11 +567,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t hi = (uint32_t)(smem_desc(0, 16, 1024) >> 32);   // (the strides' high word is the same for all three)
     // S[buffer] = Q[M tile] K[slot]^T; the K buffer and Q are given back by the last products that read them
     auto scores = [&](int buf, int m, int slot, bool free_k, bool free_q) {
-      const uint32_t q0 = __shfl_sync(0xffffffffu, q_lo + m * (C::kQTile >> 4), 0);
-      const uint32_t k0 = __shfl_sync(0xffffffffu, k_lo + slot * (C::kTile >> 4), 0);
-      const uint32_t d = __shfl_sync(0xffffffffu, tb + buf * KT, 0);
+      const uint32_t q0 = q_lo + m * (C::kQTile >> 4), k0 = k_lo + slot * (C::kTile >> 4), d = tb + buf * KT;
       tc_fence_after();
-      if (lead) {
+      if (lead && ok) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           mma_bf16(d, desc64(q0 + (((kk >> 2) * kM * 128 + (kk & 3) * 32) >> 4), hi),
@@ -560,12 +581,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     };
     // O[stream] (+)= P[buffer] V[slot]
-    auto outputs = [&](int buf, uint32_t o_col, int slot, bool more, bool free_v) {
-      const uint32_t v0 = __shfl_sync(0xffffffffu, v_lo + slot * (C::kTile >> 4), 0);
-      const uint32_t p = __shfl_sync(0xffffffffu, tb + buf * KT, 0), d = __shfl_sync(0xffffffffu, tb + o_col, 0);
-      const uint32_t acc = __shfl_sync(0xffffffffu, (uint32_t)more, 0);
+    auto outputs = [&](int buf, int st, int slot, bool more, bool free_v) {
+      const uint32_t v0 = v_lo + slot * (C::kTile >> 4), p = tb + buf * KT, d = tb + C::kTmemO + st * D;
+      const uint32_t acc = more;
       tc_fence_after();
-      if (lead) {
+      if (lead && ok) {
 #pragma unroll
         for (int kk = 0; kk < KT / 16; ++kk)
           mma_f16_tmem_a(d, p + kk * 8, desc64(v0 + ((kk * 2048) >> 4), hi), kIdO, kk > 0 ? 1u : acc);
@@ -574,62 +594,69 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     };
-    auto filled = [&](long long fill) { return warp_wait(&s.full[fill % NS], (uint32_t)(fill / NS) & 1, a.budget); };
-    long long g = 0;                // tiles of the segments before
-    long long steps[2] = {0, 0};    // products of each stream (kSplit: buffer) so far
+    // A wait without a vote: a lane whose wait ran out issues nothing more, and the warp leaves together at
+    // the end of the tile.
+    auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && (a.budget == 0 ? test_wait(bar, parity) : mbar_wait(bar, parity, a.budget)); };
+    Ring<NS> kr, vr;                // the next tile's keys and values
+    vr.step(1);
+    uint32_t steps[2] = {0, 0};     // scores formed for each stream so far (kSplit: in all)
     while (ok && w.next(a)) {
-      ok = warp_wait(&s.q_full, w.index & 1, a.budget);
-      const int T = w.t1 - w.t0;
+      wait(&s.q_full, w.index & 1);
+      // (the same in every lane: broadcast, so that loop counts, addresses and descriptors stay in uniform registers)
+      const int T = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0);
+      const bool first = __shfl_sync(0xffffffffu, w.index, 0) == 0;
+      const uint32_t o_parity = __shfl_sync(0xffffffffu, (uint32_t)(w.index - 1) & 1, 0);
+      const int streams = kForm == kWide ? __shfl_sync(0xffffffffu, w.m_tiles(a), 0) : kForm == kNarrow ? 2 : 1;
       if constexpr (kForm == kSplit) {
-        for (int j = -1; ok && j < T; ++j) {
-          if (j + 1 < T) {          // S of tile j + 1: its buffer is free once P V of tile j - 1 is done
-            const long long x = g + j + 1;
-            if (x >= 2) ok = warp_wait(&s.pv[x & 1], (uint32_t)((x - 2) >> 1) & 1, a.budget);
-            ok = ok && filled(2 * x);
-            if (!ok) break;
-            scores((int)(x & 1), 0, (int)((2 * x) % NS), true, j + 2 == T);
+        // S of tile j + 1, then P V of tile j
+        for (int j = -1; j < T; ++j) {
+          if (j + 1 < T) {
+            const uint32_t x = steps[0]++;
+            wait(&s.full[kr.slot], kr.parity);
+            if (x >= 2) wait(&s.pv[x & 1], ((x - 2) >> 1) & 1);   // (P V of tile j - 1 is done)
+            scores(x & 1, 0, kr.slot, true, j + 2 == T);
+            kr.step(2);
           }
           if (j >= 0) {
-            const long long x = g + j;
-            if (j == 0 && w.index > 0) ok = warp_wait(&s.o_free, (w.index - 1) & 1, a.budget);
-            ok = ok && warp_wait(&s.p_full[x & 1], (uint32_t)(x >> 1) & 1, a.budget);
-            ok = ok && filled(2 * x + 1);
-            if (!ok) break;
-            outputs((int)(x & 1), C::kTmemO, (int)((2 * x + 1) % NS), j > 0, true);
+            const uint32_t x = steps[0] - (j + 1 < T ? 2 : 1);      // tile j
+            if (j == 0 && !first) wait(&s.o_free, o_parity);
+            wait(&s.full[vr.slot], vr.parity);
+            wait(&s.p_full[x & 1], (x >> 1) & 1);
+            outputs(x & 1, 0, vr.slot, j > 0, true);
+            vr.step(2);
           }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
         }
       } else {
-        const int streams = kForm == kWide ? w.m_tiles(a) : 2;
-        // stream st takes tile j = k (kWide) or 2 k + st (kNarrow) at its step k
-        auto tile = [&](int st, int k) { return kForm == kWide ? k : 2 * k + st; };
-        const int last = kForm == kWide ? T : (T + 1) / 2;
-        for (int k = 0; ok && k <= last; ++k) {
+        // one buffer a stream: S of a stream's next tile goes over P of its last one, once that product is
+        // done; the streams take turns (kNarrow: tiles st, st + 2, ...; kWide: every tile)
+        constexpr int kStep = kForm == kNarrow ? 2 : 1;
+        for (int k = 0; k <= (T + kStep - 1) / kStep; ++k) {
 #pragma unroll
           for (int st = 0; st < 2; ++st) {
-            if (!ok || st >= streams) break;
-            if (k > 0 && tile(st, k - 1) < T) {
-              const int j = tile(st, k - 1);
-              const long long fill = 2 * (g + j) + 1;
-              if (k == 1 && w.index > 0 && st == 0) ok = warp_wait(&s.o_free, (w.index - 1) & 1, a.budget);
-              ok = ok && warp_wait(&s.p_full[st], (uint32_t)(steps[st] - 1) & 1, a.budget);
-              ok = ok && filled(fill);
-              if (!ok) break;
-              outputs(st, C::kTmemO + st * D, (int)(fill % NS), k > 1, kForm == kNarrow || st == streams - 1);
+            if (st >= streams) break;
+            const int j = kForm == kNarrow ? 2 * k + st : k;
+            const bool last = kForm == kNarrow || st == streams - 1;
+            if (k > 0 && j - kStep < T) {
+              if (k == 1 && st == 0 && !first) wait(&s.o_free, o_parity);
+              if (kForm == kNarrow || st == 0) wait(&s.full[vr.slot], vr.parity);   // (kWide: one tile for both)
+              wait(&s.p_full[st], (steps[st] - 1) & 1);
+              outputs(st, st, vr.slot, k > 1, last);
+              if (last) vr.step(2);
             }
-            if (tile(st, k) < T) {   // S of the next tile, over P of the last one
-              const int j = tile(st, k);
-              const long long fill = 2 * (g + j);
-              if (steps[st] > 0) ok = warp_wait(&s.pv[st], (uint32_t)(steps[st] - 1) & 1, a.budget);
-              ok = ok && filled(fill);
-              if (!ok) break;
-              const bool end_k = kForm == kNarrow || st == streams - 1;
-              scores(st, kForm == kWide ? st : 0, (int)(fill % NS), end_k, j == T - 1 && end_k);
+            if (j < T) {
+              if (kForm == kNarrow || st == 0) wait(&s.full[kr.slot], kr.parity);
+              if (steps[st] > 0) wait(&s.pv[st], (steps[st] - 1) & 1);
+              scores(st, kForm == kWide ? st : 0, kr.slot, last, j == T - 1 && last);
               ++steps[st];
+              if (last) kr.step(2);
             }
           }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
         }
       }
-      g += T;
     }
     // no product of this block is left in flight
     if (lead) mma_commit(&s.drain);
@@ -645,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int st = (warp - 4) >> 2, quarter = warp & 3, row = 32 * quarter + lane;   // st: stream, or half of the columns
     const uint32_t rows_at = tb + ((uint32_t)(32 * quarter) << 16);
     const int wtid = tid - 128;
-    long long g = 0, step = 0;
+    long long g = 0, step = 0;   // tiles of the segments before, tiles of this stream so far
     while (w.next(a)) {
       const int m = kForm == kWide ? st : 0;                     // M tile of the item
       const int node0 = w.mt * a.npi + m * a.npt;
@@ -662,11 +689,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = kForm == kNarrow ? st : 0; works && j < T; j += kStep, ++step) {
         const int t = w.t0 + j;
         const bool masked = (t + 1) * KT > w.ctx;
-        const int buf = kForm == kSplit ? (int)((g + j) & 1) : st;
-        const uint32_t phase = kForm == kSplit ? (uint32_t)((g + j) >> 1) & 1 : (uint32_t)step & 1;
-        // (kWide: the first M tile's product with V is issued first, so its warps clean for both)
-        if (masked && (kForm != kWide || st == 0)) {
-          const long long fill = 2 * (g + j) + 1;
+        // this tile's buffer and how often it was used before
+        const long long use = kForm == kSplit ? g + j : step;
+        const int buf = kForm == kSplit ? (int)(use & 1) : st;
+        const uint32_t phase = kForm == kSplit ? (uint32_t)(use >> 1) & 1 : (uint32_t)use & 1;
+        // V of a masked tile (kWide: the first M tile's product with V is issued first, so its warps clean for
+        // both). A parity tells a phase from the next one alone: in the ring's first round V may be asked for
+        // at once, later only when S is there, whose product comes after the one with the buffer's last V.
+        const long long fill = 2 * (g + j) + 1;
+        auto clean = [&] {
           ok = ok && warp_wait(&s.full[fill % NS], (uint32_t)(fill / NS) & 1, a.budget);
           if (ok) {
             uint8_t* vt = sm + C::kRing + (fill % NS) * C::kTile;
@@ -674,8 +705,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               s.bad[w.index % 3] = 1;
             fence_async_smem();
           }
-        }
+          __syncwarp();   // the lanes' shares differ, and what follows on TMEM wants the whole warp
+        };
+        const bool cleans = masked && (kForm != kWide || st == 0);
+        if (cleans && fill < NS) clean();
         ok = ok && warp_wait(&s.s_full[buf], phase, a.budget);
+        if (cleans && fill >= NS) clean();
         const uint32_t sb = rows_at + buf * KT;
         if (active) {
           // this thread's columns of its row: all, or a half
@@ -687,8 +722,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (kCols == 32) {
               tmem_ld32(sb + col0, x);
             } else {
-              tmem_ld64(sb, x);
-              tmem_ld64(sb + 64, x + 64);
+#pragma unroll
+              for (int c = 0; c < kCols; c += 64) tmem_ld64(sb + c, x + c);
             }
           }
           if (masked && live) {
@@ -696,11 +731,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (kCols == 32) {
               hide<32>(x, seen(a, words, i, w.n, rel));
             } else {
-              hide<64>(x, seen(a, words, i, w.n, rel));
-              hide<64>(x + 64, seen(a, words, i, w.n, rel + 64));
+#pragma unroll
+              for (int c = 0; c < kCols; c += 64) hide<64>(x + c, seen(a, words, i, w.n, rel + c));
             }
           }
           float mx = largest<kCols>(x);
+          __syncwarp();   // (rows differ in what they hide)
           if constexpr (kForm == kSplit) {
             float* mine = red + ((g + j) & 1) * 256;
             mine[st * 128 + row] = mx;
@@ -716,8 +752,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (j >= kStep) {
               const float f = m_ref == m_new ? 1.f : ex2_approx((m_ref - m_new) * a.sl2);
               l *= f;
-              if (kForm == kSplit) ok = ok && warp_wait(&s.pv[buf ^ 1], (uint32_t)((g + j - 1) >> 1) & 1, a.budget);
-              else ok = ok && warp_wait(&s.pv[st], (uint32_t)(step - 1) & 1, a.budget);
+              if (kForm != kSplit) ok = ok && warp_wait(&s.pv[st], (uint32_t)(use - 1) & 1, a.budget);
+              else ok = ok && warp_wait(&s.pv[buf ^ 1], (uint32_t)((use - 1) >> 1) & 1, a.budget);
               if (ok) {
                 tc_fence_after();
                 if (kForm == kSplit) rescale<D / 2>(rows_at + C::kTmemO + st * (D / 2), f);
@@ -733,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok) tmem_st16_nowait(sb + st * 16, p);
           } else {
 #pragma unroll
-            for (int c = 0; c < 128; c += 32) {
+            for (int c = 0; c < kCols; c += 32) {
               uint32_t p[16];
               l += weights<32>(x + c, a.sl2, off, p);
               if (ok) tmem_st16_nowait(sb + c / 2, p);
@@ -754,6 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float2* both_ml = reinterpret_cast<float2*>(red);
       if constexpr (kForm == kSplit) ml[st * 128 + row] = l;
       if constexpr (kForm == kNarrow) both_ml[st * 128 + row] = make_float2(m_ref, l);
+      __syncwarp();
       ok = named_bar_and(kSoftmaxBar, 256, ok);
       const bool bad = masked_any && s.bad[w.index % 3];
       if (wtid == 0) s.bad[(w.index + 2) % 3] = 0;   // read before this barrier, set after the next
@@ -767,6 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l = l * self + two.y * other;
         m_ref = top;
       }
+      __syncwarp();
       if constexpr (kForm != kWide) ok = named_bar_and(kSoftmaxBar, 256, ok);   // `red` may be written again
       const bool sees = l > 0.f || l != l;
       const float inv = sees ? 1.f / l : 0.f;
@@ -795,6 +833,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (live) put32(o, whole, a.o + orow * D + d0 + c, a.part_o + prow * D + d0 + c);
+          __syncwarp();   // (before the next load of the whole warp)
         }
         tc_fence_before();
       }
@@ -837,6 +876,7 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const __gr
   __shared__ long long sums[2][kJoinWarps];
   __shared__ float s_acc[kShare ? kJoinWarps : 1][D];
   __shared__ float s_sum[kJoinWarps];
+  __shared__ int s_part[kBlocks];
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int item = blockIdx.x / splits, split = blockIdx.x - item * splits;
   const int hk = item / mts, mt = item - hk * mts;
@@ -867,9 +907,14 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const __gr
   wait_prerequisite();
   const bool cut = c0 != c1;
   if (!cut && node0 + nodes <= n) return;   // written whole, no absent nodes
-  auto share = [&](int c) { return first_unit(total, c) < first_unit(total, c + 1); };   // the block has units
-  // a block's first segment is its part 0: block c0's only where the item starts its share
-  auto part0 = [&](int c) { return (size_t)(2 * c + (first_unit(total, c) < x0)) * kRows; };
+  // the places of the item's parts, block by block (-1: a block without units). A block's first segment is
+  // its part 0: block c0's only where the item starts its share
+  const int parts = c1 - c0 + 1;
+  if (cut && tid < parts)
+    s_part[tid] = first_unit(total, c0 + tid) < first_unit(total, c0 + tid + 1)
+                      ? (2 * (c0 + tid) + (first_unit(total, c0 + tid) < x0)) * kRows
+                      : -1;
+  __syncthreads();
   for (int rr = kShare ? split : split * kJoinWarps + warp; rr < nodes * a.G; rr += splits * (kShare ? 1 : kJoinWarps)) {
     const int nl = rr / a.G, hg = rr - nl * a.G, m = nl / a.npt;
     const int i = node0 + nl, row = m * kM + (nl - m * a.npt) * a.G + hg;
@@ -882,8 +927,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const __gr
       if (!cut) continue;   // (the same in every warp of the row)
       float top = -INFINITY;
       bool nan = false;
-      for (int c = c0 + lane; c <= c1; c += 32) {
-        const float x = share(c) ? a.part_lse[part0(c) + row] : -INFINITY;
+      for (int c = lane; c < parts; c += 32) {
+        const float x = s_part[c] >= 0 ? a.part_lse[s_part[c] + row] : -INFINITY;
         nan |= x != x;
         top = fmaxf(top, x);
       }
@@ -893,13 +938,14 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const __gr
       const float ref = top == -INFINITY ? 0.f : top;
       float sum = 0.f;
       constexpr int kStep = kShare ? kJoinWarps : 1;
-      for (int cc = c0 + (kShare ? warp : 0); cc <= c1; cc += 4 * kStep) {
+      for (int cc = kShare ? warp : 0; cc < parts; cc += 4 * kStep) {
         float w[4], x[4][kVec];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int c = cc + u * kStep;
-          const bool there = c <= c1 && share(c);
-          const size_t p = part0(there ? c : c0) + row;
+          const int at = c < parts ? s_part[c] : -1;
+          const bool there = at >= 0;
+          const size_t p = (there ? at : s_part[0]) + row;   // (block c0 holds the item's first unit)
           w[u] = there ? a.part_lse[p] : -INFINITY;
           const float* po = a.part_o + p * D + lane * kVec;
 #pragma unroll

@@ -1,5 +1,8 @@
 """Python binding of libgdr (the C ABI in include/gdr.h): argument marshalling only.
 
+The attention-layer operators go through a compiled binding (_gdr_bind, csrc/gdr_bind.cpp), the other
+calls through ctypes.
+
 Each function checks tensor devices, dtypes, shapes and contiguity, allocates outputs the
 caller did not pass (torch.empty: memory plumbing, no arithmetic), hands raw device pointers
 and the current CUDA stream to the library and raises ``GdrError`` on a non-OK status. Every
@@ -472,64 +475,28 @@ def gdr_backward_chunked(q, k, v, g, beta, S0, dO, dS_T=None, ws=None, stream=No
 # --------------------------------------------------------------------------------------------------
 # softmax-attention layers: drafted tokens over a cache of pages
 #
-# Single-token calls take a few microseconds of GPU time, so these bindings check with one plain
-# condition each and build a message only to raise it.
+# A decoding step makes these calls once a layer, on kernels of a few microseconds: their checks and
+# marshalling are compiled (csrc/gdr_bind.cpp) and raise ValueError for a tensor of the wrong device,
+# dtype, shape or layout, GdrError for what the library refuses.
 # --------------------------------------------------------------------------------------------------
-def _is(t, dtype, shape=None) -> bool:
-    """A contiguous CUDA tensor of this dtype (and shape)."""
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.is_contiguous()
-            and (shape is None or t.shape == shape))
+_bind_mod = None
 
 
-def _heads(name, t, like):
-    """Strides (token, head) of [B, N, H, D], which may be a slice of a wider projection."""
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 4):
-        raise ValueError(f"{name} must be a CUDA tensor [B, N, H, D]")
-    B, N, H, Dk = t.shape
-    sb, sn, sh, sd = t.stride()
-    if t is not like and not (t.dtype is like.dtype and (B, N) == like.shape[:2] and Dk == like.shape[3]):
-        raise ValueError(f"{name} must share q's dtype, rows, tokens and head dimension")
-    if sd != 1 and Dk > 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    tok = sn if N > 1 else (sb if B > 1 else H * Dk)
-    if B > 1 and N > 1 and sb != N * tok:
-        raise ValueError(f"{name}: tokens of all rows must lie at one stride")
-    return tok, (sh if H > 1 else Dk)
+def _bind():
+    global _bind_mod
+    if _bind_mod is None:
+        lib()
+        try:
+            from . import _gdr_bind
+        except ImportError as e:
+            raise RuntimeError("the compiled binding _gdr_bind is missing: build it with __graft_entry__.build() "
+                               f"or python -m gated_deltanet_rule_gb300.build ({e})") from e
+        _bind_mod = _gdr_bind
+    return _bind_mod
 
 
-def _rope_common(q, k, q_w, k_w, inv_freq, pos):
-    q_tok, q_head = _heads("q", q, q)
-    k_tok, k_head = _heads("k", k, q)
-    B, N, Hq, Dk = q.shape
-    if not (_is(q_w, torch.float32, (Dk,)) and _is(k_w, torch.float32, (Dk,))):
-        raise ValueError("q_w and k_w must be contiguous CUDA float32 [D]")
-    if not (_is(inv_freq, torch.float64) and inv_freq.dim() == 1):
-        raise ValueError("inv_freq must be contiguous CUDA float64 [R / 2]")
-    if not _is(pos, torch.int32, (B, N)):
-        raise ValueError("pos must be contiguous CUDA int32 [B, N]")
-    return B, N, Hq, k.shape[2], Dk, 2 * inv_freq.shape[0], q_tok, q_head, k_tok, k_head, _dtype_code(q)
-
-
-def _pages(k_pages, v_pages, table, ctx, B, Dk, dtype):
-    """(P, page, Hk, M)"""
-    if not (_is(k_pages, dtype) and k_pages.dim() == 4 and _is(v_pages, dtype, k_pages.shape) and k_pages.shape[3] == Dk):
-        raise ValueError("k_pages and v_pages must be contiguous CUDA tensors [P, page, Hk, D] of q's dtype and head dimension")
-    if not (_is(table, torch.int32) and table.dim() == 2 and table.shape[0] == B and _is(ctx, torch.int32, (B,))):
-        raise ValueError("table must be contiguous CUDA int32 [B, M] and ctx [B]")
-    return *k_pages.shape[:3], table.shape[1]
-
-
-def _out(name, t, shape, dtype, device):
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not _is(t, dtype, shape):
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of shape {tuple(shape)} and dtype {dtype}")
-    return t
-
-
-def _lengths(lengths, B):
-    if lengths is not None and not _is(lengths, torch.int32, (B,)):
-        raise ValueError("lengths must be contiguous CUDA int32 [B]")
+def _raw(stream):
+    return None if stream is None else stream.cuda_stream
 
 
 def gdr_qk_norm_rope(q, k, q_w, k_w, inv_freq, pos, eps: float = 1e-6, interleaved: bool = False, q_out=None,
@@ -537,52 +504,22 @@ def gdr_qk_norm_rope(q, k, q_w, k_w, inv_freq, pos, eps: float = 1e-6, interleav
     """RMS norm of every head of q [B,N,Hq,D] and k [B,N,Hk,D] (views of one projection are read in
     place) and the rotation of its first R = 2 len(inv_freq) elements by pos [B,N] int32 times inv_freq
     (float64). Returns (q_out, k_out), contiguous, in q's dtype."""
-    B, N, Hq, Hk, Dk, R, q_tok, q_head, k_tok, k_head, dt = _rope_common(q, k, q_w, k_w, inv_freq, pos)
-    q_out = _out("q_out", q_out, q.shape, q.dtype, q.device)
-    k_out = _out("k_out", k_out, k.shape, q.dtype, q.device)
-    _check(lib().gdr_qk_norm_rope(q.data_ptr(), k.data_ptr(), q_w.data_ptr(), k_w.data_ptr(), inv_freq.data_ptr(),
-                                  pos.data_ptr(), eps, interleaved, q_out.data_ptr(), k_out.data_ptr(), B, N, Hq, Hk, Dk,
-                                  R, q_tok, q_head, k_tok, k_head, dt, _stream(stream)))
-    return q_out, k_out
+    return _bind().norm_rope(q, k, q_w, k_w, inv_freq, pos, eps, interleaved, q_out, k_out, _raw(stream))
 
 
 def gdr_qk_norm_rope_append(q, k, v, q_w, k_w, inv_freq, pos, k_pages, v_pages, table, ctx, lengths=None,
                             eps: float = 1e-6, interleaved: bool = False, q_out=None, stream=None):
     """gdr_qk_norm_rope that leaves the keys, and v as it is, in the pages of table [B,M] at positions
     ctx[b] + i (i < lengths[b] where given). Returns q_out."""
-    B, N, Hq, Hk, Dk, R, q_tok, q_head, k_tok, k_head, dt = _rope_common(q, k, q_w, k_w, inv_freq, pos)
-    v_tok, v_head = _heads("v", v, q)
-    P, page, H, M = _pages(k_pages, v_pages, table, ctx, B, Dk, q.dtype)
-    if v.shape[2] != Hk or H != Hk:
-        raise ValueError("v and the pages must have k's heads")
-    _lengths(lengths, B)
-    q_out = _out("q_out", q_out, q.shape, q.dtype, q.device)
-    _check(lib().gdr_qk_norm_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_w.data_ptr(), k_w.data_ptr(),
-                                         inv_freq.data_ptr(), pos.data_ptr(), eps, interleaved, q_out.data_ptr(),
-                                         k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), ctx.data_ptr(),
-                                         _p(lengths), P, page, M, B, N, Hq, Hk, Dk, R, q_tok, q_head, k_tok, k_head,
-                                         v_tok, v_head, dt, _stream(stream)))
-    return q_out
+    return _bind().norm_rope_append(q, k, q_w, k_w, inv_freq, pos, v, k_pages, v_pages, table, ctx, lengths, eps,
+                                    interleaved, q_out, _raw(stream))
 
 
 def gdr_qk_norm_rope_backward(q, k, q_w, k_w, inv_freq, pos, dq_out, dk_out, eps: float = 1e-6,
                               interleaved: bool = False, ws=None, stream=None):
     """Gradients of gdr_qk_norm_rope from dq_out, dk_out (contiguous, q's dtype): (dq, dk, dq_w, dk_w),
     all float32."""
-    B, N, Hq, Hk, Dk, R, q_tok, q_head, k_tok, k_head, dt = _rope_common(q, k, q_w, k_w, inv_freq, pos)
-    if not (_is(dq_out, q.dtype, q.shape) and _is(dk_out, q.dtype, k.shape)):
-        raise ValueError("dq_out and dk_out must be contiguous CUDA tensors like q and k")
-    dev = q.device
-    dq, dk = (torch.empty(t.shape, dtype=torch.float32, device=dev) for t in (q, k))
-    dq_w, dk_w = (torch.empty(Dk, dtype=torch.float32, device=dev) for _ in "qk")
-    if ws is None:
-        ws = torch.empty(max(int(lib().gdr_qk_norm_rope_backward_workspace_bytes(Dk)), 16), dtype=torch.uint8, device=dev)
-    _check(lib().gdr_qk_norm_rope_backward(q.data_ptr(), k.data_ptr(), q_w.data_ptr(), k_w.data_ptr(),
-                                           inv_freq.data_ptr(), pos.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), eps,
-                                           interleaved, dq.data_ptr(), dk.data_ptr(), dq_w.data_ptr(), dk_w.data_ptr(),
-                                           B, N, Hq, Hk, Dk, R, q_tok, q_head, k_tok, k_head, dt, ws.data_ptr(),
-                                           ws.numel() * ws.element_size(), _stream(stream)))
-    return dq, dk, dq_w, dk_w
+    return _bind().norm_rope_backward(q, k, q_w, k_w, inv_freq, pos, dq_out, dk_out, eps, interleaved, ws, _raw(stream))
 
 
 def tree_attn_workspace_bytes(D: int = D) -> int:
@@ -595,24 +532,7 @@ def gdr_tree_attn(q, k_pages, v_pages, table, ctx, lengths=None, mask=None, scal
     mask [B,N,ceil(N/64)] int64 (bit j: node i sees node j; None: nodes 0 .. i) lets them see, the pages
     already holding the nodes' keys and values. scale defaults to D^-1/2. Returns o, or (o, lse [B,N,Hq]
     float32) with want_lse or lse given."""
-    if not (_is(q, torch.bfloat16) and q.dim() == 4):
-        raise ValueError("q must be a contiguous CUDA bfloat16 tensor [B, N, Hq, D]")
-    B, N, Hq, Dk = q.shape
-    P, page, Hk, M = _pages(k_pages, v_pages, table, ctx, B, Dk, torch.bfloat16)
-    _lengths(lengths, B)
-    if mask is not None and not _is(mask, torch.int64, (B, N, (N + 63) // 64)):
-        raise ValueError("mask must be contiguous CUDA int64 [B, N, ceil(N / 64)]")
-    dev = q.device
-    o = _out("o", o, q.shape, torch.bfloat16, dev)
-    if lse is not None or want_lse:
-        lse = _out("lse", lse, (B, N, Hq), torch.float32, dev)
-    if ws is None:
-        ws = torch.empty(max(tree_attn_workspace_bytes(Dk), 16), dtype=torch.uint8, device=dev)
-    _check(lib().gdr_tree_attn(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), table.data_ptr(), ctx.data_ptr(),
-                               _p(lengths), _p(mask), Dk ** -0.5 if scale is None else scale, o.data_ptr(), _p(lse), B, N,
-                               Hq, Hk, Dk, P, page, M, GDR_BF16, ws.data_ptr(), ws.numel() * ws.element_size(),
-                               _stream(stream)))
-    return o if lse is None else (o, lse)
+    return _bind().tree_attn(q, k_pages, v_pages, table, ctx, lengths, mask, scale, o, lse, want_lse, ws, _raw(stream))
 
 
 def gdr_verify_draft(tokens, parents, lengths, p, q, u, u_next, path=None, n_path=None, next_token=None, stream=None):
@@ -620,97 +540,32 @@ def gdr_verify_draft(tokens, parents, lengths, p, q, u, u_next, path=None, n_pat
     target's probabilities p [B,N,V] and the drafts' q [B,N,V] (None: given drafts) with the uniform
     numbers u [B,N], u_next [B]. Returns (path [B,N] of accepted nodes, root first, -1 after them;
     n_path [B]; next_token [B])."""
-    if not (isinstance(p, torch.Tensor) and p.dim() == 3 and _is(p, p.dtype)):
-        raise ValueError("p must be a contiguous CUDA tensor [B, N, V]")
-    dt = _dtype_code(p)
-    B, N, V = p.shape
-    if q is not None and not _is(q, p.dtype, p.shape):
-        raise ValueError("q must be None or like p")
-    if not (_is(tokens, torch.int32, (B, N)) and _is(parents, torch.int32, (B, N)) and _is(lengths, torch.int32, (B,))):
-        raise ValueError("tokens and parents must be contiguous CUDA int32 [B, N] and lengths [B]")
-    if not (_is(u, torch.float32, (B, N)) and _is(u_next, torch.float32, (B,))):
-        raise ValueError("u must be contiguous CUDA float32 [B, N] and u_next [B]")
-    dev = p.device
-    path = _out("path", path, (B, N), torch.int32, dev)
-    n_path = _out("n_path", n_path, (B,), torch.int32, dev)
-    next_token = _out("next_token", next_token, (B,), torch.int32, dev)
-    _check(lib().gdr_verify_draft(tokens.data_ptr(), parents.data_ptr(), lengths.data_ptr(), p.data_ptr(), _p(q),
-                                  u.data_ptr(), u_next.data_ptr(), path.data_ptr(), n_path.data_ptr(),
-                                  next_token.data_ptr(), B, N, V, dt, _stream(stream)))
-    return path, n_path, next_token
-
-
-def _cache(k_cache, v_cache):
-    """(layers, P, page, row bytes) of caches [layers, P, page, Hk, D]."""
-    if not (isinstance(k_cache, torch.Tensor) and k_cache.dim() == 5 and _is(k_cache, k_cache.dtype)
-            and _is(v_cache, k_cache.dtype, k_cache.shape)):
-        raise ValueError("k_cache and v_cache must be contiguous CUDA tensors [layers, P, page, Hk, D] of one dtype")
-    layers, P, page, Hk, Dk = k_cache.shape
-    return layers, P, page, Hk * Dk * k_cache.element_size()
-
-
-def _row_list(table, ctx, refs, rows, more=None):
-    """(F, rows, M)"""
-    if not (_is(table, torch.int32) and table.dim() == 2 and _is(ctx, torch.int32, table.shape[:1])
-            and _is(refs, torch.int32) and refs.dim() == 1):
-        raise ValueError("table must be contiguous CUDA int32 [rows, M], ctx [rows] and refs [P]")
-    if not (_is(rows, torch.int32) and rows.dim() == 1 and (more is None or _is(more, torch.int32, rows.shape))):
-        raise ValueError("row lists must be contiguous CUDA int32 [F]")
-    return rows.shape[0], *table.shape
+    return _bind().verify(tokens, parents, lengths, p, q, u, u_next, path, n_path, next_token, _raw(stream))
 
 
 def cache_workspace_bytes(F: int, M: int) -> int:
     return int(lib().gdr_cache_workspace_bytes(F, M))
 
 
-def _cache_ws(ws, F, M, device):
-    if ws is None:
-        ws = torch.empty(max(cache_workspace_bytes(F, M), 16), dtype=torch.uint8, device=device)
-    return ws, ws.numel() * ws.element_size()
-
-
 def gdr_cache_reserve(table, ctx, refs, rows, extra: int, page: int, ws=None, stream=None) -> None:
     """Gives rows (int32 [F]) pages so that ctx + extra positions of each fit; table, refs in place."""
-    F, R, M = _row_list(table, ctx, refs, rows)
-    ws, ws_bytes = _cache_ws(ws, F, M, table.device)
-    _check(lib().gdr_cache_reserve(table.data_ptr(), ctx.data_ptr(), refs.data_ptr(), rows.data_ptr(), extra, F, R, M,
-                                   refs.shape[0], page, ws.data_ptr(), ws_bytes, _stream(stream)))
+    _bind().cache_reserve(table, ctx, refs, rows, extra, page, ws, _raw(stream))
 
 
 def gdr_cache_fork(k_cache, v_cache, table, ctx, refs, src, dst, ws=None, stream=None) -> None:
     """Row dst[f] becomes a copy of row src[f]: full pages shared, the last one copied. In place."""
-    layers, P, page, row_bytes = _cache(k_cache, v_cache)
-    F, R, M = _row_list(table, ctx, refs, dst, src)
-    if refs.shape[0] != P:
-        raise ValueError("refs must be [P]")
-    ws, ws_bytes = _cache_ws(ws, F, M, table.device)
-    _check(lib().gdr_cache_fork(k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), ctx.data_ptr(), refs.data_ptr(),
-                                src.data_ptr(), dst.data_ptr(), F, R, M, layers, P, page, row_bytes, ws.data_ptr(),
-                                ws_bytes, _stream(stream)))
+    _bind().cache_fork(k_cache, v_cache, table, ctx, refs, src, dst, ws, _raw(stream))
 
 
 def gdr_cache_free(table, ctx, refs, rows, stream=None) -> None:
     """Gives the pages of rows (int32 [F]) back; table, ctx, refs in place."""
-    F, R, M = _row_list(table, ctx, refs, rows)
-    _check(lib().gdr_cache_free(table.data_ptr(), ctx.data_ptr(), refs.data_ptr(), rows.data_ptr(), F, R, M,
-                                refs.shape[0], _stream(stream)))
+    _bind().cache_free(table, ctx, refs, rows, _raw(stream))
 
 
 def gdr_cache_compact(k_cache, v_cache, table, ctx, path, n_path, new_ctx=None, stream=None):
     """Moves the entries of the accepted paths (gdr_verify_draft's path, n_path) to the front of their
     rows in every layer; returns new_ctx = ctx + n_path (which may not be ctx itself)."""
-    layers, P, page, row_bytes = _cache(k_cache, v_cache)
-    if not (_is(path, torch.int32) and path.dim() == 2):
-        raise ValueError("path must be contiguous CUDA int32 [B, W]")
-    B, W = path.shape
-    if not (_is(table, torch.int32) and table.dim() == 2 and table.shape[0] == B and _is(ctx, torch.int32, (B,))
-            and _is(n_path, torch.int32, (B,))):
-        raise ValueError("table must be contiguous CUDA int32 [B, M], ctx and n_path [B]")
-    new_ctx = _out("new_ctx", new_ctx, (B,), torch.int32, ctx.device)
-    _check(lib().gdr_cache_compact(k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), ctx.data_ptr(),
-                                   path.data_ptr(), n_path.data_ptr(), new_ctx.data_ptr(), B, W, table.shape[1], layers, P,
-                                   page, row_bytes, _stream(stream)))
-    return new_ctx
+    return _bind().cache_compact(k_cache, v_cache, table, ctx, path, n_path, new_ctx, _raw(stream))
 
 
 def gdr_sync_status(stream=None) -> None:
