@@ -247,7 +247,7 @@ gdr_status gdr_tree_attn(const void* q, const void* k_pages, const void* v_pages
   if (st == GDR_OK) st = check_pages(P, page, M, who);
   if (st != GDR_OK) return st;
   if (Hq / Hk > 128) return fail(GDR_ERR_UNSUPPORTED, "%s: Hq/Hk=%d exceeds 128 heads a group", who, Hq / Hk);
-  if (B > 65535 || (long long)N * Hq > 1 << 28) return fail(GDR_ERR_UNSUPPORTED, "%s: B=%d or N*Hq too large", who, B);
+  if (B > 65535 || (long long)N * Hq > 1 << 28 || (long long)B * N * Hk > 0x7fffffffll) return fail(GDR_ERR_UNSUPPORTED, "%s: B=%d or N*Hq too large", who, B);
   if (!(scale > 0.f) || scale > 1e30f) return fail(GDR_ERR_INVALID_ARG, "%s: scale must be positive and finite", who);
   for (const void* p : {q, k_pages, v_pages, (const void*)o})
     if (!aligned(p, 16)) return fail(GDR_ERR_INVALID_ARG, "%s: q, k_pages, v_pages and o must be 16-byte aligned", who);

@@ -61,6 +61,14 @@ constexpr long long kDrainBudget = 2000000000ll;   // cycles an aborting block w
 
 enum Form { kSplit = 0, kNarrow = 1, kWide = 2 };
 
+// Where an item's parts are: blocks first .. last (last < first: the item is whole), and the number of
+// units in all, from which each block's share follows.
+struct Cut {
+  long long total;
+  long long unit;   // the item's first unit
+  int item, first, last, pad;
+};
+
 struct Args {
   const int32_t* table;
   const int32_t* ctx;
@@ -72,6 +80,9 @@ struct Args {
   float* lse;
   float* part_o;             // [2 C][rows of an item][D]
   float* part_lse;           // [2 C][rows of an item]
+  Cut* cuts;                 // [C]: by item where there are at most C, else by the block that begins it
+  int items;                 // B Hk mts
+  int mts;                   // items of a row and key head, N nodes' worth
   int B, N, Hq, Hk, G, W, P, page, page_shift, M;
   int npt, npi;              // nodes of an M tile, of an item
   long long budget;
@@ -103,7 +114,7 @@ struct Bars {
   int bad[3];          // a cleaned node element was not finite, by segment modulo three
   // the block's first unit, found by the thread whose rows hold it
   int b0, hk0, mt0, t0;
-  long long todo;
+  long long todo, x0, total;
 };
 static_assert(sizeof(Bars) <= 512, "barriers fit their region");
 
@@ -457,7 +468,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long before;
     const long long total = block_sum(mine, reinterpret_cast<long long*>(red), before);
     const long long x0 = first_unit(total, blockIdx.x), x1 = first_unit(total, blockIdx.x + 1);
-    if (tid == 0) s.todo = x1 - x0;
+    if (tid == 0) {
+      s.todo = x1 - x0;
+      s.x0 = x0;
+      s.total = total;
+    }
     if (x1 > x0 && x0 >= before && x0 < before + mine) {
       long long at = x0 - before;
       for (int b = r0; b < r1; ++b) {
@@ -661,6 +676,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // no product of this block is left in flight
     if (lead) mma_commit(&s.drain);
     warp_wait(&s.drain, 0, kDrainBudget);
+    } else {
+      // ------------------------------------------------------------------------------ absent nodes: 0, -inf
+      const int vecs = a.Hq * D / 8;
+      for (int x = 2 * blockIdx.x + warp - 2; x < a.B * a.N; x += 2 * kBlocks) {
+        const int b = x / a.N, i = x - b * a.N;
+        int n, ctx;
+        row_of(a, b, n, ctx);
+        if (i < n) continue;
+        uint4* o = reinterpret_cast<uint4*>(a.o + (size_t)x * a.Hq * D);
+        for (int v = lane; v < vecs; v += 32) o[v] = make_uint4(0, 0, 0, 0);
+        for (int h = lane; a.lse && h < a.Hq; h += 32) a.lse[(size_t)x * a.Hq + h] = -INFINITY;
+      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
@@ -673,7 +700,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t rows_at = tb + ((uint32_t)(32 * quarter) << 16);
     const int wtid = tid - 128;
     long long g = 0, step = 0;   // tiles of the segments before, tiles of this stream so far
+    const bool by_item = a.items <= kBlocks;
+    bool noted = false;          // (by block: an item that is cut begins in its last segment)
     while (w.next(a)) {
+      if (wtid == 0 && w.t0 == 0) {
+        const bool cut = w.t1 < w.tiles;
+        const int item = (w.b * a.Hk + w.hk) * a.mts + w.mt;
+        if (by_item || cut) {
+          const long long unit = s.x0 + g;
+          a.cuts[by_item ? item : blockIdx.x] = Cut{s.total, unit, item, (int)blockIdx.x,
+                                                    cut ? block_of(s.total, unit + w.tiles - 1) : -1, 0};
+          noted = true;
+        }
+      }
       const int m = kForm == kWide ? st : 0;                     // M tile of the item
       const int node0 = w.mt * a.npi + m * a.npt;
       const int used = max(0, min(a.npt, w.n - node0)) * a.G;
@@ -851,6 +890,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       g += T;
     }
+    if (wtid == 0 && !by_item && !noted) a.cuts[blockIdx.x] = Cut{0, 0, -1, 0, -1, 0};
   }
   if (!ok && lane == 0) atomicCAS(a.err, 0, kErrTimeout);
   __syncwarp();
@@ -862,133 +902,105 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the parts of items that several blocks shared, and fills the rows of absent nodes (0, -inf):
-// o = sum_s e^(lse_s - lse) o_s over a row's parts. A block takes rows of one item, so an item that one
-// block wrote whole costs a block's start and no more. Few items have many parts each (one item is cut
-// over up to every block): with kShare the block's eight warps share a row, warp w taking parts w, w + 8,
-// ... and the block adding the warps' sums in order; otherwise a warp takes a row. Parts are read four at
-// a time: the loop is bound by their latency (38 parts of 224 rows of 256: 33 us one after the other by
-// one warp a row, 8 us so).
+// Joins the parts of items that several blocks shared: o = sum_s e^(lse_s - lse) o_s over a row's parts.
+// Grid (item, or block that begins one; share of the item's rows). An item in eight parts or more (few
+// items, each cut over many blocks) has the block's eight warps share a row, warp w taking parts w, w + 8,
+// ... and the block adding the warps' sums in order; otherwise a warp takes a row. Parts are read four at a
+// time: the loop is bound by their latency (38 parts of 224 rows of 256: 33 us by one warp a row, one part
+// after the other).
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
-template <int D, int KT, int kRows, bool kShare>
-__global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const __grid_constant__ Args a, int mts, int splits) {
+template <int D, int kRows>
+__global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const __grid_constant__ Args a) {
   constexpr int kVec = D / 32;
-  __shared__ long long sums[2][kJoinWarps];
-  __shared__ float s_acc[kShare ? kJoinWarps : 1][D];
+  __shared__ float s_acc[kJoinWarps][D];
   __shared__ float s_sum[kJoinWarps];
   __shared__ int s_part[kBlocks];
-  const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int item = blockIdx.x / splits, split = blockIdx.x - item * splits;
-  const int hk = item / mts, mt = item - hk * mts;
-  long long mine = 0, before_b = 0;   // units of all rows, and of rows before b
-  for (int r = tid; r < a.B; r += kJoinThreads) {
-    int n, ctx;
-    row_of(a, r, n, ctx);
-    const long long u = units_of<KT>(a, n, ctx) * a.Hk;
-    mine += u;
-    if (r < b) before_b += u;
-  }
-  long long dummy;
-  const long long total = block_sum(mine, sums[0], dummy);
-  before_b = block_sum(before_b, sums[1], dummy);
-  int n, ctx;
-  row_of(a, b, n, ctx);
-  const int node0 = mt * a.npi, nodes = min(a.npi, a.N - node0);
-  int c0 = 0, c1 = 0;
-  long long x0 = 0;
-  if (node0 < n) {
-    x0 = before_b + hk * units_of<KT>(a, n, ctx);
-    if (a.mask) x0 += (long long)mt * tiles_of<KT>(a, n, ctx, 0);
-    else
-      for (int t = 0; t < mt; ++t) x0 += tiles_of<KT>(a, n, ctx, t);
-    c0 = block_of(total, x0);
-    c1 = block_of(total, x0 + tiles_of<KT>(a, n, ctx, mt) - 1);
-  }
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   wait_prerequisite();
-  const bool cut = c0 != c1;
-  if (!cut && node0 + nodes <= n) return;   // written whole, no absent nodes
-  // the places of the item's parts, block by block (-1: a block without units). A block's first segment is
-  // its part 0: block c0's only where the item starts its share
-  const int parts = c1 - c0 + 1;
-  if (cut && tid < parts)
-    s_part[tid] = first_unit(total, c0 + tid) < first_unit(total, c0 + tid + 1)
-                      ? (2 * (c0 + tid) + (first_unit(total, c0 + tid) < x0)) * kRows
-                      : -1;
+  int n = 1, ctx, item = blockIdx.x;
+  if (a.items <= kBlocks) row_of(a, item / (a.Hk * a.mts), n, ctx);   // an item without nodes has no note
+  if (a.items <= kBlocks && item % a.mts * a.npi >= n) return;
+  const Cut cut = a.cuts[blockIdx.x];
+  // (the bounds hold for every note the first kernel writes; one that gave up at its start wrote none)
+  if (cut.last <= cut.first || cut.first < 0 || cut.last >= kBlocks || cut.item < 0 || cut.item >= a.items) return;
+  item = cut.item;
+  const int b = item / (a.Hk * a.mts), hk = item / a.mts % a.Hk, mt = item % a.mts;
+  row_of(a, b, n, ctx);
+  const int node0 = mt * a.npi, nodes = min(a.npi, n - node0);
+  // the parts' places, block by block (-1: a block without units). A block's first segment is its part 0:
+  // the first block's only where the item begins its share
+  const int parts = cut.last - cut.first + 1;
+  if (tid < parts) {
+    const int c = cut.first + tid;
+    const long long at = first_unit(cut.total, c);
+    s_part[tid] = at < first_unit(cut.total, c + 1) ? (2 * c + (at < cut.unit)) * kRows : -1;
+  }
   __syncthreads();
-  for (int rr = kShare ? split : split * kJoinWarps + warp; rr < nodes * a.G; rr += splits * (kShare ? 1 : kJoinWarps)) {
+  const bool share = parts >= kJoinWarps;
+  const int step = share ? kJoinWarps : 1;   // a warp's parts
+  for (int rr = share ? blockIdx.y : blockIdx.y * kJoinWarps + warp; rr < nodes * a.G; rr += gridDim.y * (share ? 1 : kJoinWarps)) {
     const int nl = rr / a.G, hg = rr - nl * a.G, m = nl / a.npt;
-    const int i = node0 + nl, row = m * kM + (nl - m * a.npt) * a.G + hg;
-    const size_t orow = ((size_t)b * a.N + i) * a.Hq + hk * a.G + hg;
-    float acc[kVec];
+    const int row = m * kM + (nl - m * a.npt) * a.G + hg;
+    const size_t orow = ((size_t)b * a.N + node0 + nl) * a.Hq + hk * a.G + hg;
+    float acc[kVec], top = -INFINITY, sum = 0.f;
+    bool nan = false;
 #pragma unroll
     for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
-    float lse = -INFINITY;
-    if (i < n) {
-      if (!cut) continue;   // (the same in every warp of the row)
-      float top = -INFINITY;
-      bool nan = false;
-      for (int c = lane; c < parts; c += 32) {
-        const float x = s_part[c] >= 0 ? a.part_lse[s_part[c] + row] : -INFINITY;
-        nan |= x != x;
-        top = fmaxf(top, x);
-      }
-#pragma unroll
-      for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-      nan = __any_sync(0xffffffffu, nan);
-      const float ref = top == -INFINITY ? 0.f : top;
-      float sum = 0.f;
-      constexpr int kStep = kShare ? kJoinWarps : 1;
-      for (int cc = kShare ? warp : 0; cc < parts; cc += 4 * kStep) {
-        float w[4], x[4][kVec];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int c = cc + u * kStep;
-          const int at = c < parts ? s_part[c] : -1;
-          const bool there = at >= 0;
-          const size_t p = (there ? at : s_part[0]) + row;   // (block c0 holds the item's first unit)
-          w[u] = there ? a.part_lse[p] : -INFINITY;
-          const float* po = a.part_o + p * D + lane * kVec;
-#pragma unroll
-          for (int e = 0; e < kVec; e += 2) {
-            const float2 y = *reinterpret_cast<const float2*>(po + e);
-            x[u][e] = y.x;
-            x[u][e + 1] = y.y;
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const float f = ex2_approx((w[u] - ref) * kLog2e);
-          sum += f;
-          if (f != 0.f) {   // a part that saw nothing may hold anything
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) acc[e] = fmaf(f, x[u][e], acc[e]);
-          }
-        }
-      }
-      if constexpr (kShare) {
-        __syncthreads();   // (the row before has been read)
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) s_acc[warp][lane * kVec + e] = acc[e];
-        if (lane == 0) s_sum[warp] = sum;
-        __syncthreads();
-        if (warp > 0) continue;
-        sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
-#pragma unroll
-        for (int v = 0; v < kJoinWarps; ++v) {
-          sum += s_sum[v];
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) acc[e] += s_acc[v][lane * kVec + e];
-        }
-      }
-      const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) acc[e] *= inv;
-      lse = nan ? NAN : sum > 0.f ? ref + logf(sum) : -INFINITY;
-    } else if (kShare && warp > 0) {
-      continue;
+    for (int c = lane; c < parts; c += 32) {
+      const float x = s_part[c] >= 0 ? a.part_lse[s_part[c] + row] : -INFINITY;
+      nan |= x != x;
+      top = fmaxf(top, x);
     }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    nan = __any_sync(0xffffffffu, nan);
+    const float ref = top == -INFINITY ? 0.f : top;
+    for (int cc = share ? warp : 0; cc < parts; cc += 4 * step) {
+      float w[4], x[4][kVec];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int c = cc + u * step, at = c < parts ? s_part[c] : -1;
+        const size_t p = (at >= 0 ? at : s_part[0]) + row;   // (the first block holds the item's first unit)
+        w[u] = at >= 0 ? a.part_lse[p] : -INFINITY;
+        const float* po = a.part_o + p * D + lane * kVec;
+#pragma unroll
+        for (int e = 0; e < kVec; e += 2) {
+          const float2 y = *reinterpret_cast<const float2*>(po + e);
+          x[u][e] = y.x;
+          x[u][e + 1] = y.y;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float f = ex2_approx((w[u] - ref) * kLog2e);
+        sum += f;
+        if (f != 0.f) {   // a part that saw nothing may hold anything
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) acc[e] = fmaf(f, x[u][e], acc[e]);
+        }
+      }
+    }
+    if (share) {   // (the same in every warp, and so is the row)
+      __syncthreads();   // the row before has been read
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) s_acc[warp][lane * kVec + e] = acc[e];
+      if (lane == 0) s_sum[warp] = sum;
+      __syncthreads();
+      if (warp > 0) continue;
+      sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
+#pragma unroll
+      for (int v = 0; v < kJoinWarps; ++v) {
+        sum += s_sum[v];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) acc[e] += s_acc[v][lane * kVec + e];
+      }
+    }
+    const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) acc[e] *= inv;
+    const float lse = nan ? NAN : sum > 0.f ? ref + logf(sum) : -INFINITY;
     __nv_bfloat16* out = a.o + orow * D + lane * kVec;
 #pragma unroll
     for (int e = 0; e < kVec; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(acc[e], acc[e + 1]);
@@ -1043,6 +1055,9 @@ cudaError_t launch(const TreeAttnArgs& p, cudaStream_t st) {
   a.part_lse = a.part_o + (size_t)2 * kBlocks * C::kRows * D;
   a.B = p.B; a.N = p.N; a.Hq = p.Hq; a.Hk = p.Hk; a.W = (p.N + 63) / 64; a.P = p.P; a.page = p.page; a.M = p.M;
   a.page_shift = __builtin_ctz((unsigned)p.page);
+  a.mts = (p.N + a.npi - 1) / a.npi;
+  a.items = p.B * p.Hk * a.mts;
+  a.cuts = reinterpret_cast<Cut*>(a.part_lse + (size_t)2 * kBlocks * C::kRows);
   a.budget = wait_budget_cycles();
   a.err = p.err;
   cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D, kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
@@ -1051,12 +1066,10 @@ cudaError_t launch(const TreeAttnArgs& p, cudaStream_t st) {
   tree_attn_kernel<D, kForm><<<kBlocks, kThreads, C::kSmem, st>>>(mq, mk, mv, a);
   stage_timer_end(slot, st);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int mts = (p.N + a.npi - 1) / a.npi;
-  const long long items = (long long)p.B * p.Hk * mts;
-  const bool share = items <= 16;   // ten parts a row and more; below, eight warps would find one or two each
-  const int splits = share ? a.npi * a.G : (int)std::max(1ll, std::min(8ll, 1024 / items));
+  // shares of an item's rows: about eight blocks a SM in all, one row each at most
+  const int x = std::min(a.items, kBlocks);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.Hk * mts * splits), p.B);
+  cfg.gridDim = dim3(x, std::max(1, std::min(a.npi * a.G, kNumSMs * 8 / x)));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -1065,8 +1078,7 @@ cudaError_t launch(const TreeAttnArgs& p, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   slot = stage_timer_begin(st, kKernTreeAttnJoin);
-  e = share ? cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D, C::KT, C::kRows, true>, a, mts, splits)
-            : cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D, C::KT, C::kRows, false>, a, mts, splits);
+  e = cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D, C::kRows>, a);
   stage_timer_end(slot, st);
   return e;
 }
@@ -1080,7 +1092,9 @@ cudaError_t launch_two(const TreeAttnArgs& a, cudaStream_t s) {
 }  // namespace
 
 // Two parts a block, each of the largest item's rows: 256, or 128 for D = 256.
-size_t tree_attn_workspace_bytes(int D) { return (size_t)2 * kBlocks * (D == 256 ? kM : 2 * kM) * (D + 1) * sizeof(float); }
+size_t tree_attn_workspace_bytes(int D) {
+  return (size_t)2 * kBlocks * (D == 256 ? kM : 2 * kM) * (D + 1) * sizeof(float) + kBlocks * sizeof(Cut);
+}
 
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t s) {
   return a.D == 64 ? launch_two<64>(a, s) : a.D == 128 ? launch_two<128>(a, s) : launch<256, kSplit>(a, s);
