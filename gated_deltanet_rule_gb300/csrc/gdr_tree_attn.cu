@@ -273,7 +273,8 @@ __device__ __forceinline__ long long block_sum(long long v, long long* warps, lo
 }
 
 // Bits k = 0 .. 63: position pos0 + k is seen by node i (rel = pos0 - ctx).
-__device__ __forceinline__ uint64_t seen(const Args& a, const uint64_t* words, int i, int n, long long rel) {
+// words: the node's mask, word0 its first word (loaded once a segment).
+__device__ __forceinline__ uint64_t seen(const Args& a, const uint64_t* words, uint64_t word0, int i, int n, long long rel) {
   if (rel + 64 <= 0) return ~0ull;
   uint64_t ctx_bits = 0, bits;
   int sh;         // bit k is node k - sh
@@ -289,7 +290,7 @@ __device__ __forceinline__ uint64_t seen(const Args& a, const uint64_t* words, i
   if (a.mask) {
     const long long w = j0 >> 6;
     const int o = (int)(j0 & 63);
-    const uint64_t lo = w < a.W ? __ldg(words + w) : 0, hi = (o && w + 1 < a.W) ? __ldg(words + w + 1) : 0;
+    const uint64_t lo = w == 0 ? word0 : w < a.W ? __ldg(words + w) : 0, hi = (o && w + 1 < a.W) ? __ldg(words + w + 1) : 0;
     bits = (lo >> o) | (o ? hi << (64 - o) : 0);
   } else {
     const long long k = i - j0 + 1;   // nodes j0 .. i
@@ -301,8 +302,14 @@ __device__ __forceinline__ uint64_t seen(const Args& a, const uint64_t* words, i
   return ctx_bits | (bits << sh);
 }
 
+__device__ __forceinline__ float got(const float* p) { return __ldcg(p); }
+__device__ __forceinline__ float got(const __nv_bfloat16* p) {
+  return __uint_as_float((uint32_t)__ldcg(reinterpret_cast<const unsigned short*>(p)) << 16);
+}
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16(x); }
 // Adds the elements of seen nodes' V that are not finite (cleaned away before the product) to what the
-// row's thread has just written to out[0 .. cols).
+// warp has just written to out[0 .. cols).
 template <typename T>
 __device__ __noinline__ void add_back(const Args& a, int b, int hk, int i, int n, int ctx, int lo, int hi, int D, int d0,
                                       int cols, T* out) {
@@ -315,7 +322,7 @@ __device__ __noinline__ void add_back(const Args& a, int b, int hk, int i, int n
     const __nv_bfloat16* v = a.v_pages + (((size_t)pg * a.page + pos % a.page) * a.Hk + hk) * D + d0;
     for (int d = 0; d < cols; ++d) {
       const float x = __bfloat162float(v[d]);
-      if (!(fabsf(x) < INFINITY)) out[d] = (T)((float)out[d] + x);
+      if (!(fabsf(x) < INFINITY)) put(out + d, got(out + d) + x);
     }
   }
 }
@@ -335,19 +342,16 @@ __device__ __forceinline__ bool clean_tile(uint8_t* vt, int t, int ctx, int end,
     }
     uint4 v = *p;
     uint32_t* u = reinterpret_cast<uint32_t*>(&v);
-    bool hit = false;
+    // an exponent of all ones carries into the sign's place when one is added to it
+    uint32_t hit = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if ((u[e] & 0x7F80u) == 0x7F80u) {
-        u[e] &= 0xFFFF0000u;
-        hit = true;
-      }
-      if ((u[e] & 0x7F800000u) == 0x7F800000u) {
-        u[e] &= 0xFFFFu;
-        hit = true;
-      }
-    }
+    for (int e = 0; e < 4; ++e) hit |= ((u[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
     if (hit) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if ((u[e] & 0x7F80u) == 0x7F80u) u[e] &= 0xFFFF0000u;
+        if ((u[e] & 0x7F800000u) == 0x7F800000u) u[e] &= 0xFFFFu;
+      }
       *p = v;
       bad = true;
     }
@@ -393,7 +397,7 @@ __device__ __forceinline__ void hide(float* x, uint64_t seen) {
 // Multiplies kCols accumulator columns of the warp's rows.
 template <int kCols>
 __device__ __forceinline__ void rescale(uint32_t at, float f) {
-#pragma unroll 2
+#pragma unroll 1
   for (int c = 0; c < kCols; c += 32) {
     float o[32];
     uint32_t u[32];
@@ -403,18 +407,52 @@ __device__ __forceinline__ void rescale(uint32_t at, float f) {
     tmem_st32(at + c, u);
   }
 }
-// Scaled accumulator columns to o (bf16) or to the part (float32).
-__device__ __forceinline__ void put32(const float* o, bool whole, __nv_bfloat16* out, float* part) {
+// Four lanes hold four 16-byte units of a row each; afterwards lane q of the four holds unit q of their
+// four rows.
+__device__ __forceinline__ void turn_units(uint32_t (&u)[4][4]) {
+  const int q = threadIdx.x & 3;
+#pragma unroll
+  for (int m = 1; m <= 2; m <<= 1) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (x & m) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, (q & m) ? u[x][e] : u[x | m][e], m);
+        if (q & m) u[x][e] = got;
+        else u[x | m][e] = got;
+      }
+    }
+  }
+}
+// 32 scaled accumulator columns of the warp's rows to o (bf16) or to the part (float32). A thread's columns
+// are 64 or 128 bytes of one row: written as they are, a store would touch 32 rows, and the stores were two
+// thirds of a segment's end. at[k]: the place of row k of the lane's four in units of 16 bytes (< 0: none).
+__device__ __forceinline__ void put32(const float* o, bool whole, uint4* out, const long long (&at)[4]) {
+  const int q = threadIdx.x & 3;
   if (whole) {
-    uint4* to = reinterpret_cast<uint4*>(out);
+    uint32_t u[4][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      to[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
-                         pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[x][e] = pack_bf16x2(o[8 * x + 2 * e], o[8 * x + 2 * e + 1]);
+    turn_units(u);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (at[k] >= 0) out[at[k] + q] = make_uint4(u[k][0], u[k][1], u[k][2], u[k][3]);
   } else {
-    float4* to = reinterpret_cast<float4*>(part);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) to[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+    for (int h = 0; h < 2; ++h) {
+      uint32_t u[4][4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[x][e] = __float_as_uint(o[16 * h + 4 * x + e]);
+      turn_units(u);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (at[k] >= 0) out[at[k] + 4 * h + q] = make_uint4(u[k][0], u[k][1], u[k][2], u[k][3]);
+    }
   }
 }
 
@@ -610,7 +648,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     };
     // A wait without a vote: a lane whose wait ran out issues nothing more, and the warp leaves together at
-    // the end of the tile.
+    // the end of the tile. While products run, their operands fill shared memory's bandwidth and even a
+    // wait that is satisfied takes 200 to 400 cycles; so what the next products need is asked for before
+    // these are issued (`early`), and waited for only if it was not there yet.
+    auto early = [&](uint64_t* bar, uint32_t parity) { return test_wait(bar, parity); };
     auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && (a.budget == 0 ? test_wait(bar, parity) : mbar_wait(bar, parity, a.budget)); };
     Ring<NS> kr, vr;                // the next tile's keys and values
     vr.step(1);
@@ -624,19 +665,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int streams = kForm == kWide ? __shfl_sync(0xffffffffu, w.m_tiles(a), 0) : kForm == kNarrow ? 2 : 1;
       if constexpr (kForm == kSplit) {
         // S of tile j + 1, then P V of tile j
+        bool k_there = false, v_there = false;
         for (int j = -1; j < T; ++j) {
           if (j + 1 < T) {
             const uint32_t x = steps[0]++;
-            wait(&s.full[kr.slot], kr.parity);
+            if (!k_there) wait(&s.full[kr.slot], kr.parity);
             if (x >= 2) wait(&s.pv[x & 1], ((x - 2) >> 1) & 1);   // (P V of tile j - 1 is done)
+            if (j >= 0) v_there = early(&s.full[vr.slot], vr.parity);
             scores(x & 1, 0, kr.slot, true, j + 2 == T);
             kr.step(2);
           }
           if (j >= 0) {
             const uint32_t x = steps[0] - (j + 1 < T ? 2 : 1);      // tile j
             if (j == 0 && !first) wait(&s.o_free, o_parity);
-            wait(&s.full[vr.slot], vr.parity);
+            if (!v_there || j + 1 == T) wait(&s.full[vr.slot], vr.parity);
             wait(&s.p_full[x & 1], (x >> 1) & 1);
+            k_there = j + 2 < T && early(&s.full[kr.slot], kr.parity);
             outputs(x & 1, 0, vr.slot, j > 0, true);
             vr.step(2);
           }
@@ -647,26 +691,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         // one buffer a stream: S of a stream's next tile goes over P of its last one, once that product is
         // done; the streams take turns (kNarrow: tiles st, st + 2, ...; kWide: every tile)
         constexpr int kStep = kForm == kNarrow ? 2 : 1;
+        bool k_there = false, v_there = false, p_there = false;
         for (int k = 0; k <= (T + kStep - 1) / kStep; ++k) {
 #pragma unroll
           for (int st = 0; st < 2; ++st) {
             if (st >= streams) break;
             const int j = kForm == kNarrow ? 2 * k + st : k;
             const bool last = kForm == kNarrow || st == streams - 1;
+            const bool own_tile = kForm == kNarrow || st == 0;     // (kWide: the first stream waits for both)
             if (k > 0 && j - kStep < T) {
               if (k == 1 && st == 0 && !first) wait(&s.o_free, o_parity);
-              if (kForm == kNarrow || st == 0) wait(&s.full[vr.slot], vr.parity);   // (kWide: one tile for both)
-              wait(&s.p_full[st], (steps[st] - 1) & 1);
+              if (own_tile && !v_there) wait(&s.full[vr.slot], vr.parity);
+              if (!p_there) wait(&s.p_full[st], (steps[st] - 1) & 1);
+              k_there = own_tile && j < T && early(&s.full[kr.slot], kr.parity);
               outputs(st, st, vr.slot, k > 1, last);
               if (last) vr.step(2);
             }
+            v_there = p_there = false;
             if (j < T) {
-              if (kForm == kNarrow || st == 0) wait(&s.full[kr.slot], kr.parity);
+              if (own_tile && !k_there) wait(&s.full[kr.slot], kr.parity);
               if (steps[st] > 0) wait(&s.pv[st], (steps[st] - 1) & 1);
+              // the products after these: P V of the other stream's last tile (streams == 1: of this one's)
+              const int next = streams == 1 ? 0 : st ^ 1;
+              const int next_j = kForm == kNarrow ? j - 1 : st == streams - 1 ? k : k - 1;
+              if (next != st && next_j >= 0) p_there = early(&s.p_full[next], (steps[next] - 1) & 1);
+              if (next_j >= 0 && (kForm == kNarrow || next == 0)) v_there = early(&s.full[vr.slot], vr.parity);
               scores(st, kForm == kWide ? st : 0, kr.slot, last, j == T - 1 && last);
               ++steps[st];
               if (last) kr.step(2);
             }
+            k_there = false;
           }
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
@@ -719,6 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool active = 32 * quarter < used, live = row < used;
       const int i = node0 + (live ? row / a.G : 0), hg = live ? row % a.G : 0;
       const uint64_t* words = a.mask && live ? a.mask + ((size_t)w.b * a.N + i) * a.W : nullptr;
+      const uint64_t word0 = words ? __ldg(words) : 0;
       const int end = w.ctx + w.n;
       const int T = w.t1 - w.t0;
       const bool masked_any = w.t1 * KT > w.ctx;
@@ -768,10 +823,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (masked && live) {
             const long long rel = (long long)t * KT + col0 - w.ctx;
             if constexpr (kCols == 32) {
-              hide<32>(x, seen(a, words, i, w.n, rel));
+              hide<32>(x, seen(a, words, word0, i, w.n, rel));
             } else {
 #pragma unroll
-              for (int c = 0; c < kCols; c += 64) hide<64>(x + c, seen(a, words, i, w.n, rel + c));
+              for (int c = 0; c < kCols; c += 64) hide<64>(x + c, seen(a, words, word0, i, w.n, rel + c));
             }
           }
           float mx = largest<kCols>(x);
@@ -856,8 +911,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (active && ok) {
         tc_fence_after();
         const bool both = kForm == kNarrow && T > 1;             // (one tile: the second accumulator was not written)
-        const float f0 = (st == 0 || kForm != kNarrow ? self : other) * inv, f1 = (st == 0 ? other : self) * inv;
+        // the places of the rows of this lane's four: of o, or of the part
+        uint4* out = reinterpret_cast<uint4*>(whole ? (void*)a.o : (void*)a.part_o);
+        long long at[4];
 #pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const long long mine = whole ? (long long)orow * (D / 8) + d0 / 8 : (long long)prow * (D / 4) + d0 / 4;
+          at[k] = __shfl_sync(0xffffffffu, live ? mine : -1, (lane & ~3) | k);
+        }
+        const float f0 = (st == 0 || kForm != kNarrow ? self : other) * inv, f1 = (st == 0 ? other : self) * inv;
+#pragma unroll 1   // (a call on few positions is bound by fetching its instructions)
         for (int c = 0; c < kOut; c += 32) {
           float o[32];
           tmem_ld32(rows_at + C::kTmemO + (kForm == kWide ? st * D : 0) + d0 + c, o);
@@ -871,9 +934,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int e = 0; e < 32; ++e) o[e] = fmaf(o1[e], f1, o[e]);
             }
           }
-          if (live) put32(o, whole, a.o + orow * D + d0 + c, a.part_o + prow * D + d0 + c);
+          put32(o, whole, out + (whole ? c / 8 : c / 4), at);
           __syncwarp();   // (before the next load of the whole warp)
         }
+        if (bad) __threadfence();   // (add_back reads what neighbouring lanes wrote)
+        __syncwarp();
         tc_fence_before();
       }
       __syncwarp();
