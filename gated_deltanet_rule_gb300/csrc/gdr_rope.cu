@@ -4,10 +4,10 @@
 // Pairs are (j, j + R/2), or (2j, 2j + 1) when interleaved. Forward (dense outputs, or k and v left
 // in a cache's pages) and gradient.
 //
-// Layout: D/16 lanes hold one head, two runs of eight elements each (16-byte loads of bf16), chosen so
-// that both members of a pair lie in one lane: in the half-split form a lane of the rotated part holds
-// eight elements at 8 l and their partners at R/2 + 8 l, every other lane sixteen neighbours. Pair j of
-// lane l is 8 l + (0..7) in both forms. The head's sum of squares is the only exchange (shuffles).
+// Layout: D/16 lanes hold one head, two runs of eight elements each: lane l of the rotated part those at
+// 8 l and R/2 + 8 l, the lanes of the rest likewise. So neighbouring lanes read and write neighbouring 16
+// bytes, and both members of a pair lie in one lane, in the half-split form (run against run) and in the
+// interleaved one (neighbours). The head's sum of squares is the only exchange (shuffles).
 //
 // A block takes the heads of one kind (queries, keys, or values to be copied) of a few tokens: it forms
 // the tokens' cosines and sines once in shared memory, one entry a thread, and its warps then walk the
@@ -17,6 +17,7 @@
 // a 64-bit binary fraction, times the position, dropping whole turns), exact to 2^-32 turn at any
 // 31-bit position; float32 angles would be off by 0.06 rad at position 2^20, and float64 arithmetic
 // runs at 1/64 of the float32 rate here. The fraction is reduced to an eighth turn before sincospif.
+#include <algorithm>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -30,6 +31,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPairs = 2048;       // (token, pair) angles of a block
 constexpr int kMostTokens = 256;   // tokens of a block
+constexpr int kDepth = 4;          // rows of every lane in flight (the gradient of float32: 2)
 
 // Two floats in one register pair: the packed operations halve the instructions of this kernel, whose
 // issue rate is what bounds it beside HBM.
@@ -54,51 +56,55 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
 }
 __device__ __forceinline__ F2 neg2(F2 a) { return {a.v ^ 0x8000000080000000ull}; }
 
-// Eight consecutive elements as loaded.
-template <typename T>
-struct Raw;
-template <>
-struct Raw<__nv_bfloat16> {
-  uint4 u;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldg(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void get(F2* x) const {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Eight consecutive elements in shared memory (staged by asynchronous copies, 16 bytes at a time).
+__device__ __forceinline__ void get(const __nv_bfloat16* p, F2* x) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = pack(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
-  }
-  __device__ __forceinline__ static void put(__nv_bfloat16* p, const F2* x) {
-    uint32_t w[4];
+  for (int e = 0; e < 4; ++e) x[e] = pack(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
+}
+__device__ __forceinline__ void get(const float* p, F2* x) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float lo, hi;
-      unpack(x[e], lo, hi);
-      w[e] = ptx::pack_bf16x2(lo, hi);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int h = 0; h < 2; ++h) {
+    const ulonglong2 u = reinterpret_cast<const ulonglong2*>(p)[h * kThreads];   // (pieces lie kThreads apart)
+    x[2 * h] = {u.x};
+    x[2 * h + 1] = {u.y};
   }
-  __device__ __forceinline__ void copy(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = u; }
-};
-template <>
-struct Raw<float> {
-  float4 u, v;
-  __device__ __forceinline__ void load(const float* p) {
-    u = __ldg(reinterpret_cast<const float4*>(p));
-    v = __ldg(reinterpret_cast<const float4*>(p) + 1);
+}
+__device__ __forceinline__ void put(__nv_bfloat16* p, const F2* x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float lo, hi;
+    unpack(x[e], lo, hi);
+    w[e] = ptx::pack_bf16x2(lo, hi);
   }
-  __device__ __forceinline__ void get(F2* x) const {
-    x[0] = pack(u.x, u.y);
-    x[1] = pack(u.z, u.w);
-    x[2] = pack(v.x, v.y);
-    x[3] = pack(v.z, v.w);
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void put(float* p, const F2* x) {
+  reinterpret_cast<ulonglong2*>(p)[0] = make_ulonglong2(x[0].v, x[1].v);
+  reinterpret_cast<ulonglong2*>(p)[1] = make_ulonglong2(x[2].v, x[3].v);
+}
+
+// A thread's own ring in shared memory: kDepth rows of kPieces 16-byte pieces, piece p of every thread side
+// by side. Only the thread that copied a piece reads it, so a wait for its own copies is all it needs; the
+// copies hold no registers, which is what bounded the rows in flight.
+template <int kPieces, int kDepth>
+struct Ring {
+  uint4* mine;
+  __device__ __forceinline__ explicit Ring(void* smem) : mine(static_cast<uint4*>(smem) + threadIdx.x) {}
+  __device__ __forceinline__ uint4* at(int slot, int piece) const { return mine + (slot * kPieces + piece) * kThreads; }
+  // eight elements from src into pieces first, first + 1, ...
+  template <typename T>
+  __device__ __forceinline__ void copy(int slot, int first, const T* src) const {
+#pragma unroll
+    for (int e = 0; e < (int)(8 * sizeof(T) / 16); ++e)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(at(slot, first + e))),
+                   "l"(reinterpret_cast<const uint4*>(src) + e)
+                   : "memory");
   }
-  __device__ __forceinline__ static void put(float* p, const F2* x) {
-    reinterpret_cast<ulonglong2*>(p)[0] = make_ulonglong2(x[0].v, x[1].v);
-    reinterpret_cast<ulonglong2*>(p)[1] = make_ulonglong2(x[2].v, x[3].v);
-  }
-  __device__ __forceinline__ void copy(float* p) const {
-    reinterpret_cast<float4*>(p)[0] = u;
-    reinterpret_cast<float4*>(p)[1] = v;
-  }
+  template <typename T>
+  __device__ __forceinline__ const T* row(int slot, int piece) const { return reinterpret_cast<const T*>(at(slot, piece)); }
 };
 
 // inv_freq / (2 pi) modulo one as a 64-bit binary fraction, from the bits of the double.
@@ -142,9 +148,9 @@ struct Lane {
     sub = lane / kLanes;
     l = lane % kLanes;
     turns = 16 * l < a.R;
-    const bool split = turns && !a.interleaved;
-    off0 = split ? 8 * l : 16 * l;
-    off1 = split ? a.R / 2 + 8 * l : 16 * l + 8;
+    const int first = turns ? 8 * l : a.R + 8 * (l - a.R / 16);
+    off0 = first;
+    off1 = first + (turns ? a.R : D - a.R) / 2;
   }
 };
 
@@ -156,8 +162,15 @@ __device__ __forceinline__ void form_angles(const RopeArgs& a, long long t0, int
     float c, s;
     turn_sincos(turn_fraction(__ldg(a.inv_freq + j)), __ldg(a.pos + t0 + t), c, s);
     // four runs of [lane][4]: the lanes' first and last four cosines, then sines, so that the lanes of a
-    // head read neighbouring 16 bytes
-    float* at = cs + t * a.R + ((j >> 2) & 1) * (a.R / 4) + (j >> 3) * 4 + (j & 3);
+    // head read neighbouring 16 bytes. Pair j is entry e of lane l: half-split j = 8 l + e; interleaved
+    // j = 4 l + e in a lane's first run, R/4 + 4 l + e - 4 in its second
+    int l = j >> 3, e = j & 7;
+    if (a.interleaved) {
+      const int second = 4 * j >= a.R, k = second ? j - a.R / 4 : j;
+      l = k >> 2;
+      e = 4 * second + (k & 3);
+    }
+    float* at = cs + t * a.R + (e >> 2) * (a.R / 4) + l * 4 + (e & 3);
     at[0] = c;
     at[a.R / 2] = s;
   }
@@ -248,11 +261,14 @@ struct Kind {
 };
 
 // Normed, turned and written (kPages: keys into the pages, values copied there). HBM-bound: each element
-// is read and written once, 16 bytes a load, two rows of every lane in flight.
+// is read and written once; every lane has kDepth rows in flight in shared memory (ROPE_ROW).
 template <typename T, int D, bool kPages, bool kInter>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a) {
+  constexpr int kRun = 8 * sizeof(T) / 16, kPieces = 2 * kRun;   // 16-byte pieces of a run, of a lane's row
+  extern __shared__ __align__(16) uint8_t stage[];
   __shared__ __align__(16) float cs[2 * kPairs];
   __shared__ long long slot[kMostTokens];
+  const Ring<kPieces, kDepth> ring(stage);
   const Lane<D> ln(a);
   const long long tokens = (long long)a.B * a.N;
   const int kind = blockIdx.x < a.blocks[0] ? 0 : blockIdx.x < a.blocks[0] + a.blocks[1] ? 1 : 2;
@@ -271,19 +287,19 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
   const T* base = k.src + t0 * k.tok;
   const int tok = (int)k.tok, head = (int)k.head;
   // the first rows are on their way while the angles are formed
-  constexpr int kAhead = 2;
-  Raw<T> raw[kAhead][2];
   auto load = [&](int u, int x) {
-    if (x >= rows) return;
-    int t, h;
-    row_at(x, k.H, magic, t, h);
-    const T* src = base + (t * tok + h * head);   // (below 2^31: tokens of a block <= 256)
-    raw[u][0].load(src + ln.off0);
-    raw[u][1].load(src + ln.off1);
+    if (x < rows) {
+      int t, h;
+      row_at(x, k.H, magic, t, h);
+      const T* src = base + (t * tok + h * head);   // (below 2^31: tokens of a block <= 256)
+      ring.copy(u, 0, src + ln.off0);
+      ring.copy(u, kRun, src + ln.off1);
+    }
+    ptx::cp_async_commit();
   };
   const int x0 = warp * Lane<D>::kHeads + ln.sub;
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u) load(u, x0 + u * step);
+  for (int u = 0; u < kDepth; ++u) load(u, x0 + u * step);
   F2 w[8];
   if (kind < 2) {
     load16(k.w, ln.off0, ln.off1, w);
@@ -305,48 +321,49 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
     }
   }
   __syncthreads();
-  for (int xw = warp * Lane<D>::kHeads; xw < rows; xw += kAhead * step) {   // the same in every lane
+  int u = 0;
+  for (int xw = warp * Lane<D>::kHeads; xw < rows; xw += step, u = u + 1 == kDepth ? 0 : u + 1) {   // the same in every lane
+    const int x = xw + ln.sub;
+    const bool live = x < rows;
+    int t, h;
+    row_at(live ? x : rows - 1, k.H, magic, t, h);
+    const long long first = to_pages ? slot[t] * k.H + h : t0 * k.H + x;
+    T* out = k.out + first * D;
+    const bool write = live && first >= 0;
+    ptx::cp_async_wait<kDepth - 1>();
+    if (kPages && kind == 2) {
+      if (write) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int x = xw + u * step + ln.sub;
-      if (xw + u * step >= rows) break;   // the same in every lane
-      const bool live = x < rows;
-      int t, h;
-      row_at(live ? x : rows - 1, k.H, magic, t, h);
-      const long long first = to_pages ? slot[t] * k.H + h : t0 * k.H + x;
-      T* out = k.out + first * D;
-      const bool write = live && first >= 0;
-      if (kPages && kind == 2) {
-        if (write) {
-          raw[u][0].copy(out + ln.off0);
-          raw[u][1].copy(out + ln.off1);
-        }
-      } else {
-        F2 y[8];
-        raw[u][0].get(y);
-        raw[u][1].get(y + 4);
-        F2 sq = mul2(y[0], y[0]);
-#pragma unroll
-        for (int e = 1; e < 8; ++e) sq = fma2(y[e], y[e], sq);
-        float s0, s1;
-        unpack(sq, s0, s1);
-        const float ss = head_sum<D>(live ? s0 + s1 : 0.f);
-        const float r = rsqrtf(ss * (1.f / D) + a.eps);
-        const F2 rr = pack(r, r);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = mul2(mul2(w[e], y[e]), rr);
-        if (ln.turns) turn<kInter, false>(y, cs + t * a.R, a.R, ln.l);
-        if (write) {
-          Raw<T>::put(out + ln.off0, y);
-          Raw<T>::put(out + ln.off1, y + 4);
+        for (int e = 0; e < kRun; ++e) {
+          reinterpret_cast<uint4*>(out + ln.off0)[e] = *ring.at(u, e);
+          reinterpret_cast<uint4*>(out + ln.off1)[e] = *ring.at(u, kRun + e);
         }
       }
-      load(u, x + kAhead * step);
+    } else {
+      F2 y[8];
+      get(ring.template row<T>(u, 0), y);
+      get(ring.template row<T>(u, kRun), y + 4);
+      F2 sq = mul2(y[0], y[0]);
+#pragma unroll
+      for (int e = 1; e < 8; ++e) sq = fma2(y[e], y[e], sq);
+      float s0, s1;
+      unpack(sq, s0, s1);
+      const float ss = head_sum<D>(live ? s0 + s1 : 0.f);
+      const float r = rsqrtf(ss * (1.f / D) + a.eps);
+      const F2 rr = pack(r, r);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = mul2(mul2(w[e], y[e]), rr);
+      if (ln.turns) turn<kInter, false>(y, cs + t * a.R, a.R, ln.l);
+      if (write) {
+        put(out + ln.off0, y);
+        put(out + ln.off1, y + 4);
+      }
     }
+    load(u, x + kDepth * step);
   }
 }
 
-constexpr int kBwdBlocks = kNumSMs * 6;   // blocks of the gradient, and rows of its partial sums, at most
+constexpr int kBwdBlocks = kNumSMs * 2;   // blocks of the gradient (one wave), and rows of its partial sums, at most
 
 // Gradient, with dy = R^T dout and r = 1 / sqrt(mean(x^2) + eps):
 //   dx = r (w dy - x r^2 mean(w dy x)),  dw = sum over tokens and heads of dy x r.
@@ -356,8 +373,12 @@ constexpr int kBwdBlocks = kNumSMs * 6;   // blocks of the gradient, and rows of
 // time.
 template <typename T, int D, bool kInter>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeArgs a) {
+  constexpr int kRun = 8 * sizeof(T) / 16;            // 16-byte pieces of a run; a lane's row has four runs
+  constexpr int kDepthB = kRun == 1 ? kDepth : kDepth / 2;
+  extern __shared__ __align__(16) uint8_t stage[];
   __shared__ __align__(16) float cs[2 * kPairs];
   __shared__ float acc[kWarps][D];
+  const Ring<4 * kRun, kDepthB> ring(stage);
   const Lane<D> ln(a);
   const long long tokens = (long long)a.B * a.N;
   const bool is_q = blockIdx.x < a.blocks[0];
@@ -376,33 +397,37 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeAr
   for (long long group = is_q ? blockIdx.x : blockIdx.x - a.blocks[0]; group * per < tokens; group += stride) {
     const long long t0 = group * per;
     const int n = (int)min((long long)per, tokens - t0), rows = n * H;
-    Raw<T> rx[2], rd[2];
-    auto load = [&](int x) {
-      if (x >= rows) return;
-      int t, h;
-      row_at(x, H, magic, t, h);
-      const T* s = src + t0 * tok + (t * (int)tok + h * (int)head);
-      const T* d = dsrc + (t0 * H + x) * D;
-      rx[0].load(s + ln.off0);
-      rx[1].load(s + ln.off1);
-      rd[0].load(d + ln.off0);
-      rd[1].load(d + ln.off1);
+    auto load = [&](int u, int x) {
+      if (x < rows) {
+        int t, h;
+        row_at(x, H, magic, t, h);
+        const T* s = src + t0 * tok + (t * (int)tok + h * (int)head);
+        const T* d = dsrc + (t0 * H + x) * D;
+        ring.copy(u, 0, s + ln.off0);
+        ring.copy(u, kRun, s + ln.off1);
+        ring.copy(u, 2 * kRun, d + ln.off0);
+        ring.copy(u, 3 * kRun, d + ln.off1);
+      }
+      ptx::cp_async_commit();
     };
-    load(warp * Lane<D>::kHeads + ln.sub);
+#pragma unroll
+    for (int u = 0; u < kDepthB; ++u) load(u, (warp + u * kWarps) * Lane<D>::kHeads + ln.sub);
     __syncthreads();   // the group before has been walked
     form_angles(a, t0, n, cs);
     __syncthreads();
-    for (int xw = warp * Lane<D>::kHeads; xw < rows; xw += step) {   // the same in every lane
+    int u = 0;
+    for (int xw = warp * Lane<D>::kHeads; xw < rows; xw += step, u = u + 1 == kDepthB ? 0 : u + 1) {   // the same in every lane
       const int x = xw + ln.sub;
       const bool live = x < rows;
       int t, h;
       row_at(live ? x : rows - 1, H, magic, t, h);
+      ptx::cp_async_wait<kDepthB - 1>();
       F2 y[8], dy[8];
-      rx[0].get(y);
-      rx[1].get(y + 4);
-      rd[0].get(dy);
-      rd[1].get(dy + 4);
-      load(x + step);
+      get(ring.template row<T>(u, 0), y);
+      get(ring.template row<T>(u, kRun), y + 4);
+      get(ring.template row<T>(u, 2 * kRun), dy);
+      get(ring.template row<T>(u, 3 * kRun), dy + 4);
+      load(u, x + kDepthB * step);
       if (ln.turns) turn<kInter, true>(dy, cs + t * a.R, a.R, ln.l);
       F2 sq = mul2(y[0], y[0]), dt = mul2(mul2(w[0], dy[0]), y[0]);
 #pragma unroll
@@ -425,8 +450,8 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeAr
         g[e] = fma2(dy[e], mul2(y[e], rr), g[e]);
       }
       float* out = dst + (t0 * H + x) * D;
-      Raw<float>::put(out + ln.off0, dx);
-      Raw<float>::put(out + ln.off1, dx + 4);
+      put(out + ln.off0, dx);
+      put(out + ln.off1, dx + 4);
     }
   }
   // the block's sum: lanes of equal elements within a warp, then the warps in order
@@ -474,60 +499,71 @@ __global__ void __launch_bounds__(1024) qk_norm_rope_bwd_join_kernel(const RopeA
 }
 
 // Tokens of a block so that its rows come to about `rows`, within the shared memory for angles.
-int tokens_of(const RopeArgs& a, int H, int rows, long long tokens) {
+int tokens_of(const RopeArgs& a, int H, long long rows, long long tokens) {
   const int most = a.R > 0 && 2 * kPairs / a.R < kMostTokens ? 2 * kPairs / a.R : kMostTokens;
   long long t = (rows + H - 1) / H;
   if (t > most) t = most;
   if (t > tokens) t = tokens;
   return (int)(t < 1 ? 1 : t);
 }
-// Rows of a block: a few for each of its warps' lane groups when there are many, so that the angles'
-// forming and the block's start are spread over them; one round when that is needed to fill the SMs.
-int rows_of(int D, long long rows, int rounds) {
+// Rows of a forward block: as many rounds of its lane groups as make one wave of four blocks a SM, so
+// that the angles' forming and the ring's filling are spread over them; one round when there are few.
+int rows_of(int D, long long rows) {
   const int round = kWarps * (32 / (D / 16));
-  const long long full = rows / ((long long)kNumSMs * 6 * round);
-  return (int)(full < 1 ? 1 : full > rounds ? rounds : full) * round;
+  const long long wave = (long long)kNumSMs * 4 * round, rounds = (rows + wave - 1) / wave;
+  return (int)(rounds > 32 ? 32 : rounds) * round;
 }
 
 template <typename T, int D>
 cudaError_t forward(RopeArgs& a, cudaStream_t s) {
   const long long tokens = (long long)a.B * a.N;
-  const int rows = rows_of(D, tokens * (a.Hq + a.Hk), 6);
+  const int rows = rows_of(D, tokens * (a.Hq + (a.k_pages ? 2 : 1) * a.Hk));
   a.tokens[0] = tokens_of(a, a.Hq, rows, tokens);
   a.tokens[1] = tokens_of(a, a.Hk, rows, tokens);
   a.blocks[0] = (int)((tokens + a.tokens[0] - 1) / a.tokens[0]);
   a.blocks[1] = (int)((tokens + a.tokens[1] - 1) / a.tokens[1]);
   const unsigned blocks = a.blocks[0] + (a.k_pages ? 2 : 1) * a.blocks[1];
-  const int slot = stage_timer_begin(s, kKernQkNormRope);
+  constexpr int kSmem = kThreads * 16 * sizeof(T) * kDepth;
+  auto launch = [&](auto kernel) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    const int slot = stage_timer_begin(s, kKernQkNormRope);
+    kernel<<<blocks, kThreads, kSmem, s>>>(a);
+    e = cudaGetLastError();
+    stage_timer_end(slot, s);
+    return e;
+  };
   if (a.k_pages) {
-    if (a.interleaved) qk_norm_rope_kernel<T, D, true, true><<<blocks, kThreads, 0, s>>>(a);
-    else qk_norm_rope_kernel<T, D, true, false><<<blocks, kThreads, 0, s>>>(a);
-  } else {
-    if (a.interleaved) qk_norm_rope_kernel<T, D, false, true><<<blocks, kThreads, 0, s>>>(a);
-    else qk_norm_rope_kernel<T, D, false, false><<<blocks, kThreads, 0, s>>>(a);
+    return a.interleaved ? launch(qk_norm_rope_kernel<T, D, true, true>) : launch(qk_norm_rope_kernel<T, D, true, false>);
   }
-  const cudaError_t e = cudaGetLastError();
-  stage_timer_end(slot, s);
-  return e;
+  return a.interleaved ? launch(qk_norm_rope_kernel<T, D, false, true>) : launch(qk_norm_rope_kernel<T, D, false, false>);
 }
 
 template <typename T, int D>
 cudaError_t backward(RopeArgs& a, cudaStream_t s) {
   const long long tokens = (long long)a.B * a.N;
-  const int rows = rows_of(D, tokens * (a.Hq + a.Hk), 4);
-  a.tokens[0] = tokens_of(a, a.Hq, rows, tokens);
-  a.tokens[1] = tokens_of(a, a.Hk, rows, tokens);
-  const long long gq = (tokens + a.tokens[0] - 1) / a.tokens[0], gk = (tokens + a.tokens[1] - 1) / a.tokens[1];
-  // blocks in proportion to the kinds' rows, at most kBwdBlocks in all
-  long long bq = (long long)(kBwdBlocks - 1) * a.Hq / (a.Hq + a.Hk);
-  if (bq < 1) bq = 1;
-  a.blocks[0] = (int)(gq < bq ? gq : bq);
-  a.blocks[1] = (int)(gk < kBwdBlocks - bq ? gk : kBwdBlocks - bq);
+  // blocks in proportion to the kinds' rows; each takes one run of tokens, or several where a run's angles
+  // do not fit
+  long long most[2];
+  most[0] = (long long)(kBwdBlocks - 1) * a.Hq / (a.Hq + a.Hk);
+  if (most[0] < 1) most[0] = 1;
+  most[1] = kBwdBlocks - most[0];
+  for (int kind = 0; kind < 2; ++kind) {
+    const int H = kind ? a.Hk : a.Hq;
+    const long long per = (tokens + most[kind] - 1) / most[kind];
+    // (not under a round of the block's lane groups: a block's start costs more than its rows)
+    const long long rows = std::max(per * H, (long long)kWarps * (32 / (D / 16)));
+    a.tokens[kind] = tokens_of(a, H, rows, tokens);
+    a.blocks[kind] = (int)std::min(most[kind], (tokens + a.tokens[kind] - 1) / a.tokens[kind]);
+  }
   const unsigned blocks = a.blocks[0] + a.blocks[1];
+  constexpr int kSmem = kThreads * 32 * sizeof(T) * (sizeof(T) == 2 ? kDepth : kDepth / 2);
+  auto kernel = a.interleaved ? qk_norm_rope_bwd_kernel<T, D, true> : qk_norm_rope_bwd_kernel<T, D, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
   const int slot = stage_timer_begin(s, kKernQkNormRopeBwd);
-  if (a.interleaved) qk_norm_rope_bwd_kernel<T, D, true><<<blocks, kThreads, 0, s>>>(a);
-  else qk_norm_rope_bwd_kernel<T, D, false><<<blocks, kThreads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  kernel<<<blocks, kThreads, kSmem, s>>>(a);
+  e = cudaGetLastError();
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(D / 32, 2);
