@@ -15,15 +15,18 @@
 // once, so the walk runs in shared memory), and a pass splits the vocabulary over the cluster's 64
 // warps, each a contiguous run of 128-entry chunks (four entries a lane, 16-byte loads where rows are
 // aligned), whose sums the blocks exchange through distributed shared memory. The token is then found
-// by halving the range eightfold per step: block, warp, an eighth of its run, ... , chunk, lane, entry.
+// step by step: block, warp, an eighth of its run, ... , chunk, lane, entry.
 // A pass is bound by the latency of its loads and, over many rows, by its arithmetic (about 20
 // instructions an entry); blocks of 256 threads keep 48 rows of 131072 entries resident at once.
-// Measured: a row of 32000 entries and five drafts 17.8 -> VERIFY_CHAIN us, 48 trees of 24 nodes over
-// 131072 entries 104 -> VERIFY_TREES us against single-entry loads, float64 reductions and 512 threads.
+// Measured (V = 131072): a float32 chain of 8 in 10.3 us, 48 bfloat16 trees of 16 in 39.1 us. Steps: float64
+// reductions and scalars 17.8 / 104 us; pairs of floats in the passes, four entries a lane, asynchronous
+// copies 12.4 / 41.0 us; pairs in the walk and the search as well, the present figures. Clusters of sixteen
+// shorten a row's pass but no longer keep the rows resident: 12.4 / 50.5 us against 12.4 / 41.0. Two chunks
+// at a time spill: 11.0 / 44.1 us.
 //
 // Sums decide whole numbers, so they are carried to about 2^-46: unevaluated pairs of floats (error-free
-// sums of two floats) in lanes, warps and blocks, float64 in the scalars of the walk. Float64 throughout
-// would run at 1/64 of the float32 rate.
+// sums of two floats) throughout. Float64, at 1/64 of the float32 rate, took longer for the walk's and the
+// search's few scalars than the passes did for the vocabulary.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -37,6 +40,7 @@ constexpr int kCluster = 8;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kChunk4 = 128;   // entries of a chunk: four a lane
+constexpr int kAhead = 8;      // chunks of p and q on their way to a thread
 constexpr unsigned kAll = 0xffffffffu;
 
 __device__ __forceinline__ float above_zero(float x) { return x > 0.f ? x : 0.f; }   // nan and negatives count as 0
@@ -68,6 +72,23 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, int i, int V, floa
   }
 }
 
+// Four entries copied asynchronously to shared memory, and read from there.
+__device__ __forceinline__ void copy4(void* to, const float* from) { ptx::cp_async16_zfill(to, from, 16); }
+__device__ __forceinline__ void copy4(void* to, const __nv_bfloat16* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void read4(const float* p, bool there, float* x) {
+  const float4 v = there ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
+  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+}
+__device__ __forceinline__ void read4(const __nv_bfloat16* p, bool there, float* x) {
+  const uint2 v = there ? *reinterpret_cast<const uint2*>(p) : make_uint2(0u, 0u);
+  x[0] = __uint_as_float(v.x << 16);
+  x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+  x[2] = __uint_as_float(v.y << 16);
+  x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+}
+
 // A sum as an unevaluated pair hi + lo.
 struct Pair {
   float hi, lo;
@@ -83,12 +104,80 @@ __device__ __forceinline__ Pair add(Pair a, Pair b) {
   two_sum(a.hi, b.hi, s, e);
   return {s, __fadd_rn(__fadd_rn(a.lo, b.lo), e)};
 }
-__device__ __forceinline__ double wide(Pair a) { return (double)a.hi + (double)a.lo; }
+__device__ __forceinline__ Pair negative(Pair a) { return {-a.hi, -a.lo}; }
+__device__ __forceinline__ Pair times(float x, Pair a) {
+  const float h = __fmul_rn(x, a.hi), l = __fmaf_rn(x, a.lo, __fmaf_rn(x, a.hi, -h)), s = __fadd_rn(h, l);
+  return {s, __fadd_rn(l, -__fadd_rn(s, -h))};
+}
+// whether a > b (false where a difference is nan: an infinite b, an infinite total)
+__device__ __forceinline__ bool above(Pair a, Pair b) {
+  float s, e;
+  two_sum(a.hi, -b.hi, s, e);
+  return __fadd_rn(s, __fadd_rn(e, __fadd_rn(a.lo, -b.lo))) > 0.f;
+}
 template <int kLanes>
 __device__ __forceinline__ Pair lanes_sum(Pair v) {   // the same in every lane of the group
 #pragma unroll
   for (int m = kLanes / 2; m >= 1; m >>= 1) v = add(v, {__shfl_xor_sync(kAll, v.hi, m), __shfl_xor_sync(kAll, v.lo, m)});
   return v;
+}
+
+// Two floats in one register pair: a pass over many rows is bound by its arithmetic, which the packed
+// operations halve.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 pack(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack(F2 x, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x.v)); }
+__device__ __forceinline__ F2 add(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 sub(F2 a, F2 b) { return fma(b, pack(-1.f, -1.f), a); }   // a - b, one rounding
+// a + b as s + e exactly, and a - b
+__device__ __forceinline__ void two_sum(F2 a, F2 b, F2& s, F2& e) {
+  s = add(a, b);
+  const F2 bb = sub(s, a);
+  e = add(sub(a, sub(s, bb)), sub(b, bb));
+}
+__device__ __forceinline__ void two_diff(F2 a, F2 b, F2& s, F2& e) {
+  s = sub(a, b);
+  const F2 bb = sub(s, a);
+  e = sub(sub(a, sub(s, bb)), add(b, bb));
+}
+
+// Two sums at once.
+struct Pair2 {
+  F2 hi, lo;
+};
+__device__ __forceinline__ Pair2 add(Pair2 a, Pair2 b) {
+  F2 s, e;
+  two_sum(a.hi, b.hi, s, e);
+  return {s, add(add(a.lo, b.lo), e)};
+}
+__device__ __forceinline__ void halves(Pair2 x, Pair& a, Pair& b) {
+  unpack(x.hi, a.hi, b.hi);
+  unpack(x.lo, a.lo, b.lo);
+}
+__device__ __forceinline__ Pair both(Pair2 x) {
+  Pair a, b;
+  halves(x, a, b);
+  return add(a, b);
 }
 
 // rho of four entries: max(p - c q, 0) with c = ch + cl (q NULL or c = 0: p), or 0 for a token taken out.
@@ -99,85 +188,144 @@ struct Dist {
   float ch, cl;
   const int* gone;
   int n_gone, V;
-  __device__ __forceinline__ void of(const float* pv, const float* qv, int i, Pair* rho) const {
+  __device__ __forceinline__ void of(const float* pv, const float* qv, int i, Pair2* rho) const {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float x = above_zero(pv[e]);
-      rho[e] = {x, 0.f};
+    for (int h = 0; h < 2; ++h) {
+      const F2 x = pack(above_zero(pv[2 * h]), above_zero(pv[2 * h + 1]));
+      rho[h] = {x, {0}};
       if (q) {
-        const float y = above_zero(qv[e]);
-        const float t = __fmul_rn(ch, y), te = __fmaf_rn(cl, y, __fmaf_rn(ch, y, -t));
-        float s, r;
-        two_sum(x, -t, s, r);
-        r = __fadd_rn(r, -te);
-        const bool pos = __fadd_rn(s, r) > 0.f;
-        rho[e] = {pos ? s : 0.f, pos ? r : 0.f};
+        const F2 y = pack(above_zero(qv[2 * h]), above_zero(qv[2 * h + 1]));
+        F2 s, r;
+        if (ch == 1.f && cl == 0.f) {   // the first refusal
+          two_diff(x, y, s, r);
+        } else {
+          const F2 c = pack(ch, ch), t = mul(c, y);
+          two_diff(x, t, s, r);
+          r = sub(r, fma(pack(cl, cl), y, fma(c, y, sub({0}, t))));   // less the product's own error
+        }
+        float s0, s1, r0, r1, g0, g1;
+        unpack(add(s, r), g0, g1);
+        unpack(s, s0, s1);
+        unpack(r, r0, r1);
+        rho[h] = {pack(g0 > 0.f ? s0 : 0.f, g1 > 0.f ? s1 : 0.f), pack(g0 > 0.f ? r0 : 0.f, g1 > 0.f ? r1 : 0.f)};
       }
     }
     for (int g = 0; g < n_gone; ++g) {
       const int at = gone[g] - i;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (at == e) rho[e] = {0.f, 0.f};
+      for (int h = 0; h < 2; ++h) {
+        float s0, s1;
+        unpack(rho[h].hi, s0, s1);
+        rho[h].hi = pack(at == 2 * h ? 0.f : s0, at == 2 * h + 1 ? 0.f : s1);   // (given drafts: lo is 0)
+      }
     }
   }
-  // Sum of chunks [c0, c1), the same in every lane.
-  __device__ __forceinline__ Pair sum(int c0, int c1) const {
-    constexpr int kBatch = 4;   // chunks in flight
+  // Sum of chunks [c0, c1), the same in every lane. The latency of the loads is what a pass costs: with
+  // aligned rows each thread keeps kAhead chunks on their way into its own places of `ring`, else four in
+  // registers.
+  __device__ __forceinline__ Pair sum(int c0, int c1, uint8_t* ring) const {
     const int lane = threadIdx.x & 31;
-    Pair acc[4];
+    Pair2 acc[2] = {{{0}, {0}}, {{0}, {0}}};
+    auto take = [&](const float* pv, const float* qv, int i) {
+      Pair2 rho[2];
+      of(pv, qv, i, rho);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] = {0.f, 0.f};
-    for (int c = c0; c < c1; c += kBatch) {
-      float pv[kBatch][4], qv[kBatch][4];
+      for (int h = 0; h < 2; ++h) acc[h] = add(acc[h], rho[h]);
+    };
+    if constexpr (kVec) {
+      constexpr int kPiece = 4 * sizeof(T);   // bytes of four entries
+      uint8_t* mine = ring + threadIdx.x * kPiece;
+      auto place = [&](int slot, int of_q) { return mine + (2 * slot + of_q) * kThreads * kPiece; };
+      auto copy = [&](int c, int slot) {
+        const int i = c * kChunk4 + 4 * lane;
+        if (c < c1 && i < V) {
+          copy4(place(slot, 0), p + i);
+          if (q) copy4(place(slot, 1), q + i);
+        }
+        ptx::cp_async_commit();
+      };
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int i = c + k < c1 ? (c + k) * kChunk4 + 4 * lane : V;
-        load4<kVec>(p, i, V, pv[k]);
-        if (q) load4<kVec>(q, i, V, qv[k]);
+      for (int k = 0; k < kAhead; ++k) copy(c0 + k, k);
+      int slot = 0;
+      for (int c = c0; c < c1; ++c, slot = slot + 1 == kAhead ? 0 : slot + 1) {
+        ptx::cp_async_wait<kAhead - 1>();
+        const int i = c * kChunk4 + 4 * lane;
+        float pv[4], qv[4];
+        read4(reinterpret_cast<const T*>(place(slot, 0)), i < V, pv);
+        if (q) read4(reinterpret_cast<const T*>(place(slot, 1)), i < V, qv);
+        copy(c + kAhead, slot);
+        take(pv, qv, i);
       }
+    } else {
+      constexpr int kBatch = 4;
+      for (int c = c0; c < c1; c += kBatch) {
+        float pv[kBatch][4], qv[kBatch][4];
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        Pair rho[4];
-        of(pv[k], qv[k], c + k < c1 ? (c + k) * kChunk4 + 4 * lane : V, rho);
+        for (int k = 0; k < kBatch; ++k) {
+          const int i = c + k < c1 ? (c + k) * kChunk4 + 4 * lane : V;
+          load4<kVec>(p, i, V, pv[k]);
+          if (q) load4<kVec>(q, i, V, qv[k]);
+        }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] = add(acc[e], rho[e]);
+        for (int k = 0; k < kBatch; ++k) take(pv[k], qv[k], c + k < c1 ? (c + k) * kChunk4 + 4 * lane : V);
       }
     }
-    return lanes_sum<32>(add(add(acc[0], acc[1]), add(acc[2], acc[3])));
+    return lanes_sum<32>(both(add(acc[0], acc[1])));
+  }
+  // Sums of up to four chunks c0 .. c0 + n - 1, one by one.
+  __device__ __forceinline__ void each(int c0, int n, Pair* sums) const {
+    const int lane = threadIdx.x & 31;
+    float pv[4][4], qv[4][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = k < n ? (c0 + k) * kChunk4 + 4 * lane : V;
+      load4<kVec>(p, i, V, pv[k]);
+      if (q) load4<kVec>(q, i, V, qv[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      Pair2 rho[2];
+      of(pv[k], qv[k], k < n ? (c0 + k) * kChunk4 + 4 * lane : V, rho);
+      sums[k] = lanes_sum<32>(both(add(rho[0], rho[1])));
+    }
   }
 };
 
-// Of n <= 32 parts (lane r < n holds part r's sum), the first whose running sum passes the target; the
+// Of kParts <= 32 parts (lane r holds part r's sum), the first whose running sum passes the target; the
 // target then counts from that part's start. Where none passes (the sums agree with the whole only to
-// rounding, or u_next is not below 1) the last part that holds anything, and the target becomes
-// infinite, so that later steps do the same. -1 if every part is empty.
-__device__ __forceinline__ int pick(double v, int n, double& target) {
+// rounding, or u_next is not below 1) the last part that holds anything, and the target becomes infinite,
+// so that later steps do the same. -1 if every part is empty.
+template <int kParts>
+__device__ __forceinline__ int pick(Pair v, Pair& target) {
   const int lane = threadIdx.x & 31;
-  double incl = lane < n ? v : 0.0;
+  if (lane >= kParts) v = {0.f, 0.f};
+  const bool holds = v.hi > 0.f;
+  Pair incl = v;
 #pragma unroll
-  for (int m = 1; m < 32; m <<= 1) {
-    if (m >= n) break;
-    const double up = __shfl_up_sync(kAll, incl, m);
-    if (lane >= m) incl += up;
+  for (int m = 1; m < kParts; m <<= 1) {
+    const Pair up = {__shfl_up_sync(kAll, incl.hi, m), __shfl_up_sync(kAll, incl.lo, m)};
+    if (lane >= m) incl = add(up, incl);
   }
-  const unsigned over = __ballot_sync(kAll, lane < n && v > 0.0 && incl > target);
-  const unsigned any = __ballot_sync(kAll, lane < n && v > 0.0);
+  const unsigned over = __ballot_sync(kAll, holds && above(incl, target)), any = __ballot_sync(kAll, holds);
   if (over) {
-    const int who = __ffs(over) - 1;
-    target -= __shfl_sync(kAll, incl - v, who);
+    const int who = __ffs(over) - 1, from = who > 0 ? who - 1 : 0;
+    const Pair before = {__shfl_sync(kAll, incl.hi, from), __shfl_sync(kAll, incl.lo, from)};
+    if (who > 0) target = add(target, negative(before));
     return who;
   }
-  target = INFINITY;
+  target = {INFINITY, 0.f};
   return any ? 31 - __clz(any) : -1;
 }
+
+// Bytes before the ring: seven words a node.
+__host__ __device__ constexpr int ring_at(int N) { return (N * 28 + 15) & ~15; }
 
 struct Shared {
   Pair ctas[2][kCluster];   // totals of the cluster's blocks, by pass parity
   Pair warps[kWarps];
-  float ch, cl;
+  Pair chunks[32];
+  Pair c, target;
   int cur, n_gone, act, found, c0, c1;
-  double target;
 };
 
 template <typename T, bool kVec>
@@ -191,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCluster, 1, 1) 
   int* s_token = s_parent + a.N;
   int* s_path = s_token + a.N;
   int* s_gone = s_path + a.N;
+  uint8_t* ring = dyn + ring_at(a.N);
   const int b = blockIdx.x / kCluster, rank = (int)ptx::cluster_ctarank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n = __ldg(a.lengths + b);
@@ -201,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCluster, 1, 1) 
   const size_t row = (size_t)b * a.N;
   const T* P = static_cast<const T*>(a.p) + row * a.V;
   const T* Q = a.q ? static_cast<const T*>(a.q) + row * a.V : nullptr;
-  const double u_next = (double)__ldg(a.u_next + b);
+  const float u_next = __ldg(a.u_next + b);
   for (int i = tid + 1; i < n; i += kThreads) {
     int parent = __ldg(a.parents + row + i);
     const int t = __ldg(a.tokens + row + i);
@@ -223,54 +372,82 @@ __global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCluster, 1, 1) 
   auto first = [&](int w) { return (int)((long long)chunks * w / (kCluster * kWarps)); };
   const int run0 = first(rank * kWarps + warp), run1 = first(rank * kWarps + warp + 1);
 
-  // thread 0's walk
+  // warp 0's walk, the same in all its lanes
   int cur = 0, i = 1, count = 0, n_gone = 0, pass = 0;
-  double c = 0.0, Z = 1.0, c_new = 0.0;
+  Pair c = {0.f, 0.f}, Z = {1.f, 0.f}, c_new = {0.f, 0.f};
+  bool fresh = true;                   // (c, Z) = (0, 1)
   bool summed = false, bare = false;   // the totals at hand are the present state's; rho given up for p
-  if (tid == 0 && n > 0) s_path[count++] = 0;
+  if (warp == 0 && n > 0) {
+    if (lane == 0) s_path[0] = 0;
+    count = 1;
+  }
   enum { kRefused = 0, kSum = 1, kDone = 2 };
   if (n > 0) {
     while (true) {
-      if (tid == 0) {
+      if (warp == 0) {
         int act = -1;
-        for (; act < 0 && i < n; ++i) {
-          if (s_parent[i] != cur) continue;
-          const int t = s_token[i];
-          double here = (double)s_p[i];
-          if (Q) here = fmax(here - c * (double)s_q[i], 0.0);
-          for (int g = 0; g < n_gone; ++g)
-            if (s_gone[g] == t) here = 0.0;
-          if ((double)s_u[i] * (double)s_q[i] * Z < here) {
-            s_path[count++] = i;
+        while (act < 0 && i < n) {
+          // the next candidate: the first node from i on whose parent is cur
+          const unsigned child = __ballot_sync(kAll, i + lane < n && s_parent[min(i + lane, n - 1)] == cur);
+          if (!child) {
+            i += 32;
+            continue;
+          }
+          i += __ffs(child) - 1;
+          const float pi = s_p[i], qi = s_q[i], ui = s_u[i];
+          bool yes;
+          Pair here = {pi, 0.f};
+          if (fresh) {
+            // u q < p: the float product decides, or where it equals p its error does
+            const float uq = __fmul_rn(ui, qi);
+            yes = uq < pi || (uq == pi && __fmaf_rn(ui, qi, -uq) < 0.f);
+          } else {
+            if (Q) {
+              here = add(here, negative(times(qi, c)));
+              if (!(here.hi > 0.f)) here = {0.f, 0.f};
+            }
+            for (int g = 0; g < n_gone; ++g)
+              if (s_gone[g] == s_token[i]) here = {0.f, 0.f};
+            yes = above(here, times(ui, times(qi, Z)));
+          }
+          if (yes) {
+            if (lane == 0) s_path[count] = i;
+            ++count;
             cur = i;
-            c = 0.0;
-            Z = 1.0;
+            c = {0.f, 0.f};
+            Z = {1.f, 0.f};
+            fresh = true;
             n_gone = 0;
             summed = false;
           } else if (Q) {
-            c_new = c + Z;
+            c_new = add(c, Z);
             act = kRefused;
           } else {
-            Z -= here;
-            s_gone[n_gone++] = t;
+            Z = add(Z, negative(here));
+            fresh = false;
+            if (lane == 0) s_gone[n_gone] = s_token[i];
+            ++n_gone;
+            __syncwarp();
           }
+          ++i;
         }
         if (act < 0) {
           act = summed ? kDone : kSum;
           c_new = c;
         }
-        sh.act = act;
-        sh.cur = cur;
-        sh.n_gone = n_gone;
-        sh.ch = (float)c_new;
-        sh.cl = (float)(c_new - (double)sh.ch);
+        if (lane == 0) {
+          sh.act = act;
+          sh.cur = cur;
+          sh.n_gone = n_gone;
+          sh.c = c_new;
+        }
       }
       __syncthreads();
       const int act = sh.act;
       if (act == kDone) break;
-      const Dist<T, kVec> dist{P + (size_t)sh.cur * a.V, (Q && sh.ch != 0.f) ? Q + (size_t)sh.cur * a.V : nullptr,
-                               sh.ch, sh.cl, s_gone, sh.n_gone, a.V};
-      const Pair mine = dist.sum(run0, run1);
+      const Dist<T, kVec> dist{P + (size_t)sh.cur * a.V, (Q && sh.c.hi != 0.f) ? Q + (size_t)sh.cur * a.V : nullptr,
+                               sh.c.hi, sh.c.lo, s_gone, sh.n_gone, a.V};
+      const Pair mine = dist.sum(run0, run1, ring);
       if (lane == 0) sh.warps[warp] = mine;
       __syncthreads();
       const int par = pass & 1;
@@ -284,19 +461,21 @@ __global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCluster, 1, 1) 
       ptx::cluster_sync_all();
       ++pass;
       if (warp == 0) {
-        const double total = wide(lanes_sum<kCluster>(sh.ctas[par][lane & (kCluster - 1)]));
+        const Pair total = lanes_sum<kCluster>(sh.ctas[par][lane & (kCluster - 1)]);
         if (act == kRefused) {
-          summed = total > 0.0;
+          summed = total.hi > 0.f;
           if (summed) {
             c = c_new;
             Z = total;
+            fresh = false;
           }
-        } else if (total > 0.0 || bare) {
+        } else if (total.hi > 0.f || bare) {
           summed = true;
         } else {   // everything was taken out: the next token comes from p itself
           bare = true;
           n_gone = 0;
-          c = 0.0;
+          c = {0.f, 0.f};
+          fresh = true;
         }
       }
     }
@@ -304,10 +483,10 @@ __global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCluster, 1, 1) 
     if (warp == 0) {
       const int par = (pass - 1) & 1;
       const Pair mine = sh.ctas[par][lane & (kCluster - 1)];
-      double target = u_next * wide(lanes_sum<kCluster>(mine));
-      const int block = pick(wide(mine), kCluster, target);
+      Pair target = times(u_next, lanes_sum<kCluster>(mine));
+      const int block = pick<kCluster>(mine, target);
       int w = -1;
-      if (block == rank) w = pick(wide(sh.warps[lane & (kWarps - 1)]), kWarps, target);
+      if (block == rank) w = pick<kWarps>(sh.warps[lane & (kWarps - 1)], target);
       if (lane == 0) {
         sh.found = block == rank;
         sh.c0 = first(rank * kWarps + w);
@@ -318,20 +497,29 @@ __global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCluster, 1, 1) 
     }
     __syncthreads();
     if (sh.found) {
-      const Dist<T, kVec> dist{P + (size_t)sh.cur * a.V, (Q && sh.ch != 0.f) ? Q + (size_t)sh.cur * a.V : nullptr,
-                               sh.ch, sh.cl, s_gone, sh.n_gone, a.V};
+      const Dist<T, kVec> dist{P + (size_t)sh.cur * a.V, (Q && sh.c.hi != 0.f) ? Q + (size_t)sh.cur * a.V : nullptr,
+                               sh.c.hi, sh.c.lo, s_gone, sh.n_gone, a.V};
       int c0 = sh.c0, c1 = sh.c1;
       while (c1 - c0 > 1) {
+        // a step down: to an eighth of the range, or, where a warp has four chunks or fewer, to the chunk
         const int per = (c1 - c0 + kWarps - 1) / kWarps;
-        const Pair mine = dist.sum(min(c1, c0 + warp * per), min(c1, c0 + (warp + 1) * per));
-        if (lane == 0) sh.warps[warp] = mine;
+        const bool chunk = per <= 4;
+        const int mine0 = min(c1, c0 + warp * per), mine1 = min(c1, mine0 + per);
+        if (chunk) {
+          Pair sums[4];
+          dist.each(mine0, mine1 - mine0, sums);
+          if (lane < 4) sh.chunks[4 * warp + lane] = lane == 0 ? sums[0] : lane == 1 ? sums[1] : lane == 2 ? sums[2] : sums[3];
+        } else {
+          const Pair mine = dist.sum(mine0, mine1, ring);
+          if (lane == 0) sh.warps[warp] = mine;
+        }
         __syncthreads();
         if (warp == 0) {
-          double target = sh.target;
-          const int w = max(0, pick(wide(sh.warps[lane & (kWarps - 1)]), kWarps, target));
+          Pair target = sh.target;
+          const int w = max(0, chunk ? pick<32>(sh.chunks[lane], target) : pick<kWarps>(sh.warps[lane & (kWarps - 1)], target));
           if (lane == 0) {
-            sh.c0 = c0 + w * per;
-            sh.c1 = min(c1, c0 + (w + 1) * per);
+            sh.c0 = chunk ? c0 + (w >> 2) * per + (w & 3) : c0 + w * per;
+            sh.c1 = chunk ? sh.c0 + 1 : min(c1, c0 + (w + 1) * per);
             sh.target = target;
           }
         }
@@ -344,21 +532,23 @@ __global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCluster, 1, 1) 
         float pv[4], qv[4];
         load4<kVec>(dist.p, at, a.V, pv);
         if (dist.q) load4<kVec>(dist.q, at, a.V, qv);
+        Pair2 two[2];
+        dist.of(pv, qv, at, two);
         Pair rho[4];
-        dist.of(pv, qv, at, rho);
-        double target = sh.target;
-        const int who = max(0, pick(wide(add(add(rho[0], rho[1]), add(rho[2], rho[3]))), 32, target));
+        halves(two[0], rho[0], rho[1]);
+        halves(two[1], rho[2], rho[3]);
+        Pair target = sh.target;
+        const int who = max(0, pick<32>(add(add(rho[0], rho[1]), add(rho[2], rho[3])), target));
         if (lane == who) {
           int token = at;
           bool found = false;
-          double run = 0.0;
+          Pair run = {0.f, 0.f};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const double x = wide(rho[e]);
-            run += x;
-            if (!found && x > 0.0) {
+            run = add(run, rho[e]);
+            if (!found && rho[e].hi > 0.f) {
               token = at + e;           // the last that holds anything, unless one passes the target
-              found = run > target;
+              found = above(run, target);
             }
           }
           a.next_token[b] = token;
@@ -380,11 +570,13 @@ __global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCluster, 1, 1) 
   ptx::cluster_sync_all();   // no block leaves while another may still write to its shared memory
 }
 
-template <typename T>
-void launch(const VerifyArgs& a, bool vec, cudaStream_t s) {
-  const size_t smem = (size_t)a.N * 7 * 4;
-  if (vec) verify_kernel<T, true><<<a.B * kCluster, kThreads, smem, s>>>(a);
-  else verify_kernel<T, false><<<a.B * kCluster, kThreads, smem, s>>>(a);
+template <typename T, bool kVec>
+cudaError_t launch(const VerifyArgs& a, cudaStream_t s) {
+  const int smem = ring_at(a.N) + (kVec ? kAhead * 2 * kThreads * 4 * (int)sizeof(T) : 0);
+  const cudaError_t e = cudaFuncSetAttribute(verify_kernel<T, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  verify_kernel<T, kVec><<<a.B * kCluster, kThreads, smem, s>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -393,9 +585,8 @@ cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t s) {
   const uintptr_t quad = a.bf16 ? 8 : 16;   // bytes of four entries
   const bool vec = a.V % 4 == 0 && reinterpret_cast<uintptr_t>(a.p) % quad == 0 && reinterpret_cast<uintptr_t>(a.q) % quad == 0;
   const int slot = stage_timer_begin(s, kKernVerifyDraft);
-  if (a.bf16) launch<__nv_bfloat16>(a, vec, s);
-  else launch<float>(a, vec, s);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = a.bf16 ? (vec ? launch<__nv_bfloat16, true>(a, s) : launch<__nv_bfloat16, false>(a, s))
+                               : (vec ? launch<float, true>(a, s) : launch<float, false>(a, s));
   stage_timer_end(slot, s);
   return e;
 }
