@@ -67,9 +67,11 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const CacheArgs a) {
           have += held;
           if (held < kThreads) break;
         }
-        // entries past a gap would be lost, pages short of the context never were there
         need = pages > have ? pages - have : 0;
-        bad = have < (n + a.page - 1) / a.page;
+        bad = (long long)have * a.page < n;             // pages of the context that never were there
+        bool lost = false;                              // pages behind a gap would be overwritten
+        for (int m = have + tid; m < pages; m += kThreads) lost |= row[m] >= 0;
+        if (__syncthreads_or(lost)) bad = true;
       }
     }
   }

@@ -13,7 +13,6 @@ constexpr int kChunk = 64;   // tokens per chunk of the tensor-core path
 // Device error codes written into the sticky error word (same values as gdr_status).
 constexpr int kErrDeviceIndex = 4;
 constexpr int kErrTimeout = 5;
-constexpr int kErrNoPages = 6;
 
 // Kernel ids for the stage timer.
 enum KernelId : int {

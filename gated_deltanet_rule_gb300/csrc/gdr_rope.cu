@@ -261,7 +261,9 @@ struct Kind {
 };
 
 // Normed, turned and written (kPages: keys into the pages, values copied there). HBM-bound: each element
-// is read and written once; every lane has kDepth rows in flight in shared memory (ROPE_ROW).
+// is read and written once; every lane has kDepth rows in flight in shared memory. Measured: 8192 tokens of
+// 32 + 8 heads of 128, bfloat16: 34.0 us, 73% of the copy bandwidth (37.6 us with the rows loaded into
+// registers and lanes 32 bytes apart).
 template <typename T, int D, bool kPages, bool kInter>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a) {
   constexpr int kRun = 8 * sizeof(T) / 16, kPieces = 2 * kRun;   // 16-byte pieces of a run, of a lane's row
@@ -370,7 +372,7 @@ constexpr int kBwdBlocks = kNumSMs * 2;   // blocks of the gradient (one wave), 
 // As the forward, but a block walks several groups of tokens of one kind and keeps the weight gradients
 // of a lane's sixteen elements in registers over all of them; it adds its lanes in a fixed order and
 // writes one row of partial sums, which the second kernel adds in order: no atomics, the same bits every
-// time.
+// time. Measured: 3 x 2731 tokens of 16 + 2 heads of 256, bfloat16: 67.7 us, 66% of the copy bandwidth.
 template <typename T, int D, bool kInter>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeArgs a) {
   constexpr int kRun = 8 * sizeof(T) / 16;            // 16-byte pieces of a run; a lane's row has four runs

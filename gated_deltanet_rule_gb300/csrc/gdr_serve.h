@@ -22,6 +22,7 @@ constexpr int kKernCacheAlloc = 14;
 constexpr int kKernCacheCopy = 15;
 
 constexpr int kNumSMs = 152;   // GB300
+constexpr int kErrNoPages = 6;   // device error code (gdr_status): a cache had too few free pages
 
 // RMS norm of every query and key head and the rotation by position. The three entry points share
 // these arguments: dense outputs (k_out set), keys and values into pages (k_pages set), gradient

@@ -81,6 +81,19 @@ def test_reserve():
         _same(pool, d)
 
 
+def test_reserve_refuses_a_gap():
+    """A page behind an empty entry would be overwritten: the row is left alone, the others are served."""
+    pool, d = _pool([40, 20], 2, 8, 16)
+    d[2][0, 5] = 0   # (row 0 holds entries 0 .. 2)
+    want = d[2].clone()
+    with pytest.raises(gdr.GdrError) as e:
+        gdr.gdr_cache_reserve(*d[2:], _i([0, 1]), 60, 16)
+        gdr.gdr_sync_status()
+    assert e.value.status == gdr.GDR_ERR_DEVICE_INDEX
+    pool.reserve([1], 60)
+    assert d[2][0].tolist() == want[0].tolist() and d[2][1].tolist() == pool.table[1]
+
+
 def test_many_rows_and_pages():
     """More rows than one block's threads, more pages than one pass of the search."""
     F = 1500
