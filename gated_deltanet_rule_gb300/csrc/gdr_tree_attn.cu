@@ -14,7 +14,7 @@
 //   kWide   D <= 128 and more than 128 rows a key head: two M tiles an item, one a warpgroup; both read the
 //           same key/value tiles, the products of one run under the softmax of the other. (Tiles of 64
 //           positions with two S buffers a stream, so that S is always there in time, were slower, 119
-//           against 98 us for 8 trees of 64 nodes over 16384 positions: products of N = 64 are bound by
+//           against 98 us then for 8 trees of 64 nodes over 16384 positions: products of N = 64 are bound by
 //           reading Q from shared memory, and every product costs two waits.)
 //   kNarrow D <= 128, up to 128 rows: one M tile, the warpgroups take every other key tile, each with
 //           its own accumulator, maximum and sum, joined at the end of the segment.
@@ -27,7 +27,8 @@
 //
 // Work split: all (row, key head, M tile or pair of them) items laid end to end are (sum of their key tiles) units; block
 // c of C takes units [c U / C, (c + 1) U / C), so every SM reads the same number of tiles whatever the
-// rows' lengths. An item cut across blocks leaves its parts (O / l and lse in float32) in the workspace
+// rows' lengths, but for an item's start and end (queries loaded, the softmax drained, results written),
+// which count as kPad tiles. An item cut across blocks leaves its parts (O / l and lse in float32) in the workspace
 // and a second kernel joins them in order.
 //
 // The running maximum is kept as a reference that moves only when the maximum has grown by more than 8
@@ -57,6 +58,9 @@ constexpr int kThreads = 384;   // warps: 0 loads, 1 products, 2-3 idle, 4-11 so
 constexpr int kBlocks = kNumSMs;
 constexpr int kM = 128;         // rows of an M tile
 constexpr float kLog2e = 1.4426950408889634f;
+// Units that an item's start and end count for (16 rows of 13 nodes: 77.3 us with 0, 75.8 with 3; 8 of 64
+// nodes over 16384 positions: 100.1 and 95.6; 2 and 4 are within 1% of 3).
+constexpr int kPad = 3;
 constexpr long long kDrainBudget = 2000000000ll;   // cycles an aborting block waits for its own work
 
 enum Form { kSplit = 0, kNarrow = 1, kWide = 2 };
@@ -115,6 +119,7 @@ struct Bars {
   // the block's first unit, found by the thread whose rows hold it
   int b0, hk0, mt0, t0;
   long long todo, x0, total;
+  int later;           // that unit begins an item after the share's first unit
 };
 static_assert(sizeof(Bars) <= 512, "barriers fit their region");
 
@@ -134,14 +139,14 @@ __device__ __forceinline__ int tiles_of(const Args& a, int n, int ctx, int mt) {
   const int nodes = a.mask ? n : min(n, (mt + 1) * a.npi);
   return (ctx + nodes + KT - 1) / KT;
 }
-// Units of one key head of a row.
+// Units of one key head of a row: its items' key tiles, and kPad for each item's start and end.
 template <int KT>
 __device__ __forceinline__ long long units_of(const Args& a, int n, int ctx) {
   if (n == 0) return 0;
   const int mts = (n + a.npi - 1) / a.npi;
-  if (a.mask || mts == 1) return (long long)mts * tiles_of<KT>(a, n, ctx, mts - 1);
+  if (a.mask || mts == 1) return (long long)mts * (tiles_of<KT>(a, n, ctx, mts - 1) + kPad);
   long long u = 0;
-  for (int mt = 0; mt < mts; ++mt) u += tiles_of<KT>(a, n, ctx, mt);
+  for (int mt = 0; mt < mts; ++mt) u += tiles_of<KT>(a, n, ctx, mt) + kPad;
   return u;
 }
 __device__ __forceinline__ long long first_unit(long long total, int c) { return total * c / kBlocks; }
@@ -153,14 +158,28 @@ __device__ __forceinline__ int block_of(long long total, long long x) {
   return c;
 }
 
+// The item after one; units are left, so there is one.
+__device__ __forceinline__ void next_item(const Args& a, int& b, int& hk, int& mt, int& n, int& ctx) {
+  if (++mt * a.npi < n) return;
+  mt = 0;
+  if (++hk < a.Hk) return;
+  hk = 0;
+  do {
+    ++b;
+    row_of(a, b, n, ctx);
+  } while (n == 0);
+}
+
 // Walks the block's segments: a run of key tiles [t0, t1) of one item.
 template <int KT>
 struct Walk {
   int b, hk, mt, t0, t1, tiles, n, ctx, index;
-  long long todo;
+  long long todo;   // units left (not positive: none)
+  long long unit;   // the item's first unit
   __device__ __forceinline__ void start(const Args& a, const Bars& s) {
     b = s.b0; hk = s.hk0; mt = s.mt0; t1 = s.t0;
     todo = s.todo;
+    unit = s.x0 - t1;
     index = -1;
     if (todo > 0) {
       row_of(a, b, n, ctx);
@@ -171,21 +190,13 @@ struct Walk {
     if (todo <= 0) return false;
     if (index >= 0) {   // the last segment ended its item
       t1 = 0;
-      if (++mt * a.npi >= n) {
-        mt = 0;
-        if (++hk == a.Hk) {
-          hk = 0;
-          do {
-            ++b;
-            row_of(a, b, n, ctx);
-          } while (n == 0);   // units are left, so a row with nodes is
-        }
-      }
+      unit += tiles + kPad;
+      next_item(a, b, hk, mt, n, ctx);
       tiles = tiles_of<KT>(a, n, ctx, mt);
     }
     t0 = t1;
     t1 = (int)min((long long)tiles, t0 + todo);
-    todo -= t1 - t0;
+    todo -= t1 - t0 + (t1 == tiles ? kPad : 0);
     ++index;
     return true;
   }
@@ -503,14 +514,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!row_of(a, b, n, ctx) && blockIdx.x == 0) atomicCAS(a.err, 0, kErrDeviceIndex);
       mine += units_of<KT>(a, n, ctx) * a.Hk;
     }
+    if (tid == 0) s.todo = 0;
     long long before;
     const long long total = block_sum(mine, reinterpret_cast<long long*>(red), before);
     const long long x0 = first_unit(total, blockIdx.x), x1 = first_unit(total, blockIdx.x + 1);
-    if (tid == 0) {
-      s.todo = x1 - x0;
-      s.x0 = x0;
-      s.total = total;
-    }
+    if (tid == 0) s.total = total;
     if (x1 > x0 && x0 >= before && x0 < before + mine) {
       long long at = x0 - before;
       for (int b = r0; b < r1; ++b) {
@@ -521,11 +529,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           at -= head * a.Hk;
           continue;
         }
+        int hk = (int)(at / head), mt = 0;
+        at -= hk * head;
+        while (at >= tiles_of<KT>(a, n, ctx, mt) + kPad) at -= tiles_of<KT>(a, n, ctx, mt++) + kPad;
+        const long long skip = tiles_of<KT>(a, n, ctx, mt) + kPad - at;
+        const bool later = skip <= kPad;   // behind the item's last tile
+        if (later && x1 - x0 > skip) {
+          next_item(a, b, hk, mt, n, ctx);
+          at = 0;
+        }
+        s.todo = later ? x1 - x0 - skip : x1 - x0;
+        s.x0 = later ? x0 + skip : x0;
+        s.later = later;
         s.b0 = b;
-        s.hk0 = (int)(at / head);
-        at -= s.hk0 * head;
-        int mt = 0;
-        while (at >= tiles_of<KT>(a, n, ctx, mt)) at -= tiles_of<KT>(a, n, ctx, mt++);
+        s.hk0 = hk;
         s.mt0 = mt;
         s.t0 = (int)at;
         break;
@@ -662,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int T = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0);
       const bool first = __shfl_sync(0xffffffffu, w.index, 0) == 0;
       const uint32_t o_parity = __shfl_sync(0xffffffffu, (uint32_t)(w.index - 1) & 1, 0);
-      const int streams = kForm == kWide ? __shfl_sync(0xffffffffu, w.m_tiles(a), 0) : kForm == kNarrow ? 2 : 1;
+      const int streams = __shfl_sync(0xffffffffu, w.m_tiles(a), 0);   // (kWide)
       if constexpr (kForm == kSplit) {
         // S of tile j + 1, then P V of tile j
         bool k_there = false, v_there = false;
@@ -687,38 +704,59 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
         }
-      } else {
+      } else if constexpr (kForm == kWide) {
         // one buffer a stream: S of a stream's next tile goes over P of its last one, once that product is
-        // done; the streams take turns (kNarrow: tiles st, st + 2, ...; kWide: every tile)
-        constexpr int kStep = kForm == kNarrow ? 2 : 1;
-        bool k_there = false, v_there = false, p_there = false;
-        for (int k = 0; k <= (T + kStep - 1) / kStep; ++k) {
+        // done; the streams take turns. What a product needs is waited for while the one before it runs.
+        for (int k = 0; k <= T; ++k) {
 #pragma unroll
           for (int st = 0; st < 2; ++st) {
             if (st >= streams) break;
-            const int j = kForm == kNarrow ? 2 * k + st : k;
-            const bool last = kForm == kNarrow || st == streams - 1;
-            const bool own_tile = kForm == kNarrow || st == 0;     // (kWide: the first stream waits for both)
-            if (k > 0 && j - kStep < T) {
+            const bool last = st == streams - 1;
+            if (k > 0) {
               if (k == 1 && st == 0 && !first) wait(&s.o_free, o_parity);
-              if (own_tile && !v_there) wait(&s.full[vr.slot], vr.parity);
-              if (!p_there) wait(&s.p_full[st], (steps[st] - 1) & 1);
-              k_there = own_tile && j < T && early(&s.full[kr.slot], kr.parity);
+              wait(&s.p_full[st], (steps[st] - 1) & 1);
               outputs(st, st, vr.slot, k > 1, last);
               if (last) vr.step(2);
             }
-            v_there = p_there = false;
-            if (j < T) {
-              if (own_tile && !k_there) wait(&s.full[kr.slot], kr.parity);
+            if (k < T) {
+              if (st == 0) wait(&s.full[kr.slot], kr.parity);
+              if (last) wait(&s.full[vr.slot], vr.parity);
               if (steps[st] > 0) wait(&s.pv[st], (steps[st] - 1) & 1);
-              // the products after these: P V of the other stream's last tile (streams == 1: of this one's)
-              const int next = streams == 1 ? 0 : st ^ 1;
-              const int next_j = kForm == kNarrow ? j - 1 : st == streams - 1 ? k : k - 1;
-              if (next != st && next_j >= 0) p_there = early(&s.p_full[next], (steps[next] - 1) & 1);
-              if (next_j >= 0 && (kForm == kNarrow || next == 0)) v_there = early(&s.full[vr.slot], vr.parity);
-              scores(st, kForm == kWide ? st : 0, kr.slot, last, j == T - 1 && last);
+              scores(st, st, kr.slot, last, k == T - 1 && last);
               ++steps[st];
               if (last) kr.step(2);
+            }
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
+      } else {
+        // the same with tiles st, st + 2, ... of one M tile; here K and V are what is waited for, so what the
+        // next products need is asked for without waiting before these are issued
+        bool k_there = false, v_there = false, p_there = false;
+        for (int k = 0; k <= (T + 1) / 2; ++k) {
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            const int j = 2 * k + st;
+            if (k > 0 && j - 2 < T) {
+              if (k == 1 && st == 0 && !first) wait(&s.o_free, o_parity);
+              if (!v_there) wait(&s.full[vr.slot], vr.parity);
+              if (!p_there) wait(&s.p_full[st], (steps[st] - 1) & 1);
+              k_there = j < T && early(&s.full[kr.slot], kr.parity);
+              outputs(st, st, vr.slot, k > 1, true);
+              vr.step(2);
+            }
+            v_there = p_there = false;
+            if (j < T) {
+              if (!k_there) wait(&s.full[kr.slot], kr.parity);
+              if (steps[st] > 0) wait(&s.pv[st], (steps[st] - 1) & 1);
+              if (j > 0) {   // the products after these: P V of the other stream's last tile
+                p_there = early(&s.p_full[st ^ 1], (steps[st ^ 1] - 1) & 1);
+                v_there = early(&s.full[vr.slot], vr.parity);
+              }
+              scores(st, 0, kr.slot, true, j == T - 1);
+              ++steps[st];
+              kr.step(2);
             }
             k_there = false;
           }
@@ -731,6 +769,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lead) mma_commit(&s.drain);
     warp_wait(&s.drain, 0, kDrainBudget);
     } else {
+      // ------------------------------------------------------------------------------ notes for the join
+      if (warp == 3) {
+        Walk<KT> w;
+        w.start(a, s);
+        const bool by_item = a.items <= kBlocks;
+        bool noted = false;          // (by block: an item that is cut begins in its last segment)
+        while (w.next(a)) {
+          if (w.t0 > 0) continue;
+          const bool cut = w.t1 < w.tiles;
+          if (!by_item && !cut) continue;
+          noted = true;
+          const int item = (w.b * a.Hk + w.hk) * a.mts + w.mt;
+          if (lane == 0)
+            a.cuts[by_item ? item : blockIdx.x] = Cut{s.total, w.unit, item, (int)blockIdx.x,
+                                                      cut ? block_of(s.total, w.unit + w.tiles - 1) : -1, 0};
+        }
+        if (lane == 0 && !by_item && !noted) a.cuts[blockIdx.x] = Cut{0, 0, -1, 0, -1, 0};
+      }
       // ------------------------------------------------------------------------------ absent nodes: 0, -inf
       const int vecs = a.Hq * D / 8;
       for (int x = 2 * blockIdx.x + warp - 2; x < a.B * a.N; x += 2 * kBlocks) {
@@ -754,19 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t rows_at = tb + ((uint32_t)(32 * quarter) << 16);
     const int wtid = tid - 128;
     long long g = 0, step = 0;   // tiles of the segments before, tiles of this stream so far
-    const bool by_item = a.items <= kBlocks;
-    bool noted = false;          // (by block: an item that is cut begins in its last segment)
     while (w.next(a)) {
-      if (wtid == 0 && w.t0 == 0) {
-        const bool cut = w.t1 < w.tiles;
-        const int item = (w.b * a.Hk + w.hk) * a.mts + w.mt;
-        if (by_item || cut) {
-          const long long unit = s.x0 + g;
-          a.cuts[by_item ? item : blockIdx.x] = Cut{s.total, unit, item, (int)blockIdx.x,
-                                                    cut ? block_of(s.total, unit + w.tiles - 1) : -1, 0};
-          noted = true;
-        }
-      }
       const int m = kForm == kWide ? st : 0;                     // M tile of the item
       const int node0 = w.mt * a.npi + m * a.npt;
       const int used = max(0, min(a.npt, w.n - node0)) * a.G;
@@ -905,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float lse = sees ? m_ref * a.sl2 * (1.f / kLog2e) + logf(l) : -INFINITY;
       const bool whole = w.t0 == 0 && w.t1 == w.tiles;
       const size_t orow = ((size_t)w.b * a.N + i) * a.Hq + w.hk * a.G + hg;
-      const size_t prow = (size_t)(2 * blockIdx.x + (w.index > 0)) * C::kRows + m * kM + row;
+      const size_t prow = (size_t)(2 * blockIdx.x + (w.index > 0 || s.later)) * C::kRows + m * kM + row;
       constexpr int kOut = kForm == kWide ? D : D / 2;           // this thread's output columns
       const int d0 = kForm == kWide ? 0 : st * (D / 2);
       if (active && ok) {
@@ -955,7 +999,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       g += T;
     }
-    if (wtid == 0 && !by_item && !noted) a.cuts[blockIdx.x] = Cut{0, 0, -1, 0, -1, 0};
   }
   if (!ok && lane == 0) atomicCAS(a.err, 0, kErrTimeout);
   __syncwarp();
