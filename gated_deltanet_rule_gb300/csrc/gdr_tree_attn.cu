@@ -65,14 +65,6 @@ constexpr long long kDrainBudget = 2000000000ll;   // cycles an aborting block w
 
 enum Form { kSplit = 0, kNarrow = 1, kWide = 2 };
 
-// Where an item's parts are: blocks first .. last (last < first: the item is whole), and the number of
-// units in all, from which each block's share follows.
-struct Cut {
-  long long total;
-  long long unit;   // the item's first unit
-  int item, first, last, pad;
-};
-
 struct Args {
   const int32_t* table;
   const int32_t* ctx;
@@ -84,7 +76,6 @@ struct Args {
   float* lse;
   float* part_o;             // [2 C][rows of an item][D]
   float* part_lse;           // [2 C][rows of an item]
-  Cut* cuts;                 // [C]: by item where there are at most C, else by the block that begins it
   int items;                 // B Hk mts
   int mts;                   // items of a row and key head, N nodes' worth
   int B, N, Hq, Hk, G, W, P, page, page_shift, M;
@@ -118,7 +109,7 @@ struct Bars {
   int bad[3];          // a cleaned node element was not finite, by segment modulo three
   // the block's first unit, found by the thread whose rows hold it
   int b0, hk0, mt0, t0;
-  long long todo, x0, total;
+  long long todo;
   int later;           // that unit begins an item after the share's first unit
 };
 static_assert(sizeof(Bars) <= 512, "barriers fit their region");
@@ -175,11 +166,9 @@ template <int KT>
 struct Walk {
   int b, hk, mt, t0, t1, tiles, n, ctx, index;
   long long todo;   // units left (not positive: none)
-  long long unit;   // the item's first unit
   __device__ __forceinline__ void start(const Args& a, const Bars& s) {
     b = s.b0; hk = s.hk0; mt = s.mt0; t1 = s.t0;
     todo = s.todo;
-    unit = s.x0 - t1;
     index = -1;
     if (todo > 0) {
       row_of(a, b, n, ctx);
@@ -190,7 +179,6 @@ struct Walk {
     if (todo <= 0) return false;
     if (index >= 0) {   // the last segment ended its item
       t1 = 0;
-      unit += tiles + kPad;
       next_item(a, b, hk, mt, n, ctx);
       tiles = tiles_of<KT>(a, n, ctx, mt);
     }
@@ -281,6 +269,50 @@ __device__ __forceinline__ long long block_sum(long long v, long long* warps, lo
     total += warps[w];
   }
   return total;
+}
+
+// The units of a thread's rows [r0, r1), of those before them, and of all (the block's threads share the rows).
+struct Rows {
+  int r0, r1;
+  long long mine, before, total;
+};
+template <int KT>
+__device__ __forceinline__ Rows count_rows(const Args& a, long long* warps, bool report) {
+  const int per = (a.B + (int)blockDim.x - 1) / (int)blockDim.x;
+  Rows r;
+  r.r0 = min(a.B, (int)threadIdx.x * per);
+  r.r1 = min(a.B, r.r0 + per);
+  r.mine = 0;
+  for (int b = r.r0; b < r.r1; ++b) {
+    int n, ctx;
+    if (!row_of(a, b, n, ctx) && report) atomicCAS(a.err, 0, kErrDeviceIndex);
+    r.mine += units_of<KT>(a, n, ctx) * a.Hk;
+  }
+  r.total = block_sum(r.mine, warps, r.before);
+  return r;
+}
+// An item (row, key head, M tiles), and a unit's place in it.
+struct Place {
+  int b, hk, mt, n, ctx, tiles, unit;
+};
+// The place of unit x < total: true in the one thread that holds its row.
+template <int KT>
+__device__ __forceinline__ bool locate(const Args& a, const Rows& r, long long x, Place& p) {
+  if (x < r.before || x >= r.before + r.mine) return false;
+  long long at = x - r.before;
+  for (p.b = r.r0;; ++p.b) {
+    row_of(a, p.b, p.n, p.ctx);
+    const long long head = units_of<KT>(a, p.n, p.ctx);
+    if (at >= head * a.Hk) {
+      at -= head * a.Hk;
+      continue;
+    }
+    p.hk = (int)(at / head);
+    at -= p.hk * head;
+    for (p.mt = 0; at >= (p.tiles = tiles_of<KT>(a, p.n, p.ctx, p.mt)) + kPad; ++p.mt) at -= p.tiles + kPad;
+    p.unit = (int)at;
+    return true;
+  }
 }
 
 // Bits k = 0 .. 63: position pos0 + k is seen by node i (rel = pos0 - ctx).
@@ -507,46 +539,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_alloc(&s.tmem, 512);
   // the block's share of the units
   {
-    const int per = (a.B + kThreads - 1) / kThreads, r0 = min(a.B, tid * per), r1 = min(a.B, r0 + per);
-    long long mine = 0;
-    for (int b = r0; b < r1; ++b) {
-      int n, ctx;
-      if (!row_of(a, b, n, ctx) && blockIdx.x == 0) atomicCAS(a.err, 0, kErrDeviceIndex);
-      mine += units_of<KT>(a, n, ctx) * a.Hk;
-    }
     if (tid == 0) s.todo = 0;
-    long long before;
-    const long long total = block_sum(mine, reinterpret_cast<long long*>(red), before);
-    const long long x0 = first_unit(total, blockIdx.x), x1 = first_unit(total, blockIdx.x + 1);
-    if (tid == 0) s.total = total;
-    if (x1 > x0 && x0 >= before && x0 < before + mine) {
-      long long at = x0 - before;
-      for (int b = r0; b < r1; ++b) {
-        int n, ctx;
-        row_of(a, b, n, ctx);
-        const long long head = units_of<KT>(a, n, ctx);
-        if (at >= head * a.Hk) {
-          at -= head * a.Hk;
-          continue;
-        }
-        int hk = (int)(at / head), mt = 0;
-        at -= hk * head;
-        while (at >= tiles_of<KT>(a, n, ctx, mt) + kPad) at -= tiles_of<KT>(a, n, ctx, mt++) + kPad;
-        const long long skip = tiles_of<KT>(a, n, ctx, mt) + kPad - at;
-        const bool later = skip <= kPad;   // behind the item's last tile
-        if (later && x1 - x0 > skip) {
-          next_item(a, b, hk, mt, n, ctx);
-          at = 0;
-        }
-        s.todo = later ? x1 - x0 - skip : x1 - x0;
-        s.x0 = later ? x0 + skip : x0;
-        s.later = later;
-        s.b0 = b;
-        s.hk0 = hk;
-        s.mt0 = mt;
-        s.t0 = (int)at;
-        break;
+    const Rows rows = count_rows<KT>(a, reinterpret_cast<long long*>(red), blockIdx.x == 0);
+    const long long x0 = first_unit(rows.total, blockIdx.x), x1 = first_unit(rows.total, blockIdx.x + 1);
+    Place at;
+    if (x1 > x0 && locate<KT>(a, rows, x0, at)) {
+      const int skip = at.tiles + kPad - at.unit;
+      const bool later = skip <= kPad;   // behind the item's last tile
+      if (later && x1 - x0 > skip) {
+        next_item(a, at.b, at.hk, at.mt, at.n, at.ctx);
+        at.unit = 0;
       }
+      s.todo = later ? x1 - x0 - skip : x1 - x0;
+      s.later = later;
+      s.b0 = at.b;
+      s.hk0 = at.hk;
+      s.mt0 = at.mt;
+      s.t0 = at.unit;
     }
   }
   tc_fence_before();
@@ -769,24 +778,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lead) mma_commit(&s.drain);
     warp_wait(&s.drain, 0, kDrainBudget);
     } else {
-      // ------------------------------------------------------------------------------ notes for the join
-      if (warp == 3) {
-        Walk<KT> w;
-        w.start(a, s);
-        const bool by_item = a.items <= kBlocks;
-        bool noted = false;          // (by block: an item that is cut begins in its last segment)
-        while (w.next(a)) {
-          if (w.t0 > 0) continue;
-          const bool cut = w.t1 < w.tiles;
-          if (!by_item && !cut) continue;
-          noted = true;
-          const int item = (w.b * a.Hk + w.hk) * a.mts + w.mt;
-          if (lane == 0)
-            a.cuts[by_item ? item : blockIdx.x] = Cut{s.total, w.unit, item, (int)blockIdx.x,
-                                                      cut ? block_of(s.total, w.unit + w.tiles - 1) : -1, 0};
-        }
-        if (lane == 0 && !by_item && !noted) a.cuts[blockIdx.x] = Cut{0, 0, -1, 0, -1, 0};
-      }
       // ------------------------------------------------------------------------------ absent nodes: 0, -inf
       const int vecs = a.Hq * D / 8;
       for (int x = 2 * blockIdx.x + warp - 2; x < a.B * a.N; x += 2 * kBlocks) {
@@ -1011,39 +1002,71 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of items that several blocks shared: o = sum_s e^(lse_s - lse) o_s over a row's parts.
-// Grid (item, or block that begins one; share of the item's rows). An item in eight parts or more (few
+// Grid (item, or block that begins one; share of the item's rows). What follows from the rows' lengths is
+// worked out before the first kernel has ended, and the first parts are read while their greatest lse is
+// found: only the parts' reading and the sum are left to wait for (both together: 86.1 -> 81.6 us for 2 rows of 131072
+// positions, 16.4 -> 14.4 us for one token). An item in eight parts or more (few
 // items, each cut over many blocks) has the block's eight warps share a row, warp w taking parts w, w + 8,
 // ... and the block adding the warps' sums in order; otherwise a warp takes a row. Parts are read four at a
 // time: the loop is bound by their latency (38 parts of 224 rows of 256: 33 us by one warp a row, one part
 // after the other).
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
-template <int D, int kRows>
+template <int D, int kRows, int KT>
 __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const __grid_constant__ Args a) {
   constexpr int kVec = D / 32;
   __shared__ float s_acc[kJoinWarps][D];
   __shared__ float s_sum[kJoinWarps];
   __shared__ int s_part[kBlocks];
+  __shared__ long long s_warps[kJoinWarps], s_unit;
+  __shared__ Place s_item;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  wait_prerequisite();
-  int n = 1, ctx, item = blockIdx.x;
-  if (a.items <= kBlocks) row_of(a, item / (a.Hk * a.mts), n, ctx);   // an item without nodes has no note
-  if (a.items <= kBlocks && item % a.mts * a.npi >= n) return;
-  const Cut cut = a.cuts[blockIdx.x];
-  // (the bounds hold for every note the first kernel writes; one that gave up at its start wrote none)
-  if (cut.last <= cut.first || cut.first < 0 || cut.last >= kBlocks || cut.item < 0 || cut.item >= a.items) return;
-  item = cut.item;
-  const int b = item / (a.Hk * a.mts), hk = item / a.mts % a.Hk, mt = item % a.mts;
-  row_of(a, b, n, ctx);
+  // the item, and the blocks that hold its parts: from the rows alone, before the first kernel has ended
+  if (tid == 0) s_item.tiles = 0;
+  const Rows rows = count_rows<KT>(a, s_warps, false);
+  Place p;
+  if (a.items <= kBlocks) {   // a block of the grid for each item
+    p.b = blockIdx.x / (a.Hk * a.mts);
+    if (p.b >= rows.r0 && p.b < rows.r1) {
+      p.hk = blockIdx.x / a.mts % a.Hk;
+      p.mt = blockIdx.x % a.mts;
+      s_unit = rows.before;
+      for (int b = rows.r0; b < p.b; ++b) {
+        row_of(a, b, p.n, p.ctx);
+        s_unit += units_of<KT>(a, p.n, p.ctx) * a.Hk;
+      }
+      row_of(a, p.b, p.n, p.ctx);
+      if (p.mt * a.npi < p.n) {
+        s_unit += units_of<KT>(a, p.n, p.ctx) * p.hk;
+        for (int mt = 0; mt < p.mt; ++mt) s_unit += tiles_of<KT>(a, p.n, p.ctx, mt) + kPad;
+        p.tiles = tiles_of<KT>(a, p.n, p.ctx, p.mt);
+        s_item = p;
+      }
+    }
+  } else {                    // for each block of the first kernel: the item that its share's last unit lies in
+    const long long x0 = first_unit(rows.total, blockIdx.x), x1 = first_unit(rows.total, blockIdx.x + 1);
+    if (x1 > x0 && locate<KT>(a, rows, x1 - 1, p) && x1 - 1 - p.unit >= x0 && p.unit < p.tiles) {
+      s_unit = x1 - 1 - p.unit;
+      s_item = p;
+    }
+  }
+  __syncthreads();
+  p = s_item;
+  const bool begins = p.tiles > 0;
+  const long long unit = begins ? s_unit : 0;
+  const int first = begins ? block_of(rows.total, unit) : 0, last = begins ? block_of(rows.total, unit + p.tiles - 1) : 0;
+  const int b = p.b, hk = p.hk, mt = p.mt, n = p.n;
   const int node0 = mt * a.npi, nodes = min(a.npi, n - node0);
   // the parts' places, block by block (-1: a block without units). A block's first segment is its part 0:
   // the first block's only where the item begins its share
-  const int parts = cut.last - cut.first + 1;
+  const int parts = last - first + 1;
   if (tid < parts) {
-    const int c = cut.first + tid;
-    const long long at = first_unit(cut.total, c);
-    s_part[tid] = at < first_unit(cut.total, c + 1) ? (2 * c + (at < cut.unit)) * kRows : -1;
+    const int c = first + tid;
+    const long long at = first_unit(rows.total, c);
+    s_part[tid] = at < first_unit(rows.total, c + 1) ? (2 * c + (at < unit)) * kRows : -1;
   }
   __syncthreads();
+  wait_prerequisite();         // (in every block: this grid must not end before the first one)
+  if (last == first) return;   // whole
   const bool share = parts >= kJoinWarps;
   const int step = share ? kJoinWarps : 1;   // a warp's parts
   for (int rr = share ? blockIdx.y : blockIdx.y * kJoinWarps + warp; rr < nodes * a.G; rr += gridDim.y * (share ? 1 : kJoinWarps)) {
@@ -1054,17 +1077,10 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const __gr
     bool nan = false;
 #pragma unroll
     for (int e = 0; e < kVec; ++e) acc[e] = 0.f;
-    for (int c = lane; c < parts; c += 32) {
-      const float x = s_part[c] >= 0 ? a.part_lse[s_part[c] + row] : -INFINITY;
-      nan |= x != x;
-      top = fmaxf(top, x);
-    }
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    nan = __any_sync(0xffffffffu, nan);
-    const float ref = top == -INFINITY ? 0.f : top;
-    for (int cc = share ? warp : 0; cc < parts; cc += 4 * step) {
-      float w[4], x[4][kVec];
+    // four parts at once, the first of them while their greatest lse is found
+    const int c0 = share ? warp : 0;
+    float w[4], x[4][kVec];
+    auto load = [&](int cc) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int c = cc + u * step, at = c < parts ? s_part[c] : -1;
@@ -1078,6 +1094,18 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const __gr
           x[u][e + 1] = y.y;
         }
       }
+    };
+    load(c0);
+    for (int c = lane; c < parts; c += 32) {
+      const float lse = s_part[c] >= 0 ? a.part_lse[s_part[c] + row] : -INFINITY;
+      nan |= lse != lse;
+      top = fmaxf(top, lse);
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    nan = __any_sync(0xffffffffu, nan);
+    const float ref = top == -INFINITY ? 0.f : top;
+    for (int cc = c0; cc < parts;) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const float f = ex2_approx((w[u] - ref) * kLog2e);
@@ -1087,6 +1115,8 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const __gr
           for (int e = 0; e < kVec; ++e) acc[e] = fmaf(f, x[u][e], acc[e]);
         }
       }
+      cc += 4 * step;
+      if (cc < parts) load(cc);
     }
     if (share) {   // (the same in every warp, and so is the row)
       __syncthreads();   // the row before has been read
@@ -1165,7 +1195,6 @@ cudaError_t launch(const TreeAttnArgs& p, cudaStream_t st) {
   a.page_shift = __builtin_ctz((unsigned)p.page);
   a.mts = (p.N + a.npi - 1) / a.npi;
   a.items = p.B * p.Hk * a.mts;
-  a.cuts = reinterpret_cast<Cut*>(a.part_lse + (size_t)2 * kBlocks * C::kRows);
   a.budget = wait_budget_cycles();
   a.err = p.err;
   cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D, kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
@@ -1186,7 +1215,7 @@ cudaError_t launch(const TreeAttnArgs& p, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   slot = stage_timer_begin(st, kKernTreeAttnJoin);
-  e = cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D, C::kRows>, a);
+  e = cudaLaunchKernelEx(&cfg, tree_attn_join_kernel<D, C::kRows, C::KT>, a);
   stage_timer_end(slot, st);
   return e;
 }
@@ -1201,7 +1230,7 @@ cudaError_t launch_two(const TreeAttnArgs& a, cudaStream_t s) {
 
 // Two parts a block, each of the largest item's rows: 256, or 128 for D = 256.
 size_t tree_attn_workspace_bytes(int D) {
-  return (size_t)2 * kBlocks * (D == 256 ? kM : 2 * kM) * (D + 1) * sizeof(float) + kBlocks * sizeof(Cut);
+  return (size_t)2 * kBlocks * (D == 256 ? kM : 2 * kM) * (D + 1) * sizeof(float);
 }
 
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t s) {
