@@ -516,6 +516,19 @@ int rows_of(int D, long long rows) {
   return (int)(rounds > 32 ? 32 : rounds) * round;
 }
 
+template <typename T, int D, bool kPages, bool kInter>
+cudaError_t launch_rows(const RopeArgs& a, unsigned blocks, cudaStream_t s) {
+  constexpr int kSmem = kThreads * 16 * sizeof(T) * kDepth;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(qk_norm_rope_kernel<T, D, kPages, kInter>), kSmem, done);
+  if (e != cudaSuccess) return e;
+  const int slot = stage_timer_begin(s, kKernQkNormRope);
+  qk_norm_rope_kernel<T, D, kPages, kInter><<<blocks, kThreads, kSmem, s>>>(a);
+  e = cudaGetLastError();
+  stage_timer_end(slot, s);
+  return e;
+}
+
 template <typename T, int D>
 cudaError_t forward(RopeArgs& a, cudaStream_t s) {
   const long long tokens = (long long)a.B * a.N;
@@ -525,24 +538,12 @@ cudaError_t forward(RopeArgs& a, cudaStream_t s) {
   a.blocks[0] = (int)((tokens + a.tokens[0] - 1) / a.tokens[0]);
   a.blocks[1] = (int)((tokens + a.tokens[1] - 1) / a.tokens[1]);
   const unsigned blocks = a.blocks[0] + (a.k_pages ? 2 : 1) * a.blocks[1];
-  constexpr int kSmem = kThreads * 16 * sizeof(T) * kDepth;
-  auto launch = [&](auto kernel) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    const int slot = stage_timer_begin(s, kKernQkNormRope);
-    kernel<<<blocks, kThreads, kSmem, s>>>(a);
-    e = cudaGetLastError();
-    stage_timer_end(slot, s);
-    return e;
-  };
-  if (a.k_pages) {
-    return a.interleaved ? launch(qk_norm_rope_kernel<T, D, true, true>) : launch(qk_norm_rope_kernel<T, D, true, false>);
-  }
-  return a.interleaved ? launch(qk_norm_rope_kernel<T, D, false, true>) : launch(qk_norm_rope_kernel<T, D, false, false>);
+  if (a.k_pages) return a.interleaved ? launch_rows<T, D, true, true>(a, blocks, s) : launch_rows<T, D, true, false>(a, blocks, s);
+  return a.interleaved ? launch_rows<T, D, false, true>(a, blocks, s) : launch_rows<T, D, false, false>(a, blocks, s);
 }
 
-template <typename T, int D>
-cudaError_t backward(RopeArgs& a, cudaStream_t s) {
+template <typename T, int D, bool kInter>
+cudaError_t backward_of(RopeArgs& a, cudaStream_t s) {
   const long long tokens = (long long)a.B * a.N;
   // blocks in proportion to the kinds' rows; each takes one run of tokens, or several where a run's angles
   // do not fit
@@ -560,11 +561,11 @@ cudaError_t backward(RopeArgs& a, cudaStream_t s) {
   }
   const unsigned blocks = a.blocks[0] + a.blocks[1];
   constexpr int kSmem = kThreads * 32 * sizeof(T) * (sizeof(T) == 2 ? kDepth : kDepth / 2);
-  auto kernel = a.interleaved ? qk_norm_rope_bwd_kernel<T, D, true> : qk_norm_rope_bwd_kernel<T, D, false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(qk_norm_rope_bwd_kernel<T, D, kInter>), kSmem, done);
   if (e != cudaSuccess) return e;
   const int slot = stage_timer_begin(s, kKernQkNormRopeBwd);
-  kernel<<<blocks, kThreads, kSmem, s>>>(a);
+  qk_norm_rope_bwd_kernel<T, D, kInter><<<blocks, kThreads, kSmem, s>>>(a);
   e = cudaGetLastError();
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
@@ -580,6 +581,11 @@ cudaError_t backward(RopeArgs& a, cudaStream_t s) {
   }
   stage_timer_end(slot, s);
   return e;
+}
+
+template <typename T, int D>
+cudaError_t backward(RopeArgs& a, cudaStream_t s) {
+  return a.interleaved ? backward_of<T, D, true>(a, s) : backward_of<T, D, false>(a, s);
 }
 
 }  // namespace

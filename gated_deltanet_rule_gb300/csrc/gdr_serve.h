@@ -2,6 +2,7 @@
 // ABI): q/k norm + rotation, tree attention over pages, draft verification, cache pages.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -138,5 +139,18 @@ struct CompactArgs {
 };
 constexpr int kCompactMaxPath = 2048;   // path entries whose slots fit the kernel's shared memory
 cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t s);
+
+// Lets a kernel use `bytes` of dynamic shared memory: set once on each device (`done`, a bit a device), as
+// setting it costs a call 0.8 us.
+inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 }  // namespace gdr

@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return;
   }
 
-  if (tid == 0) {
+  if (tid == 64) {   // (the first warps have the first rows to count)
     for (int i = 0; i < NS; ++i) {
       mbar_init(&s.full[i], 1);
       mbar_init(&s.empty[i], 1);
@@ -1197,7 +1197,8 @@ cudaError_t launch(const TreeAttnArgs& p, cudaStream_t st) {
   a.items = p.B * p.Hk * a.mts;
   a.budget = wait_budget_cycles();
   a.err = p.err;
-  cudaError_t e = cudaFuncSetAttribute(tree_attn_kernel<D, kForm>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(tree_attn_kernel<D, kForm>), C::kSmem, done);
   if (e != cudaSuccess) return e;
   int slot = stage_timer_begin(st, kKernTreeAttn);
   tree_attn_kernel<D, kForm><<<kBlocks, kThreads, C::kSmem, st>>>(mq, mk, mv, a);

@@ -572,10 +572,11 @@ __global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCluster, 1, 1) 
 
 template <typename T, bool kVec>
 cudaError_t launch(const VerifyArgs& a, cudaStream_t s) {
-  const int smem = ring_at(a.N) + (kVec ? kAhead * 2 * kThreads * 4 * (int)sizeof(T) : 0);
-  const cudaError_t e = cudaFuncSetAttribute(verify_kernel<T, kVec>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int kRing = kVec ? kAhead * 2 * kThreads * 4 * (int)sizeof(T) : 0;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(verify_kernel<T, kVec>), ring_at(kVerifyMaxNodes) + kRing, done);
   if (e != cudaSuccess) return e;
-  verify_kernel<T, kVec><<<a.B * kCluster, kThreads, smem, s>>>(a);
+  verify_kernel<T, kVec><<<a.B * kCluster, kThreads, ring_at(a.N) + kRing, s>>>(a);
   return cudaGetLastError();
 }
 
