@@ -347,6 +347,8 @@ __global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCluster, 1, 1) 
     if (rank == 0 && tid == 0) atomicCAS(a.err, 0, kErrDeviceIndex);
     return;
   }
+  // (no block writes to another's shared memory before that one has started: arrived here, waited for below)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const size_t row = (size_t)b * a.N;
   const T* P = static_cast<const T*>(a.p) + row * a.V;
   const T* Q = a.q ? static_cast<const T*>(a.q) + row * a.V : nullptr;
@@ -366,6 +368,7 @@ __global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCluster, 1, 1) 
     s_token[i] = t;
   }
   __syncthreads();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 
   // the vocabulary's chunks, in contiguous runs: block r's, and of those warp w's
   const int chunks = (a.V + kChunk4 - 1) / kChunk4;
