@@ -18,6 +18,8 @@
 // 31-bit position; float32 angles would be off by 0.06 rad at position 2^20, and float64 arithmetic
 // runs at 1/64 of the float32 rate here. The fraction is reduced to an eighth turn before sincospif.
 #include <algorithm>
+#include <cstring>
+#include <type_traits>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -31,7 +33,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPairs = 2048;       // (token, pair) angles of a block
 constexpr int kMostTokens = 256;   // tokens of a block
-constexpr int kDepth = 4;          // rows of every lane in flight (the gradient of float32: 2)
+constexpr int kDepth = 4;          // rows of every lane in flight
+constexpr int kDepthB = 3;         // the same, gradient
 
 // Two floats in one register pair: the packed operations halve the instructions of this kernel, whose
 // issue rate is what bounds it beside HBM.
@@ -56,21 +59,26 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
 }
 __device__ __forceinline__ F2 neg2(F2 a) { return {a.v ^ 0x8000000080000000ull}; }
 
-// Eight consecutive elements in shared memory (staged by asynchronous copies, 16 bytes at a time).
+// kE (eight or four) consecutive elements in shared memory (staged by asynchronous copies, in pieces V that
+// lie kThreads apart).
+template <int kE>
 __device__ __forceinline__ void get(const __nv_bfloat16* p, F2* x) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  const auto v = *reinterpret_cast<const std::conditional_t<kE == 8, uint4, uint2>*>(p);
+  uint32_t w[kE / 2];
+  memcpy(w, &v, sizeof(v));
 #pragma unroll
-  for (int e = 0; e < 4; ++e) x[e] = pack(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
+  for (int e = 0; e < kE / 2; ++e) x[e] = pack(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
 }
+template <int kE>
 __device__ __forceinline__ void get(const float* p, F2* x) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const ulonglong2 u = reinterpret_cast<const ulonglong2*>(p)[h * kThreads];   // (pieces lie kThreads apart)
+  for (int h = 0; h < kE / 4; ++h) {
+    const ulonglong2 u = reinterpret_cast<const ulonglong2*>(p)[h * kThreads];
     x[2 * h] = {u.x};
     x[2 * h + 1] = {u.y};
   }
 }
+// Eight elements to memory; four of the gradient's.
 __device__ __forceinline__ void put(__nv_bfloat16* p, const F2* x) {
   uint32_t w[4];
 #pragma unroll
@@ -81,27 +89,40 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, const F2* x) {
   }
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
+// (32 bytes in one store: two of 16 would each write half of every sector)
 __device__ __forceinline__ void put(float* p, const F2* x) {
-  reinterpret_cast<ulonglong2*>(p)[0] = make_ulonglong2(x[0].v, x[1].v);
-  reinterpret_cast<ulonglong2*>(p)[1] = make_ulonglong2(x[2].v, x[3].v);
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(p), "l"(x[0].v), "l"(x[1].v), "l"(x[2].v), "l"(x[3].v) : "memory");
+  } else {
+    reinterpret_cast<ulonglong2*>(p)[0] = make_ulonglong2(x[0].v, x[1].v);
+    reinterpret_cast<ulonglong2*>(p)[1] = make_ulonglong2(x[2].v, x[3].v);
+  }
 }
 
-// A thread's own ring in shared memory: kDepth rows of kPieces 16-byte pieces, piece p of every thread side
+__device__ __forceinline__ void put4(float* p, const F2* x) { *reinterpret_cast<ulonglong2*>(p) = make_ulonglong2(x[0].v, x[1].v); }
+
+// A thread's own ring in shared memory: kDepth rows of kPieces pieces V, piece p of every thread side
 // by side. Only the thread that copied a piece reads it, so a wait for its own copies is all it needs; the
 // copies hold no registers, which is what bounded the rows in flight.
-template <int kPieces, int kDepth>
+template <int kPieces, int kDepth, typename V>
 struct Ring {
-  uint4* mine;
-  __device__ __forceinline__ explicit Ring(void* smem) : mine(static_cast<uint4*>(smem) + threadIdx.x) {}
-  __device__ __forceinline__ uint4* at(int slot, int piece) const { return mine + (slot * kPieces + piece) * kThreads; }
-  // eight elements from src into pieces first, first + 1, ...
-  template <typename T>
-  __device__ __forceinline__ void copy(int slot, int first, const T* src) const {
+  V* mine;
+  __device__ __forceinline__ explicit Ring(void* smem) : mine(static_cast<V*>(smem) + threadIdx.x) {}
+  __device__ __forceinline__ V* at(int slot, int piece) const { return mine + (slot * kPieces + piece) * kThreads; }
+  // n pieces from src into pieces first, first + 1, ...
+  template <int n>
+  __device__ __forceinline__ void copy(int slot, int first, const void* src) const {
 #pragma unroll
-    for (int e = 0; e < (int)(8 * sizeof(T) / 16); ++e)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(at(slot, first + e))),
-                   "l"(reinterpret_cast<const uint4*>(src) + e)
-                   : "memory");
+    for (int e = 0; e < n; ++e) {
+      if (sizeof(V) == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(at(slot, first + e))),
+                     "l"(static_cast<const V*>(src) + e)
+                     : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(ptx::smem_u32(at(slot, first + e))),
+                     "l"(static_cast<const V*>(src) + e)
+                     : "memory");
+    }
   }
   template <typename T>
   __device__ __forceinline__ const T* row(int slot, int piece) const { return reinterpret_cast<const T*>(at(slot, piece)); }
@@ -136,10 +157,10 @@ __device__ __forceinline__ void turn_sincos(uint64_t frac, int pos, float& c, fl
   if (quad & 2) s = -s;
 }
 
-// What a lane holds of a head: two runs of eight elements.
-template <int D>
+// What a lane holds of a head: two runs of kE elements.
+template <int D, int kE>
 struct Lane {
-  static constexpr int kLanes = D / 16;        // lanes of one head
+  static constexpr int kLanes = D / (2 * kE);  // lanes of one head
   static constexpr int kHeads = 32 / kLanes;   // rows of one warp
   int sub, l, off0, off1;
   bool turns;
@@ -147,41 +168,43 @@ struct Lane {
     const int lane = threadIdx.x & 31;
     sub = lane / kLanes;
     l = lane % kLanes;
-    turns = 16 * l < a.R;
-    const int first = turns ? 8 * l : a.R + 8 * (l - a.R / 16);
+    turns = 2 * kE * l < a.R;
+    const int first = turns ? kE * l : a.R + kE * (l - a.R / (2 * kE));
     off0 = first;
     off1 = first + (turns ? a.R : D - a.R) / 2;
   }
 };
 
 // cos and sin of a block's tokens [t0, t0 + n) into cs, R floats a token.
+template <int kE>
 __device__ __forceinline__ void form_angles(const RopeArgs& a, long long t0, int n, float* cs) {
   const int half = a.R / 2;
   for (int x = threadIdx.x; x < n * half; x += kThreads) {
     const int t = x / half, j = x - t * half;
     float c, s;
     turn_sincos(turn_fraction(__ldg(a.inv_freq + j)), __ldg(a.pos + t0 + t), c, s);
-    // four runs of [lane][4]: the lanes' first and last four cosines, then sines, so that the lanes of a
-    // head read neighbouring 16 bytes. Pair j is entry e of lane l: half-split j = 8 l + e; interleaved
-    // j = 4 l + e in a lane's first run, R/4 + 4 l + e - 4 in its second
-    int l = j >> 3, e = j & 7;
+    // runs of [lane][4]: the lanes' first four cosines, (kE = 8) their last four, then sines, so that the
+    // lanes of a head read neighbouring 16 bytes. Pair j is entry e of lane l: half-split j = kE l + e;
+    // interleaved j = kE/2 l + e in a lane's first run, R/4 + kE/2 l + e - kE/2 in its second
+    int l = j / kE, e = j % kE;
     if (a.interleaved) {
       const int second = 4 * j >= a.R, k = second ? j - a.R / 4 : j;
-      l = k >> 2;
-      e = 4 * second + (k & 3);
+      l = k / (kE / 2);
+      e = kE / 2 * second + k % (kE / 2);
     }
-    float* at = cs + t * a.R + (e >> 2) * (a.R / 4) + l * 4 + (e & 3);
+    float* at = cs + t * a.R + (e >> 2) * (2 * a.R / kE) + l * 4 + (e & 3);
     at[0] = c;
     at[a.R / 2] = s;
   }
 }
 
-// A lane's pairs' cosines and sines, as four packed pairs each.
+// A lane's pairs' cosines and sines, packed two by two.
+template <int kE>
 __device__ __forceinline__ void read_angles(const float* cs, int R, int l, F2* c, F2* s) {
   const ulonglong2* at = reinterpret_cast<const ulonglong2*>(cs) + l;
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const ulonglong2 cv = at[q * (R / 16)], sv = at[(q + 2) * (R / 16)];
+  for (int q = 0; q < kE / 4; ++q) {
+    const ulonglong2 cv = at[q * (R / (2 * kE))], sv = at[(q + kE / 4) * (R / (2 * kE))];
     c[2 * q] = {cv.x};
     c[2 * q + 1] = {cv.y};
     s[2 * q] = {sv.x};
@@ -189,14 +212,14 @@ __device__ __forceinline__ void read_angles(const float* cs, int R, int l, F2* c
   }
 }
 
-// Turn a lane's sixteen values (eight packed pairs) by its angles; kBack turns back.
-template <bool kInter, bool kBack>
+// Turn a lane's 2 kE values (kE packed pairs) by its angles; kBack turns back.
+template <int kE, bool kInter, bool kBack>
 __device__ __forceinline__ void turn(F2* y, const float* cs, int R, int l) {
-  F2 c[4], s[4];
-  read_angles(cs, R, l, c, s);
+  F2 c[kE / 2], s[kE / 2];
+  read_angles<kE>(cs, R, l, c, s);
   if (kInter) {   // (y_2j, y_2j+1) are the members of pair j
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < kE / 2; ++q) {
       float c0, c1, s0, s1;
       unpack(c[q], c0, c1);
       unpack(s[q], s0, s1);
@@ -212,31 +235,32 @@ __device__ __forceinline__ void turn(F2* y, const float* cs, int R, int l) {
         y[2 * q + u] = pack(ya * cj - yb * sj, yb * cj + ya * sj);
       }
     }
-  } else {        // y[q] holds the first members of pairs 2q and 2q + 1, y[4 + q] the second ones
+  } else {        // y[q] holds the first members of pairs 2q and 2q + 1, y[kE/2 + q] the second ones
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const F2 ya = y[q], yb = y[4 + q], sq = kBack ? neg2(s[q]) : s[q];
+    for (int q = 0; q < kE / 2; ++q) {
+      const F2 ya = y[q], yb = y[kE / 2 + q], sq = kBack ? neg2(s[q]) : s[q];
       y[q] = fma2(ya, c[q], neg2(mul2(yb, sq)));
-      y[4 + q] = fma2(yb, c[q], mul2(ya, sq));
+      y[kE / 2 + q] = fma2(yb, c[q], mul2(ya, sq));
     }
   }
 }
 
-template <int D>
+template <int kLanes>
 __device__ __forceinline__ float head_sum(float v) {
 #pragma unroll
-  for (int m = D / 32; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  for (int m = kLanes / 2; m >= 1; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
   return v;
 }
 
-__device__ __forceinline__ void load16(const float* w, int off0, int off1, F2* x) {
+template <int kE>
+__device__ __forceinline__ void load_weights(const float* w, int off0, int off1, F2* x) {
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
+  for (int q = 0; q < kE / 4; ++q) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(w + off0) + q), b = __ldg(reinterpret_cast<const float4*>(w + off1) + q);
     x[2 * q] = pack(a.x, a.y);
     x[2 * q + 1] = pack(a.z, a.w);
-    x[4 + 2 * q] = pack(b.x, b.y);
-    x[4 + 2 * q + 1] = pack(b.z, b.w);
+    x[kE / 2 + 2 * q] = pack(b.x, b.y);
+    x[kE / 2 + 2 * q + 1] = pack(b.z, b.w);
   }
 }
 
@@ -262,16 +286,18 @@ struct Kind {
 
 // Normed, turned and written (kPages: keys into the pages, values copied there). HBM-bound: each element
 // is read and written once; every lane has kDepth rows in flight in shared memory. Measured: 8192 tokens of
-// 32 + 8 heads of 128, bfloat16: 34.0 us, 73% of the copy bandwidth (37.6 us with the rows loaded into
-// registers and lanes 32 bytes apart).
+// 32 + 8 heads of 128, bfloat16: 33.7 us, 73% of the copy bandwidth (a plain
+// copy of as many bytes: 28.9 us; with the rows loaded into registers and lanes 32 bytes apart 37.6 us; with
+// blocks that walk both kinds, as the gradient's do, 36.5 us).
 template <typename T, int D, bool kPages, bool kInter>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a) {
   constexpr int kRun = 8 * sizeof(T) / 16, kPieces = 2 * kRun;   // 16-byte pieces of a run, of a lane's row
   extern __shared__ __align__(16) uint8_t stage[];
   __shared__ __align__(16) float cs[2 * kPairs];
   __shared__ long long slot[kMostTokens];
-  const Ring<kPieces, kDepth> ring(stage);
-  const Lane<D> ln(a);
+  const Ring<kPieces, kDepth, uint4> ring(stage);
+  using Ln = Lane<D, 8>;
+  const Ln ln(a);
   const long long tokens = (long long)a.B * a.N;
   const int kind = blockIdx.x < a.blocks[0] ? 0 : blockIdx.x < a.blocks[0] + a.blocks[1] ? 1 : 2;
   const long long block = blockIdx.x - (kind == 0 ? 0 : kind == 1 ? a.blocks[0] : a.blocks[0] + a.blocks[1]);
@@ -283,7 +309,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
   const long long t0 = block * k.tokens;
   const int n = (int)min((long long)k.tokens, tokens - t0), rows = n * k.H;
   const uint32_t magic = k.H == 1 ? 0xFFFFFFFFu : (uint32_t)((1ull << 32) / k.H);
-  const int warp = threadIdx.x >> 5, step = kWarps * Lane<D>::kHeads;
+  const int warp = threadIdx.x >> 5, step = kWarps * Ln::kHeads;
   const bool to_pages = kPages && kind > 0;
 
   const T* base = k.src + t0 * k.tok;
@@ -294,18 +320,18 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
       int t, h;
       row_at(x, k.H, magic, t, h);
       const T* src = base + (t * tok + h * head);   // (below 2^31: tokens of a block <= 256)
-      ring.copy(u, 0, src + ln.off0);
-      ring.copy(u, kRun, src + ln.off1);
+      ring.template copy<kRun>(u, 0, src + ln.off0);
+      ring.template copy<kRun>(u, kRun, src + ln.off1);
     }
     ptx::cp_async_commit();
   };
-  const int x0 = warp * Lane<D>::kHeads + ln.sub;
+  const int x0 = warp * Ln::kHeads + ln.sub;
 #pragma unroll
   for (int u = 0; u < kDepth; ++u) load(u, x0 + u * step);
   F2 w[8];
   if (kind < 2) {
-    load16(k.w, ln.off0, ln.off1, w);
-    form_angles(a, t0, n, cs);
+    load_weights<8>(k.w, ln.off0, ln.off1, w);
+    form_angles<8>(a, t0, n, cs);
   }
   if (to_pages) {
     for (int t = threadIdx.x; t < n; t += kThreads) {
@@ -324,7 +350,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
   }
   __syncthreads();
   int u = 0;
-  for (int xw = warp * Lane<D>::kHeads; xw < rows; xw += step, u = u + 1 == kDepth ? 0 : u + 1) {   // the same in every lane
+  for (int xw = warp * Ln::kHeads; xw < rows; xw += step, u = u + 1 == kDepth ? 0 : u + 1) {   // the same in every lane
     const int x = xw + ln.sub;
     const bool live = x < rows;
     int t, h;
@@ -343,19 +369,19 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
       }
     } else {
       F2 y[8];
-      get(ring.template row<T>(u, 0), y);
-      get(ring.template row<T>(u, kRun), y + 4);
+      get<8>(ring.template row<T>(u, 0), y);
+      get<8>(ring.template row<T>(u, kRun), y + 4);
       F2 sq = mul2(y[0], y[0]);
 #pragma unroll
       for (int e = 1; e < 8; ++e) sq = fma2(y[e], y[e], sq);
       float s0, s1;
       unpack(sq, s0, s1);
-      const float ss = head_sum<D>(live ? s0 + s1 : 0.f);
+      const float ss = head_sum<Ln::kLanes>(live ? s0 + s1 : 0.f);
       const float r = rsqrtf(ss * (1.f / D) + a.eps);
       const F2 rr = pack(r, r);
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = mul2(mul2(w[e], y[e]), rr);
-      if (ln.turns) turn<kInter, false>(y, cs + t * a.R, a.R, ln.l);
+      if (ln.turns) turn<8, kInter, false>(y, cs + t * a.R, a.R, ln.l);
       if (write) {
         put(out + ln.off0, y);
         put(out + ln.off1, y + 4);
@@ -365,119 +391,126 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
   }
 }
 
-constexpr int kBwdBlocks = kNumSMs * 2;   // blocks of the gradient (one wave), and rows of its partial sums, at most
+constexpr int kPerSM = 4;                       // blocks of the gradient on each SM
+constexpr int kBwdBlocks = kNumSMs * kPerSM;   // blocks of the gradient (one wave), and rows of its partial sums, at most
 
 // Gradient, with dy = R^T dout and r = 1 / sqrt(mean(x^2) + eps):
 //   dx = r (w dy - x r^2 mean(w dy x)),  dw = sum over tokens and heads of dy x r.
-// As the forward, but a block walks several groups of tokens of one kind and keeps the weight gradients
-// of a lane's sixteen elements in registers over all of them; it adds its lanes in a fixed order and
-// writes one row of partial sums, which the second kernel adds in order: no atomics, the same bits every
-// time. Measured: 3 x 2731 tokens of 16 + 2 heads of 256, bfloat16: 67.7 us, 66% of the copy bandwidth.
+// As the forward, but lanes hold half as much, and a block walks the queries of its tokens and then their
+// keys, keeping the weight gradients of a lane's eight elements in registers; it adds its lanes in a fixed
+// order and writes a row of partial sums of each kind, which the second kernel adds in order: no atomics, the
+// same bits every time. Measured: 3 x 2731 tokens of 16 + 2 heads of 256, bfloat16: 59.7 us, 75% of the copy
+// bandwidth (a plain copy of as many bytes: 48.6 us). With blocks of one kind each, whose work was uneven,
+// 65.6 us; with sixteen elements a lane and half the warps besides, 67.7 us.
 template <typename T, int D, bool kInter>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeArgs a) {
-  constexpr int kRun = 8 * sizeof(T) / 16;            // 16-byte pieces of a run; a lane's row has four runs
-  constexpr int kDepthB = kRun == 1 ? kDepth : kDepth / 2;
+__global__ void __launch_bounds__(kThreads, kPerSM) qk_norm_rope_bwd_kernel(const RopeArgs a) {
+  using V = std::conditional_t<sizeof(T) == 2, uint2, uint4>;   // a run of four elements
+  using Ln = Lane<D, 4>;
   extern __shared__ __align__(16) uint8_t stage[];
   __shared__ __align__(16) float cs[2 * kPairs];
   __shared__ float acc[kWarps][D];
-  const Ring<4 * kRun, kDepthB> ring(stage);
-  const Lane<D> ln(a);
+  const Ring<4, kDepthB, V> ring(stage);   // x and dy, two runs each
+  const Ln ln(a);
   const long long tokens = (long long)a.B * a.N;
-  const bool is_q = blockIdx.x < a.blocks[0];
-  const T* src = static_cast<const T*>(is_q ? a.q : a.k);
-  const T* dsrc = static_cast<const T*>(is_q ? a.dq_out : a.dk_out);
-  float* dst = is_q ? a.dq : a.dk;
-  const long long tok = is_q ? a.q_tok : a.k_tok, head = is_q ? a.q_head : a.k_head;
-  const int H = is_q ? a.Hq : a.Hk, per = a.tokens[is_q ? 0 : 1];
-  const uint32_t magic = H == 1 ? 0xFFFFFFFFu : (uint32_t)((1ull << 32) / H);
-  const int warp = threadIdx.x >> 5, step = kWarps * Lane<D>::kHeads;
-  const int stride = a.blocks[is_q ? 0 : 1];
-  F2 w[8], g[8];
-  load16(is_q ? a.q_w : a.k_w, ln.off0, ln.off1, w);
+  const int warp = threadIdx.x >> 5, step = kWarps * Ln::kHeads, per = a.tokens[1], most = a.tokens[0];
+  const long long begin = (long long)blockIdx.x * per, end = min(tokens, begin + per);
+#pragma unroll 1
+  for (int kind = 0; kind < 2; ++kind) {
+    const bool is_q = kind == 0;
+    const T* src = static_cast<const T*>(is_q ? a.q : a.k);
+    const T* dsrc = static_cast<const T*>(is_q ? a.dq_out : a.dk_out);
+    float* dst = is_q ? a.dq : a.dk;
+    const long long tok = is_q ? a.q_tok : a.k_tok, head = is_q ? a.q_head : a.k_head;
+    const int H = is_q ? a.Hq : a.Hk;
+    const uint32_t magic = H == 1 ? 0xFFFFFFFFu : (uint32_t)((1ull << 32) / H);
+    F2 w[4], g[4];
+    load_weights<4>(is_q ? a.q_w : a.k_w, ln.off0, ln.off1, w);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) g[e] = {0};
-  for (long long group = is_q ? blockIdx.x : blockIdx.x - a.blocks[0]; group * per < tokens; group += stride) {
-    const long long t0 = group * per;
-    const int n = (int)min((long long)per, tokens - t0), rows = n * H;
-    auto load = [&](int u, int x) {
-      if (x < rows) {
+    for (int e = 0; e < 4; ++e) g[e] = {0};
+    for (long long t0 = begin; t0 < end; t0 += most) {
+      const int n = (int)min((long long)most, end - t0), rows = n * H;
+      auto load = [&](int u, int x) {
+        if (x < rows) {
+          int t, h;
+          row_at(x, H, magic, t, h);
+          const T* s = src + t0 * tok + (t * (int)tok + h * (int)head);
+          const T* d = dsrc + (t0 * H + x) * D;
+          ring.template copy<1>(u, 0, s + ln.off0);
+          ring.template copy<1>(u, 1, s + ln.off1);
+          ring.template copy<1>(u, 2, d + ln.off0);
+          ring.template copy<1>(u, 3, d + ln.off1);
+        }
+        ptx::cp_async_commit();
+      };
+#pragma unroll
+      for (int u = 0; u < kDepthB; ++u) load(u, (warp + u * kWarps) * Ln::kHeads + ln.sub);
+      if (kind == 0 || end - begin > most) {   // (the keys' angles are there already where one run holds them)
+        __syncthreads();   // the run before has been walked
+        form_angles<4>(a, t0, n, cs);
+      }
+      __syncthreads();
+      int u = 0;
+      for (int xw = warp * Ln::kHeads; xw < rows; xw += step, u = u + 1 == kDepthB ? 0 : u + 1) {   // the same in every lane
+        const int x = xw + ln.sub;
+        const bool live = x < rows;
         int t, h;
-        row_at(x, H, magic, t, h);
-        const T* s = src + t0 * tok + (t * (int)tok + h * (int)head);
-        const T* d = dsrc + (t0 * H + x) * D;
-        ring.copy(u, 0, s + ln.off0);
-        ring.copy(u, kRun, s + ln.off1);
-        ring.copy(u, 2 * kRun, d + ln.off0);
-        ring.copy(u, 3 * kRun, d + ln.off1);
-      }
-      ptx::cp_async_commit();
-    };
+        row_at(live ? x : rows - 1, H, magic, t, h);
+        ptx::cp_async_wait<kDepthB - 1>();
+        F2 y[4], dy[4];
+        get<4>(ring.template row<T>(u, 0), y);
+        get<4>(ring.template row<T>(u, 1), y + 2);
+        get<4>(ring.template row<T>(u, 2), dy);
+        get<4>(ring.template row<T>(u, 3), dy + 2);
+        load(u, x + kDepthB * step);
+        if (ln.turns) turn<4, kInter, true>(dy, cs + t * a.R, a.R, ln.l);
+        F2 sq = mul2(y[0], y[0]), dt = mul2(mul2(w[0], dy[0]), y[0]);
 #pragma unroll
-    for (int u = 0; u < kDepthB; ++u) load(u, (warp + u * kWarps) * Lane<D>::kHeads + ln.sub);
-    __syncthreads();   // the group before has been walked
-    form_angles(a, t0, n, cs);
+        for (int e = 1; e < 4; ++e) {
+          sq = fma2(y[e], y[e], sq);
+          dt = fma2(mul2(w[e], dy[e]), y[e], dt);
+        }
+        float s0, s1, d0, d1;
+        unpack(sq, s0, s1);
+        unpack(dt, d0, d1);
+        const float ss = head_sum<Ln::kLanes>(live ? s0 + s1 : 0.f), dot = head_sum<Ln::kLanes>(live ? d0 + d1 : 0.f);
+        if (!live) continue;
+        const float r = rsqrtf(ss * (1.f / D) + a.eps);
+        const float m = -dot * (1.f / D) * r * r;
+        const F2 rr = pack(r, r), mm = pack(m, m);
+        F2 dx[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          dx[e] = mul2(rr, fma2(y[e], mm, mul2(w[e], dy[e])));
+          g[e] = fma2(dy[e], mul2(y[e], rr), g[e]);
+        }
+        float* out = dst + (t0 * H + x) * D;
+        put4(out + ln.off0, dx);
+        put4(out + ln.off1, dx + 2);
+      }
+    }
+    // the block's sum: lanes of equal elements within a warp, then the warps in order
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float g0, g1;
+      unpack(g[e], g0, g1);
+#pragma unroll
+      for (int m = 16; m >= Ln::kLanes; m >>= 1) {
+        g0 += __shfl_xor_sync(0xffffffffu, g0, m);
+        g1 += __shfl_xor_sync(0xffffffffu, g1, m);
+      }
+      if (ln.sub == 0) {
+        float* at = acc[warp] + (e < 2 ? ln.off0 : ln.off1) + 2 * (e & 1);
+        at[0] = g0;
+        at[1] = g1;
+      }
+    }
     __syncthreads();
-    int u = 0;
-    for (int xw = warp * Lane<D>::kHeads; xw < rows; xw += step, u = u + 1 == kDepthB ? 0 : u + 1) {   // the same in every lane
-      const int x = xw + ln.sub;
-      const bool live = x < rows;
-      int t, h;
-      row_at(live ? x : rows - 1, H, magic, t, h);
-      ptx::cp_async_wait<kDepthB - 1>();
-      F2 y[8], dy[8];
-      get(ring.template row<T>(u, 0), y);
-      get(ring.template row<T>(u, kRun), y + 4);
-      get(ring.template row<T>(u, 2 * kRun), dy);
-      get(ring.template row<T>(u, 3 * kRun), dy + 4);
-      load(u, x + kDepthB * step);
-      if (ln.turns) turn<kInter, true>(dy, cs + t * a.R, a.R, ln.l);
-      F2 sq = mul2(y[0], y[0]), dt = mul2(mul2(w[0], dy[0]), y[0]);
+    for (int i = threadIdx.x; i < D; i += kThreads) {
+      float sum = 0.f;
 #pragma unroll
-      for (int e = 1; e < 8; ++e) {
-        sq = fma2(y[e], y[e], sq);
-        dt = fma2(mul2(w[e], dy[e]), y[e], dt);
-      }
-      float s0, s1, d0, d1;
-      unpack(sq, s0, s1);
-      unpack(dt, d0, d1);
-      const float ss = head_sum<D>(live ? s0 + s1 : 0.f), dot = head_sum<D>(live ? d0 + d1 : 0.f);
-      if (!live) continue;
-      const float r = rsqrtf(ss * (1.f / D) + a.eps);
-      const float m = -dot * (1.f / D) * r * r;
-      const F2 rr = pack(r, r), mm = pack(m, m);
-      F2 dx[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        dx[e] = mul2(rr, fma2(y[e], mm, mul2(w[e], dy[e])));
-        g[e] = fma2(dy[e], mul2(y[e], rr), g[e]);
-      }
-      float* out = dst + (t0 * H + x) * D;
-      put(out + ln.off0, dx);
-      put(out + ln.off1, dx + 4);
+      for (int v = 0; v < kWarps; ++v) sum += acc[v][i];
+      a.partial[((long long)kind * gridDim.x + blockIdx.x) * D + i] = sum;
     }
-  }
-  // the block's sum: lanes of equal elements within a warp, then the warps in order
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    float g0, g1;
-    unpack(g[e], g0, g1);
-#pragma unroll
-    for (int m = 16; m >= Lane<D>::kLanes; m >>= 1) {
-      g0 += __shfl_xor_sync(0xffffffffu, g0, m);
-      g1 += __shfl_xor_sync(0xffffffffu, g1, m);
-    }
-    if (ln.sub == 0) {
-      float* at = acc[warp] + (e < 4 ? ln.off0 : ln.off1) + 2 * (e & 3);
-      at[0] = g0;
-      at[1] = g1;
-    }
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < D; i += kThreads) {
-    float sum = 0.f;
-#pragma unroll
-    for (int v = 0; v < kWarps; ++v) sum += acc[v][i];
-    a.partial[(long long)blockIdx.x * D + i] = sum;
   }
 }
 
@@ -486,7 +519,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_kernel(const RopeAr
 __global__ void __launch_bounds__(1024) qk_norm_rope_bwd_join_kernel(const RopeArgs a) {
   __shared__ float tile[32][33];
   ptx::wait_prerequisite();
-  const int kind = blockIdx.y, first = kind ? a.blocks[0] : 0, rows = a.blocks[kind];
+  const int kind = blockIdx.y, first = kind ? a.blocks[0] : 0, rows = a.blocks[0];
   const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
   const float* p = a.partial + (long long)first * a.D + blockIdx.x * 32 + lane;
   float sum = 0.f;
@@ -545,22 +578,15 @@ cudaError_t forward(RopeArgs& a, cudaStream_t s) {
 template <typename T, int D, bool kInter>
 cudaError_t backward_of(RopeArgs& a, cudaStream_t s) {
   const long long tokens = (long long)a.B * a.N;
-  // blocks in proportion to the kinds' rows; each takes one run of tokens, or several where a run's angles
-  // do not fit
-  long long most[2];
-  most[0] = (long long)(kBwdBlocks - 1) * a.Hq / (a.Hq + a.Hk);
-  if (most[0] < 1) most[0] = 1;
-  most[1] = kBwdBlocks - most[0];
-  for (int kind = 0; kind < 2; ++kind) {
-    const int H = kind ? a.Hk : a.Hq;
-    const long long per = (tokens + most[kind] - 1) / most[kind];
-    // (not under a round of the block's lane groups: a block's start costs more than its rows)
-    const long long rows = std::max(per * H, (long long)kWarps * (32 / (D / 16)));
-    a.tokens[kind] = tokens_of(a, H, rows, tokens);
-    a.blocks[kind] = (int)std::min(most[kind], (tokens + a.tokens[kind] - 1) / a.tokens[kind]);
-  }
-  const unsigned blocks = a.blocks[0] + a.blocks[1];
-  constexpr int kSmem = kThreads * 32 * sizeof(T) * (sizeof(T) == 2 ? kDepth : kDepth / 2);
+  // one wave of blocks, each with one run of tokens, or several where a run's angles do not fit (not under
+  // a round of the block's lane groups: a block's start costs more than its rows)
+  long long per = (tokens + kBwdBlocks - 1) / kBwdBlocks;
+  const long long least = (kWarps * Lane<D, 4>::kHeads + a.Hq - 1) / a.Hq;
+  per = std::min(std::max(per, least), tokens);
+  a.tokens[0] = tokens_of(a, a.Hq, per * a.Hq, tokens);
+  a.tokens[1] = (int)per;
+  const unsigned blocks = a.blocks[0] = (int)((tokens + per - 1) / per);
+  constexpr int kSmem = kThreads * 16 * sizeof(T) * kDepthB;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(qk_norm_rope_bwd_kernel<T, D, kInter>), kSmem, done);
   if (e != cudaSuccess) return e;
@@ -590,7 +616,7 @@ cudaError_t backward(RopeArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t qk_norm_rope_backward_workspace_bytes(int D) { return (size_t)kBwdBlocks * D * sizeof(float); }
+size_t qk_norm_rope_backward_workspace_bytes(int D) { return (size_t)kBwdBlocks * 2 * D * sizeof(float); }
 
 cudaError_t launch_qk_norm_rope(RopeArgs a, cudaStream_t s) {
   switch (a.D) {
