@@ -4,14 +4,15 @@
 // Pairs are (j, j + R/2), or (2j, 2j + 1) when interleaved. Forward (dense outputs, or k and v left
 // in a cache's pages) and gradient.
 //
-// Layout: D/16 lanes hold one head, two runs of eight elements each: lane l of the rotated part those at
+// Layout: D/16 lanes hold one head, two runs of eight elements each (in the gradient D/8 lanes, runs of four): lane l of the rotated part those at
 // 8 l and R/2 + 8 l, the lanes of the rest likewise. So neighbouring lanes read and write neighbouring 16
 // bytes, and both members of a pair lie in one lane, in the half-split form (run against run) and in the
 // interleaved one (neighbours). The head's sum of squares is the only exchange (shuffles).
 //
-// A block takes the heads of one kind (queries, keys, or values to be copied) of a few tokens: it forms
-// the tokens' cosines and sines once in shared memory, one entry a thread, and its warps then walk the
-// (token, head) rows. Forming them in every warp instead cost a third of the instructions.
+// A block takes the heads of one kind (queries, keys, or values to be copied; in the gradient queries and
+// then keys) of a few tokens: it forms the tokens' cosines and sines once in shared memory, one entry a
+// thread, and its warps then walk the (token, head) rows. Forming them in every warp instead cost a third of
+// the instructions.
 //
 // Angles: pos inv_freq is formed in turns modulo one by 64-bit integer arithmetic (inv_freq / 2 pi as
 // a 64-bit binary fraction, times the position, dropping whole turns), exact to 2^-32 turn at any
@@ -264,7 +265,7 @@ __device__ __forceinline__ void load_weights(const float* w, int off0, int off1,
   }
 }
 
-// The (token, head) row `x` of a block's tokens: token and head by one multiplication (x < 2^16).
+// The (token, head) row `x` of a block's tokens: token and head by one multiplication.
 __device__ __forceinline__ void row_at(int x, int H, uint32_t magic, int& t, int& h) {
   t = (int)__umulhi((uint32_t)x, magic);
   h = x - t * H;
@@ -514,23 +515,26 @@ __global__ void __launch_bounds__(kThreads, kPerSM) qk_norm_rope_bwd_kernel(cons
   }
 }
 
-// dw: a block adds 32 columns of one kind's partial rows, 32 rows of threads taking every 32nd row, then
-// those by a fixed tree.
+// dw: a block adds eight columns of one kind's partial rows: a thread every 128th row of one column (all of
+// them in flight), then those by a fixed tree.
 __global__ void __launch_bounds__(1024) qk_norm_rope_bwd_join_kernel(const RopeArgs a) {
-  __shared__ float tile[32][33];
+  __shared__ float tile[8][33];
   ptx::wait_prerequisite();
-  const int kind = blockIdx.y, first = kind ? a.blocks[0] : 0, rows = a.blocks[0];
-  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
-  const float* p = a.partial + (long long)first * a.D + blockIdx.x * 32 + lane;
+  const int kind = blockIdx.y, rows = a.blocks[0];
+  const int col = threadIdx.x & 7, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float* p = a.partial + (long long)kind * rows * a.D + blockIdx.x * 8 + col;
   float sum = 0.f;
 #pragma unroll 8
-  for (int r = part; r < rows; r += 32) sum += p[(long long)r * a.D];
-  tile[part][lane] = sum;
+  for (int r = threadIdx.x >> 3; r < rows; r += 128) sum += p[(long long)r * a.D];
+  sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+  sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+  if (lane < 8) tile[lane][warp] = sum;
   __syncthreads();
-  sum = tile[lane][part];   // warp `part` adds column 32 blockIdx.x + part
+  if (warp >= 8) return;   // warp w adds column w
+  sum = tile[warp][lane];
 #pragma unroll
   for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-  if (lane == 0) (kind ? a.dk_w : a.dq_w)[blockIdx.x * 32 + part] = sum;
+  if (lane == 0) (kind ? a.dk_w : a.dq_w)[blockIdx.x * 8 + warp] = sum;
 }
 
 // Tokens of a block so that its rows come to about `rows`, within the shared memory for angles.
@@ -595,7 +599,7 @@ cudaError_t backward_of(RopeArgs& a, cudaStream_t s) {
   e = cudaGetLastError();
   if (e == cudaSuccess) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(D / 32, 2);
+    cfg.gridDim = dim3(D / 8, 2);
     cfg.blockDim = dim3(1024);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

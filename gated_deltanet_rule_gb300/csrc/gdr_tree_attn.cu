@@ -1011,6 +1011,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // time: the loop is bound by their latency (38 parts of 224 rows of 256: 33 us by one warp a row, one part
 // after the other).
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+// Blocks an SM: as many as fit at once, or the rest would begin their set-up only when the first kernel has
+// ended (16 rows of 13 nodes, 8 of 64: 74.6 and 95.4 us with 3, 73.6 and 93.6 with 4, 74.3 and 94.1 with 8).
+constexpr int kJoinPerSM = 4;
 template <int D, int kRows, int KT>
 __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const __grid_constant__ Args a) {
   constexpr int kVec = D / 32;
@@ -1018,42 +1021,50 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const __gr
   __shared__ float s_sum[kJoinWarps];
   __shared__ int s_part[kBlocks];
   __shared__ long long s_warps[kJoinWarps], s_unit;
+  __shared__ int s_first, s_last;
   __shared__ Place s_item;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // the item, and the blocks that hold its parts: from the rows alone, before the first kernel has ended
-  if (tid == 0) s_item.tiles = 0;
+  if (tid == 0) s_first = s_last = 0;
   const Rows rows = count_rows<KT>(a, s_warps, false);
   Place p;
+  bool mine = false;   // one thread has the item, if there is one
+  long long unit;
   if (a.items <= kBlocks) {   // a block of the grid for each item
     p.b = blockIdx.x / (a.Hk * a.mts);
     if (p.b >= rows.r0 && p.b < rows.r1) {
       p.hk = blockIdx.x / a.mts % a.Hk;
       p.mt = blockIdx.x % a.mts;
-      s_unit = rows.before;
+      unit = rows.before;
       for (int b = rows.r0; b < p.b; ++b) {
         row_of(a, b, p.n, p.ctx);
-        s_unit += units_of<KT>(a, p.n, p.ctx) * a.Hk;
+        unit += units_of<KT>(a, p.n, p.ctx) * a.Hk;
       }
       row_of(a, p.b, p.n, p.ctx);
       if (p.mt * a.npi < p.n) {
-        s_unit += units_of<KT>(a, p.n, p.ctx) * p.hk;
-        for (int mt = 0; mt < p.mt; ++mt) s_unit += tiles_of<KT>(a, p.n, p.ctx, mt) + kPad;
+        unit += units_of<KT>(a, p.n, p.ctx) * p.hk;
+        for (int mt = 0; mt < p.mt; ++mt) unit += tiles_of<KT>(a, p.n, p.ctx, mt) + kPad;
         p.tiles = tiles_of<KT>(a, p.n, p.ctx, p.mt);
-        s_item = p;
+        mine = true;
       }
     }
   } else {                    // for each block of the first kernel: the item that its share's last unit lies in
     const long long x0 = first_unit(rows.total, blockIdx.x), x1 = first_unit(rows.total, blockIdx.x + 1);
-    if (x1 > x0 && locate<KT>(a, rows, x1 - 1, p) && x1 - 1 - p.unit >= x0 && p.unit < p.tiles) {
-      s_unit = x1 - 1 - p.unit;
-      s_item = p;
+    if (x1 > x0 && locate<KT>(a, rows, x1 - 1, p)) {
+      unit = x1 - 1 - p.unit;
+      mine = unit >= x0 && p.unit < p.tiles;
     }
+  }
+  if (mine) {
+    s_item = p;
+    s_unit = unit;
+    s_first = block_of(rows.total, unit);
+    s_last = block_of(rows.total, unit + p.tiles - 1);
   }
   __syncthreads();
   p = s_item;
-  const bool begins = p.tiles > 0;
-  const long long unit = begins ? s_unit : 0;
-  const int first = begins ? block_of(rows.total, unit) : 0, last = begins ? block_of(rows.total, unit + p.tiles - 1) : 0;
+  unit = s_unit;
+  const int first = s_first, last = s_last;
   const int b = p.b, hk = p.hk, mt = p.mt, n = p.n;
   const int node0 = mt * a.npi, nodes = min(a.npi, n - node0);
   // the parts' places, block by block (-1: a block without units). A block's first segment is its part 0:
@@ -1204,10 +1215,10 @@ cudaError_t launch(const TreeAttnArgs& p, cudaStream_t st) {
   tree_attn_kernel<D, kForm><<<kBlocks, kThreads, C::kSmem, st>>>(mq, mk, mv, a);
   stage_timer_end(slot, st);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  // shares of an item's rows: about eight blocks a SM in all, one row each at most
+  // shares of an item's rows, one row each at least
   const int x = std::min(a.items, kBlocks);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(x, std::max(1, std::min(a.npi * a.G, kNumSMs * 8 / x)));
+  cfg.gridDim = dim3(x, std::max(1, std::min(a.npi * a.G, kNumSMs * kJoinPerSM / x)));
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
