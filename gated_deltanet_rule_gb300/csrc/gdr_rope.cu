@@ -4,10 +4,11 @@
 // Pairs are (j, j + R/2), or (2j, 2j + 1) when interleaved. Forward (dense outputs, or k and v left
 // in a cache's pages) and gradient.
 //
-// Layout: D/16 lanes hold one head, two runs of eight elements each (in the gradient D/8 lanes, runs of four): lane l of the rotated part those at
-// 8 l and R/2 + 8 l, the lanes of the rest likewise. So neighbouring lanes read and write neighbouring 16
-// bytes, and both members of a pair lie in one lane, in the half-split form (run against run) and in the
-// interleaved one (neighbours). The head's sum of squares is the only exchange (shuffles).
+// Layout: D/16 lanes hold one head, two runs of eight elements each (in the gradient D/8 lanes, runs of
+// four): lane l of the rotated part those at 8 l and R/2 + 8 l, the lanes of the rest likewise. So
+// neighbouring lanes read and write neighbouring 16 bytes, and both members of a pair lie in one lane, in
+// the half-split form (run against run) and in the interleaved one (neighbours). The head's sum of squares
+// is the only exchange (shuffles).
 //
 // A block takes the heads of one kind (queries, keys, or values to be copied; in the gradient queries and
 // then keys) of a few tokens: it forms the tokens' cosines and sines once in shared memory, one entry a

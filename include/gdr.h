@@ -456,8 +456,9 @@ gdr_status gdr_verify_draft(const int32_t* tokens, const int32_t* parents, const
  *   not overlap ctx.
  * A row is refused, untouched, with GDR_ERR_DEVICE_INDEX, if its index is out of range, an earlier
  * entry lists it too, a fork's source is itself listed as dst, its context or pages are out of range
- * (reserve: or fewer than its context needs), or its path does not rise inside the table. Where pages
- * run out (GDR_ERR_NO_PAGES) a row to be reserved stays as it was and a row to be forked is left empty.
+ * (reserve: or fewer than its context needs, or one behind an empty entry), or its path does not rise
+ * inside the table. Where pages run out (GDR_ERR_NO_PAGES) a row to be reserved stays as it was and a row
+ * to be forked is left empty.
  */
 size_t gdr_cache_workspace_bytes(int F, int M);
 gdr_status gdr_cache_reserve(int32_t* table, const int32_t* ctx, int32_t* refs, const int32_t* rows, int extra,

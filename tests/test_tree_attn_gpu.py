@@ -115,6 +115,18 @@ def test_long_context_is_split_over_blocks(D, page):
     _check(c, *_run(c))
 
 
+@pytest.mark.parametrize("B,N,Hq,Hk,D,seed", [(40, 2, 5, 5, 64, 0), (40, 2, 5, 5, 64, 1), (40, 1, 10, 5, 128, 2), (7, 2, 6, 3, 128, 3),
+                                              (31, 1, 5, 5, 256, 4), (9, 20, 10, 1, 64, 5), (60, 70, 6, 3, 64, 6)])
+def test_shares_begin_anywhere(B, N, Hq, Hk, D, seed):
+    """Items of all lengths, more and fewer than blocks: shares begin and end inside items, at their ends and
+    between them."""
+    g = torch.Generator().manual_seed(seed)
+    most = 2500 if N < 20 else 900
+    ctx = (most * torch.rand(B, generator=g) ** 2).int().tolist()
+    c = _case(B, N, Hq, Hk, D, 16, ctx, "tree", seed=seed, lengths=[N, N, max(1, N // 2)])
+    _check(c, *_run(c))
+
+
 def test_chain_of_many_nodes_is_a_prefill():
     c = _case(2, 300, 4, 2, 128, 64, [0, 77], "chain", seed=6, lengths=[300, 211])
     _check(c, *_run(c))
