@@ -234,23 +234,25 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactArgs a) 
   extern __shared__ long long slots[];   // from [W], to [W]
   __shared__ int first_move;
   const int b = blockIdx.x, tid = threadIdx.x;
-  const int n = __ldg(a.n_path + b), ctx = __ldg(a.ctx + b);
+  const int n = __ldg(a.n_path + b), ctx = __ldg(a.ctx + b), shift = __ffs(a.page) - 1;
   const int32_t* path = a.path + (size_t)b * a.W;
   const int32_t* table = a.table + (size_t)b * a.M;
+  // (few moves are bound by the latency of dependent reads: the path's do not wait for its length)
+  const int node0 = tid < a.W ? __ldg(path + tid) : 0, before0 = tid > 0 && tid <= a.W ? __ldg(path + tid - 1) : -1;
   bool bad = n < 0 || n > a.W || ctx < 0;
   if (tid == 0) first_move = a.W;
   __syncthreads();
   if (!bad) {
     for (int i = tid; i < n; i += kThreads) {
-      const int node = __ldg(path + i), before = i ? __ldg(path + i - 1) : -1;
+      const int node = i == tid ? node0 : __ldg(path + i), before = i == tid ? before0 : __ldg(path + i - 1);
       const long long from = (long long)ctx + node, to = (long long)ctx + i;
       // to's page too has to be there: from's are checked below to rise through it
       bool off = node <= before || node < i || from >= (long long)a.M * a.page;
       if (!off) {
-        const int pf = __ldg(table + from / a.page), pt = __ldg(table + to / a.page);
+        const int pf = __ldg(table + (from >> shift)), pt = __ldg(table + (to >> shift));
         off = pf < 0 || pf >= a.P || pt < 0 || pt >= a.P;
-        slots[i] = (long long)pf * a.page + from % a.page;
-        slots[a.W + i] = (long long)pt * a.page + to % a.page;
+        slots[i] = (long long)pf * a.page + (from & (a.page - 1));
+        slots[a.W + i] = (long long)pt * a.page + (to & (a.page - 1));
       }
       bad |= off;
       if (node != i) atomicMin(&first_move, i);

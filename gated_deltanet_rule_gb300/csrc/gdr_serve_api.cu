@@ -65,8 +65,8 @@ gdr_status check_pages(int P, int page, int M, const char* who) {
   if (P < 1 || M < 1) return fail(GDR_ERR_INVALID_ARG, "%s: sizes must be >= 1 (P=%d M=%d)", who, P, M);
   if (page != 16 && page != 32 && page != 64 && page != 128)
     return fail(GDR_ERR_UNSUPPORTED, "%s: pages of %d positions are not implemented (16, 32, 64 or 128)", who, page);
-  if ((long long)M * page > 0x7fffffffll)
-    return fail(GDR_ERR_UNSUPPORTED, "%s: M*page=%lld positions exceed 2^31 - 1", who, (long long)M * page);
+  if ((long long)M * page > 0x7fffff00ll)   // (kernels count positions in whole tiles of up to 128)
+    return fail(GDR_ERR_UNSUPPORTED, "%s: M*page=%lld positions exceed 2^31 - 256", who, (long long)M * page);
   return GDR_OK;
 }
 

@@ -331,10 +331,10 @@ gdr_status gdr_backward_chunked_saved(const void* q, const void* k, const void* 
  *   table [rows, M] int32                  row b's positions [m page, (m+1) page) live in page
  *                                          table[b][m]; -1 where the row holds none
  *   ctx   [rows] int32                     committed positions of each row
- * page is 16, 32, 64 or 128; D is 64, 128 or 256; Hq is a multiple of Hk (query head h reads key
- * head h / (Hq / Hk)). Drafted nodes 0 .. N-1 of row b (node 0 the last committed token, whose
- * keys are not in the cache yet; every node after its parent) take positions ctx[b] .. ctx[b]+N-1
- * until the accepted ones are moved to the front; lengths [B] int32 (NULL = N) gives each row's
+ * page is 16, 32, 64 or 128 and M page at most 2^31 - 256; D is 64, 128 or 256; Hq is a multiple of Hk
+ * (query head h reads key head h / (Hq / Hk)). Drafted nodes 0 .. N-1 of row b (node 0 the last committed
+ * token, whose keys are not in the cache yet; every node after its parent) take positions ctx[b] ..
+ * ctx[b]+N-1 until the accepted ones are moved to the front; lengths [B] int32 (NULL = N) gives each row's
  * nodes. A length outside [0, N], a context that leaves the table, or a page outside [0, P) is
  * recorded as GDR_ERR_DEVICE_INDEX.
  * ---------------------------------------------------------------------------------------------
