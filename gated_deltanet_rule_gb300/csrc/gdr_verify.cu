@@ -15,12 +15,13 @@
 // once, so the walk runs in shared memory), and a pass splits the vocabulary over the cluster's 64
 // warps, each a contiguous run of 128-entry chunks (four entries a lane, 16-byte loads where rows are
 // aligned), whose sums the blocks exchange through distributed shared memory. The token is then found
-// step by step: block, warp, an eighth of its run, ... , chunk, lane, entry.
+// step by step: block, warp, an eighth of its run, ... , and then chunk, lane and entry at once.
 // A pass is bound by the latency of its loads and, over many rows, by its arithmetic (about 20
 // instructions an entry); blocks of 256 threads keep 48 rows of 131072 entries resident at once.
-// Measured (V = 131072): a float32 chain of 8 in 10.3 us, 48 bfloat16 trees of 16 in 39.1 us. Steps: float64
-// reductions and scalars 17.8 / 104 us; pairs of floats in the passes, four entries a lane, asynchronous
-// copies 12.4 / 41.0 us; pairs in the walk and the search as well, the present figures. Clusters of sixteen
+// Measured: a float32 chain of 6 over 32000 entries 8.5 us, 48 float32 trees of 24 over 131072 39 us. Steps:
+// float64 reductions and scalars 17.8 / 104 us; pairs of floats in the passes, four entries a lane,
+// asynchronous copies 12.4 / 41.0 us; pairs in the walk and the search as well 10.2 / 39 us; the last chunks
+// searched at once by one warp, first nodes read along with the length 8.5 / 39 us. Clusters of sixteen
 // shorten a row's pass but no longer keep the rows resident: 12.4 / 50.5 us against 12.4 / 41.0. Two chunks
 // at a time spill: 11.0 / 44.1 us.
 //
@@ -41,6 +42,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kChunk4 = 128;   // entries of a chunk: four a lane
 constexpr int kAhead = 8;      // chunks of p and q on their way to a thread
+constexpr int kLast = 4;       // chunks that one warp searches at once
 constexpr unsigned kAll = 0xffffffffu;
 
 __device__ __forceinline__ float above_zero(float x) { return x > 0.f ? x : 0.f; }   // nan and negatives count as 0
@@ -272,23 +274,6 @@ struct Dist {
     }
     return lanes_sum<32>(both(add(acc[0], acc[1])));
   }
-  // Sums of up to four chunks c0 .. c0 + n - 1, one by one.
-  __device__ __forceinline__ void each(int c0, int n, Pair* sums) const {
-    const int lane = threadIdx.x & 31;
-    float pv[4][4], qv[4][4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = k < n ? (c0 + k) * kChunk4 + 4 * lane : V;
-      load4<kVec>(p, i, V, pv[k]);
-      if (q) load4<kVec>(q, i, V, qv[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      Pair2 rho[2];
-      of(pv[k], qv[k], k < n ? (c0 + k) * kChunk4 + 4 * lane : V, rho);
-      sums[k] = lanes_sum<32>(both(add(rho[0], rho[1])));
-    }
-  }
 };
 
 // Of kParts <= 32 parts (lane r holds part r's sum), the first whose running sum passes the target; the
@@ -323,7 +308,6 @@ __host__ __device__ constexpr int ring_at(int N) { return (N * 28 + 15) & ~15; }
 struct Shared {
   Pair ctas[2][kCluster];   // totals of the cluster's blocks, by pass parity
   Pair warps[kWarps];
-  Pair chunks[32];
   Pair c, target;
   int cur, n_gone, act, found, c0, c1;
 };
@@ -342,21 +326,25 @@ __global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCluster, 1, 1) 
   uint8_t* ring = dyn + ring_at(a.N);
   const int b = blockIdx.x / kCluster, rank = (int)ptx::cluster_ctarank();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const size_t row = (size_t)b * a.N;
+  // (a thread's first node is read along with the length)
   const int n = __ldg(a.lengths + b);
+  const bool there = tid + 1 < a.N;
+  const int parent1 = there ? __ldg(a.parents + row + tid + 1) : 0, token1 = there ? __ldg(a.tokens + row + tid + 1) : 0;
+  const float u1 = there ? __ldg(a.u + row + tid + 1) : 0.f;
   if (n < 0 || n > a.N) {   // the same in every block of the cluster
     if (rank == 0 && tid == 0) atomicCAS(a.err, 0, kErrDeviceIndex);
     return;
   }
   // (no block writes to another's shared memory before that one has started: arrived here, waited for below)
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  const size_t row = (size_t)b * a.N;
   const T* P = static_cast<const T*>(a.p) + row * a.V;
   const T* Q = a.q ? static_cast<const T*>(a.q) + row * a.V : nullptr;
   const float u_next = __ldg(a.u_next + b);
   for (int i = tid + 1; i < n; i += kThreads) {
-    int parent = __ldg(a.parents + row + i);
-    const int t = __ldg(a.tokens + row + i);
-    s_u[i] = __ldg(a.u + row + i);
+    int parent = i == tid + 1 ? parent1 : __ldg(a.parents + row + i);
+    const int t = i == tid + 1 ? token1 : __ldg(a.tokens + row + i);
+    s_u[i] = i == tid + 1 ? u1 : __ldg(a.u + row + i);
     if (parent < 0 || parent >= i || t < 0 || t >= a.V) {
       atomicCAS(a.err, 0, kErrDeviceIndex);
       parent = -1;
@@ -503,26 +491,18 @@ __global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCluster, 1, 1) 
       const Dist<T, kVec> dist{P + (size_t)sh.cur * a.V, (Q && sh.c.hi != 0.f) ? Q + (size_t)sh.cur * a.V : nullptr,
                                sh.c.hi, sh.c.lo, s_gone, sh.n_gone, a.V};
       int c0 = sh.c0, c1 = sh.c1;
-      while (c1 - c0 > 1) {
-        // a step down: to an eighth of the range, or, where a warp has four chunks or fewer, to the chunk
+      while (c1 - c0 > kLast) {   // a step down: to an eighth of the range
         const int per = (c1 - c0 + kWarps - 1) / kWarps;
-        const bool chunk = per <= 4;
         const int mine0 = min(c1, c0 + warp * per), mine1 = min(c1, mine0 + per);
-        if (chunk) {
-          Pair sums[4];
-          dist.each(mine0, mine1 - mine0, sums);
-          if (lane < 4) sh.chunks[4 * warp + lane] = lane == 0 ? sums[0] : lane == 1 ? sums[1] : lane == 2 ? sums[2] : sums[3];
-        } else {
-          const Pair mine = dist.sum(mine0, mine1, ring);
-          if (lane == 0) sh.warps[warp] = mine;
-        }
+        const Pair mine = dist.sum(mine0, mine1, ring);
+        if (lane == 0) sh.warps[warp] = mine;
         __syncthreads();
         if (warp == 0) {
           Pair target = sh.target;
-          const int w = max(0, chunk ? pick<32>(sh.chunks[lane], target) : pick<kWarps>(sh.warps[lane & (kWarps - 1)], target));
+          const int w = max(0, pick<kWarps>(sh.warps[lane & (kWarps - 1)], target));
           if (lane == 0) {
-            sh.c0 = chunk ? c0 + (w >> 2) * per + (w & 3) : c0 + w * per;
-            sh.c1 = chunk ? sh.c0 + 1 : min(c1, c0 + (w + 1) * per);
+            sh.c0 = c0 + w * per;
+            sh.c1 = min(c1, c0 + (w + 1) * per);
             sh.target = target;
           }
         }
@@ -530,19 +510,44 @@ __global__ void __launch_bounds__(kThreads, 3) __cluster_dims__(kCluster, 1, 1) 
         c0 = sh.c0;
         c1 = sh.c1;
       }
-      if (warp == 0) {
-        const int at = c0 * kChunk4 + 4 * lane;
-        float pv[4], qv[4];
-        load4<kVec>(dist.p, at, a.V, pv);
-        if (dist.q) load4<kVec>(dist.q, at, a.V, qv);
-        Pair2 two[2];
-        dist.of(pv, qv, at, two);
-        Pair rho[4];
-        halves(two[0], rho[0], rho[1]);
-        halves(two[1], rho[2], rho[3]);
+      if (warp == 0) {   // the last chunks at once: the chunk, the lane, the entry
         Pair target = sh.target;
-        const int who = max(0, pick<32>(add(add(rho[0], rho[1]), add(rho[2], rho[3])), target));
+        Pair rho[4], lanes[kLast], mine = {0.f, 0.f};
+        float pv[kLast][4], qv[kLast][4];
+#pragma unroll
+        for (int k = 0; k < kLast; ++k) {
+          const int i = c0 + k < c1 ? (c0 + k) * kChunk4 + 4 * lane : a.V;
+          load4<kVec>(dist.p, i, a.V, pv[k]);
+          if (dist.q) load4<kVec>(dist.q, i, a.V, qv[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < kLast; ++k) {
+          Pair2 two[2];
+          dist.of(pv[k], qv[k], c0 + k < c1 ? (c0 + k) * kChunk4 + 4 * lane : a.V, two);
+          lanes[k] = both(add(two[0], two[1]));
+          const Pair sum = lanes_sum<32>(lanes[k]);
+          if (lane == k) mine = sum;
+        }
+        const int chunk = max(0, pick<kLast>(mine, target));
+        Pair at_lane = lanes[0];
+#pragma unroll
+        for (int k = 1; k < kLast; ++k) {
+          if (chunk == k) {
+            at_lane = lanes[k];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              pv[0][e] = pv[k][e];
+              qv[0][e] = qv[k][e];
+            }
+          }
+        }
+        const int who = max(0, pick<32>(at_lane, target));
         if (lane == who) {
+          const int at = (c0 + chunk) * kChunk4 + 4 * lane;
+          Pair2 two[2];
+          dist.of(pv[0], qv[0], at, two);
+          halves(two[0], rho[0], rho[1]);
+          halves(two[1], rho[2], rho[3]);
           int token = at;
           bool found = false;
           Pair run = {0.f, 0.f};
