@@ -61,15 +61,17 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const CacheArgs a) {
         bad = __syncthreads_or(off);
         need = n % a.page ? 1 : 0;
       } else {
-        for (int m0 = 0; m0 < a.M; m0 += kThreads) {   // pages held: the leading entries
+        bool lost = false;                              // a page behind a gap
+        for (int m0 = 0; m0 < a.M; m0 += kThreads) {    // pages held: the leading entries
           const int m = m0 + tid;
-          const int held = __syncthreads_count(m < a.M && row[m] >= 0);
+          const bool holds = m < a.M && row[m] >= 0;
+          const int held = __syncthreads_count(holds);
+          lost |= holds && tid >= held;
           have += held;
           if (held < kThreads) break;
         }
         need = pages > have ? pages - have : 0;
         bad = (long long)have * a.page < n;             // pages of the context that never were there
-        bool lost = false;                              // pages behind a gap would be overwritten
         for (int m = have + tid; m < pages; m += kThreads) lost |= row[m] >= 0;
         if (__syncthreads_or(lost)) bad = true;
       }

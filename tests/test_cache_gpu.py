@@ -94,6 +94,18 @@ def test_reserve_refuses_a_gap():
     assert d[2][0].tolist() == want[0].tolist() and d[2][1].tolist() == pool.table[1]
 
 
+@pytest.mark.parametrize("extra", [10, 30, 60])   # the new pages end before the page behind the gap, at it, past it
+def test_reserve_never_fills_around_a_gap(extra):
+    pool, d = _pool([40], 2, 8, 16)
+    d[2][0, 4] = 0   # (row 0 holds entries 0 .. 2)
+    want = d[2].clone(), d[4].clone()
+    gdr.gdr_cache_reserve(*d[2:], _i([0]), extra, 16)
+    with pytest.raises(gdr.GdrError) as e:
+        gdr.gdr_sync_status()
+    assert e.value.status == gdr.GDR_ERR_DEVICE_INDEX
+    assert torch.equal(d[2], want[0]) and torch.equal(d[4], want[1])
+
+
 def test_many_rows_and_pages():
     """More rows than one block's threads, more pages than one pass of the search."""
     F = 1500
