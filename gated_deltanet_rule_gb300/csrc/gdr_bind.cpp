@@ -24,9 +24,10 @@ struct Error {};   // a Python exception has been set
   throw Error{};
 }
 
-// Argument i as a tensor (NULL for None where that is allowed).
+// Argument i as a tensor (NULL for None where that is allowed). The last argument is the launch stream.
 struct Call {
   PyObject* const* args;
+  int last;
   const Tensor* tensor(int i, const char* name, bool none = false) const {
     if (none && args[i] == Py_None) return nullptr;
     if (!THPVariable_Check(args[i])) refuse("%s must be a tensor", name);
@@ -58,17 +59,34 @@ struct Call {
   }
   bool truth(int i) const { return PyObject_IsTrue(args[i]) == 1; }
   // the stream's raw handle, or None for the current stream
-  gdr_stream_t stream(int i) const {
-    if (args[i] == Py_None) return reinterpret_cast<gdr_stream_t>(c10::cuda::getCurrentCUDAStream().stream());
-    return static_cast<gdr_stream_t>(PyLong_AsVoidPtr(args[i]));
+  gdr_stream_t stream() const {
+    if (args[last] == Py_None) return reinterpret_cast<gdr_stream_t>(c10::cuda::getCurrentCUDAStream().stream());
+    return static_cast<gdr_stream_t>(PyLong_AsVoidPtr(args[last]));
+  }
+  // A new tensor, of the launch stream's memory: the allocator hands memory out again in the order of the
+  // stream it was taken for, so a workspace that is dropped when the call returns, or an output that the
+  // caller drops, is not given to anyone whose work does not come after the kernels. An output (kept) may be
+  // read on the current stream as well, and is not handed out again before that stream is past the reads.
+  Tensor empty(at::IntArrayRef shape, at::ScalarType type, const Tensor& near, bool kept) const {
+    const auto options = near.options().dtype(type);
+    if (args[last] == Py_None) return at::empty(shape, options);
+    struct Back {   // the current stream, set again on the way out
+      c10::cuda::CUDAStream stream;
+      ~Back() { c10::cuda::setCurrentCUDAStream(stream); }
+    } back{c10::cuda::getCurrentCUDAStream(near.get_device())};
+    c10::cuda::setCurrentCUDAStream(
+        c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(PyLong_AsVoidPtr(args[last])), near.get_device()));
+    Tensor t = at::empty(shape, options);
+    if (kept) t.record_stream(back.stream.unwrap());
+    return t;
   }
   // an output: the caller's, or a new one like `near`
   Tensor output(int i, const char* name, at::IntArrayRef shape, at::ScalarType type, const Tensor& near) const {
-    if (args[i] == Py_None) return at::empty(shape, near.options().dtype(type));
+    if (args[i] == Py_None) return empty(shape, type, near, true);
     return *of(i, name, type, shape);
   }
   Tensor workspace(int i, size_t bytes, const Tensor& near) const {
-    if (args[i] == Py_None) return at::empty({(int64_t)(bytes < 16 ? 16 : bytes)}, near.options().dtype(at::kByte));
+    if (args[i] == Py_None) return empty({(int64_t)(bytes < 16 ? 16 : bytes)}, at::kByte, near, false);
     return *tensor(i, "ws");
   }
 };
@@ -179,7 +197,7 @@ PyObject* norm_rope(const Call& c) {
   Tensor k_out = c.output(9, "k_out", r.k->sizes(), r.q->scalar_type(), *r.q);
   check(gdr_qk_norm_rope(ptr(r.q), ptr(r.k), ptr<float>(r.q_w), ptr<float>(r.k_w), ptr<double>(r.inv_freq),
                          ptr<int32_t>(r.pos), (float)c.number(6), c.truth(7), q_out.data_ptr(), k_out.data_ptr(), r.B, r.N,
-                         r.Hq, r.Hk, r.D, r.R, r.qs.tok, r.qs.head, r.ks.tok, r.ks.head, r.dt, c.stream(10)));
+                         r.Hq, r.Hk, r.D, r.R, r.qs.tok, r.qs.head, r.ks.tok, r.ks.head, r.dt, c.stream()));
   return wrap({q_out, k_out});
 }
 
@@ -196,7 +214,7 @@ PyObject* norm_rope_append(const Call& c) {
                                 ptr<int32_t>(r.pos), (float)c.number(12), c.truth(13), q_out.data_ptr(), ptr(p.k), ptr(p.v),
                                 ptr<int32_t>(p.table), ptr<int32_t>(p.ctx), ptr<int32_t>(lengths), p.P, p.page, p.M, r.B,
                                 r.N, r.Hq, r.Hk, r.D, r.R, r.qs.tok, r.qs.head, r.ks.tok, r.ks.head, vs.tok, vs.head, r.dt,
-                                c.stream(15)));
+                                c.stream()));
   return THPVariable_Wrap(q_out);
 }
 
@@ -204,14 +222,13 @@ PyObject* norm_rope_append(const Call& c) {
 PyObject* norm_rope_backward(const Call& c) {
   const Rope r(c, 0);
   const Tensor *dqo = c.of(6, "dq_out", r.q->scalar_type(), r.q->sizes()), *dko = c.of(7, "dk_out", r.q->scalar_type(), r.k->sizes());
-  const auto f32 = r.q->options().dtype(at::kFloat);
-  Tensor dq = at::empty(r.q->sizes(), f32), dk = at::empty(r.k->sizes(), f32);
-  Tensor dq_w = at::empty({r.q->size(3)}, f32), dk_w = at::empty({r.q->size(3)}, f32);
+  auto grad = [&](at::IntArrayRef shape) { return c.empty(shape, at::kFloat, *r.q, true); };
+  Tensor dq = grad(r.q->sizes()), dk = grad(r.k->sizes()), dq_w = grad({r.q->size(3)}), dk_w = grad({r.q->size(3)});
   Tensor ws = c.workspace(10, gdr_qk_norm_rope_backward_workspace_bytes(r.D), *r.q);
   check(gdr_qk_norm_rope_backward(ptr(r.q), ptr(r.k), ptr<float>(r.q_w), ptr<float>(r.k_w), ptr<double>(r.inv_freq),
                                   ptr<int32_t>(r.pos), ptr(dqo), ptr(dko), (float)c.number(8), c.truth(9), ptr<float>(&dq),
                                   ptr<float>(&dk), ptr<float>(&dq_w), ptr<float>(&dk_w), r.B, r.N, r.Hq, r.Hk, r.D, r.R,
-                                  r.qs.tok, r.qs.head, r.ks.tok, r.ks.head, r.dt, ws.data_ptr(), bytes_of(ws), c.stream(11)));
+                                  r.qs.tok, r.qs.head, r.ks.tok, r.ks.head, r.dt, ws.data_ptr(), bytes_of(ws), c.stream()));
   return wrap({dq, dk, dq_w, dk_w});
 }
 
@@ -230,7 +247,7 @@ PyObject* tree_attn(const Call& c) {
   Tensor ws = c.workspace(11, gdr_tree_attn_workspace_bytes((int)D), *q);
   check(gdr_tree_attn(ptr(q), ptr(p.k), ptr(p.v), ptr<int32_t>(p.table), ptr<int32_t>(p.ctx), ptr<int32_t>(lengths),
                       ptr<uint64_t>(mask), (float)scale, o.data_ptr(), with_lse ? ptr<float>(&lse) : nullptr, (int)B, (int)N,
-                      (int)Hq, p.Hk, (int)D, p.P, p.page, p.M, GDR_BF16, ws.data_ptr(), bytes_of(ws), c.stream(12)));
+                      (int)Hq, p.Hk, (int)D, p.P, p.page, p.M, GDR_BF16, ws.data_ptr(), bytes_of(ws), c.stream()));
   return with_lse ? wrap({o, lse}) : THPVariable_Wrap(o);
 }
 
@@ -247,7 +264,7 @@ PyObject* verify(const Call& c) {
   Tensor next = c.output(9, "next_token", {B}, at::kInt, *p);
   check(gdr_verify_draft(ptr<int32_t>(tokens), ptr<int32_t>(parents), ptr<int32_t>(lengths), ptr(p), ptr(q), ptr<float>(u),
                          ptr<float>(u_next), ptr<int32_t>(&path), ptr<int32_t>(&n_path), ptr<int32_t>(&next), (int)B, (int)N,
-                         (int)V, dt, c.stream(10)));
+                         (int)V, dt, c.stream()));
   return wrap({path, n_path, next});
 }
 
@@ -288,7 +305,7 @@ PyObject* cache_reserve(const Call& c) {
   Tensor ws = c.workspace(6, gdr_cache_workspace_bytes(r.F, r.M), *r.table);
   check(gdr_cache_reserve(ptr<int32_t>(r.table), ptr<int32_t>(r.ctx), ptr<int32_t>(r.refs), ptr<int32_t>(r.list),
                           (int)c.integer(4), r.F, r.R, r.M, (int)r.refs->size(0), (int)c.integer(5), ws.data_ptr(),
-                          bytes_of(ws), c.stream(7)));
+                          bytes_of(ws), c.stream()));
   Py_RETURN_NONE;
 }
 
@@ -301,7 +318,7 @@ PyObject* cache_fork(const Call& c) {
   Tensor ws = c.workspace(7, gdr_cache_workspace_bytes(r.F, r.M), *r.table);
   check(gdr_cache_fork(ptr(k.k), ptr(k.v), ptr<int32_t>(r.table), ptr<int32_t>(r.ctx), ptr<int32_t>(r.refs),
                        ptr<int32_t>(src), ptr<int32_t>(r.list), r.F, r.R, r.M, k.layers, k.P, k.page, k.row_bytes,
-                       ws.data_ptr(), bytes_of(ws), c.stream(8)));
+                       ws.data_ptr(), bytes_of(ws), c.stream()));
   Py_RETURN_NONE;
 }
 
@@ -309,7 +326,7 @@ PyObject* cache_fork(const Call& c) {
 PyObject* cache_free(const Call& c) {
   const Rows r(c, 0, 3, "rows");
   check(gdr_cache_free(ptr<int32_t>(r.table), ptr<int32_t>(r.ctx), ptr<int32_t>(r.refs), ptr<int32_t>(r.list), r.F, r.R,
-                       r.M, (int)r.refs->size(0), c.stream(4)));
+                       r.M, (int)r.refs->size(0), c.stream()));
   Py_RETURN_NONE;
 }
 
@@ -324,7 +341,7 @@ PyObject* cache_compact(const Call& c) {
   Tensor new_ctx = c.output(6, "new_ctx", {B}, at::kInt, *ctx);
   check(gdr_cache_compact(ptr(k.k), ptr(k.v), ptr<int32_t>(table), ptr<int32_t>(ctx), ptr<int32_t>(path),
                           ptr<int32_t>(n_path), ptr<int32_t>(&new_ctx), (int)B, (int)path->size(1), (int)table->size(1),
-                          k.layers, k.P, k.page, k.row_bytes, c.stream(7)));
+                          k.layers, k.P, k.page, k.row_bytes, c.stream()));
   return THPVariable_Wrap(new_ctx);
 }
 
@@ -336,7 +353,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return nullptr;
   }
   try {
-    return kFn(Call{args});
+    return kFn(Call{args, kArgs - 1});
   } catch (const Error&) {
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
