@@ -4,8 +4,8 @@ The attention-layer operators go through a compiled binding (_gdr_bind, csrc/gdr
 calls through ctypes.
 
 Each function checks tensor devices, dtypes, shapes and contiguity, allocates outputs the
-caller did not pass (torch.empty: memory plumbing, no arithmetic), hands raw device pointers
-and the current CUDA stream to the library and raises ``GdrError`` on a non-OK status. Every
+caller did not pass (memory of the launch stream: plumbing, no arithmetic), hands raw device pointers
+and the current CUDA stream, or the one given, to the library and raises ``GdrError`` on a non-OK status. Every
 step of the computation runs in the library's kernels; there is no CPU fallback: if
 ``libgdr.so`` is missing this module raises instead of computing anything.
 """
@@ -157,6 +157,21 @@ def _stream(stream) -> int:
     return stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A new output or workspace, of the launch stream's memory: the allocator hands memory out again in
+    the order of the stream it was taken for, so what is dropped while the kernels run goes to nobody
+    whose work does not come after them. The current stream may read it too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):   # any object with the raw handle
+        raw = stream.cuda_stream
+        stream = torch.cuda.ExternalStream(raw, device) if raw else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.float32:
         return GDR_F32
@@ -200,15 +215,15 @@ def gdr_chunk_fwd(q, k, v, g, beta, S0=None, o=None, S_T=None, ws=None, stream=N
     B, L, Hk, Hv, Dk = _check_inputs(q, k, v, g, beta)
     dt = _dtype_code(q)
     if o is None:
-        o = torch.empty_like(v)
+        o = _empty(v.shape, v.dtype, v.device, stream)
     if S_T is None and final_state:
-        S_T = torch.empty(B, Hv, Dk, v.shape[3], device=v.device, dtype=torch.float32)
+        S_T = _empty((B, Hv, Dk, v.shape[3]), torch.float32, v.device, stream)
     for name, t in (("S0", S0), ("S_T", S_T)):
         if t is not None:
             _need(t.dtype == torch.float32 and t.is_contiguous() and t.is_cuda, f"{name} must be contiguous CUDA float32")
     need = workspace_bytes(B, L, Hk, Hv, Dk, q.dtype)
     if need and ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws = _empty(need, torch.uint8, q.device, stream)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     if lengths is None:
         _check(lib().gdr_chunk_fwd(_p(q), _p(k), _p(v), _p(g), _p(beta), _p(S0), _p(o), _p(S_T),
@@ -230,12 +245,12 @@ def gdr_chunk_fwd_gated(q, k, v, g, beta, S0, z, w, eps: float, out=None, S_T=No
     _need(z.is_cuda and z.dtype == torch.bfloat16 and z.shape == v.shape and z.is_contiguous(), "z: contiguous CUDA bf16 like v")
     _need(w.is_cuda and w.dtype == torch.float32 and w.shape == (Dk,) and w.is_contiguous(), "w: contiguous CUDA float32 [D]")
     if out is None:
-        out = torch.empty_like(v)
+        out = _empty(v.shape, v.dtype, v.device, stream)
     if S_T is None and final_state:
-        S_T = torch.empty(B, Hv, Dk, v.shape[3], device=v.device, dtype=torch.float32)
+        S_T = _empty((B, Hv, Dk, v.shape[3]), torch.float32, v.device, stream)
     need = workspace_bytes(B, L, Hk, Hv, Dk, q.dtype)
     if need and ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws = _empty(need, torch.uint8, q.device, stream)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check(lib().gdr_chunk_fwd_gated(_p(q), _p(k), _p(v), _p(g), _p(beta), _p(S0), _p(z), _p(w), float(eps), _p(out),
                                      _p(S_T), B, L, Hk, Hv, Dk, dt, _p(ws), ws_bytes, _stream(stream)))
@@ -255,12 +270,12 @@ def gdr_fork_fwd(q, k, v, g, beta, trunk, trunk_idx, o=None, states_out=None, st
     _need(trunk.is_cuda and trunk.dtype == torch.float32 and trunk.is_contiguous(), "trunk: CUDA float32")
     _need(trunk_idx.is_cuda and trunk_idx.dtype == torch.int64 and trunk_idx.shape == (F,), "trunk_idx: CUDA int64 [F]")
     if o is None:
-        o = torch.empty_like(v)
+        o = _empty(v.shape, v.dtype, v.device, stream)
     if states_out is None and keep:
-        states_out = torch.empty(F, Hv, Dk, v.shape[3], device=v.device, dtype=torch.float32)
+        states_out = _empty((F, Hv, Dk, v.shape[3]), torch.float32, v.device, stream)
     need = fork_workspace_bytes(F, L, Hk, Hv, Dk, q.dtype)
     if need and ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws = _empty(need, torch.uint8, q.device, stream)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check(lib().gdr_fork_fwd(_p(q), _p(k), _p(v), _p(g), _p(beta), _p(trunk), _p(trunk_idx),
                               trunk.shape[0], _p(o), _p(states_out), F, L, Hk, Hv, Dk, dt,
@@ -275,7 +290,7 @@ def gdr_decode_step(q, k, v, g, beta, states, o=None, stream=None):
     dt = _dtype_code(q)
     _need(states.is_cuda and states.dtype == torch.float32 and states.is_contiguous(), "states: CUDA float32")
     if o is None:
-        o = torch.empty_like(v)
+        o = _empty(v.shape, v.dtype, v.device, stream)
     _check(lib().gdr_decode_step(_p(q), _p(k), _p(v), _p(g), _p(beta), _p(states), _p(o),
                                  F, Hk, Hv, Dk, dt, _stream(stream)))
     return o
@@ -304,17 +319,17 @@ def gdr_prologue(mixed, conv_w, a, b, A_log, dt_bias, Hk: int, Hv: int, tail=Non
         _need(lengths.is_cuda and lengths.dtype == torch.int32 and lengths.shape == (B,), "lengths must be CUDA int32 [B]")
     dev = mixed.device
     if q is None:
-        q = torch.empty(B, L, Hk, D, device=dev, dtype=torch.bfloat16)
+        q = _empty((B, L, Hk, D), torch.bfloat16, dev, stream)
     if k is None:
-        k = torch.empty(B, L, Hk, D, device=dev, dtype=torch.bfloat16)
+        k = _empty((B, L, Hk, D), torch.bfloat16, dev, stream)
     if v is None:
-        v = torch.empty(B, L, Hv, D, device=dev, dtype=torch.bfloat16)
+        v = _empty((B, L, Hv, D), torch.bfloat16, dev, stream)
     if g is None:
-        g = torch.empty(B, L, Hv, device=dev, dtype=torch.float32)
+        g = _empty((B, L, Hv), torch.float32, dev, stream)
     if beta is None:
-        beta = torch.empty(B, L, Hv, device=dev, dtype=torch.float32)
+        beta = _empty((B, L, Hv), torch.float32, dev, stream)
     if new_tail is None and keep_tail and K > 1:
-        new_tail = torch.empty(B, K - 1, C, device=dev, dtype=torch.bfloat16)
+        new_tail = _empty((B, K - 1, C), torch.bfloat16, dev, stream)
     _check(lib().gdr_prologue(_p(mixed), _p(tail), _p(conv_w), _p(a), _p(b), _p(A_log), _p(dt_bias), _p(lengths),
                               _p(q), _p(k), _p(v), _p(g), _p(beta), _p(new_tail), B, L, Hk, Hv, D, K,
                               _stream(stream)))
@@ -351,14 +366,14 @@ def gdr_chunk_fwd_prologue(mixed, conv_w, a, b, A_log, dt_bias, Hk: int, Hv: int
                   f"{name} must be contiguous CUDA float32 [B, Hv, D, D]")
     dev = mixed.device
     if o is None:
-        o = torch.empty(B, L, Hv, D, device=dev, dtype=torch.bfloat16)
+        o = _empty((B, L, Hv, D), torch.bfloat16, dev, stream)
     if S_T is None and final_state:
-        S_T = torch.empty(B, Hv, D, D, device=dev, dtype=torch.float32)
+        S_T = _empty((B, Hv, D, D), torch.float32, dev, stream)
     if new_tail is None and keep_tail and K > 1:
-        new_tail = torch.empty(B, K - 1, C, device=dev, dtype=torch.bfloat16)
+        new_tail = _empty((B, K - 1, C), torch.bfloat16, dev, stream)
     need = prologue_workspace_bytes(B, L, Hk, Hv, K)
     if ws is None and need:
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws = _empty(need, torch.uint8, dev, stream)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check(lib().gdr_chunk_fwd_prologue(_p(mixed), _p(tail), _p(conv_w), _p(a), _p(b), _p(A_log), _p(dt_bias),
                                         _p(S0), _p(o), _p(S_T), _p(new_tail), B, L, Hk, Hv, D, K, _p(ws), ws_bytes,
@@ -374,7 +389,7 @@ def gdr_gated_rmsnorm(x, z, w, eps: float = 1e-6, out=None, stream=None):
     _need(x.dtype == torch.bfloat16 and z.dtype == torch.bfloat16 and z.shape == x.shape, "x and z: bfloat16, same shape")
     _need(w.dtype == torch.float32 and w.shape == (x.shape[-1],), "w must be float32 [D]")
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty(x.shape, x.dtype, x.device, stream)
     rows = x.numel() // x.shape[-1]
     _check(lib().gdr_gated_rmsnorm(_p(x), _p(z), _p(w), float(eps), _p(out), rows, x.shape[-1], _stream(stream)))
     return out
@@ -395,16 +410,16 @@ def gdr_backward(q, k, v, g, beta, S0, dO, dS_T=None, ws=None, stream=None, want
         if t is not None:
             _need(t.dtype == torch.float32 and t.is_contiguous() and t.is_cuda and t.shape == (B, Hv, Dk, v.shape[3]),
                   f"{name} must be contiguous CUDA float32 [B, Hv, D, D]")
-    f32 = dict(dtype=torch.float32, device=q.device)
-    dq = torch.empty(q.shape, **f32)
-    dk = torch.empty(k.shape, **f32)
-    dv = torch.empty(v.shape, **f32)
-    dg = torch.empty(g.shape, **f32)
-    dbeta = torch.empty(beta.shape, **f32)
-    dS0 = torch.empty(B, Hv, Dk, v.shape[3], **f32) if want_dS0 else None
+    f32 = torch.float32, q.device, stream
+    dq = _empty(q.shape, *f32)
+    dk = _empty(k.shape, *f32)
+    dv = _empty(v.shape, *f32)
+    dg = _empty(g.shape, *f32)
+    dbeta = _empty(beta.shape, *f32)
+    dS0 = _empty((B, Hv, Dk, v.shape[3]), *f32) if want_dS0 else None
     need = backward_workspace_bytes(B, L, Hk, Hv, Dk)
     if ws is None:
-        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        ws = _empty(max(need, 1), torch.uint8, q.device, stream)
     ws_bytes = ws.numel() * ws.element_size()
     _check(lib().gdr_backward(_p(q), _p(k), _p(v), _p(g), _p(beta), _p(S0), _p(dO), _p(dS_T), _p(dq), _p(dk),
                               _p(dv), _p(dg), _p(dbeta), _p(dS0), B, L, Hk, Hv, Dk, dt, _p(ws), ws_bytes,
@@ -424,15 +439,15 @@ def gdr_chunk_fwd_save(q, k, v, g, beta, S0=None, saved=None, o=None, S_T=None, 
     B, L, Hk, Hv, Dk = _check_inputs(q, k, v, g, beta)
     _need(q.dtype == torch.bfloat16, "gdr_chunk_fwd_save takes bf16 q, k, v")
     if o is None:
-        o = torch.empty_like(v)
+        o = _empty(v.shape, v.dtype, v.device, stream)
     if S_T is None and final_state:
-        S_T = torch.empty(B, Hv, Dk, v.shape[3], device=v.device, dtype=torch.float32)
+        S_T = _empty((B, Hv, Dk, v.shape[3]), torch.float32, v.device, stream)
     for name, t in (("S0", S0), ("S_T", S_T)):
         if t is not None:
             _need(t.dtype == torch.float32 and t.is_contiguous() and t.is_cuda, f"{name} must be contiguous CUDA float32")
     need = backward_chunked_workspace_bytes(B, L, Hk, Hv, Dk)
     if saved is None:
-        saved = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        saved = _empty(max(need, 1), torch.uint8, q.device, stream)
     _check(lib().gdr_chunk_fwd_save(_p(q), _p(k), _p(v), _p(g), _p(beta), _p(S0), _p(o), _p(S_T), B, L, Hk, Hv, Dk,
                                     _dtype_code(q), _p(saved), saved.numel() * saved.element_size(), _stream(stream)))
     return o, S_T, saved
@@ -452,19 +467,19 @@ def gdr_backward_chunked(q, k, v, g, beta, S0, dO, dS_T=None, ws=None, stream=No
         if t is not None:
             _need(t.dtype == torch.float32 and t.is_contiguous() and t.is_cuda and t.shape == (B, Hv, Dk, v.shape[3]),
                   f"{name} must be contiguous CUDA float32 [B, Hv, D, D]")
-    f32 = dict(dtype=torch.float32, device=q.device)
-    dq = torch.empty(q.shape, **f32)
-    dk = torch.empty(k.shape, **f32)
-    dv = torch.empty(v.shape, **f32)
-    dg = torch.empty(g.shape, **f32)
-    dbeta = torch.empty(beta.shape, **f32)
-    dS0 = torch.empty(B, Hv, Dk, v.shape[3], **f32) if want_dS0 else None
+    f32 = torch.float32, q.device, stream
+    dq = _empty(q.shape, *f32)
+    dk = _empty(k.shape, *f32)
+    dv = _empty(v.shape, *f32)
+    dg = _empty(g.shape, *f32)
+    dbeta = _empty(beta.shape, *f32)
+    dS0 = _empty((B, Hv, Dk, v.shape[3]), *f32) if want_dS0 else None
     need = backward_chunked_workspace_bytes(B, L, Hk, Hv, Dk)
     if saved is not None:
         _need(ws is None, "pass either ws or saved")
         ws = saved
     if ws is None:
-        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        ws = _empty(max(need, 1), torch.uint8, q.device, stream)
     ws_bytes = ws.numel() * ws.element_size()
     fn = lib().gdr_backward_chunked_saved if saved is not None else lib().gdr_backward_chunked
     _check(fn(_p(q), _p(k), _p(v), _p(g), _p(beta), _p(S0), _p(dO), _p(dS_T), _p(dq), _p(dk), _p(dv), _p(dg),

@@ -54,6 +54,77 @@ def _cache(seed):
     return call
 
 
+def _delta_inputs(seed, B=2, L=700, Hk=2, Hv=4, D=128, dtype=torch.bfloat16):
+    f32 = torch.float32
+    return (_randn(seed, B, L, Hk, D, dtype=dtype), _randn(seed + 1, B, L, Hk, D, dtype=dtype), _randn(seed + 2, B, L, Hv, D, dtype=dtype),
+            -_randn(seed + 3, B, L, Hv, dtype=f32).abs(), torch.sigmoid(_randn(seed + 4, B, L, Hv, dtype=f32)))
+
+
+def _prefill(seed):
+    a = _delta_inputs(seed)
+    return lambda **kw: gdr.gdr_chunk_fwd(*a, **kw)
+
+
+def _delta_forks(seed):
+    a = _delta_inputs(seed, B=40, L=16)
+    trunk, idx = _randn(seed + 5, 3, 4, 128, 128, dtype=torch.float32), torch.arange(40, device="cuda") % 3
+    return lambda **kw: gdr.gdr_fork_fwd(*a, trunk, idx, **kw)
+
+
+def _delta_decode(seed):
+    a, states = _delta_inputs(seed, L=1), _randn(seed + 5, 2, 4, 128, 128, dtype=torch.float32)
+
+    def call(**kw):
+        if "stream" in kw:
+            kw["stream"].wait_stream(torch.cuda.current_stream())
+        return (gdr.gdr_decode_step(*a, states.clone(), **kw),)
+    return call
+
+
+def _delta_grad(seed):
+    a, dO = _delta_inputs(seed), _randn(seed + 6, 2, 700, 4, 128)
+    return lambda **kw: gdr.gdr_backward_chunked(*a, None, dO, want_dS0=False, **kw)[:5]
+
+
+def _delta_grad_f32(seed):
+    a, dO = _delta_inputs(seed, L=90, dtype=torch.float32), _randn(seed + 6, 2, 90, 4, 128, dtype=torch.float32)
+    return lambda **kw: gdr.gdr_backward(*a, None, dO, want_dS0=False, **kw)[:5]
+
+
+def _prologue_inputs(seed, B=2, L=300, Hk=2, Hv=4):
+    f32 = torch.float32
+    return (_randn(seed, B, L, (2 * Hk + Hv) * 128), _randn(seed + 1, (2 * Hk + Hv) * 128, 4, dtype=f32), _randn(seed + 2, B, L, Hv, dtype=f32),
+            _randn(seed + 3, B, L, Hv, dtype=f32), _randn(seed + 4, Hv, dtype=f32), _randn(seed + 5, Hv, dtype=f32), Hk, Hv)
+
+
+def _prologue(seed):
+    a = _prologue_inputs(seed)
+    return lambda **kw: gdr.gdr_prologue(*a, **kw)
+
+
+def _fused_prologue(seed):
+    a = _prologue_inputs(seed)
+    return lambda **kw: gdr.gdr_chunk_fwd_prologue(*a, **kw)
+
+
+def _gated(seed):
+    x, z, w = _randn(seed, 3000, 128), _randn(seed + 1, 3000, 128), _randn(seed + 2, 128, dtype=torch.float32)
+    return lambda **kw: (gdr.gdr_gated_rmsnorm(x, z, w, **kw),)
+
+
+def _prefill_gated(seed):
+    a, z, w = _delta_inputs(seed), _randn(seed + 6, 2, 700, 4, 128), _randn(seed + 7, 128, dtype=torch.float32)
+    return lambda **kw: gdr.gdr_chunk_fwd_gated(*a, None, z, w, 1e-6, **kw)
+
+
+def _prefill_save(seed):
+    a = _delta_inputs(seed)
+    return lambda **kw: gdr.gdr_chunk_fwd_save(*a, **kw)[:2]
+
+
+DELTA = [_prefill, _delta_forks, _delta_grad, _delta_grad_f32, _prologue, _fused_prologue, _gated, _prefill_gated, _prefill_save]
+
+
 def _segments():
     return {s["address"]: s["stream"] for s in torch.cuda.memory_snapshot()}
 
@@ -69,7 +140,7 @@ def _taken_for(call, s):
     return {stream for at, stream in after.items() if at not in before}
 
 
-@pytest.mark.parametrize("make", [_attn, _grad])
+@pytest.mark.parametrize("make", [_attn, _grad] + DELTA)
 def test_memory_is_of_the_launch_stream(make):
     call, s = make(1), torch.cuda.Stream()
     call()   # (what the library sets up at its first call)
@@ -78,7 +149,7 @@ def test_memory_is_of_the_launch_stream(make):
     gdr.gdr_sync_status()
 
 
-@pytest.mark.parametrize("make", [_attn, _grad, _cache])
+@pytest.mark.parametrize("make", [_attn, _grad, _cache, _delta_decode] + DELTA)
 def test_calls_on_two_streams_keep_apart(make):
     """Calls of two streams in flight at once, while the current stream takes and overwrites memory."""
     calls = [make(10), make(20)]
