@@ -6,6 +6,7 @@
 #include <Python.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -28,11 +29,14 @@ struct Error {};   // a Python exception has been set
 struct Call {
   PyObject* const* args;
   int last;
+  mutable c10::DeviceIndex device = -1;   // the tensors'
   const Tensor* tensor(int i, const char* name, bool none = false) const {
     if (none && args[i] == Py_None) return nullptr;
     if (!THPVariable_Check(args[i])) refuse("%s must be a tensor", name);
     const Tensor& t = THPVariable_Unpack(args[i]);
     if (!t.is_cuda()) refuse("%s must be a CUDA tensor", name);
+    if (device < 0) device = t.device().index();
+    if (t.device().index() != device) refuse("%s must be on the device of the other tensors", name);
     return &t;
   }
   // contiguous, of this type and shape (empty: any)
@@ -60,7 +64,8 @@ struct Call {
   bool truth(int i) const { return PyObject_IsTrue(args[i]) == 1; }
   // the stream's raw handle, or None for the current stream
   gdr_stream_t stream() const {
-    if (args[last] == Py_None) return reinterpret_cast<gdr_stream_t>(c10::cuda::getCurrentCUDAStream().stream());
+    if (c10::cuda::current_device() != device) refuse("the tensors must be on the current CUDA device");
+    if (args[last] == Py_None) return reinterpret_cast<gdr_stream_t>(c10::cuda::getCurrentCUDAStream(device).stream());
     return static_cast<gdr_stream_t>(PyLong_AsVoidPtr(args[last]));
   }
   // A new tensor, of the launch stream's memory: the allocator hands memory out again in the order of the
@@ -73,9 +78,9 @@ struct Call {
     struct Back {   // the current stream, set again on the way out
       c10::cuda::CUDAStream stream;
       ~Back() { c10::cuda::setCurrentCUDAStream(stream); }
-    } back{c10::cuda::getCurrentCUDAStream(near.get_device())};
+    } back{c10::cuda::getCurrentCUDAStream(device)};
     c10::cuda::setCurrentCUDAStream(
-        c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(PyLong_AsVoidPtr(args[last])), near.get_device()));
+        c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(PyLong_AsVoidPtr(args[last])), device));
     Tensor t = at::empty(shape, options);
     if (kept) t.record_stream(back.stream.unwrap());
     return t;
@@ -222,9 +227,9 @@ PyObject* norm_rope_append(const Call& c) {
 PyObject* norm_rope_backward(const Call& c) {
   const Rope r(c, 0);
   const Tensor *dqo = c.of(6, "dq_out", r.q->scalar_type(), r.q->sizes()), *dko = c.of(7, "dk_out", r.q->scalar_type(), r.k->sizes());
+  Tensor ws = c.workspace(10, gdr_qk_norm_rope_backward_workspace_bytes(r.D), *r.q);
   auto grad = [&](at::IntArrayRef shape) { return c.empty(shape, at::kFloat, *r.q, true); };
   Tensor dq = grad(r.q->sizes()), dk = grad(r.k->sizes()), dq_w = grad({r.q->size(3)}), dk_w = grad({r.q->size(3)});
-  Tensor ws = c.workspace(10, gdr_qk_norm_rope_backward_workspace_bytes(r.D), *r.q);
   check(gdr_qk_norm_rope_backward(ptr(r.q), ptr(r.k), ptr<float>(r.q_w), ptr<float>(r.k_w), ptr<double>(r.inv_freq),
                                   ptr<int32_t>(r.pos), ptr(dqo), ptr(dko), (float)c.number(8), c.truth(9), ptr<float>(&dq),
                                   ptr<float>(&dk), ptr<float>(&dq_w), ptr<float>(&dk_w), r.B, r.N, r.Hq, r.Hk, r.D, r.R,

@@ -491,8 +491,8 @@ def gdr_backward_chunked(q, k, v, g, beta, S0, dO, dS_T=None, ws=None, stream=No
 # softmax-attention layers: drafted tokens over a cache of pages
 #
 # A decoding step makes these calls once a layer, on kernels of a few microseconds: their checks and
-# marshalling are compiled (csrc/gdr_bind.cpp) and raise ValueError for a tensor of the wrong device,
-# dtype, shape or layout, GdrError for what the library refuses.
+# marshalling are compiled (csrc/gdr_bind.cpp) and raise ValueError for a tensor of the wrong device (all
+# of them are on the current one), dtype, shape or layout, GdrError for what the library refuses.
 # --------------------------------------------------------------------------------------------------
 _bind_mod = None
 
