@@ -10,6 +10,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <climits>
 #include <cmath>
 #include <initializer_list>
 
@@ -25,11 +26,24 @@ struct Error {};   // a Python exception has been set
   throw Error{};
 }
 
-// Argument i as a tensor (NULL for None where that is allowed). The last argument is the launch stream.
+// The library counts in 32 bits: nothing is cut to them.
+int int32(int64_t x, const char* name) {
+  if (x < INT_MIN || x > INT_MAX) refuse("%s does not fit in 32 bits", name);
+  return (int)x;
+}
+int size(const Tensor& t, int dim, const char* name) { return int32(t.size(dim), name); }
+
+// A call's arguments, of which the last is the launch stream: its raw handle, or None for the current one.
 struct Call {
   PyObject* const* args;
-  int last;
+  bool given;              // a stream
+  cudaStream_t handle;
   mutable c10::DeviceIndex device = -1;   // the tensors'
+  Call(PyObject* const* args, int last) : args(args), given(args[last] != Py_None), handle(nullptr) {
+    if (given) handle = static_cast<cudaStream_t>(PyLong_AsVoidPtr(args[last]));
+    if (PyErr_Occurred()) throw Error{};
+  }
+  // argument i (NULL for None where that is allowed)
   const Tensor* tensor(int i, const char* name, bool none = false) const {
     if (none && args[i] == Py_None) return nullptr;
     if (!THPVariable_Check(args[i])) refuse("%s must be a tensor", name);
@@ -56,17 +70,19 @@ struct Call {
     if (x == -1.0 && PyErr_Occurred()) throw Error{};
     return x;
   }
-  long integer(int i) const {
+  int integer(int i, const char* name) const {
     const long x = PyLong_AsLong(args[i]);
     if (x == -1 && PyErr_Occurred()) throw Error{};
-    return x;
+    return int32(x, name);
   }
-  bool truth(int i) const { return PyObject_IsTrue(args[i]) == 1; }
-  // the stream's raw handle, or None for the current stream
+  bool truth(int i) const {
+    const int x = PyObject_IsTrue(args[i]);
+    if (x < 0) throw Error{};
+    return x == 1;
+  }
   gdr_stream_t stream() const {
     if (c10::cuda::current_device() != device) refuse("the tensors must be on the current CUDA device");
-    if (args[last] == Py_None) return reinterpret_cast<gdr_stream_t>(c10::cuda::getCurrentCUDAStream(device).stream());
-    return static_cast<gdr_stream_t>(PyLong_AsVoidPtr(args[last]));
+    return reinterpret_cast<gdr_stream_t>(given ? handle : c10::cuda::getCurrentCUDAStream(device).stream());
   }
   // A new tensor, of the launch stream's memory: the allocator hands memory out again in the order of the
   // stream it was taken for, so a workspace that is dropped when the call returns, or an output that the
@@ -74,13 +90,12 @@ struct Call {
   // read on the current stream as well, and is not handed out again before that stream is past the reads.
   Tensor empty(at::IntArrayRef shape, at::ScalarType type, const Tensor& near, bool kept) const {
     const auto options = near.options().dtype(type);
-    if (args[last] == Py_None) return at::empty(shape, options);
+    if (!given) return at::empty(shape, options);
     struct Back {   // the current stream, set again on the way out
       c10::cuda::CUDAStream stream;
       ~Back() { c10::cuda::setCurrentCUDAStream(stream); }
     } back{c10::cuda::getCurrentCUDAStream(device)};
-    c10::cuda::setCurrentCUDAStream(
-        c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(PyLong_AsVoidPtr(args[last])), device));
+    c10::cuda::setCurrentCUDAStream(c10::cuda::getStreamFromExternal(handle, device));
     Tensor t = at::empty(shape, options);
     if (kept) t.record_stream(back.stream.unwrap());
     return t;
@@ -162,18 +177,18 @@ struct Rope {
     k = c.tensor(i + 1, "k");
     qs = heads(*q, "q", *q);
     ks = heads(*k, "k", *q);
-    B = q->size(0);
-    N = q->size(1);
-    Hq = q->size(2);
-    Hk = k->size(2);
-    D = q->size(3);
+    B = size(*q, 0, "q's size");
+    N = size(*q, 1, "q's size");
+    Hq = size(*q, 2, "q's size");
+    Hk = size(*k, 2, "k's size");
+    D = size(*q, 3, "q's size");
     dt = dtype(*q, "q and k");
     q_w = c.of(i + 2, "q_w", at::kFloat, {q->size(3)});
     k_w = c.of(i + 3, "k_w", at::kFloat, {q->size(3)});
     inv_freq = c.of(i + 4, "inv_freq", at::kDouble);
     if (inv_freq->dim() != 1) refuse("inv_freq must be [R / 2]");
     pos = c.ints(i + 5, "pos", {q->size(0), q->size(1)});
-    R = 2 * inv_freq->size(0);
+    R = int32(2 * inv_freq->size(0), "inv_freq's size");
   }
 };
 
@@ -188,20 +203,22 @@ struct Pages {
     table = c.ints(i + 2, "table");
     if (table->dim() != 2 || table->size(0) != q.size(0)) refuse("table must be [B, M]");
     ctx = c.ints(i + 3, "ctx", {q.size(0)});
-    P = k->size(0);
-    page = k->size(1);
-    Hk = k->size(2);
-    M = table->size(1);
+    P = size(*k, 0, "k_pages' size");
+    page = size(*k, 1, "k_pages' size");
+    Hk = size(*k, 2, "k_pages' size");
+    M = size(*table, 1, "table's size");
   }
 };
 
 // q, k, q_w, k_w, inv_freq, pos, eps, interleaved, q_out, k_out, stream
 PyObject* norm_rope(const Call& c) {
   const Rope r(c, 0);
+  const float eps = (float)c.number(6);
+  const bool interleaved = c.truth(7);
   Tensor q_out = c.output(8, "q_out", r.q->sizes(), r.q->scalar_type(), *r.q);
   Tensor k_out = c.output(9, "k_out", r.k->sizes(), r.q->scalar_type(), *r.q);
   check(gdr_qk_norm_rope(ptr(r.q), ptr(r.k), ptr<float>(r.q_w), ptr<float>(r.k_w), ptr<double>(r.inv_freq),
-                         ptr<int32_t>(r.pos), (float)c.number(6), c.truth(7), q_out.data_ptr(), k_out.data_ptr(), r.B, r.N,
+                         ptr<int32_t>(r.pos), eps, interleaved, q_out.data_ptr(), k_out.data_ptr(), r.B, r.N,
                          r.Hq, r.Hk, r.D, r.R, r.qs.tok, r.qs.head, r.ks.tok, r.ks.head, r.dt, c.stream()));
   return wrap({q_out, k_out});
 }
@@ -209,6 +226,8 @@ PyObject* norm_rope(const Call& c) {
 // q, k, q_w, k_w, inv_freq, pos, v, k_pages, v_pages, table, ctx, lengths, eps, interleaved, q_out, stream
 PyObject* norm_rope_append(const Call& c) {
   const Rope r(c, 0);
+  const float eps = (float)c.number(12);
+  const bool interleaved = c.truth(13);
   const Tensor* v = c.tensor(6, "v");
   const Heads vs = heads(*v, "v", *r.q);
   const Pages p(c, 7, *r.q);
@@ -216,7 +235,7 @@ PyObject* norm_rope_append(const Call& c) {
   const Tensor* lengths = c.ints(11, "lengths", {r.q->size(0)}, true);
   Tensor q_out = c.output(14, "q_out", r.q->sizes(), r.q->scalar_type(), *r.q);
   check(gdr_qk_norm_rope_append(ptr(r.q), ptr(r.k), ptr(v), ptr<float>(r.q_w), ptr<float>(r.k_w), ptr<double>(r.inv_freq),
-                                ptr<int32_t>(r.pos), (float)c.number(12), c.truth(13), q_out.data_ptr(), ptr(p.k), ptr(p.v),
+                                ptr<int32_t>(r.pos), eps, interleaved, q_out.data_ptr(), ptr(p.k), ptr(p.v),
                                 ptr<int32_t>(p.table), ptr<int32_t>(p.ctx), ptr<int32_t>(lengths), p.P, p.page, p.M, r.B,
                                 r.N, r.Hq, r.Hk, r.D, r.R, r.qs.tok, r.qs.head, r.ks.tok, r.ks.head, vs.tok, vs.head, r.dt,
                                 c.stream()));
@@ -226,12 +245,14 @@ PyObject* norm_rope_append(const Call& c) {
 // q, k, q_w, k_w, inv_freq, pos, dq_out, dk_out, eps, interleaved, ws, stream
 PyObject* norm_rope_backward(const Call& c) {
   const Rope r(c, 0);
+  const float eps = (float)c.number(8);
+  const bool interleaved = c.truth(9);
   const Tensor *dqo = c.of(6, "dq_out", r.q->scalar_type(), r.q->sizes()), *dko = c.of(7, "dk_out", r.q->scalar_type(), r.k->sizes());
   Tensor ws = c.workspace(10, gdr_qk_norm_rope_backward_workspace_bytes(r.D), *r.q);
   auto grad = [&](at::IntArrayRef shape) { return c.empty(shape, at::kFloat, *r.q, true); };
   Tensor dq = grad(r.q->sizes()), dk = grad(r.k->sizes()), dq_w = grad({r.q->size(3)}), dk_w = grad({r.q->size(3)});
   check(gdr_qk_norm_rope_backward(ptr(r.q), ptr(r.k), ptr<float>(r.q_w), ptr<float>(r.k_w), ptr<double>(r.inv_freq),
-                                  ptr<int32_t>(r.pos), ptr(dqo), ptr(dko), (float)c.number(8), c.truth(9), ptr<float>(&dq),
+                                  ptr<int32_t>(r.pos), ptr(dqo), ptr(dko), eps, interleaved, ptr<float>(&dq),
                                   ptr<float>(&dk), ptr<float>(&dq_w), ptr<float>(&dk_w), r.B, r.N, r.Hq, r.Hk, r.D, r.R,
                                   r.qs.tok, r.qs.head, r.ks.tok, r.ks.head, r.dt, ws.data_ptr(), bytes_of(ws), c.stream()));
   return wrap({dq, dk, dq_w, dk_w});
@@ -241,18 +262,18 @@ PyObject* norm_rope_backward(const Call& c) {
 PyObject* tree_attn(const Call& c) {
   const Tensor* q = c.of(0, "q", at::kBFloat16);
   if (q->dim() != 4) refuse("q must be [B, N, Hq, D]");
-  const int64_t B = q->size(0), N = q->size(1), Hq = q->size(2), D = q->size(3);
+  const int B = size(*q, 0, "q's size"), N = size(*q, 1, "q's size"), Hq = size(*q, 2, "q's size"), D = size(*q, 3, "q's size");
   const Pages p(c, 1, *q);
   const Tensor* lengths = c.ints(5, "lengths", {B}, true);
-  const Tensor* mask = c.of(6, "mask", at::kLong, {B, N, (N + 63) / 64}, true);
+  const Tensor* mask = c.of(6, "mask", at::kLong, {B, N, ((int64_t)N + 63) / 64}, true);
   const double scale = c.args[7] == Py_None ? 1.0 / std::sqrt((double)D) : c.number(7);
   Tensor o = c.output(8, "o", q->sizes(), at::kBFloat16, *q), lse;
   const bool with_lse = c.args[9] != Py_None || c.truth(10);
   if (with_lse) lse = c.output(9, "lse", {B, N, Hq}, at::kFloat, *q);
-  Tensor ws = c.workspace(11, gdr_tree_attn_workspace_bytes((int)D), *q);
+  Tensor ws = c.workspace(11, gdr_tree_attn_workspace_bytes(D), *q);
   check(gdr_tree_attn(ptr(q), ptr(p.k), ptr(p.v), ptr<int32_t>(p.table), ptr<int32_t>(p.ctx), ptr<int32_t>(lengths),
-                      ptr<uint64_t>(mask), (float)scale, o.data_ptr(), with_lse ? ptr<float>(&lse) : nullptr, (int)B, (int)N,
-                      (int)Hq, p.Hk, (int)D, p.P, p.page, p.M, GDR_BF16, ws.data_ptr(), bytes_of(ws), c.stream()));
+                      ptr<uint64_t>(mask), (float)scale, o.data_ptr(), with_lse ? ptr<float>(&lse) : nullptr, B, N, Hq,
+                      p.Hk, D, p.P, p.page, p.M, GDR_BF16, ws.data_ptr(), bytes_of(ws), c.stream()));
   return with_lse ? wrap({o, lse}) : THPVariable_Wrap(o);
 }
 
@@ -261,15 +282,15 @@ PyObject* verify(const Call& c) {
   const Tensor* p = c.tensor(3, "p");
   const gdr_dtype dt = dtype(*p, "p");
   if (p->dim() != 3 || !p->is_contiguous()) refuse("p must be a contiguous tensor [B, N, V]");
-  const int64_t B = p->size(0), N = p->size(1), V = p->size(2);
+  const int B = size(*p, 0, "p's size"), N = size(*p, 1, "p's size"), V = size(*p, 2, "p's size");
   const Tensor* q = c.of(4, "q", p->scalar_type(), p->sizes(), true);
   const Tensor *tokens = c.ints(0, "tokens", {B, N}), *parents = c.ints(1, "parents", {B, N}), *lengths = c.ints(2, "lengths", {B});
   const Tensor *u = c.of(5, "u", at::kFloat, {B, N}), *u_next = c.of(6, "u_next", at::kFloat, {B});
   Tensor path = c.output(7, "path", {B, N}, at::kInt, *p), n_path = c.output(8, "n_path", {B}, at::kInt, *p);
   Tensor next = c.output(9, "next_token", {B}, at::kInt, *p);
   check(gdr_verify_draft(ptr<int32_t>(tokens), ptr<int32_t>(parents), ptr<int32_t>(lengths), ptr(p), ptr(q), ptr<float>(u),
-                         ptr<float>(u_next), ptr<int32_t>(&path), ptr<int32_t>(&n_path), ptr<int32_t>(&next), (int)B, (int)N,
-                         (int)V, dt, c.stream()));
+                         ptr<float>(u_next), ptr<int32_t>(&path), ptr<int32_t>(&n_path), ptr<int32_t>(&next), B, N, V,
+                         dt, c.stream()));
   return wrap({path, n_path, next});
 }
 
@@ -281,15 +302,15 @@ struct Cache {
     k = c.tensor(i, "k_cache");
     if (k->dim() != 5 || !k->is_contiguous()) refuse("k_cache must be a contiguous tensor [layers, P, page, Hk, D]");
     v = c.of(i + 1, "v_cache", k->scalar_type(), k->sizes());
-    layers = k->size(0);
-    P = k->size(1);
-    page = k->size(2);
+    layers = size(*k, 0, "k_cache's size");
+    P = size(*k, 1, "k_cache's size");
+    page = size(*k, 2, "k_cache's size");
     row_bytes = (long long)k->size(3) * k->size(4) * k->element_size();
   }
 };
 struct Rows {
   const Tensor *table, *ctx, *refs, *list;
-  int F, R, M;
+  int F, R, M, P;
   // arguments i .. i + 2: table, ctx, refs; j: the row list
   Rows(const Call& c, int i, int j, const char* name) {
     table = c.ints(i, "table");
@@ -298,19 +319,20 @@ struct Rows {
     refs = c.ints(i + 2, "refs");
     list = c.ints(j, name);
     if (refs->dim() != 1 || list->dim() != 1) refuse("refs must be [P] and row lists [F]");
-    F = list->size(0);
-    R = table->size(0);
-    M = table->size(1);
+    F = size(*list, 0, name);
+    R = size(*table, 0, "table's size");
+    M = size(*table, 1, "table's size");
+    P = size(*refs, 0, "refs' size");
   }
 };
 
 // table, ctx, refs, rows, extra, page, ws, stream
 PyObject* cache_reserve(const Call& c) {
   const Rows r(c, 0, 3, "rows");
+  const int extra = c.integer(4, "extra"), page = c.integer(5, "page");
   Tensor ws = c.workspace(6, gdr_cache_workspace_bytes(r.F, r.M), *r.table);
   check(gdr_cache_reserve(ptr<int32_t>(r.table), ptr<int32_t>(r.ctx), ptr<int32_t>(r.refs), ptr<int32_t>(r.list),
-                          (int)c.integer(4), r.F, r.R, r.M, (int)r.refs->size(0), (int)c.integer(5), ws.data_ptr(),
-                          bytes_of(ws), c.stream()));
+                          extra, r.F, r.R, r.M, r.P, page, ws.data_ptr(), bytes_of(ws), c.stream()));
   Py_RETURN_NONE;
 }
 
@@ -319,7 +341,7 @@ PyObject* cache_fork(const Call& c) {
   const Cache k(c, 0);
   const Rows r(c, 2, 6, "dst");
   const Tensor* src = c.ints(5, "src", r.list->sizes());
-  if (r.refs->size(0) != k.P) refuse("refs must be [P]");
+  if (r.P != k.P) refuse("refs must be [P]");
   Tensor ws = c.workspace(7, gdr_cache_workspace_bytes(r.F, r.M), *r.table);
   check(gdr_cache_fork(ptr(k.k), ptr(k.v), ptr<int32_t>(r.table), ptr<int32_t>(r.ctx), ptr<int32_t>(r.refs),
                        ptr<int32_t>(src), ptr<int32_t>(r.list), r.F, r.R, r.M, k.layers, k.P, k.page, k.row_bytes,
@@ -331,7 +353,7 @@ PyObject* cache_fork(const Call& c) {
 PyObject* cache_free(const Call& c) {
   const Rows r(c, 0, 3, "rows");
   check(gdr_cache_free(ptr<int32_t>(r.table), ptr<int32_t>(r.ctx), ptr<int32_t>(r.refs), ptr<int32_t>(r.list), r.F, r.R,
-                       r.M, (int)r.refs->size(0), c.stream()));
+                       r.M, r.P, c.stream()));
   Py_RETURN_NONE;
 }
 
@@ -340,13 +362,14 @@ PyObject* cache_compact(const Call& c) {
   const Cache k(c, 0);
   const Tensor* path = c.ints(4, "path");
   if (path->dim() != 2) refuse("path must be [B, W]");
-  const int64_t B = path->size(0);
+  const int B = size(*path, 0, "path's size"), W = size(*path, 1, "path's size");
   const Tensor *table = c.ints(2, "table"), *ctx = c.ints(3, "ctx", {B}), *n_path = c.ints(5, "n_path", {B});
   if (table->dim() != 2 || table->size(0) != B) refuse("table must be [B, M]");
+  const int M = size(*table, 1, "table's size");
   Tensor new_ctx = c.output(6, "new_ctx", {B}, at::kInt, *ctx);
   check(gdr_cache_compact(ptr(k.k), ptr(k.v), ptr<int32_t>(table), ptr<int32_t>(ctx), ptr<int32_t>(path),
-                          ptr<int32_t>(n_path), ptr<int32_t>(&new_ctx), (int)B, (int)path->size(1), (int)table->size(1),
-                          k.layers, k.P, k.page, k.row_bytes, c.stream()));
+                          ptr<int32_t>(n_path), ptr<int32_t>(&new_ctx), B, W, M, k.layers, k.P, k.page,
+                          k.row_bytes, c.stream()));
   return THPVariable_Wrap(new_ctx);
 }
 
@@ -358,7 +381,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     return nullptr;
   }
   try {
-    return kFn(Call{args, kArgs - 1});
+    return kFn(Call(args, kArgs - 1));
   } catch (const Error&) {
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());

@@ -97,3 +97,39 @@ def test_tensors_of_two_devices(make):
     for name, t in make()[1].items():
         if isinstance(t, torch.Tensor):
             _refused(make, "device of the other tensors", **{name: T(tuple(t.shape), t.dtype, "cuda:1")})
+
+
+BIG = 2 ** 32
+
+
+@pytest.mark.parametrize("make,kw", [
+    (_reserve, dict(extra=BIG)), (_reserve, dict(extra=-BIG - 3)), (_reserve, dict(page=BIG + 16)), (_reserve, dict(refs=T((BIG + 9,)))),
+    (_reserve, dict(rows=T((BIG + 2,)))), (_free, dict(table=T((6, BIG + 4)))), (_free, dict(refs=T((BIG + 9,)))),
+    (_fork, dict(k_cache=T((BIG + 2, 9, 16, 2, 64), BF16), v_cache=T((BIG + 2, 9, 16, 2, 64), BF16))),
+    (_compact, dict(path=T((6, BIG + 5)))), (_compact, dict(table=T((6, BIG + 4)))),
+    (_verify, dict(p=T((2, 3, BIG + 50), F32), q=None)), (_attn, dict(table=T((2, BIG + 4)))),
+    (_attn, dict(k_pages=T((BIG + 9, 16, 2, 128), BF16), v_pages=T((BIG + 9, 16, 2, 128), BF16))),
+    (_rope, dict(inv_freq=T((2 ** 31 + 32,), F64))),
+])
+def test_what_does_not_fit_in_32_bits(make, kw):
+    _refused(make, "32 bits", **kw)
+
+
+class Odd:
+    def __bool__(self):
+        raise ArithmeticError("neither true nor false")
+
+
+@pytest.mark.parametrize("make,kw", [(_rope, dict(interleaved=Odd())), (_append, dict(interleaved=Odd())), (_back, dict(interleaved=Odd())),
+                                     (_attn, dict(want_lse=Odd(), lse=None))])
+def test_a_truth_value_that_raises(make, kw):
+    _refused(make, "neither true nor false", ArithmeticError, **kw)
+
+
+class OddStream:
+    cuda_stream = "seven"
+
+
+@pytest.mark.parametrize("make", [_attn, _reserve])
+def test_a_stream_handle_that_is_no_number(make):
+    _refused(make, None, TypeError, stream=OddStream(), ws=None)
