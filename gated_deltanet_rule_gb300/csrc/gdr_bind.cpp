@@ -107,7 +107,9 @@ struct Call {
   }
   Tensor workspace(int i, size_t bytes, const Tensor& near) const {
     if (args[i] == Py_None) return empty({(int64_t)(bytes < 16 ? 16 : bytes)}, at::kByte, near, false);
-    return *tensor(i, "ws");
+    const Tensor* t = tensor(i, "ws");   // (its elements have to be its memory: a workspace is written as bytes)
+    if (!t->is_contiguous()) refuse("%s must be contiguous", "ws");
+    return *t;
   }
 };
 

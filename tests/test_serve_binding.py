@@ -133,3 +133,10 @@ class OddStream:
 @pytest.mark.parametrize("make", [_attn, _reserve])
 def test_a_stream_handle_that_is_no_number(make):
     _refused(make, None, TypeError, stream=OddStream(), ws=None)
+
+
+@pytest.mark.parametrize("make", [_attn, _back, _reserve, _fork])
+@pytest.mark.parametrize("strides", [(0,), (2,)])
+def test_a_workspace_with_less_or_other_memory_than_elements(make, strides):
+    """One byte seen many times would pass for as many bytes."""
+    _refused(make, "ws must be contiguous", ws=T((1 << 28,), U8, strides=strides))
