@@ -98,6 +98,14 @@ unsigned long long span(const RopeArgs& a, int H, long long tok, long long head,
   return ((unsigned long long)((long long)a.B * a.N - 1) * tok + (unsigned long long)(H - 1) * head + a.D) * es;
 }
 
+// The same for the three norm + rotation calls, whose weights, frequencies and positions are inputs besides `ins`.
+gdr_status apart_rope(const RopeArgs& a, std::initializer_list<Range> outs, std::initializer_list<Range> ins, const char* who) {
+  const gdr_status st = apart(outs, ins, who);
+  if (st != GDR_OK) return st;
+  return apart(outs, {{a.q_w, a.D * 4ull, "q_w"}, {a.k_w, a.D * 4ull, "k_w"}, {a.inv_freq, a.R * 4ull, "inv_freq"},
+                      {a.pos, (unsigned long long)a.B * a.N * 4, "pos"}}, who);
+}
+
 gdr_status check_cache(const void* k_cache, const void* v_cache, int layers, int P, int page, long long row_bytes,
                        const char* who) {
   if (!k_cache || !v_cache) return fail(GDR_ERR_INVALID_ARG, "%s: k_cache and v_cache must be non-NULL", who);
@@ -107,8 +115,10 @@ gdr_status check_cache(const void* k_cache, const void* v_cache, int layers, int
     return fail(GDR_ERR_INVALID_ARG, "%s: layers=%d must be >= 1 and row_bytes=%lld a multiple of 16", who, layers, row_bytes);
   if (layers > 16383 || row_bytes > (1ll << 30))
     return fail(GDR_ERR_UNSUPPORTED, "%s: layers=%d or row_bytes=%lld too large", who, layers, row_bytes);
-  const unsigned long long bytes = (unsigned long long)layers * P * page * row_bytes;
-  return apart({{k_cache, bytes, "k_cache"}}, {{v_cache, bytes, "v_cache"}}, who);
+  return GDR_OK;
+}
+unsigned long long cache_bytes(int layers, int P, int page, long long row_bytes) {
+  return (unsigned long long)layers * P * page * row_bytes;
 }
 
 gdr_status check_rows(const void* table, const void* ctx, const void* refs, const void* rows, int F, int R, int M, int P,
@@ -155,8 +165,8 @@ gdr_status gdr_qk_norm_rope(const void* q, const void* k, const float* q_w, cons
     return fail(GDR_ERR_INVALID_ARG, "%s: q_out and k_out must be 16-byte aligned", who);
   const int es = dt == GDR_BF16 ? 2 : 4;
   const unsigned long long T = (unsigned long long)B * N * D * es;
-  st = apart({{q_out, T * Hq, "q_out"}, {k_out, T * Hk, "k_out"}},
-             {{q, span(a, Hq, q_tok, q_head, es), "q"}, {k, span(a, Hk, k_tok, k_head, es), "k"}}, who);
+  st = apart_rope(a, {{q_out, T * Hq, "q_out"}, {k_out, T * Hk, "k_out"}},
+                  {{q, span(a, Hq, q_tok, q_head, es), "q"}, {k, span(a, Hk, k_tok, k_head, es), "k"}}, who);
   if (st != GDR_OK) return st;
   return launched(launch_qk_norm_rope(a, reinterpret_cast<cudaStream_t>(stream)), who);
 }
@@ -187,9 +197,10 @@ gdr_status gdr_qk_norm_rope_append(const void* q, const void* k, const void* v, 
     if (!aligned(p, 4)) return fail(GDR_ERR_INVALID_ARG, "%s: table, ctx and lengths must be 4-byte aligned", who);
   const int es = dt == GDR_BF16 ? 2 : 4;
   const unsigned long long pages = (unsigned long long)P * page * Hk * D * es;
-  st = apart({{q_out, (unsigned long long)B * N * Hq * D * es, "q_out"}, {k_pages, pages, "k_pages"}, {v_pages, pages, "v_pages"}},
-             {{q, span(a, Hq, q_tok, q_head, es), "q"}, {k, span(a, Hk, k_tok, k_head, es), "k"},
-              {v, span(a, Hk, v_tok, v_head, es), "v"}}, who);
+  st = apart_rope(a, {{q_out, (unsigned long long)B * N * Hq * D * es, "q_out"}, {k_pages, pages, "k_pages"}, {v_pages, pages, "v_pages"}},
+                  {{q, span(a, Hq, q_tok, q_head, es), "q"}, {k, span(a, Hk, k_tok, k_head, es), "k"},
+                   {v, span(a, Hk, v_tok, v_head, es), "v"}, {table, (unsigned long long)B * M * 4, "table"},
+                   {ctx, B * 4ull, "ctx"}, {lengths, B * 4ull, "lengths"}}, who);
   if (st != GDR_OK) return st;
   a.err = device_error_word();
   if (!a.err) return no_device(who);
@@ -223,10 +234,9 @@ gdr_status gdr_qk_norm_rope_backward(const void* q, const void* k, const float* 
   if (st != GDR_OK) return st;
   const int es = dt == GDR_BF16 ? 2 : 4;
   const unsigned long long T = (unsigned long long)B * N * D;
-  st = apart({{dq, T * Hq * 4, "dq"}, {dk, T * Hk * 4, "dk"}, {dq_w, D * 4ull, "dq_w"}, {dk_w, D * 4ull, "dk_w"}, {ws, need, "ws"}},
-             {{q, span(a, Hq, q_tok, q_head, es), "q"}, {k, span(a, Hk, k_tok, k_head, es), "k"},
-              {dq_out, T * Hq * es, "dq_out"}, {dk_out, T * Hk * es, "dk_out"}, {q_w, D * 4ull, "q_w"}, {k_w, D * 4ull, "k_w"}},
-             who);
+  st = apart_rope(a, {{dq, T * Hq * 4, "dq"}, {dk, T * Hk * 4, "dk"}, {dq_w, D * 4ull, "dq_w"}, {dk_w, D * 4ull, "dk_w"}, {ws, need, "ws"}},
+                  {{q, span(a, Hq, q_tok, q_head, es), "q"}, {k, span(a, Hk, k_tok, k_head, es), "k"},
+                   {dq_out, T * Hq * es, "dq_out"}, {dk_out, T * Hk * es, "dk_out"}}, who);
   if (st != GDR_OK) return st;
   return launched(launch_qk_norm_rope_backward(a, reinterpret_cast<cudaStream_t>(stream)), who);
 }
@@ -310,6 +320,9 @@ gdr_status gdr_cache_reserve(int32_t* table, const int32_t* ctx, int32_t* refs, 
   if (st == GDR_OK) st = check_pages(P, page, M, who);
   if (st == GDR_OK && extra < 0) st = fail(GDR_ERR_INVALID_ARG, "%s: extra=%d must be >= 0", who, extra);
   if (st == GDR_OK) st = check_ws(ws, ws_bytes, cache_workspace_bytes(F, M), who);
+  if (st == GDR_OK)
+    st = apart({{table, (unsigned long long)R * M * 4, "table"}, {refs, P * 4ull, "refs"}, {ws, cache_workspace_bytes(F, M), "ws"}},
+               {{ctx, R * 4ull, "ctx"}, {rows, F * 4ull, "rows"}}, who);
   if (st != GDR_OK) return st;
   CacheArgs a{};
   a.table = table; a.ctx = const_cast<int32_t*>(ctx); a.refs = refs; a.dst = rows; a.extra = extra;
@@ -329,6 +342,12 @@ gdr_status gdr_cache_fork(void* k_cache, void* v_cache, int32_t* table, int32_t*
     st = fail(GDR_ERR_INVALID_ARG, "%s: src must be non-NULL and 4-byte aligned", who);
   if (st == GDR_OK) st = check_cache(k_cache, v_cache, layers, P, page, row_bytes, who);
   if (st == GDR_OK) st = check_ws(ws, ws_bytes, cache_workspace_bytes(F, M), who);
+  if (st == GDR_OK) {
+    const unsigned long long bytes = cache_bytes(layers, P, page, row_bytes);
+    st = apart({{k_cache, bytes, "k_cache"}, {v_cache, bytes, "v_cache"}, {table, (unsigned long long)R * M * 4, "table"},
+                {ctx, R * 4ull, "ctx"}, {refs, P * 4ull, "refs"}, {ws, cache_workspace_bytes(F, M), "ws"}},
+               {{src, F * 4ull, "src"}, {dst, F * 4ull, "dst"}}, who);
+  }
   if (st != GDR_OK) return st;
   CacheArgs a{};
   a.k_cache = static_cast<uint8_t*>(k_cache); a.v_cache = static_cast<uint8_t*>(v_cache);
@@ -343,7 +362,10 @@ gdr_status gdr_cache_fork(void* k_cache, void* v_cache, int32_t* table, int32_t*
 gdr_status gdr_cache_free(int32_t* table, int32_t* ctx, int32_t* refs, const int32_t* rows, int F, int R, int M,
                           int P, gdr_stream_t stream) {
   const char* who = "gdr_cache_free";
-  const gdr_status st = check_rows(table, ctx, refs, rows, F, R, M, P, who);
+  gdr_status st = check_rows(table, ctx, refs, rows, F, R, M, P, who);
+  if (st == GDR_OK)
+    st = apart({{table, (unsigned long long)R * M * 4, "table"}, {ctx, R * 4ull, "ctx"}, {refs, P * 4ull, "refs"}},
+               {{rows, F * 4ull, "rows"}}, who);
   if (st != GDR_OK) return st;
   CacheArgs a{};
   a.table = table; a.ctx = ctx; a.refs = refs; a.dst = rows; a.F = F; a.rows = R; a.M = M; a.P = P;
@@ -366,8 +388,9 @@ gdr_status gdr_cache_compact(void* k_cache, void* v_cache, const int32_t* table,
   if (st != GDR_OK) return st;
   for (const void* x : {(const void*)table, (const void*)ctx, (const void*)path, (const void*)n_path, (const void*)new_ctx})
     if (!aligned(x, 4)) return fail(GDR_ERR_INVALID_ARG, "%s: int32 arrays must be 4-byte aligned", who);
-  st = apart({{new_ctx, B * 4ull, "new_ctx"}}, {{ctx, B * 4ull, "ctx"}, {n_path, B * 4ull, "n_path"},
-             {path, (unsigned long long)B * W * 4, "path"}, {table, (unsigned long long)B * M * 4, "table"}}, who);
+  const unsigned long long bytes = cache_bytes(layers, P, page, row_bytes);
+  st = apart({{k_cache, bytes, "k_cache"}, {v_cache, bytes, "v_cache"}, {new_ctx, B * 4ull, "new_ctx"}},
+             {{ctx, B * 4ull, "ctx"}, {n_path, B * 4ull, "n_path"}, {path, (unsigned long long)B * W * 4, "path"}, {table, (unsigned long long)B * M * 4, "table"}}, who);
   if (st != GDR_OK) return st;
   int* err = device_error_word();
   if (!err) return no_device(who);

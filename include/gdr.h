@@ -336,7 +336,8 @@ gdr_status gdr_backward_chunked_saved(const void* q, const void* k, const void* 
  * token, whose keys are not in the cache yet; every node after its parent) take positions ctx[b] ..
  * ctx[b]+N-1 until the accepted ones are moved to the front; lengths [B] int32 (NULL = N) gives each row's
  * nodes. A length outside [0, N], a context that leaves the table, or a page outside [0, P) is
- * recorded as GDR_ERR_DEVICE_INDEX.
+ * recorded as GDR_ERR_DEVICE_INDEX. No array that a call writes (workspace included) may overlap another
+ * of its arrays; overlaps are refused (GDR_ERR_INVALID_ARG).
  * ---------------------------------------------------------------------------------------------
  */
 
