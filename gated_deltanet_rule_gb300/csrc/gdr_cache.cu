@@ -37,6 +37,7 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const CacheArgs a) {
   const int f = blockIdx.x, tid = threadIdx.x;
   const int dst = __ldg(a.dst + f);
   bool bad = dst < 0 || dst >= a.rows;
+  __shared__ int s_have;   // reserve: written by one thread (of a row that is refused by more)
   int src = dst, n = 0, have = 0, need = 0;
   if (kMode == kFork) {
     src = __ldg(a.src + f);
@@ -61,19 +62,19 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const CacheArgs a) {
         bad = __syncthreads_or(off);
         need = n % a.page ? 1 : 0;
       } else {
-        bool lost = false;                              // a page behind a gap
-        for (int m0 = 0; m0 < a.M; m0 += kThreads) {    // pages held: the leading entries
-          const int m = m0 + tid;
-          const bool holds = m < a.M && row[m] >= 0;
-          const int held = __syncthreads_count(holds);
-          lost |= holds && tid >= held;
-          have += held;
-          if (held < kThreads) break;
+        // pages held: the leading entries. The entry before the first empty one says how many; a page right
+        // behind an empty entry, wherever it lies, says that they do not lie together
+        bool off = false;
+        for (int m = tid; m < a.M; m += kThreads) {
+          const int e = row[m], after = m + 1 < a.M ? row[m + 1] : -1;
+          off |= e >= a.P || (e < 0 && after >= 0);
+          if (e >= 0 && after < 0) s_have = m + 1;
+          if (e < 0 && m == 0) s_have = 0;
         }
+        bad = __syncthreads_or(off);
+        have = s_have;
+        bad = bad || (long long)have * a.page < n;      // pages of the context that never were there
         need = pages > have ? pages - have : 0;
-        bad = (long long)have * a.page < n;             // pages of the context that never were there
-        for (int m = have + tid; m < pages; m += kThreads) lost |= row[m] >= 0;
-        if (__syncthreads_or(lost)) bad = true;
       }
     }
   }

@@ -329,7 +329,8 @@ gdr_status gdr_backward_chunked_saved(const void* q, const void* k, const void* 
  * rows (sequences, forks) share:
  *   k_pages, v_pages [P, page, Hk, D] dt   one layer's pages (one layer of [layers, P, page, Hk, D])
  *   table [rows, M] int32                  row b's positions [m page, (m+1) page) live in page
- *                                          table[b][m]; -1 where the row holds none
+ *                                          table[b][m]; negative (-1 as the calls write it) where the
+ *                                          row holds none
  *   ctx   [rows] int32                     committed positions of each row
  * page is 16, 32, 64 or 128 and M page at most 2^31 - 256; D is 64, 128 or 256; Hq is a multiple of Hk
  * (query head h reads key head h / (Hq / Hk)). Drafted nodes 0 .. N-1 of row b (node 0 the last committed
