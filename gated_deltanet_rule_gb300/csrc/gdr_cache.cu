@@ -31,52 +31,52 @@ enum Mode { kFork = 0, kReserve = 1, kFree = 2 };
 
 // One block per listed row. A row is refused (untouched, kErrDeviceIndex) when its index or its
 // source's is out of range, when an earlier entry lists it too, when a fork's source is itself a
-// forked row, or when its context or a page it needs is out of range.
+// forked row, or when the context (the source's in a fork; not looked at by free), a page that it needs
+// or a page that the row holds is out of range.
 template <int kMode>
 __global__ void __launch_bounds__(kThreads) release_kernel(const CacheArgs a) {
+  __shared__ int s_have;
   const int f = blockIdx.x, tid = threadIdx.x;
-  const int dst = __ldg(a.dst + f);
-  bool bad = dst < 0 || dst >= a.rows;
-  __shared__ int s_have;   // reserve: written by one thread (of a row that is refused by more)
-  int src = dst, n = 0, have = 0, need = 0;
-  if (kMode == kFork) {
-    src = __ldg(a.src + f);
-    bad = bad || src < 0 || src >= a.rows;
-  }
-  for (int g = tid; g < a.F; g += kThreads) {
-    const int other = __ldg(a.dst + g);
-    if (g < f && other == dst) bad = true;
-    if (kMode == kFork && other == src) bad = true;
-  }
-  bad = __syncthreads_or(bad);
-  if (!bad && kMode != kFree) {
-    n = a.ctx[src];
-    const long long end = (long long)n + (kMode == kReserve ? a.extra : 0);
-    bad = n < 0 || end > (long long)a.M * a.page;
-    if (!bad) {
-      const int32_t* row = a.table + (size_t)src * a.M;
-      const int pages = (int)((end + a.page - 1) / a.page);
-      if (kMode == kFork) {
-        bool off = false;
-        for (int m = tid; m < pages; m += kThreads) off |= row[m] < 0 || row[m] >= a.P;
-        bad = __syncthreads_or(off);
-        need = n % a.page ? 1 : 0;
+  const int dst = __ldg(a.dst + f), src = kMode == kFork ? __ldg(a.src + f) : dst;
+  bool bad = dst < 0 || dst >= a.rows || src < 0 || src >= a.rows;
+  int n = 0, pages = 0, need = 0;
+  // (a row that another entry lists may be released under these reads: it is refused whatever they see)
+  if (!bad) {
+    for (int g = tid; g < a.F; g += kThreads) {
+      const int other = __ldg(a.dst + g);
+      bad |= (g < f && other == dst) || (kMode == kFork && other == src);
+    }
+    const int32_t* held = a.table + (size_t)dst * a.M;
+    if (kMode != kReserve)   // a page that is none cannot be given back
+      for (int m = tid; m < a.M; m += kThreads) bad |= held[m] >= a.P;
+    if (kMode != kFree) {
+      n = a.ctx[src];
+      const long long end = (long long)n + (kMode == kReserve ? a.extra : 0);
+      if (n < 0 || end > (long long)a.M * a.page) {
+        bad = true;
+      } else if (kMode == kFork) {
+        const int32_t* from = a.table + (size_t)src * a.M;
+        pages = (int)((end + a.page - 1) / a.page);
+        for (int m = tid; m < pages; m += kThreads) bad |= from[m] < 0 || from[m] >= a.P;
       } else {
         // pages held: the leading entries. The entry before the first empty one says how many; a page right
-        // behind an empty entry, wherever it lies, says that they do not lie together
-        bool off = false;
+        // behind an empty entry, wherever it lies, says that they do not lie together (the row is refused)
+        pages = (int)((end + a.page - 1) / a.page);
         for (int m = tid; m < a.M; m += kThreads) {
-          const int e = row[m], after = m + 1 < a.M ? row[m + 1] : -1;
-          off |= e >= a.P || (e < 0 && after >= 0);
+          const int e = held[m], after = m + 1 < a.M ? held[m + 1] : -1;
+          bad |= e >= a.P || (e < 0 && after >= 0);
           if (e >= 0 && after < 0) s_have = m + 1;
           if (e < 0 && m == 0) s_have = 0;
         }
-        bad = __syncthreads_or(off);
-        have = s_have;
-        bad = bad || (long long)have * a.page < n;      // pages of the context that never were there
-        need = pages > have ? pages - have : 0;
       }
     }
+  }
+  bad = __syncthreads_or(bad);
+  if (!bad && kMode == kFork) need = n % a.page ? 1 : 0;
+  if (!bad && kMode == kReserve) {
+    const int have = s_have;
+    need = pages > have ? pages - have : 0;
+    bad = (long long)have * a.page < n;   // pages of the context that never were there
   }
   if (bad) {
     if (tid == 0) {
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const CacheArgs a) {
     int32_t* row = a.table + (size_t)dst * a.M;
     for (int m = tid; m < a.M; m += kThreads) {
       const int e = row[m];
-      if (e >= 0 && e < a.P) atomicSub(a.refs + e, 1);
+      if (e >= 0) atomicSub(a.refs + e, 1);
       row[m] = -1;
     }
     if (tid == 0) a.ctx[dst] = 0;

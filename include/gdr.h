@@ -457,8 +457,9 @@ gdr_status gdr_verify_draft(const int32_t* tokens, const int32_t* parents, const
  *   (path rising, as gdr_verify_draft leaves it), and new_ctx[b] = ctx[b] + n_path[b]. new_ctx may
  *   not overlap ctx.
  * A row is refused, untouched, with GDR_ERR_DEVICE_INDEX, if its index is out of range, an earlier
- * entry lists it too, a fork's source is itself listed as dst, its context or pages are out of range
- * (reserve: or fewer than its context needs, or one behind an empty entry), or its path does not rise
+ * entry lists it too, a fork's source is itself listed as dst, its context (a fork's source's; free does
+ * not look at it) or any page that it or its source's context holds is out of range (reserve: or it has
+ * fewer pages than its context needs, or one behind an empty entry), or its path does not rise
  * inside the table. Where pages run out (GDR_ERR_NO_PAGES) a row to be reserved stays as it was and a row
  * to be forked is left empty.
  */

@@ -50,3 +50,25 @@ def test_reserve_refuses_a_page_out_of_range(at, entry):
         _refused(gdr.gdr_cache_reserve, *d[2:], _i([0, 1]), extra, 16)
         pool.reserve([1], extra)
         _same(pool, d)
+
+
+@pytest.mark.parametrize("entry", ["P", 2 ** 31 - 1])
+@pytest.mark.parametrize("at", [0, 2, 3, 400])
+def test_free_refuses_a_page_out_of_range(at, entry):
+    """A page that is none cannot be given back: the row is left as it is."""
+    pool, d = _pool([40, 100, 0], 4, 500, 16, layers=1, Hk=1)
+    d[2][0, at] = pool.table[0][at] = len(pool.refs) if entry == "P" else entry
+    _refused(gdr.gdr_cache_free, *d[2:], _i([0, 1, 2]))
+    pool.release(1)
+    pool.release(2)
+    _same(pool, d)
+
+
+@pytest.mark.parametrize("entry", ["P", 2 ** 31 - 1])
+@pytest.mark.parametrize("at", [0, 2, 3, 400])
+def test_fork_refuses_a_row_that_holds_a_page_out_of_range(at, entry):
+    pool, d = _pool([40, 100, 60], 5, 500, 16, layers=1, Hk=1)
+    d[2][2, at] = pool.table[2][at] = len(pool.refs) if entry == "P" else entry
+    _refused(gdr.gdr_cache_fork, *d, _i([0, 0, 1]), _i([2, 3, 4]))
+    pool.fork([0, 1], [3, 4])
+    _same(pool, d)
