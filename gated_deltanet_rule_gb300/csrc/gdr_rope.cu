@@ -16,9 +16,10 @@
 // the instructions.
 //
 // Angles: pos inv_freq is formed in turns modulo one by 64-bit integer arithmetic (inv_freq / 2 pi as
-// a 64-bit binary fraction, times the position, dropping whole turns), exact to 2^-32 turn at any
-// 31-bit position; float32 angles would be off by 0.06 rad at position 2^20, and float64 arithmetic
-// runs at 1/64 of the float32 rate here. The fraction is reduced to an eighth turn before sincospif.
+// a 64-bit binary fraction, times the position, dropping whole turns), to within 2^-31 turn at any 32-bit
+// position (half of 2^-32 from the fraction, 2^-32 from the bits dropped behind it); float32 angles would
+// be off by 0.06 rad at position 2^20, and float64 arithmetic runs at 1/64 of the float32 rate here. The
+// fraction is reduced to an eighth turn before sincospif.
 #include <algorithm>
 #include <cstring>
 #include <type_traits>
@@ -130,18 +131,28 @@ struct Ring {
   __device__ __forceinline__ const T* row(int slot, int piece) const { return reinterpret_cast<const T*>(at(slot, piece)); }
 };
 
-// inv_freq / (2 pi) modulo one as a 64-bit binary fraction, from the bits of the double.
+__device__ __forceinline__ int exponent(double f) { return (int)(((uint64_t)__double_as_longlong(f) >> 52) & 0x7FF) - 1023; }
+
+// f / (2 pi) modulo one as a 64-bit binary fraction, from the bits of the double, to within one unit: a
+// product with enough digits of 1 / (2 pi) that those of the whole turns can be dropped (the argument
+// reduction of Payne and Hanek, 1983). 1 / (2 pi) = C 2^-66 with C = 2^65 / pi, and |f| = m 2^(e - 63), so
+// the fraction is m C 2^-64 2^(e - 1) modulo 2^64 (e = exponent(f)).
+// kFar: any |f| < 2^62; otherwise |f| < 4.
+template <bool kFar>
 __device__ __forceinline__ uint64_t turn_fraction(double f) {
   const uint64_t bits = (uint64_t)__double_as_longlong(f);
-  const int e = (int)((bits >> 52) & 0x7FF) - 1023;
-  if (e == -1023) return 0;   // zero (and subnormals: below 2^-1022 rad per position)
-  const uint64_t m = (bits << 11) | 0x8000000000000000ull;                 // f = m 2^(e - 63)
-  // 1 / (2 pi) = C 2^-66, C = round(2^65 / pi); m C 2^-64 2^(e - 65) = f / (2 pi)
-  const uint64_t t = __umul64hi(m, 0xA2F9836E4E44152Aull);
-  const int sh = e - 1;                                                    // fraction = t 2^sh mod 2^64
-  uint64_t r = 0;
-  if (sh >= 0) r = sh < 64 ? t << sh : 0;
-  else if (sh > -64) r = t >> -sh;
+  const int e = exponent(f), sh = e - 1;
+  const uint64_t m = (bits << 11) | 0x8000000000000000ull;
+  uint64_t r;
+  if (kFar && sh > 0) {   // the bits shifted in come from 64 more bits of C, rounded
+    const uint64_t c1 = 0xA2F9836E4E441529ull, c0 = 0xFC2757D1F534DDC1ull;
+    const uint64_t mid = m * c1, low = mid + __umul64hi(m, c0);
+    const uint64_t high = __umul64hi(m, c1) + (low < mid);
+    r = (high << sh) | (low >> (64 - sh));
+  } else {                // C rounded; zero and what is below 2^-64 turn per position: 0
+    const uint64_t t = __umul64hi(m, 0xA2F9836E4E44152Aull);
+    r = sh > -64 ? t >> (-sh & 63) : 0;
+  }
   return (bits >> 63) ? 0ull - r : r;
 }
 
@@ -181,13 +192,10 @@ struct Lane {
 template <int kE>
 __device__ __forceinline__ void form_angles(const RopeArgs& a, long long t0, int n, float* cs) {
   const int half = a.R / 2;
-  for (int x = threadIdx.x; x < n * half; x += kThreads) {
-    const int t = x / half, j = x - t * half;
-    float c, s;
-    turn_sincos(turn_fraction(__ldg(a.inv_freq + j)), __ldg(a.pos + t0 + t), c, s);
-    // runs of [lane][4]: the lanes' first four cosines, (kE = 8) their last four, then sines, so that the
-    // lanes of a head read neighbouring 16 bytes. Pair j is entry e of lane l: half-split j = kE l + e;
-    // interleaved j = kE/2 l + e in a lane's first run, R/4 + kE/2 l + e - kE/2 in its second
+  // runs of [lane][4]: the lanes' first four cosines, (kE = 8) their last four, then sines, so that the
+  // lanes of a head read neighbouring 16 bytes. Pair j is entry e of lane l: half-split j = kE l + e;
+  // interleaved j = kE/2 l + e in a lane's first run, R/4 + kE/2 l + e - kE/2 in its second
+  auto put_angle = [&](int t, int j, float c, float s) {
     int l = j / kE, e = j % kE;
     if (a.interleaved) {
       const int second = 4 * j >= a.R, k = second ? j - a.R / 4 : j;
@@ -197,6 +205,27 @@ __device__ __forceinline__ void form_angles(const RopeArgs& a, long long t0, int
     float* at = cs + t * a.R + (e >> 2) * (2 * a.R / kE) + l * 4 + (e & 3);
     at[0] = c;
     at[a.R / 2] = s;
+  };
+  bool far = false;
+  for (int x = threadIdx.x; x < n * half; x += kThreads) {
+    const int t = x / half, j = x - t * half;
+    const double f = __ldg(a.inv_freq + j);
+    far |= exponent(f) >= 2;
+    float c, s;
+    turn_sincos(turn_fraction<false>(f), __ldg(a.pos + t0 + t), c, s);
+    put_angle(t, j, c, s);
+  }
+  // a thread that met 4 rad per position or more (no position encoding's frequency) forms those angles again.
+  // With the choice in the loop above 8192 tokens of 32 + 8 heads took 36.4 us instead of 34.1
+  if (!far) return;
+#pragma unroll 1
+  for (int x = threadIdx.x; x < n * half; x += kThreads) {
+    const int t = x / half, j = x - t * half;
+    const double f = __ldg(a.inv_freq + j);
+    if (exponent(f) < 2) continue;
+    float c = NAN, s = NAN;   // 2^62 and more, infinite or nan: no angle
+    if (exponent(f) < 62) turn_sincos(turn_fraction<true>(f), __ldg(a.pos + t0 + t), c, s);
+    put_angle(t, j, c, s);
   }
 }
 

@@ -354,7 +354,8 @@ gdr_status gdr_backward_chunked_saved(const void* q, const void* k, const void* 
  *   inv_freq [R/2] float64 radians per position;  pos [B, N] int32
  *   q_out [B, N, Hq, D], k_out [B, N, Hk, D] dt   contiguous; may not overlap q or k
  * R is a multiple of 16 in [0, D]. Arithmetic is float32 with one rounding of the outputs; angles are
- * formed modulo a turn in 64-bit integers (exact to 2^-32 turn at any position).
+ * formed modulo a turn in 64-bit integers (to within 2^-31 turn at any position, for |inv_freq| < 2^62; an
+ * inv_freq that is larger, infinite or nan makes its pair nan).
  */
 gdr_status gdr_qk_norm_rope(const void* q, const void* k, const float* q_w, const float* k_w,
                             const double* inv_freq, const int32_t* pos, float eps, int interleaved, void* q_out,
