@@ -407,7 +407,8 @@ gdr_status gdr_qk_norm_rope_backward(const void* q, const void* k, const float* 
  * is out of range counts as having no nodes; a page out of range is read as zeros; both record
  * GDR_ERR_DEVICE_INDEX. bfloat16 only (dt other than GDR_BF16: GDR_ERR_UNSUPPORTED), Hq / Hk <= 128.
  * Scores, sums and accumulators are float32; the softmax weights are rounded to bfloat16 for their
- * product with v, o once at the end.
+ * product with v, o once at the end. The same call gives the same bits every time; where a row's sums are
+ * cut follows from all rows' lengths, so a row beside other rows may round differently.
  */
 size_t gdr_tree_attn_workspace_bytes(int D);
 gdr_status gdr_tree_attn(const void* q, const void* k_pages, const void* v_pages, const int32_t* table,
