@@ -137,8 +137,8 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const CacheArgs a)
     wanted += total;
   }
   int found = 0;
-  for (int p0 = 0; p0 < a.P && found < wanted; p0 += kAllocThreads * 4) {
-    const int p = p0 + (int)threadIdx.x * 4;
+  for (long long p0 = 0; p0 < a.P && found < wanted; p0 += kAllocThreads * 4) {   // (P may be up to 2^31 - 1)
+    const long long p = p0 + (int)threadIdx.x * 4;
     int free4 = 0, count = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kAllocThreads) alloc_kernel(const CacheArgs a)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       if (free4 >> e & 1) {
-        if (at < wanted) ws_list(a)[at] = p + e;
+        if (at < wanted) ws_list(a)[at] = (int)p + e;
         ++at;
       }
     found += total;

@@ -72,3 +72,18 @@ def test_fork_refuses_a_row_that_holds_a_page_out_of_range(at, entry):
     _refused(gdr.gdr_cache_fork, *d, _i([0, 0, 1]), _i([2, 3, 4]))
     pool.fork([0, 1], [3, 4])
     _same(pool, d)
+
+
+def test_as_many_pages_as_32_bits_count():
+    """The search for free pages ends where the counts do, past every page in use."""
+    P = 2 ** 31 - 1
+    refs = torch.ones(P, dtype=torch.int32, device="cuda")
+    table, ctx = torch.full((2, 4), -1, dtype=torch.int32, device="cuda"), _i([0, 0])
+    gdr.gdr_cache_reserve(table, ctx, refs, _i([0]), 10, 16)
+    with pytest.raises(gdr.GdrError) as e:
+        gdr.gdr_sync_status()
+    assert e.value.status == gdr.GDR_ERR_NO_PAGES and (table == -1).all()
+    refs[P - 2:] = 0
+    gdr.gdr_cache_reserve(table, ctx, refs, _i([1]), 20, 16)
+    gdr.gdr_sync_status()
+    assert table.tolist() == [[-1] * 4, [P - 2, P - 1, -1, -1]] and (refs[P - 3:] == 1).all()
