@@ -216,7 +216,7 @@ __device__ __forceinline__ void form_angles(const RopeArgs& a, long long t0, int
     put_angle(t, j, c, s);
   }
   // a thread that met 4 rad per position or more (no position encoding's frequency) forms those angles again.
-  // With the choice in the loop above 8192 tokens of 32 + 8 heads took 36.4 us instead of 34.1
+  // With the choice in the loop above 8192 tokens of 32 + 8 heads took 36.4 us instead of 33.3
   if (!far) return;
 #pragma unroll 1
   for (int x = threadIdx.x; x < n * half; x += kThreads) {
@@ -317,9 +317,9 @@ struct Kind {
 
 // Normed, turned and written (kPages: keys into the pages, values copied there). HBM-bound: each element
 // is read and written once; every lane has kDepth rows in flight in shared memory. Measured: 8192 tokens of
-// 32 + 8 heads of 128, bfloat16: 33.7 us, 73% of the copy bandwidth (a plain
-// copy of as many bytes: 28.9 us; with the rows loaded into registers and lanes 32 bytes apart 37.6 us; with
-// blocks that walk both kinds, as the gradient's do, 36.5 us).
+// 32 + 8 heads of 128, bfloat16: 31.8 us a call among others, 78% of the copy bandwidth. As a replayed graph
+// 33.3 us, a plain copy of as many bytes 28.9. (When it took 34.1: with the rows loaded into registers and
+// lanes 32 bytes apart 37.6, with blocks that walk both kinds, as the gradient's do, 36.5.)
 template <typename T, int D, bool kPages, bool kInter>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a) {
   constexpr int kRun = 8 * sizeof(T) / 16, kPieces = 2 * kRun;   // 16-byte pieces of a run, of a lane's row
@@ -430,9 +430,10 @@ constexpr int kBwdBlocks = kNumSMs * kPerSM;   // blocks of the gradient (one wa
 // As the forward, but lanes hold half as much, and a block walks the queries of its tokens and then their
 // keys, keeping the weight gradients of a lane's eight elements in registers; it adds its lanes in a fixed
 // order and writes a row of partial sums of each kind, which the second kernel adds in order: no atomics, the
-// same bits every time. Measured: 3 x 2731 tokens of 16 + 2 heads of 256, bfloat16: 59.7 us, 75% of the copy
-// bandwidth (a plain copy of as many bytes: 48.6 us). With blocks of one kind each, whose work was uneven,
-// 65.6 us; with sixteen elements a lane and half the warps besides, 67.7 us.
+// same bits every time. Measured: 3 x 2731 tokens of 16 + 2 heads of 256, bfloat16: 57.6 us a call among
+// others, 77% of the copy bandwidth. As a replayed graph 58.1 us (a plain copy of as many bytes 48.6; with
+// blocks of one kind each, whose work was uneven, 65.6; with sixteen elements a lane and half the warps
+// besides, 67.7).
 template <typename T, int D, bool kInter>
 __global__ void __launch_bounds__(kThreads, kPerSM) qk_norm_rope_bwd_kernel(const RopeArgs a) {
   using V = std::conditional_t<sizeof(T) == 2, uint2, uint4>;   // a run of four elements

@@ -31,15 +31,17 @@
 // results written), which count as kPad tiles. An item cut across blocks leaves its parts (O / l and lse in
 // float32) in the workspace and a second kernel joins them in order.
 //
-// Measured (bfloat16, GPU time of a call): one token over 700 positions 14.4 us (latency); 16 trees of 13
-// nodes over up to 8192 positions, 32 / 8 heads of 128: 73.4 us, 72% of the copy bandwidth (95% while it
-// streams); 8 trees of 64 nodes over up to 16384, 32 / 4 heads of 128: 93.8 us, 47% of the matrix rate; 2
-// trees of 7 over 131072, 16 / 2 heads of 256: 81.5 us, 75% of the copy bandwidth.
+// Measured (bfloat16, a call among others): one token over 700 positions 12.3 us (latency); 16 trees of 13
+// nodes over up to 8192 positions, 32 / 8 heads of 128: 72.4 us, 73% of the copy bandwidth (95% while it
+// streams); 8 trees of 64 nodes over up to 16384, 32 / 4 heads of 128: 93.9 us, 47% of the matrix rate; 2
+// trees of 7 over 131072, 16 / 2 heads of 256: 80.5 us, 76% of the copy bandwidth. (Comparisons below that
+// give slightly other times for these are of replayed graphs.)
 //
 // The running maximum is kept as a reference that moves only when the maximum has grown by more than 8
 // (in log2): P <= 2^8 then, the sums stay in range, and O in TMEM is rescaled only at those rare tiles.
-// P is rounded to bf16 for the product with V (one rounding of 2^-9 relative per term, independent
-// between terms); the sum l adds the unrounded P in float32.
+// P is rounded to bf16 for the product with V, as a matrix instruction takes both operands of one type (one
+// rounding of at most 2^-8 relative per term, independent between terms: outputs are off by 0.0023 of their
+// norm, with float32 weights it would be 0.0017); the sum l adds the unrounded P in float32.
 //
 // Masked places: K of an unseen position only enters a score that is replaced by -inf. V is different
 // (0 times inf is nan), so tiles that reach past ctx have V cleaned in shared memory first: positions
@@ -63,8 +65,10 @@ constexpr int kThreads = 384;   // warps: 0 loads, 1 products, 2-3 idle, 4-11 so
 constexpr int kBlocks = kNumSMs;
 constexpr int kM = 128;         // rows of an M tile
 constexpr float kLog2e = 1.4426950408889634f;
-// Units that an item's start and end count for (16 rows of 13 nodes: 77.3 us with 0, 75.8 with 3; 8 of 64
-// nodes over 16384 positions: 100.1 and 95.6; 2 and 4 are within 1% of 3).
+// Units that an item's start and end count for. 16 rows of 13 nodes over up to 8192 positions with 0, 2, 3, 4
+// and 6: heads of 64 53.6, 51.9, 51.5, 52.1, 53.3 us; of 128 75.3, 73.5, 73.7, 74.0, 74.5; of 256 57.9, 57.0,
+// 57.0, 56.8, 56.4. 8 rows of 64 nodes over up to 16384: heads of 64 86.1, 84.5, 83.0, 83.8, 85.2; of 128
+// 97.9, 94.7, 93.6, 93.4, 93.6. Two rows over 131072: within 1% from 2 on.
 constexpr int kPad = 3;
 constexpr long long kDrainBudget = 2000000000ll;   // cycles an aborting block waits for its own work
 
@@ -1016,7 +1020,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // bound by their latency (38 parts of 224 rows of 256: 33 us by one warp a row, one part after the other).
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 // Blocks an SM: as many as fit at once, or the rest would begin their set-up only when the first kernel has
-// ended (16 rows of 13 nodes, 8 of 64: 74.6 and 95.4 us with 3, 73.6 and 93.6 with 4, 74.3 and 94.1 with 8).
+// ended. With 2, 3, 4 and 8: 16 rows of 13 nodes, heads of 64 55.3, 53.1, 51.5, 51.7 us, of 128 76.5, 74.9,
+// 73.7, 75.0, of 256 66.3, 58.7, 57.0, 55.5; 8 rows of 64 nodes, heads of 64 92.5, 85.6, 83.0, 81.8, of 128
+// 101.8, 95.8, 93.6, 94.2.
 constexpr int kJoinPerSM = 4;
 template <int D, int kRows, int KT>
 __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const __grid_constant__ Args a) {
@@ -1238,7 +1244,13 @@ cudaError_t launch(const TreeAttnArgs& p, cudaStream_t st) {
 
 template <int D>
 cudaError_t launch_two(const TreeAttnArgs& a, cudaStream_t s) {
-  // more nodes than one M tile holds: two M tiles share the key/value tiles' way through shared memory
+  // more nodes than one M tile holds: two M tiles share the key/value tiles' way through shared memory and
+  // from HBM. What decides is whether the keys and values fit in L2, which the host cannot know (the contexts
+  // are on the device). Where they do not, kWide is far ahead (heads of 64, then of 128; kWide and kNarrow):
+  // 16 rows of 17 nodes over up to 32768 positions, 32 / 4 heads 123 and 150, 142 and 222 us; 8 rows of 64
+  // nodes over 65536, 32 / 8 heads 246 and 343, 290 and 456; 8 rows of 64 nodes over 16384, 32 / 4 heads of 128
+  // 95 and 111. Where they do, kNarrow is ahead by up to a fifth: 8 rows of 17 and of 32 nodes over 8192, 32 / 4
+  // heads 39.0 and 34.9, 43.0 and 39.7 us, and 44.5 and 35.2, 49.4 and 41.6; a prefill chain of 2048 by 4%.
   return a.N > kM / (a.Hq / a.Hk) ? launch<D, kWide>(a, s) : launch<D, kNarrow>(a, s);
 }
 

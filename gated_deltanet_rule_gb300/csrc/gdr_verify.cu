@@ -18,15 +18,16 @@
 // step by step: block, warp, an eighth of its run, ... , and then chunk, lane and entry at once.
 // A pass is bound by the latency of its loads and, over many rows, by its arithmetic (about 20
 // instructions an entry); blocks of 256 threads keep 48 rows of 131072 entries resident at once.
-// Measured: a float32 chain of 6 over 32000 entries 8.5 us, 48 float32 trees of 24 over 131072 39 us. Steps:
+// Measured: a float32 chain of 6 over 32000 entries 8.9 us, 48 float32 trees of 24 over 131072 35 to 46 us by
+// how many drafts the inputs have refused. Steps (on one input):
 // float64 reductions and scalars 17.8 / 104 us; pairs of floats in the passes, four entries a lane,
 // asynchronous copies 12.4 / 41.0 us; pairs in the walk and the search as well 10.2 / 39 us; the last chunks
 // searched at once by one warp, first nodes read along with the length 8.5 / 39 us. Clusters of sixteen
 // shorten a row's pass but no longer keep the rows resident: 12.4 / 50.5 us against 12.4 / 41.0. Two chunks
 // at a time spill: 11.0 / 44.1 us.
 //
-// Sums decide whole numbers, so they are carried to about 2^-46: unevaluated pairs of floats (error-free
-// sums of two floats) throughout. Float64, at 1/64 of the float32 rate, took longer for the walk's and the
+// Sums decide whole numbers, so they are carried to about 2^-46: unevaluated pairs of floats (Knuth's
+// error-free sum of two floats) throughout. Float64, at 1/64 of the float32 rate, took longer for the walk's and the
 // search's few scalars than the passes did for the vocabulary.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -7,7 +7,8 @@ Each function checks tensor devices, dtypes, shapes and contiguity, allocates ou
 caller did not pass (memory of the launch stream: plumbing, no arithmetic), hands raw device pointers
 and the current CUDA stream, or the one given, to the library and raises ``GdrError`` on a non-OK status. Every
 step of the computation runs in the library's kernels; there is no CPU fallback: if
-``libgdr.so`` is missing this module raises instead of computing anything.
+``libgdr.so`` is missing this module raises instead of computing anything. No call is recorded by
+autograd: gradients are calls of their own.
 """
 from __future__ import annotations
 

@@ -429,7 +429,7 @@ gdr_status gdr_tree_attn(const void* q, const void* k_pages, const void* v_pages
  *   tokens, parents [B, N] int32   node i > 0 has parent parents[i] in [0, i); node 0 is the root.
  *                                  A node with a parent or token out of range is no candidate
  *                                  (GDR_ERR_DEVICE_INDEX)
- *   lengths [B] int32              nodes of each row, in [0, N]; 0: path -1, n_path 0, next_token -1;
+ *   lengths [B] int32              nodes of each row (not NULL), in [0, N]; 0: path -1, n_path 0, next_token -1;
  *                                  outside: the row's outputs untouched, GDR_ERR_DEVICE_INDEX
  *   p [B, N, V], q [B, N, V] or NULL, dt   target and draft probabilities at each node (entries that
  *                                  are not > 0 count as 0); q's row of a node is what its children
