@@ -403,7 +403,8 @@ gdr_status gdr_qk_norm_rope_backward(const void* q, const void* k, const float* 
  *   lse [B, N, Hq] float32, or NULL;  scale > 0
  *   ws at least gdr_tree_attn_workspace_bytes(D) bytes (0 for a D that is not implemented)
  * A node that sees nothing, and every node at or past its row's length, gets o = 0 and lse = -inf.
- * Values of unseen positions do not matter, infinities and NaN included. A row whose length or context
+ * Values of unseen positions do not matter, infinities and NaN included; those of seen nodes reach o however
+ * small their weight. A row whose length or context
  * is out of range counts as having no nodes; a page out of range is read as zeros; both record
  * GDR_ERR_DEVICE_INDEX. bfloat16 only (dt other than GDR_BF16: GDR_ERR_UNSUPPORTED), Hq / Hk <= 128.
  * Scores, sums and accumulators are float32; the softmax weights are rounded to bfloat16 for their

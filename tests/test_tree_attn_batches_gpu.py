@@ -1,6 +1,8 @@
 """A row of gdr_tree_attn beside other rows: where its item is cut over blocks follows from all rows' units, so
 its bits may change with the batch, but alone and beside any others it stays within the bound of the float64
 form, and the same call always gives the same bits."""
+import math
+
 import pytest
 import torch
 
@@ -25,3 +27,25 @@ def test_a_row_alone_and_beside_others(D, N):
         _check(part, *got)
         again = _run(part)
         assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("ctx", [70, 640, 9000])   # a tile of both; tiles of their own, each a part; an item cut over many blocks
+def test_a_seen_infinity_of_vanishing_weight(ctx, D):
+    """A node's V holds infinities and a nan; its weight against the context's is below the smallest float."""
+    c = _case(1, 4, 4, 2, D, 64, [ctx], "tree", seed=D)
+    c["see"][0] = torch.eye(4, dtype=torch.bool)
+    c["see"][0, 3, 2] = True
+    at = ctx + torch.arange(4)
+    pages = c["table"][0].long()[at // 64]
+    c["q"][:] = 8
+    c["k"][pages, at % 64] = -8                       # the nodes' scores: -64 D^1/2, at most -512
+    c["v"][pages[2], at[2] % 64, :, 5] = math.inf
+    c["v"][pages[2], at[2] % 64, :, 6] = -math.inf
+    c["v"][pages[2], at[2] % 64, :, 37] = math.nan
+    o, lse = _run(c)
+    rows = torch.tensor([2, 3])
+    assert (o[0, rows, :, 5] == math.inf).all() and (o[0, rows, :, 6] == -math.inf).all() and torch.isnan(o[0, rows, :, 37]).all()
+    rest = torch.ones(D, dtype=torch.bool)
+    rest[[5, 6, 37]] = False
+    assert torch.isfinite(o[0, :2]).all() and torch.isfinite(o[..., rest]).all() and torch.isfinite(lse).all()
