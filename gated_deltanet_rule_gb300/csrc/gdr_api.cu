@@ -692,6 +692,9 @@ const char* gdr_kernel_name(int id) {
     case kKernVerifyDraft: return "gdr_verify_draft";
     case kKernCacheAlloc: return "gdr_cache_alloc";
     case kKernCacheCopy: return "gdr_cache_copy";
+    case kKernBlockNorm: return "gdr_block_norm";
+    case kKernBlockNormBwd: return "gdr_block_norm_backward";
+    case kKernSample: return "gdr_sample";
   }
   return nullptr;
 }

@@ -138,7 +138,7 @@ void check(gdr_status st) {
   throw Error{};
 }
 
-PyObject* wrap(std::initializer_list<Tensor> ts) {
+PyObject* wrap(std::initializer_list<Tensor> ts) {   // (a tensor that is not there: None)
   PyObject* t = PyTuple_New(ts.size());
   if (!t) throw Error{};
   Py_ssize_t i = 0;
@@ -375,6 +375,96 @@ PyObject* cache_compact(const Call& c) {
   return THPVariable_Wrap(new_ctx);
 }
 
+// logits, temperature, u, top_k, top_p, min_p, token, probs, want_probs, stream
+PyObject* sample(const Call& c) {
+  const Tensor* l = c.tensor(0, "logits");
+  const gdr_dtype dt = dtype(*l, "logits");
+  if (l->dim() != 2) refuse("logits must be [R, V]");
+  const int R = size(*l, 0, "logits' size"), V = size(*l, 1, "logits' size");
+  if (V > 1 && l->stride(1) != 1) refuse("logits: the last dimension must be contiguous");
+  const Tensor *t = c.of(1, "temperature", at::kFloat, {R}), *u = c.of(2, "u", at::kFloat, {R}, true);
+  const Tensor *k = c.ints(3, "top_k", {R}, true), *p = c.of(4, "top_p", at::kFloat, {R}, true);
+  const Tensor* m = c.of(5, "min_p", at::kFloat, {R}, true);
+  const bool with_probs = c.args[7] != Py_None || c.truth(8);
+  if (!u && c.args[6] != Py_None) refuse("token is drawn with u");
+  Tensor token, probs;
+  if (u) token = c.output(6, "token", {R}, at::kInt, *l);
+  if (with_probs) probs = c.output(7, "probs", {R, V}, at::kFloat, *l);
+  check(gdr_sample(ptr(l), R > 1 ? l->stride(0) : V, ptr<float>(t), ptr<float>(u), ptr<int32_t>(k), ptr<float>(p),
+                   ptr<float>(m), u ? ptr<int32_t>(&token) : nullptr, with_probs ? ptr<float>(&probs) : nullptr, R, V, dt,
+                   c.stream()));
+  return wrap({token, probs});
+}
+
+// Residual, block output, gate and weights of [..., C]: any leading dimensions whose rows lie at one stride.
+struct Block {
+  const Tensor *h, *y, *pre_w, *post_w, *gate, *scale;
+  long long rows, y_row, gate_row;
+  int C;
+  gdr_dtype dt;
+  static long long row_stride(const Tensor& t, const char* name, const Tensor& like) {
+    if (t.scalar_type() != like.scalar_type() || t.sizes() != like.sizes()) refuse("%s must have h's dtype and shape", name);
+    const int64_t n = t.dim();
+    if (t.size(n - 1) > 1 && t.stride(n - 1) != 1) refuse("%s: the last dimension must be contiguous", name);
+    long long row = 0, step = 0;   // stride of a row; what the next dimension's has to be
+    for (int64_t d = n - 2; d >= 0; --d) {
+      if (t.size(d) == 1) continue;
+      if (!row) row = t.stride(d);
+      else if (t.stride(d) != step) refuse("%s: rows must lie at one stride", name);
+      step = t.stride(d) * t.size(d);
+    }
+    return row ? row : t.size(n - 1);
+  }
+  // arguments 0 .. 5: h, y, pre_w, post_w, gate, scale
+  explicit Block(const Call& c) {
+    h = c.tensor(0, "h");
+    dt = dtype(*h, "h");
+    if (h->dim() < 1 || !h->is_contiguous()) refuse("h must be a contiguous tensor [..., C]");
+    C = size(*h, h->dim() - 1, "h's size");
+    rows = C > 0 ? h->numel() / C : 0;
+    y = c.tensor(1, "y");
+    gate = c.tensor(4, "gate", true);
+    y_row = row_stride(*y, "y", *h);
+    gate_row = gate ? row_stride(*gate, "gate", *h) : C;
+    pre_w = c.of(2, "pre_w", at::kFloat, {C});
+    post_w = c.of(3, "post_w", at::kFloat, {C}, true);
+    scale = c.of(5, "scale", at::kFloat, {C}, true);
+  }
+};
+
+// h, y, pre_w, post_w, gate, scale, eps, h_out, n_out, stream
+PyObject* block_norm(const Call& c) {
+  const Block b(c);
+  const float eps = (float)c.number(6);
+  Tensor h_out = c.output(7, "h_out", b.h->sizes(), b.h->scalar_type(), *b.h);
+  Tensor n_out = c.output(8, "n_out", b.h->sizes(), b.h->scalar_type(), *b.h);
+  check(gdr_block_norm(ptr(b.h), ptr(b.y), ptr(b.gate), ptr<float>(b.post_w), ptr<float>(b.scale), ptr<float>(b.pre_w),
+                       eps, h_out.data_ptr(), n_out.data_ptr(), b.rows, b.C, b.y_row, b.gate_row, b.dt, c.stream()));
+  return wrap({h_out, n_out});
+}
+
+// h, y, pre_w, post_w, gate, scale, dn, dh_out, eps, dh, ws, stream
+PyObject* block_norm_backward(const Call& c) {
+  const Block b(c);
+  const Tensor *dn = c.of(6, "dn", b.h->scalar_type(), b.h->sizes()), *dh_out = c.of(7, "dh_out", at::kFloat, b.h->sizes(), true);
+  const float eps = (float)c.number(8);
+  Tensor dh = c.output(9, "dh", b.h->sizes(), at::kFloat, *b.h);
+  Tensor ws = c.workspace(10, gdr_block_norm_backward_workspace_bytes(b.C), *b.h);
+  auto like = [&](at::ScalarType t) { return c.empty(b.h->sizes(), t, *b.h, true); };
+  auto channels = [&] { return c.empty({b.C}, at::kFloat, *b.h, true); };
+  Tensor dy = like(b.h->scalar_type()), dgate, dpre_w = channels(), dpost_w, dscale;
+  if (b.gate) dgate = like(b.h->scalar_type());
+  if (b.post_w) dpost_w = channels();
+  if (b.scale) dscale = channels();
+  auto at = [](const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
+  check(gdr_block_norm_backward(ptr(b.h), ptr(b.y), ptr(b.gate), ptr<float>(b.post_w), ptr<float>(b.scale),
+                                ptr<float>(b.pre_w), ptr<float>(dh_out), ptr(dn), eps, ptr<float>(&dh), dy.data_ptr(),
+                                at(dgate), ptr<float>(&dpre_w), static_cast<float*>(at(dpost_w)),
+                                static_cast<float*>(at(dscale)), b.rows, b.C, b.y_row, b.gate_row, b.dt, ws.data_ptr(),
+                                bytes_of(ws), c.stream()));
+  return wrap({dh, dy, dgate, dpre_w, dpost_w, dscale});
+}
+
 // No C++ exception leaves a call.
 template <PyObject* (*kFn)(const Call&), int kArgs>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -397,6 +487,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 PyMethodDef methods[] = {GDR_ENTRY(norm_rope, 11),   GDR_ENTRY(norm_rope_append, 16), GDR_ENTRY(norm_rope_backward, 12),
                          GDR_ENTRY(tree_attn, 13),   GDR_ENTRY(verify, 11),           GDR_ENTRY(cache_reserve, 8),
                          GDR_ENTRY(cache_fork, 9),   GDR_ENTRY(cache_free, 5),        GDR_ENTRY(cache_compact, 8),
+                         GDR_ENTRY(sample, 10),      GDR_ENTRY(block_norm, 10),       GDR_ENTRY(block_norm_backward, 12),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gdr_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -21,6 +21,9 @@ constexpr int kKernTreeAttnJoin = 12;
 constexpr int kKernVerifyDraft = 13;
 constexpr int kKernCacheAlloc = 14;
 constexpr int kKernCacheCopy = 15;
+constexpr int kKernBlockNorm = 16;
+constexpr int kKernBlockNormBwd = 17;
+constexpr int kKernSample = 18;
 
 constexpr int kNumSMs = 152;   // GB300
 constexpr int kErrNoPages = 6;   // device error code (gdr_status): a cache had too few free pages
@@ -139,6 +142,55 @@ struct CompactArgs {
 };
 constexpr int kCompactMaxPath = 2048;   // path entries whose slots fit the kernel's shared memory
 cudaError_t launch_cache_compact(const CompactArgs& a, cudaStream_t s);
+
+// Tokens drawn from filtered logits, and the probabilities that are left.
+struct SampleArgs {
+  const void* logits;        // [R, V], rows `stride` elements apart
+  const float* temperature;  // [R]
+  const float* u;            // [R] (with token)
+  const int32_t* top_k;      // [R] or NULL
+  const float* top_p;        // [R] or NULL
+  const float* min_p;        // [R] or NULL
+  int32_t* token;            // [R] or NULL
+  float* probs;              // [R, V] or NULL
+  int R, V;
+  long long stride;
+  bool bf16;
+  int* err;
+  int cluster;               // set by the launch: blocks of a row
+};
+constexpr int kSampleMaxV = 1 << 18;   // entries of a row that a cluster's shared memory holds
+cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s);
+
+// The norms around a block with its gate and residual scale: x = h + scale sigmoid(gate) norm(y), norm(x).
+struct BlockNormArgs {
+  const void* h;             // [rows, C]
+  const void* y;             // [rows, C], rows y_row elements apart
+  const void* gate;          // [rows, C] or NULL, rows gate_row elements apart
+  const float* post_w;       // [C] or NULL (y is not normed)
+  const float* scale;        // [C] or NULL (ones)
+  const float* pre_w;        // [C]
+  float eps;
+  void* h_out;
+  void* n_out;
+  long long rows, y_row, gate_row;
+  int C;
+  bool bf16;
+  // gradient
+  const float* dh_out;       // [rows, C] or NULL (zeros)
+  const void* dn;
+  float* dh;
+  void* dy;
+  void* dgate;               // (where there is a gate, a post norm, a scale)
+  float* dpre_w;
+  float* dpost_w;
+  float* dscale;
+  float* partial;
+};
+constexpr int kBlockNormMaxC = 16384;
+size_t block_norm_backward_workspace_bytes(int C);
+cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t s);
+cudaError_t launch_block_norm_backward(const BlockNormArgs& a, cudaStream_t s);
 
 // Lets a kernel use `bytes` of dynamic shared memory: set once on each device (`done`, a bit a device), as
 // setting it costs a call 0.8 us.

@@ -141,6 +141,30 @@ gdr_status check_ws(const void* ws, size_t given, size_t need, const char* who) 
   return GDR_OK;
 }
 
+gdr_status check_block_norm(const BlockNormArgs& a, gdr_dtype dt, const char* who) {
+  if (!a.h || !a.y || !a.pre_w) return fail(GDR_ERR_INVALID_ARG, "%s: h, y and pre_w must be non-NULL", who);
+  if (a.rows < 1 || a.C < 1) return fail(GDR_ERR_INVALID_ARG, "%s: sizes must be >= 1 (rows=%lld C=%d)", who, a.rows, a.C);
+  if (dt != GDR_F32 && dt != GDR_BF16) return fail(GDR_ERR_INVALID_ARG, "%s: unknown dtype %d", who, (int)dt);
+  if (a.C % 8 != 0 || a.C > kBlockNormMaxC || a.rows > 1ll << 40)
+    return fail(GDR_ERR_UNSUPPORTED, "%s: C=%d is not a multiple of 8 of at most %d, or rows=%lld exceeds 2^40", who, a.C, kBlockNormMaxC, a.rows);
+  if (!(a.eps >= 0.f)) return fail(GDR_ERR_INVALID_ARG, "%s: eps must be >= 0", who);
+  const int es = dt == GDR_BF16 ? 2 : 4;
+  for (long long s : {a.y_row, a.gate ? a.gate_row : a.C})
+    if (s < a.C || s * es % 16 != 0 || s > 1ll << 22)
+      return fail(GDR_ERR_INVALID_ARG, "%s: rows of y and gate must be a multiple of 16 bytes apart, from C to 2^22 elements", who);
+  for (const void* p : {a.h, a.y, a.gate, (const void*)a.post_w, (const void*)a.scale, (const void*)a.pre_w})
+    if (!aligned(p, 16)) return fail(GDR_ERR_INVALID_ARG, "%s: h, y, gate, post_w, scale and pre_w must be 16-byte aligned", who);
+  return GDR_OK;
+}
+// Outputs apart from one another and from all inputs (h NULL: compared by the caller).
+gdr_status apart_block_norm(const BlockNormArgs& a, std::initializer_list<Range> outs, std::initializer_list<Range> ins, const void* h, const char* who) {
+  const unsigned long long es = a.bf16 ? 2 : 4, c4 = a.C * 4ull, r = (unsigned long long)a.rows - 1;
+  const gdr_status st = apart(outs, ins, who);
+  if (st != GDR_OK) return st;
+  return apart(outs, {{h, (r + 1) * a.C * es, "h"}, {a.y, (r * a.y_row + a.C) * es, "y"}, {a.gate, (r * a.gate_row + a.C) * es, "gate"},
+                      {a.post_w, c4, "post_w"}, {a.scale, c4, "scale"}, {a.pre_w, c4, "pre_w"}}, who);
+}
+
 gdr_status no_device(const char* who) { return fail(GDR_ERR_CUDA, "%s: no CUDA device available", who); }
 
 }  // namespace
@@ -397,6 +421,92 @@ gdr_status gdr_cache_compact(void* k_cache, void* v_cache, const int32_t* table,
   const CompactArgs a{static_cast<uint8_t*>(k_cache), static_cast<uint8_t*>(v_cache), table, ctx, path, n_path, new_ctx,
                       layers, P, page, B, M, W, row_bytes, err};
   return launched(launch_cache_compact(a, reinterpret_cast<cudaStream_t>(stream)), who);
+}
+
+gdr_status gdr_sample(const void* logits, long long stride, const float* temperature, const float* u,
+                      const int32_t* top_k, const float* top_p, const float* min_p, int32_t* token, float* probs,
+                      int R, int V, gdr_dtype dt, gdr_stream_t stream) {
+  const char* who = "gdr_sample";
+  if (!logits || !temperature) return fail(GDR_ERR_INVALID_ARG, "%s: logits and temperature must be non-NULL", who);
+  if (!token && !probs) return fail(GDR_ERR_INVALID_ARG, "%s: token or probs must be non-NULL", who);
+  if ((token != nullptr) != (u != nullptr)) return fail(GDR_ERR_INVALID_ARG, "%s: token and u are given together", who);
+  if (R < 1 || V < 1) return fail(GDR_ERR_INVALID_ARG, "%s: sizes must be >= 1 (R=%d V=%d)", who, R, V);
+  if (dt != GDR_F32 && dt != GDR_BF16) return fail(GDR_ERR_INVALID_ARG, "%s: unknown dtype %d", who, (int)dt);
+  const int es = dt == GDR_BF16 ? 2 : 4;
+  const bool whole = aligned(logits, 16) && (R == 1 || stride * es % 16 == 0);
+  if (V > (whole ? kSampleMaxV : kSampleMaxV - 8) || R > 1 << 24)
+    return fail(GDR_ERR_UNSUPPORTED, "%s: R=%d exceeds 2^24, or V=%d 2^18 (2^18 - 8 where rows do not begin on 16 bytes)", who, R, V);
+  if (R > 1 && (stride < V || stride > (1ll << 32)))
+    return fail(GDR_ERR_INVALID_ARG, "%s: stride=%lld is below V=%d or above 2^32", who, stride, V);
+  if (!aligned(logits, es)) return fail(GDR_ERR_INVALID_ARG, "%s: logits must be aligned to their elements", who);
+  for (const void* p : {(const void*)temperature, (const void*)u, (const void*)top_k, (const void*)top_p, (const void*)min_p,
+                        (const void*)token, (const void*)probs})
+    if (!aligned(p, 4)) return fail(GDR_ERR_INVALID_ARG, "%s: arrays of 32-bit numbers must be 4-byte aligned", who);
+  const unsigned long long r4 = R * 4ull;
+  const gdr_status st = apart({{token, r4, "token"}, {probs, r4 * V, "probs"}},
+                              {{logits, ((unsigned long long)(R - 1) * (R > 1 ? stride : 0) + V) * es, "logits"},
+                               {temperature, r4, "temperature"}, {u, r4, "u"}, {top_k, r4, "top_k"}, {top_p, r4, "top_p"},
+                               {min_p, r4, "min_p"}}, who);
+  if (st != GDR_OK) return st;
+  SampleArgs a{};
+  a.logits = logits; a.temperature = temperature; a.u = u; a.top_k = top_k; a.top_p = top_p; a.min_p = min_p;
+  a.token = token; a.probs = probs; a.R = R; a.V = V; a.stride = R > 1 ? stride : 0; a.bf16 = dt == GDR_BF16;
+  a.err = device_error_word();
+  if (!a.err) return no_device(who);
+  return launched(launch_sample(a, reinterpret_cast<cudaStream_t>(stream)), who);
+}
+
+gdr_status gdr_block_norm(const void* h, const void* y, const void* gate, const float* post_w, const float* scale,
+                          const float* pre_w, float eps, void* h_out, void* n_out, long long rows, int C,
+                          long long y_row, long long gate_row, gdr_dtype dt, gdr_stream_t stream) {
+  const char* who = "gdr_block_norm";
+  BlockNormArgs a{};
+  a.h = h; a.y = y; a.gate = gate; a.post_w = post_w; a.scale = scale; a.pre_w = pre_w; a.eps = eps;
+  a.h_out = h_out; a.n_out = n_out; a.rows = rows; a.y_row = y_row; a.gate_row = gate_row; a.C = C; a.bf16 = dt == GDR_BF16;
+  gdr_status st = check_block_norm(a, dt, who);
+  if (st != GDR_OK) return st;
+  if (!h_out || !n_out) return fail(GDR_ERR_INVALID_ARG, "%s: h_out and n_out must be non-NULL", who);
+  if (!aligned(h_out, 16) || !aligned(n_out, 16))
+    return fail(GDR_ERR_INVALID_ARG, "%s: h_out and n_out must be 16-byte aligned", who);
+  const unsigned long long n = (unsigned long long)rows * C * (a.bf16 ? 2 : 4);
+  st = apart_block_norm(a, {{h_out, n, "h_out"}, {n_out, n, "n_out"}}, {}, h_out == h ? nullptr : h, who);
+  if (st == GDR_OK && h_out == h) st = apart({{n_out, n, "n_out"}}, {{h, n, "h"}}, who);
+  if (st != GDR_OK) return st;
+  return launched(launch_block_norm(a, reinterpret_cast<cudaStream_t>(stream)), who);
+}
+
+size_t gdr_block_norm_backward_workspace_bytes(int C) {
+  return C >= 8 && C % 8 == 0 && C <= kBlockNormMaxC ? block_norm_backward_workspace_bytes(C) : 0;
+}
+
+gdr_status gdr_block_norm_backward(const void* h, const void* y, const void* gate, const float* post_w,
+                                   const float* scale, const float* pre_w, const float* dh_out, const void* dn,
+                                   float eps, float* dh, void* dy, void* dgate, float* dpre_w, float* dpost_w,
+                                   float* dscale, long long rows, int C, long long y_row, long long gate_row,
+                                   gdr_dtype dt, void* ws, size_t ws_bytes, gdr_stream_t stream) {
+  const char* who = "gdr_block_norm_backward";
+  BlockNormArgs a{};
+  a.h = h; a.y = y; a.gate = gate; a.post_w = post_w; a.scale = scale; a.pre_w = pre_w; a.eps = eps;
+  a.rows = rows; a.y_row = y_row; a.gate_row = gate_row; a.C = C; a.bf16 = dt == GDR_BF16;
+  a.dh_out = dh_out; a.dn = dn; a.dh = dh; a.dy = dy; a.dgate = dgate; a.dpre_w = dpre_w; a.dpost_w = dpost_w; a.dscale = dscale;
+  a.partial = static_cast<float*>(ws);
+  gdr_status st = check_block_norm(a, dt, who);
+  if (st != GDR_OK) return st;
+  if (!dn || !dh || !dy || !dpre_w) return fail(GDR_ERR_INVALID_ARG, "%s: dn, dh, dy and dpre_w must be non-NULL", who);
+  if ((dgate != nullptr) != (gate != nullptr) || (dpost_w != nullptr) != (post_w != nullptr) || (dscale != nullptr) != (scale != nullptr))
+    return fail(GDR_ERR_INVALID_ARG, "%s: dgate, dpost_w and dscale are given exactly where gate, post_w and scale are", who);
+  for (const void* p : {(const void*)dh_out, dn, (const void*)dh, (const void*)dy, (const void*)dgate, (const void*)dpre_w,
+                        (const void*)dpost_w, (const void*)dscale})
+    if (!aligned(p, 16)) return fail(GDR_ERR_INVALID_ARG, "%s: every gradient must be 16-byte aligned", who);
+  const size_t need = block_norm_backward_workspace_bytes(C);
+  st = check_ws(ws, ws_bytes, need, who);
+  if (st != GDR_OK) return st;
+  const unsigned long long n = (unsigned long long)rows * C, es = a.bf16 ? 2 : 4, c4 = C * 4ull;
+  st = apart_block_norm(a, {{dh, n * 4, "dh"}, {dy, n * es, "dy"}, {dgate, n * es, "dgate"}, {dpre_w, c4, "dpre_w"},
+                            {dpost_w, c4, "dpost_w"}, {dscale, c4, "dscale"}, {ws, need, "ws"}},
+                        {{dn, n * es, "dn"}, {dh == dh_out ? nullptr : dh_out, n * 4, "dh_out"}}, h, who);
+  if (st != GDR_OK) return st;
+  return launched(launch_block_norm_backward(a, reinterpret_cast<cudaStream_t>(stream)), who);
 }
 
 }  // extern "C"

@@ -35,6 +35,7 @@ EXPORTS = ["gdr_chunk_workspace_bytes", "gdr_chunk_fwd", "gdr_chunk_fwd_varlen",
            "gdr_qk_norm_rope", "gdr_qk_norm_rope_append", "gdr_qk_norm_rope_backward_workspace_bytes",
            "gdr_qk_norm_rope_backward", "gdr_tree_attn_workspace_bytes", "gdr_tree_attn", "gdr_verify_draft",
            "gdr_cache_workspace_bytes", "gdr_cache_reserve", "gdr_cache_fork", "gdr_cache_free", "gdr_cache_compact",
+           "gdr_sample", "gdr_block_norm", "gdr_block_norm_backward_workspace_bytes", "gdr_block_norm_backward",
            "gdr_sync_status", "gdr_status_string", "gdr_last_error_message",
            "gdr_stage_timer_enable", "gdr_stage_timer_collect", "gdr_kernel_name", "gdr_debug_set_wait_budget"]
 
@@ -122,6 +123,15 @@ def lib() -> ctypes.CDLL:
     L.gdr_cache_free.restype = i
     L.gdr_cache_compact.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, i, ll, vp]
     L.gdr_cache_compact.restype = i
+    L.gdr_sample.argtypes = [vp, ll, fp, fp, vp, fp, fp, vp, fp, i, i, i, vp]
+    L.gdr_sample.restype = i
+    L.gdr_block_norm.argtypes = [vp, vp, vp, fp, fp, fp, f32, vp, vp, ll, i, ll, ll, i, vp]
+    L.gdr_block_norm.restype = i
+    L.gdr_block_norm_backward_workspace_bytes.argtypes = [i]
+    L.gdr_block_norm_backward_workspace_bytes.restype = sz
+    L.gdr_block_norm_backward.argtypes = [vp, vp, vp, fp, fp, fp, fp, vp, f32, fp, vp, vp, fp, fp, fp, ll, i, ll, ll, i,
+                                          vp, sz, vp]
+    L.gdr_block_norm_backward.restype = i
     L.gdr_sync_status.argtypes = [vp]
     L.gdr_sync_status.restype = i
     L.gdr_status_string.argtypes = [i]
@@ -582,6 +592,34 @@ def gdr_cache_compact(k_cache, v_cache, table, ctx, path, n_path, new_ctx=None, 
     """Moves the entries of the accepted paths (gdr_verify_draft's path, n_path) to the front of their
     rows in every layer; returns new_ctx = ctx + n_path (which may not be ctx itself)."""
     return _bind().cache_compact(k_cache, v_cache, table, ctx, path, n_path, new_ctx, _raw(stream))
+
+
+def gdr_sample(logits, temperature, u=None, top_k=None, top_p=None, min_p=None, token=None, probs=None,
+               want_probs: bool = False, stream=None):
+    """Tokens drawn from logits [R,V] (rows may be slices of wider ones) with temperature [R] (0: the largest
+    logit) and the uniform numbers u [R], of the tokens that top_k [R] int32 (0: all), top_p [R] and min_p [R]
+    leave. Returns (token [R] int32, or None without u; probs [R,V] float32, or None unless want_probs or probs
+    are given): the probabilities that gdr_verify_draft takes."""
+    return _bind().sample(logits, temperature, u, top_k, top_p, min_p, token, probs, want_probs, _raw(stream))
+
+
+def block_norm_backward_workspace_bytes(C: int) -> int:
+    return int(lib().gdr_block_norm_backward_workspace_bytes(C))
+
+
+def gdr_block_norm(h, y, pre_w, post_w=None, gate=None, scale=None, eps: float = 1e-6, h_out=None, n_out=None,
+                   stream=None):
+    """Between two blocks: x = h + scale sigmoid(gate) norm(y, post_w), then norm(x, pre_w), for h, y, gate
+    [...,C] (y and gate may be slices of one projection) and float32 weights [C]; without post_w y is not normed.
+    Returns (h_out = x, n_out) in h's dtype; h_out may be h."""
+    return _bind().block_norm(h, y, pre_w, post_w, gate, scale, eps, h_out, n_out, _raw(stream))
+
+
+def gdr_block_norm_backward(h, y, pre_w, post_w=None, gate=None, scale=None, dn=None, dh_out=None, eps: float = 1e-6,
+                            dh=None, ws=None, stream=None):
+    """Gradients of gdr_block_norm from dn (h's dtype) and dh_out (float32; None: zeros): (dh float32, dy, dgate
+    in h's dtype, dpre_w, dpost_w, dscale float32), None for what was not given. dh may be dh_out."""
+    return _bind().block_norm_backward(h, y, pre_w, post_w, gate, scale, dn, dh_out, eps, dh, ws, _raw(stream))
 
 
 def gdr_sync_status(stream=None) -> None:

@@ -479,6 +479,67 @@ gdr_status gdr_cache_compact(void* k_cache, void* v_cache, const int32_t* table,
                              const int32_t* path, const int32_t* n_path, int32_t* new_ctx, int B, int W, int M,
                              int layers, int P, int page, long long row_bytes, gdr_stream_t stream);
 
+/*
+ * Tokens drawn from logits, and the probabilities that the filters leave (what gdr_verify_draft takes as p and
+ * q). Per row, with w_i = e^((l_i - max l) / temperature) and tokens in the order of falling logits (equal ones
+ * by rising index):
+ *   top_k   keeps the first top_k of them (0: all);
+ *   top_p   of these the tokens with less than top_p times their mass before them, at least the first (1: all);
+ *   min_p   of these the tokens with w_i >= min_p (0: all).
+ * The token is the smallest index whose running sum (in index order) of the kept w passes u times their total;
+ * probabilities are w_i / total, 0 for tokens that are not kept. temperature 0 keeps the largest logit alone
+ * (the first by index).
+ *   logits [R, V] dt      row r starts at r * stride elements (any alignment of an element)
+ *   temperature [R] float32, >= 0;  top_k [R] int32, >= 0;  top_p, min_p [R] float32 in [0, 1]; the last three NULL
+ *                         for no such filter
+ *   u [R] float32         uniform numbers in [0, 1) (larger ones count as 1: the last kept token); with token
+ *   token [R] int32, probs [R, V] float32   either may be NULL, not both
+ * A logit that is -inf or nan is never kept; logits of +inf share all the weight. A row without any other logit
+ * gets token -1 and probabilities 0. A row whose temperature, top_k, top_p or min_p is out of range keeps its
+ * outputs untouched and records GDR_ERR_DEVICE_INDEX. Weights are formed to about 2^-38 of their size and summed in
+ * units of 2^-40 of the largest (a weight below half a unit is not drawn). V <= 2^18, less 8 where rows do not
+ * begin on 16 bytes; R <= 2^24.
+ */
+gdr_status gdr_sample(const void* logits, long long stride, const float* temperature, const float* u,
+                      const int32_t* top_k, const float* top_p, const float* min_p, int32_t* token, float* probs,
+                      int R, int V, gdr_dtype dt, gdr_stream_t stream);
+
+/*
+ * What stands between two blocks of a layer, in one pass over each token's C channels: the norm after the one
+ * block, its gate and residual scale, the sum into the residual, and the norm before the other:
+ *   z = post_w y / sqrt(mean(y^2) + eps),   x = h + scale sigmoid(gate) z,
+ *   h_out = x,   n_out = pre_w x / sqrt(mean(x^2) + eps)
+ *   h [rows, C] dt            the residual;  y, gate [rows, C] dt  the block's output and its gate, rows y_row and
+ *                             gate_row elements apart (multiples of 16 bytes; slices of one projection)
+ *   post_w, gate, scale       NULL: z = y, no gate (1), no scale (1)
+ *   post_w, scale, pre_w [C] float32;  eps >= 0
+ *   h_out, n_out [rows, C] dt   h_out may be h itself; otherwise outputs overlap nothing
+ * C is a multiple of 8, at most 16384. Arithmetic is float32 with one rounding of each output (the second norm
+ * is of the unrounded sum).
+ */
+gdr_status gdr_block_norm(const void* h, const void* y, const void* gate, const float* post_w, const float* scale,
+                          const float* pre_w, float eps, void* h_out, void* n_out, long long rows, int C,
+                          long long y_row, long long gate_row, gdr_dtype dt, gdr_stream_t stream);
+
+/*
+ * Gradient of gdr_block_norm, from dh_out [rows, C] float32 (NULL: zeros), the gradient of the residual that the
+ * layers behind it left, and dn [rows, C] dt: with s = 1 / sqrt(mean(x^2) + eps), r = 1 / sqrt(mean(y^2) + eps), g = sigmoid(gate),
+ *   dx = dh_out + s (pre_w dn - x s^2 mean(pre_w dn x)),   dh = dx,   dz = dx scale g,
+ *   dy = r (post_w dz - y r^2 mean(post_w dz y)) (dz without post_w),   dgate = dx scale z g (1 - g),
+ *   dpre_w = sum dn x s,   dpost_w = sum dz y r,   dscale = sum dx g z   (over the rows)
+ *   dh [rows, C] float32 (the residual's gradient is summed over the layers);  dy, dgate [rows, C] dt
+ *   dpre_w, dpost_w, dscale [C] float32;  dgate, dpost_w, dscale non-NULL exactly where gate, post_w, scale are
+ *   ws at least gdr_block_norm_backward_workspace_bytes(C) bytes (0 for a C that is not implemented)
+ * The inputs are the forward's (h as it was before). dh may be dh_out itself; otherwise outputs and ws overlap nothing.
+ * The sums run in a fixed order: the same bits every time.
+ */
+size_t gdr_block_norm_backward_workspace_bytes(int C);
+gdr_status gdr_block_norm_backward(const void* h, const void* y, const void* gate, const float* post_w,
+                                   const float* scale, const float* pre_w, const float* dh_out, const void* dn,
+                                   float eps, float* dh, void* dy, void* dgate, float* dpre_w, float* dpost_w,
+                                   float* dscale, long long rows, int C, long long y_row, long long gate_row,
+                                   gdr_dtype dt, void* ws, size_t ws_bytes, gdr_stream_t stream);
+
 /* Synchronise `stream`, then read and clear the sticky device error word of the current device. */
 gdr_status gdr_sync_status(gdr_stream_t stream);
 
