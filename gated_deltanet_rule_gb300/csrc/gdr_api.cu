@@ -695,6 +695,8 @@ const char* gdr_kernel_name(int id) {
     case kKernBlockNorm: return "gdr_block_norm";
     case kKernBlockNormBwd: return "gdr_block_norm_backward";
     case kKernSample: return "gdr_sample";
+    case kKernForkAttnShared: return "gdr_fork_attn_shared";
+    case kKernForkAttnOwn: return "gdr_fork_attn_own";
   }
   return nullptr;
 }

@@ -260,23 +260,59 @@ PyObject* norm_rope_backward(const Call& c) {
   return wrap({dq, dk, dq_w, dk_w});
 }
 
+// Queries of drafted nodes, the pages, who sees what, and the outputs of the two attention calls.
+// Arguments 0 .. 4: q, k_pages, v_pages, table, ctx; from i: lengths, mask, scale, o, lse, want_lse.
+struct Attn {
+  const Tensor* q;
+  const Pages p;
+  int B, N, Hq, D;
+  const Tensor *lengths, *mask;
+  float scale;
+  Tensor o, lse;
+  bool with_lse;
+  static const Tensor* queries(const Call& c) {
+    const Tensor* q = c.of(0, "q", at::kBFloat16);
+    if (q->dim() != 4) refuse("q must be [B, N, Hq, D]");
+    return q;
+  }
+  Attn(const Call& c, int i) : q(queries(c)), p(c, 1, *q) {
+    B = size(*q, 0, "q's size");
+    N = size(*q, 1, "q's size");
+    Hq = size(*q, 2, "q's size");
+    D = size(*q, 3, "q's size");
+    lengths = c.ints(i, "lengths", {B}, true);
+    mask = c.of(i + 1, "mask", at::kLong, {B, N, ((int64_t)N + 63) / 64}, true);
+    scale = (float)(c.args[i + 2] == Py_None ? 1.0 / std::sqrt((double)D) : c.number(i + 2));
+    o = c.output(i + 3, "o", q->sizes(), at::kBFloat16, *q);
+    with_lse = c.args[i + 4] != Py_None || c.truth(i + 5);
+    if (with_lse) lse = c.output(i + 4, "lse", {B, N, Hq}, at::kFloat, *q);
+  }
+  float* lse_at() const { return with_lse ? static_cast<float*>(lse.data_ptr()) : nullptr; }
+  PyObject* result() const { return with_lse ? wrap({o, lse}) : THPVariable_Wrap(o); }
+};
+
 // q, k_pages, v_pages, table, ctx, lengths, mask, scale, o, lse, want_lse, ws, stream
 PyObject* tree_attn(const Call& c) {
-  const Tensor* q = c.of(0, "q", at::kBFloat16);
-  if (q->dim() != 4) refuse("q must be [B, N, Hq, D]");
-  const int B = size(*q, 0, "q's size"), N = size(*q, 1, "q's size"), Hq = size(*q, 2, "q's size"), D = size(*q, 3, "q's size");
-  const Pages p(c, 1, *q);
-  const Tensor* lengths = c.ints(5, "lengths", {B}, true);
-  const Tensor* mask = c.of(6, "mask", at::kLong, {B, N, ((int64_t)N + 63) / 64}, true);
-  const double scale = c.args[7] == Py_None ? 1.0 / std::sqrt((double)D) : c.number(7);
-  Tensor o = c.output(8, "o", q->sizes(), at::kBFloat16, *q), lse;
-  const bool with_lse = c.args[9] != Py_None || c.truth(10);
-  if (with_lse) lse = c.output(9, "lse", {B, N, Hq}, at::kFloat, *q);
-  Tensor ws = c.workspace(11, gdr_tree_attn_workspace_bytes(D), *q);
-  check(gdr_tree_attn(ptr(q), ptr(p.k), ptr(p.v), ptr<int32_t>(p.table), ptr<int32_t>(p.ctx), ptr<int32_t>(lengths),
-                      ptr<uint64_t>(mask), (float)scale, o.data_ptr(), with_lse ? ptr<float>(&lse) : nullptr, B, N, Hq,
-                      p.Hk, D, p.P, p.page, p.M, GDR_BF16, ws.data_ptr(), bytes_of(ws), c.stream()));
-  return with_lse ? wrap({o, lse}) : THPVariable_Wrap(o);
+  const Attn a(c, 5);
+  Tensor ws = c.workspace(11, gdr_tree_attn_workspace_bytes(a.D), *a.q);
+  check(gdr_tree_attn(ptr(a.q), ptr(a.p.k), ptr(a.p.v), ptr<int32_t>(a.p.table), ptr<int32_t>(a.p.ctx), ptr<int32_t>(a.lengths),
+                      ptr<uint64_t>(a.mask), a.scale, a.o.data_ptr(), a.lse_at(), a.B, a.N, a.Hq, a.p.Hk, a.D, a.p.P, a.p.page,
+                      a.p.M, GDR_BF16, ws.data_ptr(), bytes_of(ws), c.stream()));
+  return a.result();
+}
+
+// q, k_pages, v_pages, table, ctx, first, shared, lengths, mask, scale, o, lse, want_lse, ws, stream
+PyObject* fork_attn(const Call& c) {
+  const Attn a(c, 7);
+  const Tensor* shared = c.ints(6, "shared");
+  if (shared->dim() != 1) refuse("shared must be [T]");
+  const Tensor* first = c.ints(5, "first", {shared->size(0) + 1});
+  const int T = size(*shared, 0, "shared's size");
+  Tensor ws = c.workspace(13, gdr_fork_attn_workspace_bytes(a.B, a.N, a.Hq, a.D), *a.q);
+  check(gdr_fork_attn(ptr(a.q), ptr(a.p.k), ptr(a.p.v), ptr<int32_t>(a.p.table), ptr<int32_t>(a.p.ctx), ptr<int32_t>(a.lengths),
+                      ptr<uint64_t>(a.mask), ptr<int32_t>(first), ptr<int32_t>(shared), a.scale, a.o.data_ptr(), a.lse_at(),
+                      a.B, a.N, a.Hq, a.p.Hk, a.D, a.p.P, a.p.page, a.p.M, T, GDR_BF16, ws.data_ptr(), bytes_of(ws), c.stream()));
+  return a.result();
 }
 
 // tokens, parents, lengths, p, q, u, u_next, path, n_path, next_token, stream
@@ -487,7 +523,7 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
 PyMethodDef methods[] = {GDR_ENTRY(norm_rope, 11),   GDR_ENTRY(norm_rope_append, 16), GDR_ENTRY(norm_rope_backward, 12),
                          GDR_ENTRY(tree_attn, 13),   GDR_ENTRY(verify, 11),           GDR_ENTRY(cache_reserve, 8),
                          GDR_ENTRY(cache_fork, 9),   GDR_ENTRY(cache_free, 5),        GDR_ENTRY(cache_compact, 8),
-                         GDR_ENTRY(sample, 10),      GDR_ENTRY(block_norm, 10),       GDR_ENTRY(block_norm_backward, 12),
+                         GDR_ENTRY(fork_attn, 15),   GDR_ENTRY(sample, 10),      GDR_ENTRY(block_norm, 10),       GDR_ENTRY(block_norm_backward, 12),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gdr_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

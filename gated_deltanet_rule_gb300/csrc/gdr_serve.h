@@ -24,6 +24,8 @@ constexpr int kKernCacheCopy = 15;
 constexpr int kKernBlockNorm = 16;
 constexpr int kKernBlockNormBwd = 17;
 constexpr int kKernSample = 18;
+constexpr int kKernForkAttnShared = 19;
+constexpr int kKernForkAttnOwn = 20;
 
 constexpr int kNumSMs = 152;   // GB300
 constexpr int kErrNoPages = 6;   // device error code (gdr_status): a cache had too few free pages
@@ -87,6 +89,16 @@ struct TreeAttnArgs {
 };
 size_t tree_attn_workspace_bytes(int D);
 cudaError_t launch_tree_attn(const TreeAttnArgs& a, cudaStream_t s);
+
+// Attention of forked rows over the positions that groups of them share and over their own.
+struct ForkAttnArgs {
+  TreeAttnArgs t;            // (t.ws: parts, then dense results)
+  const int32_t* first;      // [T + 1]
+  const int32_t* shared;     // [T]
+  int T;
+};
+size_t fork_attn_workspace_bytes(int B, int N, int Hq, int D);
+cudaError_t launch_fork_attn(const ForkAttnArgs& a, cudaStream_t s);
 
 // Verification of drafted tokens: one cluster of blocks per row walks the row's tree.
 struct VerifyArgs {

@@ -141,6 +141,33 @@ gdr_status check_ws(const void* ws, size_t given, size_t need, const char* who) 
   return GDR_OK;
 }
 
+// What the two attention calls share.
+gdr_status check_attn(const TreeAttnArgs& a, gdr_dtype dt, const char* who) {
+  if (!a.q || !a.k_pages || !a.v_pages || !a.table || !a.ctx || !a.o)
+    return fail(GDR_ERR_INVALID_ARG, "%s: q, k_pages, v_pages, table, ctx and o must be non-NULL", who);
+  gdr_status st = check_heads(a.B, a.N, a.Hq, a.Hk, a.D, dt, who);
+  if (st == GDR_OK && dt != GDR_BF16) st = fail(GDR_ERR_UNSUPPORTED, "%s: bfloat16 only (dt=%d)", who, (int)dt);
+  if (st == GDR_OK) st = check_pages(a.P, a.page, a.M, who);
+  if (st != GDR_OK) return st;
+  if (a.Hq / a.Hk > 128) return fail(GDR_ERR_UNSUPPORTED, "%s: Hq/Hk=%d exceeds 128 heads a group", who, a.Hq / a.Hk);
+  if (a.B > 65535 || (long long)a.N * a.Hq > 1 << 28 || (long long)a.B * a.N * a.Hk > 0x7fffffffll) return fail(GDR_ERR_UNSUPPORTED, "%s: B=%d or N*Hq too large", who, a.B);
+  if (!(a.scale > 0.f) || a.scale > 1e30f) return fail(GDR_ERR_INVALID_ARG, "%s: scale must be positive and finite", who);
+  for (const void* p : {a.q, a.k_pages, a.v_pages, (const void*)a.o})
+    if (!aligned(p, 16)) return fail(GDR_ERR_INVALID_ARG, "%s: q, k_pages, v_pages and o must be 16-byte aligned", who);
+  for (const void* p : {(const void*)a.table, (const void*)a.ctx, (const void*)a.lengths, (const void*)a.lse})
+    if (!aligned(p, 4)) return fail(GDR_ERR_INVALID_ARG, "%s: table, ctx, lengths and lse must be 4-byte aligned", who);
+  if (!aligned(a.mask, 8)) return fail(GDR_ERR_INVALID_ARG, "%s: mask must be 8-byte aligned", who);
+  return GDR_OK;
+}
+gdr_status apart_attn(const TreeAttnArgs& a, size_t need, const int32_t* first, const int32_t* shared, int T, const char* who) {
+  const unsigned long long rows = (unsigned long long)a.B * a.N * a.Hq, pages = (unsigned long long)a.P * a.page * a.Hk * a.D * 2;
+  return apart({{a.o, rows * a.D * 2, "o"}, {a.lse, rows * 4, "lse"}, {a.ws, need, "ws"}},
+               {{a.q, rows * a.D * 2, "q"}, {a.k_pages, pages, "k_pages"}, {a.v_pages, pages, "v_pages"},
+                {a.table, (unsigned long long)a.B * a.M * 4, "table"}, {a.ctx, a.B * 4ull, "ctx"}, {a.lengths, a.B * 4ull, "lengths"},
+                {a.mask, (unsigned long long)a.B * a.N * ((a.N + 63) / 64) * 8, "mask"}, {first, T * 4ull + 4, "first"},
+                {shared, T * 4ull, "shared"}}, who);
+}
+
 gdr_status check_block_norm(const BlockNormArgs& a, gdr_dtype dt, const char* who) {
   if (!a.h || !a.y || !a.pre_w) return fail(GDR_ERR_INVALID_ARG, "%s: h, y and pre_w must be non-NULL", who);
   if (a.rows < 1 || a.C < 1) return fail(GDR_ERR_INVALID_ARG, "%s: sizes must be >= 1 (rows=%lld C=%d)", who, a.rows, a.C);
@@ -274,34 +301,45 @@ gdr_status gdr_tree_attn(const void* q, const void* k_pages, const void* v_pages
                          float* lse, int B, int N, int Hq, int Hk, int D, int P, int page, int M, gdr_dtype dt,
                          void* ws, size_t ws_bytes, gdr_stream_t stream) {
   const char* who = "gdr_tree_attn";
-  if (!q || !k_pages || !v_pages || !table || !ctx || !o)
-    return fail(GDR_ERR_INVALID_ARG, "%s: q, k_pages, v_pages, table, ctx and o must be non-NULL", who);
-  gdr_status st = check_heads(B, N, Hq, Hk, D, dt, who);
-  if (st == GDR_OK && dt != GDR_BF16) st = fail(GDR_ERR_UNSUPPORTED, "%s: bfloat16 only (dt=%d)", who, (int)dt);
-  if (st == GDR_OK) st = check_pages(P, page, M, who);
+  TreeAttnArgs a{q, k_pages, v_pages, table, ctx, lengths, mask, scale, o, lse, B, N, Hq, Hk, D, P, page, M,
+                 static_cast<uint8_t*>(ws), nullptr};
+  gdr_status st = check_attn(a, dt, who);
   if (st != GDR_OK) return st;
-  if (Hq / Hk > 128) return fail(GDR_ERR_UNSUPPORTED, "%s: Hq/Hk=%d exceeds 128 heads a group", who, Hq / Hk);
-  if (B > 65535 || (long long)N * Hq > 1 << 28 || (long long)B * N * Hk > 0x7fffffffll) return fail(GDR_ERR_UNSUPPORTED, "%s: B=%d or N*Hq too large", who, B);
-  if (!(scale > 0.f) || scale > 1e30f) return fail(GDR_ERR_INVALID_ARG, "%s: scale must be positive and finite", who);
-  for (const void* p : {q, k_pages, v_pages, (const void*)o})
-    if (!aligned(p, 16)) return fail(GDR_ERR_INVALID_ARG, "%s: q, k_pages, v_pages and o must be 16-byte aligned", who);
-  for (const void* p : {(const void*)table, (const void*)ctx, (const void*)lengths, (const void*)lse})
-    if (!aligned(p, 4)) return fail(GDR_ERR_INVALID_ARG, "%s: table, ctx, lengths and lse must be 4-byte aligned", who);
-  if (!aligned(mask, 8)) return fail(GDR_ERR_INVALID_ARG, "%s: mask must be 8-byte aligned", who);
   const size_t need = tree_attn_workspace_bytes(D);
   st = check_ws(ws, ws_bytes, need, who);
+  if (st == GDR_OK) st = apart_attn(a, need, nullptr, nullptr, 0, who);
   if (st != GDR_OK) return st;
-  const unsigned long long rows = (unsigned long long)B * N * Hq, pages = (unsigned long long)P * page * Hk * D * 2;
-  st = apart({{o, rows * D * 2, "o"}, {lse, rows * 4, "lse"}, {ws, need, "ws"}},
-             {{q, rows * D * 2, "q"}, {k_pages, pages, "k_pages"}, {v_pages, pages, "v_pages"},
-              {table, (unsigned long long)B * M * 4, "table"}, {ctx, B * 4ull, "ctx"}, {lengths, B * 4ull, "lengths"},
-              {mask, (unsigned long long)B * N * ((N + 63) / 64) * 8, "mask"}}, who);
-  if (st != GDR_OK) return st;
-  int* err = device_error_word();
-  if (!err) return no_device(who);
-  const TreeAttnArgs a{q, k_pages, v_pages, table, ctx, lengths, mask, scale, o, lse, B, N, Hq, Hk, D, P, page, M,
-                       static_cast<uint8_t*>(ws), err};
+  a.err = device_error_word();
+  if (!a.err) return no_device(who);
   return launched(launch_tree_attn(a, reinterpret_cast<cudaStream_t>(stream)), who);
+}
+
+size_t gdr_fork_attn_workspace_bytes(int B, int N, int Hq, int D) {
+  if ((D != 64 && D != 128 && D != 256) || B < 1 || N < 1 || Hq < 1 || (long long)B * N > 1ll << 24 || Hq > 65535) return 0;
+  return fork_attn_workspace_bytes(B, N, Hq, D);
+}
+
+gdr_status gdr_fork_attn(const void* q, const void* k_pages, const void* v_pages, const int32_t* table,
+                         const int32_t* ctx, const int32_t* lengths, const uint64_t* mask, const int32_t* first,
+                         const int32_t* shared, float scale, void* o, float* lse, int B, int N, int Hq, int Hk, int D,
+                         int P, int page, int M, int T, gdr_dtype dt, void* ws, size_t ws_bytes, gdr_stream_t stream) {
+  const char* who = "gdr_fork_attn";
+  ForkAttnArgs a{{q, k_pages, v_pages, table, ctx, lengths, mask, scale, o, lse, B, N, Hq, Hk, D, P, page, M,
+                  static_cast<uint8_t*>(ws), nullptr}, first, shared, T};
+  gdr_status st = check_attn(a.t, dt, who);
+  if (st != GDR_OK) return st;
+  if (!first || !shared || !aligned(first, 4) || !aligned(shared, 4))
+    return fail(GDR_ERR_INVALID_ARG, "%s: first and shared must be non-NULL and 4-byte aligned", who);
+  if (T < 1) return fail(GDR_ERR_INVALID_ARG, "%s: sizes must be >= 1 (T=%d)", who, T);
+  if (T > 65535 || (long long)N * (Hq / Hk) >= 1 << 22)
+    return fail(GDR_ERR_UNSUPPORTED, "%s: T=%d exceeds 65535, or N*Hq/Hk=%lld 2^22 - 1", who, T, (long long)N * (Hq / Hk));
+  const size_t need = fork_attn_workspace_bytes(B, N, Hq, D);
+  st = check_ws(ws, ws_bytes, need, who);
+  if (st == GDR_OK) st = apart_attn(a.t, need, first, shared, T, who);
+  if (st != GDR_OK) return st;
+  a.t.err = device_error_word();
+  if (!a.t.err) return no_device(who);
+  return launched(launch_fork_attn(a, reinterpret_cast<cudaStream_t>(stream)), who);
 }
 
 gdr_status gdr_verify_draft(const int32_t* tokens, const int32_t* parents, const int32_t* lengths, const void* p,

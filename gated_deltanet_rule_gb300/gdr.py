@@ -34,6 +34,7 @@ EXPORTS = ["gdr_chunk_workspace_bytes", "gdr_chunk_fwd", "gdr_chunk_fwd_varlen",
            "gdr_chunk_fwd_save", "gdr_backward_chunked_saved",
            "gdr_qk_norm_rope", "gdr_qk_norm_rope_append", "gdr_qk_norm_rope_backward_workspace_bytes",
            "gdr_qk_norm_rope_backward", "gdr_tree_attn_workspace_bytes", "gdr_tree_attn", "gdr_verify_draft",
+           "gdr_fork_attn_workspace_bytes", "gdr_fork_attn",
            "gdr_cache_workspace_bytes", "gdr_cache_reserve", "gdr_cache_fork", "gdr_cache_free", "gdr_cache_compact",
            "gdr_sample", "gdr_block_norm", "gdr_block_norm_backward_workspace_bytes", "gdr_block_norm_backward",
            "gdr_sync_status", "gdr_status_string", "gdr_last_error_message",
@@ -111,6 +112,10 @@ def lib() -> ctypes.CDLL:
     L.gdr_tree_attn_workspace_bytes.restype = sz
     L.gdr_tree_attn.argtypes = [vp, vp, vp, vp, vp, vp, vp, f32, vp, fp, i, i, i, i, i, i, i, i, i, vp, sz, vp]
     L.gdr_tree_attn.restype = i
+    L.gdr_fork_attn_workspace_bytes.argtypes = [i, i, i, i]
+    L.gdr_fork_attn_workspace_bytes.restype = sz
+    L.gdr_fork_attn.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, f32, vp, fp, i, i, i, i, i, i, i, i, i, i, vp, sz, vp]
+    L.gdr_fork_attn.restype = i
     L.gdr_verify_draft.argtypes = [vp, vp, vp, vp, vp, fp, fp, vp, vp, vp, i, i, i, i, vp]
     L.gdr_verify_draft.restype = i
     L.gdr_cache_workspace_bytes.argtypes = [i, i]
@@ -559,6 +564,18 @@ def gdr_tree_attn(q, k_pages, v_pages, table, ctx, lengths=None, mask=None, scal
     already holding the nodes' keys and values. scale defaults to D^-1/2. Returns o, or (o, lse [B,N,Hq]
     float32) with want_lse or lse given."""
     return _bind().tree_attn(q, k_pages, v_pages, table, ctx, lengths, mask, scale, o, lse, want_lse, ws, _raw(stream))
+
+
+def fork_attn_workspace_bytes(B: int, N: int, Hq: int, D: int = D) -> int:
+    return int(lib().gdr_fork_attn_workspace_bytes(B, N, Hq, D))
+
+
+def gdr_fork_attn(q, k_pages, v_pages, table, ctx, first, shared, lengths=None, mask=None, scale: float | None = None,
+                  o=None, lse=None, want_lse: bool = False, ws=None, stream=None):
+    """gdr_tree_attn for forked rows: rows first[t] .. first[t+1]-1 (first [T+1] int32) share their first shared[t]
+    positions (whole pages; read through the first of them, once for all), and go on over their own."""
+    return _bind().fork_attn(q, k_pages, v_pages, table, ctx, first, shared, lengths, mask, scale, o, lse, want_lse, ws,
+                             _raw(stream))
 
 
 def gdr_verify_draft(tokens, parents, lengths, p, q, u, u_next, path=None, n_path=None, next_token=None, stream=None):

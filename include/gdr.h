@@ -418,6 +418,25 @@ gdr_status gdr_tree_attn(const void* q, const void* k_pages, const void* v_pages
                          void* ws, size_t ws_bytes, gdr_stream_t stream);
 
 /*
+ * gdr_tree_attn for rows whose leading positions are the same, as forks of a trunk have them (gdr_cache_fork shares a
+ * source's full pages): keys and values of the shared positions are read once for all rows of a group.
+ *   first [T + 1] int32, rising in [0, B]: group t is the rows first[t] .. first[t + 1] - 1 (neighbours; a
+ *        group may be empty, rows outside all groups share nothing)
+ *   shared [T] int32: positions that the rows of group t share, a multiple of page, at most each row's ctx. They
+ *        are read through the table of the group's first row; that of the others is not looked at there.
+ * Everything else as for gdr_tree_attn, results too, but for roundings: shared and own positions are attended apart,
+ * in float32, and joined by their lse.
+ *   ws at least gdr_fork_attn_workspace_bytes(B, N, Hq, D) bytes (0 for sizes that are not implemented)
+ * If first falls anywhere, no row is attended (o = 0, lse = -inf); a group whose numbers are out of range, or a row with
+ * ctx below shared, counts as having no nodes. Both record GDR_ERR_DEVICE_INDEX. The same call gives the same bits.
+ */
+size_t gdr_fork_attn_workspace_bytes(int B, int N, int Hq, int D);
+gdr_status gdr_fork_attn(const void* q, const void* k_pages, const void* v_pages, const int32_t* table,
+                         const int32_t* ctx, const int32_t* lengths, const uint64_t* mask, const int32_t* first,
+                         const int32_t* shared, float scale, void* o, float* lse, int B, int N, int Hq, int Hk, int D,
+                         int P, int page, int M, int T, gdr_dtype dt, void* ws, size_t ws_bytes, gdr_stream_t stream);
+
+/*
  * Verification of drafted tokens against the target's probabilities (speculative sampling over a
  * tree; a chain is the tree of one child each). Per row, from the root on: at node `cur` the
  * candidates are its children in index order. With (c, Z) = (0, 1) and rho = max(p[cur] - c q[cur], 0),

@@ -1,0 +1,253 @@
+"""gdr_fork_attn against float64 over the seen positions alone, row by row.
+
+Tolerances as for gdr_tree_attn: a softmax weight is rounded to bf16 (2^-8 relative), its score is off by at most
+(D + 8) 2^-22 of E = max_j scale sum |q k| and the exponential by 2^-21; the same score error sits in the sum. The
+two parts' weights add less than 2^-20 of A = sum p |v|. So o is off by at most (2^-8 + 2 e) A + 2^-8 |o| with
+e = (D + 8) 2^-22 E + 2^-19, and lse by e + 2^-22 (1 + |lse| + E)."""
+import math
+
+import pytest
+import torch
+
+from gated_deltanet_rule_gb300 import gdr
+from tests import serve_ref as ref
+
+pytestmark = pytest.mark.gpu
+I32 = torch.int32
+
+
+def _pack(see):
+    B, N, _ = see.shape
+    W = (N + 63) // 64
+    full = torch.zeros(B, N, W * 64, dtype=torch.int64)
+    full[..., :N] = see.long()
+    return (full.view(B, N, W, 64) << torch.arange(64)).sum(-1)
+
+
+def _see(kind, B, N, g):
+    i = torch.arange(N)
+    if kind == "chain":
+        return (i[None, :] <= i[:, None]).expand(B, N, N).clone()
+    see = torch.rand(B, N, N, generator=g) < 0.4   # any mask at all, nodes that see no node among them
+    see[:, ::3] = False
+    return see
+
+
+def _case(first, shared, own, N, Hq, Hk, D, page, kind="chain", seed=0, lengths=None, qs=1.5):
+    """first, shared: the groups; own: own positions of the rows, by turns."""
+    g = torch.Generator().manual_seed(seed)
+    B = max(first[-1], 1)
+    group = [next((t for t in range(len(shared)) if first[t] <= b < first[t + 1]), -1) for b in range(B)]
+    sh = [shared[t] if t >= 0 else 0 for t in group]
+    own = [own[b % len(own)] for b in range(B)]
+    ctx = torch.tensor([s + o for s, o in zip(sh, own)], dtype=I32)
+    lengths = torch.tensor([N] * B if lengths is None else [lengths[b % len(lengths)] for b in range(B)], dtype=I32)
+    need = [-(-(o + N) // page) for o in own]
+    P, M = sum(shared) // page + sum(need) + 2, max(s // page + n for s, n in zip(sh, need))
+    order = torch.randperm(P, generator=g).int().tolist()
+    trunk = [[order.pop() for _ in range(s // page)] for s in shared]
+    table = torch.full((B, M), -1, dtype=I32)
+    for b in range(B):
+        row = (trunk[group[b]] if group[b] >= 0 else []) + [order.pop() for _ in range(need[b])]
+        table[b, :len(row)] = torch.tensor(row, dtype=I32)
+    q = (qs * torch.randn(B, N, Hq, D, generator=g)).bfloat16()
+    k, v = (torch.randn(P, page, Hk, D, generator=g).bfloat16() for _ in "kv")
+    return dict(q=q, k=k, v=v, table=table, ctx=ctx, lengths=lengths, see=_see(kind, B, N, g), kind=kind, scale=D ** -0.5,
+                first=torch.tensor(first, dtype=I32), shared=torch.tensor(shared, dtype=I32))
+
+
+def _args(c):
+    d = {n: c[n].cuda() for n in ("q", "k", "v", "table", "ctx", "first", "shared", "lengths")}
+    return (*d.values(), _pack(c["see"]).cuda() if c["kind"] != "chain" else None, c["scale"])
+
+
+def _run(c):
+    o, lse = gdr.gdr_fork_attn(*_args(c), want_lse=True)
+    gdr.gdr_sync_status()
+    return o.double().cpu(), lse.double().cpu()
+
+
+def _check(c, o=None, lse=None):
+    if o is None:
+        o, lse = _run(c)
+    D = c["q"].shape[-1]
+    wo, wl, A, E = ref.tree_attn(c["q"], c["k"], c["v"], c["table"], c["ctx"], c["lengths"], c["see"], c["scale"])
+    e = (D + 8) * 2.0 ** -22 * E + 2.0 ** -19
+    empty = wl == -math.inf
+    assert torch.equal(lse == -math.inf, empty) and (o[empty] == 0).all()
+    off = (o - wo).abs() - ((2.0 ** -8 + 2 * e[..., None]) * A + 2.0 ** -8 * wo.abs())
+    assert torch.isfinite(o).all() and off.max() <= 0, f"o off by {off.max():.3e} over the bound"
+    loff = (lse - wl).abs() - (e + 2.0 ** -22 * (1 + wl.abs() + E))
+    assert loff[~empty].numel() == 0 or loff[~empty].max() <= 0, f"lse off by {loff[~empty].max():.3e} over the bound"
+
+
+CASES = [   # first, shared, own, N, Hq, Hk, D, page
+    ([0, 1], [64], [0], 1, 1, 1, 128, 64), ([0, 3], [128], [0, 1, 63], 1, 4, 2, 128, 64), ([0, 2, 5], [16, 304], [5, 0, 130], 1, 8, 1, 64, 16),
+    ([0, 4], [96], [33, 7], 2, 6, 2, 128, 32), ([0, 1, 1, 3], [128, 256, 0], [10], 3, 16, 2, 256, 128), ([0, 7, 9], [512, 64], [64, 3], 1, 5, 5, 64, 64),
+    ([2, 6], [256], [100, 17], 1, 8, 2, 128, 64), ([0, 3], [1040], [15], 5, 12, 4, 256, 16), ([0, 2, 4], [64, 192], [70, 1], 17, 8, 4, 128, 32),
+    ([0, 2], [128], [20], 64, 8, 2, 128, 64), ([0, 3], [320], [9, 40], 65, 4, 1, 64, 32), ([0, 2], [64], [130], 30, 6, 1, 256, 64),
+    ([0, 2], [384], [3], 2, 128, 1, 128, 128), ([0, 40], [192], [2, 30], 1, 16, 1, 128, 64),
+]
+
+
+@pytest.mark.parametrize("kind", ["chain", "random"])
+@pytest.mark.parametrize("case", CASES)
+def test_against_float64(case, kind):
+    _check(_case(*case, kind, seed=case[0][-1] + case[6]))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["chain", "random"])
+def test_ragged_lengths(kind, D):
+    """Rows of no nodes, one, some, all; padded nodes give 0 and -inf."""
+    _check(_case([0, 2, 6], [96, 320], [100, 0, 300, 5, 700, 64], 20, 4, 2, D, 16, kind, seed=D, lengths=[0, 1, 20, 7, 13, 19]))
+
+
+def test_more_groups_than_blocks_and_rows_than_threads():
+    first = [b * 3 for b in range(201)]
+    _check(_case(first, [16 * (t % 5) for t in range(200)], [0, 40, 3, 129, 17], 2, 4, 2, 64, 16, seed=3, lengths=[2, 1, 0, 2]))
+
+
+@pytest.mark.parametrize("D,page,B,N", [(64, 16, 3, 1), (128, 64, 2, 3), (256, 128, 2, 2), (128, 32, 40, 8)])
+def test_long_trunk_is_split_over_blocks(D, page, B, N):
+    _check(_case([0, B], [20096], [77, 1], N, 4, 2 if B < 10 else 1, D, page, seed=5))
+
+
+def test_long_own_part():
+    _check(_case([0, 2], [64], [9001, 40], 2, 4, 2, 128, 16, seed=6))
+
+
+def test_same_as_tree_attention():
+    """With nothing shared, and beside gdr_tree_attn on the same rows."""
+    c = _case([0, 0], [0], [1], 3, 8, 2, 128, 64, seed=8)
+    c2 = _case([0, 5], [640], [33, 200], 3, 8, 2, 128, 64, seed=9)
+    for x in (c, c2):
+        a = _args(x)
+        o1, l1 = gdr.gdr_fork_attn(*a, want_lse=True)
+        o2, l2 = gdr.gdr_tree_attn(a[0], a[1], a[2], a[3], a[4], a[7], a[8], x["scale"], want_lse=True)
+        gdr.gdr_sync_status()
+        # two roundings of each weight (2^-8 of |v| < 6) and of each result
+        assert (o1.double() - o2.double()).abs().max() <= 2 * 2.0 ** -8 * 6 and (l1 - l2).abs().max() < 1e-4
+
+
+def test_rising_and_far_scores():
+    """The shared part's scores far above or below the own ones: the smaller weight vanishes."""
+    for D in (64, 128, 256):
+        for sign in (1.0, -1.0):
+            c = _case([0, 2], [256], [120], 2, 4, 1, D, 32, seed=10)
+            c["q"] = torch.ones_like(c["q"])
+            c["k"][:] = 0.0
+            at = c["table"][:, :8].long().unique()
+            c["k"][at] = sign * 16 * 128.0 / D
+            c["k"][at, 5] = sign * 17 * 128.0 / D
+            _check(c)
+
+
+def test_unseen_places_do_not_matter():
+    """inf and nan behind the rows' ends, in other rows' pages and at unseen nodes."""
+    for D in (64, 128, 256):
+        c = _case([0, 3], [96], [40, 0, 13], 9, 6, 2, D, 32, "random", seed=11, lengths=[9, 5, 0])
+        clean_o, clean_l = _run(c)
+        k, v = c["k"].clone(), c["v"].clone()
+        used = torch.zeros(k.shape[:2], dtype=torch.bool)
+        for b in range(3):
+            for pos in range(int(c["ctx"][b]) + int(c["lengths"][b])):
+                used[c["table"][b, pos // 32].long(), pos % 32] = True
+        k[~used], v[~used] = float("nan"), float("inf")
+        # a node that nobody sees
+        c["see"][:, :, 4] = False
+        clean = _run(c)
+        for b in (0,):
+            pos = int(c["ctx"][b]) + 4
+            k[c["table"][b, pos // 32].long(), pos % 32] = float("inf")
+            v[c["table"][b, pos // 32].long(), pos % 32] = float("nan")
+        c["k"], c["v"] = k, v
+        o, l = _run(c)
+        assert torch.equal(o, clean[0]) and torch.equal(l, clean[1])
+        del clean_o, clean_l
+
+
+def test_seen_infinities_reach_the_output():
+    c = _case([0, 2], [64], [20], 3, 4, 2, 128, 32, seed=12)
+    pos = int(c["ctx"][0]) + 1                      # node 1 of row 0: nodes 1 and 2 see it
+    c["v"][c["table"][0, pos // 32].long(), pos % 32, 0, 7] = float("inf")
+    c["v"][c["table"][1, 0].long(), 3, 1, 9] = float("-inf")   # a shared position: everyone sees it
+    o, _ = _run(c)
+    assert torch.isinf(o[0, 1:, :2, 7]).all() and torch.isfinite(o[0, 0, :, 7]).all() and torch.isfinite(o[1, :, :, 7]).all()
+    assert torch.isinf(o[:, :, 2:, 9]).all() and torch.isfinite(o[:, :, :2, 9]).all()
+
+
+def _refused(c, rows, **change):
+    want = _run(c)
+    for k, v in change.items():
+        c[k] = v
+    o, lse = gdr.gdr_fork_attn(*_args(c), want_lse=True)
+    with pytest.raises(gdr.GdrError) as e:
+        gdr.gdr_sync_status()
+    assert e.value.status == gdr.GDR_ERR_DEVICE_INDEX
+    o, lse = o.double().cpu(), lse.double().cpu()
+    for b in range(c["q"].shape[0]):
+        if b in rows:
+            assert (o[b] == 0).all() and (lse[b] == -math.inf).all(), b
+        else:
+            assert torch.equal(o[b], want[0][b]) and torch.equal(lse[b], want[1][b]), b
+
+
+def test_refusals_on_the_device():
+    make = lambda: _case([0, 2, 4], [64, 128], [20, 33], 2, 4, 2, 128, 32, seed=13)   # noqa: E731
+    t = lambda *x: torch.tensor(x, dtype=I32)   # noqa: E731
+    _refused(make(), [0, 1, 2, 3], first=t(0, 3, 2))
+    _refused(make(), [0, 1], shared=t(48, 128))
+    _refused(make(), [0, 1], shared=t(-32, 128))
+    _refused(make(), [2, 3], shared=t(64, 1 << 20))
+    _refused(make(), [2, 3], shared=t(64, 192))        # beyond the rows' contexts
+    _refused(make(), [1], lengths=t(2, 3, 2, 2))
+    _refused(make(), [0], ctx=t(1 << 30, 97, 148, 161))
+    _refused(make(), [2], ctx=t(84, 97, 100, 161))     # below what its group shares
+    c = make()
+    _refused(c, [2, 3], first=t(0, 2, 5))              # a group that leaves the rows
+
+
+def test_pages_out_of_range_are_read_as_zeros():
+    for at, rows in ((1, [0, 1]), (3, [0])):           # a shared page (of the first row's table), an own one
+        c = _case([0, 2, 4], [64, 128], [50, 33], 2, 4, 2, 128, 32, seed=14)
+        want = _run(c)
+        c["table"][0, at] = 10 ** 6
+        o, lse = gdr.gdr_fork_attn(*_args(c), want_lse=True)
+        with pytest.raises(gdr.GdrError):
+            gdr.gdr_sync_status()
+        o = o.double().cpu()
+        assert torch.isfinite(o).all()
+        for b in range(4):
+            assert torch.equal(o[b], want[0][b]) == (b not in rows), b
+
+
+def test_only_the_first_rows_table_counts_for_what_is_shared():
+    c = _case([0, 3], [128], [9], 1, 4, 2, 128, 32, seed=15)
+    want = _run(c)
+    c["table"][1:, :4] = -1
+    assert all(torch.equal(a, b) for a, b in zip(want, _run(c)))
+
+
+def test_same_bits_other_stream_and_replay():
+    c = _case([0, 9, 12], [2048, 512], [50, 333, 4], 3, 8, 2, 128, 64, seed=16)
+    a = _args(c)
+    o, lse = gdr.gdr_fork_attn(*a, want_lse=True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for kw in (dict(), dict(stream=s)):
+        o2, l2 = gdr.gdr_fork_attn(*a, want_lse=True, **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(o, o2) and torch.equal(lse, l2)
+    ws = torch.empty(gdr.fork_attn_workspace_bytes(12, 3, 8, 128), dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o3, l3 = gdr.gdr_fork_attn(*a, want_lse=True, ws=ws)
+    for k in (1.0, 0.5):
+        a[0].mul_(k)
+        g.replay()
+        torch.cuda.synchronize()
+        got = o3.clone(), l3.clone()
+        o4, l4 = gdr.gdr_fork_attn(*a, want_lse=True)
+        gdr.gdr_sync_status()
+        assert torch.equal(got[0], o4) and torch.equal(got[1], l4)
