@@ -38,7 +38,7 @@ using u64 = unsigned long long;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 1024;
-constexpr int kPerOctave = 32;      // steps of a binary order in the first histogram
+constexpr int kPerOctave = 128;     // float32: steps of a binary order in the first histogram
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kTarget = 100 << 10;  // bytes of a block's part of a row: two blocks an SM
 
@@ -142,6 +142,23 @@ __device__ __forceinline__ u64 fixed(const W2& w) {
   return fixed(a, c) + fixed(b, d);
 }
 
+// a f exactly, rounded up or down; 0 <= f.
+__device__ __forceinline__ u64 times(u64 a, float f, bool up) {
+  if (f >= 1.f) return a;
+  const uint32_t b = __float_as_uint(f), e = b >> 23, m = (b & 0x7FFFFFu) | (e ? 0x800000u : 0u);
+  const int shift = 150 - (int)max(1u, e);   // f = m 2^-shift, shift >= 24
+  const u64 lo = a * m, hi = __umul64hi(a, m);
+  u64 r, rest;
+  if (shift < 64) {
+    r = (lo >> shift) | (hi << (64 - shift));
+    rest = lo << (64 - shift);
+  } else {
+    r = shift < 128 ? hi >> (shift - 64) : 0;
+    rest = lo | (shift == 64 ? 0 : shift < 128 ? hi << (128 - shift) : hi);
+  }
+  return r + (up && rest ? 1 : 0);
+}
+
 // Floats in order as integers (no nan, one zero).
 __device__ __forceinline__ uint32_t key_of(float x) {
   const uint32_t b = __float_as_uint(x);
@@ -166,6 +183,17 @@ struct Unit<float> {
     return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
   }
   static __device__ __forceinline__ float one(const float* p) { return *p; }
+  // as the rest takes them, and the largest of them and `top`
+  static __device__ __forceinline__ uint4 clean_max(const uint4& u, float& top) {
+    float x[4];
+    read(u, x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] = clean(x[e]);
+      top = fmaxf(top, x[e]);
+    }
+    return write(x);
+  }
 };
 template <>
 struct Unit<bf16> {
@@ -185,6 +213,24 @@ struct Unit<bf16> {
     return make_uint4(v[0], v[1], v[2], v[3]);
   }
   static __device__ __forceinline__ float one(const bf16* p) { return __bfloat162float(*p); }
+  static __device__ __forceinline__ uint4 clean_max(const uint4& u, float& top) {   // (-0 stays: only keys tell it from 0)
+    float x[8];
+    read(u, x);
+    // an exponent of all ones carries into the sign's place when one is added to it
+    const uint32_t hit = ((((u.x & 0x7F807F80u) + 0x00800080u) | ((u.y & 0x7F807F80u) + 0x00800080u) |
+                           ((u.z & 0x7F807F80u) + 0x00800080u) | ((u.w & 0x7F807F80u) + 0x00800080u)) & 0x80008000u);
+    if (!hit) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, x[e]);
+      return u;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      x[e] = fminf(clean(x[e]), kBf16Max);
+      top = fmaxf(top, x[e]);
+    }
+    return write(x);
+  }
 };
 
 __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
@@ -195,33 +241,74 @@ __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+__device__ __forceinline__ uint4 ld_cluster4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_cluster4(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
 __device__ __forceinline__ void st_cluster64(uint32_t addr, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
+constexpr int kOctaves = 15;                       // bf16: binary orders below the largest magnitude with a bin for each value
+constexpr int kSide = kOctaves * 128;              // bins of one sign
+constexpr int kMaxSteps = 4096;
+template <typename T>
+struct Bins;
+template <>
+struct Bins<float> {
+  static constexpr int n = kMaxSteps;              // steps of 1 / kPerOctave of a binary order of the weight
+};
+template <>
+struct Bins<bf16> {
+  static constexpr int n = 2 * kSide + 2;          // positive values falling, around zero, negative ones, the rest
+};
+
 struct Hist {
   uint32_t n[kBins], lo[kBins], hi[kBins];   // counts, and masses in two words
 };
+constexpr int kList = 2048;                  // candidates of a row: places, shared out evenly to its blocks
+constexpr int kMiddle = 256;
 struct Shared {
   float2 table[64];
-  Hist hist[2];              // by turns: a block may still read its neighbours' last one
+  union {
+    Hist hist[2];                            // by turns: a block may still read its neighbours' last one
+    struct {
+      uint32_t steps[kMaxSteps];             // counts of the first histogram: this block's,
+      uint32_t all[kMaxSteps];               // all blocks'
+    };
+    u64 list[kList];                         // candidates, by block; other blocks write them, while this one may still
+                                             // read `all`: they lie over `steps`, which everyone has read by then
+    u64 weight[Bins<bf16>::n];               // bf16: the weight of each bin's value
+  };
+  float middle[kMiddle];                     // bf16: logits around zero
+  double min_p;                              // T ln(min_p)
   float tops[kMaxCluster];
   u64 sums[2][3][kMaxCluster];   // the blocks' totals, by turns
+  int listed[kMaxCluster];
   u64 warps[kWarps], chunks[kWarps];
   u64 scan_m[kWarps];
+  float scan_f[kWarps];
   uint32_t scan_n[kWarps];
   uint32_t edge[2];
   float reds[kWarps];
-  // a border search's answer
-  int bin;
+  // answers of a search
+  int bin, bin2;
   uint32_t bin_n, above_n;
   u64 bin_m, above_m;
-  int bin2;
+  int mine;
   int cut;
 };
+static_assert(Bins<bf16>::n <= kMaxSteps && kList * sizeof(u64) <= kMaxSteps * sizeof(uint32_t), "bins and lists fit");
 
 template <typename T>
 struct Row {
+  using U = Unit<T>;
+  static constexpr int kSteps = Bins<T>::n;
+  static constexpr bool kValues = sizeof(T) == 2;   // a step is one value (but for the middle and the last)
   const T* tile;     // this block's part of the row
   int first;         // index of its first entry (may be before the row: such entries are -inf)
   int units;         // of 16 bytes
@@ -229,9 +316,28 @@ struct Row {
   Shared* sh;
   Scale s;
   float top, steps;  // maximum, steps of the first histogram a unit of logits
+  int least_code;    // bf16: the smallest magnitude with a bin of its own
+  float low;         // bf16: logits below it have no weight to speak of
   int turn_h, turn_s;
+  bool read_others;  // other blocks may still be reading this one's last histogram
 
-  __device__ __forceinline__ int bin_of(float l) const { return (int)fminf((top - l) * steps, (float)(kBins - 1)); }
+  // The step of a logit: it rises as the logit falls.
+  __device__ __forceinline__ int step_of(float l) const {
+    if constexpr (kValues) {
+      const uint32_t b = __float_as_uint(l) >> 16;
+      const int m = (int)(b & 0x7FFFu) - least_code + 1, v = m > 0 ? m : 0;
+      const int at = kSide + ((b & 0x8000u) ? v : -v);
+      return l < low ? kSteps - 1 : at;
+    } else {
+      return (int)fminf((top - l) * steps, (float)(kSteps - 1));
+    }
+  }
+  // The value of a step that holds one (kValues).
+  __device__ __forceinline__ bool one_value(int step) const { return kValues && step != kSide && step != kSteps - 1; }
+  __device__ __forceinline__ float value_of(int step) const {
+    const uint32_t m = (uint32_t)(abs(kSide - step) - 1 + least_code);
+    return __uint_as_float((m | (step > kSide ? 0x8000u : 0u)) << 16);
+  }
 
   // All blocks' v (n of them), in order of rank: sums before this block, and of all.
   template <int n>
@@ -241,34 +347,155 @@ struct Row {
     ptx::cluster_sync_all();
     for (int i = 0; i < n; ++i) {
       before[i] = total[i] = 0;
-      for (int r = 0; r < ranks; ++r) {
-        const u64 x = sh->sums[turn_s][i][r];
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        const u64 x = r < ranks ? sh->sums[turn_s][i][r] : 0;
         if (r < rank) before[i] += x;
         total[i] += x;
       }
     }
     turn_s ^= 1;
   }
-  // Sum over the block, in every thread (u64: any order).
+  // Sum over the block, in every thread (u64: any order); the warps' stay in sh->warps.
   __device__ __forceinline__ u64 block_sum(u64 v) {
+#pragma unroll
     for (int m = 16; m >= 1; m >>= 1) v += __shfl_xor_sync(kAll, v, m);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) sh->warps[threadIdx.x >> 5] = v;
     __syncthreads();
     v = 0;
+#pragma unroll
     for (int w = 0; w < kWarps; ++w) v += sh->warps[w];
     return v;
+  }
+  // Sums over the threads before this one, of three kinds at once.
+  __device__ __forceinline__ void block_scan(uint32_t n, u64 m, float f, uint32_t& bn, u64& bm, float& bf) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t in = n;
+    u64 im = m;
+    float jf = f;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t un = __shfl_up_sync(kAll, in, d);
+      const u64 um = __shfl_up_sync(kAll, im, d);
+      const float uf = __shfl_up_sync(kAll, jf, d);
+      if (lane >= d) {
+        in += un;
+        im += um;
+        jf += uf;
+      }
+    }
+    if (lane == 31) {
+      sh->scan_n[warp] = in;
+      sh->scan_m[warp] = im;
+      sh->scan_f[warp] = jf;
+    }
+    __syncthreads();
+    bn = in - n;
+    bm = im - m;
+    bf = jf - f;
+    for (int w = 0; w < warp; ++w) {
+      bn += sh->scan_n[w];
+      bm += sh->scan_m[w];
+      bf += sh->scan_f[w];
+    }
+    __syncthreads();
   }
 
   // Calls f(x[n], index of x[0]) for the block's units, a thread's share.
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    constexpr int n = Unit<T>::n;
     for (int i = threadIdx.x; i < units; i += kThreads) {
-      float x[n];
-      Unit<T>::read(reinterpret_cast<const uint4*>(tile)[i], x);
-      f(x, first + i * n);
+      float x[U::n];
+      U::read(reinterpret_cast<const uint4*>(tile)[i], x);
+      f(x, first + i * U::n);
     }
+  }
+  // The mass of the thread's share where on(x) holds.
+  template <typename F>
+  __device__ __forceinline__ u64 mass_where(F on) const {
+    W2 acc = {{0}, {0}};
+    each([&](const float* x, int) {
+      bool some = false;
+#pragma unroll
+      for (int e = 0; e < U::n; ++e) some |= on(x[e]);
+      if (!some) return;
+#pragma unroll
+      for (int e = 0; e < U::n; e += 2) {
+        const W2 w = weights(s, sh->table, x[e], x[e + 1]);
+        const F2 is = pack(on(x[e]) ? 1.f : 0.f, on(x[e + 1]) ? 1.f : 0.f);
+        accumulate(acc, mul(w.hi, is), mul(w.lo, is));
+      }
+    });
+    return fixed(acc);
+  }
+
+  // Counts of the row's logits by step, over all blocks: of this thread's steps, kMine neighbours. Each block adds up a
+  // part of the steps and hands the sums to all (reading every block's counts everywhere took five times as long).
+  // bf16 with `masses`: the mass of the logits around zero, too.
+  static constexpr int kMine = kMaxSteps / kThreads;
+  __device__ __forceinline__ u64 count_steps(bool masses, uint32_t (&n)[kMine]) {
+    for (int i = threadIdx.x; i < kMaxSteps / 4; i += kThreads) reinterpret_cast<uint4*>(sh->steps)[i] = make_uint4(0, 0, 0, 0);
+    if (threadIdx.x == 0) sh->mine = 0;
+    __syncthreads();
+    each([&](const float* x, int) {
+#pragma unroll
+      for (int e = 0; e < U::n; ++e) {
+        if (!(x[e] > -INFINITY)) continue;
+        const int step = step_of(x[e]);
+        atomicAdd(&sh->steps[step], 1u);
+        if (kValues && step == kSide) {
+          const int i = atomicAdd(&sh->mine, 1);
+          if (i < kMiddle) sh->middle[i] = x[e];
+        }
+      }
+    });
+    if (kValues && masses) {
+      __syncthreads();
+      const int count = sh->mine;
+      u64 v = 0;
+      if (count > kMiddle) {
+        const float small = __uint_as_float((uint32_t)least_code << 16);
+        v = mass_where([&](float x) { return fabsf(x) < small; });
+      } else if (threadIdx.x < count) {
+        v = gdr::weight(s, sh->table, sh->middle[threadIdx.x]);
+      }
+      if (count) v = block_sum(v);
+      if (threadIdx.x < ranks) st_cluster64(ptx::dsmem_addr(&sh->sums[turn_s][0][rank], threadIdx.x), v);
+    }
+    ptx::cluster_sync_all();
+    // (1, 2, 4 or 8 blocks: parts of whole 16 bytes)
+    const int part = kMaxSteps / 4 / ranks;
+    for (int i = threadIdx.x; i < part; i += kThreads) {
+      uint4 t = make_uint4(0, 0, 0, 0);
+      const int at = rank * part + i;
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q) {
+        if (q >= ranks) continue;
+        const uint4 x = ld_cluster4(ptx::dsmem_addr(&sh->steps[4 * at], q));
+        t.x += x.x;
+        t.y += x.y;
+        t.z += x.z;
+        t.w += x.w;
+      }
+      for (int q = 0; q < ranks; ++q) st_cluster4(ptx::dsmem_addr(&sh->all[4 * at], q), t);
+    }
+    ptx::cluster_sync_all();
+    u64 mass = 0;
+    if (kValues && masses) {
+      for (int q = 0; q < ranks; ++q) mass += sh->sums[turn_s][0][q];
+      turn_s ^= 1;
+    }
+#pragma unroll
+    for (int i = 0; i < kMine; i += 4) {
+      const uint4 x = reinterpret_cast<const uint4*>(sh->all)[(threadIdx.x * kMine + i) / 4];
+      n[i] = x.x;
+      n[i + 1] = x.y;
+      n[i + 2] = x.z;
+      n[i + 3] = x.w;
+    }
+    __syncthreads();   // (what lies in the same place is written next)
+    return mass;
   }
 
   // Zeroes the histogram of this turn (each block its own), to be filled by `fill`; then finds the first bin at
@@ -285,10 +512,12 @@ struct Row {
     fill(h);
     ptx::cluster_sync_all();
     // two neighbouring bins a thread
-    const int b0 = 2 * threadIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int b0 = 2 * threadIdx.x;
     uint32_t n[2] = {0, 0};
     u64 m[2] = {0, 0};
-    for (int r = 0; r < ranks; ++r) {
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      if (r >= ranks) continue;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         n[i] += ld_cluster(ptx::dsmem_addr(&h.n[b0 + i], r));
@@ -296,27 +525,10 @@ struct Row {
           m[i] += (u64)ld_cluster(ptx::dsmem_addr(&h.lo[b0 + i], r)) + ((u64)ld_cluster(ptx::dsmem_addr(&h.hi[b0 + i], r)) << 32);
       }
     }
-    uint32_t in = n[0] + n[1];
-    u64 im = m[0] + m[1];
-    for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t un = __shfl_up_sync(kAll, in, d);
-      const u64 um = kMass ? __shfl_up_sync(kAll, im, d) : 0;
-      if (lane >= d) {
-        in += un;
-        im += um;
-      }
-    }
-    if (lane == 31) {
-      sh->scan_n[warp] = in;
-      sh->scan_m[warp] = im;
-    }
-    __syncthreads();
-    uint32_t bn = in - n[0] - n[1];
-    u64 bm = im - m[0] - m[1];
-    for (int w = 0; w < warp; ++w) {
-      bn += sh->scan_n[w];
-      bm += sh->scan_m[w];
-    }
+    uint32_t bn;
+    u64 bm;
+    float bf;
+    block_scan(n[0] + n[1], m[0] + m[1], 0.f, bn, bm, bf);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const u64 a = kMass ? bm : bn, b = a + (kMass ? m[i] : n[i]);
@@ -324,7 +536,6 @@ struct Row {
         sh->bin = b0 + i;
         sh->bin_n = n[i];
         sh->above_n = bn;
-        sh->bin_m = m[i];
         sh->above_m = bm;
       }
       bn += n[i];
@@ -332,21 +543,22 @@ struct Row {
     }
     __syncthreads();
     turn_h ^= 1;
+    read_others = true;
     return sh->bin >= 0;
   }
 
-  // Key range of a step of the first histogram: it falls with the key, so its ends are found by bisection.
-  __device__ void step_keys(int bin, uint32_t& lo, uint32_t& hi) {
+  // Key range of a step: it falls with the key, so its ends are found by bisection.
+  __device__ void step_keys(int step, uint32_t& lo, uint32_t& hi) {
     __syncthreads();
     if (threadIdx.x < 2) {
-      const int b = bin - (int)threadIdx.x;   // the smallest key whose step is at most b
+      const int b = step - (int)threadIdx.x;   // the smallest key whose step is at most b
       uint32_t l = key_of(-FLT_MAX), r = key_of(top);
-      if (b < 0) {
+      if (b < 0 || step_of(top) > b) {
         l = r + 1;
       } else {
         while (l < r) {
           const uint32_t mid = l + (r - l) / 2;
-          if (bin_of(of_key(mid)) <= b) r = mid;
+          if (step_of(of_key(mid)) <= b) r = mid;
           else l = mid + 1;
         }
       }
@@ -366,8 +578,8 @@ struct Row {
       const bool got = border<kMass>(need, [&](Hist& h) {
         each([&](const float* x, int) {
 #pragma unroll
-          for (int e = 0; e < Unit<T>::n; ++e) {
-            const uint32_t k = key_of(x[e]);
+          for (int e = 0; e < U::n; ++e) {
+            const uint32_t k = key_of(x[e] + 0.f);
             if (k >= lo && k <= hi) count<kMass>(h, (hi - k) >> shift, x[e]);
           }
         });
@@ -388,17 +600,394 @@ struct Row {
   }
   template <bool kMass>
   __device__ __forceinline__ void count(Hist& h, uint32_t b, float l) const {
-    if (!kMass) {
-      atomicAdd(&h.n[b], 1u);
-      return;
-    }
     atomicAdd(&h.n[b], 1u);
-    const u64 w = weight(s, sh->table, l);
+    if (!kMass) return;
+    const u64 w = gdr::weight(s, sh->table, l);
     const uint32_t old = atomicAdd(&h.lo[b], (uint32_t)w);
     const uint32_t up = (uint32_t)(w >> 32) + (old + (uint32_t)w < old);
     if (up) atomicAdd(&h.hi[b], up);
   }
 };
+
+// What is kept of a row: logits above `value`, and those equal to it up to index `cut`.
+struct Border {
+  float value;
+  uint32_t ties, equal;   // how many of the equal ones are kept, and how many there are
+  int cut;
+  bool known;             // cut is given (ties and equal are not needed)
+};
+
+// The border of top-k (0: none) and top-p (1: none) in a row whose logits are counted by step.
+template <typename T>
+__device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
+  using U = Unit<T>;
+  constexpr int kMine = Row<T>::kMine, kSteps = Row<T>::kSteps;
+  Shared& sh = *r.sh;
+  const int tid = threadIdx.x, s0 = tid * kMine;
+  Border out = {-INFINITY, 0, 0, -1, false};
+  const bool cuts_k = k > 0, cuts_p = p < 1.f;
+  uint32_t n[kMine];
+  const u64 middle = r.count_steps(p < 1.f, n);
+
+  // counts above this thread's steps; masses: of each step's value, or (float32) bounds that the steps' width gives
+  uint32_t sum_n = 0, bn;
+  u64 m[kMine], sum_m = 0, bm;
+  float sum_f = 0.f, bf;
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    sum_n += n[i];
+    m[i] = 0;
+    if (Row<T>::kValues) {
+      if (n[i] && cuts_p && r.one_value(s0 + i)) m[i] = n[i] * weight(r.s, sh.table, r.value_of(s0 + i));
+      sum_m += m[i];
+    } else {
+      sum_f += (float)n[i] * ptx::ex2_approx(-(float)(s0 + i) * (1.f / kPerOctave));
+    }
+  }
+  if (Row<T>::kValues && kSide / kMine == tid) {
+    m[kSide % kMine] = middle;
+    sum_m += middle;
+  }
+  r.block_scan(sum_n, sum_m, sum_f, bn, bm, bf);
+
+  // ------------------------------------------------------------------ the step of the k-th logit
+  uint32_t total_n = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) total_n += sh.scan_n[w];
+  const bool k_on = cuts_k && (uint32_t)k < total_n;
+  int k_step = kSteps;
+  uint32_t k_above = 0, k_equal = 0;
+  u64 k_mass = 0;      // (values) mass above that step
+  if (k_on) {
+    uint32_t at = bn;
+    u64 am = bm;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      if (at < (uint32_t)k && at + n[i] >= (uint32_t)k) {
+        sh.bin = s0 + i;
+        sh.bin_n = n[i];
+        sh.above_n = at;
+        sh.above_m = am;
+      }
+      at += n[i];
+      am += m[i];
+    }
+    __syncthreads();
+    k_step = sh.bin;
+    k_equal = sh.bin_n;
+    k_above = sh.above_n;
+    k_mass = sh.above_m;
+    __syncthreads();
+  }
+
+  if constexpr (Row<T>::kValues) {
+    // a step is a value: the border lies in it, or (rarely) in the middle or the rest
+    if (k_on) {
+      u64 need = (u64)k - k_above;
+      uint32_t n_key = k_equal;
+      out.value = r.value_of(k_step);
+      if (!r.one_value(k_step)) {
+        uint32_t lo, hi, key;
+        r.step_keys(k_step, lo, hi);
+        r.template refine<false>(lo, hi, need, key, n_key);
+        out.value = of_key(key);
+      }
+      out.ties = (uint32_t)need;
+      out.equal = n_key;
+    }
+    if (!cuts_p) return out;
+    u64 all = 0;
+    if (!k_on) {
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) all += sh.scan_m[w];
+    } else if (r.one_value(k_step)) {
+      all = k_mass + out.ties * weight(r.s, sh.table, out.value);
+    } else {
+      const float b = out.value;
+      const u64 v[1] = {r.block_sum(r.mass_where([&](float x) { return x > b; }))};
+      u64 before[1], mass[1];
+      r.cluster_sums(v, before, mass);
+      all = mass[0] + out.ties * weight(r.s, sh.table, b);
+    }
+    u64 need = max((u64)1, times(all, p, true));
+    if (tid == 0) sh.bin = -1;
+    __syncthreads();
+    u64 am = bm;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      if (am < need && am + m[i] >= need) {
+        sh.bin = s0 + i;
+        sh.bin_n = n[i];
+        sh.above_m = am;
+      }
+      am += m[i];
+    }
+    __syncthreads();
+    const int step = sh.bin;
+    const uint32_t equal = sh.bin_n;
+    const u64 above = sh.above_m;
+    __syncthreads();
+    if (step < 0 || step > k_step) return out;   // (roundings at p next to 1)
+    need -= above;
+    if (r.one_value(step)) {
+      const u64 w = max((u64)1, weight(r.s, sh.table, r.value_of(step)));
+      const uint32_t ties = (uint32_t)min((u64)equal, (need + w - 1) / w);
+      if (k_on && step == k_step) {
+        out.ties = min(out.ties, ties);
+      } else {
+        out.value = r.value_of(step);
+        out.ties = ties;
+        out.equal = equal;
+      }
+      return out;
+    }
+    uint32_t lo, hi, key, n_key;
+    r.step_keys(step, lo, hi);
+    if (r.template refine<true>(lo, hi, need, key, n_key) && (!k_on || of_key(key) >= out.value)) {
+      const float b = of_key(key);
+      const u64 w = max((u64)1, weight(r.s, sh.table, b));
+      const uint32_t ties = (uint32_t)min((u64)n_key, (need + w - 1) / w);
+      if (k_on && b == out.value) {
+        out.ties = min(out.ties, ties);
+      } else {
+        out.value = b;
+        out.ties = ties;
+        out.equal = n_key;
+      }
+    }
+    return out;
+  } else {
+    // ---------------------------------------------------------------- float32: the steps that may hold the border
+    int lo_step = 0, hi_step = k_on ? k_step : kSteps - 1;
+    if (cuts_p && !k_on) {
+      // Between the running sums' bounds: a step's weights lie within a factor of 2^(-1/128) of its upper end's (the
+      // last step's between 0 and that); 2^-10 for the sums' own roundings and those of the steps' borders.
+      float all = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) all += sh.scan_f[w];
+      constexpr float kWidth = 0.99459939f;   // 2^(-1 / 128)
+      if (tid == 0) {
+        sh.bin = kSteps - 1;
+        sh.bin2 = kSteps - 1;
+      }
+      __syncthreads();
+      const float least = p * all * kWidth * (1.f - 0x1p-10f) - 0x1p-14f, most = p * all * (1.f + 0x1p-10f) + 0x1p-14f;
+      float at = bf;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const float up = at + (float)n[i] * ptx::ex2_approx(-(float)(s0 + i) * (1.f / kPerOctave));
+        if (at < least && up >= least) atomicMin(&sh.bin, s0 + i);
+        if (at * kWidth < most && up * kWidth >= most) atomicMin(&sh.bin2, s0 + i);
+        at = up;
+      }
+      if (tid == 0 && least <= 0.f) sh.bin = 0;
+      __syncthreads();
+      lo_step = sh.bin;
+      hi_step = max(sh.bin2, lo_step);
+      __syncthreads();
+    }
+    // candidates: the logits of those steps
+    if (tid == 0) sh.above_n = sh.bin_n = 0;
+    __syncthreads();
+    {
+      uint32_t at = bn;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        if (s0 + i == lo_step) sh.bin_n = at;
+        at += n[i];
+        if (s0 + i == hi_step) sh.above_n = at;
+      }
+    }
+    if (tid == 0) sh.mine = 0;
+    __syncthreads();
+    const int room = kList / r.ranks;
+    const bool few = sh.above_n - sh.bin_n <= kList;
+    // one pass: the mass of all, the mass above lo_step, and the candidates handed to every block
+    u64 all = 0, above = 0;
+    {
+      W2 acc = {{0}, {0}}, acc_above = {{0}, {0}};
+      const bool sums = cuts_p && !k_on;
+      r.each([&](const float* x, int at) {
+        int step[U::n];
+        bool some = sums;
+#pragma unroll
+        for (int e = 0; e < U::n; ++e) {
+          step[e] = x[e] > -INFINITY ? r.step_of(x[e]) : kSteps;
+          some |= step[e] >= lo_step && step[e] <= hi_step;
+        }
+        if (!some) return;
+        if (sums) {
+#pragma unroll
+          for (int e = 0; e < U::n; e += 2) {
+            const W2 w = weights(r.s, sh.table, x[e], x[e + 1]);
+            const F2 is = pack(step[e] < kSteps ? 1.f : 0.f, step[e + 1] < kSteps ? 1.f : 0.f);
+            accumulate(acc, mul(w.hi, is), mul(w.lo, is));
+            if (step[e] < lo_step || step[e + 1] < lo_step) {
+              const F2 up = pack(step[e] < lo_step ? 1.f : 0.f, step[e + 1] < lo_step ? 1.f : 0.f);
+              accumulate(acc_above, mul(w.hi, up), mul(w.lo, up));
+            }
+          }
+        }
+        if (few)
+#pragma unroll
+          for (int e = 0; e < U::n; ++e)
+            if (step[e] >= lo_step && step[e] <= hi_step) {
+              const int i = atomicAdd(&sh.mine, 1);
+              const u64 c = ((u64)key_of(x[e]) << 32) | (0xFFFFFFFFu - (uint32_t)(at + e));
+              if (i < room)
+                for (int q = 0; q < r.ranks; ++q) st_cluster64(ptx::dsmem_addr(&sh.list[r.rank * room + i], q), c);
+            }
+      });
+      if (sums) {
+        all = fixed(acc);
+        above = fixed(acc_above);
+      }
+    }
+    if (cuts_p && !k_on) {
+      all = r.block_sum(all);
+      above = r.block_sum(above);
+    } else {
+      __syncthreads();
+    }
+    // (a third number that travels with the masses: the candidates of each block)
+    {
+      const u64 v[3] = {all, above, (u64)sh.mine};
+      if (tid < r.ranks)
+        for (int i = 0; i < 3; ++i) st_cluster64(ptx::dsmem_addr(&sh.sums[r.turn_s][i][r.rank], tid), v[i]);
+      ptx::cluster_sync_all();
+      all = above = 0;
+      bool fits = few;
+      int offset[kMaxCluster + 1];
+      offset[0] = 0;
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q) {
+        const int c = q < r.ranks ? (int)sh.sums[r.turn_s][2][q] : 0;
+        if (q < r.ranks) {
+          all += sh.sums[r.turn_s][0][q];
+          above += sh.sums[r.turn_s][1][q];
+        }
+        fits = fits && c <= room;
+        offset[q + 1] = offset[q] + c;
+      }
+      r.turn_s ^= 1;
+      if (fits) {
+        // ------------------------------------------------------------ few: in order, every block for itself
+        const int count = offset[kMaxCluster];
+        if (count == 0) return out;   // (cannot be: the first of those steps holds a logit)
+        int size = 32;
+        while (size < count) size <<= 1;
+        constexpr int kEach = kList / kThreads;
+        u64 mine[kEach];
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+          const int i = tid + j * kThreads;
+          mine[j] = 0;
+          if (i < count) {
+            int q = 0;
+#pragma unroll
+            for (int z = 1; z < kMaxCluster; ++z) q += i >= offset[z];
+            mine[j] = sh.list[q * room + i - offset[q]];
+          }
+        }
+        __syncthreads();
+        u64* sorted = sh.list;   // (packed, in place)
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+          if (tid + j * kThreads < size) sorted[tid + j * kThreads] = mine[j];
+        __syncthreads();
+        for (int len = 2; len <= size; len <<= 1)
+          for (int d = len >> 1; d > 0; d >>= 1) {
+            for (int i = tid; i < size / 2; i += kThreads) {
+              const int lo = 2 * i - (i & (d - 1)), hi = lo + d;
+              const u64 x = sorted[lo], y = sorted[hi];
+              if ((x < y) == ((lo & len) == 0)) {   // falling
+                sorted[lo] = y;
+                sorted[hi] = x;
+              }
+            }
+            if (d > 32 || size > 64) __syncthreads();
+            else __syncwarp();
+          }
+        __syncthreads();
+        // neighbours' weights and their running sums
+        const int per = max(1, size / kThreads);
+        u64 w[kEach], mass = 0, before;
+        uint32_t un;
+        float uf;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+          const int i = tid * per + j;
+          w[j] = j < per && i < count && cuts_p ? weight(r.s, sh.table, of_key((uint32_t)(sorted[i] >> 32))) : 0;
+          if (k_on && i >= k) w[j] = 0;
+          mass += w[j];
+        }
+        r.block_scan(0, mass, 0.f, un, before, uf);
+        if (k_on) {
+          all = 0;
+#pragma unroll
+          for (int v = 0; v < kWarps; ++v) all += sh.scan_m[v];
+        }
+        const u64 want = max((u64)1, times(all, p, true)), need = want > above ? want - above : 1;
+        const int most = k_on ? min(k, count) : count;
+        if (tid == 0) sh.bin = most - 1;
+        __syncthreads();
+        if (cuts_p) {
+          u64 at = before;
+#pragma unroll
+          for (int j = 0; j < kEach; ++j) {
+            const int i = tid * per + j;
+            if (j < per && i < most && at < need && at + w[j] >= need) atomicMin(&sh.bin, i);
+            at += w[j];
+          }
+          __syncthreads();
+        }
+        const u64 last = sorted[sh.bin];
+        out.value = of_key((uint32_t)(last >> 32));
+        out.cut = (int)(0xFFFFFFFFu - (uint32_t)last);
+        out.known = true;
+        return out;
+      }
+    }
+    // ---------------------------------------------------------------- many: histograms of the doubtful steps' floats
+    if (k_on) {
+      u64 need = (u64)k - k_above;
+      uint32_t lo, hi, key, n_key = 0;
+      r.step_keys(k_step, lo, hi);
+      r.template refine<false>(lo, hi, need, key, n_key);
+      out.value = of_key(key);
+      out.ties = (uint32_t)need;
+      out.equal = n_key;
+      if (!cuts_p) return out;
+      const float b = out.value;
+      const u64 v[1] = {r.block_sum(r.mass_where([&](float x) { return x > b; }))};
+      u64 before[1], mass[1];
+      r.cluster_sums(v, before, mass);
+      all = mass[0] + out.ties * weight(r.s, sh.table, b);
+      above = 0;
+      const u64 want = max((u64)1, times(all, p, true));
+      if (want > mass[0]) {   // inside the tokens that equal the k-th
+        const u64 w = max((u64)1, weight(r.s, sh.table, b));
+        out.ties = (uint32_t)min((u64)out.ties, (want - mass[0] + w - 1) / w);
+        return out;
+      }
+    }
+    if (!cuts_p) return out;
+    u64 need = max((u64)1, times(all, p, true));
+    if (need <= above) return out;   // (cannot be: the bounds hold)
+    need -= above;
+    uint32_t lo, hi, ends, key, n_key;
+    r.step_keys(lo_step, ends, hi);
+    if (k_on) lo = key_of(out.value) + 1;
+    else r.step_keys(hi_step, lo, ends);
+    if (r.template refine<true>(lo, hi, need, key, n_key)) {
+      out.value = of_key(key);
+      const u64 w = max((u64)1, weight(r.s, sh.table, out.value));
+      out.ties = (uint32_t)min((u64)n_key, (need + w - 1) / w);
+      out.equal = n_key;
+    }
+    return out;
+  }
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a, const __grid_constant__ Table tab) {
@@ -423,6 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   }
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // (waited for before the first remote write)
   if (tid < 64) sh.table[tid] = tab.t[tid];
+  if (tid == kThreads - 1 && min_p > 0.f) sh.min_p = (double)temperature * log((double)min_p);   // (read after barriers)
 
   Row<T> r;
   r.tile = reinterpret_cast<const T*>(dyn);
@@ -430,6 +1020,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   r.rank = rank;
   r.ranks = ranks;
   r.turn_h = r.turn_s = 0;
+  r.read_others = false;
   // 16-byte units from the aligned address at or before the row's first entry
   const int skew = (int)((reinterpret_cast<uintptr_t>(logits) & 15) / sizeof(T));
   const int all = (a.V + skew + U::n - 1) / U::n, per = (all + ranks - 1) / ranks;
@@ -442,7 +1033,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   {
     uint4* to = reinterpret_cast<uint4*>(dyn);
     const uint4* from = reinterpret_cast<const uint4*>(logits + r.first);
-    constexpr int kAhead = 4;
+    constexpr int kAhead = 8;
     for (int i0 = tid; i0 < r.units; i0 += kAhead * kThreads) {
       uint4 v[kAhead];
 #pragma unroll
@@ -462,36 +1053,37 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       for (int c = 0; c < kAhead; ++c) {
         const int i = i0 + c * kThreads;
         if (i >= r.units) continue;
-        float x[U::n];
-        U::read(v[c], x);
-#pragma unroll
-        for (int e = 0; e < U::n; ++e) {
-          x[e] = clean(x[e]);
-          top = fmaxf(top, x[e]);
-        }
-        to[i] = U::write(x);
+        to[i] = U::clean_max(v[c], top);
       }
     }
   }
-  if (sizeof(T) == 2) top = fminf(top, kBf16Max);   // (as it was written)
+#pragma unroll
   for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, m));
   if (lane == 0) sh.reds[warp] = top;
   __syncthreads();
+#pragma unroll
   for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sh.reds[w]);
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   if (tid < ranks) st_cluster(ptx::dsmem_addr(&sh.tops[rank], tid), __float_as_uint(top));
   ptx::cluster_sync_all();
   for (int i = 0; i < ranks; ++i) top = fmaxf(top, sh.tops[i]);
+  top += 0.f;
   r.top = top;
 
   u64 total = 0;
-  float border = -INFINITY;   // kept: above it, and the first `ties` that equal it
-  uint32_t ties = 0, equal = 0;
   if (top > -INFINITY) {
     {
-      const double c = temperature == 0.f ? 1.4426950408889634 : fmin(1.4426950408889634 / (double)temperature, 1e30);
-      r.s.ch = (float)c;
-      r.s.cl = (float)(c - (double)r.s.ch);
+      const float t = temperature == 0.f ? 1.f : temperature;
+      // log2(e) / T as a pair: the quotient, and what it leaves over T
+      constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.9259629911266174681e-8f;
+      r.s.ch = kLog2e / t;
+      r.s.cl = (fmaf(-r.s.ch, t, kLog2e) + kLog2eLow) / t;
+      if (!(r.s.ch < 1e30f)) {   // (only logits that equal the largest have weight)
+        r.s.ch = 1e30f;
+        r.s.cl = 0.f;
+      } else if (!(t < INFINITY)) {
+        r.s.cl = 0.f;
+      }
       const bool near = fabsf(top) * r.s.ch < 300.f;
       r.s.ref = near ? 0.f : top;
       const float z = near ? top : 0.f;
@@ -499,96 +1091,28 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       r.s.ml = __fmaf_rn(z, r.s.cl, __fmaf_rn(z, r.s.ch, -r.s.mh));
       r.s.least = fmaxf((r.s.mh - 150.f) / r.s.ch, -FLT_MAX);
       r.steps = r.s.ch * (float)kPerOctave;
+      // bf16: bins for the magnitudes from the largest that has weight down over kOctaves binary orders
+      r.low = fmaxf(top - 64.f / r.s.ch, -kBf16Max);
+      const int code = (int)(__float_as_uint(fmaxf(fabsf(top), fabsf(r.low))) >> 16);
+      r.least_code = max(1, (code & ~127) - (kOctaves - 1) * 128);
     }
-
-    // ---------------------------------------------------------------- top-k
-    const bool cuts_k = k > 0 && k < a.V, cuts_p = p < 1.f;
-    int last_bin = kBins - 1;    // steps that hold kept tokens
-    bool counted = false;
-    if (cuts_k) {
-      auto fill = [&](Hist& h) {
-        r.each([&](const float* x, int) {
-#pragma unroll
-          for (int e = 0; e < U::n; ++e)
-            if (x[e] > -INFINITY) atomicAdd(&h.n[r.bin_of(x[e])], 1u);
-        });
-      };
-      if (r.template border<false>((u64)k, fill)) {
-        u64 need = (u64)k - sh.above_n;
-        last_bin = sh.bin;
-        uint32_t lo, hi, key, n;
-        r.step_keys(last_bin, lo, hi);
-        r.template refine<false>(lo, hi, need, key, n);
-        border = of_key(key);
-        ties = (uint32_t)need;
-        equal = n;
-        counted = true;
-      }
-    }
-
-    // ---------------------------------------------------------------- top-p: of the tokens above the border
-    if (cuts_p) {
-      // the mass above the border, and a histogram of it
-      u64 mine = 0;
-      {
-        W2 acc = {{0}, {0}};
-        r.each([&](const float* x, int) {
-          bool some = false;
-#pragma unroll
-          for (int e = 0; e < U::n; ++e) some |= x[e] > border;
-          if (!some) return;
-#pragma unroll
-          for (int e = 0; e < U::n; e += 2) {
-            const W2 w = weights(r.s, sh.table, x[e], x[e + 1]);
-            const F2 on = pack(x[e] > border ? 1.f : 0.f, x[e + 1] > border ? 1.f : 0.f);
-            accumulate(acc, mul(w.hi, on), mul(w.lo, on));
-          }
-        });
-        mine = fixed(acc);
-      }
-      const u64 v[1] = {r.block_sum(mine)};
-      u64 before[1], sum[1];
-      r.cluster_sums(v, before, sum);
-      const u64 each_tie = counted ? weight(r.s, sh.table, border) : 0;
-      const double mass = (double)(sum[0] + ties * each_tie) * (double)p;
-      u64 need = max((u64)1, (u64)ceil(mass));
-      auto fill = [&](Hist& h) {
-        r.each([&](const float* x, int) {
-#pragma unroll
-          for (int e = 0; e < U::n; ++e)
-            if (x[e] > border) r.template count<true>(h, r.bin_of(x[e]), x[e]);
-        });
-      };
-      if (r.template border<true>(need, fill)) {
-        need -= sh.above_m;
-        const int bin = sh.bin;
-        uint32_t lo, hi, key, n;
-        r.step_keys(bin, lo, hi);
-        if (counted) lo = max(lo, key_of(border) + 1);
-        if (r.template refine<true>(lo, hi, need, key, n)) {
-          border = of_key(key);
-          const u64 w = max((u64)1, weight(r.s, sh.table, border));
-          ties = (uint32_t)min((u64)n, (need + w - 1) / w);
-          equal = n;
-        }
-      } else if (counted && each_tie > 0 && need > sum[0]) {   // inside the tokens that equal the k-th
-        ties = (uint32_t)min((u64)ties, (need - sum[0] + each_tie - 1) / each_tie);
-      }
-    }
+    Border edge = {-INFINITY, 0, 0, -1, false};
+    if (!(k > 0 && k < a.V)) k = 0;
+    if (k > 0 || p < 1.f) edge = find_border(r, k, p);
 
     // ---------------------------------------------------------------- min-p
     if (min_p > 0.f && temperature > 0.f) {
-      const double least = (double)top + (double)temperature * log((double)min_p);
+      const double least = (double)top + sh.min_p;
       const float f = __double2float_ru(least) + 0.f;   // the smallest logit that is kept
-      if (f > border) {
-        border = of_key(key_of(f) - (f == 0.f ? 2 : 1));   // the float below it
-        ties = 0;
+      if (f > edge.value) {
+        edge = {of_key(key_of(f) - (f == 0.f ? 2 : 1)), 0, 0, -1, true};   // the float below it
       }
     }
+    const float border = edge.value;
 
     // ---------------------------------------------------------------- which of the equal ones
-    const bool part = ties > 0 && ties < equal;
-    int cut = ties > 0 ? 0x7fffffff : -1;   // the last index of them that is kept
+    const bool part = !edge.known && edge.ties > 0 && edge.ties < edge.equal;
+    int cut = edge.known ? edge.cut : edge.ties > 0 ? 0x7fffffff : -1;   // the last index of them that is kept
     // a warp's run of units
     const int run = (r.units + kWarps - 1) / kWarps, w0 = min(r.units, warp * run), w1 = min(r.units, w0 + run);
     const uint4* tile = reinterpret_cast<const uint4*>(dyn);
@@ -613,6 +1137,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         }
       }
       u64 incl = mine;
+#pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const u64 up = __shfl_up_sync(kAll, incl, d);
         if (lane >= d) incl += up;
@@ -652,7 +1177,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
       u64 v[1] = {r.block_sum(n)}, before[1], sum[1];
       r.cluster_sums(v, before, sum);
-      search(ties - 1, before[0], is, [&](int at) {
+      search(edge.ties - 1, before[0], is, [&](int at) {
         for (int i = 0; i < ranks; ++i) st_cluster(ptx::dsmem_addr(&sh.cut, i), (uint32_t)at);
       });
       ptx::cluster_sync_all();
@@ -662,7 +1187,32 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     // ---------------------------------------------------------------- the kept mass, the token
     auto kept = [&](float x, int at) { return x > border || (x == border && x > -INFINITY && at <= cut); };
     u64 mine = 0;
-    {
+    if constexpr (Row<T>::kValues) {
+      // the weights of the bins' values that may be kept, once
+      if (r.read_others) ptx::cluster_sync_all();
+      else __syncthreads();
+      const int last = border > -INFINITY ? r.step_of(border) : Row<T>::kSteps - 2;
+      for (int i = tid; i <= min(last, Row<T>::kSteps - 2); i += kThreads)
+        if (r.one_value(i)) sh.weight[i] = weight(r.s, sh.table, r.value_of(i));
+      __syncthreads();
+    }
+    auto weight_of = [&](float x) -> u64 {
+      if constexpr (Row<T>::kValues) {
+        const int step = r.step_of(x);
+        if (r.one_value(step)) return sh.weight[step];
+      }
+      return weight(r.s, sh.table, x);
+    };
+    if constexpr (Row<T>::kValues) {
+      for (int i = w0 + lane; i < w1; i += 32) {
+        float x[U::n];
+        U::read(tile[i], x);
+        const int at = r.first + i * U::n;
+#pragma unroll
+        for (int e = 0; e < U::n; ++e)
+          if (kept(x[e], at + e)) mine += weight_of(x[e]);
+      }
+    } else {
       W2 acc = {{0}, {0}};
       for (int i = w0 + lane; i < w1; i += 32) {
         float x[U::n];
@@ -687,27 +1237,25 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     total = sum[0];
     if (a.token) {
       const float u = __ldg(a.u + row);
-      const double at = u > 0.f ? (double)fminf(u, 1.f) * (double)total : 0.0;
-      const u64 target = min((u64)at, total - 1);
-      search(target, before[0], [&](float x, int i) { return kept(x, i) ? weight(r.s, sh.table, x) : (u64)0; },
+      const u64 target = u > 0.f ? min(times(total, u, false), total - 1) : 0;
+      search(target, before[0], [&](float x, int i) { return kept(x, i) ? weight_of(x) : (u64)0; },
              [&](int i) { a.token[row] = i; });
     }
     if (a.probs) {
       float* out = a.probs + (long long)row * a.V;
       const float inv = 1.f / (float)total;
-      const T* x = r.tile;
-      for (int i = tid; i < r.units * U::n; i += kThreads) {
-        const int at = r.first + i;
-        if (at < 0 || at >= a.V) continue;
-        const float l = U::one(x + i);
-        float w = 0.f;
-        if (kept(l, at)) {
-          const W2 both_w = weights(r.s, sh.table, l, l);
-          float h, g;
-          unpack(add(both_w.hi, both_w.lo), h, g);
-          w = h * inv;
+      const int n = r.units * U::n;
+      for (int i = tid; i < n; i += 2 * kThreads) {
+        const int j = i + kThreads, ai = r.first + i, aj = r.first + j;
+        const float x = U::one(r.tile + i), y = j < n ? U::one(r.tile + j) : -INFINITY;
+        const bool kx = kept(x, ai), ky = kept(y, aj);
+        float px = 0.f, py = 0.f;
+        if (kx || ky) {
+          const W2 w = weights(r.s, sh.table, x, y);
+          unpack(mul(add(w.hi, w.lo), both(inv)), px, py);
         }
-        out[at] = w;
+        if (ai >= 0 && ai < a.V) out[ai] = kx ? px : 0.f;
+        if (j < n && aj >= 0 && aj < a.V) out[aj] = ky ? py : 0.f;
       }
     }
   } else {   // nothing to draw from
