@@ -93,31 +93,30 @@ __device__ __forceinline__ W2 weights(const Scale& s, const float2* table, float
     unpack(z, a, b);
     z = pack(fmaxf(a, s.least), fmaxf(b, s.least));
   }
-  const F2 ch = both(s.ch), ph = mul(z, ch), pl = fma(z, both(s.cl), fma(z, ch, mul(ph, both(-1.f))));
-  // less the maximum's product: d + dl
-  const F2 mh = both(-s.mh), d = add(ph, mh), dd = sub(d, ph);
-  const F2 dl = add(add(sub(ph, sub(d, dd)), sub(mh, dd)), add(pl, both(-s.ml)));
+  // the product's negative, and what its rounding left; with the maximum's product: -(d + dl)
+  const F2 np = mul(z, both(-s.ch)), pl = fma(z, both(s.cl), fma(z, both(s.ch), np));
+  const F2 mh = both(s.mh), nd = add(np, mh), dd = sub(nd, np);
+  const F2 dl = sub(add(pl, both(-s.ml)), add(sub(np, sub(nd, dd)), sub(mh, dd)));
   constexpr float kMagic = 196608.f;   // 1.5 2^17: the sum's last place is 1 / 64
-  const F2 t = add(d, both(kMagic)), r = sub(d, add(t, both(-kMagic)));   // r exactly
-  const F2 x = add(r, dl), xl = sub(dl, sub(x, r));                       // x + xl = r + dl
+  const F2 t = sub(both(kMagic), nd), r = sub(sub(both(kMagic), t), nd);   // r exactly
+  const F2 x = add(r, dl), xl = sub(dl, sub(x, r));                        // x + xl = r + dl
   // 2^x - 1 = a + b
   constexpr float kL1 = 0.693147182464599609375f, kL1l = -1.9046542999577679e-9f;   // ln 2 as a pair
   constexpr float kL2 = 0.2402265069591007f, kL3 = 0.05550410866482158f, kL4 = 0.009618129107628477f;
   const F2 a = mul(x, both(kL1));
-  F2 b = fma(x, both(kL1), mul(a, both(-1.f)));
+  F2 b = fma(x, both(kL1), mul(x, both(-kL1)));
   b = fma(x, both(kL1l), b);
   b = fma(xl, both(kL1), b);
   b = fma(mul(x, x), fma(x, fma(x, both(kL4), both(kL3)), both(kL2)), b);
-  // times 2^(k / 64) 2^e
+  // times 2^(k / 64) 2^e: th (1 + a) and what its rounding left (th - hi is exact)
   float t0, t1;
   unpack(t, t0, t1);
   const int j0 = __float_as_int(t0) - __float_as_int(kMagic), j1 = __float_as_int(t1) - __float_as_int(kMagic);
   const float2 e0 = table[j0 & 63], e1 = table[j1 & 63];
   const float f0 = __int_as_float((127 + 40 + (j0 >> 6)) << 23), f1 = __int_as_float((127 + 40 + (j1 >> 6)) << 23);
   const F2 th = pack(e0.x, e1.x), tl = pack(e0.y, e1.y), f = pack(f0, f1);
-  const F2 m = mul(th, a), hi = add(th, m);
-  F2 lo = add(sub(m, sub(hi, th)), fma(th, a, mul(m, both(-1.f))));
-  lo = add(lo, fma(th, b, tl));
+  const F2 hi = fma(th, a, th);
+  const F2 lo = add(fma(th, a, sub(th, hi)), fma(th, b, tl));
   return {mul(hi, f), mul(lo, f)};
 }
 __device__ __forceinline__ u64 fixed(float hi, float lo) { return (u64)(__float2ll_rn(hi) + __float2ll_rn(lo)); }
@@ -233,11 +232,6 @@ struct Unit<bf16> {
   }
 };
 
-__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -267,15 +261,15 @@ struct Bins<bf16> {
   static constexpr int n = 2 * kSide + 2;          // positive values falling, around zero, negative ones, the rest
 };
 
-struct Hist {
-  uint32_t n[kBins], lo[kBins], hi[kBins];   // counts, and masses in two words
-};
 constexpr int kList = 2048;                  // candidates of a row: places, shared out evenly to its blocks
 constexpr int kMiddle = 256;
 struct Shared {
   float2 table[64];
   union {
-    Hist hist[2];                            // by turns: a block may still read its neighbours' last one
+    struct {
+      uint4 hist[kBins];                     // counts, and masses in two words: this block's,
+      uint4 hist_all[kBins];                 // all blocks'
+    };
     struct {
       uint32_t steps[kMaxSteps];             // counts of the first histogram: this block's,
       uint32_t all[kMaxSteps];               // all blocks'
@@ -318,8 +312,7 @@ struct Row {
   float top, steps;  // maximum, steps of the first histogram a unit of logits
   int least_code;    // bf16: the smallest magnitude with a bin of its own
   float low;         // bf16: logits below it have no weight to speak of
-  int turn_h, turn_s;
-  bool read_others;  // other blocks may still be reading this one's last histogram
+  int turn_s;
 
   // The step of a logit: it rises as the logit falls.
   __device__ __forceinline__ int step_of(float l) const {
@@ -329,9 +322,11 @@ struct Row {
       const int at = kSide + ((b & 0x8000u) ? v : -v);
       return l < low ? kSteps - 1 : at;
     } else {
-      return (int)fminf((top - l) * steps, (float)(kSteps - 1));
+      return (int)place(l);
     }
   }
+  // float32: the same before it is cut to a step.
+  __device__ __forceinline__ float place(float l) const { return fminf((top - l) * steps, (float)(kSteps - 1)); }
   // The value of a step that holds one (kValues).
   __device__ __forceinline__ bool one_value(int step) const { return kValues && step != kSide && step != kSteps - 1; }
   __device__ __forceinline__ float value_of(int step) const {
@@ -422,9 +417,8 @@ struct Row {
       if (!some) return;
 #pragma unroll
       for (int e = 0; e < U::n; e += 2) {
-        const W2 w = weights(s, sh->table, x[e], x[e + 1]);
-        const F2 is = pack(on(x[e]) ? 1.f : 0.f, on(x[e + 1]) ? 1.f : 0.f);
-        accumulate(acc, mul(w.hi, is), mul(w.lo, is));
+        const W2 w = weights(s, sh->table, on(x[e]) ? x[e] : -INFINITY, on(x[e + 1]) ? x[e + 1] : -INFINITY);
+        accumulate(acc, w.hi, w.lo);
       }
     });
     return fixed(acc);
@@ -498,32 +492,40 @@ struct Row {
     return mass;
   }
 
-  // Zeroes the histogram of this turn (each block its own), to be filled by `fill`; then finds the first bin at
-  // which the running count (or mass) over all blocks reaches `need`. False if the whole does not.
+  // Zeroes this block's histogram, to be filled by `fill`; then finds the first bin at which the running count (or mass)
+  // over all blocks reaches `need`. False if the whole does not. (Added up in parts, as the steps are.)
   template <bool kMass, typename F>
   __device__ bool border(u64 need, F fill) {
-    Hist& h = sh->hist[turn_h];
-    for (int i = threadIdx.x; i < kBins; i += kThreads) {
-      h.n[i] = 0;
-      if (kMass) h.lo[i] = h.hi[i] = 0;
-    }
+    for (int i = threadIdx.x; i < kBins; i += kThreads) sh->hist[i] = make_uint4(0, 0, 0, 0);
     if (threadIdx.x == 0) sh->bin = -1;
     __syncthreads();
-    fill(h);
+    fill(sh->hist);
+    ptx::cluster_sync_all();
+    const int part = kBins / ranks;
+    for (int i = threadIdx.x; i < part; i += kThreads) {
+      const int at = rank * part + i;
+      uint32_t n = 0;
+      u64 m = 0;
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q) {
+        if (q >= ranks) continue;
+        const uint4 x = ld_cluster4(ptx::dsmem_addr(&sh->hist[at], q));
+        n += x.x;
+        m += (u64)x.y + ((u64)x.z << 32);
+      }
+      const uint4 t = make_uint4(n, (uint32_t)m, (uint32_t)(m >> 32), 0);
+      for (int q = 0; q < ranks; ++q) st_cluster4(ptx::dsmem_addr(&sh->hist_all[at], q), t);
+    }
     ptx::cluster_sync_all();
     // two neighbouring bins a thread
     const int b0 = 2 * threadIdx.x;
-    uint32_t n[2] = {0, 0};
-    u64 m[2] = {0, 0};
+    uint32_t n[2];
+    u64 m[2];
 #pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) {
-      if (r >= ranks) continue;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        n[i] += ld_cluster(ptx::dsmem_addr(&h.n[b0 + i], r));
-        if (kMass)
-          m[i] += (u64)ld_cluster(ptx::dsmem_addr(&h.lo[b0 + i], r)) + ((u64)ld_cluster(ptx::dsmem_addr(&h.hi[b0 + i], r)) << 32);
-      }
+    for (int i = 0; i < 2; ++i) {
+      const uint4 x = sh->hist_all[b0 + i];
+      n[i] = x.x;
+      m[i] = (u64)x.y + ((u64)x.z << 32);
     }
     uint32_t bn;
     u64 bm;
@@ -542,8 +544,6 @@ struct Row {
       bm += m[i];
     }
     __syncthreads();
-    turn_h ^= 1;
-    read_others = true;
     return sh->bin >= 0;
   }
 
@@ -575,7 +575,7 @@ struct Row {
   __device__ bool refine(uint32_t lo, uint32_t hi, u64& need, uint32_t& key, uint32_t& n) {
     for (;;) {
       const int bits = 32 - __clz(hi - lo), shift = max(0, bits - 10);
-      const bool got = border<kMass>(need, [&](Hist& h) {
+      const bool got = border<kMass>(need, [&](uint4* h) {
         each([&](const float* x, int) {
 #pragma unroll
           for (int e = 0; e < U::n; ++e) {
@@ -599,13 +599,13 @@ struct Row {
     }
   }
   template <bool kMass>
-  __device__ __forceinline__ void count(Hist& h, uint32_t b, float l) const {
-    atomicAdd(&h.n[b], 1u);
+  __device__ __forceinline__ void count(uint4* h, uint32_t b, float l) const {
+    atomicAdd(&h[b].x, 1u);
     if (!kMass) return;
     const u64 w = gdr::weight(s, sh->table, l);
-    const uint32_t old = atomicAdd(&h.lo[b], (uint32_t)w);
+    const uint32_t old = atomicAdd(&h[b].y, (uint32_t)w);
     const uint32_t up = (uint32_t)(w >> 32) + (old + (uint32_t)w < old);
-    if (up) atomicAdd(&h.hi[b], up);
+    if (up) atomicAdd(&h[b].z, up);
   }
 };
 
@@ -758,14 +758,15 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
     return out;
   } else {
     // ---------------------------------------------------------------- float32: the steps that may hold the border
+    constexpr float kWidth = 0.99459939f;   // 2^(-1 / 128)
     int lo_step = 0, hi_step = k_on ? k_step : kSteps - 1;
+    int first_step = 0;   // narrowed down
     if (cuts_p && !k_on) {
       // Between the running sums' bounds: a step's weights lie within a factor of 2^(-1/128) of its upper end's (the
       // last step's between 0 and that); 2^-10 for the sums' own roundings and those of the steps' borders.
       float all = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) all += sh.scan_f[w];
-      constexpr float kWidth = 0.99459939f;   // 2^(-1 / 128)
       if (tid == 0) {
         sh.bin = kSteps - 1;
         sh.bin2 = kSteps - 1;
@@ -784,16 +785,70 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
       __syncthreads();
       lo_step = sh.bin;
       hi_step = max(sh.bin2, lo_step);
+      first_step = lo_step;
       __syncthreads();
     }
-    // candidates: the logits of those steps
+    u64 all = 0, above = 0;   // the mass of all (of the first k), and above lo_step
+    if (cuts_p && !k_on) {
+      W2 acc = {{0}, {0}}, acc_above = {{0}, {0}};
+      const float lo_edge = (float)lo_step;
+      r.each([&](const float* x, int) {
+#pragma unroll
+        for (int e = 0; e < U::n; e += 2) {
+          const W2 w = weights(r.s, sh.table, x[e], x[e + 1]);
+          accumulate(acc, w.hi, w.lo);
+          const bool u0 = r.place(x[e]) < lo_edge, u1 = r.place(x[e + 1]) < lo_edge;
+          if (u0 || u1) {
+            const F2 up = pack(u0 ? 1.f : 0.f, u1 ? 1.f : 0.f);
+            accumulate(acc_above, mul(w.hi, up), mul(w.lo, up));
+          }
+        }
+      });
+      const u64 mine_all = r.block_sum(fixed(acc)), v[2] = {mine_all, r.block_sum(fixed(acc_above))};
+      u64 before[2], sum[2];
+      r.cluster_sums(v, before, sum);
+      all = sum[0];
+      above = sum[1];
+      // With these the doubt is about the window's own mass alone: usually one or two steps are left.
+      const u64 want = max((u64)1, times(all, p, true));
+      const float need = want > above ? (float)(want - above) * 0x1p-40f : 0.f, slack = (float)all * 0x1p-58f;
+      if (tid == 0) {
+        sh.bin = hi_step;
+        sh.bin2 = hi_step;
+        sh.reds[0] = 0.f;
+      }
+      __syncthreads();
+      float at = bf;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        if (s0 + i == lo_step) sh.reds[0] = at;   // the float sums' value where the window begins
+        at += (float)n[i] * ptx::ex2_approx(-(float)(s0 + i) * (1.f / kPerOctave));
+      }
+      __syncthreads();
+      at = bf - sh.reds[0];
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const float up = at + (float)n[i] * ptx::ex2_approx(-(float)(s0 + i) * (1.f / kPerOctave));
+        const int step = s0 + i;
+        if (step >= lo_step && step <= hi_step) {
+          if (up + slack >= need * (1.f - 0x1p-10f)) atomicMin(&sh.bin, step);
+          if ((up - slack) * kWidth >= need * (1.f + 0x1p-10f)) atomicMin(&sh.bin2, step);
+        }
+        at = up;
+      }
+      __syncthreads();
+      first_step = min(sh.bin, hi_step);
+      hi_step = max(min(sh.bin2, hi_step), first_step);
+      __syncthreads();
+    }
+    // candidates: the logits of steps first_step .. hi_step, handed to every block; and the mass of those before
     if (tid == 0) sh.above_n = sh.bin_n = 0;
     __syncthreads();
     {
       uint32_t at = bn;
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
-        if (s0 + i == lo_step) sh.bin_n = at;
+        if (s0 + i == first_step) sh.bin_n = at;
         at += n[i];
         if (s0 + i == hi_step) sh.above_n = at;
       }
@@ -801,71 +856,52 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
     if (tid == 0) sh.mine = 0;
     __syncthreads();
     const int room = kList / r.ranks;
-    const bool few = sh.above_n - sh.bin_n <= kList;
-    // one pass: the mass of all, the mass above lo_step, and the candidates handed to every block
-    u64 all = 0, above = 0;
+    const bool few = sh.above_n - sh.bin_n <= kList / 2;
+    u64 between = 0;
     {
-      W2 acc = {{0}, {0}}, acc_above = {{0}, {0}};
-      const bool sums = cuts_p && !k_on;
+      W2 acc = {{0}, {0}};
+      const float w_edge = (float)lo_step, lo_edge = (float)first_step, hi_edge = (float)(hi_step + 1);
+      const bool open = hi_step == kSteps - 1, mass = first_step > lo_step;
       r.each([&](const float* x, int at) {
-        int step[U::n];
-        bool some = sums;
+        float y[U::n];
+        bool some = false, part = false;
 #pragma unroll
         for (int e = 0; e < U::n; ++e) {
-          step[e] = x[e] > -INFINITY ? r.step_of(x[e]) : kSteps;
-          some |= step[e] >= lo_step && step[e] <= hi_step;
+          y[e] = r.place(x[e]);
+          some |= y[e] >= lo_edge && (y[e] < hi_edge || open);
+          part |= y[e] >= w_edge && y[e] < lo_edge;
         }
-        if (!some) return;
-        if (sums) {
+        if (mass && part)
 #pragma unroll
           for (int e = 0; e < U::n; e += 2) {
-            const W2 w = weights(r.s, sh.table, x[e], x[e + 1]);
-            const F2 is = pack(step[e] < kSteps ? 1.f : 0.f, step[e + 1] < kSteps ? 1.f : 0.f);
-            accumulate(acc, mul(w.hi, is), mul(w.lo, is));
-            if (step[e] < lo_step || step[e + 1] < lo_step) {
-              const F2 up = pack(step[e] < lo_step ? 1.f : 0.f, step[e + 1] < lo_step ? 1.f : 0.f);
-              accumulate(acc_above, mul(w.hi, up), mul(w.lo, up));
-            }
+            const W2 w = weights(r.s, sh.table, y[e] >= w_edge && y[e] < lo_edge ? x[e] : -INFINITY,
+                                 y[e + 1] >= w_edge && y[e + 1] < lo_edge ? x[e + 1] : -INFINITY);
+            accumulate(acc, w.hi, w.lo);
           }
-        }
-        if (few)
+        if (few && some)
 #pragma unroll
           for (int e = 0; e < U::n; ++e)
-            if (step[e] >= lo_step && step[e] <= hi_step) {
+            if (y[e] >= lo_edge && (y[e] < hi_edge || open) && x[e] > -INFINITY) {
               const int i = atomicAdd(&sh.mine, 1);
               const u64 c = ((u64)key_of(x[e]) << 32) | (0xFFFFFFFFu - (uint32_t)(at + e));
               if (i < room)
                 for (int q = 0; q < r.ranks; ++q) st_cluster64(ptx::dsmem_addr(&sh.list[r.rank * room + i], q), c);
             }
       });
-      if (sums) {
-        all = fixed(acc);
-        above = fixed(acc_above);
-      }
+      between = fixed(acc);
     }
-    if (cuts_p && !k_on) {
-      all = r.block_sum(all);
-      above = r.block_sum(above);
-    } else {
-      __syncthreads();
-    }
-    // (a third number that travels with the masses: the candidates of each block)
     {
-      const u64 v[3] = {all, above, (u64)sh.mine};
+      const u64 mine_between = r.block_sum(between), v[2] = {mine_between, (u64)sh.mine};
       if (tid < r.ranks)
-        for (int i = 0; i < 3; ++i) st_cluster64(ptx::dsmem_addr(&sh.sums[r.turn_s][i][r.rank], tid), v[i]);
+        for (int i = 0; i < 2; ++i) st_cluster64(ptx::dsmem_addr(&sh.sums[r.turn_s][i][r.rank], tid), v[i]);
       ptx::cluster_sync_all();
-      all = above = 0;
       bool fits = few;
       int offset[kMaxCluster + 1];
       offset[0] = 0;
 #pragma unroll
       for (int q = 0; q < kMaxCluster; ++q) {
-        const int c = q < r.ranks ? (int)sh.sums[r.turn_s][2][q] : 0;
-        if (q < r.ranks) {
-          all += sh.sums[r.turn_s][0][q];
-          above += sh.sums[r.turn_s][1][q];
-        }
+        const int c = q < r.ranks ? (int)sh.sums[r.turn_s][1][q] : 0;
+        if (q < r.ranks) above += sh.sums[r.turn_s][0][q];
         fits = fits && c <= room;
         offset[q + 1] = offset[q] + c;
       }
@@ -874,10 +910,9 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
         // ------------------------------------------------------------ few: in order, every block for itself
         const int count = offset[kMaxCluster];
         if (count == 0) return out;   // (cannot be: the first of those steps holds a logit)
-        int size = 32;
-        while (size < count) size <<= 1;
-        constexpr int kEach = kList / kThreads;
-        u64 mine[kEach];
+        // packed into the list's first half; then each to the place that the number of larger ones gives
+        constexpr int kEach = kList / 2 / kThreads;
+        u64 mine[kEach], *packed = sh.list, *sorted = sh.list + kList / 2;
 #pragma unroll
         for (int j = 0; j < kEach; ++j) {
           const int i = tid + j * kThreads;
@@ -890,53 +925,47 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
           }
         }
         __syncthreads();
-        u64* sorted = sh.list;   // (packed, in place)
 #pragma unroll
         for (int j = 0; j < kEach; ++j)
-          if (tid + j * kThreads < size) sorted[tid + j * kThreads] = mine[j];
+          if (tid + j * kThreads < count) packed[tid + j * kThreads] = mine[j];
         __syncthreads();
-        for (int len = 2; len <= size; len <<= 1)
-          for (int d = len >> 1; d > 0; d >>= 1) {
-            for (int i = tid; i < size / 2; i += kThreads) {
-              const int lo = 2 * i - (i & (d - 1)), hi = lo + d;
-              const u64 x = sorted[lo], y = sorted[hi];
-              if ((x < y) == ((lo & len) == 0)) {   // falling
-                sorted[lo] = y;
-                sorted[hi] = x;
-              }
-            }
-            if (d > 32 || size > 64) __syncthreads();
-            else __syncwarp();
-          }
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+          if (tid + j * kThreads >= count) continue;
+          int place = 0;
+#pragma unroll 8
+          for (int i = 0; i < count; ++i) place += packed[i] > mine[j];
+          sorted[place] = mine[j];
+        }
         __syncthreads();
         // neighbours' weights and their running sums
-        const int per = max(1, size / kThreads);
         u64 w[kEach], mass = 0, before;
         uint32_t un;
         float uf;
 #pragma unroll
         for (int j = 0; j < kEach; ++j) {
-          const int i = tid * per + j;
-          w[j] = j < per && i < count && cuts_p ? weight(r.s, sh.table, of_key((uint32_t)(sorted[i] >> 32))) : 0;
-          if (k_on && i >= k) w[j] = 0;
+          const int i = tid * kEach + j;
+          w[j] = i < count && cuts_p && !(k_on && i >= k) ? weight(r.s, sh.table, of_key((uint32_t)(sorted[i] >> 32))) : 0;
           mass += w[j];
         }
-        r.block_scan(0, mass, 0.f, un, before, uf);
-        if (k_on) {
-          all = 0;
+        if (cuts_p) {
+          r.block_scan(0, mass, 0.f, un, before, uf);
+          if (k_on) {
+            all = 0;
 #pragma unroll
-          for (int v = 0; v < kWarps; ++v) all += sh.scan_m[v];
+            for (int v = 0; v < kWarps; ++v) all += sh.scan_m[v];
+          }
         }
-        const u64 want = max((u64)1, times(all, p, true)), need = want > above ? want - above : 1;
         const int most = k_on ? min(k, count) : count;
         if (tid == 0) sh.bin = most - 1;
         __syncthreads();
         if (cuts_p) {
+          const u64 want = max((u64)1, times(all, p, true)), need = want > above ? want - above : 1;
           u64 at = before;
 #pragma unroll
           for (int j = 0; j < kEach; ++j) {
-            const int i = tid * per + j;
-            if (j < per && i < most && at < need && at + w[j] >= need) atomicMin(&sh.bin, i);
+            const int i = tid * kEach + j;
+            if (i < most && at < need && at + w[j] >= need) atomicMin(&sh.bin, i);
             at += w[j];
           }
           __syncthreads();
@@ -963,7 +992,6 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
       u64 before[1], mass[1];
       r.cluster_sums(v, before, mass);
       all = mass[0] + out.ties * weight(r.s, sh.table, b);
-      above = 0;
       const u64 want = max((u64)1, times(all, p, true));
       if (want > mass[0]) {   // inside the tokens that equal the k-th
         const u64 w = max((u64)1, weight(r.s, sh.table, b));
@@ -976,7 +1004,7 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
     if (need <= above) return out;   // (cannot be: the bounds hold)
     need -= above;
     uint32_t lo, hi, ends, key, n_key;
-    r.step_keys(lo_step, ends, hi);
+    r.step_keys(first_step, ends, hi);
     if (k_on) lo = key_of(out.value) + 1;
     else r.step_keys(hi_step, lo, ends);
     if (r.template refine<true>(lo, hi, need, key, n_key)) {
@@ -1019,8 +1047,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   r.sh = &sh;
   r.rank = rank;
   r.ranks = ranks;
-  r.turn_h = r.turn_s = 0;
-  r.read_others = false;
+  r.turn_s = 0;
   // 16-byte units from the aligned address at or before the row's first entry
   const int skew = (int)((reinterpret_cast<uintptr_t>(logits) & 15) / sizeof(T));
   const int all = (a.V + skew + U::n - 1) / U::n, per = (all + ranks - 1) / ranks;
@@ -1073,15 +1100,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   u64 total = 0;
   if (top > -INFINITY) {
     {
-      const float t = temperature == 0.f ? 1.f : temperature;
+      // (above 1e36 the lowest logit would have weight, and -inf, which stands for what is not kept, is taken for it)
+      const float t = temperature == 0.f ? 1.f : fminf(temperature, 1e36f);
       // log2(e) / T as a pair: the quotient, and what it leaves over T
       constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.9259629911266174681e-8f;
       r.s.ch = kLog2e / t;
       r.s.cl = (fmaf(-r.s.ch, t, kLog2e) + kLog2eLow) / t;
       if (!(r.s.ch < 1e30f)) {   // (only logits that equal the largest have weight)
         r.s.ch = 1e30f;
-        r.s.cl = 0.f;
-      } else if (!(t < INFINITY)) {
         r.s.cl = 0.f;
       }
       const bool near = fabsf(top) * r.s.ch < 300.f;
@@ -1189,8 +1215,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     u64 mine = 0;
     if constexpr (Row<T>::kValues) {
       // the weights of the bins' values that may be kept, once
-      if (r.read_others) ptx::cluster_sync_all();
-      else __syncthreads();
+      __syncthreads();
       const int last = border > -INFINITY ? r.step_of(border) : Row<T>::kSteps - 2;
       for (int i = tid; i <= min(last, Row<T>::kSteps - 2); i += kThreads)
         if (r.one_value(i)) sh.weight[i] = weight(r.s, sh.table, r.value_of(i));
@@ -1224,9 +1249,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         if (!some) continue;
 #pragma unroll
         for (int e = 0; e < U::n; e += 2) {
-          const W2 w = weights(r.s, sh.table, x[e], x[e + 1]);
-          const F2 on = pack(kept(x[e], at + e) ? 1.f : 0.f, kept(x[e + 1], at + e + 1) ? 1.f : 0.f);
-          accumulate(acc, mul(w.hi, on), mul(w.lo, on));
+          const W2 w = weights(r.s, sh.table, kept(x[e], at + e) ? x[e] : -INFINITY, kept(x[e + 1], at + e + 1) ? x[e + 1] : -INFINITY);
+          accumulate(acc, w.hi, w.lo);
         }
       }
       mine = fixed(acc);
