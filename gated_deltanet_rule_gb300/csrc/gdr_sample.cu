@@ -615,6 +615,7 @@ struct Border {
   uint32_t ties, equal;   // how many of the equal ones are kept, and how many there are
   int cut;
   bool known;             // cut is given (ties and equal are not needed)
+  u64 mass;               // of what is kept, where it came about (0: not)
 };
 
 // The border of top-k (0: none) and top-p (1: none) in a row whose logits are counted by step.
@@ -624,7 +625,7 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
   constexpr int kMine = Row<T>::kMine, kSteps = Row<T>::kSteps;
   Shared& sh = *r.sh;
   const int tid = threadIdx.x, s0 = tid * kMine;
-  Border out = {-INFINITY, 0, 0, -1, false};
+  Border out = {-INFINITY, 0, 0, -1, false, 0};
   const bool cuts_k = k > 0, cuts_p = p < 1.f;
   uint32_t n[kMine];
   const u64 middle = r.count_steps(p < 1.f, n);
@@ -969,6 +970,14 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
             at += w[j];
           }
           __syncthreads();
+          at = before;
+#pragma unroll
+          for (int j = 0; j < kEach; ++j) {
+            at += w[j];
+            if (tid * kEach + j == sh.bin) sh.above_m = at;
+          }
+          __syncthreads();
+          out.mass = above + sh.above_m;
         }
         const u64 last = sorted[sh.bin];
         out.value = of_key((uint32_t)(last >> 32));
@@ -1122,7 +1131,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const int code = (int)(__float_as_uint(fmaxf(fabsf(top), fabsf(r.low))) >> 16);
       r.least_code = max(1, (code & ~127) - (kOctaves - 1) * 128);
     }
-    Border edge = {-INFINITY, 0, 0, -1, false};
+    Border edge = {-INFINITY, 0, 0, -1, false, 0};
     if (!(k > 0 && k < a.V)) k = 0;
     if (k > 0 || p < 1.f) edge = find_border(r, k, p);
 
@@ -1131,7 +1140,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const double least = (double)top + sh.min_p;
       const float f = __double2float_ru(least) + 0.f;   // the smallest logit that is kept
       if (f > edge.value) {
-        edge = {of_key(key_of(f) - (f == 0.f ? 2 : 1)), 0, 0, -1, true};   // the float below it
+        edge = {of_key(key_of(f) - (f == 0.f ? 2 : 1)), 0, 0, -1, true, 0};   // the float below it
       }
     }
     const float border = edge.value;
@@ -1211,59 +1220,62 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
 
     // ---------------------------------------------------------------- the kept mass, the token
+    total = edge.mass;
     auto kept = [&](float x, int at) { return x > border || (x == border && x > -INFINITY && at <= cut); };
-    u64 mine = 0;
-    if constexpr (Row<T>::kValues) {
-      // the weights of the bins' values that may be kept, once
-      __syncthreads();
-      const int last = border > -INFINITY ? r.step_of(border) : Row<T>::kSteps - 2;
-      for (int i = tid; i <= min(last, Row<T>::kSteps - 2); i += kThreads)
-        if (r.one_value(i)) sh.weight[i] = weight(r.s, sh.table, r.value_of(i));
-      __syncthreads();
-    }
-    auto weight_of = [&](float x) -> u64 {
+    if (a.token || total == 0) {
+      u64 mine = 0;
       if constexpr (Row<T>::kValues) {
-        const int step = r.step_of(x);
-        if (r.one_value(step)) return sh.weight[step];
+        // the weights of the bins' values that may be kept, once
+        __syncthreads();
+        const int last = border > -INFINITY ? r.step_of(border) : Row<T>::kSteps - 2;
+        for (int i = tid; i <= min(last, Row<T>::kSteps - 2); i += kThreads)
+          if (r.one_value(i)) sh.weight[i] = weight(r.s, sh.table, r.value_of(i));
+        __syncthreads();
       }
-      return weight(r.s, sh.table, x);
-    };
-    if constexpr (Row<T>::kValues) {
-      for (int i = w0 + lane; i < w1; i += 32) {
-        float x[U::n];
-        U::read(tile[i], x);
-        const int at = r.first + i * U::n;
-#pragma unroll
-        for (int e = 0; e < U::n; ++e)
-          if (kept(x[e], at + e)) mine += weight_of(x[e]);
-      }
-    } else {
-      W2 acc = {{0}, {0}};
-      for (int i = w0 + lane; i < w1; i += 32) {
-        float x[U::n];
-        U::read(tile[i], x);
-        const int at = r.first + i * U::n;
-        bool some = false;
-#pragma unroll
-        for (int e = 0; e < U::n; ++e) some |= kept(x[e], at + e);
-        if (!some) continue;
-#pragma unroll
-        for (int e = 0; e < U::n; e += 2) {
-          const W2 w = weights(r.s, sh.table, kept(x[e], at + e) ? x[e] : -INFINITY, kept(x[e + 1], at + e + 1) ? x[e + 1] : -INFINITY);
-          accumulate(acc, w.hi, w.lo);
+      auto weight_of = [&](float x) -> u64 {
+        if constexpr (Row<T>::kValues) {
+          const int step = r.step_of(x);
+          if (r.one_value(step)) return sh.weight[step];
         }
+        return weight(r.s, sh.table, x);
+      };
+      if constexpr (Row<T>::kValues) {
+        for (int i = w0 + lane; i < w1; i += 32) {
+          float x[U::n];
+          U::read(tile[i], x);
+          const int at = r.first + i * U::n;
+#pragma unroll
+          for (int e = 0; e < U::n; ++e)
+            if (kept(x[e], at + e)) mine += weight_of(x[e]);
+        }
+      } else {
+        W2 acc = {{0}, {0}};
+        for (int i = w0 + lane; i < w1; i += 32) {
+          float x[U::n];
+          U::read(tile[i], x);
+          const int at = r.first + i * U::n;
+          bool some = false;
+#pragma unroll
+          for (int e = 0; e < U::n; ++e) some |= kept(x[e], at + e);
+          if (!some) continue;
+#pragma unroll
+          for (int e = 0; e < U::n; e += 2) {
+            const W2 w = weights(r.s, sh.table, kept(x[e], at + e) ? x[e] : -INFINITY, kept(x[e + 1], at + e + 1) ? x[e + 1] : -INFINITY);
+            accumulate(acc, w.hi, w.lo);
+          }
+        }
+        mine = fixed(acc);
       }
-      mine = fixed(acc);
-    }
-    const u64 v[1] = {r.block_sum(mine)};
-    u64 before[1], sum[1];
-    r.cluster_sums(v, before, sum);
-    total = sum[0];
-    if (a.token) {
-      const float u = __ldg(a.u + row);
-      const u64 target = u > 0.f ? min(times(total, u, false), total - 1) : 0;
-      search(target, before[0], [&](float x, int i) { return kept(x, i) ? weight_of(x) : (u64)0; },
-             [&](int i) { a.token[row] = i; });
+      const u64 v[1] = {r.block_sum(mine)};
+      u64 before[1], sum[1];
+      r.cluster_sums(v, before, sum);
+      total = sum[0];
+      if (a.token) {
+        const float u = __ldg(a.u + row);
+        const u64 target = u > 0.f ? min(times(total, u, false), total - 1) : 0;
+        search(target, before[0], [&](float x, int i) { return kept(x, i) ? weight_of(x) : (u64)0; },
+               [&](int i) { a.token[row] = i; });
+      }
     }
     if (a.probs) {
       float* out = a.probs + (long long)row * a.V;
