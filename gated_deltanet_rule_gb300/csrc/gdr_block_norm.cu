@@ -87,68 +87,103 @@ __device__ __forceinline__ void weight8(const float* w, int c, float* x) {   // 
     x[4 * k] = v.x; x[4 * k + 1] = v.y; x[4 * k + 2] = v.z; x[4 * k + 3] = v.w;
   }
 }
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + __expf(-x)); }
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }   // (2 ulp; 0 where e^-x is infinite)
 
-// Sums of n values over the block, the same in every thread. `red` takes turns between two places, so that one
-// barrier an exchange is enough.
+// A thread's 16-byte units of the rows to come, in shared memory: a ring of `stages` rows of `parts` units each, every
+// unit copied (asynchronously) and read by the same thread, so that rows on their way cost neither registers nor
+// barriers. Without stages (rows too wide for two of them) a row is read when it is needed.
+struct Ring {
+  uint4* mine;      // unit u of stage s at (s parts + u) blockDim.x
+  int stages, parts, slot;
+  __device__ __forceinline__ uint4* at(int u) const { return mine + (slot * parts + u) * blockDim.x; }
+  __device__ __forceinline__ void wait() const {   // for the oldest row
+    if (stages >= 4) ptx::cp_async_wait<3>();
+    else if (stages == 3) ptx::cp_async_wait<2>();
+    else if (stages == 2) ptx::cp_async_wait<1>();
+  }
+  __device__ __forceinline__ void next() { slot = slot + 1 == stages ? 0 : slot + 1; }
+};
+template <typename T>
+__device__ __forceinline__ void copy(const Ring& g, int u, const T* p) {
+#pragma unroll
+  for (int j = 0; j < (int)(sizeof(T) / 2); ++j) ptx::cp_async16_zfill(g.at(u + j), reinterpret_cast<const uint4*>(p) + j, 16);
+}
+template <typename T>
+__device__ __forceinline__ Raw<T> take(const Ring& g, int u, const T* p) {
+  if (g.stages == 0) return load(p);
+  Raw<T> r;
+#pragma unroll
+  for (int j = 0; j < (int)(sizeof(T) / 2); ++j) r.v[j] = *g.at(u + j);
+  return r;
+}
+
+// Sums of n values over the block, the same in every thread. red holds 0 where there is no warp; a place of it is
+// written again only after another barrier.
 template <int n>
 __device__ __forceinline__ void block_sum(float (&v)[n], float (*red)[16]) {
 #pragma unroll
   for (int m = 16; m >= 1; m >>= 1)
 #pragma unroll
     for (int i = 0; i < n; ++i) v[i] += __shfl_xor_sync(kAll, v[i], m);
-  const int warps = blockDim.x >> 5;
-  if (warps == 1) return;
-  const int lane = threadIdx.x & 31;
-  if (lane == 0)
+  if (blockDim.x == 32) return;
+  if ((threadIdx.x & 31) == 0)
 #pragma unroll
     for (int i = 0; i < n; ++i) red[i][threadIdx.x >> 5] = v[i];
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < n; ++i) {
-    v[i] = (lane & 15) < warps ? red[i][lane & 15] : 0.f;
+    float4 x[4];
 #pragma unroll
-    for (int m = 8; m >= 1; m >>= 1) v[i] += __shfl_xor_sync(kAll, v[i], m);
+    for (int j = 0; j < 4; ++j) x[j] = reinterpret_cast<const float4*>(red[i])[j];
+    v[i] = ((x[0].x + x[0].y) + (x[0].z + x[0].w)) + ((x[1].x + x[1].y) + (x[1].z + x[1].w)) +
+           (((x[2].x + x[2].y) + (x[2].z + x[2].w)) + ((x[3].x + x[3].y) + (x[3].z + x[3].w)));
   }
 }
 
 // One row's vectors of a thread: k-th at channel 8 (threadIdx.x + k blockDim.x).
 template <typename T, int K>
 __global__ void __launch_bounds__(kMaxThreads, K == 1 ? 2 : 1) block_norm_kernel(const BlockNormArgs a) {
-  __shared__ float red[2][1][16];
+  constexpr int kPart = sizeof(T) / 2;   // units of 8 channels
+  extern __shared__ __align__(16) uint4 dyn[];
+  __shared__ __align__(16) float red[2][1][16];
+  if (threadIdx.x < 32) red[threadIdx.x >> 4][0][threadIdx.x & 15] = 0.f;
+  __syncthreads();
   const int C = a.C;
   const float inv_c = 1.f / (float)C;
   int at[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) at[k] = 8 * (threadIdx.x + k * blockDim.x);
   const T *h = static_cast<const T*>(a.h), *y = static_cast<const T*>(a.y), *gate = static_cast<const T*>(a.gate);
+  Ring ring{dyn + threadIdx.x, a.stages, 3 * K * kPart, 0};
+  auto fetch = [&](long long row) {   // into the ring's present slot
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (at[k] >= C || row >= a.rows) continue;
+      copy(ring, (3 * k) * kPart, y + row * a.y_row + at[k]);
+      if (gate) copy(ring, (3 * k + 1) * kPart, gate + row * a.gate_row + at[k]);
+      copy(ring, (3 * k + 2) * kPart, h + row * C + at[k]);
+    }
+    ptx::cp_async_commit();
+    ring.next();
+  };
+  for (int i = 0; i < a.stages; ++i) fetch(blockIdx.x + (long long)i * gridDim.x);
   float w_pre[8], w_post[8], w_scale[8];   // (one vector a thread: kept)
   if (K == 1 && at[0] < C) {
     weight8(a.pre_w, at[0], w_pre);
     weight8(a.post_w, at[0], w_post);
     weight8(a.scale, at[0], w_scale);
   }
-  Raw<T> rh[K], ry[K], rg[K];
-  auto fetch = [&](long long row) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (at[k] >= C || row >= a.rows) continue;
-      ry[k] = load(y + row * a.y_row + at[k]);
-      if (gate) rg[k] = load(gate + row * a.gate_row + at[k]);
-      rh[k] = load(h + row * C + at[k]);
-    }
-  };
-  fetch(blockIdx.x);
   for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
     float x[K][8], z[K][8], g[K][8];
+    ring.wait();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (at[k] >= C) continue;
-      widen(rh[k], x[k]);
-      widen(ry[k], z[k]);
-      if (gate) widen(rg[k], g[k]);
+      widen(take(ring, (3 * k + 2) * kPart, h + row * C + at[k]), x[k]);
+      widen(take(ring, (3 * k) * kPart, y + row * a.y_row + at[k]), z[k]);
+      if (gate) widen(take(ring, (3 * k + 1) * kPart, gate + row * a.gate_row + at[k]), g[k]);
     }
-    fetch(row + gridDim.x);
+    if (ring.stages) fetch(row + (long long)ring.stages * gridDim.x);
     float r = 1.f;
     if (a.post_w) {
       float s[1] = {0.f};
@@ -195,8 +230,13 @@ __global__ void __launch_bounds__(kMaxThreads, K == 1 ? 2 : 1) block_norm_kernel
 // shared memory at the thread's own places.
 template <typename T, int K>
 __global__ void __launch_bounds__(kMaxThreads, 1) block_norm_backward_kernel(const BlockNormArgs a) {
-  __shared__ float red[2][5][16];
-  extern __shared__ __align__(16) float acc_sm[];   // (K > 1) [3][C]
+  constexpr int kPart = sizeof(T) / 2;
+  extern __shared__ __align__(16) uint4 dyn[];
+  __shared__ __align__(16) float red[2][5][16];
+  if (threadIdx.x < 32)
+#pragma unroll
+    for (int i = 0; i < 5; ++i) red[threadIdx.x >> 4][i][threadIdx.x & 15] = 0.f;
+  __syncthreads();
   const int C = a.C;
   const float inv_c = 1.f / (float)C;
   int at[K];
@@ -204,6 +244,23 @@ __global__ void __launch_bounds__(kMaxThreads, 1) block_norm_backward_kernel(con
   for (int k = 0; k < K; ++k) at[k] = 8 * (threadIdx.x + k * blockDim.x);
   const T *h = static_cast<const T*>(a.h), *y = static_cast<const T*>(a.y), *gate = static_cast<const T*>(a.gate);
   const T* dn = static_cast<const T*>(a.dn);
+  constexpr int kVec = 4 * kPart + 2;   // units of a thread's vector: y, gate, h, dn, dh_out
+  Ring ring{dyn + threadIdx.x, a.stages, K * kVec, 0};
+  float* acc_sm = reinterpret_cast<float*>(dyn + (size_t)a.stages * K * kVec * blockDim.x);   // (K > 1) [3][C]
+  auto fetch = [&](long long row) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (at[k] >= C || row >= a.rows) continue;
+      copy(ring, k * kVec, y + row * a.y_row + at[k]);
+      if (gate) copy(ring, k * kVec + kPart, gate + row * a.gate_row + at[k]);
+      copy(ring, k * kVec + 2 * kPart, h + row * C + at[k]);
+      copy(ring, k * kVec + 3 * kPart, dn + row * C + at[k]);
+      if (a.dh_out) copy(ring, k * kVec + 4 * kPart, a.dh_out + row * C + at[k]);
+    }
+    ptx::cp_async_commit();
+    ring.next();
+  };
+  for (int i = 0; i < a.stages; ++i) fetch(blockIdx.x + (long long)i * gridDim.x);
   float w_pre[8], w_post[8], w_scale[8], acc[3][8];
   if (K == 1 && at[0] < C) {
     weight8(a.pre_w, at[0], w_pre);
@@ -233,38 +290,25 @@ __global__ void __launch_bounds__(kMaxThreads, 1) block_norm_backward_kernel(con
       }
     }
   };
-  Raw<T> rh[K], ry[K], rg[K], rn[K];
-  Raw<float> ro[K];
-  auto fetch = [&](long long row) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (at[k] >= C || row >= a.rows) continue;
-      ry[k] = load(y + row * a.y_row + at[k]);
-      if (gate) rg[k] = load(gate + row * a.gate_row + at[k]);
-      rh[k] = load(h + row * C + at[k]);
-      rn[k] = load(dn + row * C + at[k]);
-      if (a.dh_out) ro[k] = load(a.dh_out + row * C + at[k]);
-    }
-  };
-  fetch(blockIdx.x);
   for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
     Raw<T> cy[K], cn[K];   // y and dn stay as they are, and are widened where they are used
     float x[K][8], g[K][8], dx[K][8];
+    ring.wait();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (at[k] >= C) continue;
-      cy[k] = ry[k];
-      cn[k] = rn[k];
-      widen(rh[k], x[k]);
+      cy[k] = take(ring, k * kVec, y + row * a.y_row + at[k]);
+      cn[k] = take(ring, k * kVec + 3 * kPart, dn + row * C + at[k]);
+      widen(take(ring, k * kVec + 2 * kPart, h + row * C + at[k]), x[k]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         g[k][e] = 1.f;
         dx[k][e] = 0.f;
       }
-      if (gate) widen(rg[k], g[k]);
-      if (a.dh_out) widen(ro[k], dx[k]);
+      if (gate) widen(take(ring, k * kVec + kPart, gate + row * a.gate_row + at[k]), g[k]);
+      if (a.dh_out) widen(take(ring, k * kVec + 4 * kPart, a.dh_out + row * C + at[k]), dx[k]);
     }
-    fetch(row + gridDim.x);
+    if (ring.stages) fetch(row + (long long)ring.stages * gridDim.x);
     float r = 1.f;
     if (a.post_w) {
       float s[1] = {0.f};
@@ -384,28 +428,39 @@ int threads_of(int C) { return std::min(kMaxThreads, (C / 8 + 31) / 32 * 32); }
 int vectors_of(int C) { return (C / 8 + kMaxThreads - 1) / kMaxThreads; }
 // Blocks of the gradient that a GPU holds: 512 threads an SM.
 int backward_blocks(int C) { return kNumSMs * std::min(16, kMaxThreads / threads_of(C)); }
+// Rows on their way to a block, of `per` on an SM: at most four, none where not even two fit.
+constexpr int kSmemSM = 220 << 10;
+int stages_of(int per, int bytes, int more) {
+  const int n = std::min(4, (std::min(kSmemSM / per, 224 << 10) - 2048 - more) / bytes);
+  return n < 2 ? 0 : n;
+}
 
 template <typename T, int K>
-cudaError_t forward(const BlockNormArgs& a, cudaStream_t s) {
+cudaError_t forward(BlockNormArgs a, cudaStream_t s) {
   const int t = threads_of(a.C), per = std::min(32, (K == 1 ? 2 : 1) * kMaxThreads / t);
+  const int bytes = 3 * K * (int)(sizeof(T) / 2) * t * 16;
+  a.stages = stages_of(per, bytes, 0);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(block_norm_kernel<T, K>), 224 << 10, done);
+  if (e != cudaSuccess) return e;
   const int slot = stage_timer_begin(s, kKernBlockNorm);
-  block_norm_kernel<T, K><<<(unsigned)std::min<long long>(a.rows, kNumSMs * per), t, 0, s>>>(a);
+  block_norm_kernel<T, K><<<(unsigned)std::min<long long>(a.rows, kNumSMs * per), t, a.stages * bytes, s>>>(a);
   stage_timer_end(slot, s);
   return cudaGetLastError();
 }
 template <typename T, int K>
-cudaError_t backward(const BlockNormArgs& a, cudaStream_t s) {
-  const int blocks = (int)std::min<long long>(a.rows, backward_blocks(a.C)), smem = K == 1 ? 0 : 3 * a.C * 4;
-  if (K > 1) {
-    static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(block_norm_backward_kernel<T, K>), 3 * kBlockNormMaxC * 4, done);
-    if (e != cudaSuccess) return e;
-  }
-  int slot = stage_timer_begin(s, kKernBlockNormBwd);
-  block_norm_backward_kernel<T, K><<<blocks, threads_of(a.C), smem, s>>>(a);
-  stage_timer_end(slot, s);
-  cudaError_t e = cudaGetLastError();
+cudaError_t backward(BlockNormArgs a, cudaStream_t s) {
+  const int t = threads_of(a.C), blocks = (int)std::min<long long>(a.rows, backward_blocks(a.C));
+  const int bytes = K * (4 * (int)(sizeof(T) / 2) + 2) * t * 16, more = K == 1 ? 0 : 3 * a.C * 4;
+  a.stages = stages_of(std::min(16, kMaxThreads / t), bytes, more);
+  const int smem = a.stages * bytes + more;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(block_norm_backward_kernel<T, K>), 224 << 10, done);
   if (e != cudaSuccess) return e;
+  int slot = stage_timer_begin(s, kKernBlockNormBwd);
+  block_norm_backward_kernel<T, K><<<blocks, t, smem, s>>>(a);
+  stage_timer_end(slot, s);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   slot = stage_timer_begin(s, kKernBlockNormBwd);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((a.C + 31) / 32, 3);

@@ -198,6 +198,7 @@ struct BlockNormArgs {
   float* dpost_w;
   float* dscale;
   float* partial;
+  int stages;                // set by the launch: rows on their way to a block
 };
 constexpr int kBlockNormMaxC = 16384;
 size_t block_norm_backward_workspace_bytes(int C);
