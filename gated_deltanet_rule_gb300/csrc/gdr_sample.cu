@@ -28,10 +28,13 @@
 #include <cmath>
 
 #include "gdr_serve.h"
+#include "pairs.cuh"
 #include "ptx.cuh"
 
 namespace gdr {
 namespace {
+
+using namespace pairs;
 
 using bf16 = __nv_bfloat16;
 using u64 = unsigned long long;
@@ -45,34 +48,6 @@ constexpr int kTarget = 100 << 10;  // bytes of a block's part of a row: two blo
 struct Table {
   float2 t[64];   // 2^(k / 64) as pairs
 };
-
-// Two floats in one register pair.
-struct F2 {
-  u64 v;
-};
-__device__ __forceinline__ F2 pack(float lo, float hi) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ F2 both(float x) { return pack(x, x); }
-__device__ __forceinline__ void unpack(F2 x, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x.v)); }
-__device__ __forceinline__ F2 add(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 mul(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
-__device__ __forceinline__ F2 sub(F2 a, F2 b) { return fma(b, both(-1.f), a); }
 
 // What a row's weights are formed from.
 struct Scale {
