@@ -6,14 +6,14 @@
 //   dh = dx,   dscale = sum dx g z,   dgate = dx scale z g (1 - g),   dz = dx scale g,
 //   dpost_w = sum dz y r,   dy = r (post_w dz - y r^2 mean(post_w dz y))  (or dz).
 //
-// Both are bound by HBM. A block takes a row at a time, a thread 8 neighbouring channels of it (16 bytes of
-// bfloat16), so that a row stays in registers from its one reading to its writing; the weights of a
+// Both are bound by HBM. A block takes a row at a time, a thread 8 channels of it (16 neighbouring bytes, of
+// float32 twice), so that a row stays in registers from its one reading to its writing; the weights of a
 // thread's channels are read once and kept. Up to four rows are on their way to a block's shared memory.
 //
 // The gradient's three sums of a row follow one another (mean(y^2) gives x, x gives dx, dx gives dz), but the
 // last is linear in dx: with p = post_w scale g it is
 //   sum(p dx y) = sum(p y dh_out) + s sum(p y pre_w dn) - s^3 mean(pre_w dn x) sum(p y x),
-// so all but mean(y^2) are taken at once, and a row costs two exchanges instead of three. The weights' gradients
+// so all but mean(y^2) are taken at once, and the next row's mean(y^2) with them: a row costs one exchange, not three. The weights' gradients
 // need two sums over the rows a channel, A = sum dn x s and B = sum dx g y r: dpre_w = A, dpost_w = scale B,
 // dscale = post_w B. They stay with the thread that owns the channel (in registers, for more than kWideC
 // channels in shared memory), leave as one partial row a block and are summed in order by a second kernel: no
@@ -34,43 +34,35 @@ using namespace pairs;
 using bf16 = __nv_bfloat16;
 constexpr int kMaxThreads = 512;   // of a block; 8 channels a thread
 constexpr int kWideC = 8 * kMaxThreads;
+constexpr int kPairThreads = 320;  // of a block of the gradient that leaves room for another on its SM
 constexpr unsigned kAll = 0xffffffffu;
 
-// 8 channels as they lie in memory
+// A thread's vector: 16 bytes of neighbouring channels, so that a warp reads and writes whole sectors
 template <typename T>
-struct Raw {
-  uint4 v[sizeof(T) / 2];
+constexpr int kCh = 16 / (int)sizeof(T);
+__device__ __forceinline__ uint4 load(const void* p) {   // read once: nothing for L1 to keep
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+template <int n>
+struct Vec {   // to compute with
+  F2 p[n / 2];
 };
 template <typename T>
-__device__ __forceinline__ Raw<T> load(const T* p) {   // read once: nothing for L1 to keep
-  Raw<T> r;
+__device__ __forceinline__ Vec<kCh<T>> widen(const uint4& r) {
+  const uint32_t u[4] = {r.x, r.y, r.z, r.w};
+  Vec<kCh<T>> x;
+  if constexpr (sizeof(T) == 2) {
 #pragma unroll
-  for (int k = 0; k < (int)(sizeof(T) / 2); ++k)
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.v[k].x), "=r"(r.v[k].y), "=r"(r.v[k].z), "=r"(r.v[k].w) : "l"(reinterpret_cast<const uint4*>(p) + k));
-  return r;
-}
-// 8 channels to compute with
-struct Vec {
-  F2 p[4];
-};
-__device__ __forceinline__ Vec widen(const Raw<bf16>& r) {
-  const uint32_t u[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
-  Vec x;
+    for (int e = 0; e < 4; ++e) x.p[e] = pack(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xFFFF0000u));
+  } else {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) x.p[e] = pack(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xFFFF0000u));
-  return x;
-}
-__device__ __forceinline__ Vec widen(const Raw<float>& r) {
-  Vec x;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    x.p[2 * k] = pack(__uint_as_float(r.v[k].x), __uint_as_float(r.v[k].y));
-    x.p[2 * k + 1] = pack(__uint_as_float(r.v[k].z), __uint_as_float(r.v[k].w));
+    for (int e = 0; e < 2; ++e) x.p[e] = pack(__uint_as_float(u[2 * e]), __uint_as_float(u[2 * e + 1]));
   }
   return x;
 }
-__device__ __forceinline__ void store(bf16* p, const Vec& x) {
+__device__ __forceinline__ void store(bf16* p, const Vec<8>& x) {
   uint32_t u[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -80,26 +72,43 @@ __device__ __forceinline__ void store(bf16* p, const Vec& x) {
   }
   *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
-__device__ __forceinline__ void store(float* p, const Vec& x) {
-  float f[8];
+template <int n>
+__device__ __forceinline__ void store(float* p, const Vec<n>& x) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) unpack(x.p[e], f[2 * e], f[2 * e + 1]);
-  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  for (int e = 0; e < n / 4; ++e) {
+    float4 f;
+    unpack(x.p[2 * e], f.x, f.y);
+    unpack(x.p[2 * e + 1], f.z, f.w);
+    reinterpret_cast<float4*>(p)[e] = f;
+  }
 }
-__device__ __forceinline__ Vec filled(float x) { return {both(x), both(x), both(x), both(x)}; }
-__device__ __forceinline__ Vec weight8(const float* w, int c) {   // NULL: ones
-  if (!w) return filled(1.f);
-  Vec x;
+template <int n>
+__device__ __forceinline__ Vec<n> filled(float x) {
+  Vec<n> v;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const float4 v = __ldg(reinterpret_cast<const float4*>(w + c) + k);
-    x.p[2 * k] = pack(v.x, v.y);
-    x.p[2 * k + 1] = pack(v.z, v.w);
+  for (int e = 0; e < n / 2; ++e) v.p[e] = both(x);
+  return v;
+}
+template <int n>
+__device__ __forceinline__ Vec<n> floats(const float* p) {
+  Vec<n> x;
+#pragma unroll
+  for (int e = 0; e < n / 4; ++e) {
+    const float4 v = reinterpret_cast<const float4*>(p)[e];
+    x.p[2 * e] = pack(v.x, v.y);
+    x.p[2 * e + 1] = pack(v.z, v.w);
   }
   return x;
 }
-__device__ __forceinline__ Vec times(const Vec& a, const Vec& b) { return {mul(a.p[0], b.p[0]), mul(a.p[1], b.p[1]), mul(a.p[2], b.p[2]), mul(a.p[3], b.p[3])}; }
+template <int n>
+__device__ __forceinline__ Vec<n> weights_at(const float* w, int c) { return w ? floats<n>(w + c) : filled<n>(1.f); }   // NULL: ones
+template <int n>
+__device__ __forceinline__ Vec<n> times(const Vec<n>& a, const Vec<n>& b) {
+  Vec<n> x;
+#pragma unroll
+  for (int e = 0; e < n / 2; ++e) x.p[e] = mul(a.p[e], b.p[e]);
+  return x;
+}
 // 1 / (1 + e^-x): the exponential's and the reciprocal's approximations are good to 2 and 1 units of the last place;
 // an infinite exponential gives 0.
 __device__ __forceinline__ F2 sigmoid(F2 x) {
@@ -115,7 +124,7 @@ __device__ __forceinline__ F2 sigmoid(F2 x) {
 
 // A thread's 16-byte units of the rows to come, in shared memory: a ring of `stages` rows of `parts` units each, every
 // unit copied (asynchronously) and read by the same thread, so that rows on their way cost neither registers nor
-// barriers. Without stages (rows too wide for two of them) a row is read when it is needed.
+// barriers. Without stages (a row does not fit) a row is read when it is needed.
 struct Ring {
   uint4* mine;      // unit u of stage s at (s parts + u) blockDim.x
   int stages, parts, slot;
@@ -124,25 +133,44 @@ struct Ring {
     if (stages >= 4) ptx::cp_async_wait<3>();
     else if (stages == 3) ptx::cp_async_wait<2>();
     else if (stages == 2) ptx::cp_async_wait<1>();
+    else if (stages == 1) ptx::cp_async_wait<0>();
   }
   __device__ __forceinline__ void next() { slot = slot + 1 == stages ? 0 : slot + 1; }
 };
-template <typename T>
-__device__ __forceinline__ void copy(const Ring& g, int u, const T* p) {
+__device__ __forceinline__ void copy(const Ring& g, int u, const void* p) { ptx::cp_async16_zfill(g.at(u), p, 16); }
+__device__ __forceinline__ uint4 take(const Ring& g, int u, const void* p) { return g.stages ? *g.at(u) : load(p); }
+
+// float32 channels of a kernel whose threads own 8 of them (32 bytes): a warp's 1024 bytes are copied 16 bytes a lane in
+// order (a lane's own 32 bytes would be two half sectors), so lanes read what others copied.
+__device__ __forceinline__ void copy_wide(const Ring& g, int u, const float* row, int c, int C) {   // c: the thread's first channel
+  const int lane = threadIdx.x & 31, c0 = c - 8 * lane + 4 * lane;
+  uint4* to = g.at(u) - threadIdx.x + 2 * (threadIdx.x - lane) + lane;
 #pragma unroll
-  for (int j = 0; j < (int)(sizeof(T) / 2); ++j) ptx::cp_async16_zfill(g.at(u + j), reinterpret_cast<const uint4*>(p) + j, 16);
+  for (int j = 0; j < 2; ++j)
+    if (c0 + 128 * j < C) ptx::cp_async16_zfill(to + 32 * j, row + c0 + 128 * j, 16);
 }
-template <typename T>
-__device__ __forceinline__ Raw<T> take(const Ring& g, int u, const T* p) {
-  if (g.stages == 0) return load(p);
-  Raw<T> r;
+__device__ __forceinline__ Vec<8> take_wide(const Ring& g, int u, const float* p) {
+  if (!g.stages) return floats<8>(p);
+  return floats<8>(reinterpret_cast<const float*>(g.at(u) + threadIdx.x));
+}
+// The same for a store: two lanes exchange halves and write 32 bytes together. Every lane of the warp calls.
+__device__ __forceinline__ void store_wide(float* row, const Vec<8>& x, int c, int C) {
+  const bool odd = threadIdx.x & 1;
+  float own[4], give[4], got[4];
+  unpack(odd ? x.p[2] : x.p[0], own[0], own[1]);
+  unpack(odd ? x.p[3] : x.p[1], own[2], own[3]);
+  unpack(odd ? x.p[0] : x.p[2], give[0], give[1]);
+  unpack(odd ? x.p[1] : x.p[3], give[2], give[3]);
 #pragma unroll
-  for (int j = 0; j < (int)(sizeof(T) / 2); ++j) r.v[j] = *g.at(u + j);
-  return r;
+  for (int e = 0; e < 4; ++e) got[e] = __shfl_xor_sync(kAll, give[e], 1);
+  const float4 mine = make_float4(own[0], own[1], own[2], own[3]), other = make_float4(got[0], got[1], got[2], got[3]);
+  const int first = odd ? c - 4 : c, second = odd ? c + 4 : c + 8;   // of the even lane's 8 channels, of the odd one's
+  if (first < C) *reinterpret_cast<float4*>(row + first) = odd ? other : mine;
+  if (second < C) *reinterpret_cast<float4*>(row + second) = odd ? mine : other;
 }
 
-// Sums over the block, the same in every thread. red holds 0 where there is no warp; a place of it is written again
-// only after another barrier.
+// Sums over the block, the same in every thread: of one value, of two, of six. red holds 0 where there is no warp; a
+// place of it is written again only after another barrier.
 __device__ __forceinline__ float block_sum(float v, float* red) {
 #pragma unroll
   for (int m = 16; m >= 1; m >>= 1) v += __shfl_xor_sync(kAll, v, m);
@@ -155,14 +183,30 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   v += __shfl_xor_sync(kAll, v, 1);
   return v + __shfl_xor_sync(kAll, v, 2);
 }
-// Of five values: in each step a lane gives away half of what it holds, so that 9 exchanges do for all (lanes with the
-// same upper three bits end with one value), and the warps' sums are read four to a lane.
-__device__ __forceinline__ void block_sum5(float (&v)[5], float (*red)[16]) {
+// In each step a lane gives away half of what it holds, so that 9 exchanges do for six values (lanes with the same upper
+// three bits end with one value) and 5 for two, and the warps' sums are read four to a lane.
+__device__ __forceinline__ void block_sum(float (&v)[2], float (*red)[16]) {
+  const int lane = threadIdx.x & 31;
+  float c = (lane & 16 ? v[1] : v[0]) + __shfl_xor_sync(kAll, lane & 16 ? v[0] : v[1], 16);
+#pragma unroll
+  for (int m = 8; m >= 1; m >>= 1) c += __shfl_xor_sync(kAll, c, m);
+  if (blockDim.x > 32) {
+    if ((lane & 15) == 0) red[lane >> 4][threadIdx.x >> 5] = c;
+    __syncthreads();
+    const float4 x = reinterpret_cast<const float4*>(red[lane >> 4])[lane & 3];
+    c = (x.x + x.y) + (x.z + x.w);
+    c += __shfl_xor_sync(kAll, c, 1);
+    c += __shfl_xor_sync(kAll, c, 2);
+  }
+  v[0] = __shfl_sync(kAll, c, 0);
+  v[1] = __shfl_sync(kAll, c, 16);
+}
+__device__ __forceinline__ void block_sum(float (&v)[6], float (*red)[16]) {
   const int lane = threadIdx.x & 31;
   float a[4], b[2], c;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {   // lanes without bit 4 keep values 0 .. 3, those with it 4 .. 7 (of which 4 alone is there)
-    const float up = i == 0 ? v[4] : 0.f, got = __shfl_xor_sync(kAll, lane & 16 ? v[i] : up, 16);
+  for (int i = 0; i < 4; ++i) {   // lanes without bit 4 keep values 0 .. 3, those with it 4 .. 7 (6 and 7 are none)
+    const float up = i < 2 ? v[4 + i] : 0.f, got = __shfl_xor_sync(kAll, lane & 16 ? v[i] : up, 16);
     a[i] = (lane & 16 ? up : v[i]) + got;
   }
 #pragma unroll
@@ -179,29 +223,42 @@ __device__ __forceinline__ void block_sum5(float (&v)[5], float (*red)[16]) {
     c += __shfl_xor_sync(kAll, c, 2);
   }
 #pragma unroll
-  for (int i = 0; i < 5; ++i) v[i] = __shfl_sync(kAll, c, 4 * i);
+  for (int i = 0; i < 6; ++i) v[i] = __shfl_sync(kAll, c, 4 * i);
+}
+template <typename T, int K>
+__device__ __forceinline__ float squares(const uint4 (&y)[K], const int (&at)[K], int C) {
+  F2 s = both(0.f);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (at[k] >= C) continue;
+    const Vec<kCh<T>> v = widen<T>(y[k]);
+#pragma unroll
+    for (int e = 0; e < kCh<T> / 2; ++e) s = fma(v.p[e], v.p[e], s);
+  }
+  return sum(s);
 }
 
-// One row's vectors of a thread: k-th at channel 8 (threadIdx.x + k blockDim.x).
+// One row's vectors of a thread: the k-th is vector threadIdx.x + k blockDim.x. Up to 8 channels a thread the weights are kept.
 template <typename T, int K>
-__global__ void __launch_bounds__(kMaxThreads, K == 1 ? 2 : 1) block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
-  constexpr int kPart = sizeof(T) / 2;   // units of 8 channels
+__global__ void __launch_bounds__(kMaxThreads, K * kCh<T> <= 8 ? 2 : 1) block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
+  constexpr int n = kCh<T>;
+  constexpr bool kKeep = K * n <= 8;
   extern __shared__ __align__(16) uint4 dyn[];
-  __shared__ __align__(16) float red[2][16];
-  if (threadIdx.x < 32) red[threadIdx.x >> 4][threadIdx.x & 15] = 0.f;
+  __shared__ __align__(16) float red[3][2][16];
+  for (int i = threadIdx.x; i < 3 * 2 * 16; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
   __syncthreads();
   const int C = a.C;
   const float inv_c = 1.f / (float)C;
   int at[K];
 #pragma unroll
-  for (int k = 0; k < K; ++k) at[k] = 8 * (threadIdx.x + k * blockDim.x);
+  for (int k = 0; k < K; ++k) at[k] = n * (threadIdx.x + k * blockDim.x);
   // the next row to fetch, and the present one
   const T *y = static_cast<const T*>(a.y) + blockIdx.x * a.y_row, *gate = static_cast<const T*>(a.gate), *h = static_cast<const T*>(a.h) + (size_t)blockIdx.x * C;
   if (gate) gate += blockIdx.x * a.gate_row;
   const size_t y_step = (size_t)gridDim.x * a.y_row, gate_step = (size_t)gridDim.x * a.gate_row, step = (size_t)gridDim.x * C;
   T *h_out = static_cast<T*>(a.h_out) + (size_t)blockIdx.x * C, *n_out = static_cast<T*>(a.n_out) + (size_t)blockIdx.x * C;
   long long left = (a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x, to_fetch = left;
-  Ring ring{dyn + threadIdx.x, a.stages, 3 * K * kPart, 0};
+  Ring ring{dyn + threadIdx.x, a.stages, 3 * K, 0};
   auto ahead = [&] {
     y += y_step;
     if (gate) gate += gate_step;
@@ -212,9 +269,9 @@ __global__ void __launch_bounds__(kMaxThreads, K == 1 ? 2 : 1) block_norm_kernel
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         if (at[k] >= C) continue;
-        copy(ring, (3 * k) * kPart, y + at[k]);
-        if (gate) copy(ring, (3 * k + 1) * kPart, gate + at[k]);
-        copy(ring, (3 * k + 2) * kPart, h + at[k]);
+        copy(ring, 3 * k, y + at[k]);
+        if (gate) copy(ring, 3 * k + 1, gate + at[k]);
+        copy(ring, 3 * k + 2, h + at[k]);
       }
       ahead();
       --to_fetch;
@@ -223,75 +280,89 @@ __global__ void __launch_bounds__(kMaxThreads, K == 1 ? 2 : 1) block_norm_kernel
     ring.next();
   };
   for (int i = 0; i < a.stages; ++i) fetch();
-  Vec w_pre, w_z;   // (one vector a thread: kept)
-  if (K == 1 && at[0] < C) {
-    w_pre = weight8(a.pre_w, at[0]);
-    w_z = times(weight8(a.post_w, at[0]), weight8(a.scale, at[0]));
-  }
-  for (; left > 0; --left) {
-    Vec x[K], z[K], g[K];
-    ring.wait();
+  Vec<n> w_pre[K], w_z[K];
+  auto weigh = [&](int k) {
+    w_pre[k] = floats<n>(a.pre_w + at[k]);
+    w_z[k] = times(weights_at<n>(a.post_w, at[k]), weights_at<n>(a.scale, at[k]));
+  };
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (at[k] >= C) continue;
-      x[k] = widen(take(ring, (3 * k + 2) * kPart, h + at[k]));
-      z[k] = widen(take(ring, (3 * k) * kPart, y + at[k]));
-      if (gate) g[k] = widen(take(ring, (3 * k + 1) * kPart, gate + at[k]));
-    }
-    if (ring.stages) fetch();
-    else ahead();
-    float r = 1.f;
-    if (a.post_w) {
-      F2 s = both(0.f);
+  for (int k = 0; k < K; ++k)
+    if (kKeep && at[k] < C) weigh(k);
+  // the present row's y, and its root mean square
+  uint4 cy[K];
+  float r = 1.f;
+  auto take_y = [&] {
 #pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (at[k] < C)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s = fma(z[k].p[e], z[k].p[e], s);
-      r = rsqrtf(fmaf(block_sum(sum(s), red[0]), inv_c, a.eps));
-    }
+    for (int k = 0; k < K; ++k)
+      if (at[k] < C) cy[k] = take(ring, 3 * k, y + at[k]);
+  };
+  ring.wait();
+  take_y();
+  if (a.post_w) r = rsqrtf(fmaf(block_sum(squares<T>(cy, at, C), red[2][0]), inv_c, a.eps));
+  for (int turn = 0; left > 0; --left, turn ^= 1) {
+    Vec<n> x[K];
     F2 s = both(0.f);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (at[k] >= C) continue;
-      if (K > 1) w_z = times(weight8(a.post_w, at[k]), weight8(a.scale, at[k]));
+      if (!kKeep) weigh(k);
+      x[k] = widen<T>(take(ring, 3 * k + 2, h + at[k]));
+      const Vec<n> z = widen<T>(cy[k]);
+      Vec<n> g;
+      if (gate) g = widen<T>(take(ring, 3 * k + 1, gate + at[k]));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const F2 f = mul(mul(z[k].p[e], both(r)), w_z.p[e]);
-        x[k].p[e] = gate ? fma(f, sigmoid(g[k].p[e]), x[k].p[e]) : add(x[k].p[e], f);
+      for (int e = 0; e < n / 2; ++e) {
+        const F2 f = mul(mul(z.p[e], both(r)), w_z[k].p[e]);
+        x[k].p[e] = gate ? fma(f, sigmoid(g.p[e]), x[k].p[e]) : add(x[k].p[e], f);
         s = fma(x[k].p[e], x[k].p[e], s);
       }
       store(h_out + at[k], x[k]);
     }
-    r = rsqrtf(fmaf(block_sum(sum(s), red[1]), inv_c, a.eps));
+    if (ring.stages) fetch();
+    else ahead();
+    // the next row's y comes into the same exchange
+    float v[2] = {sum(s), 0.f};
+    if (left > 1) {
+      ring.wait();
+      take_y();
+      if (a.post_w) v[1] = squares<T>(cy, at, C);
+    }
+    if (a.post_w) {
+      block_sum(v, red[turn]);
+      r = rsqrtf(fmaf(v[1], inv_c, a.eps));
+    } else {
+      v[0] = block_sum(v[0], red[turn][0]);
+    }
+    const float q = rsqrtf(fmaf(v[0], inv_c, a.eps));
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (at[k] >= C) continue;
-      if (K > 1) w_pre = weight8(a.pre_w, at[k]);
+      if (!kKeep) weigh(k);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[k].p[e] = mul(mul(x[k].p[e], both(r)), w_pre.p[e]);
+      for (int e = 0; e < n / 2; ++e) x[k].p[e] = mul(mul(x[k].p[e], both(q)), w_pre[k].p[e]);
       store(n_out + at[k], x[k]);
     }
     h_out += step;
     n_out += step;
-    if (!a.post_w) __syncthreads();   // red[1] is written again before another barrier
   }
 }
 
-// The two sums over the rows of a thread's channels: in registers, or (more than one vector a thread) in shared
-// memory at the thread's own places.
-template <typename T, int K>
-__global__ void __launch_bounds__(kMaxThreads, 1) block_norm_backward_kernel(const __grid_constant__ BlockNormArgs a) {
-  constexpr int kPart = sizeof(T) / 2;
+// The two sums over the rows of a thread's channels: in registers, or (more than 8 channels a thread) in shared memory
+// at the thread's own places.
+template <typename T, int K, bool kWide>
+__global__ void __launch_bounds__(kWide ? kMaxThreads : kPairThreads, kWide ? 1 : 2) block_norm_backward_kernel(const __grid_constant__ BlockNormArgs a) {
+  constexpr int n = kCh<T>;
+  constexpr bool kKeep = K * n <= 8;
+  constexpr bool kF32 = sizeof(T) == 4;
   extern __shared__ __align__(16) uint4 dyn[];
-  __shared__ __align__(16) float red[2][8][16];
-  for (int i = threadIdx.x; i < 2 * 8 * 16; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
+  __shared__ __align__(16) float red[3][8][16];
+  for (int i = threadIdx.x; i < 3 * 8 * 16; i += blockDim.x) (&red[0][0][0])[i] = 0.f;
   __syncthreads();
   const int C = a.C;
   const float inv_c = 1.f / (float)C;
   int at[K];
 #pragma unroll
-  for (int k = 0; k < K; ++k) at[k] = 8 * (threadIdx.x + k * blockDim.x);
+  for (int k = 0; k < K; ++k) at[k] = n * (threadIdx.x + k * blockDim.x);
   const T *y = static_cast<const T*>(a.y) + blockIdx.x * a.y_row, *gate = static_cast<const T*>(a.gate);
   const T *h = static_cast<const T*>(a.h) + (size_t)blockIdx.x * C, *dn = static_cast<const T*>(a.dn) + (size_t)blockIdx.x * C;
   const float* dh_out = a.dh_out;
@@ -300,9 +371,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) block_norm_backward_kernel(con
   const size_t y_step = (size_t)gridDim.x * a.y_row, gate_step = (size_t)gridDim.x * a.gate_row, step = (size_t)gridDim.x * C;
   size_t out = (size_t)blockIdx.x * C;   // where the present row's outputs go
   long long left = (a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x, to_fetch = left;
-  constexpr int kVec = 4 * kPart + 2;    // units of a thread's vector: y, gate, h, dn, dh_out
-  Ring ring{dyn + threadIdx.x, a.stages, K * kVec, 0};
-  float* acc_sm = reinterpret_cast<float*>(dyn + (size_t)a.stages * K * kVec * blockDim.x);   // (K > 1) [2][C]
+  constexpr int kUnits = kF32 ? 5 : 6;   // of a thread's vector: y, gate, h, dn, dh_out
+  Ring ring{dyn + threadIdx.x, a.stages, K * kUnits, 0};
+  float* acc_sm = reinterpret_cast<float*>(dyn + (size_t)a.stages * K * kUnits * blockDim.x);   // (not kept) [2][C]
   auto ahead = [&] {
     y += y_step;
     if (gate) gate += gate_step;
@@ -311,15 +382,17 @@ __global__ void __launch_bounds__(kMaxThreads, 1) block_norm_backward_kernel(con
     if (dh_out) dh_out += step;
   };
   auto fetch = [&] {
+    if (!kF32) __syncwarp();   // (other lanes have read what is written over)
     if (to_fetch > 0) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
+        if (!kF32 && dh_out) copy_wide(ring, k * kUnits + 4, dh_out, at[k], C);
         if (at[k] >= C) continue;
-        copy(ring, k * kVec, y + at[k]);
-        if (gate) copy(ring, k * kVec + kPart, gate + at[k]);
-        copy(ring, k * kVec + 2 * kPart, h + at[k]);
-        copy(ring, k * kVec + 3 * kPart, dn + at[k]);
-        if (dh_out) copy(ring, k * kVec + 4 * kPart, dh_out + at[k]);
+        copy(ring, k * kUnits, y + at[k]);
+        if (gate) copy(ring, k * kUnits + 1, gate + at[k]);
+        copy(ring, k * kUnits + 2, h + at[k]);
+        copy(ring, k * kUnits + 3, dn + at[k]);
+        if (kF32 && dh_out) copy(ring, k * kUnits + 4, dh_out + at[k]);
       }
       ahead();
       --to_fetch;
@@ -327,61 +400,70 @@ __global__ void __launch_bounds__(kMaxThreads, 1) block_norm_backward_kernel(con
     ptx::cp_async_commit();
     ring.next();
   };
-  for (int i = 0; i < a.stages; ++i) fetch();
-  Vec w_pre, w_z, acc[2];
-  if (K == 1 && at[0] < C) {
-    w_pre = weight8(a.pre_w, at[0]);
-    w_z = times(weight8(a.post_w, at[0]), weight8(a.scale, at[0]));
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    acc[i] = filled(0.f);
-    if (K > 1)
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-        if (at[k] < C) store(acc_sm + i * C + at[k], acc[i]);
-  }
-  for (; left > 0; --left) {
-    Raw<T> cy[K], cn[K];   // y and dn stay as they are, and are widened where they are used
-    Vec x[K], g[K], dx[K];
+  auto arrived = [&] {
     ring.wait();
+    if (!kF32) __syncwarp();
+  };
+  for (int i = 0; i < a.stages; ++i) fetch();
+  Vec<n> w_pre[K], w_z[K], acc[2][K];
+  auto weigh = [&](int k) {
+    w_pre[k] = floats<n>(a.pre_w + at[k]);
+    w_z[k] = times(weights_at<n>(a.post_w, at[k]), weights_at<n>(a.scale, at[k]));
+  };
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    acc[0][k] = acc[1][k] = filled<n>(0.f);
+    if (at[k] >= C) continue;
+    if (kKeep) {
+      weigh(k);
+    } else {
+      store(acc_sm + at[k], acc[0][k]);
+      store(acc_sm + C + at[k], acc[1][k]);
+    }
+  }
+  // y and dn stay as they are, and are widened where they are used; the next row's y comes early, so that its mean
+  // square goes into the present row's exchange
+  uint4 cy[K], next_y[K];
+  float r = 1.f;
+  arrived();
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    if (at[k] < C) cy[k] = take(ring, k * kUnits, y + at[k]);
+  if (a.post_w) r = rsqrtf(fmaf(block_sum(squares<T>(cy, at, C), red[2][0]), inv_c, a.eps));
+  for (int turn = 0; left > 0; --left, turn ^= 1) {
+    uint4 cn[K];
+    Vec<n> x[K], g[K], dx[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (at[k] >= C) continue;
-      cy[k] = take(ring, k * kVec, y + at[k]);
-      cn[k] = take(ring, k * kVec + 3 * kPart, dn + at[k]);
-      x[k] = widen(take(ring, k * kVec + 2 * kPart, h + at[k]));
-      g[k] = gate ? widen(take(ring, k * kVec + kPart, gate + at[k])) : filled(1.f);
-      dx[k] = dh_out ? widen(take(ring, k * kVec + 4 * kPart, dh_out + at[k])) : filled(0.f);
+      cn[k] = take(ring, k * kUnits + 3, dn + at[k]);
+      x[k] = widen<T>(take(ring, k * kUnits + 2, h + at[k]));
+      g[k] = gate ? widen<T>(take(ring, k * kUnits + 1, gate + at[k])) : filled<n>(1.f);
+      if constexpr (kF32) dx[k] = dh_out ? widen<float>(take(ring, k * kUnits + 4, dh_out + at[k])) : filled<n>(0.f);
+      else dx[k] = dh_out ? take_wide(ring, k * kUnits + 4, dh_out + at[k]) : filled<n>(0.f);
     }
     if (ring.stages) fetch();
     else ahead();
-    float r = 1.f;
-    if (a.post_w) {
-      F2 s = both(0.f);
+    float s[6];
+    s[5] = 0.f;
+    if (left > 1) {
+      arrived();
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        if (at[k] >= C) continue;
-        const Vec v = widen(cy[k]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s = fma(v.p[e], v.p[e], s);
-      }
-      r = rsqrtf(fmaf(block_sum(sum(s), red[0][0]), inv_c, a.eps));
+      for (int k = 0; k < K; ++k)
+        if (at[k] < C) next_y[k] = take(ring, k * kUnits, y + at[k]);
+      if (a.post_w) s[5] = squares<T>(next_y, at, C);
     }
     // sums of x^2, pre_w dn x, p y dh_out, p y pre_w dn, p y x
     F2 t[5] = {both(0.f), both(0.f), both(0.f), both(0.f), both(0.f)};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       if (at[k] >= C) continue;
-      if (K > 1) {
-        w_z = times(weight8(a.post_w, at[k]), weight8(a.scale, at[k]));
-        w_pre = weight8(a.pre_w, at[k]);
-      }
-      const Vec v = widen(cy[k]), d = widen(cn[k]);
+      if (!kKeep) weigh(k);
+      const Vec<n> v = widen<T>(cy[k]), d = widen<T>(cn[k]);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < n / 2; ++e) {
         if (gate) g[k].p[e] = sigmoid(g[k].p[e]);
-        const F2 py = mul(mul(w_z.p[e], v.p[e]), g[k].p[e]), wdn = mul(w_pre.p[e], d.p[e]);
+        const F2 py = mul(mul(w_z[k].p[e], v.p[e]), g[k].p[e]), wdn = mul(w_pre[k].p[e], d.p[e]);
         x[k].p[e] = fma(py, both(r), x[k].p[e]);
         t[0] = fma(x[k].p[e], x[k].p[e], t[0]);
         t[1] = fma(wdn, x[k].p[e], t[1]);
@@ -390,61 +472,53 @@ __global__ void __launch_bounds__(kMaxThreads, 1) block_norm_backward_kernel(con
         t[4] = fma(py, x[k].p[e], t[4]);
       }
     }
-    float s[5];
 #pragma unroll
     for (int i = 0; i < 5; ++i) s[i] = sum(t[i]);
-    block_sum5(s, red[1]);
+    block_sum(s, red[turn]);
     const float q = rsqrtf(fmaf(s[0], inv_c, a.eps)), mx = s[1] * inv_c * q * q * q;
     const float my = a.post_w ? (s[2] + q * s[3] - mx * s[4]) * inv_c * r * r * r : 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (at[k] >= C) continue;
-      if (K > 1) {
-        w_z = times(weight8(a.post_w, at[k]), weight8(a.scale, at[k]));
-        w_pre = weight8(a.pre_w, at[k]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          Raw<float> v;
-          v.v[0] = reinterpret_cast<const uint4*>(acc_sm + i * C + at[k])[0];
-          v.v[1] = reinterpret_cast<const uint4*>(acc_sm + i * C + at[k])[1];
-          acc[i] = widen(v);
+      if (at[k] < C) {
+        if (!kKeep) {
+          weigh(k);
+          acc[0][k] = floats<n>(acc_sm + at[k]);
+          acc[1][k] = floats<n>(acc_sm + C + at[k]);
         }
-      }
-      const Vec d = widen(cn[k]), v = widen(cy[k]);
-      Vec dg, dy;
+        const Vec<n> d = widen<T>(cn[k]), v = widen<T>(cy[k]);
+        Vec<n> dg, dy;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        acc[0].p[e] = fma(d.p[e], mul(x[k].p[e], both(q)), acc[0].p[e]);
-        dx[k].p[e] = fma(mul(w_pre.p[e], d.p[e]), both(q), fma(x[k].p[e], both(-mx), dx[k].p[e]));
-        const F2 dxg = mul(dx[k].p[e], g[k].p[e]), b = mul(mul(dxg, both(r)), v.p[e]);   // dx g y r
-        acc[1].p[e] = add(acc[1].p[e], b);
-        const F2 bw = mul(b, w_z.p[e]);
-        dg.p[e] = sub(bw, mul(bw, g[k].p[e]));
-        dy.p[e] = fma(v.p[e], both(-my), mul(mul(dxg, both(r)), w_z.p[e]));
+        for (int e = 0; e < n / 2; ++e) {
+          acc[0][k].p[e] = fma(d.p[e], mul(x[k].p[e], both(q)), acc[0][k].p[e]);
+          dx[k].p[e] = fma(mul(w_pre[k].p[e], d.p[e]), both(q), fma(x[k].p[e], both(-mx), dx[k].p[e]));
+          const F2 dxg = mul(dx[k].p[e], g[k].p[e]), b = mul(mul(dxg, both(r)), v.p[e]);   // dx g y r
+          acc[1][k].p[e] = add(acc[1][k].p[e], b);
+          const F2 bw = mul(b, w_z[k].p[e]);
+          dg.p[e] = sub(bw, mul(bw, g[k].p[e]));
+          dy.p[e] = fma(v.p[e], both(-my), mul(mul(dxg, both(r)), w_z[k].p[e]));
+        }
+        if (gate) store(static_cast<T*>(a.dgate) + out + at[k], dg);
+        store(static_cast<T*>(a.dy) + out + at[k], dy);
+        if (!kKeep) {
+          store(acc_sm + at[k], acc[0][k]);
+          store(acc_sm + C + at[k], acc[1][k]);
+        }
+        if constexpr (kF32) store(a.dh + out + at[k], dx[k]);
       }
-      store(a.dh + out + at[k], dx[k]);
-      if (gate) store(static_cast<T*>(a.dgate) + out + at[k], dg);
-      store(static_cast<T*>(a.dy) + out + at[k], dy);
-      if (K > 1)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) store(acc_sm + i * C + at[k], acc[i]);
+      if constexpr (!kF32) store_wide(a.dh + out, dx[k], at[k], C);
     }
     out += step;
-    if (!a.post_w) __syncthreads();   // red[1] is written again before another barrier
+#pragma unroll
+    for (int k = 0; k < K; ++k) cy[k] = next_y[k];
+    if (a.post_w) r = rsqrtf(fmaf(s[5], inv_c, a.eps));
   }
   // the block's partial sums
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     if (at[k] >= C) continue;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float* to = a.partial + ((size_t)blockIdx.x * 2 + i) * C + at[k];
-      if (K == 1) {
-        store(to, acc[i]);
-      } else {
-        for (int j = 0; j < 2; ++j) reinterpret_cast<uint4*>(to)[j] = reinterpret_cast<const uint4*>(acc_sm + i * C + at[k])[j];
-      }
-    }
+    for (int i = 0; i < 2; ++i)
+      store(a.partial + ((size_t)blockIdx.x * 2 + i) * C + at[k], kKeep ? acc[i][k] : floats<n>(acc_sm + i * C + at[k]));
   }
 }
 
@@ -475,21 +549,29 @@ __global__ void __launch_bounds__(32 * kSumWarps) block_norm_sum_kernel(const __
   }
 }
 
-int threads_of(int C) { return std::min(kMaxThreads, (C / 8 + 31) / 32 * 32); }
-int vectors_of(int C) { return (C / 8 + kMaxThreads - 1) / kMaxThreads; }
-// Blocks of the gradient that a GPU holds: 512 threads an SM.
-int backward_blocks(int C) { return kNumSMs * std::min(16, kMaxThreads / threads_of(C)); }
-// Rows on their way to a block, of `per` on an SM: at most four, none where not even two fit.
+// Vectors of a row, of es bytes a channel: 1, 2, 4 or 8 a thread, for up to kMaxThreads threads (8 channels a thread while
+// that is enough).
+int vectors_of(int C, int es) {
+  int k = es / 2;
+  while (C * es / 16 > k * kMaxThreads) k *= 2;
+  return k;
+}
+int threads_of(int C, int es) { return (C * es / 16 + 32 * vectors_of(C, es) - 1) / (32 * vectors_of(C, es)) * 32; }
+// Blocks of the gradient that an SM holds.
+int backward_per(int C, int es) {
+  const int t = threads_of(C, es);
+  return t > kPairThreads || vectors_of(C, es) > es / 2 ? 1 : std::min(16, 2 * kPairThreads / t);
+}
+// Rows on their way to a block, of `per` on an SM: at most four.
 constexpr int kSmemSM = 220 << 10;
 int stages_of(int per, int bytes, int more) {
-  const int n = std::min(4, (std::min(kSmemSM / per, 224 << 10) - 2048 - more) / bytes);
-  return n < 2 ? 0 : n;
+  return std::max(0, std::min(4, (kSmemSM / per - 2048 - more) / bytes));
 }
 
 template <typename T, int K>
 cudaError_t forward(BlockNormArgs a, cudaStream_t s) {
-  const int t = threads_of(a.C), per = std::min(32, (K == 1 ? 2 : 1) * kMaxThreads / t);
-  const int bytes = 3 * K * (int)(sizeof(T) / 2) * t * 16;
+  const int t = threads_of(a.C, sizeof(T)), per = std::min(32, (K * kCh<T> <= 8 ? 2 : 1) * kMaxThreads / t);
+  const int bytes = 3 * K * t * 16;
   a.stages = stages_of(per, bytes, 0);
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(block_norm_kernel<T, K>), 224 << 10, done);
@@ -499,17 +581,17 @@ cudaError_t forward(BlockNormArgs a, cudaStream_t s) {
   stage_timer_end(slot, s);
   return cudaGetLastError();
 }
-template <typename T, int K>
+template <typename T, int K, bool kWide>
 cudaError_t backward(BlockNormArgs a, cudaStream_t s) {
-  const int t = threads_of(a.C), blocks = (int)std::min<long long>(a.rows, backward_blocks(a.C));
-  const int bytes = K * (4 * (int)(sizeof(T) / 2) + 2) * t * 16, more = K == 1 ? 0 : 2 * a.C * 4;
-  a.stages = stages_of(std::min(16, kMaxThreads / t), bytes, more);
+  const int t = threads_of(a.C, sizeof(T)), per = backward_per(a.C, sizeof(T)), blocks = (int)std::min<long long>(a.rows, kNumSMs * per);
+  const int bytes = K * (sizeof(T) == 4 ? 5 : 6) * t * 16, more = K * kCh<T> <= 8 ? 0 : 2 * a.C * 4;
+  a.stages = stages_of(per, bytes, more);
   const int smem = a.stages * bytes + more;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(block_norm_backward_kernel<T, K>), 224 << 10, done);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(block_norm_backward_kernel<T, K, kWide>), 224 << 10, done);
   if (e != cudaSuccess) return e;
   int slot = stage_timer_begin(s, kKernBlockNormBwd);
-  block_norm_backward_kernel<T, K><<<blocks, t, smem, s>>>(a);
+  block_norm_backward_kernel<T, K, kWide><<<blocks, t, smem, s>>>(a);
   stage_timer_end(slot, s);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   slot = stage_timer_begin(s, kKernBlockNormBwd);
@@ -529,17 +611,24 @@ cudaError_t backward(BlockNormArgs a, cudaStream_t s) {
 
 }  // namespace
 
-size_t block_norm_backward_workspace_bytes(int C) { return (size_t)backward_blocks(C) * 2 * C * sizeof(float); }
+size_t block_norm_backward_workspace_bytes(int C) {
+  return (size_t)kNumSMs * std::max(backward_per(C, 2), backward_per(C, 4)) * 2 * C * sizeof(float);
+}
 
 cudaError_t launch_block_norm(const BlockNormArgs& a, cudaStream_t s) {
-  const int K = vectors_of(a.C);
+  const int K = vectors_of(a.C, a.bf16 ? 2 : 4);
   if (a.bf16) return K == 1 ? forward<bf16, 1>(a, s) : K == 2 ? forward<bf16, 2>(a, s) : forward<bf16, 4>(a, s);
-  return K == 1 ? forward<float, 1>(a, s) : K == 2 ? forward<float, 2>(a, s) : forward<float, 4>(a, s);
+  return K == 2 ? forward<float, 2>(a, s) : K == 4 ? forward<float, 4>(a, s) : forward<float, 8>(a, s);
 }
 cudaError_t launch_block_norm_backward(const BlockNormArgs& a, cudaStream_t s) {
-  const int K = vectors_of(a.C);
-  if (a.bf16) return K == 1 ? backward<bf16, 1>(a, s) : K == 2 ? backward<bf16, 2>(a, s) : backward<bf16, 4>(a, s);
-  return K == 1 ? backward<float, 1>(a, s) : K == 2 ? backward<float, 2>(a, s) : backward<float, 4>(a, s);
+  const int es = a.bf16 ? 2 : 4, K = vectors_of(a.C, es);
+  const bool pair = backward_per(a.C, es) > 1;
+  if (a.bf16) {
+    if (K == 1) return pair ? backward<bf16, 1, false>(a, s) : backward<bf16, 1, true>(a, s);
+    return K == 2 ? backward<bf16, 2, true>(a, s) : backward<bf16, 4, true>(a, s);
+  }
+  if (K == 2) return pair ? backward<float, 2, false>(a, s) : backward<float, 2, true>(a, s);
+  return K == 4 ? backward<float, 4, true>(a, s) : backward<float, 8, true>(a, s);
 }
 
 }  // namespace gdr
