@@ -126,32 +126,48 @@ __device__ __forceinline__ F2 sigmoid(F2 x) {
 // unit copied (asynchronously) and read by the same thread, so that rows on their way cost neither registers nor
 // barriers. Without stages (a row does not fit) a row is read when it is needed.
 struct Ring {
-  uint4* mine;      // unit u of stage s at (s parts + u) blockDim.x
-  int stages, parts, slot;
-  __device__ __forceinline__ uint4* at(int u) const { return mine + (slot * parts + u) * blockDim.x; }
+  uint32_t base, at, end, row, unit;   // shared addresses of this thread's first unit: of the ring, the present row; bytes of a row and of a unit
+  int stages;
+  __device__ __forceinline__ Ring(void* sm, int stages, int parts)
+      : base(ptx::smem_u32(sm) + threadIdx.x * 16), at(base), row(parts * blockDim.x * 16), unit(blockDim.x * 16), stages(stages) {
+    end = base + stages * row;
+  }
   __device__ __forceinline__ void wait() const {   // for the oldest row
     if (stages >= 4) ptx::cp_async_wait<3>();
     else if (stages == 3) ptx::cp_async_wait<2>();
     else if (stages == 2) ptx::cp_async_wait<1>();
     else if (stages == 1) ptx::cp_async_wait<0>();
   }
-  __device__ __forceinline__ void next() { slot = slot + 1 == stages ? 0 : slot + 1; }
+  __device__ __forceinline__ void next() {
+    at += row;
+    if (at == end) at = base;
+  }
 };
-__device__ __forceinline__ void copy(const Ring& g, int u, const void* p) { ptx::cp_async16_zfill(g.at(u), p, 16); }
-__device__ __forceinline__ uint4 take(const Ring& g, int u, const void* p) { return g.stages ? *g.at(u) : load(p); }
+__device__ __forceinline__ void copy16(uint32_t to, const void* p) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p) : "memory");
+}
+__device__ __forceinline__ uint4 shared16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void copy(const Ring& g, int u, const void* p) { copy16(g.at + u * g.unit, p); }
+__device__ __forceinline__ uint4 take(const Ring& g, int u, const void* p) { return g.stages ? shared16(g.at + u * g.unit) : load(p); }
 
 // float32 channels of a kernel whose threads own 8 of them (32 bytes): a warp's 1024 bytes are copied 16 bytes a lane in
 // order (a lane's own 32 bytes would be two half sectors), so lanes read what others copied.
 __device__ __forceinline__ void copy_wide(const Ring& g, int u, const float* row, int c, int C) {   // c: the thread's first channel
   const int lane = threadIdx.x & 31, c0 = c - 8 * lane + 4 * lane;
-  uint4* to = g.at(u) - threadIdx.x + 2 * (threadIdx.x - lane) + lane;
+  const uint32_t to = g.at + u * g.unit + 16 * (threadIdx.x - lane);
 #pragma unroll
   for (int j = 0; j < 2; ++j)
-    if (c0 + 128 * j < C) ptx::cp_async16_zfill(to + 32 * j, row + c0 + 128 * j, 16);
+    if (c0 + 128 * j < C) copy16(to + 512 * j, row + c0 + 128 * j);
 }
 __device__ __forceinline__ Vec<8> take_wide(const Ring& g, int u, const float* p) {
   if (!g.stages) return floats<8>(p);
-  return floats<8>(reinterpret_cast<const float*>(g.at(u) + threadIdx.x));
+  const uint32_t at = g.at + u * g.unit + 16 * threadIdx.x;
+  const Vec<4> a = widen<float>(shared16(at)), b = widen<float>(shared16(at + 16));
+  return {a.p[0], a.p[1], b.p[0], b.p[1]};
 }
 // The same for a store: two lanes exchange halves and write 32 bytes together. Every lane of the warp calls.
 __device__ __forceinline__ void store_wide(float* row, const Vec<8>& x, int c, int C) {
@@ -258,7 +274,7 @@ __global__ void __launch_bounds__(kMaxThreads, K * kCh<T> <= 8 ? 2 : 1) block_no
   const size_t y_step = (size_t)gridDim.x * a.y_row, gate_step = (size_t)gridDim.x * a.gate_row, step = (size_t)gridDim.x * C;
   T *h_out = static_cast<T*>(a.h_out) + (size_t)blockIdx.x * C, *n_out = static_cast<T*>(a.n_out) + (size_t)blockIdx.x * C;
   long long left = (a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x, to_fetch = left;
-  Ring ring{dyn + threadIdx.x, a.stages, 3 * K, 0};
+  Ring ring(dyn, a.stages, 3 * K);
   auto ahead = [&] {
     y += y_step;
     if (gate) gate += gate_step;
@@ -310,10 +326,15 @@ __global__ void __launch_bounds__(kMaxThreads, K * kCh<T> <= 8 ? 2 : 1) block_no
       const Vec<n> z = widen<T>(cy[k]);
       Vec<n> g;
       if (gate) g = widen<T>(take(ring, 3 * k + 1, gate + at[k]));
+      if (gate) {
+#pragma unroll
+        for (int e = 0; e < n / 2; ++e) g.p[e] = sigmoid(g.p[e]);
+      } else {
+        g = filled<n>(1.f);
+      }
 #pragma unroll
       for (int e = 0; e < n / 2; ++e) {
-        const F2 f = mul(mul(z.p[e], both(r)), w_z[k].p[e]);
-        x[k].p[e] = gate ? fma(f, sigmoid(g.p[e]), x[k].p[e]) : add(x[k].p[e], f);
+        x[k].p[e] = fma(mul(mul(z.p[e], both(r)), w_z[k].p[e]), g.p[e], x[k].p[e]);
         s = fma(x[k].p[e], x[k].p[e], s);
       }
       store(h_out + at[k], x[k]);
@@ -372,7 +393,7 @@ __global__ void __launch_bounds__(kWide ? kMaxThreads : kPairThreads, kWide ? 1 
   size_t out = (size_t)blockIdx.x * C;   // where the present row's outputs go
   long long left = (a.rows - blockIdx.x + gridDim.x - 1) / gridDim.x, to_fetch = left;
   constexpr int kUnits = kF32 ? 5 : 6;   // of a thread's vector: y, gate, h, dn, dh_out
-  Ring ring{dyn + threadIdx.x, a.stages, K * kUnits, 0};
+  Ring ring(dyn, a.stages, K * kUnits);
   float* acc_sm = reinterpret_cast<float*>(dyn + (size_t)a.stages * K * kUnits * blockDim.x);   // (not kept) [2][C]
   auto ahead = [&] {
     y += y_step;
@@ -438,7 +459,12 @@ __global__ void __launch_bounds__(kWide ? kMaxThreads : kPairThreads, kWide ? 1 
       if (at[k] >= C) continue;
       cn[k] = take(ring, k * kUnits + 3, dn + at[k]);
       x[k] = widen<T>(take(ring, k * kUnits + 2, h + at[k]));
-      g[k] = gate ? widen<T>(take(ring, k * kUnits + 1, gate + at[k])) : filled<n>(1.f);
+      g[k] = filled<n>(1.f);
+      if (gate) {
+        g[k] = widen<T>(take(ring, k * kUnits + 1, gate + at[k]));
+#pragma unroll
+        for (int e = 0; e < n / 2; ++e) g[k].p[e] = sigmoid(g[k].p[e]);
+      }
       if constexpr (kF32) dx[k] = dh_out ? widen<float>(take(ring, k * kUnits + 4, dh_out + at[k])) : filled<n>(0.f);
       else dx[k] = dh_out ? take_wide(ring, k * kUnits + 4, dh_out + at[k]) : filled<n>(0.f);
     }
@@ -462,7 +488,6 @@ __global__ void __launch_bounds__(kWide ? kMaxThreads : kPairThreads, kWide ? 1 
       const Vec<n> v = widen<T>(cy[k]), d = widen<T>(cn[k]);
 #pragma unroll
       for (int e = 0; e < n / 2; ++e) {
-        if (gate) g[k].p[e] = sigmoid(g[k].p[e]);
         const F2 py = mul(mul(w_z[k].p[e], v.p[e]), g[k].p[e]), wdn = mul(w_pre[k].p[e], d.p[e]);
         x[k].p[e] = fma(py, both(r), x[k].p[e]);
         t[0] = fma(x[k].p[e], x[k].p[e], t[0]);
