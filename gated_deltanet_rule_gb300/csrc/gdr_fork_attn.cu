@@ -23,6 +23,7 @@ namespace gdr {
 namespace {
 
 constexpr int kOwnThreads = 128, kOwnWarps = 4;
+constexpr int kOwnPages = 128;   // a row's first own pages, looked up ahead
 
 struct OwnArgs {
   const __nv_bfloat16 *q, *k_pages, *v_pages;
@@ -73,34 +74,31 @@ __global__ void __launch_bounds__(kOwnThreads) fork_own_kernel(const __grid_cons
   using C = Own<D, WR>;
   constexpr int KT = C::KT, PW = C::PW, NS = C::NS, WK = C::WK, kRows = C::kRows;
   extern __shared__ __align__(1024) uint8_t sm[];
-  __shared__ int s_group, s_bad;
+  __shared__ int s_group, s_shared, s_bad, s_page[kOwnPages];
   __shared__ float s_m[kOwnWarps][16], s_l[kOwnWarps][16];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / a.Hk, hk = blockIdx.x - b * a.Hk, r0 = blockIdx.y * kRows;
 
-  // the row's group and its numbers
+  // the row's group and its numbers: everything asked for at once
   if (tid == 0) {
     s_group = -1;
     s_bad = 0;
   }
+  int n = a.lengths ? __ldg(a.lengths + b) : a.N;
+  const int ctx = __ldg(a.ctx + b);
   __syncthreads();
   bool falls = false;
   for (int t = tid; t < a.T; t += kOwnThreads) {
-    const int f0 = __ldg(a.first + t), f1 = __ldg(a.first + t + 1);
+    const int f0 = __ldg(a.first + t), f1 = __ldg(a.first + t + 1), sh = __ldg(a.shared + t);
     falls |= f0 > f1;
-    if (f0 <= b && b < f1) s_group = t;
+    if (f0 <= b && b < f1) {
+      s_group = group_valid(f0, f1, sh, a.B, a.page, a.M) ? t : -2;
+      s_shared = sh;
+    }
   }
   const bool any_falls = __syncthreads_or(falls);
-  const int t = s_group;
-  int n = a.lengths ? __ldg(a.lengths + b) : a.N;
-  const int ctx = __ldg(a.ctx + b);
-  int shared = 0;
-  bool valid = !any_falls;
-  if (valid && t >= 0) {
-    shared = __ldg(a.shared + t);
-    valid = group_valid(__ldg(a.first + t), __ldg(a.first + t + 1), shared, a.B, a.page, a.M);
-  }
-  valid = valid && n >= 0 && n <= a.N && ctx >= shared && (long long)ctx + n <= (long long)a.M * a.page;
+  const int shared = s_group >= 0 ? s_shared : 0;
+  const bool valid = !any_falls && s_group != -2 && n >= 0 && n <= a.N && ctx >= shared && (long long)ctx + n <= (long long)a.M * a.page;
   if (!valid) {
     if (tid == 0) atomicCAS(a.err, 0, kErrDeviceIndex);
     n = 0;
@@ -114,21 +112,25 @@ __global__ void __launch_bounds__(kOwnThreads) fork_own_kernel(const __grid_cons
 
   // ------------------------------------------------------------------------------------ loads
   const size_t step = (size_t)a.Hk * D;          // elements of a position
+  auto lookup = [&](int m) {                     // page m of the own part (-1: read as zeros, and reported)
+    const int pg = __ldg(table + m);
+    if ((unsigned)pg < (unsigned)a.P) return pg;
+    atomicCAS(a.err, 0, kErrDeviceIndex);
+    return -1;
+  };
+  for (int m = tid; m < kOwnPages; m += kOwnThreads)
+    if ((long long)m << a.page_shift < L) s_page[m] = lookup(m);
+  constexpr int kChunks = D / 8, kLoads = KT * kChunks / kOwnThreads;   // 16-byte units of a position; a thread's of a tile
+  const int ch = tid % kChunks, row0 = tid / kChunks;
+  const size_t mine = (size_t)hk * D + ch * 8;
   auto load = [&](int tile) {
     uint8_t* to = sm + C::kRing + (tile % NS) * 2 * C::kTile;
-    for (int x = tid; x < KT * (D / 8); x += kOwnThreads) {
-      const int r = x / (D / 8), ch = x % (D / 8), p = tile * KT + r;
-      int pg = -1;
-      if (p < L) {
-        pg = __ldg(table + (p >> a.page_shift));
-        if ((unsigned)pg >= (unsigned)a.P) {
-          pg = -1;
-          if (ch == 0) atomicCAS(a.err, 0, kErrDeviceIndex);   // read as zeros
-        }
-      }
-      const size_t at = pg < 0 ? 0 : ((size_t)pg * a.page + (p & (a.page - 1))) * step + (size_t)hk * D + ch * 8;
-      const uint32_t bytes = pg < 0 ? 0u : 16u;
-      const uint32_t off = unit_at<D>(r, ch);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int r = row0 + i * (kOwnThreads / kChunks), p = tile * KT + r, m = p >> a.page_shift;
+      const int pg = p >= L ? -1 : m < kOwnPages ? s_page[m] : lookup(m);
+      const size_t at = pg < 0 ? 0 : ((size_t)pg * a.page + (p & (a.page - 1))) * step + mine;
+      const uint32_t bytes = pg < 0 ? 0u : 16u, off = unit_at<D>(r, ch);
       cp_async16_zfill(to + off, a.k_pages + at, bytes);
       cp_async16_zfill(to + C::kTile + off, a.v_pages + at, bytes);
     }
@@ -139,6 +141,7 @@ __global__ void __launch_bounds__(kOwnThreads) fork_own_kernel(const __grid_cons
     const size_t at = there ? (((size_t)b * a.N + node) * a.Hq + hk * a.G + g) * D + ch * 8 : 0;
     cp_async16_zfill(sm + unit_at<D>(r, ch), a.q + at, there ? 16u : 0u);
   }
+  __syncthreads();
 #pragma unroll
   for (int s = 0; s < NS - 1; ++s) {
     if (s < tiles) load(s);
@@ -287,73 +290,100 @@ __global__ void __launch_bounds__(kOwnThreads) fork_own_kernel(const __grid_cons
   __syncthreads();
 
   // ------------------------------------------------------------------------------------ results: a warp a row
-  constexpr int kVec = D / 32;
-  for (int r = warp; r < rows; r += kOwnWarps) {
-    const int nd = (r0 + r) / a.G, g = (r0 + r) - nd * a.G;
-    const size_t orow = ((size_t)b * a.N + nd) * a.Hq + hk * a.G + g;
-    float y[kVec], lse = -INFINITY;
+  // (the shared part's results are asked for four rows at a time)
+  constexpr int kVec = D / 32, kAhead = WR == 1 ? 2 : 4;
+  const bool joins = shared > 0;
+  for (int rb = warp; rb < rows; rb += kAhead * kOwnWarps) {
+    float x[kAhead][kVec], lse_s[kAhead];
+    auto orow_of = [&](int r) {
+      const int nd = (r0 + r) / a.G, g = (r0 + r) - nd * a.G;
+      return ((size_t)b * a.N + nd) * a.Hq + hk * a.G + g;
+    };
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) y[e] = 0.f;
-    if (r < used) {
-      const int w0 = (r >> 4) * WK, rr = r & 15;
-      float top = s_m[w0][rr];
+    for (int u = 0; u < kAhead; ++u) {
+      const int r = rb + u * kOwnWarps;
+      lse_s[u] = -INFINITY;
 #pragma unroll
-      for (int w = 1; w < WK; ++w) top = fmaxf(top, s_m[w0 + w][rr]);
-      float sum = 0.f;
+      for (int e = 0; e < kVec; ++e) x[u][e] = 0.f;
+      if (r >= used || !joins) continue;
+      const size_t orow = orow_of(r);
+      lse_s[u] = __ldcg(a.dense_lse + orow);
 #pragma unroll
-      for (int w = 0; w < WK; ++w) {
-        const float mw = s_m[w0 + w][rr], f = mw == top ? 1.f : ex2_approx(mw - top);
-        sum += f * s_l[w0 + w][rr];
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          const float x = acc[((w0 + w) * 16 + rr) * D + lane * kVec + e];
-          if (f != 0.f) y[e] = fmaf(f, x, y[e]);
-          else if (mw != -INFINITY && !(fabsf(x) < INFINITY)) y[e] += x;   // an infinity that was seen counts
-        }
-      }
-      const bool sees = sum > 0.f || sum != sum;
-      lse = sees ? top * (1.f / kLog2e) + logf(sum) : -INFINITY;
-      const float inv = sees ? 1.f / sum : 0.f;
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) y[e] = sees ? y[e] * inv : 0.f;
-      if (s_bad) {   // elements that were cleaned away, of the nodes that this one sees
-        const uint64_t* wd = a.mask ? a.mask + ((size_t)b * a.N + nd) * a.W : nullptr;
-        for (int j = 0; j < n; ++j) {
-          if (wd ? !(wd[j >> 6] >> (j & 63) & 1) : j > nd) continue;
-          const int p = own + j, pg = __ldg(table + (p >> a.page_shift));
-          if ((unsigned)pg >= (unsigned)a.P) continue;
-          const __nv_bfloat16* v = a.v_pages + ((size_t)pg * a.page + (p & (a.page - 1))) * step + (size_t)hk * D + lane * kVec;
-          for (int e = 0; e < kVec; ++e) {
-            const float x = __bfloat162float(v[e]);
-            if (!(fabsf(x) < INFINITY)) y[e] += x;
-          }
-        }
-      }
-      if (shared > 0) {
-        const float lse_s = __ldcg(a.dense_lse + orow), ref = fmaxf(lse, lse_s);
-        float f[2] = {1.f, 0.f};   // the own part's weight, the shared part's
-        if (lse != lse || lse_s != lse_s) {
-          f[0] = f[1] = NAN;
-        } else if (ref > -INFINITY) {
-          f[0] = lse == ref ? 1.f : ex2_approx((lse - ref) * kLog2e);
-          f[1] = lse_s == ref ? 1.f : ex2_approx((lse_s - ref) * kLog2e);
-        }
-        const float total = f[0] + f[1], inv2 = 1.f / total;
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-          const float x = __ldcg(a.dense_o + orow * D + lane * kVec + e);
-          float z = f[0] != 0.f ? f[0] * y[e] : lse != -INFINITY && !(fabsf(y[e]) < INFINITY) ? y[e] : 0.f;
-          if (f[1] != 0.f) z = fmaf(f[1], x, z);
-          else if (lse_s != -INFINITY && !(fabsf(x) < INFINITY)) z += x;
-          y[e] = z * inv2;
-        }
-        lse = ref == -INFINITY && total == total ? -INFINITY : ref + logf(total);
+      for (int e = 0; e < kVec; e += 2) {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(a.dense_o + orow * D + lane * kVec + e));
+        x[u][e] = v.x;
+        x[u][e + 1] = v.y;
       }
     }
-    __nv_bfloat16* out = a.o + orow * D + lane * kVec;
 #pragma unroll
-    for (int e = 0; e < kVec; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(y[e], y[e + 1]);
-    if (lane == 0 && a.lse) a.lse[orow] = lse;
+    for (int u = 0; u < kAhead; ++u) {
+      const int r = rb + u * kOwnWarps;
+      if (r >= rows) break;
+      const size_t orow = orow_of(r);
+      float y[kVec], lse = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) y[e] = 0.f;
+      if (r < used) {
+        const int w0 = (r >> 4) * WK, rr = r & 15;
+        float top = s_m[w0][rr];
+#pragma unroll
+        for (int w = 1; w < WK; ++w) top = fmaxf(top, s_m[w0 + w][rr]);
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < WK; ++w) {
+          const float mw = s_m[w0 + w][rr], f = mw == top ? 1.f : ex2_approx(mw - top);
+          sum += f * s_l[w0 + w][rr];
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) {
+            const float z = acc[((w0 + w) * 16 + rr) * D + lane * kVec + e];
+            if (f != 0.f) y[e] = fmaf(f, z, y[e]);
+            else if (mw != -INFINITY && !(fabsf(z) < INFINITY)) y[e] += z;   // an infinity that was seen counts
+          }
+        }
+        const bool sees = sum > 0.f || sum != sum;
+        lse = sees ? top * (1.f / kLog2e) + logf(sum) : -INFINITY;
+        const float inv = sees ? 1.f / sum : 0.f;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) y[e] = sees ? y[e] * inv : 0.f;
+        if (s_bad) {   // elements that were cleaned away, of the nodes that this one sees
+          const int nd = (r0 + r) / a.G;
+          const uint64_t* wd = a.mask ? a.mask + ((size_t)b * a.N + nd) * a.W : nullptr;
+          for (int j = 0; j < n; ++j) {
+            if (wd ? !(wd[j >> 6] >> (j & 63) & 1) : j > nd) continue;
+            const int p = own + j, pg = __ldg(table + (p >> a.page_shift));
+            if ((unsigned)pg >= (unsigned)a.P) continue;
+            const __nv_bfloat16* v = a.v_pages + ((size_t)pg * a.page + (p & (a.page - 1))) * step + (size_t)hk * D + lane * kVec;
+            for (int e = 0; e < kVec; ++e) {
+              const float z = __bfloat162float(v[e]);
+              if (!(fabsf(z) < INFINITY)) y[e] += z;
+            }
+          }
+        }
+        if (joins) {
+          const float ref = fmaxf(lse, lse_s[u]);
+          float f[2] = {1.f, 0.f};   // the own part's weight, the shared part's
+          if (lse != lse || lse_s[u] != lse_s[u]) {
+            f[0] = f[1] = NAN;
+          } else if (ref > -INFINITY) {
+            f[0] = lse == ref ? 1.f : ex2_approx((lse - ref) * kLog2e);
+            f[1] = lse_s[u] == ref ? 1.f : ex2_approx((lse_s[u] - ref) * kLog2e);
+          }
+          const float total = f[0] + f[1], inv2 = 1.f / total;
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) {
+            float z = f[0] != 0.f ? f[0] * y[e] : lse != -INFINITY && !(fabsf(y[e]) < INFINITY) ? y[e] : 0.f;
+            if (f[1] != 0.f) z = fmaf(f[1], x[u][e], z);
+            else if (lse_s[u] != -INFINITY && !(fabsf(x[u][e]) < INFINITY)) z += x[u][e];
+            y[e] = z * inv2;
+          }
+          lse = ref == -INFINITY && total == total ? -INFINITY : ref + logf(total);
+        }
+      }
+      __nv_bfloat16* out = a.o + orow * D + lane * kVec;
+#pragma unroll
+      for (int e = 0; e < kVec; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(y[e], y[e + 1]);
+      if (lane == 0 && a.lse) a.lse[orow] = lse;
+    }
   }
 }
 
