@@ -9,11 +9,13 @@
 // groups in the place of rows). From about 280 query rows a key head on it is bound by the products, below by HBM.
 //
 // The own part: a key head of a row has few queries (nodes times heads a key head) over keys that nobody
-// else reads, so it is bound by reading them. A block of four warps takes up to 16, 32 or 64 query rows and the
-// row's positions tile by tile (asynchronous copies, several tiles ahead); each warp multiplies 16 rows by 16 or
-// 32 positions with warp-level matrix instructions, which a 128-row tcgen05 tile would fill to a sixteenth or
-// less: starting and draining such an item takes 4 us of an SM, against 2 us for its reading. Warps that share rows
-// take positions in turn and are joined at the end, in order; then the block joins the shared part's result.
+// else reads, so it is bound by reading them. An item is a row, a key head and up to 16, 32 or 64 of its query rows; a
+// block takes items one after the other, two blocks an SM. One warp looks the items up and loads (queries, and tiles of
+// the row's positions as TMA boxes of its pages, several tiles and up to two items ahead), four warps compute: each
+// multiplies 16 query rows by 16 or 32 positions with warp-level matrix instructions, which a 128-row tcgen05 tile
+// would fill to a sixteenth or less (starting and draining such an item takes 4 us of an SM, against 2 us for its
+// reading). Warps that share rows take positions in turn and are joined at the end, in order; then the shared part's
+// result is joined.
 //
 // Weights are rounded to bfloat16 for their product with v, the sum adds them unrounded; scores, sums and parts are
 // float32.
@@ -22,8 +24,8 @@
 namespace gdr {
 namespace {
 
-constexpr int kOwnThreads = 128, kOwnWarps = 4;
-constexpr int kOwnPages = 128;   // a row's first own pages, looked up ahead
+constexpr int kOwnWarps = 4, kOwnThreads = 32 * (kOwnWarps + 1);   // the last warp loads
+constexpr int kOwnBar = 1;   // named barrier of the computing warps (and the next)
 
 struct OwnArgs {
   const __nv_bfloat16 *q, *k_pages, *v_pages;
@@ -34,10 +36,13 @@ struct OwnArgs {
   float* lse;
   const float *dense_o, *dense_lse;
   int B, N, Hq, Hk, G, W, P, page, page_shift, M, T;
+  int npt, heads, splits;    // an item's nodes and heads a node; items that a node's heads of a key head take
+  int m_tiles;               // items of a row and key head
+  long long budget;
   int* err;
 };
 
-// Query rows of a block (16 a warp, WR of the four warps), positions of a tile, and tiles on their way.
+// Query rows of an item (16 a warp, WR of the four warps), positions of a tile, and tiles on their way.
 template <int D, int WR>
 struct Own {
   static constexpr int WK = kOwnWarps / WR;                  // warps that share the positions of a tile
@@ -45,17 +50,28 @@ struct Own {
   static constexpr int PW = KT / WK;                         // a warp's positions
   static constexpr int kRows = 16 * WR;
   static constexpr int kTile = KT * D * 2;                   // bytes of K or V
-  static constexpr int NS = D == 256 && WR == 1 ? 2 : D == 64 ? 4 : 3;
   static constexpr int kQ = kRows * D * 2;
-  static constexpr int kRing = kQ;
-  static constexpr int kStages = NS * 2 * kTile;
-  static constexpr int kOut = kOwnWarps * 16 * D * 4;        // accumulators, in the ring's place at the end
-  static constexpr int kSmem = kRing + (kStages > kOut ? kStages : kOut);
+  static constexpr int kAcc = kOwnWarps * 16 * D * 4;        // accumulators at the end of an item
+  static constexpr int kFit = ((D == 256 ? 216 : 108) * 1024 - 2 * kQ - kAcc) / (2 * kTile);   // one or two blocks an SM
+  static constexpr int NS = kFit > 4 ? 4 : kFit;
+  static constexpr int kRing = 2 * kQ, kOut = kRing + NS * 2 * kTile;
+  static constexpr int kSmem = kOut + kAcc;
+  static_assert(NS >= 2, "a tile is loaded while another is computed");
+};
+// What the loading warp tells the computing ones of an item.
+struct Item {
+  int b, hk, node0, h0, n, own, shared, tiles;
+  int rows, used;   // query rows, and those of them whose nodes are there
+};
+struct OwnBars {
+  uint64_t full[4], empty[4], item_full[2], item_empty[2];
+  Item item[2];
 };
 
-// 16-byte unit ch of row r in rows of D bfloat16, swizzled so that eight rows' units lie in all banks.
-template <int D>
-__device__ __forceinline__ uint32_t unit_at(int r, int ch) { return (uint32_t)(r * (D * 2) + ((ch ^ (r & 7)) << 4)); }
+// 16-byte unit ch of row r in tiles of `rows` rows, 64 columns (128 bytes) at a time, swizzled as TMA writes them.
+__device__ __forceinline__ uint32_t unit_at(int rows, int r, int ch) {
+  return (uint32_t)((ch >> 3) * rows * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+}
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -69,322 +85,463 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The row's group and its numbers (a whole warp; every lane gets the item). falls: `first` is not rising.
 template <int D, int WR>
-__global__ void __launch_bounds__(kOwnThreads) fork_own_kernel(const __grid_constant__ OwnArgs a) {
+__device__ __forceinline__ Item item_of(const OwnArgs& a, long long at, bool falls) {
+  using C = Own<D, WR>;
+  const int lane = threadIdx.x & 31;
+  Item t;
+  const int mt = (int)(at % a.m_tiles), row = (int)(at / a.m_tiles);
+  t.b = row / a.Hk;
+  t.hk = row - t.b * a.Hk;
+  t.node0 = mt / a.splits * a.npt;
+  t.h0 = mt % a.splits * a.heads;
+  t.n = a.lengths ? __ldg(a.lengths + t.b) : a.N;
+  const int ctx = __ldg(a.ctx + t.b);
+  t.shared = 0;
+  bool valid = !falls;
+  for (int g0 = 0; g0 < a.T; g0 += 32) {
+    const int g = g0 + lane;
+    int f0 = 0, f1 = 0, sh = 0;
+    if (g < a.T) {
+      f0 = __ldg(a.first + g);
+      f1 = __ldg(a.first + g + 1);
+      sh = __ldg(a.shared + g);
+    }
+    const unsigned mine = __ballot_sync(0xffffffffu, f0 <= t.b && t.b < f1);
+    if (!mine) continue;
+    const int who = __ffs(mine) - 1;
+    valid = valid && __shfl_sync(0xffffffffu, (int)group_valid(f0, f1, sh, a.B, a.page, a.M), who);
+    t.shared = __shfl_sync(0xffffffffu, sh, who);
+    break;
+  }
+  valid = valid && t.n >= 0 && t.n <= a.N && ctx >= t.shared && (long long)ctx + t.n <= (long long)a.M * a.page;
+  if (!valid) {
+    if (lane == 0) atomicCAS(a.err, 0, kErrDeviceIndex);
+    t.n = 0;
+    t.shared = 0;
+  }
+  t.own = ctx - t.shared;
+  const int heads = min(a.heads, a.G - t.h0), nodes = max(0, min(a.npt, t.n - t.node0));
+  t.rows = min(a.npt, a.N - t.node0) * heads;
+  t.used = nodes * heads;
+  // positions of the own part, a node from `own` on; a chain's item needs none past its last node
+  const int L = nodes == 0 ? 0 : t.own + (a.mask ? t.n : t.node0 + nodes);
+  t.tiles = (L + C::KT - 1) / C::KT;
+  return t;
+}
+
+template <int D, int WR>
+__global__ void __launch_bounds__(kOwnThreads, D == 256 ? 1 : 2)
+    fork_own_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const __grid_constant__ OwnArgs a) {
   using C = Own<D, WR>;
   constexpr int KT = C::KT, PW = C::PW, NS = C::NS, WK = C::WK, kRows = C::kRows;
   extern __shared__ __align__(1024) uint8_t sm[];
-  __shared__ int s_group, s_shared, s_bad, s_page[kOwnPages];
+  __shared__ OwnBars s;
   __shared__ float s_m[kOwnWarps][16], s_l[kOwnWarps][16];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int b = blockIdx.x / a.Hk, hk = blockIdx.x - b * a.Hk, r0 = blockIdx.y * kRows;
-
-  // the row's group and its numbers: everything asked for at once
+  __shared__ int s_bad;   // (the last item in which V of a node was cleaned of something)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  if (smem_u32(sm) & 1023u) {   // the swizzled tiles rely on it
+    if (tid == 0) atomicCAS(a.err, 0, kErrTimeout);
+    return;
+  }
   if (tid == 0) {
-    s_group = -1;
-    s_bad = 0;
-  }
-  int n = a.lengths ? __ldg(a.lengths + b) : a.N;
-  const int ctx = __ldg(a.ctx + b);
-  __syncthreads();
-  bool falls = false;
-  for (int t = tid; t < a.T; t += kOwnThreads) {
-    const int f0 = __ldg(a.first + t), f1 = __ldg(a.first + t + 1), sh = __ldg(a.shared + t);
-    falls |= f0 > f1;
-    if (f0 <= b && b < f1) {
-      s_group = group_valid(f0, f1, sh, a.B, a.page, a.M) ? t : -2;
-      s_shared = sh;
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], kOwnWarps);
     }
-  }
-  const bool any_falls = __syncthreads_or(falls);
-  const int shared = s_group >= 0 ? s_shared : 0;
-  const bool valid = !any_falls && s_group != -2 && n >= 0 && n <= a.N && ctx >= shared && (long long)ctx + n <= (long long)a.M * a.page;
-  if (!valid) {
-    if (tid == 0) atomicCAS(a.err, 0, kErrDeviceIndex);
-    n = 0;
-  }
-  const int own = ctx - shared, rows = min(kRows, a.N * a.G - r0);
-  const int used = min(rows, n * a.G - r0);      // rows of nodes that are there
-  // position p >= 0 of the row's own part, a node from `own` on; a chain's block needs none past its last node
-  const int L = used <= 0 ? 0 : own + (a.mask ? n : min(n, (r0 + used - 1) / a.G + 1));
-  const int tiles = (L + KT - 1) / KT;
-  const int32_t* table = a.table + (size_t)b * a.M + (shared >> a.page_shift);
-
-  // ------------------------------------------------------------------------------------ loads
-  const size_t step = (size_t)a.Hk * D;          // elements of a position
-  auto lookup = [&](int m) {                     // page m of the own part (-1: read as zeros, and reported)
-    const int pg = __ldg(table + m);
-    if ((unsigned)pg < (unsigned)a.P) return pg;
-    atomicCAS(a.err, 0, kErrDeviceIndex);
-    return -1;
-  };
-  for (int m = tid; m < kOwnPages; m += kOwnThreads)
-    if ((long long)m << a.page_shift < L) s_page[m] = lookup(m);
-  constexpr int kChunks = D / 8, kLoads = KT * kChunks / kOwnThreads;   // 16-byte units of a position; a thread's of a tile
-  const int ch = tid % kChunks, row0 = tid / kChunks;
-  const size_t mine = (size_t)hk * D + ch * 8;
-  auto load = [&](int tile) {
-    uint8_t* to = sm + C::kRing + (tile % NS) * 2 * C::kTile;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int r = row0 + i * (kOwnThreads / kChunks), p = tile * KT + r, m = p >> a.page_shift;
-      const int pg = p >= L ? -1 : m < kOwnPages ? s_page[m] : lookup(m);
-      const size_t at = pg < 0 ? 0 : ((size_t)pg * a.page + (p & (a.page - 1))) * step + mine;
-      const uint32_t bytes = pg < 0 ? 0u : 16u, off = unit_at<D>(r, ch);
-      cp_async16_zfill(to + off, a.k_pages + at, bytes);
-      cp_async16_zfill(to + C::kTile + off, a.v_pages + at, bytes);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.item_full[i], 1);
+      mbar_init(&s.item_empty[i], kOwnWarps);
     }
-  };
-  for (int x = tid; x < kRows * (D / 8); x += kOwnThreads) {
-    const int r = x / (D / 8), ch = x % (D / 8), node = (r0 + r) / a.G, g = (r0 + r) - node * a.G;
-    const bool there = r < used;
-    const size_t at = there ? (((size_t)b * a.N + node) * a.Hq + hk * a.G + g) * D + ch * 8 : 0;
-    cp_async16_zfill(sm + unit_at<D>(r, ch), a.q + at, there ? 16u : 0u);
+    s_bad = -1;
+    fence_mbar_init();
+    prefetch_tmap(&mq);
+    prefetch_tmap(&mk);
+    prefetch_tmap(&mv);
   }
   __syncthreads();
-#pragma unroll
-  for (int s = 0; s < NS - 1; ++s) {
-    if (s < tiles) load(s);
-    cp_async_commit();
-  }
+  const long long items = (long long)a.B * a.Hk * a.m_tiles;
+  const size_t step = (size_t)a.Hk * D;   // elements of a position
+  bool ok = true;
 
-  // ------------------------------------------------------------------------------------ tiles
-  const int wr = warp / WK, wk = warp % WK;
-  const uint32_t q_at = smem_u32(sm);
-  uint32_t qf[D / 16][4];
-  float o[D / 8][4];
-#pragma unroll
-  for (int d = 0; d < D / 8; ++d)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  // this thread's two rows: their nodes and first mask words
-  int node[2];
-  const uint64_t* words[2];
-  uint64_t word0[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = wr * 16 + (lane >> 2) + 8 * h;
-    node[h] = r < used ? (r0 + r) / a.G : 0;
-    words[h] = a.mask ? a.mask + ((size_t)b * a.N + node[h]) * a.W : nullptr;
-    word0[h] = words[h] && r < used ? __ldg(words[h]) : 0;
-  }
-  for (int tile = 0; tile < tiles; ++tile) {
-    cp_async_wait<NS - 2>();
-    __syncthreads();
-    uint8_t* kt = sm + C::kRing + (tile % NS) * 2 * C::kTile;
-    const bool masked = (tile + 1) * KT > own;
-    if (masked) {   // V of nodes: what is not finite must not meet a weight of 0
-      bool bad = false;
-      for (int x = tid; x < KT * (D / 8); x += kOwnThreads) {
-        const int r = x / (D / 8), p = tile * KT + r;
-        if (p < own || p >= L) continue;
-        uint4* v = reinterpret_cast<uint4*>(kt + C::kTile + unit_at<D>(r, x % (D / 8)));
-        uint32_t* u = reinterpret_cast<uint32_t*>(v);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if ((u[e] & 0x7F80u) == 0x7F80u) { u[e] &= 0xFFFF0000u; bad = true; }
-          if ((u[e] & 0x7F800000u) == 0x7F800000u) { u[e] &= 0xFFFFu; bad = true; }
-        }
+  if (warp == kOwnWarps) {
+    // ---------------------------------------------------------------------------------- loads
+    bool falls = false;
+    for (int t = lane; t < a.T; t += 32) falls |= __ldg(a.first + t) > __ldg(a.first + t + 1);
+    falls = __any_sync(0xffffffffu, falls);
+    const int rows = min(a.page, KT), most = KT / rows;   // positions of one box, boxes of a tile
+    const uint32_t box = rows * 128u;                     // its bytes in one 64-column slab
+    Ring<NS> ring;
+    int loads = 0, q_loads = 0, k = 0;
+    for (long long at = blockIdx.x; ok && at < items; at += gridDim.x, ++k) {
+      const Item t = item_of<D, WR>(a, at, falls);
+      if (k >= 2) ok = warp_wait(&s.item_empty[k & 1], ((k >> 1) & 1) ^ 1, a.budget);
+      if (!ok) break;
+      // the queries: row (node, head) as the box leaves them; rows behind it hold anything and are not used
+      if (lane == 0) {
+        s.item[k & 1] = t;
+        mbar_arrive_expect_tx(&s.item_full[k & 1], (uint32_t)(D / 64) * a.heads * a.npt * 128u);
+        for (int h = 0; h < D / 64; ++h)
+          tma_load_4d(sm + (k & 1) * C::kQ + h * kRows * 128, &mq, &s.item_full[k & 1], h * 64, t.hk * a.G + t.h0, t.node0, t.b);
       }
-      if (bad) s_bad = 1;
-      __syncthreads();
+      __syncwarp();
+      ++q_loads;
+      // its positions
+      const int end = t.tiles == 0 ? 0 : t.own + t.n;
+      const int32_t* table = a.table + (size_t)t.b * a.M + (t.shared >> a.page_shift);
+      auto page_at = [&](int tile) {
+        const int pos = tile * KT + lane * rows;
+        return lane < most && pos < end ? __ldg(table + (pos >> a.page_shift)) : -1;
+      };
+      int pg = page_at(0);
+      for (int tile = 0; tile < t.tiles; ++tile) {
+        const int pieces = min(most, (end - tile * KT + rows - 1) / rows), in_page = (tile * KT + lane * rows) & (a.page - 1);
+        int src = pg;
+        if (tile + 1 < t.tiles) pg = page_at(tile + 1);
+        if (lane < pieces && (src < 0 || src >= a.P)) {   // read as zeros (outside the tensor) and reported
+          atomicCAS(a.err, 0, kErrDeviceIndex);
+          src = -1;
+        }
+        const int slot = ring.slot;
+        if (loads == NS) ok = warp_wait(&s.empty[slot], ring.parity ^ 1, a.budget);
+        else ++loads;
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&s.full[slot], 2 * pieces * box * (D / 64));
+        __syncwarp();
+        if (lane < pieces) {
+          uint8_t* dst = sm + C::kRing + slot * 2 * C::kTile + lane * box;
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h) {
+            tma_load_4d(dst + h * KT * 128, &mk, &s.full[slot], h * 64, t.hk, in_page, src);
+            tma_load_4d(dst + C::kTile + h * KT * 128, &mv, &s.full[slot], h * 64, t.hk, in_page, src);
+          }
+        }
+        __syncwarp();
+        ring.step(1);
+      }
     }
-    if (tile == 0) {
+    // no copy of this block is left in flight
+    for (int i = 0; i < loads; ++i) warp_wait(&s.full[i], i < ring.slot ? ring.parity : ring.parity ^ 1, kDrainBudget);
+    for (int i = max(0, q_loads - 2); i < q_loads; ++i) warp_wait(&s.item_full[i & 1], (i >> 1) & 1, kDrainBudget);
+    if (!ok && lane == 0) atomicCAS(a.err, 0, kErrTimeout);
+    return;
+  }
+
+  // ------------------------------------------------------------------------------------ products and softmax
+  const int wr = warp / WK, wk = warp % WK;
+  // this lane's places in the rows that ldmatrix reads: of Q, of K (positions as rows) and of V
+  uint32_t q_off[4], k_off[4], v_off[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    q_off[j] = unit_at(kRows, wr * 16 + (lane & 15), 2 * j + (lane >> 4));
+    k_off[j] = unit_at(KT, wk * PW + (lane & 7) + ((lane >> 4) << 3), 2 * j + ((lane >> 3) & 1));
+    v_off[j] = unit_at(KT, wk * PW + (lane & 15), 2 * j + (lane >> 4));
+  }
+  // nodes of this thread's two rows within an item, and of the row whose results this lane prepares (the i-th of the
+  // warp's: rows that warps share go to them in turn); that row's place in the outputs from the item's first on
+  constexpr int kMine = 16 / WK, kVec = D / 32, kAhead = D == 256 || WR == 1 ? 2 : WR == 2 ? 4 : 8;
+  const int node_of[2] = {(wr * 16 + (lane >> 2)) / a.heads, (wr * 16 + (lane >> 2) + 8) / a.heads};
+  const int my_row = wr * 16 + (lane % kMine) * WK + wk, my_node = my_row / a.heads;
+  const int my_place = my_node * (a.Hq - a.heads) + my_row;
+  const uint32_t ring_at = smem_u32(sm) + C::kRing;
+  float* acc = reinterpret_cast<float*>(sm + C::kOut);
+  Ring<NS> ring;
+  int k = 0;
+  for (long long at = blockIdx.x; at < items; at += gridDim.x, ++k) {
+    // (Warps meet at barriers inside an item, so all of them go through all of its tiles, a warp whose wait ran out
+    // without touching them; they leave together, here or before the results.)
+    ok = named_bar_and(kOwnBar, 32 * kOwnWarps, warp_wait(&s.item_full[k & 1], (k >> 1) & 1, a.budget));
+    if (!ok) break;
+    const Item t = s.item[k & 1];
+    const int n = t.n, own = t.own, used = t.used;
+    float o[D / 8][4];
+#pragma unroll
+    for (int d = 0; d < D / 8; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    // this thread's two rows: how far a chain's node sees, or its mask
+    int sees_to[2];
+    const uint64_t* words[2];
+    uint64_t word0[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = wr * 16 + (lane >> 2) + 8 * h, node = r < used ? t.node0 + node_of[h] : 0;
+      sees_to[h] = own + min(node + 1, n);
+      words[h] = a.mask ? a.mask + ((size_t)t.b * a.N + node) * a.W : nullptr;
+      word0[h] = words[h] && r < used ? __ldg(words[h]) : 0;
+    }
+    uint32_t qf[D / 16][4];
+    if (t.tiles > 0) {
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        ldmatrix4(q_at + unit_at<D>(wr * 16 + (lane & 15), kk * 2 + (lane >> 4)), qf[kk]);
+        ldmatrix4(smem_u32(sm) + (k & 1) * C::kQ + (kk >> 2) * kRows * 128 + q_off[kk & 3], qf[kk]);
     }
-    if (tile + NS - 1 < tiles) load(tile + NS - 1);
-    cp_async_commit();
-    const uint32_t k_at = smem_u32(kt), v_at = k_at + C::kTile;
-    float s[PW / 8][4];
+    for (int tile = 0; tile < t.tiles; ++tile) {
+      ok = ok && warp_wait(&s.full[ring.slot], ring.parity, a.budget);
+      const uint32_t k_at = ring_at + ring.slot * 2 * C::kTile, v_at = k_at + C::kTile;
+      const int first = tile * KT + wk * PW;              // this warp's positions
+      const bool masked = first + PW > own;
+      if (masked) {
+        // V of positions that are not there must not meet a weight of 0, nor what is not finite of nodes that some do not
+        // see (a warp's own positions; warps of other rows with the same positions share them out)
+        if (ok) {
+          constexpr int kClean = PW / WR;
+          bool bad = false;
+          for (int x = lane; x < kClean * (D / 8); x += 32) {
+            const int r = wr * kClean + x / (D / 8), p = first + r;
+            if (p < own) continue;
+            const uint32_t u_at = v_at + unit_at(KT, wk * PW + r, x % (D / 8));
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (p < own + n) {
+              if (n == 1 && !a.mask) continue;            // (it sees itself)
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(u_at) : "memory");
+              uint32_t* u = reinterpret_cast<uint32_t*>(&v);
+              uint32_t hit = 0;
 #pragma unroll
-    for (int c = 0; c < PW / 8; ++c)
+              for (int e = 0; e < 4; ++e) hit |= ((u[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+              if (!hit) continue;
+              bad = true;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[c][e] = 0.f;
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-#pragma unroll
-      for (int c = 0; c < PW / 16; ++c) {
-        uint32_t f[4];
-        ldmatrix4(k_at + unit_at<D>(wk * PW + c * 16 + (lane & 7) + ((lane >> 4) << 3), kk * 2 + ((lane >> 3) & 1)), f);
-        mma16816(s[2 * c], qf[kk], f[0], f[1]);
-        mma16816(s[2 * c + 1], qf[kk], f[2], f[3]);
-      }
-    }
-    if (masked) {
-#pragma unroll
-      for (int c = 0; c < PW / 8; ++c)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int h = e >> 1, j = tile * KT + wk * PW + c * 8 + 2 * (lane & 3) + (e & 1) - own;
-          bool see = j < 0;
-          if (j >= 0 && j < n) {
-            if (a.mask) see = ((j < 64 ? word0[h] : __ldg(words[h] + (j >> 6))) >> (j & 63)) & 1;
-            else see = j <= node[h];
+              for (int e = 0; e < 4; ++e) {
+                if ((u[e] & 0x7F80u) == 0x7F80u) u[e] &= 0xFFFF0000u;
+                if ((u[e] & 0x7F800000u) == 0x7F800000u) u[e] &= 0xFFFFu;
+              }
+            }
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(u_at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
           }
-          if (!see) s[c][e] = -INFINITY;
+          if (bad) s_bad = k;
         }
+        __syncwarp();
+        if (WR > 1) ok = named_bar_and(kOwnBar + 2 + wk, 32 * WR, ok);
+      }
+      if (ok) {
+        float x[PW / 8][4];
+#pragma unroll
+        for (int c = 0; c < PW / 8; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[c][e] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+#pragma unroll
+          for (int c = 0; c < PW / 16; ++c) {
+            uint32_t f[4];
+            ldmatrix4(k_at + (kk >> 2) * KT * 128 + c * 16 * 128 + k_off[kk & 3], f);
+            mma16816(x[2 * c], qf[kk], f[0], f[1]);
+            mma16816(x[2 * c + 1], qf[kk], f[2], f[3]);
+          }
+        }
+        if (masked) {
+          if (a.mask) {
+#pragma unroll
+            for (int c = 0; c < PW / 8; ++c)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int h = e >> 1, j = first + c * 8 + 2 * (lane & 3) + (e & 1) - own;
+                const bool see = j < 0 || (j < n && (((j < 64 ? word0[h] : __ldg(words[h] + (j >> 6))) >> (j & 63)) & 1));
+                if (!see) x[c][e] = -INFINITY;
+              }
+          } else {
+#pragma unroll
+            for (int c = 0; c < PW / 8; ++c)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (first + c * 8 + 2 * (lane & 3) + (e & 1) >= sees_to[e >> 1]) x[c][e] = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < PW / 8; ++c) mx = fmaxf(mx, fmaxf(x[c][2 * h], x[c][2 * h + 1]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * a.sl2;
+          if (__any_sync(0xffffffffu, mx > m[h])) {
+            const float m_new = fmaxf(m[h], mx), f = m[h] == m_new ? 1.f : ex2_approx(m[h] - m_new);
+            l[h] *= f;
+            if (tile > 0) {
+#pragma unroll
+              for (int d = 0; d < D / 8; ++d) {
+                o[d][2 * h] *= f;
+                o[d][2 * h + 1] *= f;
+              }
+            }
+            m[h] = m_new;
+          }
+          const float off = m[h] == -INFINITY ? 0.f : -m[h];
+#pragma unroll
+          for (int c = 0; c < PW / 8; ++c)
+#pragma unroll
+            for (int e = 2 * h; e < 2 * h + 2; ++e) {
+              x[c][e] = ex2_approx(fmaf(x[c][e], a.sl2, off));
+              l[h] += x[c][e];
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < PW / 16; ++c) {
+          const uint32_t p[4] = {pack_bf16x2(x[2 * c][0], x[2 * c][1]), pack_bf16x2(x[2 * c][2], x[2 * c][3]),
+                                 pack_bf16x2(x[2 * c + 1][0], x[2 * c + 1][1]), pack_bf16x2(x[2 * c + 1][2], x[2 * c + 1][3])};
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) {
+            uint32_t f[4];
+            ldmatrix4_t(v_at + (d >> 2) * KT * 128 + c * 16 * 128 + v_off[d & 3], f);
+            mma16816(o[2 * d], p, f[0], f[1]);
+            mma16816(o[2 * d + 1], p, f[2], f[3]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0 && ok) mbar_arrive(&s.empty[ring.slot]);
+      ring.step(1);
+    }
+
+    // ---------------------------------------------------------------------------------- the warps' parts
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float mx = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < PW / 8; ++c) mx = fmaxf(mx, fmaxf(s[c][2 * h], s[c][2 * h + 1]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * a.sl2;
-      if (__any_sync(0xffffffffu, mx > m[h])) {
-        const float m_new = fmaxf(m[h], mx), f = m[h] == m_new ? 1.f : ex2_approx(m[h] - m_new);
-        l[h] *= f;
-#pragma unroll
-        for (int d = 0; d < D / 8; ++d) {
-          o[d][2 * h] *= f;
-          o[d][2 * h + 1] *= f;
-        }
-        m[h] = m_new;
+      const int r = (lane >> 2) + 8 * h;
+      if ((lane & 3) == 0) {
+        s_m[warp][r] = m[h];
+        s_l[warp][r] = l[h];
       }
-      const float off = m[h] == -INFINITY ? 0.f : -m[h];
+      // (8-byte units crosswise by row: rows lie 512 bytes apart or more)
 #pragma unroll
-      for (int c = 0; c < PW / 8; ++c)
-#pragma unroll
-        for (int e = 2 * h; e < 2 * h + 2; ++e) {
-          s[c][e] = ex2_approx(fmaf(s[c][e], a.sl2, off));
-          l[h] += s[c][e];
-        }
+      for (int d = 0; d < D / 8; ++d)
+        *reinterpret_cast<float2*>(acc + (warp * 16 + r) * D + ((d * 8 + 2 * (lane & 3)) ^ ((r & 7) << 3))) = make_float2(o[d][2 * h], o[d][2 * h + 1]);
     }
-#pragma unroll
-    for (int c = 0; c < PW / 16; ++c) {
-      const uint32_t p[4] = {pack_bf16x2(s[2 * c][0], s[2 * c][1]), pack_bf16x2(s[2 * c][2], s[2 * c][3]),
-                             pack_bf16x2(s[2 * c + 1][0], s[2 * c + 1][1]), pack_bf16x2(s[2 * c + 1][2], s[2 * c + 1][3])};
-#pragma unroll
-      for (int d = 0; d < D / 16; ++d) {
-        uint32_t f[4];
-        ldmatrix4_t(v_at + unit_at<D>(wk * PW + c * 16 + (lane & 15), d * 2 + (lane >> 4)), f);
-        mma16816(o[2 * d], p, f[0], f[1]);
-        mma16816(o[2 * d + 1], p, f[2], f[3]);
-      }
-    }
-  }
+    if (k == 0) wait_prerequisite();   // (in every block: this grid must not end before the ones it follows)
+    __syncwarp();
+    ok = named_bar_and(kOwnBar + 1, 32 * kOwnWarps, ok);
+    if (!ok) break;
 
-  // ------------------------------------------------------------------------------------ the warps' parts
-  cp_async_wait<0>();
+    // ---------------------------------------------------------------------------------- results: a warp a row
+    // Lane i works out the factors of the warp's i-th row: of each warp's part, and of the shared part.
+    const int w0 = wr * WK;
+    const size_t base = ((size_t)t.b * a.N + t.node0) * a.Hq + t.hk * a.G + t.h0;
+    const bool joins = t.shared > 0, cleaned = s_bad == k;
+    float c[WK], c_s = 0.f, lse = -INFINITY;
+    bool rare = false;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-    if ((lane & 3) == 0) {
-      s_m[warp][(lane >> 2) + 8 * h] = m[h];
-      s_l[warp][(lane >> 2) + 8 * h] = l[h];
-    }
-  }
-  __syncthreads();   // (and the tiles have been read)
-  float* acc = reinterpret_cast<float*>(sm + C::kRing);
+    for (int w = 0; w < WK; ++w) c[w] = 0.f;
+    if (lane < kMine && my_row < used) {
+      const int rr = lane * WK + wk;
+      const float lse_s = joins ? __ldcg(a.dense_lse + base + my_place) : -INFINITY;
+      float top = s_m[w0][rr], sum = 0.f;
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+      for (int w = 1; w < WK; ++w) top = fmaxf(top, s_m[w0 + w][rr]);
 #pragma unroll
-    for (int d = 0; d < D / 8; ++d)
-      *reinterpret_cast<float2*>(acc + (warp * 16 + (lane >> 2) + 8 * h) * D + d * 8 + 2 * (lane & 3)) =
-          make_float2(o[d][2 * h], o[d][2 * h + 1]);
-  wait_prerequisite();   // (in every block: this grid must not end before the ones it follows)
-  __syncthreads();
-
-  // ------------------------------------------------------------------------------------ results: a warp a row
-  // (the shared part's results are asked for four rows at a time)
-  constexpr int kVec = D / 32, kAhead = WR == 1 ? 2 : 4;
-  const bool joins = shared > 0;
-  for (int rb = warp; rb < rows; rb += kAhead * kOwnWarps) {
-    float x[kAhead][kVec], lse_s[kAhead];
-    auto orow_of = [&](int r) {
-      const int nd = (r0 + r) / a.G, g = (r0 + r) - nd * a.G;
-      return ((size_t)b * a.N + nd) * a.Hq + hk * a.G + g;
-    };
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int r = rb + u * kOwnWarps;
-      lse_s[u] = -INFINITY;
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) x[u][e] = 0.f;
-      if (r >= used || !joins) continue;
-      const size_t orow = orow_of(r);
-      lse_s[u] = __ldcg(a.dense_lse + orow);
-#pragma unroll
-      for (int e = 0; e < kVec; e += 2) {
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(a.dense_o + orow * D + lane * kVec + e));
-        x[u][e] = v.x;
-        x[u][e + 1] = v.y;
+      for (int w = 0; w < WK; ++w) {
+        const float mw = s_m[w0 + w][rr];
+        c[w] = mw == top ? 1.f : ex2_approx(mw - top);
+        sum += c[w] * s_l[w0 + w][rr];
+        rare |= c[w] == 0.f && mw != -INFINITY;
       }
+      const bool sees = sum > 0.f || sum != sum;
+      lse = sees ? top * (1.f / kLog2e) + logf(sum) : -INFINITY;
+      const float ref = fmaxf(lse, lse_s);
+      float f = sees ? 1.f : 0.f, total = 1.f;
+      if (lse != lse || lse_s != lse_s) {
+        f = c_s = total = NAN;
+      } else if (joins && ref > -INFINITY) {
+        f = lse == ref ? 1.f : ex2_approx((lse - ref) * kLog2e);
+        c_s = lse_s == ref ? 1.f : ex2_approx((lse_s - ref) * kLog2e);
+        rare |= (f == 0.f && lse != -INFINITY) || (c_s == 0.f && lse_s != -INFINITY);
+        total = f + c_s;
+      }
+      if (joins) lse = ref == -INFINITY && total == total ? -INFINITY : ref + logf(total);
+      const float inv = sees ? f / (sum * total) : 0.f;
+#pragma unroll
+      for (int w = 0; w < WK; ++w) c[w] *= inv;
+      c_s /= total;
     }
+    if (a.lse && lane < kMine && my_row < t.rows) a.lse[base + my_place] = lse;
+    const unsigned rares = __ballot_sync(0xffffffffu, (rare || cleaned) && lane < kMine && my_row < used);
+    const int place_of = my_place;
+    for (int i0 = 0; i0 < kMine; i0 += kAhead) {
+      if (wr * 16 + i0 * WK + wk >= t.rows) break;
+      float x[kAhead][kVec];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int r = rb + u * kOwnWarps;
-      if (r >= rows) break;
-      const size_t orow = orow_of(r);
-      float y[kVec], lse = -INFINITY;
+      for (int u = 0; u < kAhead; ++u) {
+        const int r = wr * 16 + (i0 + u) * WK + wk;
+        const size_t orow = base + __shfl_sync(0xffffffffu, place_of, i0 + u);
 #pragma unroll
-      for (int e = 0; e < kVec; ++e) y[e] = 0.f;
-      if (r < used) {
-        const int w0 = (r >> 4) * WK, rr = r & 15;
-        float top = s_m[w0][rr];
+        for (int e = 0; e < kVec; ++e) x[u][e] = 0.f;
+        if (r >= used || !joins) continue;
 #pragma unroll
-        for (int w = 1; w < WK; ++w) top = fmaxf(top, s_m[w0 + w][rr]);
-        float sum = 0.f;
+        for (int e = 0; e < kVec; e += 2) {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(a.dense_o + orow * D + lane * kVec + e));
+          x[u][e] = v.x;
+          x[u][e + 1] = v.y;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = i0 + u, r = wr * 16 + i * WK + wk, rr = i * WK + wk;
+        const size_t orow = base + __shfl_sync(0xffffffffu, place_of, i);
+        const float cs = __shfl_sync(0xffffffffu, c_s, i);
+        float y[kVec];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) y[e] = cs != 0.f ? cs * x[u][e] : 0.f;
 #pragma unroll
         for (int w = 0; w < WK; ++w) {
-          const float mw = s_m[w0 + w][rr], f = mw == top ? 1.f : ex2_approx(mw - top);
-          sum += f * s_l[w0 + w][rr];
+          const float cw = __shfl_sync(0xffffffffu, c[w], i);
+          if (cw == 0.f) continue;   // (a part without weight may hold anything)
+          const float* from = acc + ((w0 + w) * 16 + rr) * D;
 #pragma unroll
-          for (int e = 0; e < kVec; ++e) {
-            const float z = acc[((w0 + w) * 16 + rr) * D + lane * kVec + e];
-            if (f != 0.f) y[e] = fmaf(f, z, y[e]);
-            else if (mw != -INFINITY && !(fabsf(z) < INFINITY)) y[e] += z;   // an infinity that was seen counts
+          for (int e = 0; e < kVec; e += 2) {
+            const float2 v = *reinterpret_cast<const float2*>(from + ((lane * kVec + e) ^ ((rr & 7) << 3)));
+            y[e] = fmaf(cw, v.x, y[e]);
+            y[e + 1] = fmaf(cw, v.y, y[e + 1]);
           }
         }
-        const bool sees = sum > 0.f || sum != sum;
-        lse = sees ? top * (1.f / kLog2e) + logf(sum) : -INFINITY;
-        const float inv = sees ? 1.f / sum : 0.f;
+        if (r < t.rows) {
+          __nv_bfloat16* out = a.o + orow * D + lane * kVec;
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) y[e] = sees ? y[e] * inv : 0.f;
-        if (s_bad) {   // elements that were cleaned away, of the nodes that this one sees
-          const int nd = (r0 + r) / a.G;
-          const uint64_t* wd = a.mask ? a.mask + ((size_t)b * a.N + nd) * a.W : nullptr;
-          for (int j = 0; j < n; ++j) {
-            if (wd ? !(wd[j >> 6] >> (j & 63) & 1) : j > nd) continue;
-            const int p = own + j, pg = __ldg(table + (p >> a.page_shift));
-            if ((unsigned)pg >= (unsigned)a.P) continue;
-            const __nv_bfloat16* v = a.v_pages + ((size_t)pg * a.page + (p & (a.page - 1))) * step + (size_t)hk * D + lane * kVec;
-            for (int e = 0; e < kVec; ++e) {
-              const float z = __bfloat162float(v[e]);
-              if (!(fabsf(z) < INFINITY)) y[e] += z;
-            }
-          }
-        }
-        if (joins) {
-          const float ref = fmaxf(lse, lse_s[u]);
-          float f[2] = {1.f, 0.f};   // the own part's weight, the shared part's
-          if (lse != lse || lse_s[u] != lse_s[u]) {
-            f[0] = f[1] = NAN;
-          } else if (ref > -INFINITY) {
-            f[0] = lse == ref ? 1.f : ex2_approx((lse - ref) * kLog2e);
-            f[1] = lse_s[u] == ref ? 1.f : ex2_approx((lse_s[u] - ref) * kLog2e);
-          }
-          const float total = f[0] + f[1], inv2 = 1.f / total;
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) {
-            float z = f[0] != 0.f ? f[0] * y[e] : lse != -INFINITY && !(fabsf(y[e]) < INFINITY) ? y[e] : 0.f;
-            if (f[1] != 0.f) z = fmaf(f[1], x[u][e], z);
-            else if (lse_s[u] != -INFINITY && !(fabsf(x[u][e]) < INFINITY)) z += x[u][e];
-            y[e] = z * inv2;
-          }
-          lse = ref == -INFINITY && total == total ? -INFINITY : ref + logf(total);
+          for (int e = 0; e < kVec; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(y[e], y[e + 1]);
         }
       }
-      __nv_bfloat16* out = a.o + orow * D + lane * kVec;
-#pragma unroll
-      for (int e = 0; e < kVec; e += 2) *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(y[e], y[e + 1]);
-      if (lane == 0 && a.lse) a.lse[orow] = lse;
     }
+    // What is not finite counts, however small its weight: in parts whose weight vanished, and elements of seen nodes
+    // that were cleaned away. Such rows are formed once more.
+    for (unsigned left = rares; left; left &= left - 1) {
+      const int i = __ffs(left) - 1, rr = i * WK + wk;
+      const size_t orow = base + __shfl_sync(0xffffffffu, place_of, i);
+      const float cs = __shfl_sync(0xffffffffu, c_s, i);
+      const int nd = t.node0 + __shfl_sync(0xffffffffu, my_node, i);
+      const uint64_t* wd = a.mask ? a.mask + ((size_t)t.b * a.N + nd) * a.W : nullptr;
+      const int32_t* table = a.table + (size_t)t.b * a.M + (t.shared >> a.page_shift);
+      float cw[WK];
+#pragma unroll
+      for (int w = 0; w < WK; ++w) cw[w] = __shfl_sync(0xffffffffu, c[w], i);
+#pragma unroll 1
+      for (int d = lane; d < D; d += 32) {
+        float y = 0.f;
+        auto add = [&](float f, float z, bool seen) {
+          if (f != 0.f) y = fmaf(f, z, y);
+          else if (seen && !(fabsf(z) < INFINITY)) y += z;
+        };
+        if (joins) add(cs, __ldcg(a.dense_o + orow * D + d), __ldcg(a.dense_lse + orow) != -INFINITY);
+#pragma unroll
+        for (int w = 0; w < WK; ++w) add(cw[w], acc[((w0 + w) * 16 + rr) * D + (d ^ ((rr & 7) << 3))], s_m[w0 + w][rr] != -INFINITY);
+        for (int j = 0; cleaned && j < n; ++j) {
+          if (wd ? !(wd[j >> 6] >> (j & 63) & 1) : j > nd) continue;
+          const int p = own + j, pg = __ldg(table + (p >> a.page_shift));
+          if ((unsigned)pg < (unsigned)a.P)
+            add(0.f, __bfloat162float(a.v_pages[((size_t)pg * a.page + (p & (a.page - 1))) * step + (size_t)t.hk * D + d]), true);
+        }
+        a.o[orow * D + d] = __float2bfloat16(y);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.item_empty[k & 1]);
   }
+  if (k == 0) wait_prerequisite();   // (left before the first item's results)
+  if (!ok && lane == 0) atomicCAS(a.err, 0, kErrTimeout);
 }
 
 size_t dense_rows(const TreeAttnArgs& t) { return (size_t)t.B * t.N * t.Hq; }
@@ -421,11 +578,21 @@ cudaError_t own_part(const ForkAttnArgs& p, cudaStream_t s) {
   a.page_shift = __builtin_ctz((unsigned)t.page);
   a.M = t.M; a.T = p.T;
   a.err = t.err;
+  a.heads = std::min(a.G, C::kRows);
+  a.splits = (a.G + C::kRows - 1) / C::kRows;
+  a.npt = std::min(C::kRows / a.heads, t.N);
+  a.m_tiles = (t.N + a.npt - 1) / a.npt * a.splits;
+  a.budget = wait_budget_cycles();
+  CUtensorMap mq, mk, mv;
+  if (!make_map(&mq, t.q, D, t.Hq, t.N, t.B, a.heads, a.npt) ||
+      !make_map(&mk, t.k_pages, D, t.Hk, t.page, t.P, 1, std::min(t.page, C::KT)) ||
+      !make_map(&mv, t.v_pages, D, t.Hk, t.page, t.P, 1, std::min(t.page, C::KT)))
+    return cudaErrorInvalidValue;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(fork_own_kernel<D, WR>), C::kSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)t.B * t.Hk, (t.N * a.G + C::kRows - 1) / C::kRows);
+  cfg.gridDim = dim3((unsigned)std::min((long long)t.B * t.Hk * a.m_tiles, (long long)kNumSMs * (D == 256 ? 1 : 2)));
   cfg.blockDim = dim3(kOwnThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
@@ -435,7 +602,7 @@ cudaError_t own_part(const ForkAttnArgs& p, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const int slot = stage_timer_begin(s, kKernForkAttnOwn);
-  e = cudaLaunchKernelEx(&cfg, fork_own_kernel<D, WR>, a);
+  e = cudaLaunchKernelEx(&cfg, fork_own_kernel<D, WR>, mq, mk, mv, a);
   stage_timer_end(slot, s);
   return e;
 }
