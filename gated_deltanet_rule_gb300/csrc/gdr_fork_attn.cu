@@ -255,6 +255,32 @@ __global__ void __launch_bounds__(kOwnThreads, D == 256 ? 1 : 2)
     if (!ok) break;
     const Item t = s.item[k & 1];
     const int n = t.n, own = t.own, used = t.used;
+    // The shared part's results for the warp's first rows, asked for as early as they are there (from the second item on
+    // before its tiles: 102.8 -> 100.6 us for 256 forks).
+    const size_t base = ((size_t)t.b * a.N + t.node0) * a.Hq + t.hk * a.G + t.h0;
+    const bool joins = t.shared > 0;
+    float shared_x[kAhead][kVec], lse_s = -INFINITY;
+    auto ask = [&](int i0, float (&x)[kAhead][kVec]) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const size_t orow = base + __shfl_sync(0xffffffffu, my_place, i0 + u);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) x[u][e] = 0.f;
+        if (wr * 16 + (i0 + u) * WK + wk >= used || !joins) continue;
+#pragma unroll
+        for (int e = 0; e < kVec; e += 2) {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(a.dense_o + orow * D + lane * kVec + e));
+          x[u][e] = v.x;
+          x[u][e + 1] = v.y;
+        }
+      }
+    };
+    auto ask_first = [&] {
+      if (joins && lane < kMine && my_row < used) lse_s = __ldcg(a.dense_lse + base + my_place);
+      ask(0, shared_x);
+    };
+    constexpr bool kEarly = WR == 1 && D < 256;   // (registers for the rows of more warps are not left)
+    if (kEarly && k > 0) ask_first();
     float o[D / 8][4];
 #pragma unroll
     for (int d = 0; d < D / 8; ++d)
@@ -415,6 +441,7 @@ __global__ void __launch_bounds__(kOwnThreads, D == 256 ? 1 : 2)
         *reinterpret_cast<float2*>(acc + (warp * 16 + r) * D + ((d * 8 + 2 * (lane & 3)) ^ ((r & 7) << 3))) = make_float2(o[d][2 * h], o[d][2 * h + 1]);
     }
     if (k == 0) wait_prerequisite();   // (in every block: this grid must not end before the ones it follows)
+    if (!kEarly || k == 0) ask_first();
     __syncwarp();
     ok = named_bar_and(kOwnBar + 1, 32 * kOwnWarps, ok);
     if (!ok) break;
@@ -422,15 +449,13 @@ __global__ void __launch_bounds__(kOwnThreads, D == 256 ? 1 : 2)
     // ---------------------------------------------------------------------------------- results: a warp a row
     // Lane i works out the factors of the warp's i-th row: of each warp's part, and of the shared part.
     const int w0 = wr * WK;
-    const size_t base = ((size_t)t.b * a.N + t.node0) * a.Hq + t.hk * a.G + t.h0;
-    const bool joins = t.shared > 0, cleaned = s_bad == k;
+    const bool cleaned = s_bad == k;
     float c[WK], c_s = 0.f, lse = -INFINITY;
     bool rare = false;
 #pragma unroll
     for (int w = 0; w < WK; ++w) c[w] = 0.f;
     if (lane < kMine && my_row < used) {
       const int rr = lane * WK + wk;
-      const float lse_s = joins ? __ldcg(a.dense_lse + base + my_place) : -INFINITY;
       float top = s_m[w0][rr], sum = 0.f;
 #pragma unroll
       for (int w = 1; w < WK; ++w) top = fmaxf(top, s_m[w0 + w][rr]);
@@ -461,32 +486,17 @@ __global__ void __launch_bounds__(kOwnThreads, D == 256 ? 1 : 2)
     }
     if (a.lse && lane < kMine && my_row < t.rows) a.lse[base + my_place] = lse;
     const unsigned rares = __ballot_sync(0xffffffffu, (rare || cleaned) && lane < kMine && my_row < used);
-    const int place_of = my_place;
     for (int i0 = 0; i0 < kMine; i0 += kAhead) {
       if (wr * 16 + i0 * WK + wk >= t.rows) break;
-      float x[kAhead][kVec];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int r = wr * 16 + (i0 + u) * WK + wk;
-        const size_t orow = base + __shfl_sync(0xffffffffu, place_of, i0 + u);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) x[u][e] = 0.f;
-        if (r >= used || !joins) continue;
-#pragma unroll
-        for (int e = 0; e < kVec; e += 2) {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(a.dense_o + orow * D + lane * kVec + e));
-          x[u][e] = v.x;
-          x[u][e + 1] = v.y;
-        }
-      }
+      if (i0 > 0) ask(i0, shared_x);
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         const int i = i0 + u, r = wr * 16 + i * WK + wk, rr = i * WK + wk;
-        const size_t orow = base + __shfl_sync(0xffffffffu, place_of, i);
+        const size_t orow = base + __shfl_sync(0xffffffffu, my_place, i);
         const float cs = __shfl_sync(0xffffffffu, c_s, i);
         float y[kVec];
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) y[e] = cs != 0.f ? cs * x[u][e] : 0.f;
+        for (int e = 0; e < kVec; ++e) y[e] = cs != 0.f ? cs * shared_x[u][e] : 0.f;
 #pragma unroll
         for (int w = 0; w < WK; ++w) {
           const float cw = __shfl_sync(0xffffffffu, c[w], i);
@@ -510,7 +520,7 @@ __global__ void __launch_bounds__(kOwnThreads, D == 256 ? 1 : 2)
     // that were cleaned away. Such rows are formed once more.
     for (unsigned left = rares; left; left &= left - 1) {
       const int i = __ffs(left) - 1, rr = i * WK + wk;
-      const size_t orow = base + __shfl_sync(0xffffffffu, place_of, i);
+      const size_t orow = base + __shfl_sync(0xffffffffu, my_place, i);
       const float cs = __shfl_sync(0xffffffffu, c_s, i);
       const int nd = t.node0 + __shfl_sync(0xffffffffu, my_node, i);
       const uint64_t* wd = a.mask ? a.mask + ((size_t)t.b * a.N + nd) * a.W : nullptr;
