@@ -26,6 +26,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "gdr_serve.h"
 #include "pairs.cuh"
@@ -188,22 +189,21 @@ struct Unit<bf16> {
   }
   static __device__ __forceinline__ float one(const bf16* p) { return __bfloat162float(*p); }
   static __device__ __forceinline__ uint4 clean_max(const uint4& u, float& top) {   // (-0 stays: only keys tell it from 0)
-    float x[8];
-    read(u, x);
     // an exponent of all ones carries into the sign's place when one is added to it
-    const uint32_t hit = ((((u.x & 0x7F807F80u) + 0x00800080u) | ((u.y & 0x7F807F80u) + 0x00800080u) |
-                           ((u.z & 0x7F807F80u) + 0x00800080u) | ((u.w & 0x7F807F80u) + 0x00800080u)) & 0x80008000u);
-    if (!hit) {
+    const uint32_t hit = (((u.x & 0x7F807F80u) + 0x00800080u) | ((u.y & 0x7F807F80u) + 0x00800080u) |
+                          ((u.z & 0x7F807F80u) + 0x00800080u) | ((u.w & 0x7F807F80u) + 0x00800080u)) & 0x80008000u;
+    uint4 r = u;
+    if (hit) {
+      float x[8];
+      read(u, x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, x[e]);
-      return u;
+      for (int e = 0; e < 8; ++e) x[e] = fminf(clean(x[e]), kBf16Max);
+      r = write(x);
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      x[e] = fminf(clean(x[e]), kBf16Max);
-      top = fmaxf(top, x[e]);
-    }
-    return write(x);
+    auto two = [](uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); };
+    const __nv_bfloat162 m = __hmax2(__hmax2(two(r.x), two(r.y)), __hmax2(two(r.z), two(r.w)));
+    top = fmaxf(top, fmaxf(__low2float(m), __high2float(m)));
+    return r;
   }
 };
 
@@ -222,8 +222,15 @@ __device__ __forceinline__ void st_cluster64(uint32_t addr, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
-constexpr int kOctaves = 15;                       // bf16: binary orders below the largest magnitude with a bin for each value
-constexpr int kSide = kOctaves * 128;              // bins of one sign
+// bf16: a bin for each value of a magnitude from 2^-8 to 127, so that logits are counted as they arrive, before their
+// largest is known. v = 0 for smaller magnitudes, 1 .. kTop - 1 by magnitude, kTop for larger ones; a positive value's bin
+// lies at ~v, a negative one's at v (modulo 4096), which two packed minima and a mask give for two logits at once. In the
+// order of falling logits (steps) they follow one another from kFirstBin on: kTop - v, and kTop + 1 + v for negative ones.
+constexpr int kLeast = (127 - 8) << 7;             // the code of 2^-8
+constexpr int kTop = 1919;
+constexpr int kMiddleStep = kTop;                  // around zero (and the step after it, which is counted with it)
+constexpr int kFirstBin = 4095 - kTop;
+constexpr float kLarge = 127.f;                    // the magnitude with v = kTop
 constexpr int kMaxSteps = 4096;
 template <typename T>
 struct Bins;
@@ -233,11 +240,11 @@ struct Bins<float> {
 };
 template <>
 struct Bins<bf16> {
-  static constexpr int n = 2 * kSide + 2;          // positive values falling, around zero, negative ones, the rest
+  static constexpr int n = 2 * kTop + 2;           // large ones, positive values falling, around zero, negative values, the rest
 };
 
 constexpr int kList = 2048;                  // candidates of a row: places, shared out evenly to its blocks
-constexpr int kMiddle = 256;
+constexpr int kOthers = 256;
 struct Shared {
   float2 table[64];
   union {
@@ -251,14 +258,15 @@ struct Shared {
     };
     u64 list[kList];                         // candidates, by block; other blocks write them, while this one may still
                                              // read `all`: they lie over `steps`, which everyone has read by then
-    u64 weight[Bins<bf16>::n];               // bf16: the weight of each bin's value
+    u64 weight[kMaxSteps];                   // bf16: the weight of each bin's value (0: not kept)
   };
-  float middle[kMiddle];                     // bf16: logits around zero
+  float others[kOthers];                     // bf16: logits around zero
   double min_p;                              // T ln(min_p)
   float tops[kMaxCluster];
   u64 sums[2][3][kMaxCluster];   // the blocks' totals, by turns
   int listed[kMaxCluster];
   u64 warps[kWarps], chunks[kWarps];
+  uint32_t equals[kWarps], chunk_equals[kWarps];
   u64 scan_m[kWarps];
   float scan_f[kWarps];
   uint32_t scan_n[kWarps];
@@ -271,7 +279,18 @@ struct Shared {
   int mine;
   int cut;
 };
-static_assert(Bins<bf16>::n <= kMaxSteps && kList * sizeof(u64) <= kMaxSteps * sizeof(uint32_t), "bins and lists fit");
+static_assert(kFirstBin % 8 == 0 && kMaxSteps == 8 * kThreads && Bins<bf16>::n <= kMaxSteps && kList * sizeof(u64) <= kMaxSteps * sizeof(uint32_t), "bins and lists fit");
+
+// v of two bf16 logits (16 bits each), and their bins.
+__device__ __forceinline__ uint32_t magnitudes(uint32_t w) {
+  constexpr uint32_t kOff = (uint32_t)(uint16_t)(1 - kLeast) * 0x10001u;
+  return __viaddmin_s16x2_relu(w & 0x7FFF7FFFu, kOff, (uint32_t)kTop * 0x10001u);
+}
+__device__ __forceinline__ uint32_t bins(uint32_t w, uint32_t v) {
+  uint32_t negative;   // the signs, over each half
+  asm("prmt.b32 %0, %1, 0, 0xBB99;" : "=r"(negative) : "r"(w));
+  return (v ^ ~negative) & 0x0FFF0FFFu;
+}
 
 template <typename T>
 struct Row {
@@ -285,28 +304,26 @@ struct Row {
   Shared* sh;
   Scale s;
   float top, steps;  // maximum, steps of the first histogram a unit of logits
-  int least_code;    // bf16: the smallest magnitude with a bin of its own
-  float low;         // bf16: logits below it have no weight to speak of
   int turn_s;
 
   // The step of a logit: it rises as the logit falls.
   __device__ __forceinline__ int step_of(float l) const {
     if constexpr (kValues) {
-      const uint32_t b = __float_as_uint(l) >> 16;
-      const int m = (int)(b & 0x7FFFu) - least_code + 1, v = m > 0 ? m : 0;
-      const int at = kSide + ((b & 0x8000u) ? v : -v);
-      return l < low ? kSteps - 1 : at;
+      const int b = (int)(__float_as_uint(l) >> 16), v = min(max((b & 0x7FFF) - (kLeast - 1), 0), kTop);
+      return b & 0x8000 && v > 0 ? kMiddleStep + 1 + v : kMiddleStep - v;
     } else {
       return (int)place(l);
     }
   }
   // float32: the same before it is cut to a step.
   __device__ __forceinline__ float place(float l) const { return fminf((top - l) * steps, (float)(kSteps - 1)); }
-  // The value of a step that holds one (kValues).
-  __device__ __forceinline__ bool one_value(int step) const { return kValues && step != kSide && step != kSteps - 1; }
+  // Whether a step holds one value (kValues), and which.
+  __device__ __forceinline__ bool one_value(int step) const {
+    return kValues && step != 0 && step != kMiddleStep && step != kMiddleStep + 1 && step < kSteps - 1;
+  }
   __device__ __forceinline__ float value_of(int step) const {
-    const uint32_t m = (uint32_t)(abs(kSide - step) - 1 + least_code);
-    return __uint_as_float((m | (step > kSide ? 0x8000u : 0u)) << 16);
+    const int v = step > kMiddleStep ? step - kMiddleStep - 1 : kMiddleStep - step;
+    return __uint_as_float(((uint32_t)(v + kLeast - 1) | (step > kMiddleStep ? 0x8000u : 0u)) << 16);
   }
 
   // All blocks' v (n of them), in order of rank: sums before this block, and of all.
@@ -399,40 +416,53 @@ struct Row {
     return fixed(acc);
   }
 
-  // Counts of the row's logits by step, over all blocks: of this thread's steps, kMine neighbours. Each block adds up a
-  // part of the steps and hands the sums to all (reading every block's counts everywhere took five times as long).
-  // bf16 with `masses`: the mass of the logits around zero, too.
+  // Counts of the row's logits by step: this block's, then over all blocks, of this thread's steps (kMine neighbours).
+  // Each block adds up a part of the steps and hands the sums to all (reading every block's counts everywhere took five
+  // times as long). bf16 with `masses`: the masses of the steps that hold more than a value, too.
   static constexpr int kMine = kMaxSteps / kThreads;
-  __device__ __forceinline__ u64 count_steps(bool masses, uint32_t (&n)[kMine]) {
+  __device__ __forceinline__ void start_counts() {   // (before a barrier)
     for (int i = threadIdx.x; i < kMaxSteps / 4; i += kThreads) reinterpret_cast<uint4*>(sh->steps)[i] = make_uint4(0, 0, 0, 0);
     if (threadIdx.x == 0) sh->mine = 0;
-    __syncthreads();
-    each([&](const float* x, int) {
+  }
+  __device__ __forceinline__ void count_logit(float x) const {
+    if (x > -INFINITY) atomicAdd(&sh->steps[step_of(x)], 1u);
+  }
+  // bf16: eight logits by their bins (-inf among the rest), those around zero listed
+  __device__ __forceinline__ void count_unit(const uint4& u) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t zero = 0;
 #pragma unroll
-      for (int e = 0; e < U::n; ++e) {
-        if (!(x[e] > -INFINITY)) continue;
-        const int step = step_of(x[e]);
-        atomicAdd(&sh->steps[step], 1u);
-        if (kValues && step == kSide) {
-          const int i = atomicAdd(&sh->mine, 1);
-          if (i < kMiddle) sh->middle[i] = x[e];
-        }
-      }
-    });
-    if (kValues && masses) {
-      __syncthreads();
-      const int count = sh->mine;
-      u64 v = 0;
-      if (count > kMiddle) {
-        const float small = __uint_as_float((uint32_t)least_code << 16);
-        v = mass_where([&](float x) { return fabsf(x) < small; });
-      } else if (threadIdx.x < count) {
-        v = gdr::weight(s, sh->table, sh->middle[threadIdx.x]);
-      }
-      if (count) v = block_sum(v);
-      if (threadIdx.x < ranks) st_cluster64(ptx::dsmem_addr(&sh->sums[turn_s][0][rank], threadIdx.x), v);
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t v = magnitudes(w[e]), at = bins(w[e], v);
+      atomicAdd(&sh->steps[at & 0xFFFFu], 1u);
+      atomicAdd(&sh->steps[at >> 16], 1u);
+      zero |= (v - 0x00010001u) & ~v;
     }
-    ptx::cluster_sync_all();
+    if (zero & 0x80008000u) {   // (or next to one: looked at again)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t h = w[e >> 1] >> (16 * (e & 1));
+        if ((int)(h & 0x7FFFu) >= kLeast) continue;
+        const int i = atomicAdd(&sh->mine, 1);
+        if (i < kOthers) sh->others[i] = __uint_as_float(h << 16);
+      }
+    }
+  }
+  // (after a cluster barrier behind the counting) bf16: the masses of the steps that hold more than a value: large logits,
+  // those around zero, the rest
+  __device__ __forceinline__ void finish_counts(bool masses, uint32_t (&n)[kMine], u64 (&mass)[3]) {
+    if (kValues && masses) {
+      u64 v[3] = {0, 0, 0};
+      const int count = sh->mine;
+      if (count > kOthers) v[1] = mass_where([&](float x) { return fabsf(x) < 0x1p-8f; });
+      else if (threadIdx.x < count) v[1] = gdr::weight(s, sh->table, sh->others[threadIdx.x]);
+      if (count) v[1] = block_sum(v[1]);
+      if (top >= kLarge) v[0] = block_sum(mass_where([&](float x) { return x >= kLarge; }));
+      if ((-kLarge - top) * s.ch > -64.f) v[2] = block_sum(mass_where([&](float x) { return x <= -kLarge && x > -INFINITY; }));
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (threadIdx.x < ranks) st_cluster64(ptx::dsmem_addr(&sh->sums[turn_s][i][rank], threadIdx.x), v[i]);
+    }
     // (1, 2, 4 or 8 blocks: parts of whole 16 bytes)
     const int part = kMaxSteps / 4 / ranks;
     for (int i = threadIdx.x; i < part; i += kThreads) {
@@ -450,21 +480,24 @@ struct Row {
       for (int q = 0; q < ranks; ++q) st_cluster4(ptx::dsmem_addr(&sh->all[4 * at], q), t);
     }
     ptx::cluster_sync_all();
-    u64 mass = 0;
     if (kValues && masses) {
-      for (int q = 0; q < ranks; ++q) mass += sh->sums[turn_s][0][q];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        mass[i] = 0;
+        for (int q = 0; q < ranks; ++q) mass[i] += sh->sums[turn_s][i][q];
+      }
       turn_s ^= 1;
     }
 #pragma unroll
     for (int i = 0; i < kMine; i += 4) {
-      const uint4 x = reinterpret_cast<const uint4*>(sh->all)[(threadIdx.x * kMine + i) / 4];
+      // (a thread's steps lie side by side in the order of bins, too)
+      const uint4 x = reinterpret_cast<const uint4*>(sh->all)[((threadIdx.x * kMine + i + (kValues ? kFirstBin : 0)) & (kMaxSteps - 1)) / 4];
       n[i] = x.x;
       n[i + 1] = x.y;
       n[i + 2] = x.z;
       n[i + 3] = x.w;
     }
     __syncthreads();   // (what lies in the same place is written next)
-    return mass;
   }
 
   // Zeroes this block's histogram, to be filled by `fill`; then finds the first bin at which the running count (or mass)
@@ -603,7 +636,41 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
   Border out = {-INFINITY, 0, 0, -1, false, 0};
   const bool cuts_k = k > 0, cuts_p = p < 1.f;
   uint32_t n[kMine];
-  const u64 middle = r.count_steps(p < 1.f, n);
+  u64 others[3] = {0, 0, 0};
+  r.finish_counts(p < 1.f, n, others);
+  if constexpr (Row<T>::kValues) {
+    // negative zeros' neighbours belong to the middle; -inf is among the rest, which matters only where the k-th logit does
+    constexpr int kA = kMiddleStep, kB = kMiddleStep + 1, kLast = kSteps - 1;
+    static_assert(kA / kMine + 1 == kB / kMine && kB % kMine == 0, "the middle's two steps lie in neighbouring threads");
+    if (tid == kB / kMine) {
+      sh.bin_n = n[0];
+      n[0] = 0;
+    }
+    __syncthreads();
+    if (tid == kA / kMine) n[kA % kMine] += sh.bin_n;
+    uint32_t finite = 0;
+    if (cuts_k) {
+      uint32_t c = 0;
+      if (tid != kLast / kMine)
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) c += n[i];
+      else
+#pragma unroll
+        for (int i = 0; i < kLast % kMine; ++i) c += n[i];
+      if (r.block_sum(c) <= (u64)k) {   // (the same in every block)
+        u64 mine = 0;
+        r.each([&](const float* x, int) {
+#pragma unroll
+          for (int e = 0; e < U::n; ++e) mine += x[e] <= -kLarge && x[e] > -INFINITY;
+        });
+        const u64 v[1] = {r.block_sum(mine)};
+        u64 before[1], sum[1];
+        r.cluster_sums(v, before, sum);
+        finite = (uint32_t)sum[0];
+      }
+    }
+    if (tid == kLast / kMine) n[kLast % kMine] = finite;
+  }
 
   // counts above this thread's steps; masses: of each step's value, or (float32) bounds that the steps' width gives
   uint32_t sum_n = 0, bn;
@@ -620,9 +687,14 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
       sum_f += (float)n[i] * ptx::ex2_approx(-(float)(s0 + i) * (1.f / kPerOctave));
     }
   }
-  if (Row<T>::kValues && kSide / kMine == tid) {
-    m[kSide % kMine] = middle;
-    sum_m += middle;
+  if (Row<T>::kValues) {
+    constexpr int at[3] = {0, kMiddleStep, kSteps - 1};
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (at[i] / kMine == tid) {
+        m[at[i] % kMine] = others[i];
+        sum_m += others[i];
+      }
   }
   r.block_scan(sum_n, sum_m, sum_f, bn, bm, bf);
 
@@ -715,6 +787,7 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
         out.ties = ties;
         out.equal = equal;
       }
+      out.mass = above + out.ties * w;
       return out;
     }
     uint32_t lo, hi, key, n_key;
@@ -1039,7 +1112,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   r.units = min(all, u0 + per) - u0;
   r.first = u0 * U::n - skew;
 
-  // the row into shared memory, and its largest entry
+  const bool filters = (k > 0 && k < a.V) || p < 1.f;
+  if (!(k > 0 && k < a.V)) k = 0;
+  if (filters) r.start_counts();
+  __syncthreads();
+  // the row into shared memory, and its largest entry (bf16: and the counts of its values)
   float top = -INFINITY;
   {
     uint4* to = reinterpret_cast<uint4*>(dyn);
@@ -1064,7 +1141,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       for (int c = 0; c < kAhead; ++c) {
         const int i = i0 + c * kThreads;
         if (i >= r.units) continue;
-        to[i] = U::clean_max(v[c], top);
+        const uint4 x = U::clean_max(v[c], top);
+        to[i] = x;
+        if constexpr (Row<T>::kValues)
+          if (filters) r.count_unit(x);
       }
     }
   }
@@ -1101,14 +1181,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       r.s.ml = __fmaf_rn(z, r.s.cl, __fmaf_rn(z, r.s.ch, -r.s.mh));
       r.s.least = fmaxf((r.s.mh - 150.f) / r.s.ch, -FLT_MAX);
       r.steps = r.s.ch * (float)kPerOctave;
-      // bf16: bins for the magnitudes from the largest that has weight down over kOctaves binary orders
-      r.low = fmaxf(top - 64.f / r.s.ch, -kBf16Max);
-      const int code = (int)(__float_as_uint(fmaxf(fabsf(top), fabsf(r.low))) >> 16);
-      r.least_code = max(1, (code & ~127) - (kOctaves - 1) * 128);
     }
     Border edge = {-INFINITY, 0, 0, -1, false, 0};
-    if (!(k > 0 && k < a.V)) k = 0;
-    if (k > 0 || p < 1.f) edge = find_border(r, k, p);
+    if (filters) {
+      if (!Row<T>::kValues) {
+        r.each([&](const float* x, int) {
+#pragma unroll
+          for (int e = 0; e < U::n; ++e) r.count_logit(x[e]);
+        });
+        ptx::cluster_sync_all();
+      }
+      edge = find_border(r, k, p);
+    }
 
     // ---------------------------------------------------------------- min-p
     if (min_p > 0.f && temperature > 0.f) {
@@ -1120,136 +1204,186 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     const float border = edge.value;
 
-    // ---------------------------------------------------------------- which of the equal ones
+    // ---------------------------------------------------------------- the kept mass, the token
+    // Of the entries that equal the border the first `ties` are kept; where that is not all of them, they are counted along
+    // with the mass of the others, and a running sum is the mass so far and the border's weight for each kept one of them.
     const bool part = !edge.known && edge.ties > 0 && edge.ties < edge.equal;
-    int cut = edge.known ? edge.cut : edge.ties > 0 ? 0x7fffffff : -1;   // the last index of them that is kept
+    int cut = edge.known ? edge.cut : edge.ties > 0 && !part ? 0x7fffffff : -1;   // the last index of them that is kept (part: none yet)
+    const u64 tie = part ? weight(r.s, sh.table, border) : 0;
+    auto kept = [&](float x, int at) { return x > border || (x == border && x > -INFINITY && at <= cut); };
+    total = edge.mass;
+    const bool sums = a.token || total == 0, find_cut = part && a.probs;
     // a warp's run of units
     const int run = (r.units + kWarps - 1) / kWarps, w0 = min(r.units, warp * run), w1 = min(r.units, w0 + run);
     const uint4* tile = reinterpret_cast<const uint4*>(dyn);
-    // The entry at which the running sum of g(x, index) over the row passes target: its index goes to `found` in
-    // the one block that holds it (the warps' sums being in sh.warps, those before this block `before`).
-    auto search = [&](u64 target, u64 before, auto g, auto found) {
-      u64 at = before;
-      int w = 0;
-      for (; w < kWarps && at + sh.warps[w] <= target; ++w) at += sh.warps[w];
-      if (before > target || w == kWarps) return;
-      // the warps share that run: a 32-unit piece each
-      const int i0 = min(r.units, w * run) + warp * 32 + lane, end = min(r.units, (w + 1) * run);
-      float x[U::n];
-      u64 v[U::n], mine = 0;
-      const int base = r.first + i0 * U::n;
-      if (warp * 32 < run) {
-        if (i0 < end) U::read(tile[i0], x);
-#pragma unroll
-        for (int e = 0; e < U::n; ++e) {
-          v[e] = i0 < end ? g(x[e], base + e) : 0;
-          mine += v[e];
-        }
-      }
-      u64 incl = mine;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const u64 up = __shfl_up_sync(kAll, incl, d);
-        if (lane >= d) incl += up;
-      }
-      if (lane == 31) sh.chunks[warp] = incl;
-      __syncthreads();
-      int c = 0, last = 0;
-      u64 from = at;
-      for (; c < kWarps && from + sh.chunks[c] <= target; ++c) {
-        from += sh.chunks[c];
-        if (sh.chunks[c]) last = c;
-      }
-      const bool none = c == kWarps;   // (sums of pieces and of the run differ by roundings: then the last entry)
-      if (warp == (none ? last : c)) {
-        const unsigned over = __ballot_sync(kAll, none ? mine > 0 : from + incl > target);
-        if (over && lane == (none ? 31 - __clz(over) : __ffs(over) - 1)) {
-          u64 s = from + incl - mine;
-          int hit = -1;
-#pragma unroll
-          for (int e = 0; e < U::n; ++e) {
-            s += v[e];
-            if (v[e] && (none || (s > target && hit < 0))) hit = base + e;
-          }
-          found(hit);
-        }
-      }
-      __syncthreads();
-    };
-    if (part) {
-      auto is = [&](float x, int) { return (u64)(x == border); };
-      u64 n = 0;
-      for (int i = w0 + lane; i < w1; i += 32) {
-        float x[U::n];
-        U::read(tile[i], x);
-#pragma unroll
-        for (int e = 0; e < U::n; ++e) n += is(x[e], 0);
-      }
-      u64 v[1] = {r.block_sum(n)}, before[1], sum[1];
-      r.cluster_sums(v, before, sum);
-      search(edge.ties - 1, before[0], is, [&](int at) {
-        for (int i = 0; i < ranks; ++i) st_cluster(ptx::dsmem_addr(&sh.cut, i), (uint32_t)at);
-      });
-      ptx::cluster_sync_all();
-      cut = sh.cut;
-    }
-
-    // ---------------------------------------------------------------- the kept mass, the token
-    total = edge.mass;
-    auto kept = [&](float x, int at) { return x > border || (x == border && x > -INFINITY && at <= cut); };
-    if (a.token || total == 0) {
-      u64 mine = 0;
+    if (sums || find_cut) {
       if constexpr (Row<T>::kValues) {
         // the weights of the bins' values that may be kept, once
         __syncthreads();
-        const int last = border > -INFINITY ? r.step_of(border) : Row<T>::kSteps - 2;
-        for (int i = tid; i <= min(last, Row<T>::kSteps - 2); i += kThreads)
-          if (r.one_value(i)) sh.weight[i] = weight(r.s, sh.table, r.value_of(i));
+        const int last = min(border > -INFINITY ? r.step_of(border) : Row<T>::kSteps - 2, Row<T>::kSteps - 2);
+        for (int i = tid; i <= last; i += kThreads)
+          sh.weight[(i + kFirstBin) & (kMaxSteps - 1)] = r.one_value(i) ? weight(r.s, sh.table, r.value_of(i)) : 0;
+        if (tid == 0) sh.weight[0] = 0;
         __syncthreads();
       }
       auto weight_of = [&](float x) -> u64 {
         if constexpr (Row<T>::kValues) {
           const int step = r.step_of(x);
-          if (r.one_value(step)) return sh.weight[step];
+          if (r.one_value(step)) return sh.weight[(step + kFirstBin) & (kMaxSteps - 1)];
         }
         return weight(r.s, sh.table, x);
       };
-      if constexpr (Row<T>::kValues) {
+      u64 mine = 0;
+      uint32_t equal = 0;
+      W2 acc = {{0}, {0}};
+      // bf16, where every kept logit is the value of a bin: two at once, those that are not kept at the bin without weight
+      const bool quick = Row<T>::kValues && border >= 0x1p-8f && top < kLarge;
+      if (Row<T>::kValues && quick) {
+        const __nv_bfloat162 b2 = __bfloat162bfloat162(__float2bfloat16_rd(border));   // (above the one is above the other)
+        const bool all_ties = edge.ties > 0 && !part;
         for (int i = w0 + lane; i < w1; i += 32) {
-          float x[U::n];
-          U::read(tile[i], x);
-          const int at = r.first + i * U::n;
+          const uint4 u = tile[i];
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 x2 = *reinterpret_cast<const __nv_bfloat162*>(&w[e]);
+            const uint32_t same = __heq2_mask(x2, b2), on = __hgt2_mask(x2, b2) | (all_ties ? same : 0u);
+            const uint32_t at = bins(w[e], magnitudes(w[e])) & on;
+            mine += sh.weight[at & 0xFFFFu];
+            mine += sh.weight[at >> 16];
+            equal += __popc(same);
+          }
+        }
+        equal = part ? equal / 16 : 0;
+      }
+      for (int i = quick ? w1 : w0 + lane; i < w1; i += 32) {
+        float x[U::n];
+        U::read(tile[i], x);
+        const int at = r.first + i * U::n;
+        bool some = false;
+#pragma unroll
+        for (int e = 0; e < U::n; ++e) some |= x[e] >= border;
+        if (!some) continue;
+        if (part)
+#pragma unroll
+          for (int e = 0; e < U::n; ++e) equal += x[e] == border;
+        if (!sums) continue;
+        if constexpr (Row<T>::kValues) {
 #pragma unroll
           for (int e = 0; e < U::n; ++e)
             if (kept(x[e], at + e)) mine += weight_of(x[e]);
-        }
-      } else {
-        W2 acc = {{0}, {0}};
-        for (int i = w0 + lane; i < w1; i += 32) {
-          float x[U::n];
-          U::read(tile[i], x);
-          const int at = r.first + i * U::n;
-          bool some = false;
-#pragma unroll
-          for (int e = 0; e < U::n; ++e) some |= kept(x[e], at + e);
-          if (!some) continue;
+        } else {
 #pragma unroll
           for (int e = 0; e < U::n; e += 2) {
             const W2 w = weights(r.s, sh.table, kept(x[e], at + e) ? x[e] : -INFINITY, kept(x[e + 1], at + e + 1) ? x[e + 1] : -INFINITY);
             accumulate(acc, w.hi, w.lo);
           }
         }
-        mine = fixed(acc);
       }
-      const u64 v[1] = {r.block_sum(mine)};
-      u64 before[1], sum[1];
-      r.cluster_sums(v, before, sum);
-      total = sum[0];
-      if (a.token) {
-        const float u = __ldg(a.u + row);
-        const u64 target = u > 0.f ? min(times(total, u, false), total - 1) : 0;
-        search(target, before[0], [&](float x, int i) { return kept(x, i) ? weight_of(x) : (u64)0; },
-               [&](int i) { a.token[row] = i; });
+      if (!Row<T>::kValues) mine = fixed(acc);
+      {   // the warps' sums stay in sh.warps and sh.equals
+        u64 e64 = equal;
+#pragma unroll
+        for (int m = 16; m >= 1; m >>= 1) e64 += __shfl_xor_sync(kAll, e64, m);
+        mine = r.block_sum(mine);
+        if (lane == 0) sh.equals[warp] = (uint32_t)e64;
+        __syncthreads();
+        e64 = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) e64 += sh.equals[w];
+        const u64 v[2] = {mine, e64};
+        u64 before[2], sum[2];
+        r.cluster_sums(v, before, sum);
+        if (sums) total = sum[0] + edge.ties * tie;
+        // The entry at which the running sum passes target: its index goes to `found` in the one block that holds it.
+        // kMass false: the running count of the border's equals instead.
+        auto search = [&](auto mass, u64 target, auto found) {
+          constexpr bool kMass = decltype(mass)::value;
+          const u64 each_tie = kMass ? tie : 1;
+          auto sum_at = [&](u64 m, u64 n) { return (kMass ? m : 0) + min(n, (u64)edge.ties) * each_tie; };
+          u64 m = before[0], n = before[1];
+          if (sum_at(m, n) > target) return;
+          int w = 0;
+          for (; w < kWarps && sum_at(m + sh.warps[w], n + sh.equals[w]) <= target; ++w) {
+            m += sh.warps[w];
+            n += sh.equals[w];
+          }
+          if (w == kWarps) return;
+          // the warps share that run: a 32-unit piece each
+          const int i0 = min(r.units, w * run) + warp * 32 + lane, end = min(r.units, (w + 1) * run);
+          const int base = r.first + i0 * U::n;
+          const bool there = warp * 32 < run && i0 < end;
+          float x[U::n];
+          u64 vm[U::n], im = 0;
+          uint32_t in = 0;
+          if (there) U::read(tile[i0], x);
+#pragma unroll
+          for (int e = 0; e < U::n; ++e) {
+            vm[e] = kMass && there && kept(x[e], base + e) ? weight_of(x[e]) : 0;
+            im += vm[e];
+            in += part && there && x[e] == border;
+          }
+          const u64 own_m = im;
+          const uint32_t own_n = in;
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const u64 um = __shfl_up_sync(kAll, im, d);
+            const uint32_t un = __shfl_up_sync(kAll, in, d);
+            if (lane >= d) {
+              im += um;
+              in += un;
+            }
+          }
+          if (lane == 31) {
+            sh.chunks[warp] = im;
+            sh.chunk_equals[warp] = in;
+          }
+          __syncthreads();
+          int c = 0, last = 0;
+          u64 last_m = m, last_n = n;
+          for (; c < kWarps && sum_at(m + sh.chunks[c], n + sh.chunk_equals[c]) <= target; ++c) {
+            if (sh.chunks[c] || (n < edge.ties && sh.chunk_equals[c])) {
+              last = c;
+              last_m = m;
+              last_n = n;
+            }
+            m += sh.chunks[c];
+            n += sh.chunk_equals[c];
+          }
+          const bool none = c == kWarps;   // (sums of pieces and of the run differ by roundings: then the last entry)
+          if (warp == (none ? last : c)) {
+            if (none) {
+              m = last_m;
+              n = last_n;
+            }
+            const bool holds = own_m > 0 || (own_n > 0 && n + in - own_n < edge.ties);
+            const unsigned over = __ballot_sync(kAll, none ? holds : sum_at(m + im, n + in) > target);
+            if (over && lane == (none ? 31 - __clz(over) : __ffs(over) - 1)) {
+              u64 sm = m + im - own_m, sn = n + in - own_n;
+              int hit = -1;
+#pragma unroll
+              for (int e = 0; e < U::n; ++e) {
+                const bool eq = part && x[e] == border && sn < edge.ties;
+                sm += vm[e];
+                sn += part && x[e] == border;
+                if ((vm[e] || eq) && (none || (sum_at(sm, sn) > target && hit < 0))) hit = base + e;
+              }
+              found(hit);
+            }
+          }
+          __syncthreads();
+        };
+        if (a.token) {
+          const float u = __ldg(a.u + row);
+          search(std::true_type(), u > 0.f ? min(times(total, u, false), total - 1) : 0, [&](int i) { a.token[row] = i; });
+        }
+        if (find_cut) {
+          search(std::false_type(), edge.ties - 1, [&](int at) {
+            for (int i = 0; i < ranks; ++i) st_cluster(ptx::dsmem_addr(&sh.cut, i), (uint32_t)at);
+          });
+          ptx::cluster_sync_all();
+          cut = sh.cut;
+        }
       }
     }
     if (a.probs) {
