@@ -134,6 +134,14 @@ __device__ __forceinline__ u64 times(u64 a, float f, bool up) {
   return r + (up && rest ? 1 : 0);
 }
 
+// The smallest n <= most with n w >= need (a 64-bit division takes longer than the rest of a search's end).
+__device__ __forceinline__ uint32_t least_ties(u64 need, u64 w, uint32_t most) {
+  const float q = fminf(__fdividef((float)need, (float)w), 4e6f);
+  uint32_t n = (uint32_t)fmaxf(q * (1.f - 0x1p-20f) - 1.f, 0.f);
+  while (n < most && n * w < need) ++n;
+  return min(n, most);
+}
+
 // Floats in order as integers (no nan, one zero).
 __device__ __forceinline__ uint32_t key_of(float x) {
   const uint32_t b = __float_as_uint(x);
@@ -304,6 +312,9 @@ struct Row {
   Shared* sh;
   Scale s;
   float top, steps;  // maximum, steps of the first histogram a unit of logits
+  uint32_t all_n;    // of the last block_scan
+  u64 all_m;
+  float all_f;
   int turn_s;
 
   // The step of a logit: it rises as the logit falls.
@@ -350,12 +361,12 @@ struct Row {
     __syncthreads();
     if ((threadIdx.x & 31) == 0) sh->warps[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0;
+    v = sh->warps[threadIdx.x & (kWarps - 1)];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += sh->warps[w];
+    for (int m = kWarps / 2; m >= 1; m >>= 1) v += __shfl_xor_sync(kAll, v, m);
     return v;
   }
-  // Sums over the threads before this one, of three kinds at once.
+  // Sums over the threads before this one, of three kinds at once; the sums of all in all_n, all_m, all_f.
   __device__ __forceinline__ void block_scan(uint32_t n, u64 m, float f, uint32_t& bn, u64& bm, float& bf) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t in = n;
@@ -378,14 +389,31 @@ struct Row {
       sh->scan_f[warp] = jf;
     }
     __syncthreads();
-    bn = in - n;
-    bm = im - m;
-    bf = jf - f;
-    for (int w = 0; w < warp; ++w) {
-      bn += sh->scan_n[w];
-      bm += sh->scan_m[w];
-      bf += sh->scan_f[w];
+    // the warps before this one, and all: every warp scans their sums
+    uint32_t wn = lane < kWarps ? sh->scan_n[lane] : 0;
+    u64 wm = lane < kWarps ? sh->scan_m[lane] : 0;
+    float wf = lane < kWarps ? sh->scan_f[lane] : 0.f;
+#pragma unroll
+    for (int d = 1; d < kWarps; d <<= 1) {
+      const uint32_t un = __shfl_up_sync(kAll, wn, d);
+      const u64 um = __shfl_up_sync(kAll, wm, d);
+      const float uf = __shfl_up_sync(kAll, wf, d);
+      if (lane >= d) {
+        wn += un;
+        wm += um;
+        wf += uf;
+      }
     }
+    const int prev = max(warp - 1, 0);
+    const uint32_t pn = __shfl_sync(kAll, wn, prev);
+    const u64 pm = __shfl_sync(kAll, wm, prev);
+    const float pf = __shfl_sync(kAll, wf, prev);
+    bn = in - n + (warp ? pn : 0);
+    bm = im - m + (warp ? pm : 0);
+    bf = jf - f + (warp ? pf : 0.f);
+    all_n = __shfl_sync(kAll, wn, kWarps - 1);
+    all_m = __shfl_sync(kAll, wm, kWarps - 1);
+    all_f = __shfl_sync(kAll, wf, kWarps - 1);
     __syncthreads();
   }
 
@@ -699,9 +727,9 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
   r.block_scan(sum_n, sum_m, sum_f, bn, bm, bf);
 
   // ------------------------------------------------------------------ the step of the k-th logit
-  uint32_t total_n = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) total_n += sh.scan_n[w];
+  const uint32_t total_n = r.all_n;
+  const u64 total_m = r.all_m;
+  const float total_f = r.all_f;
   const bool k_on = cuts_k && (uint32_t)k < total_n;
   int k_step = kSteps;
   uint32_t k_above = 0, k_equal = 0;
@@ -746,8 +774,7 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
     if (!cuts_p) return out;
     u64 all = 0;
     if (!k_on) {
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) all += sh.scan_m[w];
+      all = total_m;
     } else if (r.one_value(k_step)) {
       all = k_mass + out.ties * weight(r.s, sh.table, out.value);
     } else {
@@ -779,7 +806,7 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
     need -= above;
     if (r.one_value(step)) {
       const u64 w = max((u64)1, weight(r.s, sh.table, r.value_of(step)));
-      const uint32_t ties = (uint32_t)min((u64)equal, (need + w - 1) / w);
+      const uint32_t ties = least_ties(need, w, equal);
       if (k_on && step == k_step) {
         out.ties = min(out.ties, ties);
       } else {
@@ -795,7 +822,7 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
     if (r.template refine<true>(lo, hi, need, key, n_key) && (!k_on || of_key(key) >= out.value)) {
       const float b = of_key(key);
       const u64 w = max((u64)1, weight(r.s, sh.table, b));
-      const uint32_t ties = (uint32_t)min((u64)n_key, (need + w - 1) / w);
+      const uint32_t ties = least_ties(need, w, n_key);
       if (k_on && b == out.value) {
         out.ties = min(out.ties, ties);
       } else {
@@ -813,9 +840,7 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
     if (cuts_p && !k_on) {
       // Between the running sums' bounds: a step's weights lie within a factor of 2^(-1/128) of its upper end's (the
       // last step's between 0 and that); 2^-10 for the sums' own roundings and those of the steps' borders.
-      float all = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) all += sh.scan_f[w];
+      const float all = total_f;
       if (tid == 0) {
         sh.bin = kSteps - 1;
         sh.bin2 = kSteps - 1;
@@ -999,11 +1024,7 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
         }
         if (cuts_p) {
           r.block_scan(0, mass, 0.f, un, before, uf);
-          if (k_on) {
-            all = 0;
-#pragma unroll
-            for (int v = 0; v < kWarps; ++v) all += sh.scan_m[v];
-          }
+          if (k_on) all = r.all_m;
         }
         const int most = k_on ? min(k, count) : count;
         if (tid == 0) sh.bin = most - 1;
@@ -1052,7 +1073,7 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
       const u64 want = max((u64)1, times(all, p, true));
       if (want > mass[0]) {   // inside the tokens that equal the k-th
         const u64 w = max((u64)1, weight(r.s, sh.table, b));
-        out.ties = (uint32_t)min((u64)out.ties, (want - mass[0] + w - 1) / w);
+        out.ties = least_ties(want - mass[0], w, out.ties);
         return out;
       }
     }
@@ -1067,7 +1088,7 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
     if (r.template refine<true>(lo, hi, need, key, n_key)) {
       out.value = of_key(key);
       const u64 w = max((u64)1, weight(r.s, sh.table, out.value));
-      out.ties = (uint32_t)min((u64)n_key, (need + w - 1) / w);
+      out.ties = least_ties(need, w, n_key);
       out.equal = n_key;
     }
     return out;
@@ -1282,15 +1303,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
       if (!Row<T>::kValues) mine = fixed(acc);
       {   // the warps' sums stay in sh.warps and sh.equals
-        u64 e64 = equal;
+        equal = __reduce_add_sync(kAll, equal);
+        if (lane == 0) sh.equals[warp] = equal;
+        mine = r.block_sum(mine);   // (its barriers are behind this write, too)
+        u64 e64;
+        e64 = sh.equals[lane & (kWarps - 1)];
 #pragma unroll
-        for (int m = 16; m >= 1; m >>= 1) e64 += __shfl_xor_sync(kAll, e64, m);
-        mine = r.block_sum(mine);
-        if (lane == 0) sh.equals[warp] = (uint32_t)e64;
-        __syncthreads();
-        e64 = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) e64 += sh.equals[w];
+        for (int m = kWarps / 2; m >= 1; m >>= 1) e64 += __shfl_xor_sync(kAll, e64, m);
         const u64 v[2] = {mine, e64};
         u64 before[2], sum[2];
         r.cluster_sums(v, before, sum);
@@ -1301,14 +1320,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
           constexpr bool kMass = decltype(mass)::value;
           const u64 each_tie = kMass ? tie : 1;
           auto sum_at = [&](u64 m, u64 n) { return (kMass ? m : 0) + min(n, (u64)edge.ties) * each_tie; };
+          // the first of kWarps parts (lane's: pm, pn) that passes; m and n are then what lies before it, or before the last
+          // part that holds anything where none passes (their sums differ from the whole's by roundings)
           u64 m = before[0], n = before[1];
+          auto first_part = [&](u64 pm, uint32_t pn, bool& none) {
+            u64 im = pm;
+            uint32_t in = pn;
+#pragma unroll
+            for (int d = 1; d < kWarps; d <<= 1) {
+              const u64 um = __shfl_up_sync(kAll, im, d);
+              const uint32_t un = __shfl_up_sync(kAll, in, d);
+              if (lane >= d) {
+                im += um;
+                in += un;
+              }
+            }
+            const u64 m0 = m + im - pm, n0 = n + in - pn;
+            const unsigned over = __ballot_sync(kAll, lane < kWarps && sum_at(m + im, n + in) > target);
+            const unsigned holds = __ballot_sync(kAll, lane < kWarps && (pm || (pn && n0 < edge.ties)));
+            none = over == 0;
+            const int who = over ? __ffs(over) - 1 : holds ? 31 - __clz(holds) : 0;
+            m = __shfl_sync(kAll, m0, who);
+            n = __shfl_sync(kAll, n0, who);
+            return who;
+          };
           if (sum_at(m, n) > target) return;
-          int w = 0;
-          for (; w < kWarps && sum_at(m + sh.warps[w], n + sh.equals[w]) <= target; ++w) {
-            m += sh.warps[w];
-            n += sh.equals[w];
-          }
-          if (w == kWarps) return;
+          bool none;
+          const int w = first_part(sh.warps[lane & (kWarps - 1)], sh.equals[lane & (kWarps - 1)], none);
+          if (none) return;
           // the warps share that run: a 32-unit piece each
           const int i0 = min(r.units, w * run) + warp * 32 + lane, end = min(r.units, (w + 1) * run);
           const int base = r.first + i0 * U::n;
@@ -1339,23 +1378,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
             sh.chunk_equals[warp] = in;
           }
           __syncthreads();
-          int c = 0, last = 0;
-          u64 last_m = m, last_n = n;
-          for (; c < kWarps && sum_at(m + sh.chunks[c], n + sh.chunk_equals[c]) <= target; ++c) {
-            if (sh.chunks[c] || (n < edge.ties && sh.chunk_equals[c])) {
-              last = c;
-              last_m = m;
-              last_n = n;
-            }
-            m += sh.chunks[c];
-            n += sh.chunk_equals[c];
-          }
-          const bool none = c == kWarps;   // (sums of pieces and of the run differ by roundings: then the last entry)
-          if (warp == (none ? last : c)) {
-            if (none) {
-              m = last_m;
-              n = last_n;
-            }
+          const int c = first_part(sh.chunks[lane & (kWarps - 1)], sh.chunk_equals[lane & (kWarps - 1)], none);
+          if (warp == c) {
             const bool holds = own_m > 0 || (own_n > 0 && n + in - own_n < edge.ties);
             const unsigned over = __ballot_sync(kAll, none ? holds : sum_at(m + im, n + in) > target);
             if (over && lane == (none ? 31 - __clz(over) : __ffs(over) - 1)) {
