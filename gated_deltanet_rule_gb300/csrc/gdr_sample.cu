@@ -103,6 +103,14 @@ __device__ __forceinline__ u64 weight(const Scale& s, const float2* table, float
   unpack(w.lo, lo, g);
   return fixed(h, lo);
 }
+__device__ __forceinline__ void weight(const Scale& s, const float2* table, float l0, float l1, u64& w0, u64& w1) {
+  const W2 w = weights(s, table, l0, l1);
+  float h0, h1, g0, g1;
+  unpack(w.hi, h0, h1);
+  unpack(w.lo, g0, g1);
+  w0 = fixed(h0, g0);
+  w1 = fixed(h1, g1);
+}
 // A running sum of pairs.
 __device__ __forceinline__ void accumulate(W2& acc, F2 hi, F2 lo) {
   const F2 s = add(acc.hi, hi), bb = sub(s, acc.hi);
@@ -417,6 +425,15 @@ struct Row {
     __syncthreads();
   }
 
+  // bf16: the weights of two neighbouring bins' values (of an even step and the next; 0 where a bin holds more than a value)
+  // into sh->weight.
+  __device__ __forceinline__ void weigh(int step, u64& w0, u64& w1) const {
+    gdr::weight(s, sh->table, value_of(step), value_of(step + 1), w0, w1);
+    if (!one_value(step)) w0 = 0;
+    if (!one_value(step + 1)) w1 = 0;
+    *reinterpret_cast<ulonglong2*>(sh->weight + ((step + kFirstBin) & (kMaxSteps - 1))) = make_ulonglong2(w0, w1);
+  }
+
   // Calls f(x[n], index of x[0]) for the block's units, a thread's share.
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
@@ -651,6 +668,7 @@ struct Border {
   uint32_t ties, equal;   // how many of the equal ones are kept, and how many there are
   int cut;
   bool known;             // cut is given (ties and equal are not needed)
+  bool weighed;           // bf16: the weights of the row's values lie in Shared::weight
   u64 mass;               // of what is kept, where it came about (0: not)
 };
 
@@ -661,7 +679,7 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
   constexpr int kMine = Row<T>::kMine, kSteps = Row<T>::kSteps;
   Shared& sh = *r.sh;
   const int tid = threadIdx.x, s0 = tid * kMine;
-  Border out = {-INFINITY, 0, 0, -1, false, 0};
+  Border out = {-INFINITY, 0, 0, -1, false, false, 0};
   const bool cuts_k = k > 0, cuts_p = p < 1.f;
   uint32_t n[kMine];
   u64 others[3] = {0, 0, 0};
@@ -708,12 +726,20 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
   for (int i = 0; i < kMine; ++i) {
     sum_n += n[i];
     m[i] = 0;
-    if (Row<T>::kValues) {
-      if (n[i] && cuts_p && r.one_value(s0 + i)) m[i] = n[i] * weight(r.s, sh.table, r.value_of(s0 + i));
-      sum_m += m[i];
-    } else {
-      sum_f += (float)n[i] * ptx::ex2_approx(-(float)(s0 + i) * (1.f / kPerOctave));
+    if (!Row<T>::kValues) sum_f += (float)n[i] * ptx::ex2_approx(-(float)(s0 + i) * (1.f / kPerOctave));
+  }
+  if (Row<T>::kValues && cuts_p) {
+    // (the kept mass is added up from these weights, too; of bins that hold nothing none is needed)
+#pragma unroll
+    for (int i = 0; i < kMine; i += 2) {
+      if (n[i] == 0 && n[i + 1] == 0) continue;
+      u64 w0, w1;
+      r.weigh(s0 + i, w0, w1);
+      m[i] = n[i] * w0;
+      m[i + 1] = n[i + 1] * w1;
+      sum_m += m[i] + m[i + 1];
     }
+    out.weighed = true;
   }
   if (Row<T>::kValues) {
     constexpr int at[3] = {0, kMiddleStep, kSteps - 1};
@@ -767,6 +793,7 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
         r.step_keys(k_step, lo, hi);
         r.template refine<false>(lo, hi, need, key, n_key);
         out.value = of_key(key);
+        out.weighed = false;
       }
       out.ties = (uint32_t)need;
       out.equal = n_key;
@@ -819,6 +846,7 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
     }
     uint32_t lo, hi, key, n_key;
     r.step_keys(step, lo, hi);
+    out.weighed = false;   // (its place is written anew)
     if (r.template refine<true>(lo, hi, need, key, n_key) && (!k_on || of_key(key) >= out.value)) {
       const float b = of_key(key);
       const u64 w = max((u64)1, weight(r.s, sh.table, b));
@@ -1203,7 +1231,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       r.s.least = fmaxf((r.s.mh - 150.f) / r.s.ch, -FLT_MAX);
       r.steps = r.s.ch * (float)kPerOctave;
     }
-    Border edge = {-INFINITY, 0, 0, -1, false, 0};
+    Border edge = {-INFINITY, 0, 0, -1, false, false, 0};
     if (filters) {
       if (!Row<T>::kValues) {
         r.each([&](const float* x, int) {
@@ -1220,7 +1248,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const double least = (double)top + sh.min_p;
       const float f = __double2float_ru(least) + 0.f;   // the smallest logit that is kept
       if (f > edge.value) {
-        edge = {of_key(key_of(f) - (f == 0.f ? 2 : 1)), 0, 0, -1, true, 0};   // the float below it
+        edge = {of_key(key_of(f) - (f == 0.f ? 2 : 1)), 0, 0, -1, true, edge.weighed, 0};   // the float below it
       }
     }
     const float border = edge.value;
@@ -1242,9 +1270,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
         // the weights of the bins' values that may be kept, once
         __syncthreads();
         const int last = min(border > -INFINITY ? r.step_of(border) : Row<T>::kSteps - 2, Row<T>::kSteps - 2);
-        for (int i = tid; i <= last; i += kThreads)
-          sh.weight[(i + kFirstBin) & (kMaxSteps - 1)] = r.one_value(i) ? weight(r.s, sh.table, r.value_of(i)) : 0;
-        if (tid == 0) sh.weight[0] = 0;
+        u64 unused0, unused1;
+        for (int i = 2 * tid; !edge.weighed && i <= last; i += 2 * kThreads) r.weigh(i, unused0, unused1);
+        if (tid == 0) sh.weight[0] = sh.weight[kMaxSteps - 1] = sh.weight[kTop] = 0;   // (around zero, and the rest)
         __syncthreads();
       }
       auto weight_of = [&](float x) -> u64 {
@@ -1256,52 +1284,57 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       };
       u64 mine = 0;
       uint32_t equal = 0;
-      W2 acc = {{0}, {0}};
-      // bf16, where every kept logit is the value of a bin: two at once, those that are not kept at the bin without weight
-      const bool quick = Row<T>::kValues && border >= 0x1p-8f && top < kLarge;
-      if (Row<T>::kValues && quick) {
+      if constexpr (Row<T>::kValues) {
+        // two at once: those that are not kept at a bin without weight, as are those whose bin holds more than one value; kept
+        // ones of these (few, or none) are added by themselves
         const __nv_bfloat162 b2 = __bfloat162bfloat162(__float2bfloat16_rd(border));   // (above the one is above the other)
         const bool all_ties = edge.ties > 0 && !part;
         for (int i = w0 + lane; i < w1; i += 32) {
           const uint4 u = tile[i];
           const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+          uint32_t odd = 0;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const __nv_bfloat162 x2 = *reinterpret_cast<const __nv_bfloat162*>(&w[e]);
             const uint32_t same = __heq2_mask(x2, b2), on = __hgt2_mask(x2, b2) | (all_ties ? same : 0u);
-            const uint32_t at = bins(w[e], magnitudes(w[e])) & on;
+            const uint32_t v = magnitudes(w[e]), at = bins(w[e], v) & on;
             mine += sh.weight[at & 0xFFFFu];
             mine += sh.weight[at >> 16];
             equal += __popc(same);
+            odd |= ((v - 0x00010001u) | (v + (0x8000u - kTop) * 0x10001u)) & on;   // v = 0 (or next to one), v = kTop
+          }
+          if (odd & 0x80008000u) {
+            float x[U::n];
+            U::read(u, x);
+            const int at = r.first + i * U::n;
+#pragma unroll
+            for (int e = 0; e < U::n; ++e)
+              if (kept(x[e], at + e) && !r.one_value(r.step_of(x[e]))) mine += weight(r.s, sh.table, x[e]);
           }
         }
         equal = part ? equal / 16 : 0;
-      }
-      for (int i = quick ? w1 : w0 + lane; i < w1; i += 32) {
-        float x[U::n];
-        U::read(tile[i], x);
-        const int at = r.first + i * U::n;
-        bool some = false;
+      } else {
+        W2 acc = {{0}, {0}};
+        for (int i = w0 + lane; i < w1; i += 32) {
+          float x[U::n];
+          U::read(tile[i], x);
+          const int at = r.first + i * U::n;
+          bool some = false;
 #pragma unroll
-        for (int e = 0; e < U::n; ++e) some |= x[e] >= border;
-        if (!some) continue;
-        if (part)
+          for (int e = 0; e < U::n; ++e) some |= x[e] >= border;
+          if (!some) continue;
+          if (part)
 #pragma unroll
-          for (int e = 0; e < U::n; ++e) equal += x[e] == border;
-        if (!sums) continue;
-        if constexpr (Row<T>::kValues) {
-#pragma unroll
-          for (int e = 0; e < U::n; ++e)
-            if (kept(x[e], at + e)) mine += weight_of(x[e]);
-        } else {
+            for (int e = 0; e < U::n; ++e) equal += x[e] == border;
+          if (!sums) continue;
 #pragma unroll
           for (int e = 0; e < U::n; e += 2) {
             const W2 w = weights(r.s, sh.table, kept(x[e], at + e) ? x[e] : -INFINITY, kept(x[e + 1], at + e + 1) ? x[e + 1] : -INFINITY);
             accumulate(acc, w.hi, w.lo);
           }
         }
+        mine = fixed(acc);
       }
-      if (!Row<T>::kValues) mine = fixed(acc);
       {   // the warps' sums stay in sh.warps and sh.equals
         equal = __reduce_add_sync(kAll, equal);
         if (lane == 0) sh.equals[warp] = equal;
@@ -1453,10 +1486,11 @@ const Table& table() {
 
 template <typename T>
 cudaError_t launch(SampleArgs a, cudaStream_t s) {
-  // Blocks of a row: enough for their parts to fit two an SM, and more of them while there are few rows.
+  // Blocks of a row: enough for their parts to fit two an SM, and more of them while all rows' blocks are resident at once
+  // (48 rows of 49999: 45 us by two, 37 by four, 52 by eight, which are not).
   auto bytes = [&](int c) { return (((a.V + Unit<T>::n - 1) / Unit<T>::n + 1 + c - 1) / c) * 16; };
   a.cluster = 1;
-  while (a.cluster < kMaxCluster && (bytes(a.cluster) > kTarget || (a.R * a.cluster < 2 * kNumSMs && bytes(a.cluster) > 16 * kThreads)))
+  while (a.cluster < kMaxCluster && (bytes(a.cluster) > kTarget || (2ll * a.R * a.cluster <= 2 * kNumSMs && bytes(a.cluster) > 16 * kThreads)))
     a.cluster *= 2;
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(sample_kernel<T>), 160 << 10, done);
