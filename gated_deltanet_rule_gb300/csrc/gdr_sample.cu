@@ -730,9 +730,12 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
   }
   if (Row<T>::kValues && cuts_p) {
     // (the kept mass is added up from these weights, too; of bins that hold nothing none is needed)
+    uint32_t some = 0;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) some |= n[i];
+    if (some)
 #pragma unroll
     for (int i = 0; i < kMine; i += 2) {
-      if (n[i] == 0 && n[i + 1] == 0) continue;
       u64 w0, w1;
       r.weigh(s0 + i, w0, w1);
       m[i] = n[i] * w0;
