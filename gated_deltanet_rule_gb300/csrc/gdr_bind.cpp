@@ -442,14 +442,14 @@ struct Block {
     if (t.scalar_type() != like.scalar_type() || t.sizes() != like.sizes()) refuse("%s must have h's dtype and shape", name);
     const int64_t n = t.dim();
     if (t.size(n - 1) > 1 && t.stride(n - 1) != 1) refuse("%s: the last dimension must be contiguous", name);
-    long long row = 0, step = 0;   // stride of a row; what the next dimension's has to be
+    long long row = -1, step = 0;   // stride of a row; what the next dimension's has to be
     for (int64_t d = n - 2; d >= 0; --d) {
       if (t.size(d) == 1) continue;
-      if (!row) row = t.stride(d);
-      else if (t.stride(d) != step) refuse("%s: rows must lie at one stride", name);
+      if (row < 0) row = t.stride(d);
+      if (t.stride(d) < 1 || (step && t.stride(d) != step)) refuse("%s: rows must lie at one stride", name);
       step = t.stride(d) * t.size(d);
     }
-    return row ? row : t.size(n - 1);
+    return row < 0 ? t.size(n - 1) : row;
   }
   // arguments 0 .. 5: h, y, pre_w, post_w, gate, scale
   explicit Block(const Call& c) {

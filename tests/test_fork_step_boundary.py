@@ -192,6 +192,10 @@ def test_layouts():
     _refused(_b_sample, "drawn with u", u=None)
     _refused(_b_norm, "last dimension", y=T((2, 5, 64), BF16, strides=(640, 128, 2)))
     _refused(_b_norm, "one stride", gate=T((2, 5, 64), BF16, strides=(1000, 128, 1)))
+    for shape, strides in (((2, 64), (0, 1)), ((2, 5, 64), (0, 0, 1)), ((2, 5, 64), (64, 0, 1)), ((2, 5, 64), (0, 64, 1))):   # expanded rows
+        for name in ("y", "gate"):
+            like = {n: T(shape, BF16) for n in ("h", "y", "gate", "h_out", "n_out")}
+            _refused(_b_norm, "one stride", **{**like, name: T(shape, BF16, strides=strides)})
     _refused(_b_norm, "contiguous", h=T((2, 5, 64), BF16, strides=(640, 128, 1)))
     _refused(_b_fork, "wrong shape", first=T((4,)))
     _refused(_b_fork, r"\[T\]", shared=T((2, 1)))
