@@ -100,7 +100,17 @@ __device__ __forceinline__ Item item_of(const OwnArgs& a, long long at, bool fal
   const int ctx = __ldg(a.ctx + t.b);
   t.shared = 0;
   bool valid = !falls;
-  for (int g0 = 0; g0 < a.T; g0 += 32) {
+  // The one group that holds row b among groups g0 .. g0 + 31: of more than these, the last that begins at or before it and
+  // those around it, a factor of 32 a step. (Where `first` falls what is found is not used.)
+  int g0 = 0;
+  for (int left = a.T; left > 32;) {
+    const int step = (left + 31) >> 5, g = g0 + lane * step;
+    const int before = __popc(__ballot_sync(0xffffffffu, lane * step < left && __ldg(a.first + g) <= t.b));
+    const int at = max(before - 1, 0) * step;
+    g0 += at;
+    left = min(step, left - at);
+  }
+  {
     const int g = g0 + lane;
     int f0 = 0, f1 = 0, sh = 0;
     if (g < a.T) {
@@ -109,11 +119,11 @@ __device__ __forceinline__ Item item_of(const OwnArgs& a, long long at, bool fal
       sh = __ldg(a.shared + g);
     }
     const unsigned mine = __ballot_sync(0xffffffffu, f0 <= t.b && t.b < f1);
-    if (!mine) continue;
-    const int who = __ffs(mine) - 1;
-    valid = valid && __shfl_sync(0xffffffffu, (int)group_valid(f0, f1, sh, a.B, a.page, a.M), who);
-    t.shared = __shfl_sync(0xffffffffu, sh, who);
-    break;
+    if (mine) {
+      const int who = __ffs(mine) - 1;
+      valid = valid && __shfl_sync(0xffffffffu, (int)group_valid(f0, f1, sh, a.B, a.page, a.M), who);
+      t.shared = __shfl_sync(0xffffffffu, sh, who);
+    }
   }
   valid = valid && t.n >= 0 && t.n <= a.N && ctx >= t.shared && (long long)ctx + t.n <= (long long)a.M * a.page;
   if (!valid) {

@@ -108,6 +108,17 @@ def test_more_groups_than_blocks_and_rows_than_threads():
     _check(_case(first, [16 * (t % 5) for t in range(200)], [0, 40, 3, 129, 17], 2, 4, 2, 64, 16, seed=3, lengths=[2, 1, 0, 2]))
 
 
+@pytest.mark.parametrize("T", [31, 32, 33, 64, 65, 1025])
+def test_many_groups(T):
+    """Groups of no rows, one and some, rows before and behind all of them."""
+    first = [1]
+    for t in range(T):
+        first.append(first[-1] + (0, 1, 1, 0, 0, 2, 0)[t % 7])
+    rows = _case(first, [16 * (t % 3) for t in range(T)], [0, 5, 21], 1, 2, 1, 64, 16, seed=T)
+    tail = {n: torch.cat([rows[n], rows[n][:1]]) for n in ("q", "ctx", "lengths", "table", "see")}   # (row 0 is in no group either)
+    _check({**rows, **tail})
+
+
 @pytest.mark.parametrize("D,page,B,N", [(64, 16, 3, 1), (128, 64, 2, 3), (256, 128, 2, 2), (128, 32, 40, 8)])
 def test_long_trunk_is_split_over_blocks(D, page, B, N):
     _check(_case([0, B], [20096], [77, 1], N, 4, 2 if B < 10 else 1, D, page, seed=5))
