@@ -221,3 +221,22 @@ def test_captured_and_replayed():
         run()
         assert torch.equal(t1, token) and torch.equal(p1, probs)
     gdr.gdr_sync_status()
+
+
+@pytest.mark.parametrize("filters", ["none", "k", "p", "kp", "min_p"])
+@pytest.mark.parametrize("shift,scale", [(0, 1e-3), (0, 0.02), (0, 1.0), (0, 60.0), (0, 400.0), (-120, 5.0), (-130, 0.5), (126, 1.0), (300, 100.0)])
+def test_bf16_logits_of_every_size(shift, scale, filters):
+    """Values that are counted one by one, those around zero and the large ones, on either side of the border."""
+    R, V = 6, 20011
+    x = (_logits(R, V, torch.float32, 11, scale=1.0) * scale + shift).bfloat16()
+    x[0, ::3] = 0.0
+    x[1, ::5] = -0.0
+    x[2, 7::11] = float("-inf")
+    a = _params(R, 11)
+    T = [t * max(scale, 0.01) for t in a["T"]]
+    kw = dict(k=[0, 10000, 13500, 40, 20000, 9000]) if filters in ("k", "kp") else {}
+    if filters in ("p", "kp"):
+        kw["p"] = [0.5, 0.7, 0.99, 0.9, 0.75, 0.6]
+    if filters == "min_p":
+        kw["m"] = [0.3, 0.5, 0.01, 1e-6, 0.9, 0.1]
+    _check(x, T, a["u"], **kw)
