@@ -66,11 +66,36 @@ struct Item {
 struct OwnBars {
   uint64_t full[4], empty[4], item_full[2], item_empty[2];
   Item item[2];
+  template <int NS>
+  __device__ void init(int warps) {   // (one thread)
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], warps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], warps);
+    }
+  }
 };
 
 // 16-byte unit ch of row r in tiles of `rows` rows, 64 columns (128 bytes) at a time, swizzled as TMA writes them.
 __device__ __forceinline__ uint32_t unit_at(int rows, int r, int ch) {
   return (uint32_t)((ch >> 3) * rows * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+}
+// Zeroes what is not finite; whether there was any.
+__device__ __forceinline__ bool finite_only(uint4& v) {
+  uint32_t* u = reinterpret_cast<uint32_t*>(&v);
+  uint32_t hit = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) hit |= ((u[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+  if (!hit) return false;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if ((u[e] & 0x7F80u) == 0x7F80u) u[e] &= 0xFFFF0000u;
+    if ((u[e] & 0x7F800000u) == 0x7F800000u) u[e] &= 0xFFFFu;
+  }
+  return true;
 }
 __device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -81,14 +106,40 @@ __device__ __forceinline__ void ldmatrix4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// A row's own and shared parts joined: their weights are own / total and shared / total (own's accumulator still lacks its
+// sum l); m: the greatest score in binary orders.
+struct Factors {
+  float own, shared, total, lse;
+  bool sees, rare;   // it sees something of its own; a weight vanished that is not 0
+};
+__device__ __forceinline__ Factors factors(bool used, bool joins, float m, float l, float lse_s) {
+  Factors f;
+  f.sees = used && (l > 0.f || l != l);
+  const float lse = f.sees ? m * (1.f / kLog2e) + logf(l) : -INFINITY, ref = fmaxf(lse, lse_s);
+  f.own = f.sees ? 1.f : 0.f;
+  f.shared = 0.f;
+  f.total = 1.f;
+  f.lse = lse;
+  f.rare = false;
+  if (lse != lse || lse_s != lse_s) {
+    f.own = f.shared = f.total = NAN;
+  } else if (joins && ref > -INFINITY) {
+    f.own = lse == ref ? 1.f : ex2_approx((lse - ref) * kLog2e);
+    f.shared = lse_s == ref ? 1.f : ex2_approx((lse_s - ref) * kLog2e);
+    f.rare = (f.own == 0.f && lse != -INFINITY) || (f.shared == 0.f && lse_s != -INFINITY);
+    f.total = f.own + f.shared;
+  }
+  if (joins) f.lse = ref == -INFINITY && f.total == f.total ? -INFINITY : ref + logf(f.total);
+  return f;
+}
+
 // The row's group and its numbers (a whole warp; every lane gets the item). falls: `first` is not rising.
-template <int D, int WR>
+template <class C>
 __device__ __forceinline__ Item item_of(const OwnArgs& a, long long at, bool falls) {
-  using C = Own<D, WR>;
   const int lane = threadIdx.x & 31;
   Item t;
   const int mt = (int)(at % a.m_tiles), row = (int)(at / a.m_tiles);
@@ -141,6 +192,73 @@ __device__ __forceinline__ Item item_of(const OwnArgs& a, long long at, bool fal
   return t;
 }
 
+// The loading warp of a team: items at0, at0 + stride, ... , two of them and NS tiles ahead of what is computed.
+template <int D, class C>
+__device__ __forceinline__ void load_items(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const OwnArgs& a, OwnBars& s,
+                                           uint8_t* sm, long long at0, long long stride, int lane) {
+  constexpr int KT = C::KT, NS = C::NS;
+  const long long items = (long long)a.B * a.Hk * a.m_tiles;
+  bool falls = false;
+  for (int t = lane; t < a.T; t += 32) falls |= __ldg(a.first + t) > __ldg(a.first + t + 1);
+  falls = __any_sync(0xffffffffu, falls);
+  const int rows = min(a.page, KT), most = KT / rows;   // positions of one box, boxes of a tile
+  const uint32_t box = rows * 128u;                     // its bytes in one 64-column slab
+  Ring<NS> ring;
+  bool ok = true;
+  int loads = 0, q_loads = 0, k = 0;
+  for (long long at = at0; ok && at < items; at += stride, ++k) {
+    const Item t = item_of<C>(a, at, falls);
+    if (k >= 2) ok = warp_wait(&s.item_empty[k & 1], ((k >> 1) & 1) ^ 1, a.budget);
+    if (!ok) break;
+    // the queries: row (node, head) as the box leaves them; rows behind it hold anything and are not used
+    if (lane == 0) {
+      s.item[k & 1] = t;
+      mbar_arrive_expect_tx(&s.item_full[k & 1], (uint32_t)(D / 64) * a.heads * a.npt * 128u);
+      for (int h = 0; h < D / 64; ++h)
+        tma_load_4d(sm + (k & 1) * C::kQ + h * C::kRows * 128, &mq, &s.item_full[k & 1], h * 64, t.hk * a.G + t.h0, t.node0, t.b);
+    }
+    __syncwarp();
+    ++q_loads;
+    // its positions
+    const int end = t.tiles == 0 ? 0 : t.own + t.n;
+    const int32_t* table = a.table + (size_t)t.b * a.M + (t.shared >> a.page_shift);
+    auto page_at = [&](int tile) {
+      const int pos = tile * KT + lane * rows;
+      return lane < most && pos < end ? __ldg(table + (pos >> a.page_shift)) : -1;
+    };
+    int pg = page_at(0);
+    for (int tile = 0; tile < t.tiles; ++tile) {
+      const int pieces = min(most, (end - tile * KT + rows - 1) / rows), in_page = (tile * KT + lane * rows) & (a.page - 1);
+      int src = pg;
+      if (tile + 1 < t.tiles) pg = page_at(tile + 1);
+      if (lane < pieces && (src < 0 || src >= a.P)) {   // read as zeros (outside the tensor) and reported
+        atomicCAS(a.err, 0, kErrDeviceIndex);
+        src = -1;
+      }
+      const int slot = ring.slot;
+      if (loads == NS) ok = warp_wait(&s.empty[slot], ring.parity ^ 1, a.budget);
+      else ++loads;
+      if (!ok) break;
+      if (lane == 0) mbar_arrive_expect_tx(&s.full[slot], 2 * pieces * box * (D / 64));
+      __syncwarp();
+      if (lane < pieces) {
+        uint8_t* dst = sm + C::kRing + slot * 2 * C::kTile + lane * box;
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+          tma_load_4d(dst + h * KT * 128, &mk, &s.full[slot], h * 64, t.hk, in_page, src);
+          tma_load_4d(dst + C::kTile + h * KT * 128, &mv, &s.full[slot], h * 64, t.hk, in_page, src);
+        }
+      }
+      __syncwarp();
+      ring.step(1);
+    }
+  }
+  // no copy of this block is left in flight
+  for (int i = 0; i < loads; ++i) warp_wait(&s.full[i], i < ring.slot ? ring.parity : ring.parity ^ 1, kDrainBudget);
+  for (int i = max(0, q_loads - 2); i < q_loads; ++i) warp_wait(&s.item_full[i & 1], (i >> 1) & 1, kDrainBudget);
+  if (!ok && lane == 0) atomicCAS(a.err, 0, kErrTimeout);
+}
+
 template <int D, int WR>
 __global__ void __launch_bounds__(kOwnThreads, D == 256 ? 1 : 2)
     fork_own_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const __grid_constant__ OwnArgs a) {
@@ -156,14 +274,7 @@ __global__ void __launch_bounds__(kOwnThreads, D == 256 ? 1 : 2)
     return;
   }
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) {
-      mbar_init(&s.full[i], 1);
-      mbar_init(&s.empty[i], kOwnWarps);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.item_full[i], 1);
-      mbar_init(&s.item_empty[i], kOwnWarps);
-    }
+    s.template init<NS>(kOwnWarps);
     s_bad = -1;
     fence_mbar_init();
     prefetch_tmap(&mq);
@@ -177,64 +288,7 @@ __global__ void __launch_bounds__(kOwnThreads, D == 256 ? 1 : 2)
 
   if (warp == kOwnWarps) {
     // ---------------------------------------------------------------------------------- loads
-    bool falls = false;
-    for (int t = lane; t < a.T; t += 32) falls |= __ldg(a.first + t) > __ldg(a.first + t + 1);
-    falls = __any_sync(0xffffffffu, falls);
-    const int rows = min(a.page, KT), most = KT / rows;   // positions of one box, boxes of a tile
-    const uint32_t box = rows * 128u;                     // its bytes in one 64-column slab
-    Ring<NS> ring;
-    int loads = 0, q_loads = 0, k = 0;
-    for (long long at = blockIdx.x; ok && at < items; at += gridDim.x, ++k) {
-      const Item t = item_of<D, WR>(a, at, falls);
-      if (k >= 2) ok = warp_wait(&s.item_empty[k & 1], ((k >> 1) & 1) ^ 1, a.budget);
-      if (!ok) break;
-      // the queries: row (node, head) as the box leaves them; rows behind it hold anything and are not used
-      if (lane == 0) {
-        s.item[k & 1] = t;
-        mbar_arrive_expect_tx(&s.item_full[k & 1], (uint32_t)(D / 64) * a.heads * a.npt * 128u);
-        for (int h = 0; h < D / 64; ++h)
-          tma_load_4d(sm + (k & 1) * C::kQ + h * kRows * 128, &mq, &s.item_full[k & 1], h * 64, t.hk * a.G + t.h0, t.node0, t.b);
-      }
-      __syncwarp();
-      ++q_loads;
-      // its positions
-      const int end = t.tiles == 0 ? 0 : t.own + t.n;
-      const int32_t* table = a.table + (size_t)t.b * a.M + (t.shared >> a.page_shift);
-      auto page_at = [&](int tile) {
-        const int pos = tile * KT + lane * rows;
-        return lane < most && pos < end ? __ldg(table + (pos >> a.page_shift)) : -1;
-      };
-      int pg = page_at(0);
-      for (int tile = 0; tile < t.tiles; ++tile) {
-        const int pieces = min(most, (end - tile * KT + rows - 1) / rows), in_page = (tile * KT + lane * rows) & (a.page - 1);
-        int src = pg;
-        if (tile + 1 < t.tiles) pg = page_at(tile + 1);
-        if (lane < pieces && (src < 0 || src >= a.P)) {   // read as zeros (outside the tensor) and reported
-          atomicCAS(a.err, 0, kErrDeviceIndex);
-          src = -1;
-        }
-        const int slot = ring.slot;
-        if (loads == NS) ok = warp_wait(&s.empty[slot], ring.parity ^ 1, a.budget);
-        else ++loads;
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&s.full[slot], 2 * pieces * box * (D / 64));
-        __syncwarp();
-        if (lane < pieces) {
-          uint8_t* dst = sm + C::kRing + slot * 2 * C::kTile + lane * box;
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h) {
-            tma_load_4d(dst + h * KT * 128, &mk, &s.full[slot], h * 64, t.hk, in_page, src);
-            tma_load_4d(dst + C::kTile + h * KT * 128, &mv, &s.full[slot], h * 64, t.hk, in_page, src);
-          }
-        }
-        __syncwarp();
-        ring.step(1);
-      }
-    }
-    // no copy of this block is left in flight
-    for (int i = 0; i < loads; ++i) warp_wait(&s.full[i], i < ring.slot ? ring.parity : ring.parity ^ 1, kDrainBudget);
-    for (int i = max(0, q_loads - 2); i < q_loads; ++i) warp_wait(&s.item_full[i & 1], (i >> 1) & 1, kDrainBudget);
-    if (!ok && lane == 0) atomicCAS(a.err, 0, kErrTimeout);
+    load_items<D, C>(mq, mk, mv, a, s, sm, blockIdx.x, gridDim.x, lane);
     return;
   }
 
@@ -333,17 +387,8 @@ __global__ void __launch_bounds__(kOwnThreads, D == 256 ? 1 : 2)
             if (p < own + n) {
               if (n == 1 && !a.mask) continue;            // (it sees itself)
               asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(u_at) : "memory");
-              uint32_t* u = reinterpret_cast<uint32_t*>(&v);
-              uint32_t hit = 0;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) hit |= ((u[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-              if (!hit) continue;
+              if (!finite_only(v)) continue;
               bad = true;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if ((u[e] & 0x7F80u) == 0x7F80u) u[e] &= 0xFFFF0000u;
-                if ((u[e] & 0x7F800000u) == 0x7F800000u) u[e] &= 0xFFFFu;
-              }
             }
             asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(u_at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
           }
@@ -427,6 +472,7 @@ __global__ void __launch_bounds__(kOwnThreads, D == 256 ? 1 : 2)
           }
         }
       }
+      if (masked) fence_async_smem();   // (what was cleaned is loaded over)
       __syncwarp();
       if (lane == 0 && ok) mbar_arrive(&s.empty[ring.slot]);
       ring.step(1);
@@ -476,23 +522,13 @@ __global__ void __launch_bounds__(kOwnThreads, D == 256 ? 1 : 2)
         sum += c[w] * s_l[w0 + w][rr];
         rare |= c[w] == 0.f && mw != -INFINITY;
       }
-      const bool sees = sum > 0.f || sum != sum;
-      lse = sees ? top * (1.f / kLog2e) + logf(sum) : -INFINITY;
-      const float ref = fmaxf(lse, lse_s);
-      float f = sees ? 1.f : 0.f, total = 1.f;
-      if (lse != lse || lse_s != lse_s) {
-        f = c_s = total = NAN;
-      } else if (joins && ref > -INFINITY) {
-        f = lse == ref ? 1.f : ex2_approx((lse - ref) * kLog2e);
-        c_s = lse_s == ref ? 1.f : ex2_approx((lse_s - ref) * kLog2e);
-        rare |= (f == 0.f && lse != -INFINITY) || (c_s == 0.f && lse_s != -INFINITY);
-        total = f + c_s;
-      }
-      if (joins) lse = ref == -INFINITY && total == total ? -INFINITY : ref + logf(total);
-      const float inv = sees ? f / (sum * total) : 0.f;
+      const Factors f = factors(true, joins, top, sum, lse_s);
+      lse = f.lse;
+      rare |= f.rare;
+      const float inv = f.sees ? f.own / (sum * f.total) : 0.f;
+      c_s = f.shared / f.total;
 #pragma unroll
       for (int w = 0; w < WK; ++w) c[w] *= inv;
-      c_s /= total;
     }
     if (a.lse && lane < kMine && my_row < t.rows) a.lse[base + my_place] = lse;
     const unsigned rares = __ballot_sync(0xffffffffu, (rare || cleaned) && lane < kMine && my_row < used);
@@ -564,6 +600,323 @@ __global__ void __launch_bounds__(kOwnThreads, D == 256 ? 1 : 2)
   if (!ok && lane == 0) atomicCAS(a.err, 0, kErrTimeout);
 }
 
+// Few query rows (up to 8): the products are turned round, S^T = K Q^T and O^T = V^T P^T: positions and channels are the 16
+// rows of the matrix instructions and queries their 8 columns, half as many instructions, exponentials and accumulators as
+// with 16 query rows of which 4 or 8 are used. An item's team is WK warps, which share a tile's positions, and one that
+// loads; a block is as many teams as fit.
+template <int D, int WK>
+struct Few {
+  static constexpr int kTeams = WK == 4 ? 1 : D == 64 ? 8 : D == 128 ? 5 : 2;
+  static constexpr int kBlocks = WK == 4 && D < 256 ? 2 : 1;   // an SM
+  static constexpr int kThreads = 32 * kTeams * (WK + 1);
+  static constexpr int kRows = 8, PW = WK == 1 ? 32 : 16, KT = PW * WK;   // positions of a warp and of a tile
+  static constexpr int kTile = KT * D * 2, kQ = kRows * D * 2, kAcc = WK > 1 ? WK * kRows * D * 4 : 0;
+  static constexpr int kFit = ((kBlocks == 2 ? 108 : 224) * 1024 / kTeams - 2 * kQ - kAcc) / (2 * kTile), NS = kFit > 4 ? 4 : kFit;
+  static constexpr int kRing = 2 * kQ, kOut = kRing + NS * 2 * kTile, kTeam = kOut + kAcc, kSmem = kTeams * kTeam;
+  static_assert(NS >= 2 && kTeam % 1024 == 0 && KT * 128 % 1024 == 0, "a tile is loaded while another is computed; swizzled tiles");
+};
+__device__ __forceinline__ uint32_t turned(uint32_t x) {   // an 8 x 8 matrix of 16-bit elements, a row's neighbours in a register
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <int D, int WK>
+__global__ void __launch_bounds__(Few<D, WK>::kThreads, Few<D, WK>::kBlocks)
+    fork_own_few_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const __grid_constant__ OwnArgs a) {
+  using C = Few<D, WK>;
+  constexpr int KT = C::KT, PW = C::PW, NS = C::NS, kTeams = C::kTeams, kBlk = PW / 16;
+  extern __shared__ __align__(1024) uint8_t dyn[];
+  __shared__ OwnBars bars[kTeams];
+  __shared__ float s_m[kTeams][WK][8], s_l[kTeams][WK][8];
+  __shared__ int s_bad[kTeams];   // the last item in which V of a node was cleaned of something
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, team = warp % kTeams, wk = warp / kTeams;
+  if (smem_u32(dyn) & 1023u) {   // the swizzled tiles rely on it
+    if (tid == 0) atomicCAS(a.err, 0, kErrTimeout);
+    return;
+  }
+  if (tid == 0) {
+    for (int t = 0; t < kTeams; ++t) {
+      bars[t].template init<NS>(WK);
+      s_bad[t] = -1;
+    }
+    fence_mbar_init();
+    prefetch_tmap(&mq);
+    prefetch_tmap(&mk);
+    prefetch_tmap(&mv);
+  }
+  __syncthreads();
+  OwnBars& s = bars[team];
+  uint8_t* sm = dyn + team * C::kTeam;
+  const long long items = (long long)a.B * a.Hk * a.m_tiles, at0 = blockIdx.x + (long long)gridDim.x * team, stride = (long long)gridDim.x * kTeams;
+  if (wk == WK) {
+    load_items<D, C>(mq, mk, mv, a, s, sm, at0, stride, lane);
+    return;
+  }
+  // this lane's places in the rows that ldmatrix reads: of Q, of K (positions as rows) and of V
+  uint32_t q_off[2], k_off[4], v_off[4];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) q_off[j] = unit_at(8, lane & 7, 4 * j + (lane >> 3));
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    k_off[j] = unit_at(KT, wk * PW + (lane & 15), 2 * j + (lane >> 4));
+    v_off[j] = unit_at(KT, wk * PW + (lane & 7) + ((lane >> 4) << 3), 2 * j + ((lane >> 3) & 1));
+  }
+  const int q0 = 2 * (lane & 3);                       // this thread's two queries, and their nodes within an item
+  const int node_of[2] = {q0 / a.heads, (q0 + 1) / a.heads};
+  const int out_row = lane >> 2, out_node = out_row / a.heads;   // the query whose results it writes
+  const size_t step = (size_t)a.Hk * D;                // elements of a position
+  const uint32_t ring_at = smem_u32(sm) + C::kRing;
+  float* acc = reinterpret_cast<float*>(sm + C::kOut);
+  Ring<NS> ring;
+  bool ok = true;
+  int k = 0;
+  for (long long at = at0; at < items; at += stride, ++k) {
+    // (a warp whose wait ran out goes on without touching anything until its team meets, here or before the results)
+    ok = warp_wait(&s.item_full[k & 1], (k >> 1) & 1, a.budget);
+    if constexpr (WK > 1) ok = named_bar_and(1 + 2 * team, 32 * WK, ok);
+    if (!ok) break;
+    const Item t = s.item[k & 1];
+    const int n = t.n, own = t.own, used = t.used;
+    float o[D / 16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[d][e] = 0.f;
+    // how far a chain's node sees, or its mask
+    int sees_to[2];
+    const uint64_t* words[2];
+    uint64_t word0[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int node = q0 + e < used ? t.node0 + node_of[e] : 0;
+      sees_to[e] = own + min(node + 1, n);
+      words[e] = a.mask ? a.mask + ((size_t)t.b * a.N + node) * a.W : nullptr;
+      word0[e] = words[e] && q0 + e < used ? __ldg(words[e]) : 0;
+    }
+    uint32_t qf[D / 32][4];
+    if (t.tiles > 0) {
+#pragma unroll
+      for (int kk = 0; kk < D / 32; ++kk) ldmatrix4(smem_u32(sm) + (k & 1) * C::kQ + (kk >> 1) * 1024 + q_off[kk & 1], qf[kk]);
+    }
+    bool bad = false;
+    for (int tile = 0; tile < t.tiles; ++tile) {
+      ok = ok && warp_wait(&s.full[ring.slot], ring.parity, a.budget);
+      if (!ok) break;
+      const uint32_t k_at = ring_at + ring.slot * 2 * C::kTile, v_at = k_at + C::kTile;
+      const int first = tile * KT + wk * PW;              // this warp's positions
+      const bool masked = first + PW > own;
+      if (masked) {
+        // V of positions that are not there must not meet a weight of 0, nor what is not finite of nodes that some do not see
+        const int r0 = max(0, own - first);
+        for (int x = lane; x < (PW - r0) * (D / 8); x += 32) {
+          const int r = r0 + x / (D / 8);
+          const uint32_t u_at = v_at + unit_at(KT, wk * PW + r, x % (D / 8));
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (first + r < own + n) {
+            if (n == 1 && !a.mask) continue;            // (it sees itself)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(u_at) : "memory");
+            if (!finite_only(v)) continue;
+            bad = true;
+          }
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(u_at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+        }
+        __syncwarp();
+      }
+      float x[kBlk][4];
+#pragma unroll
+      for (int c = 0; c < kBlk; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[c][e] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+        for (int c = 0; c < kBlk; ++c) {
+          uint32_t f[4];
+          ldmatrix4(k_at + (kk >> 2) * KT * 128 + c * 16 * 128 + k_off[kk & 3], f);
+          mma16816(x[c], f, qf[kk >> 1][2 * (kk & 1)], qf[kk >> 1][2 * (kk & 1) + 1]);
+        }
+      if (masked) {
+#pragma unroll
+        for (int c = 0; c < kBlk; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int e = i & 1, p = first + c * 16 + 8 * (i >> 1) + (lane >> 2), j = p - own;
+            bool see = p < sees_to[e];
+            if (a.mask) see = j < 0 || (j < n && (((j < 64 ? word0[e] : __ldg(words[e] + (j >> 6))) >> (j & 63)) & 1));
+            if (!see) x[c][i] = -INFINITY;
+          }
+      }
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int c = 0; c < kBlk; ++c) mx[e] = fmaxf(mx[e], fmaxf(x[c][e], x[c][e + 2]));
+#pragma unroll
+      for (int z = 4; z < 32; z <<= 1)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], z));
+      if (__any_sync(0xffffffffu, mx[0] * a.sl2 > m[0] || mx[1] * a.sl2 > m[1])) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float m_new = fmaxf(m[e], mx[e] * a.sl2), f = m[e] == m_new ? 1.f : ex2_approx(m[e] - m_new);
+          l[e] *= f;
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) {
+            o[d][e] *= f;
+            o[d][e + 2] *= f;
+          }
+          m[e] = m_new;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float off = m[e] == -INFINITY ? 0.f : -m[e];
+#pragma unroll
+        for (int c = 0; c < kBlk; ++c)
+#pragma unroll
+          for (int i = e; i < 4; i += 2) x[c][i] = ex2_approx(fmaf(x[c][i], a.sl2, off));
+#pragma unroll
+        for (int c = 0; c < kBlk; ++c) l[e] += x[c][e] + x[c][e + 2];
+      }
+      uint32_t p[kBlk][2];
+#pragma unroll
+      for (int c = 0; c < kBlk; ++c) {
+        p[c][0] = turned(pack_bf16x2(x[c][0], x[c][1]));
+        p[c][1] = turned(pack_bf16x2(x[c][2], x[c][3]));
+      }
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+        for (int c = 0; c < kBlk; ++c) {
+          uint32_t f[4];
+          ldmatrix4_t(v_at + (d >> 2) * KT * 128 + c * 16 * 128 + v_off[d & 3], f);
+          mma16816(o[d], f, p[c][0], p[c][1]);
+        }
+      if (masked) fence_async_smem();   // (what was cleaned is loaded over)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.empty[ring.slot]);
+      ring.step(1);
+    }
+    if (k == 0) wait_prerequisite();   // (in every warp: this grid must not end before the ones it follows)
+#pragma unroll
+    for (int w = 4; w < 32; w <<= 1)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) l[e] += __shfl_xor_sync(0xffffffffu, l[e], w);
+    // ---------------------------------------------------------------------------------- results: a part of the channels a warp
+    constexpr int kMine = D / 8 / WK;                    // blocks of 8 channels: wk, wk + WK, ..
+    const size_t base = ((size_t)t.b * a.N + t.node0) * a.Hq + t.hk * a.G + t.h0;
+    const bool joins = t.shared > 0;
+    float lse_s[2], z[2][kMine];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const bool takes = joins && q0 + e < used;
+      const size_t orow = base + node_of[e] * (a.Hq - a.heads) + q0 + e;
+      lse_s[e] = takes ? __ldcg(a.dense_lse + orow) : -INFINITY;
+#pragma unroll
+      for (int d = 0; d < kMine; ++d) z[e][d] = takes ? __ldcg(a.dense_o + orow * D + 8 * (d * WK + wk) + (lane >> 2)) : 0.f;
+    }
+    bool cleaned = __any_sync(0xffffffffu, bad);
+    if constexpr (WK > 1) {
+#pragma unroll
+      for (int d = 0; d < D / 8; ++d)
+        *reinterpret_cast<float2*>(acc + (wk * D + 8 * d + (lane >> 2)) * 8 + q0) = make_float2(o[d >> 1][2 * (d & 1)], o[d >> 1][2 * (d & 1) + 1]);
+      if (lane < 4) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          s_m[team][wk][q0 + e] = m[e];
+          s_l[team][wk][q0 + e] = l[e];
+        }
+      }
+      if (cleaned && lane == 0) s_bad[team] = k;
+      __syncwarp();
+      ok = named_bar_and(2 + 2 * team, 32 * WK, ok);
+      cleaned = s_bad[team] == k;
+    }
+    if (!ok) break;
+    // the weights of the warps' parts and of the shared one
+    float c[2][WK], c_s[2];
+    uint32_t rare = 0, seen = 0;                         // bit 8 e + w: part w of query e saw something (8 e + 7: the shared one)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float top = m[e], sum = l[e];
+      c[e][0] = 1.f;
+      if constexpr (WK > 1) {
+        top = -INFINITY;
+        sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < WK; ++w) top = fmaxf(top, s_m[team][w][q0 + e]);
+#pragma unroll
+        for (int w = 0; w < WK; ++w) {
+          const float mw = s_m[team][w][q0 + e];
+          c[e][w] = mw == top ? 1.f : ex2_approx(mw - top);
+          sum += c[e][w] * s_l[team][w][q0 + e];
+          if (mw != -INFINITY) seen |= 1u << (8 * e + w);
+        }
+      } else if (top != -INFINITY) {
+        seen |= 1u << (8 * e);
+      }
+      if (lse_s[e] != -INFINITY) seen |= 128u << (8 * e);
+      const Factors f = factors(q0 + e < used, joins, top, sum, lse_s[e]);
+      const float inv = f.sees ? f.own / (sum * f.total) : 0.f;
+#pragma unroll
+      for (int w = 0; w < WK; ++w) {
+        c[e][w] *= inv;
+        if (f.sees && c[e][w] == 0.f) rare |= 1u << (8 * e + w);
+      }
+      c_s[e] = f.shared / f.total;
+      if (c_s[e] == 0.f) rare |= 128u << (8 * e);
+      if (a.lse && wk == 0 && lane < 4 && q0 + e < t.rows) a.lse[base + node_of[e] * (a.Hq - a.heads) + q0 + e] = f.lse;
+    }
+    rare &= seen;                                        // what saw something and has no weight: it counts where it is not finite
+    const size_t out_at = (base + out_node * (a.Hq - a.heads) + out_row) * D + 2 * (lane & 3);
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int d = i * WK + wk;
+      float y[2] = {0.f, 0.f};
+      auto add = [&](int e, int bit, float f, float part) {
+        if (f != 0.f) y[e] = fmaf(f, part, y[e]);        // (without weight it may hold anything)
+        else if ((rare >> (8 * e + bit) & 1) && !(fabsf(part) < INFINITY)) y[e] += part;
+      };
+#pragma unroll
+      for (int w = 0; w < WK; ++w) {
+        float2 part;
+        if constexpr (WK > 1) part = *reinterpret_cast<const float2*>(acc + (w * D + 8 * d + (lane >> 2)) * 8 + q0);
+        else part = make_float2(o[i >> 1][2 * (i & 1)], o[i >> 1][2 * (i & 1) + 1]);
+        add(0, w, c[0][w], part.x);
+        add(1, w, c[1][w], part.y);
+      }
+      add(0, 7, c_s[0], z[0][i]);
+      add(1, 7, c_s[1], z[1][i]);
+      const uint32_t u = turned(pack_bf16x2(y[0], y[1]));
+      if (out_row < t.rows) *reinterpret_cast<uint32_t*>(a.o + out_at + 8 * d) = u;
+    }
+    // so do elements of seen nodes that were cleaned away
+    if (cleaned && out_row < used) {
+      const int nd = t.node0 + out_node;
+      const uint64_t* wd = a.mask ? a.mask + ((size_t)t.b * a.N + nd) * a.W : nullptr;
+      const int32_t* table = a.table + (size_t)t.b * a.M + (t.shared >> a.page_shift);
+#pragma unroll 1
+      for (int d = 2 * wk; d < 2 * (D / 8); d += d & 1 ? 2 * WK - 1 : 1) {   // (this warp's blocks)
+        __nv_bfloat16* out = a.o + out_at + 8 * (d >> 1) + (d & 1);
+        float y = 0.f;
+        for (int j = 0; j < n; ++j) {
+          if (wd ? !(wd[j >> 6] >> (j & 63) & 1) : j > nd) continue;
+          const int p = own + j, pg = __ldg(table + (p >> a.page_shift));
+          if ((unsigned)pg >= (unsigned)a.P) continue;
+          const float v = __bfloat162float(a.v_pages[((size_t)pg * a.page + (p & (a.page - 1))) * step + (size_t)t.hk * D + 8 * (d >> 1) + 2 * (lane & 3) + (d & 1)]);
+          if (!(fabsf(v) < INFINITY)) y += v;
+        }
+        if (y != 0.f) *out = __float2bfloat16(__bfloat162float(*out) + y);   // (inf or nan)
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&s.item_empty[k & 1]);
+  }
+  if (k == 0) wait_prerequisite();   // (left before the first item's results)
+  if (!ok && lane == 0) atomicCAS(a.err, 0, kErrTimeout);
+}
+
 size_t dense_rows(const TreeAttnArgs& t) { return (size_t)t.B * t.N * t.Hq; }
 float* dense_of(const TreeAttnArgs& t) { return reinterpret_cast<float*>(t.ws + parts_bytes(t.D)); }
 
@@ -580,9 +933,9 @@ cudaError_t shared_part(const ForkAttnArgs& p, cudaStream_t s) {
   return launch<D, kForm>(p.t, a, s);
 }
 
-template <int D, int WR>
+using OwnKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const OwnArgs);
+template <class C, int D, OwnKernel kKernel, int kThreads, int kBlocks>
 cudaError_t own_part(const ForkAttnArgs& p, cudaStream_t s) {
-  using C = Own<D, WR>;
   const TreeAttnArgs& t = p.t;
   OwnArgs a{};
   a.q = static_cast<const __nv_bfloat16*>(t.q);
@@ -609,11 +962,11 @@ cudaError_t own_part(const ForkAttnArgs& p, cudaStream_t s) {
       !make_map(&mv, t.v_pages, D, t.Hk, t.page, t.P, 1, std::min(t.page, C::KT)))
     return cudaErrorInvalidValue;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(fork_own_kernel<D, WR>), C::kSmem, done);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kKernel), C::kSmem, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min((long long)t.B * t.Hk * a.m_tiles, (long long)kNumSMs * (D == 256 ? 1 : 2)));
-  cfg.blockDim = dim3(kOwnThreads);
+  cfg.gridDim = dim3((unsigned)std::min((long long)t.B * t.Hk * a.m_tiles, (long long)kNumSMs * kBlocks));
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -622,9 +975,19 @@ cudaError_t own_part(const ForkAttnArgs& p, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const int slot = stage_timer_begin(s, kKernForkAttnOwn);
-  e = cudaLaunchKernelEx(&cfg, fork_own_kernel<D, WR>, mq, mk, mv, a);
+  e = cudaLaunchKernelEx(&cfg, kKernel, mq, mk, mv, a);
   stage_timer_end(slot, s);
   return e;
+}
+
+template <int D, int WK>
+cudaError_t own_few(const ForkAttnArgs& p, cudaStream_t s) {
+  using C = Few<D, WK>;
+  return own_part<C, D, fork_own_few_kernel<D, WK>, C::kThreads, C::kBlocks>(p, s);
+}
+template <int D, int WR>
+cudaError_t own_by_teams(const ForkAttnArgs& p, cudaStream_t s) {
+  return own_part<Own<D, WR>, D, fork_own_kernel<D, WR>, kOwnThreads, D == 256 ? 1 : 2>(p, s);
 }
 
 template <int D>
@@ -637,7 +1000,14 @@ cudaError_t both_parts(const ForkAttnArgs& p, cudaStream_t s) {
   else e = rows > kM ? shared_part<D, kWide>(p, s) : shared_part<D, kNarrow>(p, s);
   if (e != cudaSuccess) return e;
   const int r = p.t.N * G;
-  return r <= 16 ? own_part<D, 1>(p, s) : r <= 32 ? own_part<D, 2>(p, s) : own_part<D, 4>(p, s);
+  if (r <= 8) {
+    // Few items end sooner when four warps share each, many when more of them are under way (us by four and by one or two,
+    // all parts together, own parts of 64 and of 1000 positions; D = 128: 256 items 33 and 31, 55 and 61, 512 items 38 and 34,
+    // 80 and 80, 2048 items 61 and 53, 192 and 198; D = 256: 256 items 37 and 34, 79 and 79, 2048 items 104 and 80, 352 and 343).
+    const bool many = (long long)p.t.B * p.t.Hk >= 3 * kNumSMs;
+    return !many ? own_few<D, 4>(p, s) : own_few<D, D == 64 ? 1 : 2>(p, s);
+  }
+  return r <= 16 ? own_by_teams<D, 1>(p, s) : r <= 32 ? own_by_teams<D, 2>(p, s) : own_by_teams<D, 4>(p, s);
 }
 
 }  // namespace

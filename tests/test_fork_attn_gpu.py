@@ -262,3 +262,42 @@ def test_same_bits_other_stream_and_replay():
         o4, l4 = gdr.gdr_fork_attn(*a, want_lse=True)
         gdr.gdr_sync_status()
         assert torch.equal(got[0], o4) and torch.equal(got[1], l4)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("kind", ["chain", "random"])
+@pytest.mark.parametrize("B,N,Hq,Hk", [(5, 2, 4, 1), (240, 1, 6, 2), (238, 2, 8, 2), (160, 8, 3, 3), (479, 3, 2, 1)])
+def test_few_query_rows(B, N, Hq, Hk, kind, D):
+    """Up to eight query rows a key head, of few rows and of many, which are shared out otherwise."""
+    c = _case([1, B // 3, B - 2], [64, 192], [0, 5, 31, 32, 33, 64, 130, 300], N, Hq, Hk, D, 16 if N == 2 else 64, kind, seed=B + D,
+              lengths=[N, max(1, N - 1), N, N, 0])
+    _check(c)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("B", [3, 160])
+def test_few_query_rows_and_what_is_not_finite(B, D):
+    c = _case([0, B // 3, B], [96, 32], [40, 0, 13], 2, 12, 3, D, 32, "random", seed=21 + D, lengths=[2, 1, 0, 2])
+    c["see"][:, :, :] = torch.tensor([[True, False], [True, False]])   # nobody sees node 1
+    want = _run(c)
+    _check(c, *want)
+    used = torch.zeros(c["k"].shape[:2], dtype=torch.bool)
+    for b in range(B):
+        for pos in range(int(c["ctx"][b]) + min(1, int(c["lengths"][b]))):
+            used[c["table"][b, pos // 32].long(), pos % 32] = True
+    c["k"][~used], c["v"][~used] = float("nan"), float("inf")
+    assert all(torch.equal(a, b) for a, b in zip(want, _run(c)))
+    # seen ones reach the output, however small their weight: of a node, of the own part, of the shared part
+    for x in ("node", "own", "shared"):
+        d = {n: t.clone() if isinstance(t, torch.Tensor) else t for n, t in c.items()}
+        pos = {"node": int(d["ctx"][0]), "own": int(d["ctx"][0]) - 3, "shared": 5}[x]
+        page = d["table"][0, pos // 32].long()
+        d["v"][page, pos % 32, 1, 7] = float("-inf")
+        d["k"][page, pos % 32, 1] = 0.0
+        d["q"][0] *= 30.0                        # (the weight of a score of 0 vanishes)
+        o, _ = _run(d)
+        inside = torch.zeros_like(o, dtype=torch.bool)
+        rows = range(B // 3) if x == "shared" else [0]
+        for b in rows:
+            inside[b, :int(d["lengths"][b]), 4:8, 7] = True
+        assert not torch.isfinite(o[inside]).any() and torch.isfinite(o[~inside]).all(), x
