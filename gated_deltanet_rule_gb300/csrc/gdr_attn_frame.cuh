@@ -1159,26 +1159,44 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const __gr
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int c = cc + u * step, at = c < parts ? s_part[c] : -1;
-        const size_t p = (at >= 0 ? at : s_part[0]) + row;   // (the first block holds the item's first unit)
-        w[u] = at >= 0 ? a.part_lse[p] : -INFINITY;
+        w[u] = -INFINITY;
+        if (at < 0) continue;   // (the same in the whole warp)
+        const size_t p = (size_t)at + row;
+        w[u] = a.part_lse[p];
         const float* po = a.part_o + p * D + lane * kVec;
+        if constexpr (kVec == 2) {
+          const float2 y = *reinterpret_cast<const float2*>(po);
+          x[u][0] = y.x;
+          x[u][1] = y.y;
+        } else {
 #pragma unroll
-        for (int e = 0; e < kVec; e += 2) {
-          const float2 y = *reinterpret_cast<const float2*>(po + e);
-          x[u][e] = y.x;
-          x[u][e + 1] = y.y;
+          for (int e = 0; e < kVec; e += 4) {
+            const float4 y = *reinterpret_cast<const float4*>(po + e);
+            x[u][e] = y.x;
+            x[u][e + 1] = y.y;
+            x[u][e + 2] = y.z;
+            x[u][e + 3] = y.w;
+          }
         }
       }
     };
     load(c0);
-    for (int c = lane; c < parts; c += 32) {
-      const float lse = s_part[c] >= 0 ? a.part_lse[s_part[c] + row] : -INFINITY;
-      nan |= lse != lse;
-      top = fmaxf(top, lse);
-    }
+    if (parts <= 4) {   // every lane has them
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    nan = __any_sync(0xffffffffu, nan);
+      for (int u = 0; u < 4; ++u) {
+        nan |= w[u] != w[u];
+        top = fmaxf(top, w[u]);
+      }
+    } else {
+      for (int c = lane; c < parts; c += 32) {
+        const float lse = s_part[c] >= 0 ? a.part_lse[s_part[c] + row] : -INFINITY;
+        nan |= lse != lse;
+        top = fmaxf(top, lse);
+      }
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      nan = __any_sync(0xffffffffu, nan);
+    }
     const float ref = top == -INFINITY ? 0.f : top;
     for (int cc = c0; cc < parts;) {
 #pragma unroll
@@ -1233,7 +1251,10 @@ __global__ void __launch_bounds__(kJoinThreads) tree_attn_join_kernel(const __gr
     if constexpr (A::kShared) {
       float* out = a.dense_o + orow * D + lane * kVec;
 #pragma unroll
-      for (int e = 0; e < kVec; e += 2) *reinterpret_cast<float2*>(out + e) = make_float2(acc[e], acc[e + 1]);
+      for (int e = 0; e < kVec; e += kVec > 2 ? 4 : 2) {
+        if constexpr (kVec > 2) *reinterpret_cast<float4*>(out + e) = make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+        else *reinterpret_cast<float2*>(out + e) = make_float2(acc[e], acc[e + 1]);
+      }
       if (lane == 0) a.dense_lse[orow] = lse;
     } else {
       __nv_bfloat16* out = a.o + orow * D + lane * kVec;
