@@ -38,6 +38,7 @@ struct OwnArgs {
   int B, N, Hq, Hk, G, W, P, page, page_shift, M, T;
   int npt, heads, splits;    // an item's nodes and heads a node; items that a node's heads of a key head take
   int m_tiles;               // items of a row and key head
+  int alone;                 // there was no shared part: this one reads the shared positions, too
   long long budget;
   int* err;
 };
@@ -61,6 +62,7 @@ struct Own {
 // What the loading warp tells the computing ones of an item.
 struct Item {
   int b, hk, node0, h0, n, own, shared, tiles;
+  int lead, from;   // pages that are looked up in another row's table, and that row
   int rows, used;   // query rows, and those of them whose nodes are there
 };
 struct OwnBars {
@@ -149,7 +151,7 @@ __device__ __forceinline__ Item item_of(const OwnArgs& a, long long at, bool fal
   t.h0 = mt % a.splits * a.heads;
   t.n = a.lengths ? __ldg(a.lengths + t.b) : a.N;
   const int ctx = __ldg(a.ctx + t.b);
-  t.shared = 0;
+  t.shared = t.from = 0;
   bool valid = !falls;
   // The one group that holds row b among groups g0 .. g0 + 31: of more than these, the last that begins at or before it and
   // those around it, a factor of 32 a step. (Where `first` falls what is found is not used.)
@@ -174,6 +176,7 @@ __device__ __forceinline__ Item item_of(const OwnArgs& a, long long at, bool fal
       const int who = __ffs(mine) - 1;
       valid = valid && __shfl_sync(0xffffffffu, (int)group_valid(f0, f1, sh, a.B, a.page, a.M), who);
       t.shared = __shfl_sync(0xffffffffu, sh, who);
+      t.from = __shfl_sync(0xffffffffu, f0, who);
     }
   }
   valid = valid && t.n >= 0 && t.n <= a.N && ctx >= t.shared && (long long)ctx + t.n <= (long long)a.M * a.page;
@@ -182,7 +185,8 @@ __device__ __forceinline__ Item item_of(const OwnArgs& a, long long at, bool fal
     t.n = 0;
     t.shared = 0;
   }
-  t.own = ctx - t.shared;
+  t.lead = a.alone ? t.shared >> a.page_shift : 0;
+  t.own = ctx - (a.alone ? 0 : t.shared);
   const int heads = min(a.heads, a.G - t.h0), nodes = max(0, min(a.npt, t.n - t.node0));
   t.rows = min(a.npt, a.N - t.node0) * heads;
   t.used = nodes * heads;
@@ -192,6 +196,11 @@ __device__ __forceinline__ Item item_of(const OwnArgs& a, long long at, bool fal
   return t;
 }
 
+// The row's pages from its own part's first position on.
+__device__ __forceinline__ const int32_t* own_table(const OwnArgs& a, const Item& t) {
+  return a.table + (size_t)t.b * a.M + (a.alone ? 0 : t.shared >> a.page_shift);
+}
+
 // The loading warp of a team: items at0, at0 + stride, ... , two of them and NS tiles ahead of what is computed.
 template <int D, class C>
 __device__ __forceinline__ void load_items(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const OwnArgs& a, OwnBars& s,
@@ -199,7 +208,11 @@ __device__ __forceinline__ void load_items(const CUtensorMap& mq, const CUtensor
   constexpr int KT = C::KT, NS = C::NS;
   const long long items = (long long)a.B * a.Hk * a.m_tiles;
   bool falls = false;
-  for (int t = lane; t < a.T; t += 32) falls |= __ldg(a.first + t) > __ldg(a.first + t + 1);
+  for (int t = lane; t < a.T; t += 32) {
+    const int f0 = __ldg(a.first + t), f1 = __ldg(a.first + t + 1);
+    falls |= f0 > f1;
+    if (a.alone && at0 == 0 && !group_valid(f0, f1, __ldg(a.shared + t), a.B, a.page, a.M)) atomicCAS(a.err, 0, kErrDeviceIndex);
+  }
   falls = __any_sync(0xffffffffu, falls);
   const int rows = min(a.page, KT), most = KT / rows;   // positions of one box, boxes of a tile
   const uint32_t box = rows * 128u;                     // its bytes in one 64-column slab
@@ -221,10 +234,10 @@ __device__ __forceinline__ void load_items(const CUtensorMap& mq, const CUtensor
     ++q_loads;
     // its positions
     const int end = t.tiles == 0 ? 0 : t.own + t.n;
-    const int32_t* table = a.table + (size_t)t.b * a.M + (t.shared >> a.page_shift);
+    const int32_t *table = own_table(a, t), *lead = a.table + (size_t)t.from * a.M;
     auto page_at = [&](int tile) {
-      const int pos = tile * KT + lane * rows;
-      return lane < most && pos < end ? __ldg(table + (pos >> a.page_shift)) : -1;
+      const int pos = tile * KT + lane * rows, i = pos >> a.page_shift;
+      return lane < most && pos < end ? __ldg((i < t.lead ? lead : table) + i) : -1;
     };
     int pg = page_at(0);
     for (int tile = 0; tile < t.tiles; ++tile) {
@@ -570,7 +583,7 @@ __global__ void __launch_bounds__(kOwnThreads, D == 256 ? 1 : 2)
       const float cs = __shfl_sync(0xffffffffu, c_s, i);
       const int nd = t.node0 + __shfl_sync(0xffffffffu, my_node, i);
       const uint64_t* wd = a.mask ? a.mask + ((size_t)t.b * a.N + nd) * a.W : nullptr;
-      const int32_t* table = a.table + (size_t)t.b * a.M + (t.shared >> a.page_shift);
+      const int32_t* table = own_table(a, t);
       float cw[WK];
 #pragma unroll
       for (int w = 0; w < WK; ++w) cw[w] = __shfl_sync(0xffffffffu, c[w], i);
@@ -806,7 +819,7 @@ __global__ void __launch_bounds__(Few<D, WK>::kThreads, Few<D, WK>::kBlocks)
     // ---------------------------------------------------------------------------------- results: a part of the channels a warp
     constexpr int kMine = D / 8 / WK;                    // blocks of 8 channels: wk, wk + WK, ..
     const size_t base = ((size_t)t.b * a.N + t.node0) * a.Hq + t.hk * a.G + t.h0;
-    const bool joins = t.shared > 0;
+    const bool joins = t.shared > 0 && !a.alone;
     float lse_s[2], z[2][kMine];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -895,7 +908,7 @@ __global__ void __launch_bounds__(Few<D, WK>::kThreads, Few<D, WK>::kBlocks)
     if (cleaned && out_row < used) {
       const int nd = t.node0 + out_node;
       const uint64_t* wd = a.mask ? a.mask + ((size_t)t.b * a.N + nd) * a.W : nullptr;
-      const int32_t* table = a.table + (size_t)t.b * a.M + (t.shared >> a.page_shift);
+      const int32_t* table = own_table(a, t);
 #pragma unroll 1
       for (int d = 2 * wk; d < 2 * (D / 8); d += d & 1 ? 2 * WK - 1 : 1) {   // (this warp's blocks)
         __nv_bfloat16* out = a.o + out_at + 8 * (d >> 1) + (d & 1);
@@ -935,7 +948,7 @@ cudaError_t shared_part(const ForkAttnArgs& p, cudaStream_t s) {
 
 using OwnKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const OwnArgs);
 template <class C, int D, OwnKernel kKernel, int kThreads, int kBlocks>
-cudaError_t own_part(const ForkAttnArgs& p, cudaStream_t s) {
+cudaError_t own_part(const ForkAttnArgs& p, bool alone, cudaStream_t s) {
   const TreeAttnArgs& t = p.t;
   OwnArgs a{};
   a.q = static_cast<const __nv_bfloat16*>(t.q);
@@ -955,6 +968,7 @@ cudaError_t own_part(const ForkAttnArgs& p, cudaStream_t s) {
   a.splits = (a.G + C::kRows - 1) / C::kRows;
   a.npt = std::min(C::kRows / a.heads, t.N);
   a.m_tiles = (t.N + a.npt - 1) / a.npt * a.splits;
+  a.alone = alone;
   a.budget = wait_budget_cycles();
   CUtensorMap mq, mk, mv;
   if (!make_map(&mq, t.q, D, t.Hq, t.N, t.B, a.heads, a.npt) ||
@@ -973,7 +987,7 @@ cudaError_t own_part(const ForkAttnArgs& p, cudaStream_t s) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = alone ? 0 : 1;   // (only behind the shared part's kernels: what others have written is read at once)
   const int slot = stage_timer_begin(s, kKernForkAttnOwn);
   e = cudaLaunchKernelEx(&cfg, kKernel, mq, mk, mv, a);
   stage_timer_end(slot, s);
@@ -981,13 +995,13 @@ cudaError_t own_part(const ForkAttnArgs& p, cudaStream_t s) {
 }
 
 template <int D, int WK>
-cudaError_t own_few(const ForkAttnArgs& p, cudaStream_t s) {
+cudaError_t own_few(const ForkAttnArgs& p, bool alone, cudaStream_t s) {
   using C = Few<D, WK>;
-  return own_part<C, D, fork_own_few_kernel<D, WK>, C::kThreads, C::kBlocks>(p, s);
+  return own_part<C, D, fork_own_few_kernel<D, WK>, C::kThreads, C::kBlocks>(p, alone, s);
 }
 template <int D, int WR>
 cudaError_t own_by_teams(const ForkAttnArgs& p, cudaStream_t s) {
-  return own_part<Own<D, WR>, D, fork_own_kernel<D, WR>, kOwnThreads, D == 256 ? 1 : 2>(p, s);
+  return own_part<Own<D, WR>, D, fork_own_kernel<D, WR>, kOwnThreads, D == 256 ? 1 : 2>(p, false, s);
 }
 
 template <int D>
@@ -995,6 +1009,11 @@ cudaError_t both_parts(const ForkAttnArgs& p, cudaStream_t s) {
   const int G = p.t.Hq / p.t.Hk;
   // two M tiles an item where a group of the average size has more rows a key head than one holds
   const long long rows = ((long long)p.t.B + p.T - 1) / p.T * p.t.N * G;
+  // Short rows, all of whose items are resident at once: each reads its shared positions itself, one kernel in the place of
+  // three (us by three and by one, 3 rows, 12 items: of 250 positions 24 and 13, 500 24 and 15, 1000 23 and 21, 2000 25 and 31;
+  // D = 256: 22 and 15, 22 and 17, 22 and 23, 25 and 36). The table's width is all that the host knows of the lengths.
+  if (p.t.N * G <= 8 && (long long)p.t.B * p.t.Hk <= kNumSMs * Few<D, 4>::kBlocks && (long long)p.t.M * p.t.page <= (D == 256 ? 512 : 1024))
+    return own_few<D, 4>(p, true, s);
   cudaError_t e;
   if constexpr (D == 256) e = shared_part<D, kSplit>(p, s);
   else e = rows > kM ? shared_part<D, kWide>(p, s) : shared_part<D, kNarrow>(p, s);
@@ -1005,7 +1024,7 @@ cudaError_t both_parts(const ForkAttnArgs& p, cudaStream_t s) {
     // all parts together, own parts of 64 and of 1000 positions; D = 128: 256 items 33 and 31, 55 and 61, 512 items 38 and 34,
     // 80 and 80, 2048 items 61 and 53, 192 and 198; D = 256: 256 items 37 and 34, 79 and 79, 2048 items 104 and 80, 352 and 343).
     const bool many = (long long)p.t.B * p.t.Hk >= 3 * kNumSMs;
-    return !many ? own_few<D, 4>(p, s) : own_few<D, D == 64 ? 1 : 2>(p, s);
+    return !many ? own_few<D, 4>(p, false, s) : own_few<D, D == 64 ? 1 : 2>(p, false, s);
   }
   return r <= 16 ? own_by_teams<D, 1>(p, s) : r <= 32 ? own_by_teams<D, 2>(p, s) : own_by_teams<D, 4>(p, s);
 }

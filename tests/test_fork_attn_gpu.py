@@ -264,6 +264,34 @@ def test_same_bits_other_stream_and_replay():
         assert torch.equal(got[0], o4) and torch.equal(got[1], l4)
 
 
+def _wide(c):
+    """The same with a table of many more pages than the rows have."""
+    B, M = c["table"].shape
+    return {**c, "table": torch.cat([c["table"], torch.full((B, 2048 // c["k"].shape[1]), -1, dtype=I32)], 1)}
+
+
+@pytest.mark.parametrize("kind", ["chain", "random"])
+@pytest.mark.parametrize("case", [c for c in CASES if c[3] * c[4] // c[5] <= 8])
+def test_wide_tables(case, kind):
+    """Short rows are attended at once where the table says that they are short, in parts where it does not."""
+    c = _case(*case, kind, seed=case[0][-1] + case[6])
+    _check(c)
+    _check(_wide(c))
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_refusals_of_short_rows(wide):
+    make = lambda: (_wide if wide else dict)(_case([0, 2, 2, 4], [64, 0, 128], [20, 33], 2, 4, 2, 64, 32, seed=13))   # noqa: E731
+    t = lambda *x: torch.tensor(x, dtype=I32)   # noqa: E731
+    _refused(make(), [0, 1, 2, 3], first=t(0, 3, 2, 4))
+    _refused(make(), [0, 1], shared=t(48, 0, 128))
+    _refused(make(), [], shared=t(64, 48, 128))        # of a group without rows
+    _refused(make(), [2], ctx=t(84, 97, 100, 161))
+    _refused(make(), [3], lengths=t(2, 2, 2, 3))
+    c = make()
+    _refused(c, [2, 3], first=t(0, 2, 2, 5))
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("kind", ["chain", "random"])
 @pytest.mark.parametrize("B,N,Hq,Hk", [(5, 2, 4, 1), (240, 1, 6, 2), (238, 2, 8, 2), (160, 8, 3, 3), (479, 3, 2, 1)])
@@ -275,9 +303,10 @@ def test_few_query_rows(B, N, Hq, Hk, kind, D):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
-@pytest.mark.parametrize("B", [3, 160])
-def test_few_query_rows_and_what_is_not_finite(B, D):
+@pytest.mark.parametrize("B,wide", [(3, False), (3, True), (160, False)])
+def test_few_query_rows_and_what_is_not_finite(B, wide, D):
     c = _case([0, B // 3, B], [96, 32], [40, 0, 13], 2, 12, 3, D, 32, "random", seed=21 + D, lengths=[2, 1, 0, 2])
+    c = _wide(c) if wide else c
     c["see"][:, :, :] = torch.tensor([[True, False], [True, False]])   # nobody sees node 1
     want = _run(c)
     _check(c, *want)
