@@ -42,7 +42,12 @@ using u64 = unsigned long long;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kBins = 1024;
-constexpr int kPerOctave = 128;     // float32: steps of a binary order in the first histogram
+// float32: steps of a binary order in the first histogram, down to 28 orders below the largest weight, and 4 of them farther
+// down: a k-th logit there is found as soon as others (the 40th, 40 orders down, of a row of 49999: 32 -> 17 us, with
+// top-p 48 -> 17).
+constexpr int kPerOctave = 128, kFine = 3584, kPerFar = 4;
+constexpr float kFar = (float)kPerFar / kPerOctave;
+constexpr float kWidth = 0.99459939f, kCoarse = 0.84089642f;   // a step's least weight over its largest: 2^(-1/128), 2^(-1/4)
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kTarget = 100 << 10;  // bytes of a block's part of a row: two blocks an SM
 
@@ -335,7 +340,15 @@ struct Row {
     }
   }
   // float32: the same before it is cut to a step.
-  __device__ __forceinline__ float place(float l) const { return fminf((top - l) * steps, (float)(kSteps - 1)); }
+  __device__ __forceinline__ float place(float l) const {
+    const float y = (top - l) * steps;
+    return fminf(fminf(y, fmaf(y, kFar, kFine * (1.f - kFar))), (float)(kSteps - 1));
+  }
+  // float32: the largest weight of a step.
+  static __device__ __forceinline__ float most_of(int step) {
+    const float s = (float)step;
+    return ptx::ex2_approx(fminf(s * (-1.f / kPerOctave), fmaf(s, -1.f / kPerFar, (float)kFine / kPerFar - (float)kFine / kPerOctave)));
+  }
   // Whether a step holds one value (kValues), and which.
   __device__ __forceinline__ bool one_value(int step) const {
     return kValues && step != 0 && step != kMiddleStep && step != kMiddleStep + 1 && step < kSteps - 1;
@@ -726,7 +739,7 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
   for (int i = 0; i < kMine; ++i) {
     sum_n += n[i];
     m[i] = 0;
-    if (!Row<T>::kValues) sum_f += (float)n[i] * ptx::ex2_approx(-(float)(s0 + i) * (1.f / kPerOctave));
+    if (!Row<T>::kValues) sum_f += (float)n[i] * Row<T>::most_of(s0 + i);
   }
   if (Row<T>::kValues && cuts_p) {
     // (the kept mass is added up from these weights, too; of bins that hold nothing none is needed)
@@ -865,25 +878,26 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
     return out;
   } else {
     // ---------------------------------------------------------------- float32: the steps that may hold the border
-    constexpr float kWidth = 0.99459939f;   // 2^(-1 / 128)
     int lo_step = 0, hi_step = k_on ? k_step : kSteps - 1;
     int first_step = 0;   // narrowed down
     if (cuts_p && !k_on) {
-      // Between the running sums' bounds: a step's weights lie within a factor of 2^(-1/128) of its upper end's (the
+      // Between the running sums' bounds: a step's weights lie within a factor of kWidth or kCoarse of its largest (the
       // last step's between 0 and that); 2^-10 for the sums' own roundings and those of the steps' borders.
       const float all = total_f;
       if (tid == 0) {
         sh.bin = kSteps - 1;
         sh.bin2 = kSteps - 1;
       }
+      if (s0 == kFine) sh.reds[0] = bf;
       __syncthreads();
-      const float least = p * all * kWidth * (1.f - 0x1p-10f) - 0x1p-14f, most = p * all * (1.f + 0x1p-10f) + 0x1p-14f;
+      const float low = kWidth * sh.reds[0] + kCoarse * fmaxf(0.f, all - sh.reds[0]);
+      const float least = p * low * (1.f - 0x1p-10f) - 0x1p-14f, most = p * all * (1.f + 0x1p-10f) + 0x1p-14f;
       float at = bf;
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
-        const float up = at + (float)n[i] * ptx::ex2_approx(-(float)(s0 + i) * (1.f / kPerOctave));
+        const float up = at + (float)n[i] * Row<T>::most_of(s0 + i);
         if (at < least && up >= least) atomicMin(&sh.bin, s0 + i);
-        if (at * kWidth < most && up * kWidth >= most) atomicMin(&sh.bin2, s0 + i);
+        if (s0 + i < kFine && at * kWidth < most && up * kWidth >= most) atomicMin(&sh.bin2, s0 + i);
         at = up;
       }
       if (tid == 0 && least <= 0.f) sh.bin = 0;
@@ -927,17 +941,17 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
         if (s0 + i == lo_step) sh.reds[0] = at;   // the float sums' value where the window begins
-        at += (float)n[i] * ptx::ex2_approx(-(float)(s0 + i) * (1.f / kPerOctave));
+        at += (float)n[i] * Row<T>::most_of(s0 + i);
       }
       __syncthreads();
       at = bf - sh.reds[0];
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
-        const float up = at + (float)n[i] * ptx::ex2_approx(-(float)(s0 + i) * (1.f / kPerOctave));
+        const float up = at + (float)n[i] * Row<T>::most_of(s0 + i);
         const int step = s0 + i;
         if (step >= lo_step && step <= hi_step) {
           if (up + slack >= need * (1.f - 0x1p-10f)) atomicMin(&sh.bin, step);
-          if ((up - slack) * kWidth >= need * (1.f + 0x1p-10f)) atomicMin(&sh.bin2, step);
+          if ((up - slack) * (step < kFine ? kWidth : kCoarse) >= need * (1.f + 0x1p-10f)) atomicMin(&sh.bin2, step);
         }
         at = up;
       }

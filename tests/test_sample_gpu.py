@@ -2,7 +2,10 @@
 
 Tolerances. A weight is off by at most 2^-37 of itself (the pair of its exponent holds 2^-39, the polynomial
 2^-44, the table 2^-48) and rounded to 2^-41 of the largest weight, so running sums are off by at most
-2^-36 of the total and 2^-41 a token: a border within that distance of u may fall to either side. What equals a border
+2^-36 of the total and 2^-41 a token: a border within that distance of u may fall to either side. With p next to 1 more than
+one token lies within it (a token behind the border weighs less than (1 - p) of the total, at p = 1 - 2^-24 and a 40th of that
+each some 2^-29, and 30011 tokens allow for 2^-26): the border is then any of these, as each is p's for sums that are off by
+less. What equals a border
 of top-p by arithmetic (equal logits) has to come out exactly. Probabilities are a float (2^-24), times an inverse (2^-24
 for the total as a float, 2^-24 for the division), rounded (2^-24): 5 x 2^-24 with the weight's own rounding, and
 the smallest float where they vanish."""
@@ -39,6 +42,12 @@ def _check(logits, T, u=None, k=None, p=None, m=None):
         sets = [ref.kept(x[r], *args, off=o) for o in (0.0, -off, off)]
         got = probs[r] > 0
         near = [s for s in sets if not (got & ~s).any() and not (s & ~got & (w > 1e-30)).any()]
+        if not near:   # the first tokens of the order, and no fewer and no more than both ends of that distance leave
+            order = np.lexsort((np.arange(V), -x[r]))
+            first = np.zeros(V, dtype=bool)
+            first[order[:int(got.sum())]] = True
+            if (first == got).all() and not (sets[1] & ~got).any() and not (got & ~sets[2]).any():
+                near = [got]
         assert near, (r, args, int(got.sum()), [int(s.sum()) for s in sets])
         left = np.where(near[0], w, 0.0)
         want = left / left.sum() if left.sum() > 0 else left
@@ -240,3 +249,17 @@ def test_bf16_logits_of_every_size(shift, scale, filters):
     if filters == "min_p":
         kw["m"] = [0.3, 0.5, 0.01, 1e-6, 0.9, 0.1]
     _check(x, T, a["u"], **kw)
+
+
+@pytest.mark.parametrize("T", [0.05, 0.2, 0.45, 0.8])
+@pytest.mark.parametrize("up", [3.0, 9.0, 25.0])
+def test_borders_far_below_the_largest(up, T):
+    """Some likely tokens, and borders among those that have next to no weight."""
+    R, V = 10, 30011
+    x = _logits(R, V, torch.float32, 17, scale=2.0)
+    x[:, 5:17] += up
+    x[2, 100:200] = x[2, 99]                           # equal ones there
+    ks = [11, 13, 40, 400, 2000, 29000, 0, 0, 0, 30]
+    ps = [1.0, 1.0, 0.999, 1.0, 1.0, 1.0, 1 - 2.0 ** -20, 1 - 2.0 ** -24, 0.5, 1 - 2.0 ** -24]
+    _check(x, [T] * R, _params(R, 17)["u"], k=ks, p=ps)
+    _check(x, [T] * R, _params(R, 18)["u"], k=ks)
