@@ -3,9 +3,9 @@
 Tolerances. A weight is off by at most 2^-37 of itself (the pair of its exponent holds 2^-39, the polynomial
 2^-44, the table 2^-48) and rounded to 2^-41 of the largest weight, so running sums are off by at most
 2^-36 of the total and 2^-41 a token: a border within that distance of u may fall to either side. With p next to 1 more than
-one token lies within it (a token behind the border weighs less than (1 - p) of the total, at p = 1 - 2^-24 and a 40th of that
-each some 2^-29, and 30011 tokens allow for 2^-26): the border is then any of these, as each is p's for sums that are off by
-less. What equals a border
+one token may lie within it: what is behind the border has 1 - p of the total, at p = 1 - 2^-24 spread over thousands of tokens
+of less than 2^-30 each, and the sums of 30011 tokens may be off by 2^-36 + 30011 x 2^-41 > 2^-27. Each of these tokens is then
+p's border for sums that are off by less. What equals a border
 of top-p by arithmetic (equal logits) has to come out exactly. Probabilities are a float (2^-24), times an inverse (2^-24
 for the total as a float, 2^-24 for the division), rounded (2^-24): 5 x 2^-24 with the weight's own rounding, and
 the smallest float where they vanish."""
