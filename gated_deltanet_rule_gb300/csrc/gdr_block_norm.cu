@@ -6,6 +6,9 @@
 //   dh = dx,   dscale = sum dx g z,   dgate = dx scale z g (1 - g),   dz = dx scale g,
 //   dpost_w = sum dz y r,   dy = r (post_w dz - y r^2 mean(post_w dz y))  (or dz).
 //
+// Measured: 8192 rows of 4096 bf16 57 us (5.9 TB/s, 86% of the copy bandwidth), their gradient 124 us (5.4 TB/s, 79%),
+// that of 2731 rows of 2560 float32 without gate, scale and norm of y 36 us (4.7 TB/s), 24 rows of 2048 5.8 us (launch).
+//
 // Both are bound by HBM. A block takes a row at a time, a thread 8 channels of it (16 neighbouring bytes, of
 // float32 twice), so that a row stays in registers from its one reading to its writing; the weights of a
 // thread's channels are read once and kept. Up to four rows are on their way to a block's shared memory.

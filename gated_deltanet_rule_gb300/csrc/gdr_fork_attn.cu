@@ -9,13 +9,22 @@
 // groups in the place of rows). From about 280 query rows a key head on it is bound by the products, below by HBM.
 //
 // The own part: a key head of a row has few queries (nodes times heads a key head) over keys that nobody
-// else reads, so it is bound by reading them. An item is a row, a key head and up to 16, 32 or 64 of its query rows; a
-// block takes items one after the other, two blocks an SM. One warp looks the items up and loads (queries, and tiles of
-// the row's positions as TMA boxes of its pages, several tiles and up to two items ahead), four warps compute: each
-// multiplies 16 query rows by 16 or 32 positions with warp-level matrix instructions, which a 128-row tcgen05 tile
-// would fill to a sixteenth or less (starting and draining such an item takes 4 us of an SM, against 2 us for its
-// reading). Warps that share rows take positions in turn and are joined at the end, in order; then the shared part's
-// result is joined.
+// else reads, so it is bound by reading them. An item is a row, a key head and up to 8, 16, 32 or 64 of its query rows; a
+// team of warps takes items one after the other. One warp looks the items up and loads (queries, and tiles of
+// the row's positions as TMA boxes of its pages, several tiles and up to two items ahead), the others compute with warp-level
+// matrix instructions, of which a 128-row tcgen05 tile would fill a sixteenth or less (starting and draining such an item
+// takes 4 us of an SM, against 2 us for its reading). Warps that share rows take positions in turn and are joined at the
+// end, in order; then the shared part's result is joined.
+//   up to 8 query rows: fork_own_few_kernel, which computes the transposed products, an item a team of four warps, or of one
+//   or two where there are many;
+//   more: fork_own_kernel, 16 query rows a warp, four warps an item.
+//
+// Measured (floor: bytes at 6795 GB/s or operations at 1880 TFLOP/s): 256 forks of 8 trunks of up to 8192 positions, 32 / 8
+// heads of 128, 95.2 us (52.6 HBM): shared part 50, join 15 (partly within the others), own part 41 at 4.7 TB/s, the rest of
+// that the end, where the last items run alone. 64 forks of 65536 positions, 16 / 2 heads of 256, 106.5 (36.6 operations):
+// shared part 88, a 128-row tile an item, whose softmax runs between the products. 64 rows of 64 tokens, 4 trunks, 16 / 4 heads
+// of 128, 206.8 (89.7 operations): shared part 149 at 60% of the matrix rate (bound by the exponentials), own part 49, bound by the latency of
+// its steps with eight computing warps an SM. 3 forks of 448 positions 11.9: one kernel, eight tiles one after the other.
 //
 // Weights are rounded to bfloat16 for their product with v, the sum adds them unrounded; scores, sums and parts are
 // float32.
