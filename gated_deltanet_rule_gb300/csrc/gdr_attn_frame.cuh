@@ -68,7 +68,7 @@ using namespace ptx;
 
 namespace {
 
-constexpr int kThreads = 384;   // warps: 0 loads, 1 products, 2-3 idle, 4-11 softmax
+constexpr int kThreads = 384;   // warps: 0 loads (kSplit: 0 keys, 2 values), 1 products, 4-11 softmax
 constexpr int kBlocks = kNumSMs;
 constexpr int kM = 128;         // rows of an M tile
 constexpr float kLog2e = 1.4426950408889634f;
@@ -114,6 +114,9 @@ template <int D, int kForm>
 struct Cfg {
   static constexpr int KT = kForm == kSplit ? 64 : 128;      // positions of a tile
   static constexpr int kTiles = kForm == kWide ? 2 : 1;      // M tiles of an item
+  // Keys and values loaded by a warp each: with pages of 16 a tile of heads of 256 takes 32 copies of 2 KB, and one warp did not
+  // issue them in time (512 queries a key head over 65536 positions: 106.5 -> 92 us; pages of 32 and more, or fewer queries: the same).
+  static constexpr bool kTwoLoad = kForm == kSplit;
   static constexpr int kRows = kTiles * kM;
   static constexpr uint32_t kTile = KT * D * 2;              // bytes of a K or V tile
   static constexpr int NS = D == 64 ? 8 : kForm == kNarrow ? 6 : 5;   // tile buffers
@@ -137,6 +140,7 @@ struct Bars {
   int b0, hk0, mt0, t0;
   long long todo;
   int later;           // that unit begins an item after the share's first unit
+  long long filled[2]; // the loading warps' next tiles of keys and values when they end
 };
 static_assert(sizeof(Bars) <= 512, "barriers fit their region");
 
@@ -550,6 +554,7 @@ __device__ __forceinline__ void put32(const float* o, bool whole, uint4* out, co
 }
 
 constexpr uint32_t kSoftmaxBar = 1;   // named barrier of the eight softmax warps; 2 .. 5: pairs of kSplit
+constexpr uint32_t kLoadBar = 6;      // of the two loading warps of kSplit
 
 template <int D, int kForm, class A>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -619,15 +624,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool ok = true;
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    if (warp == 0) {
+    if (warp == 0 || (C::kTwoLoad && warp == 2)) {
     // ------------------------------------------------------------------------------ loads
+    const int kv0 = C::kTwoLoad ? warp >> 1 : 0, kvs = C::kTwoLoad ? 1 : 2;   // keys (0), values (1) or both in turn
     Walk<KT> w;
     w.start(a, s);
     const int rows = min(a.page, KT);                       // positions of one box
     const uint32_t box = rows * 128u;                       // its bytes in one 64-column slab
     const int most = KT / rows;                             // boxes of a tile
     Ring<NS> ring;
-    int loads = 0;                                          // tiles loaded, at most NS counted
+    ring.step(kv0);
+    long long fill = kv0;                                   // of the block's tiles of keys and values, in turn
     int q_loads = 0;
     while (ok && w.next(a)) {
       const int end = A::kShared ? w.ctx : w.ctx + w.n;
@@ -653,11 +660,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           atomicCAS(a.err, 0, kErrDeviceIndex);
           src = -1;
         }
-        for (int kv = 0; kv < 2; ++kv) {
+        for (int kv = kv0; kv < kv0 + kvs; ++kv) {
           const int slot = ring.slot;
-          if (loads == NS) ok = warp_wait(&s.empty[slot], ring.parity ^ 1, a.budget);
-          else ++loads;
+          if (fill >= NS) ok = warp_wait(&s.empty[slot], ring.parity ^ 1, a.budget);
           if (!ok) break;
+          fill += 3 - kvs;
           if (lane == 0) mbar_arrive_expect_tx(&s.full[slot], pieces * box * (D / 64));
           __syncwarp();
           if (lane < pieces) {
@@ -667,10 +674,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_4d(dst + h * KT * 128, kv ? &mv : &mk, &s.full[slot], h * 64, w.hk, at, src);
           }
           __syncwarp();
-          ring.step(1);
+          ring.step(3 - kvs);
         }
         if (!ok) break;
-        if (t == w.t0) {
+        if (kv0 == 0 && t == w.t0) {
           // the segment's queries, once the last segment's are done with: after the first tile, which
           // needs only free buffers, is on its way
           if (w.index > 0) ok = warp_wait(&s.q_empty, (w.index - 1) & 1, a.budget);
@@ -688,8 +695,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // no copy of this block is left in flight
-    // (a buffer before the ring's place is in its present round, the others are in the one before)
-    for (int i = 0; i < loads; ++i) warp_wait(&s.full[i], i < ring.slot ? ring.parity : ring.parity ^ 1, kDrainBudget);
+    if (lane == 0) {
+      s.filled[kv0] = fill;
+      if (!C::kTwoLoad) s.filled[1] = fill;
+    }
+    __syncwarp();
+    if constexpr (C::kTwoLoad) named_bar_and(kLoadBar, 64, true);
+    for (int i = kv0; i < NS; i += 3 - kvs) {   // (each buffer's last filling: keys have even numbers, values odd ones)
+      const long long top = max(s.filled[0], s.filled[1]) - 1;
+      long long f = top - (top - i + NS) % NS;
+      while (f >= 0 && f >= s.filled[f & 1]) f -= NS;
+      if (f >= 0) warp_wait(&s.full[i], (uint32_t)(f / NS) & 1, kDrainBudget);
+    }
     if (q_loads > 0) warp_wait(&s.q_full, (q_loads - 1) & 1, kDrainBudget);
     } else if (warp == 1) {
     // ------------------------------------------------------------------------------ products
@@ -836,7 +853,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // ------------------------------------------------------------------------------ absent nodes: 0, -inf
       const int vecs = a.Hq * D / 8;
-      for (int x = 2 * blockIdx.x + warp - 2; !A::kShared && x < a.B * a.N; x += 2 * kBlocks) {
+      constexpr int kWarps = C::kTwoLoad ? 1 : 2;
+      for (int x = kWarps * blockIdx.x + warp - 4 + kWarps; !A::kShared && x < a.B * a.N; x += kWarps * kBlocks) {
         const int b = x / a.N, i = x - b * a.N;
         int n, ctx;
         row_of(a, b, n, ctx);
