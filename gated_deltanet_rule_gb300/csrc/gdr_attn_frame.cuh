@@ -126,11 +126,12 @@ struct Cfg {
   static constexpr uint32_t kBars = kRed + 2048;
   static constexpr uint32_t kSmem = kBars + 512;
   static constexpr uint32_t kTmemO = 2 * KT;                 // two S buffers at columns 0 and KT: kSplit's tiles alternate, else one a stream
+  static constexpr uint32_t kTmemQ = kTmemO + D;             // (kSplit) the queries: all 512 columns
 };
 
 struct Bars {
   uint64_t full[8], empty[8];
-  uint64_t q_full, q_empty;
+  uint64_t q_full, q_empty, q_there;   // (q_there: kSplit's queries are in TMEM)
   uint64_t s_full[2], p_full[2], pv[2];   // by S buffer: S formed, P written, P V done
   uint64_t o_free;     // the segment's accumulators have been read
   uint64_t drain;
@@ -577,7 +578,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s.empty[i], 1);
     }
     mbar_init(&s.q_full, 1);
-    mbar_init(&s.q_empty, 1);
+    mbar_init(&s.q_empty, kForm == kSplit ? 8 : 1);
+    mbar_init(&s.q_there, 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.p_full[i], kForm == kSplit ? 8 : 4);
@@ -724,11 +726,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lead && ok) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          mma_bf16(d, desc64(q0 + (((kk >> 2) * kM * 128 + (kk & 3) * 32) >> 4), hi),
-                   desc64(k0 + (((kk >> 2) * KT * 128 + (kk & 3) * 32) >> 4), hi), kIdS, kk > 0);
+        {
+          const uint64_t kd = desc64(k0 + (((kk >> 2) * KT * 128 + (kk & 3) * 32) >> 4), hi);
+          if constexpr (kForm == kSplit) mma_f16_tmem_a(d, tb + C::kTmemQ + kk * 8, kd, kIdS, kk > 0);
+          else mma_bf16(d, desc64(q0 + (((kk >> 2) * kM * 128 + (kk & 3) * 32) >> 4), hi), kd, kIdS, kk > 0);
+        }
         mma_commit(&s.s_full[buf]);
         if (free_k) mma_commit(&s.empty[slot]);
-        if (free_q) mma_commit(&s.q_empty);
+        if (kForm != kSplit && free_q) mma_commit(&s.q_empty);
       }
       __syncwarp();
     };
@@ -756,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     vr.step(1);
     uint32_t steps[2] = {0, 0};     // scores formed for each stream so far (kSplit: in all)
     while (ok && w.next(a)) {
-      wait(&s.q_full, w.index & 1);
+      wait(kForm == kSplit ? &s.q_there : &s.q_full, w.index & 1);
       // (the same in every lane: broadcast, so that loop counts, addresses and descriptors stay in uniform registers)
       const int T = __shfl_sync(0xffffffffu, w.t1 - w.t0, 0);
       const bool first = __shfl_sync(0xffffffffu, w.index, 0) == 0;
@@ -886,6 +891,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int end = A::kShared ? w.ctx : w.ctx + w.n;
       const int T = w.t1 - w.t0;
       const bool masked_any = w.t1 * KT > w.ctx;
+      if constexpr (kForm == kSplit) {
+        // The queries into TMEM, half of its row a thread: products of 64 positions that read them from shared memory are
+        // bound by that (96 KB a tile). All scores of the segment before, the last readers, have been waited for.
+        ok = ok && warp_wait(&s.q_full, w.index & 1, a.budget);
+        if (ok) {
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {   // 32 channels
+            uint32_t q[16];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int unit = st * (D / 16) + c * 4 + e;
+              const uint4 v = *reinterpret_cast<const uint4*>(sm + (unit >> 3) * kM * 128 + row * 128 + (((unit & 7) ^ (row & 7)) << 4));
+              q[4 * e] = v.x;
+              q[4 * e + 1] = v.y;
+              q[4 * e + 2] = v.z;
+              q[4 * e + 3] = v.w;
+            }
+            tmem_st16_nowait(rows_at + C::kTmemQ + st * (D / 4) + c * 16, q);
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && ok) {
+          mbar_arrive(&s.q_there);
+          mbar_arrive(&s.q_empty);
+        }
+      }
       float m_ref = -INFINITY, l = 0.f;
       const bool works = kForm != kWide || st == 0 || used > 0;   // (an item's second M tile may be empty)
       constexpr int kStep = kForm == kNarrow ? 2 : 1;
