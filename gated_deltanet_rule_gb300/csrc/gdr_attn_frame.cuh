@@ -19,7 +19,9 @@
 //   kNarrow D <= 128, up to 128 rows: one M tile, the warpgroups take every other key tile, each with
 //           its own accumulator, maximum and sum, joined at the end of the segment.
 //   kSplit  D = 256: an accumulator takes half of TMEM, so there is one: the warpgroups take half of each
-//           tile's columns, S alternates between two buffers.
+//           tile's columns, S alternates between two buffers. The queries lie in TMEM's other quarter, and keys and
+//           values are loaded by a warp each (512 rows a key head over 65536 positions in pages of 16: 106.5 us before,
+//           90.4 with two loading warps, 87.6 with the queries in TMEM, 80.1 with seven tile buffers in their place).
 // A warp of kWide and kNarrow holds whole rows of S (a row a thread): no exchange inside a tile.
 // The products are issued by an elected lane of a converged warp, straight-line, from descriptors that
 // are one word plus a constant: 64 cycles a 128 x 128 x 16 product, against about 100 from a branch on
@@ -83,6 +85,7 @@ enum Form { kSplit = 0, kNarrow = 1, kWide = 2 };
 
 struct Args {
   static constexpr bool kShared = false;
+  const __nv_bfloat16* q;
   const int32_t* table;
   const int32_t* ctx;
   const int32_t* lengths;
@@ -114,13 +117,13 @@ template <int D, int kForm>
 struct Cfg {
   static constexpr int KT = kForm == kSplit ? 64 : 128;      // positions of a tile
   static constexpr int kTiles = kForm == kWide ? 2 : 1;      // M tiles of an item
-  // Keys and values loaded by a warp each: with pages of 16 a tile of heads of 256 takes 32 copies of 2 KB, and one warp did not
-  // issue them in time (512 queries a key head over 65536 positions: 106.5 -> 92 us; pages of 32 and more, or fewer queries: the same).
+  // Keys and values loaded by a warp each: with pages of 16 a tile of heads of 256 takes 32 copies of 2 KB, and one warp does not
+  // issue them in time (pages of 32 and more, or fewer queries: the same times).
   static constexpr bool kTwoLoad = kForm == kSplit;
   static constexpr int kRows = kTiles * kM;
   static constexpr uint32_t kTile = KT * D * 2;              // bytes of a K or V tile
-  static constexpr int NS = D == 64 ? 8 : kForm == kNarrow ? 6 : 5;   // tile buffers
-  static constexpr uint32_t kQTile = kM * D * 2;
+  static constexpr int NS = D == 64 ? 8 : kForm == kNarrow ? 6 : kForm == kWide ? 5 : 7;   // tile buffers
+  static constexpr uint32_t kQTile = kForm == kSplit ? 0 : kM * D * 2;   // (kSplit: in TMEM)
   static constexpr uint32_t kRing = kTiles * kQTile;
   static constexpr uint32_t kRed = kRing + NS * kTile;       // float [2][2][128]
   static constexpr uint32_t kBars = kRed + 2048;
@@ -578,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&s.empty[i], 1);
     }
     mbar_init(&s.q_full, 1);
-    mbar_init(&s.q_empty, kForm == kSplit ? 8 : 1);
+    mbar_init(&s.q_empty, 1);
     mbar_init(&s.q_there, 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.s_full[i], 1);
@@ -679,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ring.step(3 - kvs);
         }
         if (!ok) break;
-        if (kv0 == 0 && t == w.t0) {
+        if (kForm != kSplit && t == w.t0) {
           // the segment's queries, once the last segment's are done with: after the first tile, which
           // needs only free buffers, is on its way
           if (w.index > 0) ok = warp_wait(&s.q_empty, (w.index - 1) & 1, a.budget);
@@ -893,31 +896,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool masked_any = w.t1 * KT > w.ctx;
       if constexpr (kForm == kSplit) {
         // The queries into TMEM, half of its row a thread: products of 64 positions that read them from shared memory are
-        // bound by that (96 KB a tile). All scores of the segment before, the last readers, have been waited for.
-        ok = ok && warp_wait(&s.q_full, w.index & 1, a.budget);
+        // bound by that (96 KB a tile), and their place holds two more tiles. All scores of the segment before, the last
+        // readers, have been waited for.
+        size_t qrow = ((size_t)w.b * a.N + i) * a.Hq + w.hk * a.G + hg;
+        if constexpr (A::kShared) qrow = ((size_t)__ldg(a.first + w.b) * a.N_row + i) * a.Hq + w.hk * a.G + hg;
+        const uint4* from = reinterpret_cast<const uint4*>(a.q + qrow * D + st * (D / 2));
+        uint4 q[D / 16];
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) q[e] = live ? __ldg(from + e) : make_uint4(0, 0, 0, 0);
+        __syncwarp();
         if (ok) {
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) {   // 32 channels
-            uint32_t q[16];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int unit = st * (D / 16) + c * 4 + e;
-              const uint4 v = *reinterpret_cast<const uint4*>(sm + (unit >> 3) * kM * 128 + row * 128 + (((unit & 7) ^ (row & 7)) << 4));
-              q[4 * e] = v.x;
-              q[4 * e + 1] = v.y;
-              q[4 * e + 2] = v.z;
-              q[4 * e + 3] = v.w;
-            }
-            tmem_st16_nowait(rows_at + C::kTmemQ + st * (D / 4) + c * 16, q);
-          }
+          for (int c = 0; c < D / 64; ++c) tmem_st16_nowait(rows_at + C::kTmemQ + st * (D / 4) + c * 16, reinterpret_cast<const uint32_t*>(q + 4 * c));
           tmem_wait_st();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0 && ok) {
-          mbar_arrive(&s.q_there);
-          mbar_arrive(&s.q_empty);
-        }
+        if (lane == 0 && ok) mbar_arrive(&s.q_there);
       }
       float m_ref = -INFINITY, l = 0.f;
       const bool works = kForm != kWide || st == 0 || used > 0;   // (an item's second M tile may be empty)
@@ -1355,6 +1350,7 @@ cudaError_t launch(const TreeAttnArgs& p, A a, cudaStream_t st) {
       !make_map(&mk, p.k_pages, D, p.Hk, p.page, p.P, 1, std::min(p.page, C::KT)) ||
       !make_map(&mv, p.v_pages, D, p.Hk, p.page, p.P, 1, std::min(p.page, C::KT)))
     return cudaErrorInvalidValue;
+  a.q = static_cast<const __nv_bfloat16*>(p.q);
   a.table = p.table; a.ctx = p.ctx; a.lengths = p.lengths; a.mask = A::kShared ? nullptr : p.mask;
   a.v_pages = static_cast<const __nv_bfloat16*>(p.v_pages);
   a.sl2 = p.scale * kLog2e;
