@@ -330,3 +330,25 @@ def test_few_query_rows_and_what_is_not_finite(B, wide, D):
         for b in rows:
             inside[b, :int(d["lengths"][b]), 4:8, 7] = True
         assert not torch.isfinite(o[inside]).any() and torch.isfinite(o[~inside]).all(), x
+
+
+def test_pages_beyond_32_bit_offsets():
+    """Pools of more than 2^32 elements: the same bits as from a small one, in every form of the call."""
+    page, D = 128, 256
+    pool_pages = (1 << 32) // (page * D) + 70
+    pools = [torch.empty(pool_pages, page, 1, D, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    for B, N, Hq, wide in ((3, 2, 4, False), (3, 2, 4, True), (2, 3, 6, False), (2, 20, 4, False)):
+        c = _case([0, B], [128], [30, 100], N, Hq, 1, D, page, "random", seed=B + N)
+        c = _wide(c) if wide else c
+        P = c["k"].shape[0]
+        pos = int(c["ctx"][0])
+        c["v"][c["table"][0, pos // page].long(), pos % page, 0, 5] = float("inf")   # (read again by the rows that see it)
+        a = _args(c)
+        want = gdr.gdr_fork_attn(*a, want_lse=True)
+        for pool, x in zip(pools, (a[1], a[2])):
+            pool[pool_pages - P:] = x
+        table = torch.where(a[3] >= 0, a[3] + (pool_pages - P), a[3]).int()
+        got = gdr.gdr_fork_attn(a[0], pools[0], pools[1], table, *a[4:], want_lse=True)
+        gdr.gdr_sync_status()
+        assert all(torch.equal(x.view(torch.int16 if x.dtype == torch.bfloat16 else I32), y.view(torch.int16 if y.dtype == torch.bfloat16 else I32))
+                   for x, y in zip(want, got))
