@@ -36,7 +36,7 @@
 // Measured (bfloat16, a call among others): one token over 700 positions 12.3 us (latency); 16 trees of 13
 // nodes over up to 8192 positions, 32 / 8 heads of 128: 72.4 us, 73% of the copy bandwidth (95% while it
 // streams); 8 trees of 64 nodes over up to 16384, 32 / 4 heads of 128: 93.9 us, 47% of the matrix rate; 2
-// trees of 7 over 131072, 16 / 2 heads of 256: 80.5 us, 76% of the copy bandwidth. (Comparisons below that
+// trees of 7 over 131072, 16 / 2 heads of 256: 78.5 us, 77% of the copy bandwidth. (Comparisons below that
 // give slightly other times for these are of replayed graphs.)
 //
 // The running maximum is kept as a reference that moves only when the maximum has grown by more than 8
