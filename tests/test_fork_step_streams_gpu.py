@@ -103,3 +103,22 @@ def test_a_wait_that_runs_out_is_reported():
         gdr.debug_set_wait_budget(-1)
     assert all(torch.equal(a, b) for a, b in zip(want, call()))
     gdr.gdr_sync_status()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("B,N,Hq,Hk,shared", [(3, 1, 4, 1, 128), (31, 1, 8, 2, 4096), (240, 2, 8, 2, 2048), (20, 3, 8, 2, 4096), (12, 8, 8, 2, 4096), (12, 40, 8, 2, 4096)])
+def test_waits_that_run_out_in_every_form(B, N, Hq, Hk, shared, D):
+    a = _args(_case([0, B], [shared], [200, 400, 3], N, Hq, Hk, D, 16, seed=60 + B))
+    want = gdr.gdr_fork_attn(*a, want_lse=True)
+    gdr.gdr_sync_status()
+    gdr.debug_set_wait_budget(0)
+    try:
+        gdr.gdr_fork_attn(*a, want_lse=True)
+        with pytest.raises(gdr.GdrError) as e:
+            gdr.gdr_sync_status()
+        assert e.value.status == gdr.GDR_ERR_TIMEOUT
+    finally:
+        gdr.debug_set_wait_budget(-1)
+    got = gdr.gdr_fork_attn(*a, want_lse=True)
+    gdr.gdr_sync_status()
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
