@@ -15,8 +15,8 @@
 // matrix instructions, of which a 128-row tcgen05 tile would fill a sixteenth or less (starting and draining such an item
 // takes 4 us of an SM, against 2 us for its reading). Warps that share rows take positions in turn and are joined at the
 // end, in order; then the shared part's result is joined.
-//   up to 8 query rows: fork_own_few_kernel, which computes the transposed products, an item a team of four warps, or of one
-//   or two where there are many;
+//   up to 8 query rows: fork_own_few_kernel, which computes the transposed products, an item a team of eight or four warps, or
+//   of one or two where there are many;
 //   more: fork_own_kernel, 16 query rows a warp, four warps an item.
 //
 // Measured (floor: bytes at 6795 GB/s or operations at 1880 TFLOP/s): 256 forks of 8 trunks of up to 8192 positions, 32 / 8
@@ -24,7 +24,7 @@
 // that the end, where the last items run alone. 64 forks of 65536 positions, 16 / 2 heads of 256, 80.1 (36.6 operations):
 // shared part 64, a 128-row tile an item, whose softmax runs between the products. 64 rows of 64 tokens, 4 trunks, 16 / 4 heads
 // of 128, 206.8 (89.7 operations): shared part 149 at 60% of the matrix rate (softmax), own part 49, bound by the
-// latency of its steps with eight computing warps an SM. 3 forks of 448 positions 11.9: one kernel, eight tiles one after
+// latency of its steps with eight computing warps an SM. 3 forks of 448 positions 10.3: one kernel, four tiles one after
 // the other.
 //
 // Weights are rounded to bfloat16 for their product with v, the sum adds them unrounded; scores, sums and parts are
@@ -629,7 +629,8 @@ __global__ void __launch_bounds__(kOwnThreads, D == 256 ? 1 : 2)
 // loads; a block is as many teams as fit.
 template <int D, int WK>
 struct Few {
-  static constexpr int kTeams = WK == 4 ? 1 : D == 64 ? 8 : D == 128 ? 5 : 2;
+  // (of two warps, heads of 128: 256 forks by 5, 4 and 3 teams 95.5, 99.6, 99.9 us)
+  static constexpr int kTeams = WK >= 4 ? 1 : D == 64 ? 8 : D == 128 ? 5 : 2;
   static constexpr int kBlocks = WK == 4 && D < 256 ? 2 : 1;   // an SM
   static constexpr int kThreads = 32 * kTeams * (WK + 1);
   static constexpr int kRows = 8, PW = WK == 1 ? 32 : 16, KT = PW * WK;   // positions of a warp and of a tile
@@ -859,7 +860,7 @@ __global__ void __launch_bounds__(Few<D, WK>::kThreads, Few<D, WK>::kBlocks)
     if (!ok) break;
     // the weights of the warps' parts and of the shared one
     float c[2][WK], c_s[2];
-    uint32_t rare = 0, seen = 0;                         // bit 8 e + w: part w of query e saw something (8 e + 7: the shared one)
+    uint32_t rare = 0, seen = 0;                         // bit 16 e + w: part w of query e saw something (16 e + 15: the shared one)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       float top = m[e], sum = l[e];
@@ -874,21 +875,21 @@ __global__ void __launch_bounds__(Few<D, WK>::kThreads, Few<D, WK>::kBlocks)
           const float mw = s_m[team][w][q0 + e];
           c[e][w] = mw == top ? 1.f : ex2_approx(mw - top);
           sum += c[e][w] * s_l[team][w][q0 + e];
-          if (mw != -INFINITY) seen |= 1u << (8 * e + w);
+          if (mw != -INFINITY) seen |= 1u << (16 * e + w);
         }
       } else if (top != -INFINITY) {
-        seen |= 1u << (8 * e);
+        seen |= 1u << (16 * e);
       }
-      if (lse_s[e] != -INFINITY) seen |= 128u << (8 * e);
+      if (lse_s[e] != -INFINITY) seen |= 0x8000u << (16 * e);
       const Factors f = factors(q0 + e < used, joins, top, sum, lse_s[e]);
       const float inv = f.sees ? f.own / (sum * f.total) : 0.f;
 #pragma unroll
       for (int w = 0; w < WK; ++w) {
         c[e][w] *= inv;
-        if (f.sees && c[e][w] == 0.f) rare |= 1u << (8 * e + w);
+        if (f.sees && c[e][w] == 0.f) rare |= 1u << (16 * e + w);
       }
       c_s[e] = f.shared / f.total;
-      if (c_s[e] == 0.f) rare |= 128u << (8 * e);
+      if (c_s[e] == 0.f) rare |= 0x8000u << (16 * e);
       if (a.lse && wk == 0 && lane < 4 && q0 + e < t.rows) a.lse[base + node_of[e] * (a.Hq - a.heads) + q0 + e] = f.lse;
     }
     rare &= seen;                                        // what saw something and has no weight: it counts where it is not finite
@@ -899,7 +900,7 @@ __global__ void __launch_bounds__(Few<D, WK>::kThreads, Few<D, WK>::kBlocks)
       float y[2] = {0.f, 0.f};
       auto add = [&](int e, int bit, float f, float part) {
         if (f != 0.f) y[e] = fmaf(f, part, y[e]);        // (without weight it may hold anything)
-        else if ((rare >> (8 * e + bit) & 1) && !(fabsf(part) < INFINITY)) y[e] += part;
+        else if ((rare >> (16 * e + bit) & 1) && !(fabsf(part) < INFINITY)) y[e] += part;
       };
 #pragma unroll
       for (int w = 0; w < WK; ++w) {
@@ -909,8 +910,8 @@ __global__ void __launch_bounds__(Few<D, WK>::kThreads, Few<D, WK>::kBlocks)
         add(0, w, c[0][w], part.x);
         add(1, w, c[1][w], part.y);
       }
-      add(0, 7, c_s[0], z[0][i]);
-      add(1, 7, c_s[1], z[1][i]);
+      add(0, 15, c_s[0], z[0][i]);
+      add(1, 15, c_s[1], z[1][i]);
       const uint32_t u = turned(pack_bf16x2(y[0], y[1]));
       if (out_row < t.rows) *reinterpret_cast<uint32_t*>(a.o + out_at + 8 * d) = u;
     }
@@ -1014,16 +1015,26 @@ cudaError_t own_by_teams(const ForkAttnArgs& p, cudaStream_t s) {
   return own_part<Own<D, WR>, D, fork_own_kernel<D, WR>, kOwnThreads, D == 256 ? 1 : 2>(p, false, s);
 }
 
+// Few items: by four warps each, by eight where every item has an SM to itself (16 rows of 250, 1000 and 4000 positions of their
+// own, 32 items: 24, 30 and 63 us by four, 26, 26 and 49 by eight; 3 forks of 448 positions 12.3 and 10.3).
+template <int D>
+cudaError_t own_of_few(const ForkAttnArgs& p, bool alone, cudaStream_t s) {
+  if constexpr (D < 256)
+    if ((long long)p.t.B * p.t.Hk <= kNumSMs) return own_few<D, 8>(p, alone, s);
+  return own_few<D, 4>(p, alone, s);
+}
+
 template <int D>
 cudaError_t both_parts(const ForkAttnArgs& p, cudaStream_t s) {
   const int G = p.t.Hq / p.t.Hk;
   // two M tiles an item where a group of the average size has more rows a key head than one holds
   const long long rows = ((long long)p.t.B + p.T - 1) / p.T * p.t.N * G;
   // Short rows, all of whose items are resident at once: each reads its shared positions itself, one kernel in the place of
-  // three (us by three and by one, 3 rows, 12 items: of 250 positions 24 and 13, 500 24 and 15, 1000 23 and 21, 2000 25 and 31;
-  // D = 256: 22 and 15, 22 and 17, 22 and 23, 25 and 36). The table's width is all that the host knows of the lengths.
-  if (p.t.N * G <= 8 && (long long)p.t.B * p.t.Hk <= kNumSMs * Few<D, 4>::kBlocks && (long long)p.t.M * p.t.page <= (D == 256 ? 512 : 1024))
-    return own_few<D, 4>(p, true, s);
+  // three (us by three and by one, 3 rows, 12 items: of 250 positions 25 and 13, 500 26 and 15, 1000 26 and 17, 2000 28 and 23;
+  // 64 rows, 256 items: 35 and 15, 35 and 17, 34 and 21, 35 and 31; D = 256, 3 rows: 22 and 15, 22 and 17, 22 and 23, 25 and 36).
+  // The table's width is all that the host knows of the lengths.
+  if (p.t.N * G <= 8 && (long long)p.t.B * p.t.Hk <= kNumSMs * Few<D, 4>::kBlocks && (long long)p.t.M * p.t.page <= (D == 256 ? 512 : 2048))
+    return own_of_few<D>(p, true, s);
   cudaError_t e;
   if constexpr (D == 256) e = shared_part<D, kSplit>(p, s);
   else e = rows > kM ? shared_part<D, kWide>(p, s) : shared_part<D, kNarrow>(p, s);
@@ -1034,7 +1045,7 @@ cudaError_t both_parts(const ForkAttnArgs& p, cudaStream_t s) {
     // all parts together, own parts of 64 and of 1000 positions; D = 128: 256 items 33 and 31, 55 and 61, 512 items 38 and 34,
     // 80 and 80, 2048 items 61 and 53, 192 and 198; D = 256: 256 items 37 and 34, 79 and 79, 2048 items 104 and 80, 352 and 343).
     const bool many = (long long)p.t.B * p.t.Hk >= 3 * kNumSMs;
-    return !many ? own_few<D, 4>(p, false, s) : own_few<D, D == 64 ? 1 : 2>(p, false, s);
+    return many ? own_few<D, D == 64 ? 1 : 2>(p, false, s) : own_of_few<D>(p, false, s);
   }
   return r <= 16 ? own_by_teams<D, 1>(p, s) : r <= 32 ? own_by_teams<D, 2>(p, s) : own_by_teams<D, 4>(p, s);
 }
