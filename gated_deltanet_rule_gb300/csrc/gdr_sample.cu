@@ -27,8 +27,8 @@
 // The token is found warp, 32-unit piece, lane, entry: each a scan over lanes.
 //
 // Bound by instructions and by the steps' dependence, not by HBM: 256 rows of 131072 bf16 with top-p take 112 us (600 GB/s, issue
-// slots 54% busy), where counting is half of a block's time; 96 rows of 131072 float32 with top-p 128 us (issue 51%), a third of it
-// the pass over the exact weights (42 packed operations a pair of logits); 48 rows of 49999 38 us, one of 32000 18 us: five
+// slots 54% busy), where counting is half of a block's time; 96 rows of 131072 float32 with top-p 130 us (issue 51%), a third of it
+// the pass over the exact weights (42 packed operations a pair of logits); 48 rows of 49999 31 to 38 us, one of 32000 18 us: five
 // exchanges between the blocks and a dozen dependent steps. Weights relative to the maximum's remainder in the table, 8 operations
 // of 42 fewer, were no faster.
 #include <cuda_bf16.h>
@@ -277,6 +277,7 @@ struct Bins<bf16> {
 
 constexpr int kList = 2048;                  // candidates of a row: places, shared out evenly to its blocks
 constexpr int kOthers = 256;
+constexpr int kDirect = 384;
 struct Shared {
   float2 table[64];
   union {
@@ -532,11 +533,10 @@ struct Row {
       for (int i = 0; i < 3; ++i)
         if (threadIdx.x < ranks) st_cluster64(ptx::dsmem_addr(&sh->sums[turn_s][i][rank], threadIdx.x), v[i]);
     }
-    // (1, 2, 4 or 8 blocks: parts of whole 16 bytes)
-    const int part = kMaxSteps / 4 / ranks;
-    for (int i = threadIdx.x; i < part; i += kThreads) {
+    // (parts of whole 16 bytes)
+    const int part = (kMaxSteps / 4 + ranks - 1) / ranks, end = min((rank + 1) * part, kMaxSteps / 4);
+    for (int at = rank * part + threadIdx.x; at < end; at += kThreads) {
       uint4 t = make_uint4(0, 0, 0, 0);
-      const int at = rank * part + i;
 #pragma unroll
       for (int q = 0; q < kMaxCluster; ++q) {
         if (q >= ranks) continue;
@@ -578,9 +578,8 @@ struct Row {
     __syncthreads();
     fill(sh->hist);
     ptx::cluster_sync_all();
-    const int part = kBins / ranks;
-    for (int i = threadIdx.x; i < part; i += kThreads) {
-      const int at = rank * part + i;
+    const int part = (kBins + ranks - 1) / ranks, end = min((rank + 1) * part, kBins);
+    for (int at = rank * part + threadIdx.x; at < end; at += kThreads) {
       uint32_t n = 0;
       u64 m = 0;
 #pragma unroll
@@ -919,26 +918,77 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
       __syncthreads();
     }
     u64 all = 0, above = 0;   // the mass of all (of the first k), and above lo_step
+    // Candidates: the logits of steps first_step .. hi_step, handed to every block. How many the steps hold:
+    const int room = kList / r.ranks;
+    auto held = [&](int from, int to) {
+      if (tid == 0) {
+        sh.above_n = sh.bin_n = 0;
+        sh.mine = 0;
+      }
+      __syncthreads();
+      uint32_t at = bn;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        if (s0 + i == from) sh.bin_n = at;
+        at += n[i];
+        if (s0 + i == to) sh.above_n = at;
+      }
+      __syncthreads();
+      return sh.above_n - sh.bin_n;
+    };
+    auto hand = [&](float x, int index) {
+      const int i = atomicAdd(&sh.mine, 1);
+      const u64 c = ((u64)key_of(x) << 32) | (0xFFFFFFFFu - (uint32_t)index);
+      if (i < room)
+        for (int q = 0; q < r.ranks; ++q) st_cluster64(ptx::dsmem_addr(&sh.list[r.rank * room + i], q), c);
+    };
+    // how many each block has handed over, and whether they fit
+    int offset[kMaxCluster + 1];
+    bool fits = true;
+    auto handed = [&](int slot) {
+      offset[0] = 0;
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q) {
+        const int c = q < r.ranks ? (int)sh.sums[r.turn_s][slot][q] : 0;
+        fits = fits && c <= room;
+        offset[q + 1] = offset[q] + c;
+      }
+    };
+    // Top-p alone: a few hundred of them go along with the weighing of all, more are narrowed down first (a row of 49999: 57000
+    // cycles instead of 68700).
+    bool direct = false;
     if (cuts_p && !k_on) {
+      direct = held(lo_step, hi_step) <= kDirect;
       W2 acc = {{0}, {0}}, acc_above = {{0}, {0}};
-      const float lo_edge = (float)lo_step;
-      r.each([&](const float* x, int) {
+      const float lo_edge = (float)lo_step, hi_edge = direct ? hi_step == kSteps - 1 ? INFINITY : (float)(hi_step + 1) : lo_edge;
+      r.each([&](const float* x, int at) {
 #pragma unroll
         for (int e = 0; e < U::n; e += 2) {
           const W2 w = weights(r.s, sh.table, x[e], x[e + 1]);
           accumulate(acc, w.hi, w.lo);
-          const bool u0 = r.place(x[e]) < lo_edge, u1 = r.place(x[e + 1]) < lo_edge;
-          if (u0 || u1) {
-            const F2 up = pack(u0 ? 1.f : 0.f, u1 ? 1.f : 0.f);
+          const float y0 = r.place(x[e]), y1 = r.place(x[e + 1]);
+          if (y0 < hi_edge || y1 < hi_edge) {
+            const F2 up = pack(y0 < lo_edge ? 1.f : 0.f, y1 < lo_edge ? 1.f : 0.f);
             accumulate(acc_above, mul(w.hi, up), mul(w.lo, up));
+            if (y0 >= lo_edge && y0 < hi_edge && x[e] > -INFINITY) hand(x[e], at + e);
+            if (y1 >= lo_edge && y1 < hi_edge && x[e + 1] > -INFINITY) hand(x[e + 1], at + e + 1);
           }
         }
       });
-      const u64 mine_all = r.block_sum(fixed(acc)), v[2] = {mine_all, r.block_sum(fixed(acc_above))};
-      u64 before[2], sum[2];
-      r.cluster_sums(v, before, sum);
-      all = sum[0];
-      above = sum[1];
+      const u64 mine_all = r.block_sum(fixed(acc)), v[3] = {mine_all, r.block_sum(fixed(acc_above)), (u64)sh.mine};
+      if (tid < r.ranks)
+        for (int i = 0; i < 3; ++i) st_cluster64(ptx::dsmem_addr(&sh.sums[r.turn_s][i][r.rank], tid), v[i]);
+      ptx::cluster_sync_all();
+#pragma unroll
+      for (int q = 0; q < kMaxCluster; ++q)
+        if (q < r.ranks) {
+          all += sh.sums[r.turn_s][0][q];
+          above += sh.sums[r.turn_s][1][q];
+        }
+      handed(2);
+      r.turn_s ^= 1;
+    }
+    if (cuts_p && !k_on && !direct) {
       // With these the doubt is about the window's own mass alone: usually one or two steps are left.
       const u64 want = max((u64)1, times(all, p, true));
       const float need = want > above ? (float)(want - above) * 0x1p-40f : 0.f, slack = (float)all * 0x1p-58f;
@@ -971,24 +1021,9 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
       hi_step = max(min(sh.bin2, hi_step), first_step);
       __syncthreads();
     }
-    // candidates: the logits of steps first_step .. hi_step, handed to every block; and the mass of those before
-    if (tid == 0) sh.above_n = sh.bin_n = 0;
-    __syncthreads();
-    {
-      uint32_t at = bn;
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        if (s0 + i == first_step) sh.bin_n = at;
-        at += n[i];
-        if (s0 + i == hi_step) sh.above_n = at;
-      }
-    }
-    if (tid == 0) sh.mine = 0;
-    __syncthreads();
-    const int room = kList / r.ranks;
-    const bool few = sh.above_n - sh.bin_n <= kList / 2;
-    u64 between = 0;
-    {
+    if (!direct) {
+      const bool few = held(first_step, hi_step) <= kList / 2;
+      u64 between = 0;
       W2 acc = {{0}, {0}};
       const float w_edge = (float)lo_step, lo_edge = (float)first_step, hi_edge = (float)(hi_step + 1);
       const bool open = hi_step == kSteps - 1, mass = first_step > lo_step;
@@ -1011,31 +1046,21 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
         if (few && some)
 #pragma unroll
           for (int e = 0; e < U::n; ++e)
-            if (y[e] >= lo_edge && (y[e] < hi_edge || open) && x[e] > -INFINITY) {
-              const int i = atomicAdd(&sh.mine, 1);
-              const u64 c = ((u64)key_of(x[e]) << 32) | (0xFFFFFFFFu - (uint32_t)(at + e));
-              if (i < room)
-                for (int q = 0; q < r.ranks; ++q) st_cluster64(ptx::dsmem_addr(&sh.list[r.rank * room + i], q), c);
-            }
+            if (y[e] >= lo_edge && (y[e] < hi_edge || open) && x[e] > -INFINITY) hand(x[e], at + e);
       });
       between = fixed(acc);
-    }
-    {
       const u64 mine_between = r.block_sum(between), v[2] = {mine_between, (u64)sh.mine};
       if (tid < r.ranks)
         for (int i = 0; i < 2; ++i) st_cluster64(ptx::dsmem_addr(&sh.sums[r.turn_s][i][r.rank], tid), v[i]);
       ptx::cluster_sync_all();
-      bool fits = few;
-      int offset[kMaxCluster + 1];
-      offset[0] = 0;
 #pragma unroll
-      for (int q = 0; q < kMaxCluster; ++q) {
-        const int c = q < r.ranks ? (int)sh.sums[r.turn_s][1][q] : 0;
+      for (int q = 0; q < kMaxCluster; ++q)
         if (q < r.ranks) above += sh.sums[r.turn_s][0][q];
-        fits = fits && c <= room;
-        offset[q + 1] = offset[q] + c;
-      }
+      fits = few;
+      handed(1);
       r.turn_s ^= 1;
+    }
+    {
       if (fits) {
         // ------------------------------------------------------------ few: in order, every block for itself
         const int count = offset[kMaxCluster];
@@ -1512,14 +1537,37 @@ const Table& table() {
   return t;
 }
 
+// Blocks of a row, `bytes(c)` each of c: all at once if that can be, one an SM or (at about 1.35 the time) two, whichever
+// should end sooner. Clusters leave gaps: of more than two blocks only some 128 find an SM each, 256 a half of one. Otherwise
+// parts that two an SM can hold, or one. (us by 1, 2, 3, 4, 5, 6, 8 blocks, rows of 32000 float32, top-k and top-p: 25 rows 29, 22,
+// 20, 19, 19, 22, 22; 38 rows 29, 22, 20, 23, 23, 23, 35; 48 rows 30, 23, 26, 24, 24, 37, 40; 76 rows 29, 23, 26, 37, 38, 42, 55;
+// 150 rows 29, 29, 46, 56, 62, 77, 92. Rows of 50000, top-p alone, 48 rows by 2, 4, 5, 8: 52, 52, 47, 61.)
+template <typename F>
+int blocks_of(int R, F bytes) {
+  constexpr int kPart = 128 << 10, kHalf = 76 << 10;   // of a block, and of one that leaves room for another
+  int best = 0;
+  float least = 0.f;
+  for (int c = 1; c <= kMaxCluster; ++c) {
+    const int b = bytes(c);
+    const long long blocks = (long long)R * c;
+    if (b > kPart || (c > 1 && bytes(c - 1) <= 16 * kThreads)) continue;   // (or a thread has less than a unit)
+    const bool alone = blocks <= (c == 1 || (c == 2 && b <= kTarget) ? kNumSMs : 128);
+    if (!alone && (b > kHalf || blocks > (c <= 2 ? 2 * kNumSMs : 256))) continue;
+    const float us = (16.f + 0.2f / 1024 * b) * (alone ? 1.f : 1.35f);
+    if (!best || us < least) {
+      best = c;
+      least = us;
+    }
+  }
+  if (!best)
+    for (best = 1; best < kMaxCluster && bytes(best) > kTarget;) best *= 2;
+  return best;
+}
+
 template <typename T>
 cudaError_t launch(SampleArgs a, cudaStream_t s) {
-  // Blocks of a row: enough for their parts to fit two an SM, and more of them while all rows' blocks are resident at once
-  // (48 rows of 49999: 45 us by two, 37 by four, 52 by eight, which are not).
   auto bytes = [&](int c) { return (((a.V + Unit<T>::n - 1) / Unit<T>::n + 1 + c - 1) / c) * 16; };
-  a.cluster = 1;
-  while (a.cluster < kMaxCluster && (bytes(a.cluster) > kTarget || (2ll * a.R * a.cluster <= 2 * kNumSMs && bytes(a.cluster) > 16 * kThreads)))
-    a.cluster *= 2;
+  a.cluster = blocks_of(a.R, bytes);
   static std::atomic<uint64_t> done{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(sample_kernel<T>), 160 << 10, done);
   if (e != cudaSuccess) return e;

@@ -263,3 +263,13 @@ def test_borders_far_below_the_largest(up, T):
     ps = [1.0, 1.0, 0.999, 1.0, 1.0, 1.0, 1 - 2.0 ** -20, 1 - 2.0 ** -24, 0.5, 1 - 2.0 ** -24]
     _check(x, [T] * R, _params(R, 17)["u"], k=ks, p=ps)
     _check(x, [T] * R, _params(R, 18)["u"], k=ks)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("R,V", [(10, 60011), (20, 33001), (25, 60011), (30, 33001), (40, 60011), (60, 33001), (76, 20011), (2, 131072)])
+def test_rows_of_any_number_of_blocks(R, V, dtype):
+    """From one to eight blocks a row, powers of two and others."""
+    g = np.random.default_rng(R)
+    a = _params(R, R + 1)
+    _check(_logits(R, V, dtype, R), a["T"], a["u"], k=g.integers(0, 200, R).tolist(), p=g.choice([0.5, 0.9, 0.99, 1.0], R).tolist())
+    _check(_logits(R, V, dtype, R), a["T"], a["u"], p=g.choice([0.3, 0.9, 0.999], R).tolist(), m=g.choice([0.0, 0.05], R).tolist())
