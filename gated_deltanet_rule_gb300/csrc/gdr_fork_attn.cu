@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kOwnThreads, D == 256 ? 1 : 2)
     // The shared part's results for the warp's first rows, asked for as early as they are there (from the second item on
     // before its tiles: 102.8 -> 100.6 us for 256 forks).
     const size_t base = ((size_t)t.b * a.N + t.node0) * a.Hq + t.hk * a.G + t.h0;
-    const bool joins = t.shared > 0;
+    const bool joins = t.shared > 0 && !a.alone;
     float shared_x[kAhead][kVec], lse_s = -INFINITY;
     auto ask = [&](int i0, float (&x)[kAhead][kVec]) {
 #pragma unroll
@@ -1011,8 +1011,8 @@ cudaError_t own_few(const ForkAttnArgs& p, bool alone, cudaStream_t s) {
   return own_part<C, D, fork_own_few_kernel<D, WK>, C::kThreads, C::kBlocks>(p, alone, s);
 }
 template <int D, int WR>
-cudaError_t own_by_teams(const ForkAttnArgs& p, cudaStream_t s) {
-  return own_part<Own<D, WR>, D, fork_own_kernel<D, WR>, kOwnThreads, D == 256 ? 1 : 2>(p, false, s);
+cudaError_t own_by_teams(const ForkAttnArgs& p, bool alone, cudaStream_t s) {
+  return own_part<Own<D, WR>, D, fork_own_kernel<D, WR>, kOwnThreads, D == 256 ? 1 : 2>(p, alone, s);
 }
 
 // Few items: by four warps each, by eight where every item has an SM to itself (16 rows of 250, 1000 and 4000 positions of their
@@ -1031,23 +1031,25 @@ cudaError_t both_parts(const ForkAttnArgs& p, cudaStream_t s) {
   const long long rows = ((long long)p.t.B + p.T - 1) / p.T * p.t.N * G;
   // Short rows, all of whose items are resident at once: each reads its shared positions itself, one kernel in the place of
   // three (us by three and by one, 3 rows, 12 items: of 250 positions 25 and 13, 500 26 and 15, 1000 26 and 17, 2000 28 and 23;
-  // 64 rows, 256 items: 35 and 15, 35 and 17, 34 and 21, 35 and 31; D = 256, 3 rows: 22 and 15, 22 and 17, 22 and 23, 25 and 36).
+  // 64 rows, 256 items: 35 and 15, 35 and 17, 34 and 21, 35 and 31; D = 256, 3 rows: 22 and 15, 22 and 17, 22 and 23, 25 and 36;
+  // of 16 query rows a key head, 12 items: 26 and 15, 26 and 17, 26 and 23, 28 and 36; of 64, 6 items: 28 and 19, 28 and 25, 30 and 38).
   // The table's width is all that the host knows of the lengths.
-  if (p.t.N * G <= 8 && (long long)p.t.B * p.t.Hk <= kNumSMs * Few<D, 4>::kBlocks && (long long)p.t.M * p.t.page <= (D == 256 ? 512 : 2048))
-    return own_of_few<D>(p, true, s);
+  const int r = p.t.N * G;
+  const bool alone = r <= 64 && (long long)p.t.B * p.t.Hk <= kNumSMs * Few<D, 4>::kBlocks &&
+                     (long long)p.t.M * p.t.page <= (D == 256 || r > 16 ? 512 : r > 8 ? 1024 : 2048);
   cudaError_t e;
-  if constexpr (D == 256) e = shared_part<D, kSplit>(p, s);
+  if (alone) e = cudaSuccess;
+  else if constexpr (D == 256) e = shared_part<D, kSplit>(p, s);
   else e = rows > kM ? shared_part<D, kWide>(p, s) : shared_part<D, kNarrow>(p, s);
   if (e != cudaSuccess) return e;
-  const int r = p.t.N * G;
   if (r <= 8) {
     // Few items end sooner when four warps share each, many when more of them are under way (us by four and by one or two,
     // all parts together, own parts of 64 and of 1000 positions; D = 128: 256 items 33 and 31, 55 and 61, 512 items 38 and 34,
     // 80 and 80, 2048 items 61 and 53, 192 and 198; D = 256: 256 items 37 and 34, 79 and 79, 2048 items 104 and 80, 352 and 343).
     const bool many = (long long)p.t.B * p.t.Hk >= 3 * kNumSMs;
-    return many ? own_few<D, D == 64 ? 1 : 2>(p, false, s) : own_of_few<D>(p, false, s);
+    return many ? own_few<D, D == 64 ? 1 : 2>(p, false, s) : own_of_few<D>(p, alone, s);
   }
-  return r <= 16 ? own_by_teams<D, 1>(p, s) : r <= 32 ? own_by_teams<D, 2>(p, s) : own_by_teams<D, 4>(p, s);
+  return r <= 16 ? own_by_teams<D, 1>(p, alone, s) : r <= 32 ? own_by_teams<D, 2>(p, alone, s) : own_by_teams<D, 4>(p, alone, s);
 }
 
 }  // namespace
