@@ -902,15 +902,21 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
       __syncthreads();
       const float low = kWidth * sh.reds[0] + kCoarse * fmaxf(0.f, all - sh.reds[0]);
       const float least = p * low * (1.f - 0x1p-10f) - 0x1p-14f, most = p * all * (1.f + 0x1p-10f) + 0x1p-14f;
+      // The first step whose sum reaches each of the two, of all steps that do: a thread's last sum and the next thread's first
+      // one are added up in different orders, so a limit may lie between them, and a step at which the sum passes it need
+      // not be anywhere. (The border's own step reaches `least` whatever the sums' roundings.)
+      int lo = kSteps, hi = kSteps;
       float at = bf;
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
-        const float up = at + (float)n[i] * Row<T>::most_of(s0 + i);
-        if (at < least && up >= least) atomicMin(&sh.bin, s0 + i);
-        if (s0 + i < kFine && at * kWidth < most && up * kWidth >= most) atomicMin(&sh.bin2, s0 + i);
-        at = up;
+        at += (float)n[i] * Row<T>::most_of(s0 + i);
+        if (at >= least) lo = min(lo, s0 + i);
+        if (s0 + i < kFine && at * kWidth >= most) hi = min(hi, s0 + i);
       }
-      if (tid == 0 && least <= 0.f) sh.bin = 0;
+      lo = __reduce_min_sync(kAll, lo);
+      hi = __reduce_min_sync(kAll, hi);
+      if ((tid & 31) == 0 && lo < kSteps) atomicMin(&sh.bin, lo);
+      if ((tid & 31) == 0 && hi < kSteps) atomicMin(&sh.bin2, hi);
       __syncthreads();
       lo_step = sh.bin;
       hi_step = max(sh.bin2, lo_step);
@@ -1063,8 +1069,7 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
     {
       if (fits) {
         // ------------------------------------------------------------ few: in order, every block for itself
-        const int count = offset[kMaxCluster];
-        if (count == 0) return out;   // (cannot be: the first of those steps holds a logit)
+        const int count = offset[kMaxCluster];   // (one at least: the border's)
         // packed into the list's first half; then each to the place that the number of larger ones gives
         constexpr int kEach = kList / 2 / kThreads;
         u64 mine[kEach], *packed = sh.list, *sorted = sh.list + kList / 2;
@@ -1159,9 +1164,7 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
       }
     }
     if (!cuts_p) return out;
-    u64 need = max((u64)1, times(all, p, true));
-    if (need <= above) return out;   // (cannot be: the bounds hold)
-    need -= above;
+    u64 need = max((u64)1, times(all, p, true)) - above;   // (what lies above first_step is less by `least`'s margin)
     uint32_t lo, hi, ends, key, n_key;
     r.step_keys(first_step, ends, hi);
     if (k_on) lo = key_of(out.value) + 1;
