@@ -1386,7 +1386,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 #pragma unroll
           for (int e = 0; e < U::n; e += 2) {
             const W2 w = weights(r.s, sh.table, kept(x[e], at + e) ? x[e] : -INFINITY, kept(x[e + 1], at + e + 1) ? x[e + 1] : -INFINITY);
-            accumulate(acc, w.hi, w.lo);
+            // (what is not drawn, a weight that rounds to 0 units, adds nothing: where a sum passes there is an entry to find)
+            float h0, h1;
+            unpack(w.hi, h0, h1);
+            accumulate(acc, pack(h0 > 0.5f ? h0 : 0.f, h1 > 0.5f ? h1 : 0.f), w.lo);
           }
         }
         mine = fixed(acc);

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from gated_deltanet_rule_gb300 import gdr
-from tests.test_sample_gpu import _logits
+from tests.test_sample_gpu import _check, _logits
 
 pytestmark = pytest.mark.gpu
 F32 = torch.float32
@@ -40,3 +40,34 @@ def test_very_many_values_of_top_p(V, R, rows):
         token, (lo, hi) = token.cpu().numpy(), _last_kept(x, ps)
         off = np.nonzero((token < lo) | (token > hi))[0]
         assert len(off) == 0, (seed, len(off), [(float(ps[i]), int(token[i]), int(lo[i]), int(hi[i])) for i in off[:3]])
+
+
+@pytest.mark.parametrize("dtype", [F32, torch.bfloat16])
+@pytest.mark.parametrize("at", [0, 70001, 200002])
+@pytest.mark.parametrize("filters", [dict(), dict(top_k=150000), dict(top_k=1000), dict(min_p=1e-30)])
+def test_weights_below_half_a_unit_are_not_drawn(at, filters, dtype):
+    """One token has all the weight that counts; the others' e^-29 is 0.28 units of 2^-40 each and 2^16 units together."""
+    R, V = 6, 200003
+    x = torch.full((R, V), -29.0, device="cuda")
+    if dtype == F32:
+        x[1::2] -= torch.arange(V, device="cuda") * 1e-6
+    x[:, at] = 0
+    u = torch.tensor([0.0, 0.0, 1.0, 1.0, 2.0 ** -30, 1 - 2.0 ** -24], device="cuda")
+    kw = {k: torch.full((R,), v, dtype=torch.int32 if k == "top_k" else F32, device="cuda") for k, v in filters.items()}
+    token = torch.full((R,), -7, dtype=torch.int32, device="cuda")
+    gdr.gdr_sample(x.to(dtype), torch.ones(R, device="cuda"), u, token=token, **kw)
+    gdr.gdr_sync_status()
+    assert token.tolist() == [at] * R
+
+
+@pytest.mark.parametrize("T", [0.25, 1.0])
+def test_draws_among_weights_around_the_unit(T):
+    """A row's tail of weights between 2^-43 and 2^-37 of the largest: u at either end draws what has weight."""
+    V = 150001
+    x = (-27.75 + 2.0 * torch.randn(8, V, generator=torch.Generator().manual_seed(5))).cuda() * T
+    x[:, 75000] = 0
+    u = [0.0, 2.0 ** -31, 2.0 ** -24, 0.25, 0.75, 1 - 2.0 ** -23, 1 - 2.0 ** -24, 1.0]
+    for y in (x, x.bfloat16()):
+        _check(y, [T] * 8, u)
+        _check(y, [T] * 8, u, k=[100000] * 8)
+        _check(y, [T] * 8, u, p=[1 - 2.0 ** -24] * 8)
