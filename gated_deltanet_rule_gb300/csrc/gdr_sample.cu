@@ -468,10 +468,11 @@ struct Row {
       f(x, first + i * U::n);
     }
   }
-  // The mass of the thread's share where on(x) holds.
+  // The mass of the thread's share where on(x) holds: each weight rounded for itself, as a search through them adds them up (sums
+  // of pairs, rounded once a thread, can pass a border that the search then does not find).
   template <typename F>
   __device__ __forceinline__ u64 mass_where(F on) const {
-    W2 acc = {{0}, {0}};
+    u64 mass = 0;
     each([&](const float* x, int) {
       bool some = false;
 #pragma unroll
@@ -479,11 +480,12 @@ struct Row {
       if (!some) return;
 #pragma unroll
       for (int e = 0; e < U::n; e += 2) {
-        const W2 w = weights(s, sh->table, on(x[e]) ? x[e] : -INFINITY, on(x[e + 1]) ? x[e + 1] : -INFINITY);
-        accumulate(acc, w.hi, w.lo);
+        u64 w0, w1;
+        gdr::weight(s, sh->table, on(x[e]) ? x[e] : -INFINITY, on(x[e + 1]) ? x[e + 1] : -INFINITY, w0, w1);
+        mass += w0 + w1;
       }
     });
-    return fixed(acc);
+    return mass;
   }
 
   // Counts of the row's logits by step: this block's, then over all blocks, of this thread's steps (kMine neighbours).
@@ -837,10 +839,7 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
       r.cluster_sums(v, before, mass);
       all = mass[0] + out.ties * weight(r.s, sh.table, b);
     }
-    u64 need = max((u64)1, times(all, p, true));
-    if (tid == 0) sh.bin = -1;
-    __syncthreads();
-    u64 am = bm;
+    u64 need = max((u64)1, times(all, p, true)), am = bm;
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
       if (am < need && am + m[i] >= need) {
@@ -855,8 +854,7 @@ __device__ __forceinline__ Border find_border(Row<T>& r, int k, float p) {
     const uint32_t equal = sh.bin_n;
     const u64 above = sh.above_m;
     __syncthreads();
-    if (step < 0 || step > k_step) return out;   // (roundings at p next to 1)
-    need -= above;
+    need -= above;   // (sums of whole numbers: there is such a step, the k-th logit's at the latest)
     if (r.one_value(step)) {
       const u64 w = max((u64)1, weight(r.s, sh.table, r.value_of(step)));
       const uint32_t ties = least_ties(need, w, equal);

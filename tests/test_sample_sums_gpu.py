@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from gated_deltanet_rule_gb300 import gdr
-from tests.test_sample_gpu import _check, _logits
+from tests.test_sample_gpu import _call, _check, _logits, _params
 
 pytestmark = pytest.mark.gpu
 F32 = torch.float32
@@ -71,3 +71,40 @@ def test_draws_among_weights_around_the_unit(T):
         _check(y, [T] * 8, u)
         _check(y, [T] * 8, u, k=[100000] * 8)
         _check(y, [T] * 8, u, p=[1 - 2.0 ** -24] * 8)
+
+
+@pytest.mark.parametrize("value,below,top,steps,behind", [(0.0, -0.5, 25.375, 9, 94970), (-0.0, -0.5, 25.375, 9, 94970), (128.0, 126.5, 153.0, 4, 121072)])
+def test_top_p_ends_where_a_bin_of_several_values_ends(value, below, top, steps, behind):
+    """bf16 logits whose border lies next to the end of a bin that holds more than one value (around zero, above 127): each
+    weight of 10.5 units is rounded for itself, and 1 - p, some steps of 2^-24, is a little less than the mass behind the bin."""
+    n = 100000
+    x = torch.full((1, n + behind + 1), below, device="cuda")
+    x[0, 1:n + 1] = value
+    x[0, 0] = top
+    y = x.bfloat16()
+    assert torch.equal(y.float(), x)
+    _check(y, [(top - value) / 25.375], [0.5], p=[1 - steps * 2.0 ** -24])
+
+
+@pytest.mark.parametrize("filters", ["none", "k", "p", "kp", "min_p"])
+def test_bf16_rows_have_the_same_bits_in_any_batch(filters):
+    """Sums of bf16 rows are of whole numbers: tokens and probabilities do not depend on how many blocks share a row."""
+    V = 60011
+    x = _logits(4, V, torch.bfloat16, 21)
+    x[1] *= 50
+    x[2] *= 2.0 ** -7
+    a = _params(4, 22)
+    kw = {}
+    if "k" in filters:
+        kw["k"] = [40, 30000, 30000, 2000]
+    if filters in ("p", "kp"):
+        kw["p"] = [0.9, 0.7, 0.6, 0.999]
+    if filters == "min_p":
+        kw["m"] = [0.05, 1e-4, 0.9, 0.01]
+    T = [a["T"][0], 20.0, 0.01, a["T"][3]]
+    one = None
+    for times in (1, 3, 10, 18, 40, 100):
+        token, probs = _call(x.repeat(times, 1), T * times, a["u"] * times, **{k: v * times for k, v in kw.items()})
+        one = one or (token[:4], probs[:4])
+        for i in range(times):
+            assert (token[4 * i:4 * i + 4] == one[0]).all() and (probs[4 * i:4 * i + 4] == one[1]).all(), (times, i)
