@@ -1186,7 +1186,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   const int ranks = a.cluster, rank = (int)ptx::cluster_ctarank(), row = blockIdx.x / ranks;
   const T* logits = static_cast<const T*>(a.logits) + (long long)row * a.stride;
 
-  const float temperature = __ldg(a.temperature + row);
+  float temperature = __ldg(a.temperature + row);
   int k = a.top_k ? __ldg(a.top_k + row) : 0;
   float p = a.top_p ? __ldg(a.top_p + row) : 1.f;
   const float min_p = a.min_p ? __ldg(a.min_p + row) : 0.f;
@@ -1194,6 +1194,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (tid == 0) atomicCAS(a.err, 0, kErrDeviceIndex);
     return;
   }
+  temperature = fminf(temperature, 1e36f);   // (above, the lowest logit would have weight, and -inf, which stands for what is not kept, is taken for it)
   if (temperature == 0.f) {   // the best token alone
     k = 1;
     p = 1.f;
@@ -1267,8 +1268,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   u64 total = 0;
   if (top > -INFINITY) {
     {
-      // (above 1e36 the lowest logit would have weight, and -inf, which stands for what is not kept, is taken for it)
-      const float t = temperature == 0.f ? 1.f : fminf(temperature, 1e36f);
+      const float t = temperature == 0.f ? 1.f : temperature;
       // log2(e) / T as a pair: the quotient, and what it leaves over T
       constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.9259629911266174681e-8f;
       r.s.ch = kLog2e / t;

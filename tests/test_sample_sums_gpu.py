@@ -108,3 +108,14 @@ def test_bf16_rows_have_the_same_bits_in_any_batch(filters):
         one = one or (token[:4], probs[:4])
         for i in range(times):
             assert (token[4 * i:4 * i + 4] == one[0]).all() and (probs[4 * i:4 * i + 4] == one[1]).all(), (times, i)
+
+
+@pytest.mark.parametrize("T", [1e36, 1e38, float("inf")])
+@pytest.mark.parametrize("dtype", [F32, torch.bfloat16])
+def test_min_p_with_a_temperature_above_the_largest(T, dtype):
+    """Temperatures above 1e36 count as 1e36 for every filter: e^-100 is below 1e-3."""
+    x = torch.tensor([[3e38, 2e38, 2.98e38, -1e38]], device="cuda").to(dtype)
+    _, probs = _call(x, [T], None, m=[1e-3])
+    w = np.exp((x.double().cpu().numpy()[0] - float(x[0, 0])) / float(np.float32(1e36)))
+    want = np.where(w >= 1e-3, w, 0) / w[w >= 1e-3].sum()
+    assert (np.abs(probs[0] - want) <= 5 * 2.0 ** -24 * want).all()
