@@ -7,7 +7,7 @@
 //   dpost_w = sum dz y r,   dy = r (post_w dz - y r^2 mean(post_w dz y))  (or dz).
 //
 // Measured: 8192 rows of 4096 bf16 57 us (5.9 TB/s, 86% of the copy bandwidth), their gradient 124 us (5.4 TB/s, 79%),
-// that of 2731 rows of 2560 float32 without gate, scale and norm of y 36 us (4.7 TB/s), 24 rows of 2048 5.8 us (launch).
+// that of 2731 rows of 2560 float32 without gate, scale and norm of y 34 us (4.9 TB/s), 24 rows of 2048 5.8 us (launch).
 //
 // Both are bound by HBM. A block takes a row at a time, a thread 8 channels of it (16 neighbouring bytes, of
 // float32 twice), so that a row stays in registers from its one reading to its writing; the weights of a
@@ -112,17 +112,39 @@ __device__ __forceinline__ Vec<n> times(const Vec<n>& a, const Vec<n>& b) {
   for (int e = 0; e < n / 2; ++e) x.p[e] = mul(a.p[e], b.p[e]);
   return x;
 }
-// 1 / (1 + e^-x): the exponential's and the reciprocal's approximations are good to 2 and 1 units of the last place;
+// sigmoid(x) = 1 / (1 + e^-x): the exponential's and the reciprocal's approximations are good to 2 and 1 units of the last place;
 // an infinite exponential gives 0.
-__device__ __forceinline__ F2 sigmoid(F2 x) {
+__device__ __forceinline__ F2 exp_neg(F2 x) {
   float a, b;
   unpack(mul(x, both(-1.4426950408889634f)), a, b);
   asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
   asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
-  unpack(add(pack(a, b), both(1.f)), a, b);
+  return pack(a, b);
+}
+__device__ __forceinline__ F2 sigmoid_of(F2 e) {   // (of e^-x)
+  float a, b;
+  unpack(add(e, both(1.f)), a, b);
   asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
   asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
   return pack(a, b);
+}
+// A gate between its two uses: sigmoid(x), or where x is not negative 1 - sigmoid(x) = e^-x sigmoid(x) with the sign turned, so that
+// neither is formed as a difference that would lose it.
+__device__ __forceinline__ float gate_at(float x, float g, float rest) { return x < 0.f ? g : -rest; }
+__device__ __forceinline__ F2 kept_gate(F2 x, F2 e, F2 g) {
+  float x0, x1, g0, g1, r0, r1;
+  unpack(x, x0, x1);
+  unpack(g, g0, g1);
+  unpack(mul(e, g), r0, r1);
+  return pack(gate_at(x0, g0, r0), gate_at(x1, g1, r1));
+}
+// sigmoid(x) and 1 - sigmoid(x) of that: one of them it is, the other is 1 less that.
+__device__ __forceinline__ void both_of(F2 kept, F2& g, F2& rest) {
+  float s0, s1;
+  unpack(kept, s0, s1);
+  const int m0 = __float_as_int(s0) >> 31, m1 = __float_as_int(s1) >> 31, one = __float_as_int(1.f);
+  g = add(kept, pack(__int_as_float(one & m0), __int_as_float(one & m1)));
+  rest = sub(pack(__int_as_float(one & ~m0), __int_as_float(one & ~m1)), kept);
 }
 
 // A thread's 16-byte units of the rows to come, in shared memory: a ring of `stages` rows of `parts` units each, every
@@ -335,7 +357,7 @@ __global__ void __launch_bounds__(kMaxThreads, K * kCh<T> <= 8 ? 2 : 1) block_no
       if (gate) g = widen<T>(take(ring, 3 * k + 1, gate + at[k]));
       if (gate) {
 #pragma unroll
-        for (int e = 0; e < n / 2; ++e) g.p[e] = sigmoid(g.p[e]);
+        for (int e = 0; e < n / 2; ++e) g.p[e] = sigmoid_of(exp_neg(g.p[e]));
       } else {
         g = filled<n>(1.f);
       }
@@ -376,8 +398,9 @@ __global__ void __launch_bounds__(kMaxThreads, K * kCh<T> <= 8 ? 2 : 1) block_no
 }
 
 // The two sums over the rows of a thread's channels: in registers, or (more than 8 channels a thread) in shared memory
-// at the thread's own places.
-template <typename T, int K, bool kWide>
+// at the thread's own places. kGate is no test in the loops, as two blocks an SM then spill registers (8192 rows of 2048 bf16 82
+// us with a test, 72 without; without a gate 85 and 70 for 2560 channels).
+template <typename T, int K, bool kWide, bool kGate>
 __global__ void __launch_bounds__(kWide ? kMaxThreads : kPairThreads, kWide ? 1 : 2) block_norm_backward_kernel(const __grid_constant__ BlockNormArgs a) {
   constexpr int n = kCh<T>;
   constexpr bool kKeep = K * n <= 8;
@@ -394,7 +417,7 @@ __global__ void __launch_bounds__(kWide ? kMaxThreads : kPairThreads, kWide ? 1 
   const T *y = static_cast<const T*>(a.y) + blockIdx.x * a.y_row, *gate = static_cast<const T*>(a.gate);
   const T *h = static_cast<const T*>(a.h) + (size_t)blockIdx.x * C, *dn = static_cast<const T*>(a.dn) + (size_t)blockIdx.x * C;
   const float* dh_out = a.dh_out;
-  if (gate) gate += blockIdx.x * a.gate_row;
+  if (kGate) gate += blockIdx.x * a.gate_row;
   if (dh_out) dh_out += (size_t)blockIdx.x * C;
   const size_t y_step = (size_t)gridDim.x * a.y_row, gate_step = (size_t)gridDim.x * a.gate_row, step = (size_t)gridDim.x * C;
   size_t out = (size_t)blockIdx.x * C;   // where the present row's outputs go
@@ -405,7 +428,7 @@ __global__ void __launch_bounds__(kWide ? kMaxThreads : kPairThreads, kWide ? 1 
   const uint32_t stage = ptx::smem_u32(acc_sm + (kKeep ? 0 : 2 * C)) + (threadIdx.x >> 5) * K * 1024;
   auto ahead = [&] {
     y += y_step;
-    if (gate) gate += gate_step;
+    if (kGate) gate += gate_step;
     h += step;
     dn += step;
     if (dh_out) dh_out += step;
@@ -418,7 +441,7 @@ __global__ void __launch_bounds__(kWide ? kMaxThreads : kPairThreads, kWide ? 1 
         if (!kF32 && dh_out) copy_wide(ring, k * kUnits + 4, dh_out, at[k], C);
         if (at[k] >= C) continue;
         copy(ring, k * kUnits, y + at[k]);
-        if (gate) copy(ring, k * kUnits + 1, gate + at[k]);
+        if (kGate) copy(ring, k * kUnits + 1, gate + at[k]);
         copy(ring, k * kUnits + 2, h + at[k]);
         copy(ring, k * kUnits + 3, dn + at[k]);
         if (kF32 && dh_out) copy(ring, k * kUnits + 4, dh_out + at[k]);
@@ -467,12 +490,7 @@ __global__ void __launch_bounds__(kWide ? kMaxThreads : kPairThreads, kWide ? 1 
       if (at[k] >= C) continue;
       cn[k] = take(ring, k * kUnits + 3, dn + at[k]);
       x[k] = widen<T>(take(ring, k * kUnits + 2, h + at[k]));
-      g[k] = filled<n>(1.f);
-      if (gate) {
-        g[k] = widen<T>(take(ring, k * kUnits + 1, gate + at[k]));
-#pragma unroll
-        for (int e = 0; e < n / 2; ++e) g[k].p[e] = sigmoid(g[k].p[e]);
-      }
+      if (kGate) g[k] = widen<T>(take(ring, k * kUnits + 1, gate + at[k]));
       if constexpr (kF32) dx[k] = dh_out ? widen<float>(take(ring, k * kUnits + 4, dh_out + at[k])) : filled<n>(0.f);
       else dx[k] = dh_out ? take_wide(ring, k * kUnits + 4, dh_out + at[k]) : filled<n>(0.f);
     }
@@ -496,7 +514,13 @@ __global__ void __launch_bounds__(kWide ? kMaxThreads : kPairThreads, kWide ? 1 
       const Vec<n> v = widen<T>(cy[k]), d = widen<T>(cn[k]);
 #pragma unroll
       for (int e = 0; e < n / 2; ++e) {
-        const F2 py = mul(mul(w_z[k].p[e], v.p[e]), g[k].p[e]), wdn = mul(w_pre[k].p[e], d.p[e]);
+        F2 py = mul(w_z[k].p[e], v.p[e]);
+        const F2 wdn = mul(w_pre[k].p[e], d.p[e]);
+        if constexpr (kGate) {
+          const F2 ex = exp_neg(g[k].p[e]), open = sigmoid_of(ex);
+          py = mul(py, open);
+          g[k].p[e] = kept_gate(g[k].p[e], ex, open);
+        }
         x[k].p[e] = fma(py, both(r), x[k].p[e]);
         t[0] = fma(x[k].p[e], x[k].p[e], t[0]);
         t[1] = fma(wdn, x[k].p[e], t[1]);
@@ -524,13 +548,18 @@ __global__ void __launch_bounds__(kWide ? kMaxThreads : kPairThreads, kWide ? 1 
         for (int e = 0; e < n / 2; ++e) {
           acc[0][k].p[e] = fma(d.p[e], mul(x[k].p[e], both(q)), acc[0][k].p[e]);
           dx[k].p[e] = fma(mul(w_pre[k].p[e], d.p[e]), both(q), fma(x[k].p[e], both(-mx), dx[k].p[e]));
-          const F2 dxg = mul(dx[k].p[e], g[k].p[e]), b = mul(mul(dxg, both(r)), v.p[e]);   // dx g y r
+          F2 dxg = dx[k].p[e], rest;
+          if constexpr (kGate) {
+            F2 open;
+            both_of(g[k].p[e], open, rest);
+            dxg = mul(dxg, open);
+          }
+          const F2 b = mul(mul(dxg, both(r)), v.p[e]);   // dx g y r
           acc[1][k].p[e] = add(acc[1][k].p[e], b);
-          const F2 bw = mul(b, w_z[k].p[e]);
-          dg.p[e] = sub(bw, mul(bw, g[k].p[e]));
+          if constexpr (kGate) dg.p[e] = mul(mul(b, w_z[k].p[e]), rest);
           dy.p[e] = fma(v.p[e], both(-my), mul(mul(dxg, both(r)), w_z[k].p[e]));
         }
-        if (gate) store(static_cast<T*>(a.dgate) + out + at[k], dg);
+        if (kGate) store(static_cast<T*>(a.dgate) + out + at[k], dg);
         store(static_cast<T*>(a.dy) + out + at[k], dy);
         if (!kKeep) {
           store(acc_sm + at[k], acc[0][k]);
@@ -615,17 +644,17 @@ cudaError_t forward(BlockNormArgs a, cudaStream_t s) {
   stage_timer_end(slot, s);
   return cudaGetLastError();
 }
-template <typename T, int K, bool kWide>
-cudaError_t backward(BlockNormArgs a, cudaStream_t s) {
+template <typename T, int K, bool kWide, bool kGate>
+cudaError_t backward_of(BlockNormArgs a, cudaStream_t s) {
   const int t = threads_of(a.C, sizeof(T)), per = backward_per(a.C, sizeof(T)), blocks = (int)std::min<long long>(a.rows, kNumSMs * per);
   const int bytes = K * (sizeof(T) == 4 ? 5 : 6) * t * 16, more = (K * kCh<T> <= 8 ? 0 : 2 * a.C * 4) + (sizeof(T) == 2 ? K * t * 32 : 0);
   a.stages = stages_of(per, bytes, more);
   const int smem = a.stages * bytes + more;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(block_norm_backward_kernel<T, K, kWide>), 224 << 10, done);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(block_norm_backward_kernel<T, K, kWide, kGate>), 224 << 10, done);
   if (e != cudaSuccess) return e;
   int slot = stage_timer_begin(s, kKernBlockNormBwd);
-  block_norm_backward_kernel<T, K, kWide><<<blocks, t, smem, s>>>(a);
+  block_norm_backward_kernel<T, K, kWide, kGate><<<blocks, t, smem, s>>>(a);
   stage_timer_end(slot, s);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   slot = stage_timer_begin(s, kKernBlockNormBwd);
@@ -641,6 +670,10 @@ cudaError_t backward(BlockNormArgs a, cudaStream_t s) {
   e = cudaLaunchKernelEx(&cfg, block_norm_sum_kernel, a, blocks);
   stage_timer_end(slot, s);
   return e;
+}
+template <typename T, int K, bool kWide>
+cudaError_t backward(const BlockNormArgs& a, cudaStream_t s) {
+  return a.gate ? backward_of<T, K, kWide, true>(a, s) : backward_of<T, K, kWide, false>(a, s);
 }
 
 }  // namespace
