@@ -70,7 +70,7 @@ struct Table {
 struct Scale {
   float ch, cl;   // log2(e) / T
   float ref;      // subtracted from the logits first
-  float least;    // smaller differences count as this one (a weight of 2^-150)
+  float least;    // smaller differences count as this one (a weight of 2^-152, of which no probability is left)
   float mh, ml;   // the maximum's product with log2(e) / T, as formed for every logit: its weight is exactly 1
 };
 
@@ -1282,7 +1282,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       const float z = near ? top : 0.f;
       r.s.mh = __fmul_rn(z, r.s.ch);
       r.s.ml = __fmaf_rn(z, r.s.cl, __fmaf_rn(z, r.s.ch, -r.s.mh));
-      r.s.least = fmaxf((r.s.mh - 150.f) / r.s.ch, -FLT_MAX);
+      r.s.least = fmaxf((r.s.mh - 152.f) / r.s.ch, -FLT_MAX);
       r.steps = r.s.ch * (float)kPerOctave;
     }
     Border edge = {-INFINITY, 0, 0, -1, false, false, 0};

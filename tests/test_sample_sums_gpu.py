@@ -119,3 +119,21 @@ def test_min_p_with_a_temperature_above_the_largest(T, dtype):
     w = np.exp((x.double().cpu().numpy()[0] - float(x[0, 0])) / float(np.float32(1e36)))
     want = np.where(w >= 1e-3, w, 0) / w[w >= 1e-3].sum()
     assert (np.abs(probs[0] - want) <= 5 * 2.0 ** -24 * want).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, torch.bfloat16])
+def test_what_has_no_weight_has_no_probability(dtype):
+    """Probabilities are 0, not the smallest float, beside a logit of +inf and far below the largest one; what a float32 can
+    still show is there."""
+    x = torch.zeros(4, 64, device="cuda")
+    x[0, 5] = float("inf")
+    x[1] = -1000.0
+    x[1, 7] = 3.0
+    x[2] = 2e4
+    x[2, 9] = 3e4
+    x[3] = -100.0
+    x[3, 11] = 0.0
+    token, probs = _call(x.to(dtype), [1.0] * 4, [0.999] * 4)
+    assert token.tolist() == [5, 7, 9, 11]
+    assert [int((q > 0).sum()) for q in probs] == [1, 1, 1, 64]
+    assert np.abs(probs[3][0] - np.exp(-100.0)) <= 2.0 ** -149
