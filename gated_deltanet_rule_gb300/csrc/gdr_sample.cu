@@ -112,20 +112,21 @@ __device__ __forceinline__ W2 weights(const Scale& s, const float2* table, float
   return {mul(hi, f), mul(lo, f)};
 }
 __device__ __forceinline__ u64 fixed(float hi, float lo) { return (u64)(__float2ll_rn(hi) + __float2ll_rn(lo)); }
+__device__ __forceinline__ u64 fixed_one(float hi, float lo) { return (u64)(__float2ll_rn(hi) + __float2int_rn(lo)); }   // (one weight's: |lo| < 2^20)
 __device__ __forceinline__ u64 weight(const Scale& s, const float2* table, float l) {
   const W2 w = weights(s, table, l, l);
   float h, g, lo;
   unpack(w.hi, h, g);
   unpack(w.lo, lo, g);
-  return fixed(h, lo);
+  return fixed_one(h, lo);
 }
 __device__ __forceinline__ void weight(const Scale& s, const float2* table, float l0, float l1, u64& w0, u64& w1) {
   const W2 w = weights(s, table, l0, l1);
   float h0, h1, g0, g1;
   unpack(w.hi, h0, h1);
   unpack(w.lo, g0, g1);
-  w0 = fixed(h0, g0);
-  w1 = fixed(h1, g1);
+  w0 = fixed_one(h0, g0);
+  w1 = fixed_one(h1, g1);
 }
 // A running sum of pairs.
 __device__ __forceinline__ void accumulate(W2& acc, F2 hi, F2 lo) {
