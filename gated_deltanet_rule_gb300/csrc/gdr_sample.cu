@@ -1195,10 +1195,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     if (tid == 0) atomicCAS(a.err, 0, kErrDeviceIndex);
     return;
   }
-  temperature = fminf(temperature, 1e36f);   // (above, the lowest logit would have weight, and -inf, which stands for what is not kept, is taken for it)
   if (temperature == 0.f) {   // the best token alone
     k = 1;
     p = 1.f;
+  } else {   // (log2(e) / T stays a float; above, the lowest logit would have weight, and -inf, which stands for what is not kept, is taken for it)
+    temperature = fminf(fmaxf(temperature, 1.5e-30f), 1e36f);
   }
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");   // (waited for before the first remote write)
   if (tid < 64) sh.table[tid] = tab.t[tid];
@@ -1274,10 +1275,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.9259629911266174681e-8f;
       r.s.ch = kLog2e / t;
       r.s.cl = (fmaf(-r.s.ch, t, kLog2e) + kLog2eLow) / t;
-      if (!(r.s.ch < 1e30f)) {   // (only logits that equal the largest have weight)
-        r.s.ch = 1e30f;
-        r.s.cl = 0.f;
-      }
       const bool near = fabsf(top) * r.s.ch < 300.f;
       r.s.ref = near ? 0.f : top;
       const float z = near ? top : 0.f;

@@ -509,8 +509,8 @@ gdr_status gdr_cache_compact(void* k_cache, void* v_cache, const int32_t* table,
  * probabilities are w_i / total, 0 for tokens that are not kept. temperature 0 keeps the largest logit alone
  * (the first by index).
  *   logits [R, V] dt      row r starts at r * stride elements (any alignment of an element)
- *   temperature [R] float32, >= 0 (above 1e36 it counts as that);  top_k [R] int32, >= 0;  top_p, min_p [R] float32 in [0, 1]; the last three NULL
- *                         for no such filter
+ *   temperature [R] float32, >= 0 (but for 0, below 1.5e-30 and above 1e36 it counts as that)
+ *   top_k [R] int32, >= 0;  top_p, min_p [R] float32 in [0, 1]   NULL for no such filter
  *   u [R] float32         uniform numbers in [0, 1) (larger ones count as 1: the last kept token); with token
  *   token [R] int32, probs [R, V] float32   either may be NULL, not both
  * A logit that is -inf or nan is never kept; logits of +inf share all the weight. A row without any other logit

@@ -137,3 +137,17 @@ def test_what_has_no_weight_has_no_probability(dtype):
     assert token.tolist() == [5, 7, 9, 11]
     assert [int((q > 0).sum()) for q in probs] == [1, 1, 1, 64]
     assert np.abs(probs[3][0] - np.exp(-100.0)) <= 2.0 ** -149
+
+
+@pytest.mark.parametrize("T", [1.5e-30, 1e-33, 1e-40])
+@pytest.mark.parametrize("dtype", [F32, torch.bfloat16])
+def test_temperatures_below_the_smallest(T, dtype):
+    """Temperatures below 1.5e-30, but for 0, count as that for every filter."""
+    x = torch.tensor([[0.0, -1e-30, -1e-29, -1e-33, -1.0]] * 3, device="cuda").to(dtype)
+    least = float(np.float32(1.5e-30))
+    w = np.exp(x[0].double().cpu().numpy() / least)
+    _, probs = _call(x, [T, T, 0.0], None, m=[0.25, 0.9, 0.9])
+    for r, m in enumerate((0.25, 0.9)):
+        want = np.where(w >= m, w, 0) / w[w >= m].sum()
+        assert (np.abs(probs[r] - want) <= 5 * 2.0 ** -24 * want).all()
+    assert probs[2].tolist() == [1, 0, 0, 0, 0]
