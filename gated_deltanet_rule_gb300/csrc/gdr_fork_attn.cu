@@ -543,15 +543,17 @@ __global__ void __launch_bounds__(kOwnThreads, D == 256 ? 1 : 2)
         const float mw = s_m[w0 + w][rr];
         c[w] = mw == top ? 1.f : ex2_approx(mw - top);
         sum += c[w] * s_l[w0 + w][rr];
-        rare |= c[w] == 0.f && mw != -INFINITY;
       }
       const Factors f = factors(true, joins, top, sum, lse_s);
       lse = f.lse;
-      rare |= f.rare;
+      rare = f.rare;
       const float inv = f.sees ? f.own / (sum * f.total) : 0.f;
       c_s = f.shared / f.total;
 #pragma unroll
-      for (int w = 0; w < WK; ++w) c[w] *= inv;
+      for (int w = 0; w < WK; ++w) {
+        c[w] *= inv;   // (two small factors can vanish together)
+        rare |= c[w] == 0.f && s_m[w0 + w][rr] != -INFINITY;
+      }
     }
     if (a.lse && lane < kMine && my_row < t.rows) a.lse[base + my_place] = lse;
     const unsigned rares = __ballot_sync(0xffffffffu, (rare || cleaned) && lane < kMine && my_row < used);
