@@ -177,7 +177,7 @@ gdr_status check_block_norm(const BlockNormArgs& a, gdr_dtype dt, const char* wh
   if (!(a.eps >= 0.f)) return fail(GDR_ERR_INVALID_ARG, "%s: eps must be >= 0", who);
   const int es = dt == GDR_BF16 ? 2 : 4;
   for (long long s : {a.y_row, a.gate ? a.gate_row : a.C})
-    if (s < a.C || s * es % 16 != 0 || s > 1ll << 22)
+    if (s < a.C || s > 1ll << 22 || s * es % 16 != 0)
       return fail(GDR_ERR_INVALID_ARG, "%s: rows of y and gate must be a multiple of 16 bytes apart, from C to 2^22 elements", who);
   for (const void* p : {a.h, a.y, a.gate, (const void*)a.post_w, (const void*)a.scale, (const void*)a.pre_w})
     if (!aligned(p, 16)) return fail(GDR_ERR_INVALID_ARG, "%s: h, y, gate, post_w, scale and pre_w must be 16-byte aligned", who);
@@ -470,12 +470,12 @@ gdr_status gdr_sample(const void* logits, long long stride, const float* tempera
   if ((token != nullptr) != (u != nullptr)) return fail(GDR_ERR_INVALID_ARG, "%s: token and u are given together", who);
   if (R < 1 || V < 1) return fail(GDR_ERR_INVALID_ARG, "%s: sizes must be >= 1 (R=%d V=%d)", who, R, V);
   if (dt != GDR_F32 && dt != GDR_BF16) return fail(GDR_ERR_INVALID_ARG, "%s: unknown dtype %d", who, (int)dt);
+  if (R > 1 && (stride < V || stride > (1ll << 32)))
+    return fail(GDR_ERR_INVALID_ARG, "%s: stride=%lld is below V=%d or above 2^32", who, stride, V);
   const int es = dt == GDR_BF16 ? 2 : 4;
   const bool whole = aligned(logits, 16) && (R == 1 || stride * es % 16 == 0);
   if (V > (whole ? kSampleMaxV : kSampleMaxV - 8) || R > 1 << 24)
     return fail(GDR_ERR_UNSUPPORTED, "%s: R=%d exceeds 2^24, or V=%d 2^18 (2^18 - 8 where rows do not begin on 16 bytes)", who, R, V);
-  if (R > 1 && (stride < V || stride > (1ll << 32)))
-    return fail(GDR_ERR_INVALID_ARG, "%s: stride=%lld is below V=%d or above 2^32", who, stride, V);
   if (!aligned(logits, es)) return fail(GDR_ERR_INVALID_ARG, "%s: logits must be aligned to their elements", who);
   for (const void* p : {(const void*)temperature, (const void*)u, (const void*)top_k, (const void*)top_p, (const void*)min_p,
                         (const void*)token, (const void*)probs})
