@@ -13,7 +13,10 @@
 // of pairs, 2^s as 1 + a polynomial whose first term is a pair (table and polynomial after Tang, 1989). Products
 // with log2(e) / T cancel against the maximum only where that is exact: ref = 0 where |max| log2(e) / T < 300 (the
 // pair holds x to 2^-39 then), else ref = max, and logits that matter (150 binary orders: what float32 probabilities
-// can show) lie within a factor of two of it, where the difference is exact. Sums are kept in integers of 2^-40 (associative: no order, no rounding).
+// can show) lie within a factor of two of it, where the difference is exact. Sums are integers in units of 2^-40 of the largest weight.
+// bf16: of weights that are each rounded to such a unit, so in any order, and a row has the same bits in any batch. float32: a thread
+// adds up its pairs and rounds their sum (to 2^-37 of it), so a total's last units, and with them a token or border that lies that close,
+// depend on how many blocks share a row, and this on how many rows there are; only a border's few candidates are added up as integers.
 //
 // A cluster of blocks holds a row in shared memory, read once. The border is found by counting; all blocks know all counts.
 //   bf16: a bin for each value of a magnitude from 2^-8 to 127, counted as the logits arrive, before their largest is known.
@@ -26,11 +29,11 @@
 //     of the float at a time.
 // The token is found warp, 32-unit piece, lane, entry: each a scan over lanes.
 //
-// Bound by instructions and by the steps' dependence, not by HBM: 256 rows of 131072 bf16 with top-p take 112 us (600 GB/s, issue
-// slots 54% busy), where counting is half of a block's time; 96 rows of 131072 float32 with top-p 130 us (issue 51%), a third of it
-// the pass over the exact weights (42 packed operations a pair of logits); 48 rows of 49999 31 to 38 us, one of 32000 18 us: five
-// exchanges between the blocks and a dozen dependent steps. Weights relative to the maximum's remainder in the table, 8 operations
-// of 42 fewer, were no faster.
+// Bound by instructions and by the steps' dependence, not by HBM: 256 rows of 131072 bf16 with top-p take 108 us (620 GB/s, issue
+// slots 55% busy), where counting is half of a block's time; 96 rows of 131072 float32 with top-p 129 to 131 us (issue 52%), a
+// third of a block's time the pass over the exact weights (42 packed operations a pair of logits), and its 768 blocks, of which
+// some 256 find room at once, three rounds; 48 rows of 49999 31 to 38 us, one of 32000 18 us: five exchanges between the blocks
+// and a dozen dependent steps. Weights relative to the maximum's remainder in the table, 8 operations of 42 fewer, were no faster.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -573,7 +573,8 @@ def fork_attn_workspace_bytes(B: int, N: int, Hq: int, D: int = D) -> int:
 def gdr_fork_attn(q, k_pages, v_pages, table, ctx, first, shared, lengths=None, mask=None, scale: float | None = None,
                   o=None, lse=None, want_lse: bool = False, ws=None, stream=None):
     """gdr_tree_attn for forked rows: rows first[t] .. first[t+1]-1 (first [T+1] int32) share their first shared[t]
-    positions (whole pages; read through the first of them, once for all), and go on over their own."""
+    positions (whole pages; read through the first of them, once for all), and go on over their own. Few short rows
+    are faster in a table of at most 2048 positions."""
     return _bind().fork_attn(q, k_pages, v_pages, table, ctx, first, shared, lengths, mask, scale, o, lse, want_lse, ws,
                              _raw(stream))
 

@@ -428,7 +428,11 @@ gdr_status gdr_tree_attn(const void* q, const void* k_pages, const void* v_pages
  * in float32, and joined by their lse.
  *   ws at least gdr_fork_attn_workspace_bytes(B, N, Hq, D) bytes (0 for sizes that are not implemented)
  * If first falls anywhere, no row is attended (o = 0, lse = -inf); a group whose numbers are out of range, or a row with
- * ctx below shared, counts as having no nodes. Both record GDR_ERR_DEVICE_INDEX. The same call gives the same bits.
+ * ctx below shared, counts as having no nodes. Both record GDR_ERR_DEVICE_INDEX. The same call gives the same bits; a row
+ * beside other rows may round differently, as for gdr_tree_attn.
+ * Few short rows are faster in a table no wider than they need, as M is all that the host knows of their lengths: with
+ * B * Hk <= 304 (152 for heads of 256) and N * Hq / Hk <= 64 a call is one kernel where M * page is at most 2048 (1024 where
+ * N * Hq / Hk > 8; 512 where it is > 16 and for heads of 256), else three, which take two and a half times as long.
  */
 size_t gdr_fork_attn_workspace_bytes(int B, int N, int Hq, int D);
 gdr_status gdr_fork_attn(const void* q, const void* k_pages, const void* v_pages, const int32_t* table,
@@ -516,7 +520,8 @@ gdr_status gdr_cache_compact(void* k_cache, void* v_cache, const int32_t* table,
  * A logit that is -inf or nan is never kept; logits of +inf share all the weight. A row without any other logit
  * gets token -1 and probabilities 0. A row whose temperature, top_k, top_p or min_p is out of range keeps its
  * outputs untouched and records GDR_ERR_DEVICE_INDEX. Weights are formed to about 2^-38 of their size and summed in
- * units of 2^-40 of the largest (a weight below half a unit is not drawn). V <= 2^18, less 8 where rows do not
+ * units of 2^-40 of the largest (a weight below half a unit is not drawn). The same call gives the same bits; a bfloat16
+ * row has them in any call, a float32 row beside other rows may be off by the sums' last units (2^-37). V <= 2^18, less 8 where rows do not
  * begin on 16 bytes; R <= 2^24.
  */
 gdr_status gdr_sample(const void* logits, long long stride, const float* temperature, const float* u,
