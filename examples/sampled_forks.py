@@ -33,7 +33,7 @@ class Hybrid(Model):
         self.gate_w = [(torch.randn(HID, HID, generator=g) / math.sqrt(HID)).to(device, torch.bfloat16) for _ in LAYERS]
 
     def run(self, tokens, mixer):
-        """The logits [B, L, VOCAB] after tokens [B, L]; mixer(layer, kind, number of its kind, its input) -> [B, L, heads, D]."""
+        """The bfloat16 logits [B, L, VOCAB] after tokens [B, L]; mixer(layer, kind, number of its kind, its input) -> [B, L, heads, D]."""
         x = self.embed[tokens.long()].float()
         x, n = gdr.gdr_block_norm(x, torch.zeros_like(x), self.pre_w[0], eps=EPS)
         seen = [0, 0]
@@ -43,7 +43,7 @@ class Hybrid(Model):
             gate = (h @ self.gate_w[layer]).float()
             x, n = gdr.gdr_block_norm(x, y, self.pre_w[layer + 1], self.post_w[layer], gate, self.scale[layer], EPS, h_out=x)
             seen[kind] += 1
-        return (n.to(torch.bfloat16) @ self.head).float()
+        return n.to(torch.bfloat16) @ self.head
 
 
 class Samples:
