@@ -23,9 +23,9 @@
 // heads of 128, 94 to 98 us (52.6 HBM): shared part 50, join 15 (partly within the others), own part 41 at 4.7 TB/s, the rest of
 // that the end, where the last items run alone. 64 forks of 65536 positions, 16 / 2 heads of 256, 80 to 81 (36.6 operations):
 // shared part 64, a 128-row tile an item, whose softmax runs between the products. 64 rows of 64 tokens, 4 trunks, 16 / 4 heads
-// of 128, 206 to 211 (89.7 operations): shared part 149 at 60% of the matrix rate (softmax; absent nodes, an eighth of them, included), own part 49, bound by the
-// latency of its steps with eight computing warps an SM. 3 forks of 448 positions 10.3: one kernel, four tiles one after
-// the other.
+// of 128, 206 to 211 (89.7 operations): shared part 149 at 60% of the matrix rate (softmax; the eighth of the nodes that is
+// absent is computed, too), own part 49, bound by the latency of its steps with eight computing warps an SM. 3 forks of 448
+// positions 10.3: one kernel, four tiles one after the other.
 //
 // Weights are rounded to bfloat16 for their product with v, the sum adds them unrounded; scores, sums and parts are
 // float32.

@@ -16,7 +16,7 @@ def _give_back():
 
 
 def _room(gib):
-    if torch.cuda.get_device_properties(0).total_memory < (gib << 30):
+    if torch.cuda.mem_get_info()[0] + torch.cuda.memory_reserved() < (gib << 30):
         pytest.skip("not enough memory")
 
 
